@@ -338,6 +338,150 @@ unsigned long long kdn_chunk_prefill_backward_workspace_size(kdn_variant variant
                                                              int H, int d_k, int d_v,
                                                              int chunk, kdn_status *status);
 
+/*
+ * Linear attention with a decay for each head.  Per head
+ *     S_t = exp(g_t) S_{t-1} + k_t v_t^T,      o_t = S_t^T q_t,
+ * the recurrence above without its correction (the state "gated" by a decay
+ * and written to: "Внимание в LLM · часть 11 -- Память с поправкой", section
+ * "Сначала решить, сколько прошлого оставить"), in the two regimes of the
+ * delta-rule entry points: chunkwise for prompts, recurrent for single
+ * tokens, and with its gradients.
+ *
+ * Conventions of these entry points, beside those at the top of this file:
+ *   - log_alpha is g, the logarithm of the retention, g <= 0 (not checked):
+ *     KDN_GATE_TOKEN: one value per token and head, [.., H] in the call's
+ *     dtype; KDN_GATE_HEAD: one constant per head, [H] float32 always (a
+ *     retention near 1, as of a head with a long memory, has no bits in a
+ *     bfloat16 alpha).  g = -infinity resets the state at that token; so does
+ *     any g below -105, whose power of e is 0 in float32.
+ *   - Shared heads: there are H states and outputs; q, k and v have Hq, Hk and
+ *     Hv heads, each a divisor of H.  State h reads head h / (H / Hq) of q, and
+ *     so on.
+ *   - q, k and v may be slices of wider rows, such as one projection's output:
+ *     q_stride, k_stride and v_stride are the elements from one token to the
+ *     next (0: contiguous, heads * d), at least heads * d, and whole 16-byte
+ *     pieces.  The heads of a token are contiguous.  o is contiguous.
+ *   - dense batches: N sequences of T tokens, rows n * T + t, state n of S0 and
+ *     S_out.  Packed batches (`packed` not NULL): N sequences of any lengths
+ *     one behind the other, described by kdn_sequence_tables; T is 0; rows
+ *     behind the last sequence are not read, and their outputs are left as
+ *     they were (gradients: zero).  S0 and S_out are pools of packed->pool
+ *     states, sequence n has state slots[n] (slots NULL: n).  A sequence whose
+ *     slot is not in [0, pool) is skipped: its outputs and states are left as
+ *     they were.  States without a sequence are left as they were.  Two
+ *     sequences may share a slot only where no state is written.
+ *     The tables are device data, which the host cannot check: a row of them
+ *     that does not fit the call's sizes is skipped, and never read or written
+ *     past the call's tensors.
+ *   - Non-finite q, k, v propagate within their sequence, to the tokens of
+ *     the same chunk before them too.
+ */
+typedef enum kdn_gate {
+    KDN_GATE_TOKEN = 0,
+    KDN_GATE_HEAD = 1
+} kdn_gate;
+
+typedef struct kdn_packed {
+    int tokens;                /* rows of q, k, v and o                       */
+    int block;                 /* tokens of a block, as the tables were built */
+    int max_blocks;            /* rows of blocks                              */
+    int pool;                  /* states of S0 and S_out                      */
+    const int *blocks;         /* device, [max_blocks, 4], 16-byte aligned    */
+    const int *block_offsets;  /* device, [N + 1]                             */
+    const int *slots;          /* device, [N], or NULL: sequence n            */
+} kdn_packed;
+
+/*
+ * Tables of a packed batch from the sequences' lengths, built on the device
+ * (no copy to the host, one kernel).
+ *
+ *   N           sequences
+ *   tokens      rows of the packed batch
+ *   block       tokens of a block: a positive multiple of 64
+ *   max_blocks  kdn_sequence_max_blocks(N, tokens, block)
+ *   lengths     [N] int32; a negative length counts as 0, and what passes
+ *               `tokens` in sum is cut off
+ *   slots       [N] int32 or NULL (sequence n has slot n); only for slot_map
+ *   context     [N] int32 or NULL (zeros): tokens the sequence had before
+ * Outputs, int32, the last two may be NULL:
+ *   offsets       [N + 1]  first row of each sequence, and the end
+ *   block_offsets [N + 1]  first block of each sequence, and the end
+ *   blocks        [max_blocks, 4]  first row, tokens, sequence, index in its
+ *                 sequence; {0, 0, -1, 0} behind the last block
+ *   slot_map      [tokens]  slot of the token's sequence, -1 behind the last
+ *   positions     [tokens]  context + index in the sequence, 0 behind the last
+ * Outputs overlap no input and no other output.  All pointers on 4-byte
+ * boundaries, blocks on 16.
+ */
+kdn_status kdn_sequence_tables(int N, int tokens, int block, int max_blocks,
+                               const int *lengths, const int *slots, const int *context,
+                               int *offsets, int *block_offsets, int *blocks,
+                               int *slot_map, int *positions, void *stream);
+
+/* Blocks that N sequences of `tokens` tokens in all can have at most, or -1 if
+ * the sizes are invalid. */
+int kdn_sequence_max_blocks(int N, int tokens, int block);
+
+/* The block length kdn_linear_prefill uses for a dense batch, and a good one
+ * for a packed batch of N sequences, `tokens` rows and H states each: long
+ * enough that cutting costs little, short enough to fill the GPU.  -1 if the
+ * sizes are invalid. */
+int kdn_linear_block(int tokens, int N, int H);
+
+/*
+ * Chunkwise prefill.
+ *
+ *   q [tokens, Hq, d_k], k [tokens, Hk, d_k], v [tokens, Hv, d_v]   dtype
+ *   log_alpha   [tokens, H] dtype, or [H] float32 (gate)
+ *   S0          [N or pool, H, d_k, d_v] float32, or NULL for zero states
+ *   o           [tokens, H, d_v] dtype (output)
+ *   S_out       shaped as S0 (output), or NULL if not wanted; may be exactly
+ *               S0, must not overlap it otherwise
+ *   workspace   device memory of at least kdn_linear_prefill_workspace_size
+ *               bytes (KDN_ERR_WORKSPACE), 256-byte aligned, overlapping no
+ *               other argument; NULL if that size is 0.  Scratch.
+ * (tokens = N * T for a dense batch.)  Supported: d_k, d_v in {64, 128};
+ * KDN_F32 or KDN_BF16; any N, T, tokens >= 0 with N * T < 2^31.  A prefill of
+ * one token per sequence is a decode step with S0 kept; several are the check
+ * of draft tokens.  o overlaps no input and not S_out.  bfloat16 products
+ * round q k^T and the state they read to bfloat16 once, and keep the state
+ * itself to float32.
+ */
+kdn_status kdn_linear_prefill(kdn_dtype dtype, int N, int T, int H, int Hq, int Hk, int Hv,
+                              int d_k, int d_v, kdn_gate gate,
+                              long long q_stride, long long k_stride, long long v_stride,
+                              const void *q, const void *k, const void *v,
+                              const void *log_alpha, const float *S0, void *o, float *S_out,
+                              const kdn_packed *packed, void *workspace,
+                              unsigned long long workspace_bytes, void *stream);
+
+/* Bytes of workspace kdn_linear_prefill needs (0 for none), or 0 with *status
+ * set when the sizes are invalid or unsupported (status may be NULL).  Of
+ * `packed` only tokens, block and max_blocks are read. */
+unsigned long long kdn_linear_prefill_workspace_size(kdn_dtype dtype, int N, int T, int H,
+                                                     int d_k, int d_v, const kdn_packed *packed,
+                                                     kdn_status *status);
+
+/*
+ * One decode step for N rows from a pool of states, updated in place.
+ *
+ *   q [N, Hq, d_k], k [N, Hk, d_k], v [N, Hv, d_v] dtype, rows by stride
+ *   log_alpha   [N, H] dtype, or [H] float32 (gate)
+ *   slots       [N] int32 or NULL: state of each row.  A row whose slot is not
+ *               in [0, pool) is skipped and its o left as it was (the padding
+ *               of a batch of fixed size).  Two rows may not share a slot.
+ *   pool        states of S (slots NULL: at least N)
+ *   S           [pool, H, d_k, d_v] float32, updated in place
+ *   o           [N, H, d_v] dtype (output)
+ * o overlaps no input and not S.
+ */
+kdn_status kdn_linear_decode(kdn_dtype dtype, int N, int H, int Hq, int Hk, int Hv,
+                             int d_k, int d_v, kdn_gate gate,
+                             long long q_stride, long long k_stride, long long v_stride,
+                             const void *q, const void *k, const void *v,
+                             const void *log_alpha, const int *slots, int pool,
+                             float *S, void *o, void *stream);
+
 /* Static, NUL-terminated description of a status code. */
 const char *kdn_status_string(kdn_status status);
 

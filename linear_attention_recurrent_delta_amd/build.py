@@ -40,7 +40,13 @@ UNITS += [("kdn_prefill.hip", ["-DKDN_PREFILL_DISPATCH"], "kdn_prefill_dispatch.
           ("kdn_prefill_short.hip", ["-mllvm", "-amdgpu-mfma-vgpr-form"], "kdn_prefill_short.o"),
           ("kdn_variance.hip", [], "kdn_variance.o"),
           ("kdn_noalloc.hip", [], "kdn_noalloc.o"),
-          ("kdn_backward.hip", [], "kdn_backward.o")]
+          ("kdn_backward.hip", [], "kdn_backward.o"),
+          ("kdn_linear_abi.cpp", [], "kdn_linear_abi.o"),
+          # as for the chain: every accumulator of the state is decayed and
+          # read as an operand each chunk
+          ("kdn_linear.hip", ["-mllvm", "-amdgpu-mfma-vgpr-form"], "kdn_linear.o"),
+          ("kdn_linear_decode.hip", [], "kdn_linear_decode.o"),
+          ("kdn_tables.hip", [], "kdn_tables.o")]
 
 
 def hipcc() -> str:

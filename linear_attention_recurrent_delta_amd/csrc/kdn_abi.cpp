@@ -2,12 +2,18 @@
 // every argument (before any HIP call), then one kernel launch on the
 // caller's stream.
 #include "kdn.h"
+#include "kdn_check.h"
 #include "kdn_launch.h"
 #include "kdn_workspace.h"
 
 #include <atomic>
 #include <initializer_list>
 #include <stdint.h>
+
+using kdn::aligned;
+using kdn::overlap;
+using kdn::valid_dim;
+using kdn::valid_dtype;
 
 namespace {
 
@@ -29,16 +35,6 @@ int device_cus() {
     return n;
 }
 
-bool aligned(const void *p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
-
-// [a, a+na) and [b, b+nb) overlap (byte ranges, empty ranges never overlap)
-bool overlap(const void *a, long long na, const void *b, long long nb) {
-    if (!a || !b || na <= 0 || nb <= 0)
-        return false;
-    const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
-    return x < y + (uintptr_t)nb && y < x + (uintptr_t)na;
-}
-
 bool valid_variant(int v) { return v >= KDN_DELTANET && v <= KDN_ISO_KDN; }
 bool is_kdn(int v) { return v == KDN_DIAG_KDN || v == KDN_ISO_KDN; }
 // float32 variances per (sequence, head): d_k (diagonal KDN), 1 (isotropic)
@@ -48,8 +44,6 @@ long long p_per_head(int v, int d_k) {
 // Alignment of the variance tensors: vectors of d_k floats 16 bytes, the
 // per-head scalar of isotropic KDN one float.
 uintptr_t p_align(int v) { return v == KDN_ISO_KDN ? 4 : 16; }
-bool valid_dtype(int d) { return d == KDN_F32 || d == KDN_BF16; }
-bool valid_dim(int d) { return d == 64 || d == 128; }
 
 // Gate pointers the variant does not use must be NULL; the ones it uses must
 // be non-NULL unless the per-token tensors are empty.
@@ -82,7 +76,7 @@ const char *kdn_status_string(kdn_status s) {
     case KDN_ERR_ALIGN: return "a pointer is not aligned as required";
     case KDN_ERR_ALIAS: return "an output overlaps an input it may not overlap";
     case KDN_ERR_HIP: return "the HIP runtime rejected the kernel launch";
-    case KDN_ERR_WORKSPACE: return "the workspace is smaller than kdn_chunk_prefill_workspace_size";
+    case KDN_ERR_WORKSPACE: return "the workspace is smaller than the size query says";
     case KDN_ERR_SCRATCH: return "one chunk of every head of a sequence needs more than the library's static scratch";
     }
     return "unknown status";

@@ -1,0 +1,88 @@
+// kdn_linear.h -- launch parameters and launchers of the linear-attention
+// kernels (linear attention with a decay for each head) and of the
+// packed-batch tables.  The C ABI (kdn_linear_abi.cpp) validates arguments
+// and fills these.
+#pragma once
+
+#include <hip/hip_runtime.h>
+
+#include "kdn.h"
+
+namespace kdn {
+
+// Tokens of one chunk of the chunked form: 64 bfloat16 or 32 float32 rows of
+// q, k and v (d = 128) are 48 KB of LDS, so that two workgroups share a CU.
+__host__ __device__ constexpr int linear_chunk(bool bf16) { return bf16 ? 64 : 32; }
+
+struct LinearParams {
+    int bf16;
+    int N;                  // sequences
+    int T;                  // dense: tokens of every sequence
+    int H, Hq, Hk, Hv, dk, dv;
+    int gate;               // kdn_gate
+    long tokens;            // rows of q, k, v, o
+    long q_stride, k_stride, v_stride;   // elements between tokens
+    const void *q, *k, *v;
+    const void *la;         // log_alpha
+    // blocks of consecutive tokens of one sequence, the unit of a workgroup
+    int block;              // tokens of a block (a multiple of 64)
+    int nblocks;            // dense: blocks of a sequence; packed: rows of `blocks`
+    const int *blocks;      // packed: [nblocks][4] first token, tokens, sequence,
+                            // index in the sequence (null: dense)
+    const int *block_offsets;   // packed: [N + 1]
+    const int *slots;       // packed: [N] state of each sequence (null: n)
+    long pool;              // states of S0 / S_out
+    const float *S0;        // [pool, H, dk, dv], may be null (zero)
+    float *S_out;           // [pool, H, dk, dv], may be null (not wanted)
+    void *o;                // [tokens, H, dv]
+    // Sequences of several blocks: a block's own contribution to the state
+    // and its decay, replaced by the state at the block's start.
+    float *ws_state;        // [blocks][H][dk * dv]
+    float *ws_decay;        // [blocks][H]
+    // Gradients.
+    const void *d_o;        // [tokens, H, dv]
+    const float *dS_out;    // [pool, H, dk, dv], may be null (zero)
+    void *dq, *dk_, *dv_;   // contiguous [tokens, heads, d], call dtype
+    void *dla;              // [tokens, H] or [H], call dtype, may be null
+    float *dS0;             // may be null
+    float *ws_rstate;       // [blocks][H][dk * dv], the reverse recurrence's
+    void *ws_chunk;         // [blocks * block / chunk][H][dk * dv] state at every
+                            // chunk's start, call dtype
+    float *ws_dq, *ws_dk, *ws_dv;   // [tokens, H, d] of shared heads (else null)
+    float *ws_dla;          // [blocks][H] sums of d log_alpha (one decay per head)
+};
+
+struct LinearDecodeParams {
+    int bf16;
+    int N, H, Hq, Hk, Hv, dk, dv;
+    int gate;
+    long q_stride, k_stride, v_stride;
+    const void *q, *k, *v, *la;
+    const int *slots;       // [N] or null
+    long pool;
+    float *S;               // [pool, H, dk, dv], updated in place
+    void *o;                // [N, H, dv]
+};
+
+struct TableParams {
+    int N, tokens, block, max_blocks;
+    const int *lengths, *slots, *context;
+    int *offsets, *block_offsets, *blocks, *slot_map, *positions;
+};
+
+// Blocks of all sequences, for grids and workspaces.
+inline long linear_total_blocks(const LinearParams &P) {
+    return P.blocks ? (long)P.nblocks : (long)P.N * P.nblocks;
+}
+
+hipError_t launch_linear_prefill(const LinearParams &P, hipStream_t stream);
+hipError_t launch_linear_decode(const LinearDecodeParams &P, hipStream_t stream);
+hipError_t launch_linear_backward(const LinearParams &P, hipStream_t stream);
+hipError_t launch_sequence_tables(const TableParams &P, hipStream_t stream);
+
+// Passes shared by the prefill and its gradients (kdn_linear.hip): the blocks'
+// own contributions and their join along each sequence.
+hipError_t launch_linear_states(const LinearParams &P, hipStream_t stream);
+hipError_t launch_linear_chunk_states(const LinearParams &P, hipStream_t stream);
+
+}  // namespace kdn

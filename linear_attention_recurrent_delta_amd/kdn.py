@@ -9,6 +9,7 @@ is no fallback path.
 from __future__ import annotations
 
 import ctypes
+import dataclasses
 import os
 
 import torch
@@ -33,6 +34,17 @@ DTYPES = {torch.float32: 0, torch.bfloat16: 1}
 STATUS = {0: "KDN_OK", 1: "KDN_ERR_NULL", 2: "KDN_ERR_SHAPE",
           3: "KDN_ERR_UNSUPPORTED", 4: "KDN_ERR_ALIGN", 5: "KDN_ERR_ALIAS",
           6: "KDN_ERR_HIP", 7: "KDN_ERR_WORKSPACE", 8: "KDN_ERR_SCRATCH"}
+
+# kdn_gate values
+GATE_TOKEN, GATE_HEAD = 0, 1
+
+
+class Packed(ctypes.Structure):
+    """kdn_packed of include/kdn.h."""
+    _fields_ = [("tokens", ctypes.c_int), ("block", ctypes.c_int), ("max_blocks", ctypes.c_int),
+                ("pool", ctypes.c_int), ("blocks", ctypes.c_void_p),
+                ("block_offsets", ctypes.c_void_p), ("slots", ctypes.c_void_p)]
+
 
 _lib = None
 
@@ -70,6 +82,19 @@ def load(path: str = LIB_PATH):
     lib.kdn_chunk_prefill_backward.argtypes = [i] * 8 + [f] + [vp] * 21 + [vp, u64, vp]
     lib.kdn_chunk_prefill_backward_workspace_size.restype = u64
     lib.kdn_chunk_prefill_backward_workspace_size.argtypes = [i] * 8 + [ctypes.POINTER(i)]
+    ll, pk = ctypes.c_longlong, ctypes.POINTER(Packed)
+    lib.kdn_sequence_tables.restype = i
+    lib.kdn_sequence_tables.argtypes = [i] * 4 + [vp] * 9
+    lib.kdn_sequence_max_blocks.restype = i
+    lib.kdn_sequence_max_blocks.argtypes = [i] * 3
+    lib.kdn_linear_block.restype = i
+    lib.kdn_linear_block.argtypes = [i] * 3
+    lib.kdn_linear_prefill.restype = i
+    lib.kdn_linear_prefill.argtypes = [i] * 10 + [ll] * 3 + [vp] * 7 + [pk, vp, u64, vp]
+    lib.kdn_linear_prefill_workspace_size.restype = u64
+    lib.kdn_linear_prefill_workspace_size.argtypes = [i] * 6 + [pk, ctypes.POINTER(i)]
+    lib.kdn_linear_decode.restype = i
+    lib.kdn_linear_decode.argtypes = [i] * 9 + [ll] * 3 + [vp] * 5 + [i] + [vp] * 3
     lib.kdn_status_string.restype = ctypes.c_char_p
     lib.kdn_status_string.argtypes = [i]
     lib.kdn_chunk_prefill_chunk_size.restype = i
@@ -411,3 +436,284 @@ def prefill_backward(variant, q, k, v, d_o, alpha=None, beta=None, proc_noise=No
                                out["dbeta"], out["dproc_noise"], out["dobs_noise"],
                                out["dS0"], out["dp0"], workspace, 0, stream)
     return out
+
+
+# ---------------------------------------------------------------------------
+# Linear attention with a decay for each head, and the tables of a packed batch.
+# ---------------------------------------------------------------------------
+@dataclasses.dataclass
+class SequenceTables:
+    """Tables of a packed batch (:func:`sequence_tables`), int32 on the GPU."""
+    tokens: int                          # rows of the packed batch
+    block: int                           # tokens of a block
+    offsets: torch.Tensor                # [N + 1] first row of each sequence
+    block_offsets: torch.Tensor          # [N + 1] first block of each sequence
+    blocks: torch.Tensor                 # [max_blocks, 4]
+    slots: torch.Tensor | None           # [N] state of each sequence (None: n)
+    slot_map: torch.Tensor | None        # [tokens] state of each token
+    positions: torch.Tensor | None       # [tokens] position of each token
+
+
+def _on(x, stream):
+    """(device to make current or None, stream pointer) for a call on x."""
+    dev = x.device
+    if dev.type != "cuda":
+        raise ValueError(f"kdn: tensors must be in GPU memory, not on {dev}")
+    other = dev if dev.index != torch.cuda.current_device() else None
+    if stream is None:
+        return other, torch.cuda.current_stream(dev).cuda_stream
+    return other, _stream(stream)
+
+
+def _call(fn, args, other):
+    if other is None:
+        st = fn(*args)
+    else:
+        with torch.cuda.device(other):
+            st = fn(*args)
+    if st != 0:
+        _check(_lib, st)
+
+
+def _keep(x, stream):
+    """Memory allocated here for a call on another stream stays the call's
+    until that stream is through with it."""
+    if x is not None and stream is not None:
+        p = _stream(stream)
+        if p != torch.cuda.current_stream(x.device).cuda_stream:
+            x.record_stream(torch.cuda.ExternalStream(p, device=x.device))
+    return x
+
+
+def _p(x):
+    return None if x is None else x.data_ptr()
+
+
+def _rows(name, x, lead, dtype, dev):
+    """Checks of a per-token tensor [*lead, heads, d] whose rows may be slices
+    of wider ones; returns the elements between tokens."""
+    if not isinstance(x, torch.Tensor):
+        raise TypeError(f"kdn: {name} must be a tensor")
+    n = len(lead)
+    if x.dim() != n + 2 or tuple(x.shape[:n]) != lead:
+        raise ValueError(f"kdn: {name} has shape {tuple(x.shape)}, expected "
+                         f"{lead + ('heads', 'd')}")
+    if x.dtype != dtype:
+        raise ValueError(f"kdn: {name} has dtype {x.dtype}, expected {dtype}")
+    if x.device != dev:
+        raise ValueError(f"kdn: {name} is on {x.device}, the other tensors on {dev}")
+    heads, d = x.shape[n:]
+    if x.is_contiguous():
+        return heads * d
+    st = x.stride()
+    row = st[n - 1]
+    if st[-1] != 1 or (heads > 1 and st[-2] != d) or row < heads * d or \
+            (n == 2 and lead[0] > 1 and st[0] != lead[1] * row):
+        if n == 2 and lead[1] == 1 and st[-1] == 1 and (heads == 1 or st[-2] == d) \
+                and st[0] >= heads * d:
+            return st[0]                 # one token per sequence: any distance between them
+        raise ValueError(f"kdn: {name} must have contiguous heads and rows at one distance")
+    return row
+
+
+def _gate(log_alpha, lead, H, dtype, dev):
+    if log_alpha.dim() == 1:
+        want, dt, gate = (H,), torch.float32, GATE_HEAD
+    else:
+        want, dt, gate = lead + (H,), dtype, GATE_TOKEN
+    _expect([("log_alpha", log_alpha, want, dt)], dev)
+    return gate
+
+
+def _linear_heads(q, k, v, log_alpha):
+    """States per token: the largest head count of q, k, v and log_alpha."""
+    if not isinstance(log_alpha, torch.Tensor) or log_alpha.dim() == 0:
+        raise TypeError("kdn: log_alpha must be a tensor [.., H]")
+    H = max(q.shape[-2], k.shape[-2], v.shape[-2], log_alpha.shape[-1])
+    for name, x in (("q", q), ("k", k), ("v", v)):
+        if x.shape[-2] == 0 or H % x.shape[-2]:
+            raise ValueError(f"kdn: the {x.shape[-2]} heads of {name} do not divide {H}")
+    return H
+
+
+def linear_block(tokens, N, H):
+    """Tokens of a block for :func:`sequence_tables` of N sequences with
+    ``tokens`` rows in all and H states each."""
+    n = int(load().kdn_linear_block(int(tokens), int(N), int(H)))
+    if n < 0:
+        raise KdnError(2, kdn_status_string(2))
+    return n
+
+
+def sequence_tables(lengths, tokens, block, slots=None, context=None, maps=False, out=None,
+                    stream=None):
+    """Tables of a packed batch of ``tokens`` rows, built on the GPU from the
+    sequences' lengths [N] int32 (on the GPU; nothing is copied to the host).
+    ``block``: tokens of a block, a multiple of 64 (:func:`linear_block`).
+    ``slots`` [N] int32: state of each sequence in a pool; ``context`` [N]
+    int32: tokens each sequence had before.  ``maps``: also the slot and the
+    position of every token.  ``out``: a SequenceTables of the same sizes to
+    fill (for a captured graph).  Returns a :class:`SequenceTables`."""
+    lib = load()
+    if not isinstance(lengths, torch.Tensor) or lengths.dim() != 1:
+        raise ValueError("kdn: lengths must be a tensor [N]")
+    N, dev, i32 = lengths.shape[0], lengths.device, torch.int32
+    tokens, block = int(tokens), int(block)
+    rows = lib.kdn_sequence_max_blocks(N, tokens, block)
+    if rows < 0:
+        raise KdnError(2, f"tokens {tokens} must not be negative, block {block} a positive "
+                          "multiple of 64")
+    other, st = _on(lengths, stream)
+    if out is None:
+        new = lambda *shape: _keep(torch.empty(shape, dtype=i32, device=dev), stream)
+        out = SequenceTables(tokens, block, new(N + 1), new(N + 1), new(rows, 4), slots,
+                             new(tokens) if maps else None, new(tokens) if maps else None)
+    else:
+        out.tokens, out.block, out.slots = tokens, block, slots
+    _expect([("lengths", lengths, (N,), i32), ("slots", slots, (N,), i32),
+             ("context", context, (N,), i32), ("offsets", out.offsets, (N + 1,), i32),
+             ("block_offsets", out.block_offsets, (N + 1,), i32),
+             ("blocks", out.blocks, (rows, 4), i32), ("slot_map", out.slot_map, (tokens,), i32),
+             ("positions", out.positions, (tokens,), i32)], dev)
+    _call(lib.kdn_sequence_tables,
+          (N, tokens, block, rows, _p(lengths), _p(slots), _p(context), _p(out.offsets),
+           _p(out.block_offsets), _p(out.blocks), _p(out.slot_map), _p(out.positions), st), other)
+    return out
+
+
+def _packed(tables, pool, dev):
+    """The kdn_packed of the tables, and the number of sequences."""
+    N, i32 = tables.offsets.shape[0] - 1, torch.int32
+    rows = load().kdn_sequence_max_blocks(N, tables.tokens, tables.block)
+    _expect([("offsets", tables.offsets, (N + 1,), i32),
+             ("block_offsets", tables.block_offsets, (N + 1,), i32),
+             ("blocks", tables.blocks, (rows, 4), i32), ("slots", tables.slots, (N,), i32)], dev)
+    return Packed(tables.tokens, tables.block, rows, pool, _p(tables.blocks),
+                  _p(tables.block_offsets), _p(tables.slots)), N
+
+
+def _linear_sizes(q, tables, S0, S):
+    """(lead, sequences or None, tokens per sequence, states in S0 / S_out)."""
+    if not isinstance(q, torch.Tensor):
+        raise TypeError("kdn: q must be a tensor")
+    if tables is None:
+        if q.dim() != 4:
+            raise ValueError(f"kdn: q has shape {tuple(q.shape)}, expected [B, T, heads, d_k]")
+        return tuple(q.shape[:2]), q.shape[0], q.shape[1], q.shape[0]
+    if q.dim() != 3:
+        raise ValueError(f"kdn: q has shape {tuple(q.shape)}, expected [tokens, heads, d_k]")
+    if q.shape[0] != tables.tokens:
+        raise ValueError(f"kdn: q has {q.shape[0]} rows, the tables {tables.tokens}")
+    for x in (S0, S):
+        if x is not None:
+            return (q.shape[0],), None, 0, x.shape[0]
+    return (q.shape[0],), None, 0, tables.offsets.shape[0] - 1
+
+
+def linear_prefill(q, k, v, log_alpha, S0=None, tables=None, out=None, workspace="auto",
+                   stream=None):
+    """Chunkwise prefill of linear attention with a decay for each head:
+    S_t = exp(log_alpha_t) S_{t-1} + k_t v_t^T, o_t = S_t^T q_t.
+
+    Dense: q [B,T,Hq,dk], k [B,T,Hk,dk], v [B,T,Hv,dv] (float32 or bf16; rows
+    may be slices of one wider tensor), log_alpha [B,T,H] in q's dtype or [H]
+    float32 (one constant per head), S0 [B,H,dk,dv] float32 or None (zeros).
+    H is the largest of the head counts; the others divide it.
+    Packed (``tables`` from :func:`sequence_tables`): the same without B, rows
+    [tokens, ..]; S0 and S_out are pools [P,H,dk,dv] of states by slot.
+    ``out`` may pass (o, S_out); S_out may be S0 (in place) or None (not
+    wanted).  Without it S_out is new, and for a packed batch with S0 the pool
+    S0 itself, updated in place.  Rows of o behind the last sequence are left
+    as they were.  Returns (o, S_out)."""
+    lib = load()
+    dt, dev = q.dtype, q.device
+    if dt not in DTYPES:
+        raise ValueError(f"kdn: q has dtype {dt}, expected float32 or bfloat16")
+    lead, N, T, pool = _linear_sizes(q, tables, S0, out[1] if out is not None else None)
+    qs, ks, vs = (_rows(n, x, lead, dt, dev) for n, x in (("q", q), ("k", k), ("v", v)))
+    H = _linear_heads(q, k, v, log_alpha)
+    dk, dv, f32 = q.shape[-1], v.shape[-1], torch.float32
+    gate = _gate(log_alpha, lead, H, dt, dev)
+    pk = None
+    if tables is not None:
+        pk, N = _packed(tables, pool, dev)
+    if out is None:
+        o = _keep(torch.empty(lead + (H, dv), dtype=dt, device=dev), stream)
+        if tables is None:
+            S = _keep(torch.empty((pool, H, dk, dv), dtype=f32, device=dev), stream)
+        elif S0 is not None:
+            S = S0
+        else:
+            if tables.slots is not None:
+                raise ValueError("kdn: a pool for the tables' slots must be given (S0 or out)")
+            S = _keep(torch.empty((pool, H, dk, dv), dtype=f32, device=dev), stream)
+    else:
+        o, S = out
+    _expect([("k", k, lead + (k.shape[-2], dk), dt)] if k.shape[-1] != dk else [], dev)
+    _expect([("S0", S0, (pool, H, dk, dv), f32), ("o", o, lead + (H, dv), dt),
+             ("S_out", S, (pool, H, dk, dv), f32)], dev)
+    if isinstance(workspace, str):
+        if workspace != "auto":
+            raise ValueError(f"kdn: workspace must be 'auto', None or a tensor, not {workspace!r}")
+        workspace = _keep(linear_workspace(q, k, v, log_alpha, tables), stream)
+    nws = 0
+    if workspace is not None:
+        _expect([("workspace", workspace, (workspace.numel(),), torch.uint8)], dev)
+        nws = workspace.numel()
+    other, st = _on(q, stream)
+    _call(lib.kdn_linear_prefill,
+          (DTYPES[dt], N, T, H, q.shape[-2], k.shape[-2], v.shape[-2], dk, dv, gate, qs, ks, vs,
+           _p(q), _p(k), _p(v), _p(log_alpha), _p(S0), _p(o), _p(S), pk, _p(workspace), nws, st),
+          other)
+    return o, S
+
+
+def linear_workspace(q, k, v, log_alpha, tables=None):
+    """A workspace tensor (uint8) for :func:`linear_prefill` of these inputs,
+    None if none is needed.  Calls that share one must not overlap in time."""
+    lib = load()
+    H = _linear_heads(q, k, v, log_alpha)
+    pk = None
+    if tables is None:
+        N, T = q.shape[:2]
+    else:
+        T = 0
+        pk, N = _packed(tables, 0, q.device)
+    st = ctypes.c_int(0)
+    n = lib.kdn_linear_prefill_workspace_size(DTYPES[q.dtype], N, T, H, q.shape[-1], v.shape[-1],
+                                              pk, ctypes.byref(st))
+    _check(lib, st.value)
+    return torch.empty(n, dtype=torch.uint8, device=q.device) if n else None
+
+
+def linear_decode(q, k, v, log_alpha, S, slots=None, o=None, stream=None):
+    """One token of linear attention for N rows: q [N,Hq,dk], k [N,Hk,dk],
+    v [N,Hv,dv], log_alpha [N,H] in q's dtype or [H] float32.  S [P,H,dk,dv]
+    float32 is a pool of states, updated in place; ``slots`` [N] int32 is each
+    row's state (None: row n).  A row whose slot is not in the pool is skipped,
+    its o left as it was (zero in a new o).  Returns o [N,H,dv]."""
+    lib = load()
+    dt, dev = q.dtype, q.device
+    if dt not in DTYPES:
+        raise ValueError(f"kdn: q has dtype {dt}, expected float32 or bfloat16")
+    if q.dim() != 3:
+        raise ValueError(f"kdn: q has shape {tuple(q.shape)}, expected [N, heads, d_k]")
+    N, lead = q.shape[0], (q.shape[0],)
+    qs, ks, vs = (_rows(n, x, lead, dt, dev) for n, x in (("q", q), ("k", k), ("v", v)))
+    H = _linear_heads(q, k, v, log_alpha)
+    dk, dv = q.shape[-1], v.shape[-1]
+    gate = _gate(log_alpha, lead, H, dt, dev)
+    if not isinstance(S, torch.Tensor) or S.dim() != 4:
+        raise ValueError("kdn: S must be a tensor [P, H, dk, dv]")
+    pool = S.shape[0]
+    if o is None:
+        new = torch.empty if slots is None else torch.zeros
+        o = _keep(new((N, H, dv), dtype=dt, device=dev), stream)
+    _expect([("k", k, (N, k.shape[-2], dk), dt)] if k.shape[-1] != dk else [], dev)
+    _expect([("S", S, (pool, H, dk, dv), torch.float32), ("o", o, (N, H, dv), dt),
+             ("slots", slots, (N,), torch.int32)], dev)
+    other, st = _on(q, stream)
+    _call(lib.kdn_linear_decode,
+          (DTYPES[dt], N, H, q.shape[-2], k.shape[-2], v.shape[-2], dk, dv, gate, qs, ks, vs,
+           _p(q), _p(k), _p(v), _p(log_alpha), _p(slots), pool, _p(S), _p(o), st), other)
+    return o
