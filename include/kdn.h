@@ -482,6 +482,38 @@ kdn_status kdn_linear_decode(kdn_dtype dtype, int N, int H, int Hq, int Hk, int 
                              const void *log_alpha, const int *slots, int pool,
                              float *S, void *o, void *stream);
 
+/*
+ * Gradients of kdn_linear_prefill for a scalar L with cotangents d_o = dL/do
+ * and dS_out = dL/dS_out.
+ *
+ *   q, k, v, log_alpha, S0, packed, strides   as for kdn_linear_prefill
+ *   d_o         [tokens, H, d_v] dtype
+ *   dS_out      shaped as S0, float32, or NULL for zero
+ * Outputs, in the call's dtype (each the sum over the states that share the
+ * head; contiguous):
+ *   dq [tokens, Hq, d_k], dk [tokens, Hk, d_k], dv [tokens, Hv, d_v]
+ *   dlog_alpha  shaped as log_alpha (KDN_GATE_HEAD: [H], the sum over all
+ *               tokens), 0 at a reset; may be NULL (not wanted)
+ *   dS0         shaped as S0, float32, or NULL (not wanted); states without a
+ *               sequence are left as they were
+ *   workspace   as for kdn_linear_prefill, of at least
+ *               kdn_linear_prefill_backward_workspace_size bytes
+ * Outputs overlap no input and no other output.
+ */
+kdn_status kdn_linear_prefill_backward(kdn_dtype dtype, int N, int T, int H, int Hq, int Hk,
+                                       int Hv, int d_k, int d_v, kdn_gate gate,
+                                       long long q_stride, long long k_stride,
+                                       long long v_stride, const void *q, const void *k,
+                                       const void *v, const void *log_alpha, const float *S0,
+                                       const void *d_o, const float *dS_out, void *dq, void *dk,
+                                       void *dv, void *dlog_alpha, float *dS0,
+                                       const kdn_packed *packed, void *workspace,
+                                       unsigned long long workspace_bytes, void *stream);
+
+unsigned long long kdn_linear_prefill_backward_workspace_size(
+    kdn_dtype dtype, int N, int T, int H, int Hq, int Hk, int Hv, int d_k, int d_v,
+    kdn_gate gate, const kdn_packed *packed, kdn_status *status);
+
 /* Static, NUL-terminated description of a status code. */
 const char *kdn_status_string(kdn_status status);
 

@@ -45,6 +45,8 @@ UNITS += [("kdn_prefill.hip", ["-DKDN_PREFILL_DISPATCH"], "kdn_prefill_dispatch.
           # as for the chain: every accumulator of the state is decayed and
           # read as an operand each chunk
           ("kdn_linear.hip", ["-mllvm", "-amdgpu-mfma-vgpr-form"], "kdn_linear.o"),
+          ("kdn_linear_backward.hip", ["-mllvm", "-amdgpu-mfma-vgpr-form"],
+           "kdn_linear_backward.o"),
           ("kdn_linear_decode.hip", [], "kdn_linear_decode.o"),
           ("kdn_tables.hip", [], "kdn_tables.o")]
 

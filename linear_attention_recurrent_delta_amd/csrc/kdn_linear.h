@@ -28,8 +28,8 @@ struct LinearParams {
     int block;              // tokens of a block (a multiple of 64)
     int nblocks;            // dense: blocks of a sequence; packed: rows of `blocks`
     const int *blocks;      // packed: [nblocks][4] first token, tokens, sequence,
-                            // index in the sequence (null: dense)
-    const int *block_offsets;   // packed: [N + 1]
+                            // index in the sequence
+    const int *block_offsets;   // packed: [N + 1] (null: dense)
     const int *slots;       // packed: [N] state of each sequence (null: n)
     long pool;              // states of S0 / S_out
     const float *S0;        // [pool, H, dk, dv], may be null (zero)
@@ -46,10 +46,11 @@ struct LinearParams {
     void *dla;              // [tokens, H] or [H], call dtype, may be null
     float *dS0;             // may be null
     float *ws_rstate;       // [blocks][H][dk * dv], the reverse recurrence's
-    void *ws_chunk;         // [blocks * block / chunk][H][dk * dv] state at every
-                            // chunk's start, call dtype
+    float *ws_rdecay;       // [blocks][H]
+    void *ws_chunk;         // [chunk slots][H][dk * dv] state at every chunk's start,
+                            // call dtype, in fragment order (chunk_slot)
     float *ws_dq, *ws_dk, *ws_dv;   // [tokens, H, d] of shared heads (else null)
-    float *ws_dla;          // [blocks][H] sums of d log_alpha (one decay per head)
+    double *ws_dla;         // [blocks][H] sums of d log_alpha (one decay per head)
 };
 
 struct LinearDecodeParams {
@@ -70,9 +71,16 @@ struct TableParams {
     int *offsets, *block_offsets, *blocks, *slot_map, *positions;
 };
 
+// Place of chunk c of block b in ws_chunk: blocks may end with a part of a
+// chunk, so each adds at most one to the chunks before it.
+__host__ __device__ inline long chunk_slot(long b, long first, int c, int C) {
+    return first / C + b + c;
+}
+inline long chunk_slots(long tokens, long blocks, int C) { return tokens / C + blocks + 1; }
+
 // Blocks of all sequences, for grids and workspaces.
 inline long linear_total_blocks(const LinearParams &P) {
-    return P.blocks ? (long)P.nblocks : (long)P.N * P.nblocks;
+    return P.block_offsets ? (long)P.nblocks : (long)P.N * P.nblocks;
 }
 
 hipError_t launch_linear_prefill(const LinearParams &P, hipStream_t stream);
@@ -81,8 +89,10 @@ hipError_t launch_linear_backward(const LinearParams &P, hipStream_t stream);
 hipError_t launch_sequence_tables(const TableParams &P, hipStream_t stream);
 
 // Passes shared by the prefill and its gradients (kdn_linear.hip): the blocks'
-// own contributions and their join along each sequence.
+// own contributions and their join along each sequence, forward (ws_state) and
+// reverse (ws_rstate), and the state at every chunk's start (ws_chunk).
 hipError_t launch_linear_states(const LinearParams &P, hipStream_t stream);
+hipError_t launch_linear_reverse_states(const LinearParams &P, hipStream_t stream);
 hipError_t launch_linear_chunk_states(const LinearParams &P, hipStream_t stream);
 
 }  // namespace kdn

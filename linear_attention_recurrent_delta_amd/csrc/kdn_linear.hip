@@ -24,7 +24,12 @@
 namespace kdn {
 namespace lin {
 
-enum Mode { OWN = 0, OUT = 1, CHUNKS = 2 };
+// OWN: a block's own contribution to the state; ROWN: to the state of the
+// reverse recurrence R <- e^{G_C} R + sum_i e^{G_i} q_i do_i^T, chunks last to
+// first (q and do in the places of k and v); OUT: outputs; CHUNKS: the state
+// at every chunk's start, transposed (k and v change places, so that a lane
+// holds runs of d_v and stores whole fragments).
+enum Mode { OWN = 0, OUT = 1, CHUNKS = 2, ROWN = 3 };
 
 constexpr int NT = 256;
 
@@ -64,7 +69,16 @@ struct StateAcc {
                 for (int r = 0; r < 4; ++r)
                     t[i][c][r] = S[(16 * i + 4 * g + r) * DV + col(w, c, n)];
     }
-    template <typename TO> __device__ __forceinline__ void store(TO *S, int w, int lane) const {
+    // from the transposed matrix [DV][DK]
+    __device__ __forceinline__ void load_t(const float *S, int w, int lane) {
+        const int g = lane >> 4, n = lane & 15;
+#pragma unroll
+        for (int i = 0; i < SH::TK; ++i)
+#pragma unroll
+            for (int c = 0; c < SH::NC; ++c)
+                t[i][c] = *reinterpret_cast<const f32x4 *>(S + col(w, c, n) * DK + 16 * i + 4 * g);
+    }
+    __device__ __forceinline__ void store(float *S, int w, int lane) const {
         const int g = lane >> 4, n = lane & 15;
 #pragma unroll
         for (int i = 0; i < SH::TK; ++i)
@@ -72,7 +86,17 @@ struct StateAcc {
             for (int c = 0; c < SH::NC; ++c)
 #pragma unroll
                 for (int r = 0; r < 4; ++r)
-                    S[(16 * i + 4 * g + r) * DV + col(w, c, n)] = from_f32<TO>(t[i][c][r]);
+                    S[(16 * i + 4 * g + r) * DV + col(w, c, n)] = t[i][c][r];
+    }
+    // operand fragments [column tile][32 rows][lane], rounded to T: the
+    // products that read them round the same state in the prefill
+    __device__ __forceinline__ void store_frags(T *S, int w, int lane) const {
+#pragma unroll
+        for (int c = 0; c < SH::NC; ++c)
+#pragma unroll
+            for (int s = 0; s < DK / 32; ++s)
+                reinterpret_cast<FragV<T> *>(S)[((w * SH::NC + c) * (DK / 32) + s) * WAVE + lane] =
+                    frag_acc<T>(t[2 * s][c], t[2 * s + 1][c]);
     }
 };
 
@@ -93,12 +117,27 @@ __global__ __launch_bounds__(NT, 2) void linear_kernel(LinearParams P) {
     const long b = blockIdx.x / P.H;
     const int h = blockIdx.x % P.H;
     const Block B = get_block(P, b);
-    if (B.count == 0 || (MODE == OWN && B.last))
+    if (B.count == 0 || B.slot < 0 || (MODE == OWN && B.last) || (MODE == ROWN && B.index == 0))
         return;
 
-    const T *q = static_cast<const T *>(P.q) + B.first * P.q_stride + (h / (P.H / P.Hq)) * DK;
-    const T *k = static_cast<const T *>(P.k) + B.first * P.k_stride + (h / (P.H / P.Hk)) * DK;
-    const T *v = static_cast<const T *>(P.v) + B.first * P.v_stride + (h / (P.H / P.Hv)) * DV;
+    constexpr int HK = MODE == CHUNKS ? DV : DK, HV = MODE == CHUNKS ? DK : DV;
+    const T *q = static_cast<const T *>(P.q) + B.first * P.q_stride + (h / (P.H / P.Hq)) * HK;
+    const T *k = static_cast<const T *>(P.k) + B.first * P.k_stride + (h / (P.H / P.Hk)) * HK;
+    const T *v = static_cast<const T *>(P.v) + B.first * P.v_stride + (h / (P.H / P.Hv)) * HV;
+    long ks = P.k_stride, vs = P.v_stride;
+    if (MODE == CHUNKS) {
+        const T *x = k;
+        k = v;
+        v = x;
+        ks = P.v_stride;
+        vs = P.k_stride;
+    }
+    if (MODE == ROWN) {
+        k = q;
+        ks = P.q_stride;
+        vs = (long)P.H * DV;
+        v = static_cast<const T *>(P.d_o) + B.first * vs + h * DV;
+    }
 
     TileRegs<T, C, DK, NT> qr, kr;
     TileRegs<T, C, DV, NT> vr;
@@ -109,29 +148,31 @@ __global__ __launch_bounds__(NT, 2) void linear_kernel(LinearParams P) {
     };
     auto load_chunk = [&](int c) {
         const int cnt = B.count - c * C;
-        kr.load(k + (long)c * C * P.k_stride, P.k_stride, cnt, tid);
-        vr.load(v + (long)c * C * P.v_stride, P.v_stride, cnt, tid);
+        kr.load(k + (long)c * C * ks, ks, cnt, tid);
+        vr.load(v + (long)c * C * vs, vs, cnt, tid);
         if (MODE == OUT)
             qr.load(q + (long)c * C * P.q_stride, P.q_stride, cnt, tid);
     };
-    load_chunk(0);
+    // the chunk of step i
+    auto chunk = [&](int i) { return MODE == ROWN ? nchunk - 1 - i : i; };
+    load_chunk(chunk(0));
     float la0 = 0.f, la1 = 0.f;
     if (w == 0) {
-        la0 = gate(0);
-        la1 = gate(1);
+        la0 = gate(chunk(0));
+        la1 = nchunk > 1 ? gate(chunk(1)) : 0.f;
     }
 
     StateAcc<T, DK, DV> S;
     const long sidx = (b * P.H + h) * (long)(DK * DV);
-    if (MODE == OWN) {
+    const float *start = B.single ? P.S0 : P.ws_state;
+    if (start)
+        start += B.single ? (B.slot * P.H + h) * (long)(DK * DV) : sidx;
+    if (MODE == OWN || MODE == ROWN || !start)
         S.zero();
-    } else if (!B.single) {
-        S.load(P.ws_state + sidx, w, lane);
-    } else if (P.S0) {
-        S.load(P.S0 + (B.slot * P.H + h) * (long)(DK * DV), w, lane);
-    } else {
-        S.zero();
-    }
+    else if (MODE == CHUNKS)
+        S.load_t(start, w, lane);
+    else
+        S.load(start, w, lane);
 
     if (MODE == OUT) {
         // the 16 x 16 tiles right of the diagonal inside a step of 32 tokens
@@ -143,22 +184,22 @@ __global__ __launch_bounds__(NT, 2) void linear_kernel(LinearParams P) {
     if (w == 0)
         total = chunk_decays<C>(D[0], la0, lane);
 
-    for (int c = 0; c < nchunk; ++c) {
-        const Decays<C> &dc = D[c & 1];
+    for (int step = 0; step < nchunk; ++step) {
+        const int c = chunk(step);
+        const Decays<C> &dc = D[step & 1];
         const int cnt = B.count - c * C;       // tokens from here on
         kr.template store<PK>(Ks, tid);
         vr.template store<PV>(Vs, tid);
         if (MODE == OUT)
             qr.template store<PK>(Qs, tid);
         __syncthreads();
-        if (c + 1 < nchunk)
-            load_chunk(c + 1);
+        if (step + 1 < nchunk)
+            load_chunk(chunk(step + 1));
 
-        if (MODE == CHUNKS) {
-            T *dst = static_cast<T *>(P.ws_chunk) +
-                     ((b * (P.block / C) + c) * P.H + h) * (long)(DK * DV);
-            S.store(dst, w, lane);
-        }
+        if (MODE == CHUNKS)
+            S.store_frags(static_cast<T *>(P.ws_chunk) +
+                              (chunk_slot(b, B.first, c, C) * P.H + h) * (long)(DK * DV),
+                          w, lane);
 
         f32x4 o[IT][NC];
         if (MODE == OUT) {
@@ -218,9 +259,9 @@ __global__ __launch_bounds__(NT, 2) void linear_kernel(LinearParams P) {
             }
         }
         if (w == 0) {               // the next chunk's decays
-            if (c + 1 < nchunk)
-                total += chunk_decays<C>(D[(c + 1) & 1], la1, lane);
-            la1 = gate(c + 2);
+            if (step + 1 < nchunk)
+                total += chunk_decays<C>(D[(step + 1) & 1], la1, lane);
+            la1 = step + 2 < nchunk ? gate(chunk(step + 2)) : 0.f;
         }
         if (MODE == OUT)
             __syncthreads();        // P
@@ -248,7 +289,7 @@ __global__ __launch_bounds__(NT, 2) void linear_kernel(LinearParams P) {
                 }
             }
             float wt[8];
-            lds_ld8(dc.out + 32 * s + 8 * g, wt);
+            lds_ld8((MODE == ROWN ? dc.in : dc.out) + 32 * s + 8 * g, wt);
             const Split<T> v0(vf[0], wt);
             const Split<T> v1(vf[NC - 1], wt);
 #pragma unroll
@@ -281,10 +322,10 @@ __global__ __launch_bounds__(NT, 2) void linear_kernel(LinearParams P) {
         }
         __syncthreads();            // the chunk's tiles have been read
     }
-    if (MODE == OWN) {
-        S.store(P.ws_state + sidx, w, lane);
+    if (MODE == OWN || MODE == ROWN) {
+        S.store((MODE == OWN ? P.ws_state : P.ws_rstate) + sidx, w, lane);
         if (tid == 0)
-            P.ws_decay[b * P.H + h] = exp2_fast((float)total);
+            (MODE == OWN ? P.ws_decay : P.ws_rdecay)[b * P.H + h] = exp2_fast((float)total);
     }
     if (MODE == OUT && B.last && P.S_out)
         S.store(P.S_out + (B.slot * P.H + h) * (long)(DK * DV), w, lane);
@@ -292,12 +333,15 @@ __global__ __launch_bounds__(NT, 2) void linear_kernel(LinearParams P) {
 
 // ---------------------------------------------------------------------------
 // Join of the blocks along each sequence: block b's own contribution U_b in
-// ws_state becomes the state at its start.  One thread holds 4 values of S of
-// one (sequence, head); the blocks' values are loaded JOIN ahead.  A sequence
-// of one block has nothing to join, one without tokens passes S0 on.
+// ws_state becomes the state at its start (REV: in ws_rstate, the reverse
+// state behind its end, blocks last to first).  One thread holds 4 values of S
+// of one (sequence, head); the blocks' values are loaded JOIN ahead.  A
+// sequence of one block has nothing to join, one without tokens passes its
+// state on.
 // ---------------------------------------------------------------------------
 constexpr int JOIN = 8;
 
+template <bool REV>
 __global__ __launch_bounds__(NT) void linear_join_kernel(LinearParams P, int pieces) {
     const long id = blockIdx.x;
     const int piece = id % pieces;
@@ -306,38 +350,44 @@ __global__ __launch_bounds__(NT) void linear_join_kernel(LinearParams P, int pie
     const int e = (piece * NT + threadIdx.x) * 4;
     const long size = (long)P.dk * P.dv;
     long b0 = (long)seq * P.nblocks, b1 = b0 + P.nblocks, slot = seq;
-    if (P.blocks) {
+    if (P.block_offsets) {
         b0 = P.block_offsets[seq];
         b1 = P.block_offsets[seq + 1];
         slot = P.slots ? P.slots[seq] : seq;
         if (b0 < 0 || b1 > P.nblocks || slot < 0 || slot >= P.pool)
             return;
     }
-    if (b1 - b0 == 1)
+    const long nb = b1 - b0;
+    if (nb == 1)
         return;
+    const float *first = REV ? P.dS_out : P.S0;
+    float *pass = REV ? P.dS0 : P.S_out;
+    float *ws = REV ? P.ws_rstate : P.ws_state;
+    const float *decay = REV ? P.ws_rdecay : P.ws_decay;
     const long at = (slot * P.H + h) * size + e;
     f32x4 s = {0.f, 0.f, 0.f, 0.f};
-    if (P.S0)
-        s = *reinterpret_cast<const f32x4 *>(P.S0 + at);
-    if (b1 <= b0) {
-        if (P.S_out && P.S_out != P.S0)
-            *reinterpret_cast<f32x4 *>(P.S_out + at) = s;
+    if (first)
+        s = *reinterpret_cast<const f32x4 *>(first + at);
+    if (nb <= 0) {
+        if (pass && pass != first)
+            *reinterpret_cast<f32x4 *>(pass + at) = s;
         return;
     }
-    for (long b = b0; b < b1; b += JOIN) {
+    auto block = [&](long i) { return (REV ? b1 - 1 - i : b0 + i) * P.H + h; };
+    for (long j = 0; j < nb; j += JOIN) {
         f32x4 u[JOIN];
         float a[JOIN];
 #pragma unroll
         for (int i = 0; i < JOIN; ++i)
-            if (b + i < b1 - 1) {
-                u[i] = *reinterpret_cast<const f32x4 *>(P.ws_state + ((b + i) * P.H + h) * size + e);
-                a[i] = P.ws_decay[(b + i) * P.H + h];
+            if (j + i < nb - 1) {
+                u[i] = *reinterpret_cast<const f32x4 *>(ws + block(j + i) * size + e);
+                a[i] = decay[block(j + i)];
             }
 #pragma unroll
         for (int i = 0; i < JOIN; ++i)
-            if (b + i < b1) {
-                *reinterpret_cast<f32x4 *>(P.ws_state + ((b + i) * P.H + h) * size + e) = s;
-                if (b + i < b1 - 1)
+            if (j + i < nb) {
+                *reinterpret_cast<f32x4 *>(ws + block(j + i) * size + e) = s;
+                if (j + i < nb - 1)
                     s = s * a[i] + u[i];
             }
     }
@@ -346,8 +396,10 @@ __global__ __launch_bounds__(NT) void linear_join_kernel(LinearParams P, int pie
 template <typename T, int MODE>
 static hipError_t launch_mode(const LinearParams &P, hipStream_t st) {
     const dim3 grid((unsigned)(linear_total_blocks(P) * P.H)), block(NT);
+    // rows and columns of the state the mode works on
+    const int rows = MODE == CHUNKS ? P.dv : P.dk, cols = MODE == CHUNKS ? P.dk : P.dv;
 #define KDN_LIN(DK_, DV_)                                                              \
-    if (P.dk == DK_ && P.dv == DV_) {                                                  \
+    if (rows == DK_ && cols == DV_) {                                                  \
         hipLaunchKernelGGL((linear_kernel<T, DK_, DV_, MODE>), grid, block, 0, st, P); \
         return hipGetLastError();                                                      \
     }
@@ -359,20 +411,31 @@ static hipError_t launch_mode(const LinearParams &P, hipStream_t st) {
     return hipErrorInvalidValue;
 }
 
+// The blocks' own contributions and their join, where a sequence may have more
+// than one block; the join also passes on the states of empty sequences.
+template <bool REV> static hipError_t launch_states(const LinearParams &P, hipStream_t st) {
+    constexpr int MODE = REV ? ROWN : OWN;
+    hipError_t e = hipSuccess;
+    if (!P.block_offsets && P.nblocks == 1)
+        return e;
+    if (linear_total_blocks(P) > 0)
+        e = P.bf16 ? launch_mode<bf16, MODE>(P, st) : launch_mode<float, MODE>(P, st);
+    if (e != hipSuccess)
+        return e;
+    const int pieces = P.dk * P.dv / (4 * NT);
+    const dim3 grid((unsigned)((long)P.N * P.H * pieces)), block(NT);
+    hipLaunchKernelGGL((linear_join_kernel<REV>), grid, block, 0, st, P, pieces);
+    return hipGetLastError();
+}
+
 }  // namespace lin
 
-// States at the blocks' starts, where a sequence may have more than one block.
 hipError_t launch_linear_states(const LinearParams &P, hipStream_t st) {
-    hipError_t e = hipSuccess;
-    if (linear_total_blocks(P) > 0 && (P.blocks || P.nblocks > 1))
-        e = P.bf16 ? lin::launch_mode<bf16, lin::OWN>(P, st) : lin::launch_mode<float, lin::OWN>(P, st);
-    if (e == hipSuccess && (P.blocks || P.nblocks != 1)) {
-        const int pieces = P.dk * P.dv / (4 * lin::NT);
-        const dim3 grid((unsigned)((long)P.N * P.H * pieces)), block(lin::NT);
-        hipLaunchKernelGGL(lin::linear_join_kernel, grid, block, 0, st, P, pieces);
-        e = hipGetLastError();
-    }
-    return e;
+    return lin::launch_states<false>(P, st);
+}
+
+hipError_t launch_linear_reverse_states(const LinearParams &P, hipStream_t st) {
+    return lin::launch_states<true>(P, st);
 }
 
 hipError_t launch_linear_chunk_states(const LinearParams &P, hipStream_t st) {

@@ -278,4 +278,132 @@ kdn_status kdn_linear_decode(kdn_dtype dtype, int N, int H, int Hq, int Hk, int 
     return e == hipSuccess ? KDN_OK : KDN_ERR_HIP;
 }
 
+// ---------------------------------------------------------------------------
+// Gradients.
+// ---------------------------------------------------------------------------
+namespace {
+// Workspace, sections 256-byte aligned: the forward and the reverse states at
+// the blocks' ends with the blocks' decays (sequences of several blocks), the
+// state at every chunk's start, float32 gradients of shared heads before their
+// sum, and for one decay per head each block's sum.
+struct GradWs {
+    long long state, decay, rstate, rdecay, chunk, dq, dk, dv, dla, total;
+};
+GradWs grad_ws(const kdn::LinearParams &P, bool packed) {
+    GradWs w{};
+    const long long blocks = packed ? P.nblocks : (long long)P.N * P.nblocks;
+    if (blocks * P.H == 0)
+        return w;
+    const long long n_S = (long long)P.dk * P.dv, es = P.bf16 ? 2 : 4;
+    long long o = 0;
+    auto take = [&](long long n) {
+        const long long at = o;
+        o += up256(n);
+        return at;
+    };
+    if (packed || P.nblocks > 1) {
+        w.state = take(blocks * P.H * n_S * 4);
+        w.decay = take(blocks * P.H * 4);
+        w.rstate = take(blocks * P.H * n_S * 4);
+        w.rdecay = take(blocks * P.H * 4);
+    }
+    w.chunk = take(kdn::chunk_slots(P.tokens, blocks, kdn::linear_chunk(P.bf16)) * P.H * n_S * es);
+    if (P.Hq != P.H)
+        w.dq = take(P.tokens * P.H * P.dk * 4);
+    if (P.Hk != P.H)
+        w.dk = take(P.tokens * P.H * P.dk * 4);
+    if (P.Hv != P.H)
+        w.dv = take(P.tokens * P.H * P.dv * 4);
+    if (P.gate == KDN_GATE_HEAD)
+        w.dla = take(blocks * P.H * 8);
+    w.total = o;
+    return w;
+}
+}  // namespace
+
+unsigned long long kdn_linear_prefill_backward_workspace_size(
+    kdn_dtype dtype, int N, int T, int H, int Hq, int Hk, int Hv, int d_k, int d_v, kdn_gate gate,
+    const kdn_packed *packed, kdn_status *status) {
+    kdn::LinearParams P;
+    const kdn_status st = linear_shape(P, dtype, N, T, H, Hq, Hk, Hv, d_k, d_v, gate, packed);
+    if (status)
+        *status = st;
+    return st == KDN_OK ? (unsigned long long)grad_ws(P, packed != nullptr).total : 0;
+}
+
+kdn_status kdn_linear_prefill_backward(kdn_dtype dtype, int N, int T, int H, int Hq, int Hk,
+                                       int Hv, int d_k, int d_v, kdn_gate gate,
+                                       long long q_stride, long long k_stride,
+                                       long long v_stride, const void *q, const void *k,
+                                       const void *v, const void *log_alpha, const float *S0,
+                                       const void *d_o, const float *dS_out, void *dq, void *dk,
+                                       void *dv, void *dlog_alpha, float *dS0,
+                                       const kdn_packed *packed, void *workspace,
+                                       unsigned long long workspace_bytes, void *stream) {
+    kdn::LinearParams P;
+    if (kdn_status st = linear_shape(P, dtype, N, T, H, Hq, Hk, Hv, d_k, d_v, gate, packed))
+        return st;
+    const long long es = P.bf16 ? 2 : 4, tok = P.tokens;
+    if (kdn_status st = token_stride(q_stride, (long long)Hq * d_k, es, &P.q_stride)) return st;
+    if (kdn_status st = token_stride(k_stride, (long long)Hk * d_k, es, &P.k_stride)) return st;
+    if (kdn_status st = token_stride(v_stride, (long long)Hv * d_v, es, &P.v_stride)) return st;
+    if (tok * H > 0 && (!q || !k || !v || !log_alpha || !d_o || !dq || !dk || !dv))
+        return KDN_ERR_NULL;
+    if (kdn_status st = packed_tables(P, packed))
+        return st;
+    for (const void *x : {q, k, v, (const void *)S0, d_o, (const void *)dS_out, (const void *)dq,
+                          (const void *)dk, (const void *)dv, (const void *)dS0})
+        if (!aligned(x, 16))
+            return KDN_ERR_ALIGN;
+    if (!aligned(log_alpha, gate == KDN_GATE_HEAD ? 4 : es) || !aligned(dlog_alpha, es))
+        return KDN_ERR_ALIGN;
+    const long long n_S = P.pool * H * d_k * d_v * 4;
+    const long long n_la = gate == KDN_GATE_HEAD ? 4LL * H : tok * H * es;
+    const Range ins[] = {{q, span(tok, P.q_stride, (long long)Hq * d_k, es)},
+                         {k, span(tok, P.k_stride, (long long)Hk * d_k, es)},
+                         {v, span(tok, P.v_stride, (long long)Hv * d_v, es)},
+                         {log_alpha, n_la},
+                         {P.blocks, packed ? 16LL * P.nblocks : 0},
+                         {P.block_offsets, packed ? 4LL * (N + 1) : 0},
+                         {P.slots, packed ? 4LL * N : 0},
+                         {S0, n_S},
+                         {d_o, tok * H * d_v * es},
+                         {dS_out, n_S}};
+    const Range outs[] = {{dq, tok * Hq * d_k * es},
+                          {dk, tok * Hk * d_k * es},
+                          {dv, tok * Hv * d_v * es},
+                          {dlog_alpha, gate == KDN_GATE_HEAD ? H * es : tok * H * es},
+                          {dS0, n_S}};
+    if (clash(outs, 5, ins, 10))
+        return KDN_ERR_ALIAS;
+    const GradWs w = grad_ws(P, packed != nullptr);
+    if (w.total > 0) {
+        if (!workspace || workspace_bytes < (unsigned long long)w.total)
+            return KDN_ERR_WORKSPACE;
+        if (!aligned(workspace, 256))
+            return KDN_ERR_ALIGN;
+        const Range ws[] = {{workspace, w.total}};
+        if (clash(ws, 1, ins, 10) || clash(ws, 1, outs, 5))
+            return KDN_ERR_ALIAS;
+        char *base = static_cast<char *>(workspace);
+        auto f32 = [&](long long at) { return reinterpret_cast<float *>(base + at); };
+        if (packed || P.nblocks > 1) {
+            P.ws_state = f32(w.state);
+            P.ws_decay = f32(w.decay);
+            P.ws_rstate = f32(w.rstate);
+            P.ws_rdecay = f32(w.rdecay);
+        }
+        P.ws_chunk = base + w.chunk;
+        P.ws_dq = Hq != H ? f32(w.dq) : nullptr;
+        P.ws_dk = Hk != H ? f32(w.dk) : nullptr;
+        P.ws_dv = Hv != H ? f32(w.dv) : nullptr;
+        P.ws_dla = gate == KDN_GATE_HEAD ? reinterpret_cast<double *>(base + w.dla) : nullptr;
+    }
+    P.q = q; P.k = k; P.v = v; P.la = log_alpha;
+    P.S0 = S0; P.d_o = d_o; P.dS_out = dS_out;
+    P.dq = dq; P.dk_ = dk; P.dv_ = dv; P.dla = dlog_alpha; P.dS0 = dS0;
+    const hipError_t e = kdn::launch_linear_backward(P, static_cast<hipStream_t>(stream));
+    return e == hipSuccess ? KDN_OK : KDN_ERR_HIP;
+}
+
 }  // extern "C"

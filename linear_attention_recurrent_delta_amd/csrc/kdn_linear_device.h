@@ -22,7 +22,7 @@ struct Block {
     int seq;         // sequence
     int index, last; // index in the sequence; 1 if it is the sequence's last
     int single;      // 1: the sequence has this block only
-    long slot;       // state of the sequence
+    long slot;       // state of the sequence, -1: the sequence is skipped
 };
 
 // Row b of the blocks.  Packed tables are device data that the host cannot
@@ -30,7 +30,7 @@ struct Block {
 __device__ __forceinline__ Block get_block(const LinearParams &P, long b) {
     Block B;
     B.count = 0;
-    if (!P.blocks) {
+    if (!P.block_offsets) {
         B.seq = (int)(b / P.nblocks);
         B.index = (int)(b - (long)B.seq * P.nblocks);
         const int t0 = B.index * P.block;
@@ -49,8 +49,8 @@ __device__ __forceinline__ Block get_block(const LinearParams &P, long b) {
     if (b0 < 0 || b1 > P.nblocks || (long)b0 + r.w != b || b1 <= b)
         return B;
     B.slot = P.slots ? P.slots[r.z] : r.z;
-    if (B.slot < 0 || B.slot >= P.pool)
-        return B;
+    if (B.slot >= P.pool)
+        B.slot = -1;
     B.first = r.x;
     B.seq = r.z;
     B.index = r.w;
@@ -136,6 +136,27 @@ __device__ __forceinline__ f32x8 frag_cols(const float *m, int c0, int cs, int l
 #pragma unroll
     for (int e = 0; e < 8; ++e)
         f[e] = p[e * PITCH];
+    return f;
+}
+
+// As frag_cols, rows 4 g .. + 3 and 16 + 4 g .. + 3 (the order of frag_acc).
+template <int PITCH>
+__device__ __forceinline__ bf16x8 frag_cols_perm(const bf16 *m, int c0, int cs, int lane) {
+    const int g = lane >> 4, i = lane & 15;
+    const bf16 *p = m + (4 * g + i / 4) * PITCH + c0 + cs * (i & 3);
+    union { s16x4 s[2]; bf16x8 v; } u;
+    u.s[0] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4 *)p);
+    u.s[1] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4 *)(p + 16 * PITCH));
+    return u.v;
+}
+template <int PITCH>
+__device__ __forceinline__ f32x8 frag_cols_perm(const float *m, int c0, int cs, int lane) {
+    const int g = lane >> 4, n = lane & 15;
+    const float *p = m + 4 * g * PITCH + c0 + cs * (n >> 2) + (n & 3);
+    f32x8 f;
+#pragma unroll
+    for (int e = 0; e < 8; ++e)
+        f[e] = p[(e + (e & 4 ? 12 : 0)) * PITCH];
     return f;
 }
 

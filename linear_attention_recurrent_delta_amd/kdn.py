@@ -93,6 +93,10 @@ def load(path: str = LIB_PATH):
     lib.kdn_linear_prefill.argtypes = [i] * 10 + [ll] * 3 + [vp] * 7 + [pk, vp, u64, vp]
     lib.kdn_linear_prefill_workspace_size.restype = u64
     lib.kdn_linear_prefill_workspace_size.argtypes = [i] * 6 + [pk, ctypes.POINTER(i)]
+    lib.kdn_linear_prefill_backward.restype = i
+    lib.kdn_linear_prefill_backward.argtypes = [i] * 10 + [ll] * 3 + [vp] * 12 + [pk, vp, u64, vp]
+    lib.kdn_linear_prefill_backward_workspace_size.restype = u64
+    lib.kdn_linear_prefill_backward_workspace_size.argtypes = [i] * 10 + [pk, ctypes.POINTER(i)]
     lib.kdn_linear_decode.restype = i
     lib.kdn_linear_decode.argtypes = [i] * 9 + [ll] * 3 + [vp] * 5 + [i] + [vp] * 3
     lib.kdn_status_string.restype = ctypes.c_char_p
@@ -475,14 +479,20 @@ def _call(fn, args, other):
         _check(_lib, st)
 
 
-def _keep(x, stream):
-    """Memory allocated here for a call on another stream stays the call's
-    until that stream is through with it."""
-    if x is not None and stream is not None:
-        p = _stream(stream)
-        if p != torch.cuda.current_stream(x.device).cuda_stream:
-            x.record_stream(torch.cuda.ExternalStream(p, device=x.device))
-    return x
+def _new(shape, dtype, dev, stream, zero=False):
+    """New memory for a call on ``stream``, allocated (and cleared) as under
+    ``torch.cuda.stream(stream)``: memory of the current stream's pool could
+    still be in use there."""
+    if dev.type != "cuda":
+        raise ValueError(f"kdn: tensors must be in GPU memory, not on {dev}")
+    make = torch.zeros if zero else torch.empty
+    if stream is None:
+        return make(shape, dtype=dtype, device=dev)
+    if isinstance(stream, int):
+        stream = torch.cuda.ExternalStream(stream, device=dev) if stream \
+            else torch.cuda.default_stream(dev)
+    with torch.cuda.stream(stream):
+        return make(shape, dtype=dtype, device=dev)
 
 
 def _p(x):
@@ -565,7 +575,7 @@ def sequence_tables(lengths, tokens, block, slots=None, context=None, maps=False
                           "multiple of 64")
     other, st = _on(lengths, stream)
     if out is None:
-        new = lambda *shape: _keep(torch.empty(shape, dtype=i32, device=dev), stream)
+        new = lambda *shape: _new(shape, i32, dev, stream)
         out = SequenceTables(tokens, block, new(N + 1), new(N + 1), new(rows, 4), slots,
                              new(tokens) if maps else None, new(tokens) if maps else None)
     else:
@@ -638,15 +648,15 @@ def linear_prefill(q, k, v, log_alpha, S0=None, tables=None, out=None, workspace
     if tables is not None:
         pk, N = _packed(tables, pool, dev)
     if out is None:
-        o = _keep(torch.empty(lead + (H, dv), dtype=dt, device=dev), stream)
+        o = _new(lead + (H, dv), dt, dev, stream)
         if tables is None:
-            S = _keep(torch.empty((pool, H, dk, dv), dtype=f32, device=dev), stream)
+            S = _new((pool, H, dk, dv), f32, dev, stream)
         elif S0 is not None:
             S = S0
         else:
             if tables.slots is not None:
                 raise ValueError("kdn: a pool for the tables' slots must be given (S0 or out)")
-            S = _keep(torch.empty((pool, H, dk, dv), dtype=f32, device=dev), stream)
+            S = _new((pool, H, dk, dv), f32, dev, stream)
     else:
         o, S = out
     _expect([("k", k, lead + (k.shape[-2], dk), dt)] if k.shape[-1] != dk else [], dev)
@@ -655,7 +665,7 @@ def linear_prefill(q, k, v, log_alpha, S0=None, tables=None, out=None, workspace
     if isinstance(workspace, str):
         if workspace != "auto":
             raise ValueError(f"kdn: workspace must be 'auto', None or a tensor, not {workspace!r}")
-        workspace = _keep(linear_workspace(q, k, v, log_alpha, tables), stream)
+        workspace = linear_workspace(q, k, v, log_alpha, tables, stream)
     nws = 0
     if workspace is not None:
         _expect([("workspace", workspace, (workspace.numel(),), torch.uint8)], dev)
@@ -668,7 +678,7 @@ def linear_prefill(q, k, v, log_alpha, S0=None, tables=None, out=None, workspace
     return o, S
 
 
-def linear_workspace(q, k, v, log_alpha, tables=None):
+def linear_workspace(q, k, v, log_alpha, tables=None, stream=None):
     """A workspace tensor (uint8) for :func:`linear_prefill` of these inputs,
     None if none is needed.  Calls that share one must not overlap in time."""
     lib = load()
@@ -683,7 +693,7 @@ def linear_workspace(q, k, v, log_alpha, tables=None):
     n = lib.kdn_linear_prefill_workspace_size(DTYPES[q.dtype], N, T, H, q.shape[-1], v.shape[-1],
                                               pk, ctypes.byref(st))
     _check(lib, st.value)
-    return torch.empty(n, dtype=torch.uint8, device=q.device) if n else None
+    return _new((n,), torch.uint8, q.device, stream) if n else None
 
 
 def linear_decode(q, k, v, log_alpha, S, slots=None, o=None, stream=None):
@@ -707,8 +717,7 @@ def linear_decode(q, k, v, log_alpha, S, slots=None, o=None, stream=None):
         raise ValueError("kdn: S must be a tensor [P, H, dk, dv]")
     pool = S.shape[0]
     if o is None:
-        new = torch.empty if slots is None else torch.zeros
-        o = _keep(new((N, H, dv), dtype=dt, device=dev), stream)
+        o = _new((N, H, dv), dt, dev, stream, zero=slots is not None)
     _expect([("k", k, (N, k.shape[-2], dk), dt)] if k.shape[-1] != dk else [], dev)
     _expect([("S", S, (pool, H, dk, dv), torch.float32), ("o", o, (N, H, dv), dt),
              ("slots", slots, (N,), torch.int32)], dev)
@@ -717,3 +726,62 @@ def linear_decode(q, k, v, log_alpha, S, slots=None, o=None, stream=None):
           (DTYPES[dt], N, H, q.shape[-2], k.shape[-2], v.shape[-2], dk, dv, gate, qs, ks, vs,
            _p(q), _p(k), _p(v), _p(log_alpha), _p(slots), pool, _p(S), _p(o), st), other)
     return o
+
+
+def linear_prefill_backward(q, k, v, d_o, log_alpha, S0=None, dS_out=None, tables=None, out=None,
+                            workspace=None, stream=None):
+    """Gradients of :func:`linear_prefill` for the cotangents d_o (shaped as o)
+    and dS_out (shaped as S_out; None: zero).  Returns a dict of dq, dk, dv
+    (shaped as q, k, v, contiguous) and dlog_alpha ([..,H], or [H] for one
+    decay per head) in q's dtype, and dS0 float32.  A head that several states
+    share gets the sum of their gradients; rows behind the last sequence of a
+    packed batch get zero, and so do states of dS0 without a sequence.  ``out``
+    may pass such a dict (dlog_alpha and dS0 may be None: not wanted; in a
+    given dS0 states without a sequence are left as they were).
+    ``workspace``: a uint8 tensor of at least the queried size, or None to
+    allocate one."""
+    lib = load()
+    if not isinstance(q, torch.Tensor):
+        raise TypeError("kdn: q must be a tensor")
+    dt, dev = q.dtype, q.device
+    if dt not in DTYPES:
+        raise ValueError(f"kdn: q has dtype {dt}, expected float32 or bfloat16")
+    lead, N, T, pool = _linear_sizes(q, tables, S0, dS_out if dS_out is not None else
+                                     (out or {}).get("dS0"))
+    qs, ks, vs = (_rows(n, x, lead, dt, dev) for n, x in (("q", q), ("k", k), ("v", v)))
+    H = _linear_heads(q, k, v, log_alpha)
+    Hq, Hk, Hv = q.shape[-2], k.shape[-2], v.shape[-2]
+    dk, dv, f32 = q.shape[-1], v.shape[-1], torch.float32
+    gate = _gate(log_alpha, lead, H, dt, dev)
+    pk = None
+    if tables is not None:
+        pk, N = _packed(tables, pool, dev)
+    la_shape = (H,) if gate == GATE_HEAD else lead + (H,)
+    s_shape = (pool, H, dk, dv)
+    if out is None:
+        new = lambda *shape: _new(shape, dt, dev, stream)
+        out = dict(dq=new(*lead, Hq, dk), dk=new(*lead, Hk, dk), dv=new(*lead, Hv, dv),
+                   dlog_alpha=new(*la_shape),
+                   dS0=_new(s_shape, f32, dev, stream, zero=tables is not None))
+    _expect([("k", k, lead + (Hk, dk), dt)] if k.shape[-1] != dk else [], dev)
+    _expect([("d_o", d_o, lead + (H, dv), dt), ("S0", S0, s_shape, f32),
+             ("dS_out", dS_out, s_shape, f32), ("dq", out["dq"], lead + (Hq, dk), dt),
+             ("dk", out["dk"], lead + (Hk, dk), dt), ("dv", out["dv"], lead + (Hv, dv), dt),
+             ("dlog_alpha", out["dlog_alpha"], la_shape, dt), ("dS0", out["dS0"], s_shape, f32)],
+            dev)
+    if workspace is None:
+        st = ctypes.c_int(0)
+        n = lib.kdn_linear_prefill_backward_workspace_size(
+            DTYPES[dt], N, T, H, Hq, Hk, Hv, dk, dv, gate, pk, ctypes.byref(st))
+        _check(lib, st.value)
+        workspace = _new((n,), torch.uint8, dev, stream) if n else None
+    nws = 0
+    if workspace is not None:
+        _expect([("workspace", workspace, (workspace.numel(),), torch.uint8)], dev)
+        nws = workspace.numel()
+    other, st = _on(q, stream)
+    _call(lib.kdn_linear_prefill_backward,
+          (DTYPES[dt], N, T, H, Hq, Hk, Hv, dk, dv, gate, qs, ks, vs, _p(q), _p(k), _p(v),
+           _p(log_alpha), _p(S0), _p(d_o), _p(dS_out), _p(out["dq"]), _p(out["dk"]),
+           _p(out["dv"]), _p(out["dlog_alpha"]), _p(out["dS0"]), pk, _p(workspace), nws, st), other)
+    return out

@@ -36,6 +36,43 @@ def forward(q, k, v, a, S0):
     return o, S, m, M
 
 
+def backward(q, k, v, a, do, S0, dS):
+    """One sequence, as forward; do [T,H,dv], dS [H,dk,dv].  Returns dicts of the
+    gradients dq, dk, dv, dlog_alpha, dS0 by the recurrence
+    R_t = a_{t+1} R_{t+1} + q_t do_t^T (R_T = dS + ..), and of the same over
+    absolute values."""
+    out = []
+    for f in (lambda x: x, torch.abs):
+        Q, K, V, O = f(q), f(k), f(v), f(do)
+        S, before = f(S0), []
+        dq, dk, dv, dg = (torch.zeros_like(x) for x in (q, k, v, a))
+        for t in range(q.shape[0]):
+            S = S * a[t][:, None, None]
+            before.append(S)                      # a_t S_{t-1}
+            S = S + K[t][:, :, None] * V[t][:, None, :]
+            dq[t] = (S * O[t][:, None, :]).sum(2)
+        R = f(dS)
+        for t in range(q.shape[0] - 1, -1, -1):
+            R = R + Q[t][:, :, None] * O[t][:, None, :]
+            dk[t] = (R * V[t][:, None, :]).sum(2)
+            dv[t] = (R * K[t][:, :, None]).sum(1)
+            dg[t] = (R * before[t]).sum((1, 2))
+            R = R * a[t][:, None, None]
+        out.append(dict(dq=dq, dk=dk, dv=dv, dlog_alpha=dg, dS0=R))
+    return out
+
+
+def flow_bound(g, m, q, k, C, dtype):
+    """d log_alpha: the states' roundings on what passes the token (two of
+    them in <S, R>), float32 sums over the chunk's tokens, its own rounding."""
+    near = (q.abs() * m["dq"]).sum(-1) + (k.abs() * m["dk"]).sum(-1)
+    T = g.shape[0]
+    total = torch.stack([near[t // C * C:t // C * C + C].sum(0) for t in range(T)]) if T else near
+    h = HALF[dtype]
+    low = 2.05 * h * m["dlog_alpha"] if dtype == torch.bfloat16 else 0.0
+    return h * (g.abs() + low) + low + slack(T, 2 * C, dtype) * (m["dlog_alpha"] + total)
+
+
 def slack(T, d, dtype):
     """Relative bound of float32 sums over T tokens of d channels, with the
     decays' own roundings (a power of two is off by 2^-23, one per chunk and

@@ -194,3 +194,82 @@ def test_binding_decode_and_tables_refusals():
         kdn.sequence_tables(torch.zeros(3, dtype=torch.int32), -1, 64)
     with pytest.raises(kdn.KdnError):
         kdn.linear_block(-1, 1, 1)
+
+
+def backward(lib, dtype=BF16, N=2, T=100, H=4, Hq=4, Hk=4, Hv=4, dk=64, dv=64, gate=0, qs=0, ks=0,
+             vs=0, q=A, k=A + MB, v=A + 2 * MB, la=A + 3 * MB, S0=A + 4 * MB, do=A + 6 * MB,
+             dS=A + 8 * MB, dq=A + 10 * MB, dkk=A + 11 * MB, dvv=A + 12 * MB, dla=A + 13 * MB,
+             dS0=A + 14 * MB, pk=None, ws=A + 16 * MB, wsb=MB):
+    return lib.kdn_linear_prefill_backward(dtype, N, T, H, Hq, Hk, Hv, dk, dv, gate, qs, ks, vs, q, k,
+                                           v, la, S0, do, dS, dq, dkk, dvv, dla, dS0, pk, ws, wsb,
+                                           None)
+
+
+@pytest.mark.parametrize("kw,want", [
+    (dict(dtype=2), EUNSUP), (dict(dk=96), EUNSUP), (dict(Hv=3), ESHAPE), (dict(T=-1), ESHAPE),
+    (dict(do=None), ENULL), (dict(dq=None), ENULL), (dict(dkk=None), ENULL), (dict(dvv=None), ENULL),
+    (dict(do=A + 6 * MB + 2), EALIGN), (dict(dS=A + 8 * MB + 4), EALIGN), (dict(dla=A + 13 * MB + 1), EALIGN),
+    (dict(dq=A), EALIAS), (dict(dkk=A + 10 * MB), EALIAS), (dict(dvv=A + 6 * MB), EALIAS),
+    (dict(dla=A + 3 * MB), EALIAS), (dict(dS0=A + 8 * MB), EALIAS), (dict(dS0=A + 4 * MB), EALIAS),
+    (dict(wsb=1000), EWS), (dict(ws=None), EWS), (dict(ws=A + 16 * MB + 128), EALIGN),
+    (dict(ws=A + 14 * MB), EALIAS), (dict(ws=A + 6 * MB), EALIAS),
+    (dict(T=0, N=4, pk="max"), ESHAPE), (dict(T=3, N=4, pk="ok"), ESHAPE),
+])
+def test_backward_refusals(lib, kw, want):
+    kw = dict(kw)
+    if kw.get("pk"):
+        kw["pk"] = packed(max_blocks=99) if kw["pk"] == "max" else packed()
+    assert backward(lib, **kw) == want
+
+
+def test_backward_workspace_size(lib):
+    st = ctypes.c_int(0)
+
+    def size(*a, pk=None):
+        n = lib.kdn_linear_prefill_backward_workspace_size(*a, pk, ctypes.byref(st))
+        return n, st.value
+
+    chunk = lambda tokens, blocks, C, H, d, es: (tokens // C + blocks + 1) * H * d * d * es
+    assert size(BF16, 1, 190, 4, 4, 4, 4, 64, 64, 0) == (chunk(190, 1, 64, 4, 64, 2), OK)
+    # shared heads and one decay per head
+    assert size(F32, 1, 100, 4, 2, 4, 1, 64, 64, 1) == (
+        chunk(100, 1, 32, 4, 64, 4) + 2 * 100 * 4 * 64 * 4 + 256, OK)
+    rows = lib.kdn_sequence_max_blocks(4, 100, 64)
+    assert size(BF16, 4, 0, 2, 2, 2, 2, 64, 64, 0, pk=packed()) == (
+        2 * (rows * 2 * 16384 + 256) + chunk(100, rows, 64, 2, 64, 2), OK)
+    assert size(BF16, 0, 5, 4, 4, 4, 4, 64, 64, 0) == (0, OK)
+    assert size(BF16, 1, 5, 4, 3, 4, 4, 64, 64, 0) == (0, ESHAPE)
+
+
+def test_binding_backward_refusals():
+    q, la = z(2, 8, 4, 64), z(2, 8, 4)
+    call = kdn.linear_prefill_backward
+    with pytest.raises(ValueError, match="GPU memory"):
+        call(q, q, q, q, la)
+    with pytest.raises(ValueError, match="dtype"):
+        call(q.half(), q.half(), q.half(), q.half(), la.half())
+    with pytest.raises(TypeError, match="q must be"):
+        call(None, q, q, q, la)
+
+
+def test_reference_gradients_against_differences():
+    """The reference's own reverse recurrence (tests/linear_ref.py), in 64 bits."""
+    import linear_ref as ref
+    g = torch.Generator().manual_seed(1)
+    rnd = lambda *s: torch.randn(s, generator=g, dtype=torch.float64)
+    T, H, dk, dv = 7, 2, 3, 4
+    x = dict(q=rnd(T, H, dk), k=rnd(T, H, dk), v=rnd(T, H, dv), la=-rnd(T, H).abs(),
+             S0=rnd(H, dk, dv))
+    do, dS = rnd(T, H, dv), rnd(H, dk, dv)
+
+    def loss(y):
+        o, S, _, _ = ref.forward(y["q"], y["k"], y["v"], torch.exp(y["la"]), y["S0"])
+        return ((o * do).sum() + (S * dS).sum()).item()
+
+    grads, _ = ref.backward(x["q"], x["k"], x["v"], torch.exp(x["la"]), do, x["S0"], dS)
+    for n, name in (("q", "dq"), ("k", "dk"), ("v", "dv"), ("la", "dlog_alpha"), ("S0", "dS0")):
+        for _ in range(5):
+            way = rnd(*x[n].shape)
+            up, down = (loss(dict(x, **{n: x[n] + e * way})) for e in (1e-5, -1e-5))
+            want = (grads[name] * way).sum().item()
+            assert abs((up - down) / 2e-5 - want) <= 1e-7 * (1 + abs(want)) * 10
