@@ -592,18 +592,21 @@ def sequence_tables(lengths, tokens, block, slots=None, context=None, maps=False
 
 
 def _packed(tables, pool, dev):
-    """The kdn_packed of the tables, and the number of sequences."""
+    """The kdn_packed of the tables, and the number of sequences.  Without a
+    pool (None) the states are by sequence and the slots are not looked at."""
     N, i32 = tables.offsets.shape[0] - 1, torch.int32
     rows = load().kdn_sequence_max_blocks(N, tables.tokens, tables.block)
     _expect([("offsets", tables.offsets, (N + 1,), i32),
              ("block_offsets", tables.block_offsets, (N + 1,), i32),
              ("blocks", tables.blocks, (rows, 4), i32), ("slots", tables.slots, (N,), i32)], dev)
-    return Packed(tables.tokens, tables.block, rows, pool, _p(tables.blocks),
-                  _p(tables.block_offsets), _p(tables.slots)), N
+    return Packed(tables.tokens, tables.block, rows, N if pool is None else pool,
+                  _p(tables.blocks), _p(tables.block_offsets),
+                  None if pool is None else _p(tables.slots)), N
 
 
 def _linear_sizes(q, tables, S0, S):
-    """(lead, sequences or None, tokens per sequence, states in S0 / S_out)."""
+    """(lead, sequences or None, tokens per sequence, states in S0 / S_out or
+    None for a packed batch without a pool)."""
     if not isinstance(q, torch.Tensor):
         raise TypeError("kdn: q must be a tensor")
     if tables is None:
@@ -617,7 +620,7 @@ def _linear_sizes(q, tables, S0, S):
     for x in (S0, S):
         if x is not None:
             return (q.shape[0],), None, 0, x.shape[0]
-    return (q.shape[0],), None, 0, tables.offsets.shape[0] - 1
+    return (q.shape[0],), None, 0, None
 
 
 def linear_prefill(q, k, v, log_alpha, S0=None, tables=None, out=None, workspace="auto",
@@ -631,6 +634,7 @@ def linear_prefill(q, k, v, log_alpha, S0=None, tables=None, out=None, workspace
     H is the largest of the head counts; the others divide it.
     Packed (``tables`` from :func:`sequence_tables`): the same without B, rows
     [tokens, ..]; S0 and S_out are pools [P,H,dk,dv] of states by slot.
+    Where neither is given, states are by sequence and slots are not looked at.
     ``out`` may pass (o, S_out); S_out may be S0 (in place) or None (not
     wanted).  Without it S_out is new, and for a packed batch with S0 the pool
     S0 itself, updated in place.  Rows of o behind the last sequence are left
@@ -647,6 +651,7 @@ def linear_prefill(q, k, v, log_alpha, S0=None, tables=None, out=None, workspace
     pk = None
     if tables is not None:
         pk, N = _packed(tables, pool, dev)
+        pool = N if pool is None else pool
     if out is None:
         o = _new(lead + (H, dv), dt, dev, stream)
         if tables is None:
@@ -739,7 +744,8 @@ def linear_prefill_backward(q, k, v, d_o, log_alpha, S0=None, dS_out=None, table
     may pass such a dict (dlog_alpha and dS0 may be None: not wanted; in a
     given dS0 states without a sequence are left as they were).
     ``workspace``: a uint8 tensor of at least the queried size, or None to
-    allocate one."""
+    allocate one.  A packed batch without any of S0, dS_out and out["dS0"] has
+    no pool: dS0 is by sequence and slots are not looked at."""
     lib = load()
     if not isinstance(q, torch.Tensor):
         raise TypeError("kdn: q must be a tensor")
@@ -756,6 +762,7 @@ def linear_prefill_backward(q, k, v, d_o, log_alpha, S0=None, dS_out=None, table
     pk = None
     if tables is not None:
         pk, N = _packed(tables, pool, dev)
+        pool = N if pool is None else pool
     la_shape = (H,) if gate == GATE_HEAD else lead + (H,)
     s_shape = (pool, H, dk, dv)
     if out is None:

@@ -186,6 +186,24 @@ def test_wanted_outputs_only():
         assert torch.equal(again[n], want[n]), n
 
 
+@pytest.mark.parametrize("dtype", [BF, F32])
+def test_packed_without_a_pool(dtype):
+    """No state anywhere: every sequence counts, whatever its slot, in the
+    gradients and in the prefill."""
+    lengths, H = [70, 300, 5], 2
+    total = sum(lengths)
+    q, k, v, la = make((total,), H, H, H, H, 64, 64, dtype, seed=4)
+    do = randn((total, H, 64), dtype, 3)
+    t = kdn.sequence_tables(i32(lengths), total, 128, slots=i32([9, 3, 0]))
+    got = kdn.linear_prefill_backward(q, k, v, do, la, tables=t)
+    assert got["dS0"].shape == (3, H, 64, 64)
+    spans = [slice(0, 70), slice(70, 370), slice(370, 375)]
+    check(q, k, v, la, do, None, None, got, spans, [0, 1, 2])
+    o, S = kdn.linear_prefill(q, k, v, la, tables=t, out=(torch.full_like(v, 7.0), None))
+    plain = kdn.sequence_tables(i32(lengths), total, 128)
+    assert S is None and torch.equal(o, kdn.linear_prefill(q, k, v, la, tables=plain)[0])
+
+
 def test_no_tokens():
     z = lambda *s: torch.zeros(s, dtype=BF, device="cuda")
     dS = state(3, 2, 64, 64)
