@@ -12,13 +12,15 @@
 // the states along the sequence, and the walk then starts every block from its
 // own state.  The cut costs one more read of k and v.
 //
-// Four waves split the d_v columns; wave w keeps its columns of S in MFMA
-// accumulators (float32) for the whole block.  All products are computed
-// transposed (o^T = S^T q^T + v^T P^T), so that the accumulator tiles of S
-// are the A operand of S^T q^T as they are and a lane ends with 8 consecutive
-// values of o.  P = D (.) q k^T is computed once, one 16-row strip per wave,
-// and shared through LDS.  q, k and v of the next chunk are in flight while
-// one is worked on.
+// Four waves work on 32 x 32 tiles.  With d_v = 128 wave w keeps 32 columns of
+// S in MFMA accumulators (float32) for the whole block; all products are
+// computed transposed (o^T = S^T q^T + v^T P^T), so that the accumulators of S
+// are the A operand of S^T q^T as they are.  With d_v = 64 two waves share 32
+// columns: each keeps half of the rows of S and computes half of the tokens
+// of o, and S passes between them through LDS in the operand type.  P = D (.)
+// q k^T is computed once, a tile per wave, and shared through LDS.  q, k and v
+// of the next chunk are in flight (in registers) while one is worked on, and
+// two workgroups share a CU.
 #include "kdn_linear_device.h"
 
 namespace kdn {
@@ -37,83 +39,99 @@ template <typename T, int DK, int DV> struct Shape {
     static constexpr int C = linear_chunk(sizeof(T) == 2);
     static constexpr int PAD = 16 / sizeof(T);
     static constexpr int PK = DK + PAD, PV = DV + PAD, PP = C + PAD;   // LDS pitches
-    static constexpr int NC = DV / 64;         // 16-column tiles of a wave
-    static constexpr int TK = DK / 16;         // 16-row tiles of S
-    static constexpr int KS = C / 32;          // contraction steps over tokens
-    static constexpr int IT = C / 16;          // 16-token tiles
+    static constexpr int NCT = DV / 32;        // column tiles
+    static constexpr int TW = NT / WAVE / NCT; // waves that share a column tile
+    static constexpr int TK = DK / 32 / TW;    // row tiles of S in a wave
+    static constexpr int IT = C / 32;          // token tiles
+    static constexpr int OT = (IT + TW - 1) / TW;   // token tiles of o in a wave
+    static constexpr int KS = C / 16;          // contraction steps over tokens
 };
 
-template <typename T, int DK, int DV>
-struct StateAcc {
+// The part of the state of one wave: row tiles t TK .. + TK - 1 of column tile
+// ct (t = w / NCT, ct = w % NCT), column n at channel chan(n).
+template <typename T, int DK, int DV> struct StateAcc {
     using SH = Shape<T, DK, DV>;
-    f32x4 t[SH::TK][SH::NC];
+    f32x16 t[SH::TK];
+    int row0, col;                             // of this lane
 
-    // column of accumulator column n of tile c in wave w
-    __device__ __forceinline__ static int col(int w, int c, int n) {
-        return w * 16 * SH::NC + 4 * SH::NC * (n >> 2) + 4 * c + (n & 3);
+    __device__ __forceinline__ StateAcc(int w, int lane) {
+        row0 = w / SH::NCT * SH::TK * 32 + 4 * (lane >> 5);
+        col = w % SH::NCT * 32 + chan(lane & 31);
+    }
+    __device__ __forceinline__ int row(int i, int r) const {
+        return row0 + 32 * i + 8 * (r / 4) + r % 4;
     }
     __device__ __forceinline__ void zero() {
 #pragma unroll
         for (int i = 0; i < SH::TK; ++i)
-#pragma unroll
-            for (int c = 0; c < SH::NC; ++c)
-                t[i][c] = f32x4{0.f, 0.f, 0.f, 0.f};
+            t[i] = zero16();
     }
-    __device__ __forceinline__ void load(const float *S, int w, int lane) {
-        const int g = lane >> 4, n = lane & 15;
+    __device__ __forceinline__ void load(const float *S) {
 #pragma unroll
         for (int i = 0; i < SH::TK; ++i)
 #pragma unroll
-            for (int c = 0; c < SH::NC; ++c)
-#pragma unroll
-                for (int r = 0; r < 4; ++r)
-                    t[i][c][r] = S[(16 * i + 4 * g + r) * DV + col(w, c, n)];
+            for (int r = 0; r < 16; ++r)
+                t[i][r] = S[row(i, r) * DV + col];
     }
     // from the transposed matrix [DV][DK]
-    __device__ __forceinline__ void load_t(const float *S, int w, int lane) {
-        const int g = lane >> 4, n = lane & 15;
+    __device__ __forceinline__ void load_t(const float *S) {
 #pragma unroll
         for (int i = 0; i < SH::TK; ++i)
 #pragma unroll
-            for (int c = 0; c < SH::NC; ++c)
-                t[i][c] = *reinterpret_cast<const f32x4 *>(S + col(w, c, n) * DK + 16 * i + 4 * g);
-    }
-    __device__ __forceinline__ void store(float *S, int w, int lane) const {
-        const int g = lane >> 4, n = lane & 15;
-#pragma unroll
-        for (int i = 0; i < SH::TK; ++i)
-#pragma unroll
-            for (int c = 0; c < SH::NC; ++c)
+            for (int j = 0; j < 4; ++j) {
+                const f32x4 x = *reinterpret_cast<const f32x4 *>(S + col * DK + row(i, 4 * j));
 #pragma unroll
                 for (int r = 0; r < 4; ++r)
-                    S[(16 * i + 4 * g + r) * DV + col(w, c, n)] = t[i][c][r];
+                    t[i][4 * j + r] = x[r];
+            }
     }
-    // operand fragments [column tile][32 rows][lane], rounded to T: the
+    __device__ __forceinline__ void store(float *S) const {
+#pragma unroll
+        for (int i = 0; i < SH::TK; ++i)
+#pragma unroll
+            for (int r = 0; r < 16; ++r)
+                S[row(i, r) * DV + col] = t[i][r];
+    }
+    // operand fragments [column tile][16 rows][lane], rounded to T: the
     // products that read them round the same state in the prefill
     __device__ __forceinline__ void store_frags(T *S, int w, int lane) const {
+        const int first = (w % SH::NCT * (DK / 32) + w / SH::NCT * SH::TK) * 2;
 #pragma unroll
-        for (int c = 0; c < SH::NC; ++c)
+        for (int i = 0; i < SH::TK; ++i)
 #pragma unroll
-            for (int s = 0; s < DK / 32; ++s)
-                reinterpret_cast<FragV<T> *>(S)[((w * SH::NC + c) * (DK / 32) + s) * WAVE + lane] =
-                    frag_acc<T>(t[2 * s][c], t[2 * s + 1][c]);
+            for (int b = 0; b < 2; ++b)
+                reinterpret_cast<FragV<T> *>(S)[(first + 2 * i + b) * WAVE + lane] =
+                    frag_acc<T>(t[i], b);
+    }
+    // to LDS, transposed [DV][pitch], in the operand type
+    __device__ __forceinline__ void share(T *Ss, int pitch) const {
+#pragma unroll
+        for (int i = 0; i < SH::TK; ++i)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const float f[4] = {t[i][4 * j], t[i][4 * j + 1], t[i][4 * j + 2], t[i][4 * j + 3]};
+                lds_stn<4>(Ss + col * pitch + row(i, 4 * j), f);
+            }
     }
 };
 
 template <typename T, int DK, int DV, int MODE>
 __global__ __launch_bounds__(NT, 2) void linear_kernel(LinearParams P) {
     using SH = Shape<T, DK, DV>;
-    constexpr int C = SH::C, NC = SH::NC, TK = SH::TK, KS = SH::KS, IT = SH::IT;
-    constexpr int PK = SH::PK, PV = SH::PV, PP = SH::PP;
+    constexpr int C = SH::C, TK = SH::TK, KS = SH::KS, IT = SH::IT, OT = SH::OT, TW = SH::TW;
+    constexpr int NCT = SH::NCT, PK = SH::PK, PV = SH::PV, PP = SH::PP;
+    constexpr bool SHARED = MODE == OUT && TW > 1;     // S passes through LDS
 
     __shared__ __attribute__((aligned(16))) T Ks[C * PK];
     __shared__ __attribute__((aligned(16))) T Vs[C * PV];
     __shared__ __attribute__((aligned(16))) T Qs[MODE == OUT ? C * PK : 1];
     __shared__ __attribute__((aligned(16))) T Ps[MODE == OUT ? C * PP : 1];
+    __shared__ __attribute__((aligned(16))) T Ss[SHARED ? DV * PK : 1];
     __shared__ __attribute__((aligned(16))) Decays<C> D[2];
 
     const int tid = threadIdx.x, lane = tid & (WAVE - 1), w = tid / WAVE;
-    const int g = lane >> 4, n = lane & 15;
+    const int hf = lane >> 5, n = lane & 31, cn = chan(n);
+    const int ct = w % NCT, tw = w / NCT;
     const long b = blockIdx.x / P.H;
     const int h = blockIdx.x % P.H;
     const Block B = get_block(P, b);
@@ -142,9 +160,13 @@ __global__ __launch_bounds__(NT, 2) void linear_kernel(LinearParams P) {
     TileRegs<T, C, DK, NT> qr, kr;
     TileRegs<T, C, DV, NT> vr;
     const int nchunk = (B.count + C - 1) / C;
-    auto gate = [&](int c) {        // wave 0: log-decay of this lane's token
+    // the wave that sums the decays: not one of those with a tile of P
+    constexpr int GW = NT / WAVE - 1;
+    const float head = P.gate == KDN_GATE_HEAD ? static_cast<const float *>(P.la)[h] : 0.f;
+    GateReg<T> la0, la1;            // this lane's token of the next chunks
+    auto gate = [&](GateReg<T> &x, int c) {
         const int i = c * C + lane;
-        return (lane < C && i < B.count) ? load_gate<T>(P, B.first + i, h) : 0.f;
+        x.load(P, head, B.first + i, h, lane < C && i < B.count);
     };
     auto load_chunk = [&](int c) {
         const int cnt = B.count - c * C;
@@ -155,14 +177,14 @@ __global__ __launch_bounds__(NT, 2) void linear_kernel(LinearParams P) {
     };
     // the chunk of step i
     auto chunk = [&](int i) { return MODE == ROWN ? nchunk - 1 - i : i; };
-    load_chunk(chunk(0));
-    float la0 = 0.f, la1 = 0.f;
-    if (w == 0) {
-        la0 = gate(chunk(0));
-        la1 = nchunk > 1 ? gate(chunk(1)) : 0.f;
+    if (w == GW) {
+        gate(la0, chunk(0));
+        if (nchunk > 1)
+            gate(la1, chunk(1));
     }
+    load_chunk(chunk(0));
 
-    StateAcc<T, DK, DV> S;
+    StateAcc<T, DK, DV> S(w, lane);
     const long sidx = (b * P.H + h) * (long)(DK * DV);
     const float *start = B.single ? P.S0 : P.ws_state;
     if (start)
@@ -170,19 +192,15 @@ __global__ __launch_bounds__(NT, 2) void linear_kernel(LinearParams P) {
     if (MODE == OWN || MODE == ROWN || !start)
         S.zero();
     else if (MODE == CHUNKS)
-        S.load_t(start, w, lane);
+        S.load_t(start);
     else
-        S.load(start, w, lane);
+        S.load(start);
 
-    if (MODE == OUT) {
-        // the 16 x 16 tiles right of the diagonal inside a step of 32 tokens
-        // are read and never written again
-        for (int i = tid; i < C * PP; i += NT)
-            Ps[i] = from_f32<T>(0.f);
-    }
-    double total = 0.;              // base-2 log of the block's decay (wave 0)
-    if (w == 0)
-        total = chunk_decays<C>(D[0], la0, lane);
+    double total = 0.;              // base-2 log of the block's decay (wave GW)
+    if (w == GW)
+        total = chunk_decays<C>(D[0], la0.value(P), lane);
+    if (SHARED)
+        S.share(Ss, PK);
 
     for (int step = 0; step < nchunk; ++step) {
         const int c = chunk(step);
@@ -201,67 +219,61 @@ __global__ __launch_bounds__(NT, 2) void linear_kernel(LinearParams P) {
                               (chunk_slot(b, B.first, c, C) * P.H + h) * (long)(DK * DV),
                           w, lane);
 
-        f32x4 o[IT][NC];
+        f32x16 o[OT];
         if (MODE == OUT) {
-            // P^T strip of 16 query rows: D[j][i], lane holds i = n, j = 4 g + r
-            if (w < IT && 16 * w < cnt) {
-                const int i = 16 * w + n;
-                FragV<T> qf[DK / 32];
+            // tiles of P^T on and below the diagonal: lane n has query
+            // i = 32 it + n, registers 0-7 and 8-15 eight keys each
+            if (w < IT * (IT + 1) / 2) {
+                const int it = w > 0, jt = w > 1;
+                const int i = 32 * it + n;
+                f32x16 p = zero16();
 #pragma unroll
-                for (int s = 0; s < DK / 32; ++s)
-                    qf[s] = frag_row(Qs + i * PK + 32 * s + 8 * g);
-                const float hi = dc.hi[i], lo = dc.lo[i];
+                for (int s = 0; s < DK / 16; ++s)
+                    mma(p, frag_row(Ks + (32 * jt + cn) * PK + 16 * s + 8 * hf),
+                        frag_row(Qs + i * PK + 16 * s + 8 * hf));
 #pragma unroll
-                for (int jt = 0; jt < IT; ++jt) {
-                    if (jt > w)
-                        break;
-                    f32x4 p = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-                    for (int s = 0; s < DK / 32; ++s)
-                        mma(p, frag_row(Ks + (16 * jt + n) * PK + 32 * s + 8 * g), qf[s]);
-                    float x[4];
-#pragma unroll
-                    for (int r = 0; r < 4; ++r) {
-                        const int j = 16 * jt + 4 * g + r;
-                        x[r] = j <= i ? p[r] * decay_between<T, C>(dc, hi, lo, j) : 0.f;
-                    }
+                for (int u = 0; u < 2; ++u) {
+                    const int j = 32 * jt + 16 * u + 8 * hf;
+                    float x[8];
+                    decay_between<T, C>(dc, dc.hi[i], dc.lo[i], i, j, x);
                     // rounded to the operand type: P feeds one product whose
-                    // result is rounded to the same type
-                    lds_stn<4>(Ps + i * PP + 16 * jt + 4 * g, x);
+                    // result is rounded to the same type (not 0 * p right of
+                    // the diagonal: p may be infinite there)
+#pragma unroll
+                    for (int r = 0; r < 8; ++r)
+                        x[r] = j + r <= i ? p[8 * u + r] * x[r] : 0.f;
+                    lds_st8(Ps + i * PP + j, x);
                 }
             }
             // o^T = S^T q^T, scaled to each token
-            FragV<T> sf[NC];
 #pragma unroll
-            for (int it = 0; it < IT; ++it)
+            for (int t = 0; t < OT; ++t)
+                o[t] = zero16();
 #pragma unroll
-                for (int cc = 0; cc < NC; ++cc)
-                    o[it][cc] = f32x4{0.f, 0.f, 0.f, 0.f};
+            for (int s = 0; s < DK / 16; ++s) {
+                FragV<T> sf;
+                if constexpr (SHARED)
+                    sf = frag_row(Ss + (32 * ct + cn) * PK + 16 * s + 8 * hf);
+                else
+                    sf = frag_acc<T>(S.t[s / 2], s % 2);
 #pragma unroll
-            for (int s = 0; s < DK / 32; ++s) {
-#pragma unroll
-                for (int cc = 0; cc < NC; ++cc)
-                    sf[cc] = frag_acc<T>(S.t[2 * s][cc], S.t[2 * s + 1][cc]);
-#pragma unroll
-                for (int it = 0; it < IT; ++it) {
-                    const FragV<T> qf = frag_row_perm(Qs + (16 * it + n) * PK + 32 * s + 4 * g);
-#pragma unroll
-                    for (int cc = 0; cc < NC; ++cc)
-                        mma(o[it][cc], sf[cc], qf);
+                for (int t = 0; t < OT; ++t) {
+                    const int i = 32 * (t * TW + (IT >= TW ? tw : 0)) + n;
+                    if constexpr (SHARED)
+                        mma(o[t], sf, frag_row(Qs + i * PK + 16 * s + 8 * hf));
+                    else
+                        mma(o[t], sf, frag_row_perm(Qs + i * PK + 16 * s + 4 * hf));
                 }
             }
 #pragma unroll
-            for (int it = 0; it < IT; ++it) {
-                const float a = dc.in[16 * it + n];
-#pragma unroll
-                for (int cc = 0; cc < NC; ++cc)
-                    o[it][cc] *= a;
-            }
+            for (int t = 0; t < OT; ++t)
+                o[t] *= dc.in[32 * (t * TW + (IT >= TW ? tw : 0)) + n];
         }
-        if (w == 0) {               // the next chunk's decays
+        if (w == GW) {              // the next chunk's decays
             if (step + 1 < nchunk)
-                total += chunk_decays<C>(D[(step + 1) & 1], la1, lane);
-            la1 = step + 2 < nchunk ? gate(chunk(step + 2)) : 0.f;
+                total += chunk_decays<C>(D[(step + 1) & 1], la1.value(P), lane);
+            if (step + 2 < nchunk)
+                gate(la1, chunk(step + 2));
         }
         if (MODE == OUT)
             __syncthreads();        // P
@@ -270,65 +282,54 @@ __global__ __launch_bounds__(NT, 2) void linear_kernel(LinearParams P) {
         const float all = dc.all;
 #pragma unroll
         for (int i = 0; i < TK; ++i)
-#pragma unroll
-            for (int cc = 0; cc < NC; ++cc)
-                S.t[i][cc] *= all;
+            S.t[i] *= all;
 #pragma unroll
         for (int s = 0; s < KS; ++s) {
-            FragV<T> vf[NC];
-#pragma unroll
-            for (int cc = 0; cc < NC; ++cc)
-                vf[cc] = frag_cols<PV>(Vs + 32 * s * PV, w * 16 * NC + 4 * cc, 4 * NC, lane);
+            const FragV<T> vf = frag_cols<PV, true>(Vs + 16 * s * PV + 32 * ct, lane);
             if (MODE == OUT) {
 #pragma unroll
-                for (int it = 2 * s; it < IT; ++it) {
-                    const FragV<T> pf = frag_row(Ps + (16 * it + n) * PP + 32 * s + 8 * g);
-#pragma unroll
-                    for (int cc = 0; cc < NC; ++cc)
-                        mma(o[it][cc], vf[cc], pf);
+                for (int t = 0; t < OT; ++t) {
+                    const int it = t * TW + (IT >= TW ? tw : 0);
+                    if (s / 2 <= it)
+                        mma(o[t], vf, frag_row(Ps + (32 * it + n) * PP + 16 * s + 8 * hf));
                 }
             }
             float wt[8];
-            lds_ld8((MODE == ROWN ? dc.in : dc.out) + 32 * s + 8 * g, wt);
-            const Split<T> v0(vf[0], wt);
-            const Split<T> v1(vf[NC - 1], wt);
+            lds_ld8((MODE == ROWN ? dc.in : dc.out) + 16 * s + 8 * hf, wt);
+            const Split<T> v3(vf, wt);
 #pragma unroll
-            for (int i = 0; i < TK; ++i) {
-                const FragV<T> kf = frag_cols<PK>(Ks + 32 * s * PK, 16 * i, 4, lane);
-                v0.mma_a(S.t[i][0], kf);
-                if (NC == 2)
-                    v1.mma_a(S.t[i][NC - 1], kf);
-            }
+            for (int i = 0; i < TK; ++i)
+                v3.mma_a(S.t[i], frag_cols<PK, false>(Ks + 16 * s * PK + 32 * (tw * TK + i), lane));
         }
         if (MODE == OUT) {
 #pragma unroll
-            for (int it = 0; it < IT; ++it) {
-                const int i = 16 * it + n;
-                if (i < cnt) {
+            for (int t = 0; t < OT; ++t) {
+                const int it = t * TW + tw, i = 32 * it + n;
+                if (it < IT && i < cnt) {
                     T *dst = static_cast<T *>(P.o) +
-                             ((B.first + (long)c * C + i) * P.H + h) * DV + w * 16 * NC + 4 * NC * g;
-                    float x[4 * NC];
+                             ((B.first + (long)c * C + i) * P.H + h) * DV + 32 * ct + 8 * hf;
 #pragma unroll
-                    for (int cc = 0; cc < NC; ++cc)
+                    for (int u = 0; u < 2; ++u) {
+                        float x[8];
 #pragma unroll
-                        for (int r = 0; r < 4; ++r)
-                            x[4 * cc + r] = o[it][cc][r];
-                    if constexpr (NC == 2)
-                        lds_st8(dst, x);
-                    else
-                        lds_stn<4>(dst, x);
+                        for (int r = 0; r < 8; ++r)
+                            x[r] = o[t][8 * u + r];
+                        lds_st8(dst + 16 * u, x);
+                    }
                 }
             }
         }
+        if (SHARED)
+            S.share(Ss, PK);        // read since the barrier above: by nobody
         __syncthreads();            // the chunk's tiles have been read
     }
     if (MODE == OWN || MODE == ROWN) {
-        S.store((MODE == OWN ? P.ws_state : P.ws_rstate) + sidx, w, lane);
-        if (tid == 0)
+        S.store((MODE == OWN ? P.ws_state : P.ws_rstate) + sidx);
+        if (w == GW && lane == 0)
             (MODE == OWN ? P.ws_decay : P.ws_rdecay)[b * P.H + h] = exp2_fast((float)total);
     }
     if (MODE == OUT && B.last && P.S_out)
-        S.store(P.S_out + (B.slot * P.H + h) * (long)(DK * DV), w, lane);
+        S.store(P.S_out + (B.slot * P.H + h) * (long)(DK * DV));
 }
 
 // ---------------------------------------------------------------------------

@@ -134,10 +134,10 @@ int kdn_sequence_max_blocks(int N, int tokens, int block) {
 int kdn_linear_block(int tokens, int N, int H) {
     if (tokens < 0 || N < 0 || H < 0)
         return -1;
-    // about three workgroups for each of the 256 CUs, and blocks long enough
-    // that the state of a block (read twice, written twice) is small beside
-    // its tokens
-    const long long want = (long long)tokens * H / 768;
+    // two workgroups for each of the 256 CUs, all at once, and blocks long
+    // enough that the state of a block (read twice, written twice) is small
+    // beside its tokens
+    const long long want = ((long long)tokens * H + 511) / 512;
     long long block = (want + 63) / 64 * 64;
     if (block < 256)
         block = 256;

@@ -20,9 +20,10 @@
 // (CHUNKS, in the call's type: the precision its product reads it in); the
 // blocks' reverse states are joined as the forward ones are.  A workgroup then
 // walks the chunks of one block backwards for one head, with R in MFMA
-// accumulators, each wave the rows of dq and dk and the columns of dv and R
-// that follow from its number.  All products are computed transposed (a lane
-// ends with consecutive channels of a token).
+// accumulators (float32) and, in the operand type, in LDS; each wave has one
+// 32 x 32 tile (channels x tokens) of dq, dk and dv and its tiles of R.  All
+// products are computed transposed, so that a lane ends with runs of 8
+// consecutive channels of a token.
 #include "kdn_linear_device.h"
 
 namespace kdn {
@@ -30,26 +31,25 @@ namespace lin {
 
 template <typename T, int DK, int DV> struct GradShape {
     static constexpr int C = linear_chunk(sizeof(T) == 2);
-    static constexpr int W = (DK < DV ? DK : DV) / 16;     // waves
+    static constexpr int W = (DK > DV ? DK : DV) / 16;     // waves
     static constexpr int NT = W * WAVE;
-    static constexpr int NC = DV / 16 / W;     // column tiles of R and dv of a wave
-    static constexpr int TR = DK / 16 / W;     // row tiles of dq and dk of a wave
-    static constexpr int TK = DK / 16;         // row tiles of R
-    static constexpr int IT = C / 16, KS = C / 32;
+    static constexpr int IT = C / 32;          // token tiles
+    static constexpr int KT = DK / 32, VT = DV / 32;       // channel tiles
+    static constexpr int TR = KT * VT / W;     // row tiles of R in a wave
+    static constexpr int KS = C / 16;
     static constexpr int PAD = 16 / sizeof(T);
     static constexpr int PK = DK + PAD, PV = DV + PAD, PP = C + PAD;
 };
 
-// First channel and the step between groups of 4 of 16-channel tile t of D
-// channels: tiles share runs of 4 D / 64 channels, as the accumulators of
-// kdn_linear.hip do (the saved states are in that order).
-template <int D> __device__ __forceinline__ int tile_first(int t) {
-    return t / (D / 64) * (D / 4) + 4 * (t % (D / 64));
+// Store of channels of a token to the gradient (call dtype) or to the float32
+// partial of a shared head.
+template <typename T>
+__device__ __forceinline__ void store8(void *out, float *part, long at, const float (&f)[8]) {
+    if (part)
+        lds_st8(part + at, f);
+    else
+        lds_st8(static_cast<T *>(out) + at, f);
 }
-template <int D> constexpr int tile_step() { return 4 * (D / 64); }
-
-// Store of 4 channels of a token to the gradient (call dtype) or to the
-// float32 partial of a shared head.
 template <typename T>
 __device__ __forceinline__ void store4(void *out, float *part, long at, f32x4 x) {
     const float f[4] = {x[0], x[1], x[2], x[3]};
@@ -62,7 +62,7 @@ __device__ __forceinline__ void store4(void *out, float *part, long at, f32x4 x)
 template <typename T, int DK, int DV>
 __global__ __launch_bounds__((GradShape<T, DK, DV>::NT)) void linear_grad_kernel(LinearParams P) {
     using SH = GradShape<T, DK, DV>;
-    constexpr int C = SH::C, W = SH::W, NT = SH::NT, NC = SH::NC, TR = SH::TR, TK = SH::TK;
+    constexpr int C = SH::C, W = SH::W, NT = SH::NT, TR = SH::TR, KT = SH::KT, VT = SH::VT;
     constexpr int IT = SH::IT, KS = SH::KS, PK = SH::PK, PV = SH::PV, PP = SH::PP;
 
     __shared__ __attribute__((aligned(16))) T Qs[C * PK];
@@ -73,11 +73,14 @@ __global__ __launch_bounds__((GradShape<T, DK, DV>::NT)) void linear_grad_kernel
     __shared__ __attribute__((aligned(16))) T Ys[C * PP];
     __shared__ __attribute__((aligned(16))) T Rs[DV * PK];      // R^T
     __shared__ __attribute__((aligned(16))) Decays<C> D[2];
-    __shared__ float rowx[IT][C], colx[IT][C];   // sums of X over a tile's columns / rows
-    __shared__ float xs[W][C], ys[W][C], zs[W];
+    // sums of X over a tile's keys, and over 16 of a tile's queries
+    __shared__ __attribute__((aligned(16))) float rowx[IT][C], colx[2 * IT][C];
+    __shared__ float xs[KT][C], ys[KT][C], zs[KT];
 
     const int tid = threadIdx.x, lane = tid & (WAVE - 1), w = tid / WAVE;
-    const int g = lane >> 4, n = lane & 15;
+    const int hf = lane >> 5, n = lane & 31, cn = chan(n);
+    const int qc = w % KT, qt = w / KT;     // channel and token tile of dq and dk
+    const int vc = w % VT, vt = w / VT;     // of dv; and column tile and row group of R
     const long b = blockIdx.x / P.H;
     const int h = blockIdx.x % P.H;
     const Block B = get_block(P, b);
@@ -119,9 +122,11 @@ __global__ __launch_bounds__((GradShape<T, DK, DV>::NT)) void linear_grad_kernel
     TileRegs<T, C, DK, NT> qr, kr;
     TileRegs<T, C, DV, NT> vr, orr;
     const int nchunk = (B.count + C - 1) / C;
-    auto gate = [&](int c) {
+    const float head = P.gate == KDN_GATE_HEAD ? static_cast<const float *>(P.la)[h] : 0.f;
+    GateReg<T> la0, la1;            // wave GW: this lane's token, this chunk and the next
+    auto gate = [&](GateReg<T> &x, int c) {
         const int i = c * C + lane;
-        return (lane < C && i < B.count) ? load_gate<T>(P, B.first + i, h) : 0.f;
+        x.load(P, head, B.first + i, h, lane < C && i < B.count);
     };
     auto load_chunk = [&](int c) {
         const int cnt = B.count - c * C;
@@ -130,37 +135,50 @@ __global__ __launch_bounds__((GradShape<T, DK, DV>::NT)) void linear_grad_kernel
         vr.load(v + (long)c * C * P.v_stride, P.v_stride, cnt, tid);
         orr.load(od + (long)c * C * ostride, ostride, cnt, tid);
     };
-    load_chunk(nchunk - 1);
-    float la0 = 0.f, la1 = 0.f;     // wave 0: log-decays of this chunk and the next
-    if (w == 0) {
-        la0 = gate(nchunk - 1);
-        la1 = nchunk > 1 ? gate(nchunk - 2) : 0.f;
+    constexpr int GW = W - 1;       // the wave of the decays: not one with a tile of P
+    if (w == GW) {
+        gate(la0, nchunk - 1);
+        if (nchunk > 1)
+            gate(la1, nchunk - 2);
     }
+    load_chunk(nchunk - 1);
 
-    // R: rows 16 i + 4 g + r, column vcol(c) of this lane
-    f32x4 R[TK][NC];
-    auto vcol = [&](int c) {
-        return tile_first<DV>(w * NC + c) + tile_step<DV>() * (n >> 2) + (n & 3);
+    // R: rows row(i, r), column col of this lane
+    f32x16 R[TR];
+    const int col = 32 * vc + cn, row0 = vt * TR * 32 + 4 * hf;
+    auto row = [&](int i, int r) { return row0 + 32 * i + 8 * (r / 4) + r % 4; };
+    auto share_state = [&]() {
+#pragma unroll
+        for (int i = 0; i < TR; ++i)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const float f[4] = {R[i][4 * j], R[i][4 * j + 1], R[i][4 * j + 2], R[i][4 * j + 3]};
+                lds_stn<4>(Rs + col * PK + row(i, 4 * j), f);
+            }
     };
     const long hs = (long)DK * DV;
     const float *rstart = B.single ? P.dS_out : P.ws_rstate;
     if (rstart)
         rstart += B.single ? (B.slot * P.H + h) * hs : (b * P.H + h) * hs;
 #pragma unroll
-    for (int i = 0; i < TK; ++i)
+    for (int i = 0; i < TR; ++i)
 #pragma unroll
-        for (int c = 0; c < NC; ++c)
+        for (int r = 0; r < 16; ++r)
+            R[i][r] = rstart ? rstart[row(i, r) * DV + col] : 0.f;
+    FragV<T> sf[DV / 16];           // rows of S of this wave, a chunk ahead
+    auto load_state = [&](int c) {
+        const FragV<T> *src = reinterpret_cast<const FragV<T> *>(
+            static_cast<const T *>(P.ws_chunk) + (chunk_slot(b, B.first, c, C) * P.H + h) * hs);
 #pragma unroll
-            for (int r = 0; r < 4; ++r)
-                R[i][c][r] = rstart ? rstart[(16 * i + 4 * g + r) * DV + vcol(c)] : 0.f;
-
-    for (int i = tid; i < C * PP; i += NT) {     // right of the diagonal: never written
-        Ps[i] = from_f32<T>(0.f);
-        Ys[i] = from_f32<T>(0.f);
-    }
-    if (w == 0)
-        chunk_decays<C>(D[0], la0, lane);
-    double gsum = 0.;               // wave 0: sum of the block's d log_alpha (this lane's)
+        for (int s = 0; s < DV / 16; ++s)
+            sf[s] = src[(qc * (DV / 16) + s) * WAVE + lane];
+    };
+    if (qt < IT)
+        load_state(nchunk - 1);
+    if (w == GW)
+        chunk_decays<C>(D[0], la0.value(P), lane);
+    share_state();
+    double gsum = 0.;               // wave GW: sum of the block's d log_alpha (this lane's)
 
     for (int step = 0; step < nchunk; ++step) {
         const int c = nchunk - 1 - step;
@@ -170,162 +188,138 @@ __global__ __launch_bounds__((GradShape<T, DK, DV>::NT)) void linear_grad_kernel
         kr.template store<PK>(Ks, tid);
         vr.template store<PV>(Vs, tid);
         orr.template store<PV>(Os, tid);
-#pragma unroll
-        for (int i = 0; i < TK; ++i)
-#pragma unroll
-            for (int cc = 0; cc < NC; ++cc) {
-                const float f[4] = {R[i][cc][0], R[i][cc][1], R[i][cc][2], R[i][cc][3]};
-                lds_stn<4>(Rs + vcol(cc) * PK + 16 * i + 4 * g, f);
-            }
-        FragV<T> sf[TR][DV / 32];
-        {
-            const FragV<T> *src = reinterpret_cast<const FragV<T> *>(
-                static_cast<const T *>(P.ws_chunk) +
-                (chunk_slot(b, B.first, c, C) * P.H + h) * hs);
-#pragma unroll
-            for (int t = 0; t < TR; ++t)
-#pragma unroll
-                for (int s = 0; s < DV / 32; ++s)
-                    sf[t][s] = src[((w * TR + t) * (DV / 32) + s) * WAVE + lane];
-        }
         __syncthreads();
         if (step + 1 < nchunk)
             load_chunk(c - 1);
 
-        // 16 x 16 tiles of P and Y on and below the diagonal, and of X's sums
-        for (int t = w; t < IT * (IT + 1) / 2; t += W) {
-            int it = 0, jt = t;
-            while (jt > it)
-                jt -= ++it;
-            const int i = 16 * it + n;
-            f32x4 p = {0.f, 0.f, 0.f, 0.f}, y = p;
+        // tiles of P^T and Y^T on and below the diagonal, and of X's sums: lane n
+        // has query i = 32 it + n, registers 0-7 and 8-15 eight keys each
+        if (w < IT * (IT + 1) / 2) {
+            const int it = w > 0, jt = w > 1;
+            const int i = 32 * it + n;
+            f32x16 p = zero16(), y = zero16();
 #pragma unroll
-            for (int s = 0; s < DK / 32; ++s)
-                mma(p, frag_row(Ks + (16 * jt + n) * PK + 32 * s + 8 * g),
-                    frag_row(Qs + i * PK + 32 * s + 8 * g));
+            for (int s = 0; s < DK / 16; ++s)
+                mma(p, frag_row(Ks + (32 * jt + cn) * PK + 16 * s + 8 * hf),
+                    frag_row(Qs + i * PK + 16 * s + 8 * hf));
 #pragma unroll
-            for (int s = 0; s < DV / 32; ++s)
-                mma(y, frag_row(Vs + (16 * jt + n) * PV + 32 * s + 8 * g),
-                    frag_row(Os + i * PV + 32 * s + 8 * g));
-            const float hi = dc.hi[i], lo = dc.lo[i];
-            float pf[4], yf[4], row = 0.f;
+            for (int s = 0; s < DV / 16; ++s)
+                mma(y, frag_row(Vs + (32 * jt + cn) * PV + 16 * s + 8 * hf),
+                    frag_row(Os + i * PV + 16 * s + 8 * hf));
+            float sum = 0.f;
 #pragma unroll
-            for (int r = 0; r < 4; ++r) {
-                const int j = 16 * jt + 4 * g + r;
-                const float d = j <= i ? decay_between<T, C>(dc, hi, lo, j) : 0.f;
-                pf[r] = j <= i ? p[r] * d : 0.f;
-                yf[r] = j <= i ? y[r] * d : 0.f;
-                // X without its diagonal, which no log-decay is between
-                float x = j < i ? pf[r] * y[r] : 0.f;
-                row += x;
-                x = row16_sum_last(x);
-                if (n == 15)
-                    colx[it][j] = x;
+            for (int u = 0; u < 2; ++u) {
+                const int j = 32 * jt + 16 * u + 8 * hf;
+                float d[8], pf[8], yf[8], x[8];
+                decay_between<T, C>(dc, dc.hi[i], dc.lo[i], i, j, d);
+#pragma unroll
+                for (int r = 0; r < 8; ++r) {
+                    const bool in = j + r <= i;
+                    pf[r] = in ? p[8 * u + r] * d[r] : 0.f;
+                    yf[r] = in ? y[8 * u + r] * d[r] : 0.f;
+                    // X without its diagonal, which no log-decay is between
+                    x[r] = j + r < i ? pf[r] * y[8 * u + r] : 0.f;
+                }
+                lds_st8(Ps + i * PP + j, pf);
+                lds_st8(Ys + i * PP + j, yf);
+                if (P.dla) {
+#pragma unroll
+                    for (int r = 0; r < 8; ++r) {
+                        sum += x[r];
+                        x[r] = row16_sum_last(x[r]);
+                    }
+                    if ((n & 15) == 15)
+                        lds_st8(&colx[2 * it + (n >> 4)][j], x);
+                }
             }
-            lds_stn<4>(Ps + i * PP + 16 * jt + 4 * g, pf);
-            lds_stn<4>(Ys + i * PP + 16 * jt + 4 * g, yf);
-            row += __shfl_xor(row, 16, WAVE);
-            row += __shfl_xor(row, 32, WAVE);
-            if (g == 0)
-                rowx[jt][i] = row;
+            if (P.dla) {
+                sum += __shfl_xor(sum, 32, WAVE);
+                if (hf == 0)
+                    rowx[jt][i] = sum;
+            }
         }
 
         // what comes from S and R, scaled to each token
-        f32x4 aq[TR][IT], ak[TR][IT], av[NC][IT];
-        float z = 0.f;
+        f32x16 aq = zero16(), ak = zero16(), av = zero16();
+        if (qt < IT) {
+            const int i = 32 * qt + n;
+            float z = 0.f;
 #pragma unroll
-        for (int t = 0; t < TR; ++t) {
-            const int c0 = tile_first<DK>(w * TR + t);
+            for (int s = 0; s < DV / 16; ++s) {
+                const FragV<T> rf = frag_cols<PK, true, true>(Rs + 16 * s * PK + 32 * qc, lane);
+                if (P.dla && qt == 0) {
 #pragma unroll
-            for (int it = 0; it < IT; ++it) {
-                aq[t][it] = f32x4{0.f, 0.f, 0.f, 0.f};
-                ak[t][it] = f32x4{0.f, 0.f, 0.f, 0.f};
-            }
-#pragma unroll
-            for (int s = 0; s < DV / 32; ++s) {
-                const FragV<T> rf = frag_cols_perm<PK>(Rs + 32 * s * PK, c0, tile_step<DK>(), lane);
-#pragma unroll
-                for (int e = 0; e < 8; ++e)
-                    z += to_f32(sf[t][s][e]) * to_f32(rf[e]);
-#pragma unroll
-                for (int it = 0; it < IT; ++it) {
-                    mma(aq[t][it], sf[t][s],
-                        frag_row_perm(Os + (16 * it + n) * PV + 32 * s + 4 * g));
-                    mma(ak[t][it], rf, frag_row_perm(Vs + (16 * it + n) * PV + 32 * s + 4 * g));
+                    for (int e = 0; e < 8; ++e)
+                        z += to_f32(sf[s][e]) * to_f32(rf[e]);
                 }
+                mma(aq, sf[s], frag_row_perm(Os + i * PV + 16 * s + 4 * hf));
+                mma(ak, rf, frag_row_perm(Vs + i * PV + 16 * s + 4 * hf));
             }
-        }
-#pragma unroll
-        for (int it = 0; it < IT; ++it) {
-            const int i = 16 * it + n;
-            const float in = dc.in[i], out = dc.out[i];
-            float x = 0.f, y = 0.f;
-#pragma unroll
-            for (int t = 0; t < TR; ++t) {
-                const int c0 = tile_first<DK>(w * TR + t) + tile_step<DK>() * g;
-                aq[t][it] *= in;
-                ak[t][it] *= out;
-#pragma unroll
-                for (int r = 0; r < 4; ++r) {
-                    x += aq[t][it][r] * to_f32(Qs[i * PK + c0 + r]);
-                    y += ak[t][it][r] * to_f32(Ks[i * PK + c0 + r]);
-                }
-            }
-            x += __shfl_xor(x, 16, WAVE);
-            x += __shfl_xor(x, 32, WAVE);
-            y += __shfl_xor(y, 16, WAVE);
-            y += __shfl_xor(y, 32, WAVE);
-            if (g == 0) {
-                xs[w][i] = x;
-                ys[w][i] = y;
-            }
-        }
-        z = wave_sum(z);
-        if (lane == 0)
-            zs[w] = z;
-#pragma unroll
-        for (int cc = 0; cc < NC; ++cc) {
-#pragma unroll
-            for (int it = 0; it < IT; ++it)
-                av[cc][it] = f32x4{0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-            for (int s = 0; s < DK / 32; ++s) {
-                const FragV<T> rf = frag_acc<T>(R[2 * s][cc], R[2 * s + 1][cc]);
-#pragma unroll
-                for (int it = 0; it < IT; ++it)
-                    mma(av[cc][it], rf, frag_row_perm(Ks + (16 * it + n) * PK + 32 * s + 4 * g));
-            }
-#pragma unroll
-            for (int it = 0; it < IT; ++it)
-                av[cc][it] *= dc.out[16 * it + n];
-        }
-        const float la = la0;       // wave 0: this chunk's log-decays
-        if (w == 0) {
             if (step + 1 < nchunk)
-                chunk_decays<C>(D[(step + 1) & 1], la1, lane);
+                load_state(c - 1);
+            aq *= dc.in[i];
+            ak *= dc.out[i];
+            if (P.dla) {
+                float x = 0.f, y = 0.f;
+#pragma unroll
+                for (int u = 0; u < 2; ++u) {
+                    float qx[8], kx[8];
+                    lds_ld8(Qs + i * PK + 32 * qc + 16 * u + 8 * hf, qx);
+                    lds_ld8(Ks + i * PK + 32 * qc + 16 * u + 8 * hf, kx);
+#pragma unroll
+                    for (int r = 0; r < 8; ++r) {
+                        x += aq[8 * u + r] * qx[r];
+                        y += ak[8 * u + r] * kx[r];
+                    }
+                }
+                x += __shfl_xor(x, 32, WAVE);
+                y += __shfl_xor(y, 32, WAVE);
+                if (hf == 0) {
+                    xs[qc][i] = x;
+                    ys[qc][i] = y;
+                }
+                if (qt == 0) {
+                    z = wave_sum(z);
+                    if (lane == 0)
+                        zs[qc] = z;
+                }
+            }
+        }
+        if (vt < IT) {
+            const int i = 32 * vt + n;
+#pragma unroll
+            for (int s = 0; s < DK / 16; ++s)
+                mma(av, frag_row(Rs + (32 * vc + cn) * PK + 16 * s + 8 * hf),
+                    frag_row(Ks + i * PK + 16 * s + 8 * hf));
+            av *= dc.out[i];
+        }
+        const float la = la0.value(P);      // wave GW: this chunk's log-decays
+        if (w == GW) {
+            if (step + 1 < nchunk)
+                chunk_decays<C>(D[(step + 1) & 1], la1.value(P), lane);
             la0 = la1;
-            la1 = step + 2 < nchunk ? gate(c - 2) : 0.f;
+            if (step + 2 < nchunk)
+                gate(la1, c - 2);
         }
         __syncthreads();            // P, Y and the sums
 
-        if (w == 0 && P.dla) {
+        if (w == GW && P.dla) {
             const bool live = lane < C && lane < cnt;
             float u = 0.f, y = 0.f, zz = 0.f;
             if (live) {
-                const int t = lane / 16;
+                const int t = lane / 32;
                 for (int j = 0; j <= t; ++j)
                     u += rowx[j][lane];
-                for (int i = t; i < IT; ++i)
-                    if (16 * i < cnt)
-                        u -= colx[i][lane];
+                for (int i = 2 * t; i < 2 * IT; ++i)
+                    u -= colx[i][lane];
 #pragma unroll
-                for (int i = 0; i < W; ++i) {
+                for (int i = 0; i < KT; ++i) {
                     u += xs[i][lane];
                     y += ys[i][lane];
                 }
             }
 #pragma unroll
-            for (int i = 0; i < W; ++i)
+            for (int i = 0; i < KT; ++i)
                 zz += zs[i];
             // suffix sums of u, prefix sums of y before the token
             float before = y;
@@ -348,75 +342,74 @@ __global__ __launch_bounds__((GradShape<T, DK, DV>::NT)) void linear_grad_kernel
             }
         }
 
-        // what comes from the chunk's own tokens, and R <- all R + q^T (in (.) do)
-        const float all = dc.all;
+        // what comes from the chunk's own tokens
+        if (qt < IT) {
 #pragma unroll
-        for (int i = 0; i < TK; ++i)
-#pragma unroll
-            for (int cc = 0; cc < NC; ++cc)
-                R[i][cc] *= all;
-#pragma unroll
-        for (int s = 0; s < KS; ++s) {
-#pragma unroll
-            for (int t = 0; t < TR; ++t) {
-                const int c0 = tile_first<DK>(w * TR + t);
-                const FragV<T> kf = frag_cols<PK>(Ks + 32 * s * PK, c0, tile_step<DK>(), lane);
-                const FragV<T> qf = frag_cols<PK>(Qs + 32 * s * PK, c0, tile_step<DK>(), lane);
-#pragma unroll
-                for (int it = 0; it < IT; ++it) {
-                    if (it >= 2 * s)        // dq_i: j <= i
-                        mma(aq[t][it], kf, frag_row(Ys + (16 * it + n) * PP + 32 * s + 8 * g));
-                    if (it < 2 * s + 2)     // dk_j: i >= j
-                        mma(ak[t][it], qf, frag_cols<PP>(Ys + 32 * s * PP, 16 * it, 4, lane));
-                }
+            for (int s = 0; s < KS; ++s) {
+                if (s / 2 <= qt)        // dq_i: j <= i
+                    mma(aq, frag_cols<PK, true>(Ks + 16 * s * PK + 32 * qc, lane),
+                        frag_row(Ys + (32 * qt + n) * PP + 16 * s + 8 * hf));
+                if (s / 2 >= qt)        // dk_j: i >= j
+                    mma(ak, frag_cols<PK, true>(Qs + 16 * s * PK + 32 * qc, lane),
+                        frag_cols<PP, false>(Ys + 16 * s * PP + 32 * qt, lane));
             }
-            float wt[8];
-            lds_ld8(dc.in + 32 * s + 8 * g, wt);
-#pragma unroll
-            for (int cc = 0; cc < NC; ++cc) {
-                const FragV<T> of = frag_cols<PV>(Os + 32 * s * PV, tile_first<DV>(w * NC + cc),
-                                                  tile_step<DV>(), lane);
-#pragma unroll
-                for (int it = 0; it < IT; ++it)
-                    if (it < 2 * s + 2)
-                        mma(av[cc][it], of, frag_cols<PP>(Ps + 32 * s * PP, 16 * it, 4, lane));
-                const Split<T> os(of, wt);
-#pragma unroll
-                for (int i = 0; i < TK; ++i)
-                    os.mma_a(R[i][cc], frag_cols<PK>(Qs + 32 * s * PK, 16 * i, 4, lane));
-            }
-        }
-#pragma unroll
-        for (int it = 0; it < IT; ++it) {
-            const int i = 16 * it + n;
+            const int i = 32 * qt + n;
             if (i < cnt) {
                 const long t0 = (long)c * C + i;
 #pragma unroll
-                for (int t = 0; t < TR; ++t) {
-                    const int c0 = tile_first<DK>(w * TR + t) + tile_step<DK>() * g;
-                    store4<T>(P.dq, P.ws_dq, qat + t0 * qrow + c0, aq[t][it]);
-                    store4<T>(P.dk_, P.ws_dk, kat + t0 * krow + c0, ak[t][it]);
-                }
+                for (int u = 0; u < 2; ++u) {
+                    const int c0 = 32 * qc + 16 * u + 8 * hf;
+                    float x[8], y[8];
 #pragma unroll
-                for (int cc = 0; cc < NC; ++cc)
-                    store4<T>(P.dv_, P.ws_dv,
-                              vat + t0 * vrow + tile_first<DV>(w * NC + cc) + tile_step<DV>() * g,
-                              av[cc][it]);
+                    for (int r = 0; r < 8; ++r) {
+                        x[r] = aq[8 * u + r];
+                        y[r] = ak[8 * u + r];
+                    }
+                    store8<T>(P.dq, P.ws_dq, qat + t0 * qrow + c0, x);
+                    store8<T>(P.dk_, P.ws_dk, kat + t0 * krow + c0, y);
+                }
             }
         }
+        // and R <- all R + q^T (in (.) do)
+        const float all = dc.all;
+#pragma unroll
+        for (int i = 0; i < TR; ++i)
+            R[i] *= all;
+#pragma unroll
+        for (int s = 0; s < KS; ++s) {
+            const FragV<T> of = frag_cols<PV, true>(Os + 16 * s * PV + 32 * vc, lane);
+            if (vt < IT && s / 2 >= vt)
+                mma(av, of, frag_cols<PP, false>(Ps + 16 * s * PP + 32 * vt, lane));
+            float wt[8];
+            lds_ld8(dc.in + 16 * s + 8 * hf, wt);
+            const Split<T> o3(of, wt);
+#pragma unroll
+            for (int i = 0; i < TR; ++i)
+                o3.mma_a(R[i], frag_cols<PK, false>(Qs + 16 * s * PK + 32 * (vt * TR + i), lane));
+        }
+        if (vt < IT && 32 * vt + n < cnt) {
+            const long t0 = (long)c * C + 32 * vt + n;
+#pragma unroll
+            for (int u = 0; u < 2; ++u) {
+                float x[8];
+#pragma unroll
+                for (int r = 0; r < 8; ++r)
+                    x[r] = av[8 * u + r];
+                store8<T>(P.dv_, P.ws_dv, vat + t0 * vrow + 32 * vc + 16 * u + 8 * hf, x);
+            }
+        }
+        share_state();              // Rs was read before the barrier above
         __syncthreads();            // the chunk's tiles have been read
     }
     if (B.index == 0 && P.dS0) {
         float *dst = P.dS0 + (B.slot * P.H + h) * hs;
 #pragma unroll
-        for (int i = 0; i < TK; ++i)
+        for (int i = 0; i < TR; ++i)
 #pragma unroll
-            for (int c = 0; c < NC; ++c)
-#pragma unroll
-                for (int r = 0; r < 4; ++r)
-                    dst[(16 * i + 4 * g + r) * DV + vcol(c)] = R[i][c][r];
+            for (int r = 0; r < 16; ++r)
+                dst[row(i, r) * DV + col] = R[i][r];
     }
-    if (P.ws_dla && w == 0) {
+    if (P.ws_dla && w == GW) {
 #pragma unroll
         for (int off = 32; off >= 1; off >>= 1)
             gsum += __shfl_xor(gsum, off, WAVE);

@@ -61,27 +61,38 @@ __device__ __forceinline__ Block get_block(const LinearParams &P, long b) {
 }
 
 // ---------------------------------------------------------------------------
-// Fragments: the 8 contraction elements of one lane for a step of 32.  For
-// bfloat16 they are the operand of one v_mfma_f32_16x16x32_bf16; for float32
-// element s of every lane is the operand of the s-th of eight
-// v_mfma_f32_16x16x4_f32.  Lane l holds row (A) or column (B) l & 15; which
-// 8 of the 32 contraction indices it holds only has to agree between A and B.
+// Fragments of 32 x 32 tiles: the 8 contraction elements of one lane for a
+// step of 16.  For bfloat16 they are the operand of one
+// v_mfma_f32_32x32x16_bf16 (half as many operand reads and instructions for
+// the same products as 16 x 16 tiles); for float32 element s of every lane is
+// the operand of the s-th of eight v_mfma_f32_32x32x2_f32.  Lane l holds row
+// (A) or column (B) n = l & 31 and the half h = l >> 5 of the contraction;
+// which 8 of the 16 indices those are only has to agree between A and B.
+// Accumulator register r of lane l: row 8 (r / 4) + 4 h + r % 4, column n.
 // ---------------------------------------------------------------------------
 template <typename T> struct Frag;
 template <> struct Frag<bf16> { typedef bf16x8 V; };
 template <> struct Frag<float> { typedef f32x8 V; };
 template <typename T> using FragV = typename Frag<T>::V;
+typedef float f32x16 __attribute__((ext_vector_type(16)));
 
-__device__ __forceinline__ void mma(f32x4 &acc, bf16x8 a, bf16x8 b) {
-    acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b, acc, 0, 0, 0);
+__device__ __forceinline__ f32x16 zero16() {
+    f32x16 z;
+#pragma unroll
+    for (int i = 0; i < 16; ++i)
+        z[i] = 0.f;
+    return z;
 }
-__device__ __forceinline__ void mma(f32x4 &acc, f32x8 a, f32x8 b) {
+__device__ __forceinline__ void mma(f32x16 &acc, bf16x8 a, bf16x8 b) {
+    acc = __builtin_amdgcn_mfma_f32_32x32x16_bf16(a, b, acc, 0, 0, 0);
+}
+__device__ __forceinline__ void mma(f32x16 &acc, f32x8 a, f32x8 b) {
 #pragma unroll
     for (int s = 0; s < 8; ++s)
-        acc = __builtin_amdgcn_mfma_f32_16x16x4f32(a[s], b[s], acc, 0, 0, 0);
+        acc = __builtin_amdgcn_mfma_f32_32x32x2f32(a[s], b[s], acc, 0, 0, 0);
 }
 
-// p: this lane's row at its 8 consecutive elements (contraction 8 g + e).
+// p: this lane's row at its 8 consecutive elements (contraction 8 h + e).
 __device__ __forceinline__ bf16x8 frag_row(const bf16 *p) {
     return *reinterpret_cast<const bf16x8 *>(p);
 }
@@ -90,92 +101,80 @@ __device__ __forceinline__ f32x8 frag_row(const float *p) {
     const f32x4 b = *reinterpret_cast<const f32x4 *>(p + 4);
     return __builtin_shufflevector(a, b, 0, 1, 2, 3, 4, 5, 6, 7);
 }
-// p: this lane's row at 4 g; elements 4 g .. + 3 and 16 + 4 g .. + 3, the
-// order of two accumulator tiles (frag_acc).
+// p: this lane's row at 4 h; elements 4 h .. + 3 and 8 + 4 h .. + 3, the order
+// of an accumulator's rows (frag_acc).
 __device__ __forceinline__ bf16x8 frag_row_perm(const bf16 *p) {
     const bf16x4 a = *reinterpret_cast<const bf16x4 *>(p);
-    const bf16x4 b = *reinterpret_cast<const bf16x4 *>(p + 16);
+    const bf16x4 b = *reinterpret_cast<const bf16x4 *>(p + 8);
     return __builtin_shufflevector(a, b, 0, 1, 2, 3, 4, 5, 6, 7);
 }
 __device__ __forceinline__ f32x8 frag_row_perm(const float *p) {
     const f32x4 a = *reinterpret_cast<const f32x4 *>(p);
-    const f32x4 b = *reinterpret_cast<const f32x4 *>(p + 16);
+    const f32x4 b = *reinterpret_cast<const f32x4 *>(p + 8);
     return __builtin_shufflevector(a, b, 0, 1, 2, 3, 4, 5, 6, 7);
 }
-// Two accumulator tiles (rows 16 t + 4 g + r and 16 (t + 1) + 4 g + r) as the
-// fragment whose contraction runs over their 32 rows.
-template <typename T> __device__ __forceinline__ FragV<T> frag_acc(f32x4 a, f32x4 b) {
+// Rows 16 b .. + 15 of an accumulator tile as the fragment whose contraction
+// runs over them.
+template <typename T> __device__ __forceinline__ FragV<T> frag_acc(const f32x16 &a, int b) {
     FragV<T> f;
 #pragma unroll
-    for (int e = 0; e < 4; ++e) {
-        f[e] = from_f32<T>(a[e]);
-        f[4 + e] = from_f32<T>(b[e]);
-    }
+    for (int e = 0; e < 8; ++e)
+        f[e] = from_f32<T>(a[8 * b + e]);
     return f;
 }
 
-// Transposed read of a tile [token][column]: tokens 8 g + e of the 32 behind
-// `m`, at the 16 columns c(n) = c0 + cs * (n / 4) + n % 4 of lane n = l & 15.
-// bfloat16: ds_read_b64_tr_b16 gives lane n of a group of 16 column n of the
-// 4 rows x 16 columns whose 8-byte pieces the lanes point to (lane i: row
-// i / 4, columns 4 (i % 4) .. + 3).
-template <int PITCH>
-__device__ __forceinline__ bf16x8 frag_cols(const bf16 *m, int c0, int cs, int lane) {
-    const int g = lane >> 4, i = lane & 15;
-    const bf16 *p = m + (8 * g + i / 4) * PITCH + c0 + cs * (i & 3);
+// Channel of row or column n of a 32-channel tile.  The middle bits of the
+// groups of 4 change places, so that accumulator registers 0-7 and 8-15 of a
+// lane are 8 consecutive channels each, from 8 h and 16 + 8 h.
+__device__ __forceinline__ int chan(int n) {
+    const int q = n >> 2;
+    return 4 * ((q & 4) | ((q & 1) << 1) | ((q >> 1) & 1)) + (n & 3);
+}
+
+// Transposed read of a tile [token][channel]: tokens 8 h + e (PERM: 4 h .. + 3
+// and 8 + 4 h .. + 3) of the 16 behind `m`, channel n of the 32 behind `m` (CH:
+// in the order of chan()).  bfloat16: ds_read_b64_tr_b16 gives lane i of a
+// group of 16 column i of the 4 rows x 16 columns whose 8-byte pieces the
+// lanes point to (lane i: row i / 4, columns 4 (i % 4) .. + 3).
+template <int PITCH, bool CH, bool PERM = false>
+__device__ __forceinline__ bf16x8 frag_cols(const bf16 *m, int lane) {
+    const int i = lane & 15, h = lane >> 5, q = 4 * ((lane >> 4) & 1) + (i & 3);
+    const bf16 *p = m + ((PERM ? 4 : 8) * h + (i >> 2)) * PITCH + (CH ? chan(4 * q) : 4 * q);
     union { s16x4 s[2]; bf16x8 v; } u;
     u.s[0] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4 *)p);
-    u.s[1] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4 *)(p + 4 * PITCH));
+    u.s[1] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4 *)(p + (PERM ? 8 : 4) * PITCH));
     return u.v;
 }
-template <int PITCH>
-__device__ __forceinline__ f32x8 frag_cols(const float *m, int c0, int cs, int lane) {
-    const int g = lane >> 4, n = lane & 15;
-    const float *p = m + 8 * g * PITCH + c0 + cs * (n >> 2) + (n & 3);
+template <int PITCH, bool CH, bool PERM = false>
+__device__ __forceinline__ f32x8 frag_cols(const float *m, int lane) {
+    const int n = lane & 31, h = lane >> 5;
+    const float *p = m + (PERM ? 4 : 8) * h * PITCH + (CH ? chan(n) : n);
     f32x8 f;
 #pragma unroll
     for (int e = 0; e < 8; ++e)
-        f[e] = p[e * PITCH];
+        f[e] = p[(e + (PERM && e >= 4 ? 4 : 0)) * PITCH];
     return f;
 }
 
-// As frag_cols, rows 4 g .. + 3 and 16 + 4 g .. + 3 (the order of frag_acc).
-template <int PITCH>
-__device__ __forceinline__ bf16x8 frag_cols_perm(const bf16 *m, int c0, int cs, int lane) {
-    const int g = lane >> 4, i = lane & 15;
-    const bf16 *p = m + (4 * g + i / 4) * PITCH + c0 + cs * (i & 3);
-    union { s16x4 s[2]; bf16x8 v; } u;
-    u.s[0] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4 *)p);
-    u.s[1] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4 *)(p + 16 * PITCH));
-    return u.v;
-}
-template <int PITCH>
-__device__ __forceinline__ f32x8 frag_cols_perm(const float *m, int c0, int cs, int lane) {
-    const int g = lane >> 4, n = lane & 15;
-    const float *p = m + 4 * g * PITCH + c0 + cs * (n >> 2) + (n & 3);
-    f32x8 f;
-#pragma unroll
-    for (int e = 0; e < 8; ++e)
-        f[e] = p[(e + (e & 4 ? 12 : 0)) * PITCH];
-    return f;
-}
-
-// x (.) w as an operand that keeps 32-bit products: bfloat16 as the sum of two
-// operands (16 significant bits; a single one would leave 2^-9 in a float32
-// state), float32 as one.
+// x (.) w as an operand that keeps 32-bit products: bfloat16 as the sum of
+// three operands (24 significant bits; one would leave 2^-8 of a term in a
+// float32 state, two 2^-16), float32 as one.
 template <typename T> struct Split;
 template <> struct Split<bf16> {
-    bf16x8 hi, lo;
+    bf16x8 hi, mid, lo;
     __device__ __forceinline__ Split(bf16x8 x, const float (&w)[8]) {
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
             const float y = to_f32(x[e]) * w[e];
             hi[e] = static_cast<bf16>(y);
-            lo[e] = static_cast<bf16>(y - static_cast<float>(hi[e]));
+            const float z = y - static_cast<float>(hi[e]);
+            mid[e] = static_cast<bf16>(z);
+            lo[e] = static_cast<bf16>(z - static_cast<float>(mid[e]));
         }
     }
-    __device__ __forceinline__ void mma_a(f32x4 &acc, bf16x8 a) const {
+    __device__ __forceinline__ void mma_a(f32x16 &acc, bf16x8 a) const {
         mma(acc, a, lo);
+        mma(acc, a, mid);
         mma(acc, a, hi);
     }
 };
@@ -186,7 +185,7 @@ template <> struct Split<float> {
         for (int e = 0; e < 8; ++e)
             f[e] = x[e] * w[e];
     }
-    __device__ __forceinline__ void mma_a(f32x4 &acc, f32x8 a) const { mma(acc, a, f); }
+    __device__ __forceinline__ void mma_a(f32x16 &acc, f32x8 a) const { mma(acc, a, f); }
 };
 
 // ---------------------------------------------------------------------------
@@ -237,24 +236,55 @@ __device__ __forceinline__ double chunk_decays(Decays<C> &D, float la, int lane)
     return all;
 }
 
-// 2^(G_i - G_j)
+// 2^(G_i - G_j) of 8 consecutive j, 0 right of the diagonal (j > i)
 template <typename T, int C>
-__device__ __forceinline__ float decay_between(const Decays<C> &D, float hi_i, float lo_i, int j) {
-    float x = hi_i - D.hi[j];
+__device__ __forceinline__ void decay_between(const Decays<C> &D, float hi_i, float lo_i, int i,
+                                              int j, float (&d)[8]) {
+    float x[8];
+    lds_ld8(D.hi + j, x);
+#pragma unroll
+    for (int r = 0; r < 8; ++r)
+        x[r] = hi_i - x[r];
     // bfloat16 products: the low parts (2^-24 of a prefix sum) are far below
     // their rounding
-    if (sizeof(T) == 4)
-        x += lo_i - D.lo[j];
-    return exp2_fast(x);
+    if (sizeof(T) == 4) {
+        float lo[8];
+        lds_ld8(D.lo + j, lo);
+#pragma unroll
+        for (int r = 0; r < 8; ++r)
+            x[r] += lo_i - lo[r];
+    }
+#pragma unroll
+    for (int r = 0; r < 8; ++r) {
+        const float y = exp2_fast(x[r]);
+        d[r] = j + r <= i ? y : 0.f;
+    }
 }
 
-// log-decay of token row `row`, head h
-template <typename T>
-__device__ __forceinline__ float load_gate(const LinearParams &P, long row, int h) {
-    if (P.gate == KDN_GATE_HEAD)
-        return static_cast<const float *>(P.la)[h];
-    return to_f32(static_cast<const T *>(P.la)[row * P.H + h]);
-}
+// The log-decay of a token on its way: the bits as they were loaded, made a
+// float only where they are used (a conversion behind the load would wait for
+// it, and for the tiles requested before it).
+template <typename T> struct GateReg {
+    uint32_t bits = 0;
+    // token row `row` of head h; `live` false: 0
+    __device__ __forceinline__ void load(const LinearParams &P, float head, long row, int h,
+                                         bool live) {
+        if (P.gate == KDN_GATE_HEAD) {
+            bits = live ? __float_as_uint(head) : 0;
+            return;
+        }
+        bits = 0;
+        if (live) {
+            if (sizeof(T) == 2)
+                bits = static_cast<const uint16_t *>(P.la)[row * P.H + h];
+            else
+                bits = static_cast<const uint32_t *>(P.la)[row * P.H + h];
+        }
+    }
+    __device__ __forceinline__ float value(const LinearParams &P) const {
+        return __uint_as_float(sizeof(T) == 2 && P.gate == KDN_GATE_TOKEN ? bits << 16 : bits);
+    }
+};
 
 // ---------------------------------------------------------------------------
 // A tile [ROWS][COLS] from global memory, held in registers between its load
@@ -272,6 +302,13 @@ template <typename T, int ROWS, int COLS, int NT> struct TileRegs {
     // base: the tile's first row (element pointer), stride in elements
     __device__ __forceinline__ void load(const T *base, long stride, int count, int tid) {
         const int row = tid / PER_ROW, c = (tid % PER_ROW) * VEC;
+        if (count >= ROWS) {
+            const T *p = base + row * stride + c;
+#pragma unroll
+            for (int i = 0; i < N; ++i)
+                r[i] = *reinterpret_cast<const uint4 *>(p + i * STEP * stride);
+            return;
+        }
 #pragma unroll
         for (int i = 0; i < N; ++i) {
             const int rr = row + i * STEP;
