@@ -22,6 +22,7 @@ struct LinearParams {
     int gate;               // kdn_gate
     long tokens;            // rows of q, k, v, o
     long q_stride, k_stride, v_stride;   // elements between tokens
+    long o_stride;          // of d_o
     const void *q, *k, *v;
     const void *la;         // log_alpha
     // blocks of consecutive tokens of one sequence, the unit of a workgroup

@@ -37,8 +37,7 @@ constexpr int NT = 256;
 
 template <typename T, int DK, int DV> struct Shape {
     static constexpr int C = linear_chunk(sizeof(T) == 2);
-    static constexpr int PAD = 16 / sizeof(T);
-    static constexpr int PK = DK + PAD, PV = DV + PAD, PP = C + PAD;   // LDS pitches
+    static constexpr int PK = lds_pitch<T>(DK), PV = lds_pitch<T>(DV), PP = lds_pitch<T>(C);
     static constexpr int NCT = DV / 32;        // column tiles
     static constexpr int TW = NT / WAVE / NCT; // waves that share a column tile
     static constexpr int TK = DK / 32 / TW;    // row tiles of S in a wave
@@ -153,7 +152,7 @@ __global__ __launch_bounds__(NT, 2) void linear_kernel(LinearParams P) {
     if (MODE == ROWN) {
         k = q;
         ks = P.q_stride;
-        vs = (long)P.H * DV;
+        vs = P.o_stride;
         v = static_cast<const T *>(P.d_o) + B.first * vs + h * DV;
     }
 
@@ -165,8 +164,10 @@ __global__ __launch_bounds__(NT, 2) void linear_kernel(LinearParams P) {
     const float head = P.gate == KDN_GATE_HEAD ? static_cast<const float *>(P.la)[h] : 0.f;
     GateReg<T> la0, la1;            // this lane's token of the next chunks
     auto gate = [&](GateReg<T> &x, int c) {
-        const int i = c * C + lane;
-        x.load(P, head, B.first + i, h, lane < C && i < B.count);
+        x.template load<C>(P, B.first + (long)c * C, B.count - c * C, h, lane);
+    };
+    auto gate_value = [&](const GateReg<T> &x, int c) {
+        return x.value(P, head, lane < C && c * C + lane < B.count);
     };
     auto load_chunk = [&](int c) {
         const int cnt = B.count - c * C;
@@ -198,7 +199,7 @@ __global__ __launch_bounds__(NT, 2) void linear_kernel(LinearParams P) {
 
     double total = 0.;              // base-2 log of the block's decay (wave GW)
     if (w == GW)
-        total = chunk_decays<C>(D[0], la0.value(P), lane);
+        total = chunk_decays<C>(D[0], gate_value(la0, chunk(0)), lane);
     if (SHARED)
         S.share(Ss, PK);
 
@@ -269,39 +270,44 @@ __global__ __launch_bounds__(NT, 2) void linear_kernel(LinearParams P) {
             for (int t = 0; t < OT; ++t)
                 o[t] *= dc.in[32 * (t * TW + (IT >= TW ? tw : 0)) + n];
         }
-        if (w == GW) {              // the next chunk's decays
-            if (step + 1 < nchunk)
-                total += chunk_decays<C>(D[(step + 1) & 1], la1.value(P), lane);
-            if (step + 2 < nchunk)
-                gate(la1, chunk(step + 2));
-        }
-        if (MODE == OUT)
-            __syncthreads();        // P
 
-        // v^T P^T, and the state: S <- all S + k^T (out (.) v)
+        // the state: S <- all S + k^T (out (.) v)
         const float all = dc.all;
 #pragma unroll
         for (int i = 0; i < TK; ++i)
             S.t[i] *= all;
+        FragV<T> vf[KS];
 #pragma unroll
         for (int s = 0; s < KS; ++s) {
-            const FragV<T> vf = frag_cols<PV, true>(Vs + 16 * s * PV + 32 * ct, lane);
-            if (MODE == OUT) {
+            vf[s] = frag_cols<PV, true>(Vs + 16 * s * PV + 32 * ct, lane);
+            float wt[8];
+            lds_ld8((MODE == ROWN ? dc.in : dc.out) + 16 * s + 8 * hf, wt);
+            FragV<T> kf[TK];
+#pragma unroll
+            for (int i = 0; i < TK; ++i)
+                kf[i] = frag_cols<PK, false>(Ks + 16 * s * PK + 32 * (tw * TK + i), lane);
+            Split<T>(vf[s], wt).template mma_a<TK>(S.t, kf);
+        }
+        if (w == GW) {              // the next chunk's decays
+            if (step + 1 < nchunk)
+                total += chunk_decays<C>(D[(step + 1) & 1], gate_value(la1, chunk(step + 1)), lane);
+            if (step + 2 < nchunk)
+                gate(la1, chunk(step + 2));
+        }
+        // P is whole, and q, k and v have been read: what follows reads P and
+        // registers only, and the next chunk's tiles may be stored
+        __syncthreads();
+
+        if (MODE == OUT) {
+            // o^T += v^T P^T
+#pragma unroll
+            for (int s = 0; s < KS; ++s)
 #pragma unroll
                 for (int t = 0; t < OT; ++t) {
                     const int it = t * TW + (IT >= TW ? tw : 0);
                     if (s / 2 <= it)
-                        mma(o[t], vf, frag_row(Ps + (32 * it + n) * PP + 16 * s + 8 * hf));
+                        mma(o[t], vf[s], frag_row(Ps + (32 * it + n) * PP + 16 * s + 8 * hf));
                 }
-            }
-            float wt[8];
-            lds_ld8((MODE == ROWN ? dc.in : dc.out) + 16 * s + 8 * hf, wt);
-            const Split<T> v3(vf, wt);
-#pragma unroll
-            for (int i = 0; i < TK; ++i)
-                v3.mma_a(S.t[i], frag_cols<PK, false>(Ks + 16 * s * PK + 32 * (tw * TK + i), lane));
-        }
-        if (MODE == OUT) {
 #pragma unroll
             for (int t = 0; t < OT; ++t) {
                 const int it = t * TW + tw, i = 32 * it + n;
@@ -320,8 +326,7 @@ __global__ __launch_bounds__(NT, 2) void linear_kernel(LinearParams P) {
             }
         }
         if (SHARED)
-            S.share(Ss, PK);        // read since the barrier above: by nobody
-        __syncthreads();            // the chunk's tiles have been read
+            S.share(Ss, PK);
     }
     if (MODE == OWN || MODE == ROWN) {
         S.store((MODE == OWN ? P.ws_state : P.ws_rstate) + sidx);

@@ -64,7 +64,8 @@ kdn_status linear_shape(kdn::LinearParams &P, int dtype, int N, int T, int H, in
 kdn_status token_stride(long long given, long long row, long long es, long *out) {
     if (given == 0)
         given = row;
-    if (given < row || given >= (1LL << 31))
+    // the rows of a chunk (64 bfloat16, 32 float32) lie within 2^32 bytes
+    if (given < row || given * es >= (1LL << 26))
         return KDN_ERR_SHAPE;
     if (given * es % 16 != 0)
         return KDN_ERR_ALIGN;
@@ -347,6 +348,7 @@ kdn_status kdn_linear_prefill_backward(kdn_dtype dtype, int N, int T, int H, int
     if (kdn_status st = token_stride(q_stride, (long long)Hq * d_k, es, &P.q_stride)) return st;
     if (kdn_status st = token_stride(k_stride, (long long)Hk * d_k, es, &P.k_stride)) return st;
     if (kdn_status st = token_stride(v_stride, (long long)Hv * d_v, es, &P.v_stride)) return st;
+    if (kdn_status st = token_stride(0, (long long)H * d_v, es, &P.o_stride)) return st;
     if (tok * H > 0 && (!q || !k || !v || !log_alpha || !d_o || !dq || !dk || !dv))
         return KDN_ERR_NULL;
     if (kdn_status st = packed_tables(P, packed))

@@ -37,8 +37,7 @@ template <typename T, int DK, int DV> struct GradShape {
     static constexpr int KT = DK / 32, VT = DV / 32;       // channel tiles
     static constexpr int TR = KT * VT / W;     // row tiles of R in a wave
     static constexpr int KS = C / 16;
-    static constexpr int PAD = 16 / sizeof(T);
-    static constexpr int PK = DK + PAD, PV = DV + PAD, PP = C + PAD;
+    static constexpr int PK = lds_pitch<T>(DK), PV = lds_pitch<T>(DV), PP = lds_pitch<T>(C);
 };
 
 // Store of channels of a token to the gradient (call dtype) or to the float32
@@ -116,7 +115,7 @@ __global__ __launch_bounds__((GradShape<T, DK, DV>::NT)) void linear_grad_kernel
     const T *q = static_cast<const T *>(P.q) + B.first * P.q_stride + hq * DK;
     const T *k = static_cast<const T *>(P.k) + B.first * P.k_stride + hk * DK;
     const T *v = static_cast<const T *>(P.v) + B.first * P.v_stride + hv * DV;
-    const long ostride = (long)P.H * DV;
+    const long ostride = P.o_stride;
     const T *od = static_cast<const T *>(P.d_o) + B.first * ostride + h * DV;
 
     TileRegs<T, C, DK, NT> qr, kr;
@@ -125,8 +124,10 @@ __global__ __launch_bounds__((GradShape<T, DK, DV>::NT)) void linear_grad_kernel
     const float head = P.gate == KDN_GATE_HEAD ? static_cast<const float *>(P.la)[h] : 0.f;
     GateReg<T> la0, la1;            // wave GW: this lane's token, this chunk and the next
     auto gate = [&](GateReg<T> &x, int c) {
-        const int i = c * C + lane;
-        x.load(P, head, B.first + i, h, lane < C && i < B.count);
+        x.template load<C>(P, B.first + (long)c * C, B.count - c * C, h, lane);
+    };
+    auto gate_value = [&](const GateReg<T> &x, int c) {
+        return x.value(P, head, lane < C && c * C + lane < B.count);
     };
     auto load_chunk = [&](int c) {
         const int cnt = B.count - c * C;
@@ -176,7 +177,7 @@ __global__ __launch_bounds__((GradShape<T, DK, DV>::NT)) void linear_grad_kernel
     if (qt < IT)
         load_state(nchunk - 1);
     if (w == GW)
-        chunk_decays<C>(D[0], la0.value(P), lane);
+        chunk_decays<C>(D[0], gate_value(la0, nchunk - 1), lane);
     share_state();
     double gsum = 0.;               // wave GW: sum of the block's d log_alpha (this lane's)
 
@@ -293,10 +294,10 @@ __global__ __launch_bounds__((GradShape<T, DK, DV>::NT)) void linear_grad_kernel
                     frag_row(Ks + i * PK + 16 * s + 8 * hf));
             av *= dc.out[i];
         }
-        const float la = la0.value(P);      // wave GW: this chunk's log-decays
+        const float la = gate_value(la0, c);     // wave GW: this chunk's log-decays
         if (w == GW) {
             if (step + 1 < nchunk)
-                chunk_decays<C>(D[(step + 1) & 1], la1.value(P), lane);
+                chunk_decays<C>(D[(step + 1) & 1], gate_value(la1, c - 1), lane);
             la0 = la1;
             if (step + 2 < nchunk)
                 gate(la1, c - 2);
@@ -382,10 +383,11 @@ __global__ __launch_bounds__((GradShape<T, DK, DV>::NT)) void linear_grad_kernel
                 mma(av, of, frag_cols<PP, false>(Ps + 16 * s * PP + 32 * vt, lane));
             float wt[8];
             lds_ld8(dc.in + 16 * s + 8 * hf, wt);
-            const Split<T> o3(of, wt);
+            FragV<T> qf[TR];
 #pragma unroll
             for (int i = 0; i < TR; ++i)
-                o3.mma_a(R[i], frag_cols<PK, false>(Qs + 16 * s * PK + 32 * (vt * TR + i), lane));
+                qf[i] = frag_cols<PK, false>(Qs + 16 * s * PK + 32 * (vt * TR + i), lane);
+            Split<T>(of, wt).template mma_a<TR>(R, qf);
         }
         if (vt < IT && 32 * vt + n < cnt) {
             const long t0 = (long)c * C + 32 * vt + n;

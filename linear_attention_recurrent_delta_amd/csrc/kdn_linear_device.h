@@ -41,14 +41,19 @@ __device__ __forceinline__ Block get_block(const LinearParams &P, long b) {
         B.slot = B.seq;
         return B;
     }
-    const int4 r = reinterpret_cast<const int4 *>(P.blocks)[b];
+    int4 r = reinterpret_cast<const int4 *>(P.blocks)[b];
+    r.x = __builtin_amdgcn_readfirstlane(r.x);      // the same in every lane: scalars
+    r.y = __builtin_amdgcn_readfirstlane(r.y);
+    r.z = __builtin_amdgcn_readfirstlane(r.z);
+    r.w = __builtin_amdgcn_readfirstlane(r.w);
     if (r.z < 0 || r.z >= P.N || r.x < 0 || r.y <= 0 || r.y > P.block ||
         (long)r.x + r.y > P.tokens || r.w < 0)
         return B;
-    const int b0 = P.block_offsets[r.z], b1 = P.block_offsets[r.z + 1];
+    const int b0 = __builtin_amdgcn_readfirstlane(P.block_offsets[r.z]);
+    const int b1 = __builtin_amdgcn_readfirstlane(P.block_offsets[r.z + 1]);
     if (b0 < 0 || b1 > P.nblocks || (long)b0 + r.w != b || b1 <= b)
         return B;
-    B.slot = P.slots ? P.slots[r.z] : r.z;
+    B.slot = P.slots ? __builtin_amdgcn_readfirstlane(P.slots[r.z]) : r.z;
     if (B.slot >= P.pool)
         B.slot = -1;
     B.first = r.x;
@@ -172,10 +177,18 @@ template <> struct Split<bf16> {
             lo[e] = static_cast<bf16>(z - static_cast<float>(mid[e]));
         }
     }
-    __device__ __forceinline__ void mma_a(f32x16 &acc, bf16x8 a) const {
-        mma(acc, a, lo);
-        mma(acc, a, mid);
-        mma(acc, a, hi);
+    // acc[i] += a[i] (x (.) w)
+    template <int N>
+    __device__ __forceinline__ void mma_a(f32x16 (&acc)[N], const bf16x8 (&a)[N]) const {
+#pragma unroll
+        for (int i = 0; i < N; ++i)
+            mma(acc[i], a[i], lo);
+#pragma unroll
+        for (int i = 0; i < N; ++i)
+            mma(acc[i], a[i], mid);
+#pragma unroll
+        for (int i = 0; i < N; ++i)
+            mma(acc[i], a[i], hi);
     }
 };
 template <> struct Split<float> {
@@ -185,7 +198,12 @@ template <> struct Split<float> {
         for (int e = 0; e < 8; ++e)
             f[e] = x[e] * w[e];
     }
-    __device__ __forceinline__ void mma_a(f32x16 &acc, f32x8 a) const { mma(acc, a, f); }
+    template <int N>
+    __device__ __forceinline__ void mma_a(f32x16 (&acc)[N], const f32x8 (&a)[N]) const {
+#pragma unroll
+        for (int i = 0; i < N; ++i)
+            mma(acc[i], a[i], f);
+    }
 };
 
 // ---------------------------------------------------------------------------
@@ -261,67 +279,79 @@ __device__ __forceinline__ void decay_between(const Decays<C> &D, float hi_i, fl
     }
 }
 
-// The log-decay of a token on its way: the bits as they were loaded, made a
-// float only where they are used (a conversion behind the load would wait for
-// it, and for the tiles requested before it).
+// ---------------------------------------------------------------------------
+// Loads of a chunk's rows through buffer descriptors: rows behind the last
+// return 0 without a branch.  (A guarded and an unguarded load path that meet
+// make the compiler wait for the loads in flight on each of them.)
+// ---------------------------------------------------------------------------
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t buf_rsrc(const void *base, unsigned bytes) {
+    return __builtin_amdgcn_make_buffer_rsrc(const_cast<void *>(base), (short)0, (int)bytes,
+                                             0x00020000);
+}
+
+// The log-decays of a chunk, one per lane, on their way: the bits as they were
+// loaded, made a float only where they are used.
 template <typename T> struct GateReg {
     uint32_t bits = 0;
-    // token row `row` of head h; `live` false: 0
-    __device__ __forceinline__ void load(const LinearParams &P, float head, long row, int h,
-                                         bool live) {
-        if (P.gate == KDN_GATE_HEAD) {
-            bits = live ? __float_as_uint(head) : 0;
+    // tokens first .. + count - 1 (at most C) of head h; lane j has token j
+    template <int C>
+    __device__ __forceinline__ void load(const LinearParams &P, long first, int count, int h,
+                                         int lane) {
+        if (P.gate == KDN_GATE_HEAD)
             return;
-        }
-        bits = 0;
-        if (live) {
-            if (sizeof(T) == 2)
-                bits = static_cast<const uint16_t *>(P.la)[row * P.H + h];
-            else
-                bits = static_cast<const uint32_t *>(P.la)[row * P.H + h];
-        }
+        const int rows = min(count, C);
+        const auto r = buf_rsrc(static_cast<const T *>(P.la) + first * P.H + h,
+                                rows > 0 ? ((rows - 1) * (unsigned)P.H + 1) * sizeof(T) : 0u);
+        const int at = (int)(lane * (unsigned)P.H * sizeof(T));
+        if constexpr (sizeof(T) == 2)
+            bits = __builtin_amdgcn_raw_buffer_load_b16(r, at, 0, 0);
+        else
+            bits = __builtin_amdgcn_raw_buffer_load_b32(r, at, 0, 0);
     }
-    __device__ __forceinline__ float value(const LinearParams &P) const {
-        return __uint_as_float(sizeof(T) == 2 && P.gate == KDN_GATE_TOKEN ? bits << 16 : bits);
+    // head: the head's constant; live: the lane has a token
+    __device__ __forceinline__ float value(const LinearParams &P, float head, bool live) const {
+        if (P.gate == KDN_GATE_HEAD)
+            return live ? head : 0.f;
+        return __uint_as_float(sizeof(T) == 2 ? bits << 16 : bits);
     }
 };
 
-// ---------------------------------------------------------------------------
+// Elements between the rows of an LDS tile of D columns.  Rows n = 0 .. 15 at
+// the same 16 bytes (frag_row) have to fall into different groups of 4 banks
+// (the pitch an odd multiple of 4 of the 64), and 4 rows of 8 banks each
+// (frag_cols) next to each other: 76 and 36 banks for bfloat16 (68 doubled the
+// cycles of every transposed read), one group more than the row for float32.
+template <typename T> constexpr int lds_pitch(int d) {
+    return sizeof(T) == 4 ? d + 4 : (d == 128 ? 152 : d + 8);
+}
+
 // A tile [ROWS][COLS] from global memory, held in registers between its load
 // and its store to LDS (NT threads, 16-byte pieces); rows behind `count` are
-// zero and not read.
-// ---------------------------------------------------------------------------
+// zero and not read.  The entry points keep ROWS strides below 2^32 bytes.
 template <typename T, int ROWS, int COLS, int NT> struct TileRegs {
     static constexpr int VEC = 16 / sizeof(T);
     static constexpr int PER_ROW = COLS / VEC;
     static constexpr int STEP = NT / PER_ROW;          // rows of one pass
     static constexpr int N = ROWS / STEP;
     static_assert(NT % PER_ROW == 0 && ROWS % STEP == 0, "tile shape");
-    uint4 r[N];
+    f32x4 r[N];
 
     // base: the tile's first row (element pointer), stride in elements
     __device__ __forceinline__ void load(const T *base, long stride, int count, int tid) {
-        const int row = tid / PER_ROW, c = (tid % PER_ROW) * VEC;
-        if (count >= ROWS) {
-            const T *p = base + row * stride + c;
+        const unsigned pitch = (unsigned)stride * sizeof(T);
+        const int rows = min(count, ROWS);
+        const auto d = buf_rsrc(base, rows > 0 ? (rows - 1) * pitch + COLS * sizeof(T) : 0u);
+        const unsigned at = (tid / PER_ROW) * pitch + (tid % PER_ROW) * 16;
 #pragma unroll
-            for (int i = 0; i < N; ++i)
-                r[i] = *reinterpret_cast<const uint4 *>(p + i * STEP * stride);
-            return;
-        }
-#pragma unroll
-        for (int i = 0; i < N; ++i) {
-            const int rr = row + i * STEP;
-            r[i] = make_uint4(0, 0, 0, 0);
-            if (rr < count)
-                r[i] = *reinterpret_cast<const uint4 *>(base + rr * stride + c);
-        }
+        for (int i = 0; i < N; ++i)
+            r[i] = __builtin_bit_cast(f32x4, __builtin_amdgcn_raw_buffer_load_b128(
+                                                 d, (int)(at + i * STEP * pitch), 0, 0));
     }
     template <int PITCH> __device__ __forceinline__ void store(T *lds, int tid) const {
         const int row = tid / PER_ROW, c = (tid % PER_ROW) * VEC;
 #pragma unroll
         for (int i = 0; i < N; ++i)
-            *reinterpret_cast<uint4 *>(lds + (row + i * STEP) * PITCH + c) = r[i];
+            *reinterpret_cast<f32x4 *>(lds + (row + i * STEP) * PITCH + c) = r[i];
     }
 };
 

@@ -425,8 +425,8 @@ def test_captured_step():
 
 def test_offsets_past_32_bits():
     """Rows so far apart, and a pool so large, that bytes and elements pass 2^31."""
-    T, H, d = 70, 1, 64
-    wide = 2 ** 25 + 8                                 # elements between tokens: 70 * 2^25 > 2^31
+    T, H, d = 140, 1, 64
+    wide = 2 ** 25 - 8                                 # elements between tokens: 140 * 2^25 > 2^32
     buf = torch.empty(T * wide, dtype=BF, device="cuda")
     q, k, v, la = make((1, T), H, H, H, H, d, d, BF, seed=3)
     parts = []

@@ -36,7 +36,7 @@ def prefill(lib, dtype=BF16, N=2, T=100, H=4, Hq=4, Hk=4, Hv=4, dk=64, dv=64, ga
     (dict(dv=256), EUNSUP), (dict(dk=0), ESHAPE), (dict(N=-1), ESHAPE), (dict(T=-1), ESHAPE),
     (dict(H=-4), ESHAPE), (dict(Hq=3), ESHAPE), (dict(Hk=0), ESHAPE), (dict(Hv=8), ESHAPE),
     (dict(N=1 << 20, T=1 << 20), ESHAPE), (dict(N=1 << 24, T=1, H=1 << 10, Hq=1, Hk=1, Hv=1), ESHAPE),
-    (dict(qs=4 * 64 - 8), ESHAPE), (dict(ks=4 * 64 + 4), EALIGN), (dict(vs=1 << 31), ESHAPE),
+    (dict(qs=4 * 64 - 8), ESHAPE), (dict(ks=4 * 64 + 4), EALIGN), (dict(vs=1 << 31), ESHAPE), (dict(vs=1 << 25), ESHAPE), (dict(dtype=F32, qs=1 << 24), ESHAPE),
     (dict(dtype=F32, vs=4 * 64 + 2), EALIGN),
     (dict(q=None), ENULL), (dict(k=None), ENULL), (dict(v=None), ENULL), (dict(la=None), ENULL),
     (dict(o=None), ENULL), (dict(q=A + 8), EALIGN), (dict(o=A + 6 * MB + 4), EALIGN),
