@@ -44,6 +44,16 @@ template <typename T, int DK, int DV> struct Shape {
     static constexpr int IT = C / 32;          // token tiles
     static constexpr int OT = (IT + TW - 1) / TW;   // token tiles of o in a wave
     static constexpr int KS = C / 16;          // contraction steps over tokens
+
+    template <int MODE> struct Lds {
+        static constexpr bool SHARED = MODE == OUT && TW > 1;    // S passes through LDS
+        __attribute__((aligned(16))) T Ks[C * PK];
+        __attribute__((aligned(16))) T Vs[C * PV];
+        __attribute__((aligned(16))) T Qs[MODE == OUT ? C * PK : 1];
+        __attribute__((aligned(16))) T Ps[MODE == OUT ? C * PP : 1];
+        __attribute__((aligned(16))) T Ss[SHARED ? DV * PK : 1];
+        __attribute__((aligned(16))) Decays<C> D[2];
+    };
 };
 
 // The part of the state of one wave: row tiles t TK .. + TK - 1 of column tile
@@ -114,29 +124,22 @@ template <typename T, int DK, int DV> struct StateAcc {
     }
 };
 
-template <typename T, int DK, int DV, int MODE>
-__global__ __launch_bounds__(NT, 2) void linear_kernel(LinearParams P) {
+// PARTS: of the split operands in the update of S (Split).
+template <typename T, int DK, int DV, int MODE, int PARTS>
+__device__ __forceinline__ void linear_walk(
+    const LinearParams &P, const Block &B, long b, int h,
+    typename Shape<T, DK, DV>::template Lds<MODE> &L) {
     using SH = Shape<T, DK, DV>;
     constexpr int C = SH::C, TK = SH::TK, KS = SH::KS, IT = SH::IT, OT = SH::OT, TW = SH::TW;
     constexpr int NCT = SH::NCT, PK = SH::PK, PV = SH::PV, PP = SH::PP;
-    constexpr bool SHARED = MODE == OUT && TW > 1;     // S passes through LDS
+    constexpr bool SHARED = SH::template Lds<MODE>::SHARED;
 
-    __shared__ __attribute__((aligned(16))) T Ks[C * PK];
-    __shared__ __attribute__((aligned(16))) T Vs[C * PV];
-    __shared__ __attribute__((aligned(16))) T Qs[MODE == OUT ? C * PK : 1];
-    __shared__ __attribute__((aligned(16))) T Ps[MODE == OUT ? C * PP : 1];
-    __shared__ __attribute__((aligned(16))) T Ss[SHARED ? DV * PK : 1];
-    __shared__ __attribute__((aligned(16))) Decays<C> D[2];
+    T *const Ks = L.Ks, *const Vs = L.Vs, *const Qs = L.Qs, *const Ps = L.Ps, *const Ss = L.Ss;
+    auto &D = L.D;
 
     const int tid = threadIdx.x, lane = tid & (WAVE - 1), w = tid / WAVE;
     const int hf = lane >> 5, n = lane & 31, cn = chan(n);
     const int ct = w % NCT, tw = w / NCT;
-    const long b = blockIdx.x / P.H;
-    const int h = blockIdx.x % P.H;
-    const Block B = get_block(P, b);
-    if (B.count == 0 || B.slot < 0 || (MODE == OWN && B.last) || (MODE == ROWN && B.index == 0))
-        return;
-
     constexpr int HK = MODE == CHUNKS ? DV : DK, HV = MODE == CHUNKS ? DK : DV;
     const T *q = static_cast<const T *>(P.q) + B.first * P.q_stride + (h / (P.H / P.Hq)) * HK;
     const T *k = static_cast<const T *>(P.k) + B.first * P.k_stride + (h / (P.H / P.Hk)) * HK;
@@ -246,24 +249,44 @@ __global__ __launch_bounds__(NT, 2) void linear_kernel(LinearParams P) {
                     lds_st8(Ps + i * PP + j, x);
                 }
             }
-            // o^T = S^T q^T, scaled to each token
-#pragma unroll
-            for (int t = 0; t < OT; ++t)
-                o[t] = zero16();
-#pragma unroll
-            for (int s = 0; s < DK / 16; ++s) {
-                FragV<T> sf;
+            // o^T = S^T q^T, scaled to each token; the operands of the next
+            // steps are read and rounded between the MFMAs
+            constexpr int NS = DK / 16;
+            auto read_q = [&](int s, int t) {
+                const int i = 32 * (t * TW + (IT >= TW ? tw : 0)) + n;
+                return SHARED ? frag_row(Qs + i * PK + 16 * s + 8 * hf)
+                              : frag_row_perm(Qs + i * PK + 16 * s + 4 * hf);
+            };
+            auto read_s = [&](int s) {
                 if constexpr (SHARED)
-                    sf = frag_row(Ss + (32 * ct + cn) * PK + 16 * s + 8 * hf);
+                    return frag_row(Ss + (32 * ct + cn) * PK + 16 * s + 8 * hf);
                 else
-                    sf = frag_acc<T>(S.t[s / 2], s % 2);
+                    return frag_acc<T>(S.t[s / 2], s % 2);
+            };
+            FragV<T> qf[2][OT], sf[2];
+#pragma unroll
+            for (int t = 0; t < OT; ++t) {
+                o[t] = zero16();
+                qf[0][t] = read_q(0, t);
+                qf[1][t] = read_q(1, t);
+            }
+            sf[0] = read_s(0);
+            if (SHARED)
+                sf[1] = read_s(1);
+#pragma unroll
+            for (int s = 0; s < NS; ++s) {
 #pragma unroll
                 for (int t = 0; t < OT; ++t) {
-                    const int i = 32 * (t * TW + (IT >= TW ? tw : 0)) + n;
-                    if constexpr (SHARED)
-                        mma(o[t], sf, frag_row(Qs + i * PK + 16 * s + 8 * hf));
-                    else
-                        mma(o[t], sf, frag_row_perm(Qs + i * PK + 16 * s + 4 * hf));
+                    mma(o[t], sf[s & 1], qf[s & 1][t]);
+                    if (s + 2 < NS)
+                        qf[s & 1][t] = read_q(s + 2, t);
+                    __builtin_amdgcn_sched_barrier(0);
+                }
+                if (SHARED) {
+                    if (s + 2 < NS)
+                        sf[s & 1] = read_s(s + 2);
+                } else if (s + 1 < NS) {
+                    sf[(s + 1) & 1] = read_s(s + 1);
                 }
             }
 #pragma unroll
@@ -272,22 +295,17 @@ __global__ __launch_bounds__(NT, 2) void linear_kernel(LinearParams P) {
         }
 
         // the state: S <- all S + k^T (out (.) v)
+        FragV<T> vf[KS];
+#pragma unroll
+        for (int s = 0; s < KS; ++s)
+            vf[s] = frag_cols<PV, true>(Vs + 16 * s * PV + 32 * ct, lane);
         const float all = dc.all;
 #pragma unroll
         for (int i = 0; i < TK; ++i)
             S.t[i] *= all;
-        FragV<T> vf[KS];
-#pragma unroll
-        for (int s = 0; s < KS; ++s) {
-            vf[s] = frag_cols<PV, true>(Vs + 16 * s * PV + 32 * ct, lane);
-            float wt[8];
-            lds_ld8((MODE == ROWN ? dc.in : dc.out) + 16 * s + 8 * hf, wt);
-            FragV<T> kf[TK];
-#pragma unroll
-            for (int i = 0; i < TK; ++i)
-                kf[i] = frag_cols<PK, false>(Ks + 16 * s * PK + 32 * (tw * TK + i), lane);
-            Split<T>(vf[s], wt).template mma_a<TK>(S.t, kf);
-        }
+        update_state<T, PARTS>(S.t, vf, MODE == ROWN ? dc.in : dc.out, hf, [&](int s, int i) {
+            return frag_cols<PK, false>(Ks + 16 * s * PK + 32 * (tw * TK + i), lane);
+        });
         if (w == GW) {              // the next chunk's decays
             if (step + 1 < nchunk)
                 total += chunk_decays<C>(D[(step + 1) & 1], gate_value(la1, chunk(step + 1)), lane);
@@ -335,6 +353,29 @@ __global__ __launch_bounds__(NT, 2) void linear_kernel(LinearParams P) {
     }
     if (MODE == OUT && B.last && P.S_out)
         S.store(P.S_out + (B.slot * P.H + h) * (long)(DK * DV));
+}
+
+template <typename T, int DK, int DV, int MODE>
+__global__ __launch_bounds__(NT, 2) void linear_kernel(LinearParams P) {
+    const long b = blockIdx.x / P.H;
+    const int h = blockIdx.x % P.H;
+    const Block B = get_block(P, b);
+    if (B.count == 0 || B.slot < 0 || (MODE == OWN && B.last) || (MODE == ROWN && B.index == 0))
+        return;
+    __shared__ typename Shape<T, DK, DV>::template Lds<MODE> L;
+    // three parts for a state that is returned and for what goes into one: the
+    // last block's in the prefill, the blocks' own (the forward ones of the
+    // gradient call, which only reads them rounded, excepted)
+    if constexpr (MODE == CHUNKS) {
+        linear_walk<T, DK, DV, MODE, 2>(P, B, b, h, L);
+    } else if constexpr (MODE == ROWN) {
+        linear_walk<T, DK, DV, MODE, 3>(P, B, b, h, L);
+    } else {
+        if (MODE == OWN ? P.d_o == nullptr : B.last)
+            linear_walk<T, DK, DV, MODE, 3>(P, B, b, h, L);
+        else
+            linear_walk<T, DK, DV, MODE, 2>(P, B, b, h, L);
+    }
 }
 
 // ---------------------------------------------------------------------------

@@ -38,6 +38,20 @@ template <typename T, int DK, int DV> struct GradShape {
     static constexpr int TR = KT * VT / W;     // row tiles of R in a wave
     static constexpr int KS = C / 16;
     static constexpr int PK = lds_pitch<T>(DK), PV = lds_pitch<T>(DV), PP = lds_pitch<T>(C);
+
+    struct Lds {
+        __attribute__((aligned(16))) T Qs[C * PK];
+        __attribute__((aligned(16))) T Ks[C * PK];
+        __attribute__((aligned(16))) T Vs[C * PV];
+        __attribute__((aligned(16))) T Os[C * PV];
+        __attribute__((aligned(16))) T Ps[C * PP];
+        __attribute__((aligned(16))) T Ys[C * PP];
+        __attribute__((aligned(16))) T Rs[DV * PK];      // R^T
+        __attribute__((aligned(16))) Decays<C> D[2];
+        // sums of X over a tile's keys, and over 16 of a tile's queries
+        __attribute__((aligned(16))) float rowx[IT][C], colx[2 * IT][C];
+        float xs[KT][C], ys[KT][C], zs[KT];
+    };
 };
 
 // Store of channels of a token to the gradient (call dtype) or to the float32
@@ -58,36 +72,26 @@ __device__ __forceinline__ void store4(void *out, float *part, long at, f32x4 x)
         lds_stn<4>(static_cast<T *>(out) + at, f);
 }
 
-template <typename T, int DK, int DV>
-__global__ __launch_bounds__((GradShape<T, DK, DV>::NT)) void linear_grad_kernel(LinearParams P) {
+// PARTS: of the split operands in the update of R (Split).
+template <typename T, int DK, int DV, int PARTS>
+__device__ __forceinline__ void grad_walk(const LinearParams &P, const Block &B, long b, int h,
+                                          typename GradShape<T, DK, DV>::Lds &L) {
     using SH = GradShape<T, DK, DV>;
     constexpr int C = SH::C, W = SH::W, NT = SH::NT, TR = SH::TR, KT = SH::KT, VT = SH::VT;
     constexpr int IT = SH::IT, KS = SH::KS, PK = SH::PK, PV = SH::PV, PP = SH::PP;
 
-    __shared__ __attribute__((aligned(16))) T Qs[C * PK];
-    __shared__ __attribute__((aligned(16))) T Ks[C * PK];
-    __shared__ __attribute__((aligned(16))) T Vs[C * PV];
-    __shared__ __attribute__((aligned(16))) T Os[C * PV];
-    __shared__ __attribute__((aligned(16))) T Ps[C * PP];
-    __shared__ __attribute__((aligned(16))) T Ys[C * PP];
-    __shared__ __attribute__((aligned(16))) T Rs[DV * PK];      // R^T
-    __shared__ __attribute__((aligned(16))) Decays<C> D[2];
-    // sums of X over a tile's keys, and over 16 of a tile's queries
-    __shared__ __attribute__((aligned(16))) float rowx[IT][C], colx[2 * IT][C];
-    __shared__ float xs[KT][C], ys[KT][C], zs[KT];
+    T *const Qs = L.Qs, *const Ks = L.Ks, *const Vs = L.Vs, *const Os = L.Os;
+    T *const Ps = L.Ps, *const Ys = L.Ys, *const Rs = L.Rs;
+    auto &D = L.D;
+    auto &rowx = L.rowx;
+    auto &colx = L.colx;
+    auto &xs = L.xs, &ys = L.ys;
+    auto &zs = L.zs;
 
     const int tid = threadIdx.x, lane = tid & (WAVE - 1), w = tid / WAVE;
     const int hf = lane >> 5, n = lane & 31, cn = chan(n);
     const int qc = w % KT, qt = w / KT;     // channel and token tile of dq and dk
     const int vc = w % VT, vt = w / VT;     // of dv; and column tile and row group of R
-    const long b = blockIdx.x / P.H;
-    const int h = blockIdx.x % P.H;
-    const Block B = get_block(P, b);
-    if (P.ws_dla && (B.count == 0 || B.slot < 0) && tid == 0)
-        P.ws_dla[b * P.H + h] = 0.;
-    if (B.count == 0)
-        return;
-
     const int hq = h / (P.H / P.Hq), hk = h / (P.H / P.Hk), hv = h / (P.H / P.Hv);
     // outputs: rows of the shared heads' partials have all H heads
     const long qrow = P.ws_dq ? (long)P.H * DK : (long)P.Hq * DK;
@@ -376,19 +380,16 @@ __global__ __launch_bounds__((GradShape<T, DK, DV>::NT)) void linear_grad_kernel
 #pragma unroll
         for (int i = 0; i < TR; ++i)
             R[i] *= all;
+        FragV<T> of[KS];
 #pragma unroll
         for (int s = 0; s < KS; ++s) {
-            const FragV<T> of = frag_cols<PV, true>(Os + 16 * s * PV + 32 * vc, lane);
+            of[s] = frag_cols<PV, true>(Os + 16 * s * PV + 32 * vc, lane);
             if (vt < IT && s / 2 >= vt)
-                mma(av, of, frag_cols<PP, false>(Ps + 16 * s * PP + 32 * vt, lane));
-            float wt[8];
-            lds_ld8(dc.in + 16 * s + 8 * hf, wt);
-            FragV<T> qf[TR];
-#pragma unroll
-            for (int i = 0; i < TR; ++i)
-                qf[i] = frag_cols<PK, false>(Qs + 16 * s * PK + 32 * (vt * TR + i), lane);
-            Split<T>(of, wt).template mma_a<TR>(R, qf);
+                mma(av, of[s], frag_cols<PP, false>(Ps + 16 * s * PP + 32 * vt, lane));
         }
+        update_state<T, PARTS>(R, of, dc.in, hf, [&](int s, int i) {
+            return frag_cols<PK, false>(Qs + 16 * s * PK + 32 * (vt * TR + i), lane);
+        });
         if (vt < IT && 32 * vt + n < cnt) {
             const long t0 = (long)c * C + 32 * vt + n;
 #pragma unroll
@@ -418,6 +419,23 @@ __global__ __launch_bounds__((GradShape<T, DK, DV>::NT)) void linear_grad_kernel
         if (lane == 0)
             P.ws_dla[b * P.H + h] = gsum;
     }
+}
+
+template <typename T, int DK, int DV>
+__global__ __launch_bounds__((GradShape<T, DK, DV>::NT)) void linear_grad_kernel(LinearParams P) {
+    const long b = blockIdx.x / P.H;
+    const int h = blockIdx.x % P.H;
+    const Block B = get_block(P, b);
+    if (P.ws_dla && (B.count == 0 || B.slot < 0) && threadIdx.x == 0)
+        P.ws_dla[b * P.H + h] = 0.;
+    if (B.count == 0)
+        return;
+    __shared__ typename GradShape<T, DK, DV>::Lds L;
+    // three parts where R ends as dS0
+    if (B.index == 0)
+        grad_walk<T, DK, DV, 3>(P, B, b, h, L);
+    else
+        grad_walk<T, DK, DV, 2>(P, B, b, h, L);
 }
 
 // Rows behind the last sequence of a packed batch: zero gradients.

@@ -161,50 +161,83 @@ __device__ __forceinline__ f32x8 frag_cols(const float *m, int lane) {
     return f;
 }
 
-// x (.) w as an operand that keeps 32-bit products: bfloat16 as the sum of
-// three operands (24 significant bits; one would leave 2^-8 of a term in a
-// float32 state, two 2^-16), float32 as one.
-template <typename T> struct Split;
-template <> struct Split<bf16> {
-    bf16x8 hi, mid, lo;
-    __device__ __forceinline__ Split(bf16x8 x, const float (&w)[8]) {
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-            const float y = to_f32(x[e]) * w[e];
-            hi[e] = static_cast<bf16>(y);
-            const float z = y - static_cast<float>(hi[e]);
-            mid[e] = static_cast<bf16>(z);
-            lo[e] = static_cast<bf16>(z - static_cast<float>(mid[e]));
+// x (.) w as an operand of more bits than T has: bfloat16 as the sum of PARTS
+// operands.  Three have 24 significant bits: states that a call returns, and
+// what goes into them, stay float32.  Two leave 2^-16 of a term (2.4e-6 of a
+// state as measured): for states that are only read rounded to bfloat16,
+// within a block or a chunk's saved state (one would show, at 2^-8).  float32
+// is one operand.  It is made in 4 PARTS steps, each a part of a pair of
+// elements, so that they can stand between MFMAs.
+template <typename T, int N> struct Split;
+template <int N> struct Split<bf16, N> {
+    static constexpr int PARTS = N;
+    bf16x8 part[N];                  // low to high
+    float y[2];                      // what is left of the pair
+    __device__ __forceinline__ void step(int i, bf16x8 x, const float (&w)[8]) {
+        const int p = 2 * (i / N), l = i % N;
+        if (l == 0) {
+            y[0] = to_f32(x[p]) * w[p];
+            y[1] = to_f32(x[p + 1]) * w[p + 1];
+        } else {
+            y[0] -= static_cast<float>(part[N - l][p]);
+            y[1] -= static_cast<float>(part[N - l][p + 1]);
         }
-    }
-    // acc[i] += a[i] (x (.) w)
-    template <int N>
-    __device__ __forceinline__ void mma_a(f32x16 (&acc)[N], const bf16x8 (&a)[N]) const {
-#pragma unroll
-        for (int i = 0; i < N; ++i)
-            mma(acc[i], a[i], lo);
-#pragma unroll
-        for (int i = 0; i < N; ++i)
-            mma(acc[i], a[i], mid);
-#pragma unroll
-        for (int i = 0; i < N; ++i)
-            mma(acc[i], a[i], hi);
+        part[N - 1 - l][p] = static_cast<bf16>(y[0]);
+        part[N - 1 - l][p + 1] = static_cast<bf16>(y[1]);
     }
 };
-template <> struct Split<float> {
-    f32x8 f;
-    __device__ __forceinline__ Split(f32x8 x, const float (&w)[8]) {
-#pragma unroll
-        for (int e = 0; e < 8; ++e)
-            f[e] = x[e] * w[e];
-    }
-    template <int N>
-    __device__ __forceinline__ void mma_a(f32x16 (&acc)[N], const f32x8 (&a)[N]) const {
-#pragma unroll
-        for (int i = 0; i < N; ++i)
-            mma(acc[i], a[i], f);
+template <int N> struct Split<float, N> {
+    static constexpr int PARTS = 1;
+    f32x8 part[1];
+    __device__ __forceinline__ void step(int i, f32x8 x, const float (&w)[8]) {
+        part[0][2 * i] = x[2 * i] * w[2 * i];
+        part[0][2 * i + 1] = x[2 * i + 1] * w[2 * i + 1];
     }
 };
+
+// acc[i] += sum over the chunk's tokens of a_i (w (.) b): the update of a state.
+// b[s]: the column operand of 16 tokens (s = 0 .. KS - 1), w: the tokens'
+// weights in LDS, rows(s, i): the row operand of tile i.  Between the MFMAs of
+// a step stand the reads and the splitting of the next one, a few
+// instructions behind each MFMA (sched_barrier holds them there: left alone
+// the compiler reads, waits, splits and multiplies one after the other, and
+// two waves a SIMD cannot hide that).
+template <typename T, int PARTS, int N, int KS, typename Rows>
+__device__ __forceinline__ void update_state(f32x16 (&acc)[N], const FragV<T> (&b)[KS],
+                                             const float *w, int hf, Rows rows) {
+    typedef Split<T, PARTS> S;
+    constexpr int M = S::PARTS * N, STEPS = 4 * S::PARTS;    // of 16 tokens
+    S cur, nxt;
+    FragV<T> a[N];
+    float wt[8];
+    lds_ld8(w + 8 * hf, wt);
+#pragma unroll
+    for (int i = 0; i < N; ++i)
+        a[i] = rows(0, i);
+#pragma unroll
+    for (int i = 0; i < STEPS; ++i)
+        cur.step(i, b[0], wt);
+#pragma unroll
+    for (int s = 0; s < KS; ++s) {
+        const bool more = s + 1 < KS;
+        if (more)
+            lds_ld8(w + 16 * (s + 1) + 8 * hf, wt);
+#pragma unroll
+        for (int m = 0; m < M; ++m) {
+            mma(acc[m % N], a[m % N], cur.part[m / N]);
+            if (more) {
+                if (m >= M - N)              // its last use in this step
+                    a[m % N] = rows(s + 1, m % N);
+#pragma unroll
+                for (int i = m * STEPS / M; i < (m + 1) * STEPS / M; ++i)
+                    nxt.step(i, b[s + 1], wt);
+            }
+            __builtin_amdgcn_sched_barrier(0);
+        }
+        if (more)
+            cur = nxt;
+    }
+}
 
 // ---------------------------------------------------------------------------
 // Decays of a chunk, all in powers of two.  Prefix sums of the log-decays run
