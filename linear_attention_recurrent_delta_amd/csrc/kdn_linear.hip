@@ -137,7 +137,7 @@ __device__ __forceinline__ void linear_walk(
     T *const Ks = L.Ks, *const Vs = L.Vs, *const Qs = L.Qs, *const Ps = L.Ps, *const Ss = L.Ss;
     auto &D = L.D;
 
-    const int tid = threadIdx.x, lane = tid & (WAVE - 1), w = tid / WAVE;
+    const int tid = threadIdx.x, lane = tid & (WAVE - 1), w = wave_id();
     const int hf = lane >> 5, n = lane & 31, cn = chan(n);
     const int ct = w % NCT, tw = w / NCT;
     constexpr int HK = MODE == CHUNKS ? DV : DK, HV = MODE == CHUNKS ? DK : DV;
@@ -172,12 +172,26 @@ __device__ __forceinline__ void linear_walk(
     auto gate_value = [&](const GateReg<T> &x, int c) {
         return x.value(P, head, lane < C && c * C + lane < B.count);
     };
-    auto load_chunk = [&](int c) {
-        const int cnt = B.count - c * C;
-        kr.load(k + (long)c * C * ks, ks, cnt, tid);
-        vr.load(v + (long)c * C * vs, vs, cnt, tid);
+    typedef TileRegs<T, C, DK, NT> KT;
+    typedef TileRegs<T, C, DV, NT> VT;
+    // part i of n of chunk c's loads of k and v, and its loads of q (a chunk
+    // behind the last: nothing is read)
+    auto tokens_of = [&](int c) { return c < nchunk && c >= 0 ? B.count - c * C : 0; };
+    auto load_kv = [&](int c, int i, int n) {
+        const typename KT::Source sk(k + (long)c * C * ks, ks, tokens_of(c), tid);
+        const typename VT::Source sv(v + (long)c * C * vs, vs, tokens_of(c), tid);
+        constexpr int ALL = KT::N + VT::N;
+#pragma unroll
+        for (int j = i * ALL / n; j < (i + 1) * ALL / n; ++j) {
+            if (j < KT::N)
+                kr.load(sk, j);
+            else
+                vr.load(sv, j - KT::N);
+        }
+    };
+    auto load_q = [&](int c) {
         if (MODE == OUT)
-            qr.load(q + (long)c * C * P.q_stride, P.q_stride, cnt, tid);
+            qr.load(q + (long)c * C * P.q_stride, P.q_stride, tokens_of(c), tid);
     };
     // the chunk of step i
     auto chunk = [&](int i) { return MODE == ROWN ? nchunk - 1 - i : i; };
@@ -186,7 +200,8 @@ __device__ __forceinline__ void linear_walk(
         if (nchunk > 1)
             gate(la1, chunk(1));
     }
-    load_chunk(chunk(0));
+    load_kv(chunk(0), 0, 1);
+    load_q(chunk(0));
 
     StateAcc<T, DK, DV> S(w, lane);
     const long sidx = (b * P.H + h) * (long)(DK * DV);
@@ -215,43 +230,57 @@ __device__ __forceinline__ void linear_walk(
         if (MODE == OUT)
             qr.template store<PK>(Qs, tid);
         __syncthreads();
-        if (step + 1 < nchunk)
-            load_chunk(chunk(step + 1));
+        if (MODE != OUT)                // OUT: later, its registers are taken here
+            load_kv(chunk(step + 1), 0, 1);
 
         if (MODE == CHUNKS)
             S.store_frags(static_cast<T *>(P.ws_chunk) +
                               (chunk_slot(b, B.first, c, C) * P.H + h) * (long)(DK * DV),
                           w, lane);
 
-        f32x16 o[OT];
-        if (MODE == OUT) {
+        if (MODE == OUT && w < IT * (IT + 1) / 2) {
             // tiles of P^T on and below the diagonal: lane n has query
             // i = 32 it + n, registers 0-7 and 8-15 eight keys each
-            if (w < IT * (IT + 1) / 2) {
-                const int it = w > 0, jt = w > 1;
-                const int i = 32 * it + n;
-                f32x16 p = zero16();
+            const int it = w > 0, jt = w > 1;
+            const int i = 32 * it + n;
+            f32x16 p = zero16();
+            float d[2][8];
 #pragma unroll
-                for (int s = 0; s < DK / 16; ++s)
-                    mma(p, frag_row(Ks + (32 * jt + cn) * PK + 16 * s + 8 * hf),
-                        frag_row(Qs + i * PK + 16 * s + 8 * hf));
+            for (int u = 0; u < 2; ++u)
+                decay_between<T, C>(dc, dc.hi[i], dc.lo[i], i, 32 * jt + 16 * u + 8 * hf, d[u]);
+            mma_rows<T, DK, 8>(p, Ks + (32 * jt + cn) * PK + 8 * hf, Qs + i * PK + 8 * hf);
 #pragma unroll
-                for (int u = 0; u < 2; ++u) {
-                    const int j = 32 * jt + 16 * u + 8 * hf;
-                    float x[8];
-                    decay_between<T, C>(dc, dc.hi[i], dc.lo[i], i, j, x);
-                    // rounded to the operand type: P feeds one product whose
-                    // result is rounded to the same type (not 0 * p right of
-                    // the diagonal: p may be infinite there)
+            for (int u = 0; u < 2; ++u) {
+                // rounded to the operand type: P feeds one product whose
+                // result is rounded to the same type
+                float x[8];
 #pragma unroll
-                    for (int r = 0; r < 8; ++r)
-                        x[r] = j + r <= i ? p[8 * u + r] * x[r] : 0.f;
-                    lds_st8(Ps + i * PP + j, x);
-                }
+                for (int r = 0; r < 8; ++r)
+                    x[r] = p[8 * u + r] * d[u][r];
+                lds_st8(Ps + i * PP + 32 * jt + 16 * u + 8 * hf, x);
             }
-            // o^T = S^T q^T, scaled to each token; the operands of the next
-            // steps are read and rounded between the MFMAs
-            constexpr int NS = DK / 16;
+        }
+
+        // operands of the state's update, S <- all S + k^T (out (.) v)
+        const float all = dc.all;
+        const float *weight = MODE == ROWN ? dc.in : dc.out;
+        auto rows = [&](int s, int i) {
+            return frag_cols<PK, false>(Ks + 16 * s * PK + 32 * (tw * TK + i), lane);
+        };
+        FragV<T> vf[KS], kf[TK];
+        Split<T, PARTS> split;
+        constexpr int STEPS = 4 * Split<T, PARTS>::PARTS;
+        float wt[8];
+        lds_ld8(weight + 8 * hf, wt);
+#pragma unroll
+        for (int s = 0; s < KS; ++s)
+            vf[s] = frag_cols<PV, true>(Vs + 16 * s * PV + 32 * ct, lane);
+        f32x16 o[OT];
+        if constexpr (MODE == OUT) {
+            // o^T = S^T q^T, scaled to each token.  Between the MFMAs: the
+            // operands of the steps that follow, the state's decay and the first
+            // operands of its update
+            constexpr int NS = DK / 16, U = NS * OT;
             auto read_q = [&](int s, int t) {
                 const int i = 32 * (t * TW + (IT >= TW ? tw : 0)) + n;
                 return SHARED ? frag_row(Qs + i * PK + 16 * s + 8 * hf)
@@ -277,34 +306,49 @@ __device__ __forceinline__ void linear_walk(
             for (int s = 0; s < NS; ++s) {
 #pragma unroll
                 for (int t = 0; t < OT; ++t) {
+                    const int u = s * OT + t;
                     mma(o[t], sf[s & 1], qf[s & 1][t]);
                     if (s + 2 < NS)
                         qf[s & 1][t] = read_q(s + 2, t);
+                    if (!SHARED && t == 0 && s + 1 < NS)
+                        sf[(s + 1) & 1] = read_s(s + 1);
+                    if (SHARED) {       // the state's registers are not read here
+#pragma unroll
+                        for (int e = u * 16 * TK / U; e < (u + 1) * 16 * TK / U; ++e)
+                            S.t[e / 16][e % 16] *= all;
+                    } else if (s % 2) { // tile s / 2 has been read
+#pragma unroll
+                        for (int e = t * 16 / OT; e < (t + 1) * 16 / OT; ++e)
+                            S.t[s / 2][e] *= all;
+                    }
+#pragma unroll
+                    for (int i = u * STEPS / U; i < (u + 1) * STEPS / U; ++i)
+                        split.step(i, vf[0], wt);
+#pragma unroll
+                    for (int i = 0; i < TK; ++i)
+                        if (u == U - TK + i || (U < TK && u == 0))
+                            kf[i] = rows(0, i);
                     __builtin_amdgcn_sched_barrier(0);
                 }
-                if (SHARED) {
-                    if (s + 2 < NS)
-                        sf[s & 1] = read_s(s + 2);
-                } else if (s + 1 < NS) {
-                    sf[(s + 1) & 1] = read_s(s + 1);
-                }
+                if (SHARED && s + 2 < NS)
+                    sf[s & 1] = read_s(s + 2);
             }
 #pragma unroll
             for (int t = 0; t < OT; ++t)
                 o[t] *= dc.in[32 * (t * TW + (IT >= TW ? tw : 0)) + n];
+        } else {
+#pragma unroll
+            for (int i = 0; i < TK; ++i) {
+                kf[i] = rows(0, i);
+                S.t[i] *= all;
+            }
+#pragma unroll
+            for (int i = 0; i < STEPS; ++i)
+                split.step(i, vf[0], wt);
         }
-
-        // the state: S <- all S + k^T (out (.) v)
-        FragV<T> vf[KS];
-#pragma unroll
-        for (int s = 0; s < KS; ++s)
-            vf[s] = frag_cols<PV, true>(Vs + 16 * s * PV + 32 * ct, lane);
-        const float all = dc.all;
-#pragma unroll
-        for (int i = 0; i < TK; ++i)
-            S.t[i] *= all;
-        update_state<T, PARTS>(S.t, vf, MODE == ROWN ? dc.in : dc.out, hf, [&](int s, int i) {
-            return frag_cols<PK, false>(Ks + 16 * s * PK + 32 * (tw * TK + i), lane);
+        update_state<T, PARTS>(S.t, vf, weight, hf, split, kf, rows, [&](int u, int U) {
+            if (MODE == OUT && u < U / 2)
+                load_kv(chunk(step + 1), u, U / 2);
         });
         if (w == GW) {              // the next chunk's decays
             if (step + 1 < nchunk)
@@ -317,21 +361,29 @@ __device__ __forceinline__ void linear_walk(
         __syncthreads();
 
         if (MODE == OUT) {
-            // o^T += v^T P^T
+            load_q(chunk(step + 1));
+            // o^T += v^T P^T (right of the diagonal Ps holds nothing)
+            FragV<T> pf[OT][KS];
+#pragma unroll
+            for (int t = 0; t < OT; ++t) {
+                const int it = t * TW + (IT >= TW ? tw : 0);
+#pragma unroll
+                for (int s = 0; s < KS; ++s)
+                    if (s / 2 <= (TW > 1 ? IT : t))
+                        pf[t][s] = frag_row(Ps + (32 * it + n) * PP + 16 * s + 8 * hf);
+            }
 #pragma unroll
             for (int s = 0; s < KS; ++s)
 #pragma unroll
-                for (int t = 0; t < OT; ++t) {
-                    const int it = t * TW + (IT >= TW ? tw : 0);
-                    if (s / 2 <= it)
-                        mma(o[t], vf[s], frag_row(Ps + (32 * it + n) * PP + 16 * s + 8 * hf));
-                }
+                for (int t = 0; t < OT; ++t)
+                    if (s / 2 <= t * TW + (IT >= TW ? tw : 0))
+                        mma(o[t], vf[s], pf[t][s]);
 #pragma unroll
             for (int t = 0; t < OT; ++t) {
                 const int it = t * TW + tw, i = 32 * it + n;
                 if (it < IT && i < cnt) {
-                    T *dst = static_cast<T *>(P.o) +
-                             ((B.first + (long)c * C + i) * P.H + h) * DV + 32 * ct + 8 * hf;
+                    T *dst = static_cast<T *>(P.o) + ((B.first + (long)c * C) * P.H + h) * DV +
+                             (unsigned)i * (unsigned)(P.H * DV) + (unsigned)(32 * ct + 8 * hf);
 #pragma unroll
                     for (int u = 0; u < 2; ++u) {
                         float x[8];

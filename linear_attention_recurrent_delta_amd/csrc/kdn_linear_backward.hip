@@ -88,7 +88,7 @@ __device__ __forceinline__ void grad_walk(const LinearParams &P, const Block &B,
     auto &xs = L.xs, &ys = L.ys;
     auto &zs = L.zs;
 
-    const int tid = threadIdx.x, lane = tid & (WAVE - 1), w = tid / WAVE;
+    const int tid = threadIdx.x, lane = tid & (WAVE - 1), w = wave_id();
     const int hf = lane >> 5, n = lane & 31, cn = chan(n);
     const int qc = w % KT, qt = w / KT;     // channel and token tile of dq and dk
     const int vc = w % VT, vt = w / VT;     // of dv; and column tile and row group of R
@@ -194,8 +194,6 @@ __device__ __forceinline__ void grad_walk(const LinearParams &P, const Block &B,
         vr.template store<PV>(Vs, tid);
         orr.template store<PV>(Os, tid);
         __syncthreads();
-        if (step + 1 < nchunk)
-            load_chunk(c - 1);
 
         // tiles of P^T and Y^T on and below the diagonal, and of X's sums: lane n
         // has query i = 32 it + n, registers 0-7 and 8-15 eight keys each
@@ -203,14 +201,8 @@ __device__ __forceinline__ void grad_walk(const LinearParams &P, const Block &B,
             const int it = w > 0, jt = w > 1;
             const int i = 32 * it + n;
             f32x16 p = zero16(), y = zero16();
-#pragma unroll
-            for (int s = 0; s < DK / 16; ++s)
-                mma(p, frag_row(Ks + (32 * jt + cn) * PK + 16 * s + 8 * hf),
-                    frag_row(Qs + i * PK + 16 * s + 8 * hf));
-#pragma unroll
-            for (int s = 0; s < DV / 16; ++s)
-                mma(y, frag_row(Vs + (32 * jt + cn) * PV + 16 * s + 8 * hf),
-                    frag_row(Os + i * PV + 16 * s + 8 * hf));
+            mma_rows<T, DK, 4>(p, Ks + (32 * jt + cn) * PK + 8 * hf, Qs + i * PK + 8 * hf);
+            mma_rows<T, DV, 4>(y, Vs + (32 * jt + cn) * PV + 8 * hf, Os + i * PV + 8 * hf);
             float sum = 0.f;
 #pragma unroll
             for (int u = 0; u < 2; ++u) {
@@ -219,9 +211,8 @@ __device__ __forceinline__ void grad_walk(const LinearParams &P, const Block &B,
                 decay_between<T, C>(dc, dc.hi[i], dc.lo[i], i, j, d);
 #pragma unroll
                 for (int r = 0; r < 8; ++r) {
-                    const bool in = j + r <= i;
-                    pf[r] = in ? p[8 * u + r] * d[r] : 0.f;
-                    yf[r] = in ? y[8 * u + r] * d[r] : 0.f;
+                    pf[r] = p[8 * u + r] * d[r];
+                    yf[r] = y[8 * u + r] * d[r];
                     // X without its diagonal, which no log-decay is between
                     x[r] = j + r < i ? pf[r] * y[8 * u + r] : 0.f;
                 }
@@ -307,6 +298,8 @@ __device__ __forceinline__ void grad_walk(const LinearParams &P, const Block &B,
                 gate(la1, c - 2);
         }
         __syncthreads();            // P, Y and the sums
+        if (step + 1 < nchunk)
+            load_chunk(c - 1);
 
         if (w == GW && P.dla) {
             const bool live = lane < C && lane < cnt;
@@ -387,9 +380,20 @@ __device__ __forceinline__ void grad_walk(const LinearParams &P, const Block &B,
             if (vt < IT && s / 2 >= vt)
                 mma(av, of[s], frag_cols<PP, false>(Ps + 16 * s * PP + 32 * vt, lane));
         }
-        update_state<T, PARTS>(R, of, dc.in, hf, [&](int s, int i) {
+        auto rows = [&](int s, int i) {
             return frag_cols<PK, false>(Qs + 16 * s * PK + 32 * (vt * TR + i), lane);
-        });
+        };
+        FragV<T> rq[TR];
+        Split<T, PARTS> split;
+        float wt[8];
+        lds_ld8(dc.in + 8 * hf, wt);
+#pragma unroll
+        for (int i = 0; i < TR; ++i)
+            rq[i] = rows(0, i);
+#pragma unroll
+        for (int i = 0; i < 4 * Split<T, PARTS>::PARTS; ++i)
+            split.step(i, of[0], wt);
+        update_state<T, PARTS>(R, of, dc.in, hf, split, rq, rows, [](int, int) {});
         if (vt < IT && 32 * vt + n < cnt) {
             const long t0 = (long)c * C + 32 * vt + n;
 #pragma unroll

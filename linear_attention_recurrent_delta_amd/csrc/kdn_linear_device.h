@@ -13,6 +13,13 @@ typedef float f32x8 __attribute__((ext_vector_type(8)));
 typedef short s16x4 __attribute__((ext_vector_type(4)));
 typedef __attribute__((address_space(3))) s16x4 lds_s16x4;
 
+// The wave's number as a scalar: what depends on it are branches of the whole
+// wave.  (A vector condition may become an EXEC mask without a branch, which
+// an MFMA under it does not heed.)
+__device__ __forceinline__ int wave_id() {
+    return __builtin_amdgcn_readfirstlane((int)threadIdx.x / WAVE);
+}
+
 // ---------------------------------------------------------------------------
 // The block of a workgroup.
 // ---------------------------------------------------------------------------
@@ -197,26 +204,21 @@ template <int N> struct Split<float, N> {
 
 // acc[i] += sum over the chunk's tokens of a_i (w (.) b): the update of a state.
 // b[s]: the column operand of 16 tokens (s = 0 .. KS - 1), w: the tokens'
-// weights in LDS, rows(s, i): the row operand of tile i.  Between the MFMAs of
-// a step stand the reads and the splitting of the next one, a few
-// instructions behind each MFMA (sched_barrier holds them there: left alone
-// the compiler reads, waits, splits and multiplies one after the other, and
-// two waves a SIMD cannot hide that).
-template <typename T, int PARTS, int N, int KS, typename Rows>
+// weights in LDS, rows(s, i): the row operand of tile i.  cur and a come with
+// the operands of the first step.  Between the MFMAs of a step stand the reads
+// and the splitting of the next one and extra(u), u = 0 .. U - 1 the MFMA's
+// number (the next chunk's loads), a few instructions behind each MFMA
+// (sched_barrier holds them there: left alone the compiler reads, waits,
+// splits and multiplies one after the other, and two waves a SIMD cannot hide
+// that).
+template <typename T, int PARTS, int N, int KS, typename Rows, typename Extra>
 __device__ __forceinline__ void update_state(f32x16 (&acc)[N], const FragV<T> (&b)[KS],
-                                             const float *w, int hf, Rows rows) {
+                                             const float *w, int hf, Split<T, PARTS> &cur,
+                                             FragV<T> (&a)[N], Rows rows, Extra extra) {
     typedef Split<T, PARTS> S;
     constexpr int M = S::PARTS * N, STEPS = 4 * S::PARTS;    // of 16 tokens
-    S cur, nxt;
-    FragV<T> a[N];
+    S nxt;
     float wt[8];
-    lds_ld8(w + 8 * hf, wt);
-#pragma unroll
-    for (int i = 0; i < N; ++i)
-        a[i] = rows(0, i);
-#pragma unroll
-    for (int i = 0; i < STEPS; ++i)
-        cur.step(i, b[0], wt);
 #pragma unroll
     for (int s = 0; s < KS; ++s) {
         const bool more = s + 1 < KS;
@@ -232,10 +234,32 @@ __device__ __forceinline__ void update_state(f32x16 (&acc)[N], const FragV<T> (&
                 for (int i = m * STEPS / M; i < (m + 1) * STEPS / M; ++i)
                     nxt.step(i, b[s + 1], wt);
             }
+            extra(s * M + m, KS * M);
             __builtin_amdgcn_sched_barrier(0);
         }
         if (more)
             cur = nxt;
+    }
+}
+
+// sum over D channels of a tile's rows: acc += A B^T, the rows of lane n at a
+// and b (8 h on).  The operands of STEPS steps are read before the first of
+// their products, so that their latency is paid once.
+template <typename T, int D, int STEPS>
+__device__ __forceinline__ void mma_rows(f32x16 &acc, const T *a, const T *b) {
+    constexpr int G = sizeof(T) == 4 ? 2 : (STEPS < D / 16 ? STEPS : D / 16);
+#pragma unroll
+    for (int s0 = 0; s0 < D / 16; s0 += G) {
+        FragV<T> x[G], y[G];
+#pragma unroll
+        for (int s = 0; s < G; ++s) {
+            x[s] = frag_row(a + 16 * (s0 + s));
+            y[s] = frag_row(b + 16 * (s0 + s));
+        }
+        __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+        for (int s = 0; s < G; ++s)
+            mma(acc, x[s], y[s]);
     }
 }
 
@@ -263,18 +287,30 @@ __device__ __forceinline__ double log2_decay(float la) {
     return g < RESET2 ? (double)RESET2 : (double)la * 1.4426950408889634074;
 }
 
+// x + (x of the lane CTRL names, 0 where there is none or the row is not in
+// ROWS), in 64 bits by moves of the halves within the registers.
+template <int CTRL, int ROWS> __device__ __forceinline__ double add_dpp(double x) {
+    const uint64_t b = __builtin_bit_cast(uint64_t, x);
+    const uint32_t lo = __builtin_amdgcn_update_dpp(0, (int)(uint32_t)b, CTRL, ROWS, 0xf, false);
+    const uint32_t hi = __builtin_amdgcn_update_dpp(0, (int)(uint32_t)(b >> 32), CTRL, ROWS, 0xf, false);
+    return x + __builtin_bit_cast(double, (uint64_t)hi << 32 | lo);
+}
+
 // One wave: lane j < C holds the log-decay (natural) of token j, 0 behind the
 // end.  Returns the base-2 prefix sum of the chunk.
 template <int C>
 __device__ __forceinline__ double chunk_decays(Decays<C> &D, float la, int lane) {
     double x = log2_decay(la);
-#pragma unroll
-    for (int off = 1; off < C; off <<= 1) {
-        const double y = __shfl_up(x, off, WAVE);
-        if (lane >= off)
-            x += y;
-    }
-    const double all = __shfl(x, C - 1, WAVE);
+    x = add_dpp<0x111, 0xf>(x);      // the lane before, 2, 4 and 8 before (rows of 16)
+    x = add_dpp<0x112, 0xf>(x);
+    x = add_dpp<0x114, 0xf>(x);
+    x = add_dpp<0x118, 0xf>(x);
+    x = add_dpp<0x142, 0xa>(x);      // the end of the row before, to rows 1 and 3
+    x = add_dpp<0x143, 0xc>(x);      // lane 31, to rows 2 and 3
+    const double all = __builtin_bit_cast(
+        double, (uint64_t)(uint32_t)__builtin_amdgcn_readlane(
+                    (int)(__builtin_bit_cast(uint64_t, x) >> 32), C - 1) << 32 |
+                    (uint32_t)__builtin_amdgcn_readlane((int)__builtin_bit_cast(uint64_t, x), C - 1));
     if (lane < C) {
         const float hi = (float)x;
         D.hi[lane] = hi;
@@ -370,15 +406,25 @@ template <typename T, int ROWS, int COLS, int NT> struct TileRegs {
     f32x4 r[N];
 
     // base: the tile's first row (element pointer), stride in elements
+    struct Source {
+        __amdgpu_buffer_rsrc_t d;
+        unsigned at, pitch;
+        __device__ __forceinline__ Source(const T *base, long stride, int count, int tid) {
+            pitch = (unsigned)stride * sizeof(T);
+            const int rows = min(count, ROWS);
+            d = buf_rsrc(base, rows > 0 ? (rows - 1) * pitch + COLS * sizeof(T) : 0u);
+            at = (tid / PER_ROW) * pitch + (tid % PER_ROW) * 16;
+        }
+    };
+    __device__ __forceinline__ void load(const Source &s, int i) {
+        r[i] = __builtin_bit_cast(f32x4, __builtin_amdgcn_raw_buffer_load_b128(
+                                             s.d, (int)(s.at + i * STEP * s.pitch), 0, 0));
+    }
     __device__ __forceinline__ void load(const T *base, long stride, int count, int tid) {
-        const unsigned pitch = (unsigned)stride * sizeof(T);
-        const int rows = min(count, ROWS);
-        const auto d = buf_rsrc(base, rows > 0 ? (rows - 1) * pitch + COLS * sizeof(T) : 0u);
-        const unsigned at = (tid / PER_ROW) * pitch + (tid % PER_ROW) * 16;
+        const Source s(base, stride, count, tid);
 #pragma unroll
         for (int i = 0; i < N; ++i)
-            r[i] = __builtin_bit_cast(f32x4, __builtin_amdgcn_raw_buffer_load_b128(
-                                                 d, (int)(at + i * STEP * pitch), 0, 0));
+            load(s, i);
     }
     template <int PITCH> __device__ __forceinline__ void store(T *lds, int tid) const {
         const int row = tid / PER_ROW, c = (tid % PER_ROW) * VEC;
