@@ -135,13 +135,19 @@ int kdn_sequence_max_blocks(int N, int tokens, int block) {
 int kdn_linear_block(int tokens, int N, int H) {
     if (tokens < 0 || N < 0 || H < 0)
         return -1;
-    // two workgroups for each of the 256 CUs, all at once, and blocks long
-    // enough that the state of a block (read twice, written twice) is small
-    // beside its tokens
-    const long long want = ((long long)tokens * H + 511) / 512;
-    long long block = (want + 63) / 64 * 64;
-    if (block < 256)
-        block = 256;
+    // Two workgroups for each of the 256 CUs, all at once.  Below that the
+    // longest chain counts: the chunks of a block twice (its own state and its
+    // outputs, 3.5 us a chunk of 64 each) and the join over the sequence's blocks
+    // (1.5 us for 8), least at a block of about sqrt(2 tokens); up to 256 tokens
+    // one block is as quick as three launches.
+    const long long full = ((long long)tokens * H + 511) / 512;
+    const long long len = N > 0 ? tokens / N : 0;
+    long long chain = 64;
+    while (chain * chain < 2 * len)
+        chain += 64;
+    if (len <= 256)
+        chain = 256;
+    const long long block = ((full > chain ? full : chain) + 63) / 64 * 64;
     return (int)(block > (1 << 30) ? (1 << 30) : block);
 }
 

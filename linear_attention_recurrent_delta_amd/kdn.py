@@ -458,25 +458,37 @@ class SequenceTables:
     positions: torch.Tensor | None       # [tokens] position of each token
 
 
-def _on(x, stream):
-    """(device to make current or None, stream pointer) for a call on x."""
-    dev = x.device
+# the current stream's handle without a Stream object around it, where torch
+# has it
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+    lambda index: torch.cuda.current_stream(index).cuda_stream)
+
+
+def _call(fn, dev, stream, *args):
+    """Call fn(*args, stream) with the tensors' device current.  These calls
+    are short on the GPU too, so their checks take the quickest way that says
+    yes and leave the words to the slow one."""
     if dev.type != "cuda":
         raise ValueError(f"kdn: tensors must be in GPU memory, not on {dev}")
-    other = dev if dev.index != torch.cuda.current_device() else None
     if stream is None:
-        return other, torch.cuda.current_stream(dev).cuda_stream
-    return other, _stream(stream)
-
-
-def _call(fn, args, other):
-    if other is None:
-        st = fn(*args)
+        stream = _raw_stream(dev.index)
+    elif not isinstance(stream, int):
+        stream = stream.cuda_stream
+    if dev.index == torch.cuda.current_device():
+        st = fn(*args, stream)
     else:
-        with torch.cuda.device(other):
-            st = fn(*args)
+        with torch.cuda.device(dev):
+            st = fn(*args, stream)
     if st != 0:
         _check(_lib, st)
+
+
+def _same(name, x, shape, dtype, dev):
+    """x is None or a contiguous GPU tensor of this shape, dtype and device."""
+    if x is None or (isinstance(x, torch.Tensor) and x.shape == shape and x.dtype is dtype
+                     and x.is_cuda and x.device == dev and x.is_contiguous()):
+        return
+    _expect([(name, x, shape, dtype)], dev)
 
 
 def _new(shape, dtype, dev, stream, zero=False):
@@ -504,7 +516,10 @@ def _rows(name, x, lead, dtype, dev):
     of wider ones; returns the elements between tokens."""
     if not isinstance(x, torch.Tensor):
         raise TypeError(f"kdn: {name} must be a tensor")
-    n = len(lead)
+    n, shape = len(lead), x.shape
+    if len(shape) == n + 2 and shape[:n] == lead and x.dtype is dtype and x.device == dev \
+            and x.is_contiguous():
+        return shape[n] * shape[n + 1]
     if x.dim() != n + 2 or tuple(x.shape[:n]) != lead:
         raise ValueError(f"kdn: {name} has shape {tuple(x.shape)}, expected "
                          f"{lead + ('heads', 'd')}")
@@ -513,8 +528,6 @@ def _rows(name, x, lead, dtype, dev):
     if x.device != dev:
         raise ValueError(f"kdn: {name} is on {x.device}, the other tensors on {dev}")
     heads, d = x.shape[n:]
-    if x.is_contiguous():
-        return heads * d
     st = x.stride()
     row = st[n - 1]
     if st[-1] != 1 or (heads > 1 and st[-2] != d) or row < heads * d or \
@@ -531,7 +544,7 @@ def _gate(log_alpha, lead, H, dtype, dev):
         want, dt, gate = (H,), torch.float32, GATE_HEAD
     else:
         want, dt, gate = lead + (H,), dtype, GATE_TOKEN
-    _expect([("log_alpha", log_alpha, want, dt)], dev)
+    _same("log_alpha", log_alpha, want, dt, dev)
     return gate
 
 
@@ -539,10 +552,13 @@ def _linear_heads(q, k, v, log_alpha):
     """States per token: the largest head count of q, k, v and log_alpha."""
     if not isinstance(log_alpha, torch.Tensor) or log_alpha.dim() == 0:
         raise TypeError("kdn: log_alpha must be a tensor [.., H]")
-    H = max(q.shape[-2], k.shape[-2], v.shape[-2], log_alpha.shape[-1])
-    for name, x in (("q", q), ("k", k), ("v", v)):
-        if x.shape[-2] == 0 or H % x.shape[-2]:
-            raise ValueError(f"kdn: the {x.shape[-2]} heads of {name} do not divide {H}")
+    a, b, c, H = q.shape[-2], k.shape[-2], v.shape[-2], log_alpha.shape[-1]
+    if a == b == c == H:
+        return H
+    H = max(a, b, c, H)
+    for name, n in (("q", a), ("k", b), ("v", c)):
+        if n == 0 or H % n:
+            raise ValueError(f"kdn: the {n} heads of {name} do not divide {H}")
     return H
 
 
@@ -573,21 +589,27 @@ def sequence_tables(lengths, tokens, block, slots=None, context=None, maps=False
     if rows < 0:
         raise KdnError(2, f"tokens {tokens} must not be negative, block {block} a positive "
                           "multiple of 64")
-    other, st = _on(lengths, stream)
+    _same("lengths", lengths, (N,), i32, dev)
+    _same("slots", slots, (N,), i32, dev)
+    _same("context", context, (N,), i32, dev)
     if out is None:
-        new = lambda *shape: _new(shape, i32, dev, stream)
-        out = SequenceTables(tokens, block, new(N + 1), new(N + 1), new(rows, 4), slots,
-                             new(tokens) if maps else None, new(tokens) if maps else None)
+        # one piece of memory, the blocks (16-byte rows) first
+        n = tokens if maps else 0
+        parts = _new((4 * rows + 2 * (N + 1) + 2 * n,), i32, dev, stream).split_with_sizes(
+            [4 * rows, N + 1, N + 1, n, n])
+        out = SequenceTables(tokens, block, parts[1], parts[2], parts[0].view(rows, 4), slots,
+                             parts[3] if maps else None, parts[4] if maps else None)
     else:
         out.tokens, out.block, out.slots = tokens, block, slots
-    _expect([("lengths", lengths, (N,), i32), ("slots", slots, (N,), i32),
-             ("context", context, (N,), i32), ("offsets", out.offsets, (N + 1,), i32),
-             ("block_offsets", out.block_offsets, (N + 1,), i32),
-             ("blocks", out.blocks, (rows, 4), i32), ("slot_map", out.slot_map, (tokens,), i32),
-             ("positions", out.positions, (tokens,), i32)], dev)
-    _call(lib.kdn_sequence_tables,
-          (N, tokens, block, rows, _p(lengths), _p(slots), _p(context), _p(out.offsets),
-           _p(out.block_offsets), _p(out.blocks), _p(out.slot_map), _p(out.positions), st), other)
+        for name, x, shape in (("offsets", out.offsets, (N + 1,)),
+                               ("block_offsets", out.block_offsets, (N + 1,)),
+                               ("blocks", out.blocks, (rows, 4)),
+                               ("slot_map", out.slot_map, (tokens,)),
+                               ("positions", out.positions, (tokens,))):
+            _same(name, x, shape, i32, dev)
+    _call(lib.kdn_sequence_tables, dev, stream, N, tokens, block, rows, _p(lengths), _p(slots),
+          _p(context), _p(out.offsets), _p(out.block_offsets), _p(out.blocks), _p(out.slot_map),
+          _p(out.positions))
     return out
 
 
@@ -596,9 +618,10 @@ def _packed(tables, pool, dev):
     pool (None) the states are by sequence and the slots are not looked at."""
     N, i32 = tables.offsets.shape[0] - 1, torch.int32
     rows = load().kdn_sequence_max_blocks(N, tables.tokens, tables.block)
-    _expect([("offsets", tables.offsets, (N + 1,), i32),
-             ("block_offsets", tables.block_offsets, (N + 1,), i32),
-             ("blocks", tables.blocks, (rows, 4), i32), ("slots", tables.slots, (N,), i32)], dev)
+    _same("offsets", tables.offsets, (N + 1,), i32, dev)
+    _same("block_offsets", tables.block_offsets, (N + 1,), i32, dev)
+    _same("blocks", tables.blocks, (rows, 4), i32, dev)
+    _same("slots", tables.slots, (N,), i32, dev)
     return Packed(tables.tokens, tables.block, rows, N if pool is None else pool,
                   _p(tables.blocks), _p(tables.block_offsets),
                   None if pool is None else _p(tables.slots)), N
@@ -664,29 +687,36 @@ def linear_prefill(q, k, v, log_alpha, S0=None, tables=None, out=None, workspace
             S = _new((pool, H, dk, dv), f32, dev, stream)
     else:
         o, S = out
-    _expect([("k", k, lead + (k.shape[-2], dk), dt)] if k.shape[-1] != dk else [], dev)
-    _expect([("S0", S0, (pool, H, dk, dv), f32), ("o", o, lead + (H, dv), dt),
-             ("S_out", S, (pool, H, dk, dv), f32)], dev)
+    if k.shape[-1] != dk:
+        _same("k", k, lead + (k.shape[-2], dk), dt, dev)
+    s_shape = (pool, H, dk, dv)
+    _same("S0", S0, s_shape, f32, dev)
+    _same("o", o, lead + (H, dv), dt, dev)
+    _same("S_out", S, s_shape, f32, dev)
     if isinstance(workspace, str):
         if workspace != "auto":
             raise ValueError(f"kdn: workspace must be 'auto', None or a tensor, not {workspace!r}")
-        workspace = linear_workspace(q, k, v, log_alpha, tables, stream)
+        workspace = _linear_workspace(DTYPES[dt], N, T, H, dk, dv, pk, dev, stream)
     nws = 0
     if workspace is not None:
-        _expect([("workspace", workspace, (workspace.numel(),), torch.uint8)], dev)
         nws = workspace.numel()
-    other, st = _on(q, stream)
-    _call(lib.kdn_linear_prefill,
-          (DTYPES[dt], N, T, H, q.shape[-2], k.shape[-2], v.shape[-2], dk, dv, gate, qs, ks, vs,
-           _p(q), _p(k), _p(v), _p(log_alpha), _p(S0), _p(o), _p(S), pk, _p(workspace), nws, st),
-          other)
+        _same("workspace", workspace, (nws,), torch.uint8, dev)
+    _call(lib.kdn_linear_prefill, dev, stream, DTYPES[dt], N, T, H, q.shape[-2], k.shape[-2],
+          v.shape[-2], dk, dv, gate, qs, ks, vs, _p(q), _p(k), _p(v), _p(log_alpha), _p(S0),
+          _p(o), _p(S), pk, _p(workspace), nws)
     return o, S
+
+
+def _linear_workspace(dtype, N, T, H, dk, dv, pk, dev, stream):
+    st = ctypes.c_int(0)
+    n = load().kdn_linear_prefill_workspace_size(dtype, N, T, H, dk, dv, pk, ctypes.byref(st))
+    _check(_lib, st.value)
+    return _new((n,), torch.uint8, dev, stream) if n else None
 
 
 def linear_workspace(q, k, v, log_alpha, tables=None, stream=None):
     """A workspace tensor (uint8) for :func:`linear_prefill` of these inputs,
     None if none is needed.  Calls that share one must not overlap in time."""
-    lib = load()
     H = _linear_heads(q, k, v, log_alpha)
     pk = None
     if tables is None:
@@ -694,11 +724,8 @@ def linear_workspace(q, k, v, log_alpha, tables=None, stream=None):
     else:
         T = 0
         pk, N = _packed(tables, 0, q.device)
-    st = ctypes.c_int(0)
-    n = lib.kdn_linear_prefill_workspace_size(DTYPES[q.dtype], N, T, H, q.shape[-1], v.shape[-1],
-                                              pk, ctypes.byref(st))
-    _check(lib, st.value)
-    return _new((n,), torch.uint8, q.device, stream) if n else None
+    return _linear_workspace(DTYPES[q.dtype], N, T, H, q.shape[-1], v.shape[-1], pk, q.device,
+                             stream)
 
 
 def linear_decode(q, k, v, log_alpha, S, slots=None, o=None, stream=None):
@@ -723,13 +750,14 @@ def linear_decode(q, k, v, log_alpha, S, slots=None, o=None, stream=None):
     pool = S.shape[0]
     if o is None:
         o = _new((N, H, dv), dt, dev, stream, zero=slots is not None)
-    _expect([("k", k, (N, k.shape[-2], dk), dt)] if k.shape[-1] != dk else [], dev)
-    _expect([("S", S, (pool, H, dk, dv), torch.float32), ("o", o, (N, H, dv), dt),
-             ("slots", slots, (N,), torch.int32)], dev)
-    other, st = _on(q, stream)
-    _call(lib.kdn_linear_decode,
-          (DTYPES[dt], N, H, q.shape[-2], k.shape[-2], v.shape[-2], dk, dv, gate, qs, ks, vs,
-           _p(q), _p(k), _p(v), _p(log_alpha), _p(slots), pool, _p(S), _p(o), st), other)
+    if k.shape[-1] != dk:
+        _same("k", k, (N, k.shape[-2], dk), dt, dev)
+    _same("S", S, (pool, H, dk, dv), torch.float32, dev)
+    _same("o", o, (N, H, dv), dt, dev)
+    _same("slots", slots, (N,), torch.int32, dev)
+    _call(lib.kdn_linear_decode, dev, stream, DTYPES[dt], N, H, q.shape[-2], k.shape[-2],
+          v.shape[-2], dk, dv, gate, qs, ks, vs, _p(q), _p(k), _p(v), _p(log_alpha), _p(slots),
+          pool, _p(S), _p(o))
     return o
 
 
@@ -770,12 +798,15 @@ def linear_prefill_backward(q, k, v, d_o, log_alpha, S0=None, dS_out=None, table
         out = dict(dq=new(*lead, Hq, dk), dk=new(*lead, Hk, dk), dv=new(*lead, Hv, dv),
                    dlog_alpha=new(*la_shape),
                    dS0=_new(s_shape, f32, dev, stream, zero=tables is not None))
-    _expect([("k", k, lead + (Hk, dk), dt)] if k.shape[-1] != dk else [], dev)
-    _expect([("d_o", d_o, lead + (H, dv), dt), ("S0", S0, s_shape, f32),
-             ("dS_out", dS_out, s_shape, f32), ("dq", out["dq"], lead + (Hq, dk), dt),
-             ("dk", out["dk"], lead + (Hk, dk), dt), ("dv", out["dv"], lead + (Hv, dv), dt),
-             ("dlog_alpha", out["dlog_alpha"], la_shape, dt), ("dS0", out["dS0"], s_shape, f32)],
-            dev)
+    if k.shape[-1] != dk:
+        _same("k", k, lead + (Hk, dk), dt, dev)
+    for name, x, shape, t in (("d_o", d_o, lead + (H, dv), dt), ("S0", S0, s_shape, f32),
+                              ("dS_out", dS_out, s_shape, f32), ("dq", out["dq"], lead + (Hq, dk), dt),
+                              ("dk", out["dk"], lead + (Hk, dk), dt),
+                              ("dv", out["dv"], lead + (Hv, dv), dt),
+                              ("dlog_alpha", out["dlog_alpha"], la_shape, dt),
+                              ("dS0", out["dS0"], s_shape, f32)):
+        _same(name, x, shape, t, dev)
     if workspace is None:
         st = ctypes.c_int(0)
         n = lib.kdn_linear_prefill_backward_workspace_size(
@@ -784,11 +815,10 @@ def linear_prefill_backward(q, k, v, d_o, log_alpha, S0=None, dS_out=None, table
         workspace = _new((n,), torch.uint8, dev, stream) if n else None
     nws = 0
     if workspace is not None:
-        _expect([("workspace", workspace, (workspace.numel(),), torch.uint8)], dev)
         nws = workspace.numel()
-    other, st = _on(q, stream)
-    _call(lib.kdn_linear_prefill_backward,
-          (DTYPES[dt], N, T, H, Hq, Hk, Hv, dk, dv, gate, qs, ks, vs, _p(q), _p(k), _p(v),
-           _p(log_alpha), _p(S0), _p(d_o), _p(dS_out), _p(out["dq"]), _p(out["dk"]),
-           _p(out["dv"]), _p(out["dlog_alpha"]), _p(out["dS0"]), pk, _p(workspace), nws, st), other)
+        _same("workspace", workspace, (nws,), torch.uint8, dev)
+    _call(lib.kdn_linear_prefill_backward, dev, stream, DTYPES[dt], N, T, H, Hq, Hk, Hv, dk, dv,
+          gate, qs, ks, vs, _p(q), _p(k), _p(v), _p(log_alpha), _p(S0), _p(d_o), _p(dS_out),
+          _p(out["dq"]), _p(out["dk"]), _p(out["dv"]), _p(out["dlog_alpha"]), _p(out["dS0"]), pk,
+          _p(workspace), nws)
     return out
