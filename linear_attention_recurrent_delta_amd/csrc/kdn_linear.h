@@ -89,11 +89,10 @@ hipError_t launch_linear_decode(const LinearDecodeParams &P, hipStream_t stream)
 hipError_t launch_linear_backward(const LinearParams &P, hipStream_t stream);
 hipError_t launch_sequence_tables(const TableParams &P, hipStream_t stream);
 
-// Passes shared by the prefill and its gradients (kdn_linear.hip): the blocks'
-// own contributions and their join along each sequence, forward (ws_state) and
-// reverse (ws_rstate), and the state at every chunk's start (ws_chunk).
-hipError_t launch_linear_states(const LinearParams &P, hipStream_t stream);
-hipError_t launch_linear_reverse_states(const LinearParams &P, hipStream_t stream);
+// Passes of the gradient call that are walks of the prefill's kind
+// (kdn_linear.hip): the blocks' own contributions to the states of both
+// recurrences (ws_state, ws_rstate), and the state at every chunk's start.
+hipError_t launch_linear_own(const LinearParams &P, hipStream_t stream);
 hipError_t launch_linear_chunk_states(const LinearParams &P, hipStream_t stream);
 
 }  // namespace kdn

@@ -407,134 +407,80 @@ __device__ __forceinline__ void linear_walk(
         S.store(P.S_out + (B.slot * P.H + h) * (long)(DK * DV));
 }
 
-template <typename T, int DK, int DV, int MODE>
-__global__ __launch_bounds__(NT, 2) void linear_kernel(LinearParams P) {
-    const long b = blockIdx.x / P.H;
-    const int h = blockIdx.x % P.H;
+// One (block, head) of a mode.  Three parts for a state that is returned and
+// for what goes into one: the last block's in the prefill and the blocks' own
+// (the forward ones of the gradient call excepted, which are only read rounded).
+template <typename T, int DK, int DV, int MODE, bool GRAD>
+__device__ __forceinline__ void linear_block_head(
+    const LinearParams &P, long id, typename Shape<T, DK, DV>::template Lds<MODE> &L) {
+    const long b = id / P.H;
+    const int h = id % P.H;
     const Block B = get_block(P, b);
     if (B.count == 0 || B.slot < 0 || (MODE == OWN && B.last) || (MODE == ROWN && B.index == 0))
         return;
-    __shared__ typename Shape<T, DK, DV>::template Lds<MODE> L;
-    // three parts for a state that is returned and for what goes into one: the
-    // last block's in the prefill, the blocks' own (the forward ones of the
-    // gradient call, which only reads them rounded, excepted)
-    if constexpr (MODE == CHUNKS) {
-        linear_walk<T, DK, DV, MODE, 2>(P, B, b, h, L);
-    } else if constexpr (MODE == ROWN) {
+    if (MODE == OUT ? B.last : MODE == ROWN || (MODE == OWN && !GRAD))
         linear_walk<T, DK, DV, MODE, 3>(P, B, b, h, L);
-    } else {
-        if (MODE == OWN ? P.d_o == nullptr : B.last)
-            linear_walk<T, DK, DV, MODE, 3>(P, B, b, h, L);
-        else
-            linear_walk<T, DK, DV, MODE, 2>(P, B, b, h, L);
-    }
+    else if (MODE == OUT || MODE == CHUNKS || GRAD)
+        linear_walk<T, DK, DV, MODE, 2>(P, B, b, h, L);
 }
 
-// ---------------------------------------------------------------------------
-// Join of the blocks along each sequence: block b's own contribution U_b in
-// ws_state becomes the state at its start (REV: in ws_rstate, the reverse
-// state behind its end, blocks last to first).  One thread holds 4 values of S
-// of one (sequence, head); the blocks' values are loaded JOIN ahead.  A
-// sequence of one block has nothing to join, one without tokens passes its
-// state on.
-// ---------------------------------------------------------------------------
-constexpr int JOIN = 8;
-
-template <bool REV>
-__global__ __launch_bounds__(NT) void linear_join_kernel(LinearParams P, int pieces) {
-    const long id = blockIdx.x;
-    const int piece = id % pieces;
-    const int h = (id / pieces) % P.H;
-    const int seq = id / ((long)pieces * P.H);
-    const int e = (piece * NT + threadIdx.x) * 4;
-    const long size = (long)P.dk * P.dv;
-    long b0 = (long)seq * P.nblocks, b1 = b0 + P.nblocks, slot = seq;
-    if (P.block_offsets) {
-        b0 = P.block_offsets[seq];
-        b1 = P.block_offsets[seq + 1];
-        slot = P.slots ? P.slots[seq] : seq;
-        if (b0 < 0 || b1 > P.nblocks || slot < 0 || slot >= P.pool)
-            return;
-    }
-    const long nb = b1 - b0;
-    if (nb == 1)
-        return;
-    const float *first = REV ? P.dS_out : P.S0;
-    float *pass = REV ? P.dS0 : P.S_out;
-    float *ws = REV ? P.ws_rstate : P.ws_state;
-    const float *decay = REV ? P.ws_rdecay : P.ws_decay;
-    const long at = (slot * P.H + h) * size + e;
-    f32x4 s = {0.f, 0.f, 0.f, 0.f};
-    if (first)
-        s = *reinterpret_cast<const f32x4 *>(first + at);
-    if (nb <= 0) {
-        if (pass && pass != first)
-            *reinterpret_cast<f32x4 *>(pass + at) = s;
-        return;
-    }
-    auto block = [&](long i) { return (REV ? b1 - 1 - i : b0 + i) * P.H + h; };
-    for (long j = 0; j < nb; j += JOIN) {
-        f32x4 u[JOIN];
-        float a[JOIN];
-#pragma unroll
-        for (int i = 0; i < JOIN; ++i)
-            if (j + i < nb - 1) {
-                u[i] = *reinterpret_cast<const f32x4 *>(ws + block(j + i) * size + e);
-                a[i] = decay[block(j + i)];
-            }
-#pragma unroll
-        for (int i = 0; i < JOIN; ++i)
-            if (j + i < nb) {
-                *reinterpret_cast<f32x4 *>(ws + block(j + i) * size + e) = s;
-                if (j + i < nb - 1)
-                    s = s * a[i] + u[i];
-            }
-    }
+template <typename T, int DK, int DV, int MODE>
+__global__ __launch_bounds__(NT, 2) void linear_kernel(LinearParams P) {
+    __shared__ typename Shape<T, DK, DV>::template Lds<MODE> L;
+    linear_block_head<T, DK, DV, MODE, false>(P, blockIdx.x, L);
 }
+
+// The blocks' own contributions to both recurrences of the gradient call, in
+// one launch: forward ones in the even workgroups, reverse ones in the odd.
+template <typename T, int DK, int DV>
+__global__ __launch_bounds__(NT, 2) void linear_own_kernel(LinearParams P) {
+    __shared__ union U {
+        typename Shape<T, DK, DV>::template Lds<OWN> f;
+        typename Shape<T, DK, DV>::template Lds<ROWN> r;
+    } L;
+    if (blockIdx.x & 1)
+        linear_block_head<T, DK, DV, ROWN, true>(P, blockIdx.x >> 1, L.r);
+    else
+        linear_block_head<T, DK, DV, OWN, true>(P, blockIdx.x >> 1, L.f);
+}
+
+__global__ __launch_bounds__(JOIN_NT) void linear_join_kernel(LinearParams P, int pieces) {
+    join_blocks<false>(P, blockIdx.x, pieces);
+}
+
+#define KDN_LINEAR_SIZES(rows, cols, CASE)         \
+    if (rows == 64 && cols == 64) { CASE(64, 64) } \
+    if (rows == 64 && cols == 128) { CASE(64, 128) } \
+    if (rows == 128 && cols == 64) { CASE(128, 64) } \
+    if (rows == 128 && cols == 128) { CASE(128, 128) }
 
 template <typename T, int MODE>
 static hipError_t launch_mode(const LinearParams &P, hipStream_t st) {
     const dim3 grid((unsigned)(linear_total_blocks(P) * P.H)), block(NT);
     // rows and columns of the state the mode works on
     const int rows = MODE == CHUNKS ? P.dv : P.dk, cols = MODE == CHUNKS ? P.dk : P.dv;
-#define KDN_LIN(DK_, DV_)                                                              \
-    if (rows == DK_ && cols == DV_) {                                                  \
-        hipLaunchKernelGGL((linear_kernel<T, DK_, DV_, MODE>), grid, block, 0, st, P); \
-        return hipGetLastError();                                                      \
-    }
-    KDN_LIN(64, 64)
-    KDN_LIN(64, 128)
-    KDN_LIN(128, 64)
-    KDN_LIN(128, 128)
-#undef KDN_LIN
+#define KDN_CASE(DK_, DV_)                                                         \
+    hipLaunchKernelGGL((linear_kernel<T, DK_, DV_, MODE>), grid, block, 0, st, P); \
+    return hipGetLastError();
+    KDN_LINEAR_SIZES(rows, cols, KDN_CASE)
+#undef KDN_CASE
     return hipErrorInvalidValue;
 }
 
-// The blocks' own contributions and their join, where a sequence may have more
-// than one block; the join also passes on the states of empty sequences.
-template <bool REV> static hipError_t launch_states(const LinearParams &P, hipStream_t st) {
-    constexpr int MODE = REV ? ROWN : OWN;
-    hipError_t e = hipSuccess;
-    if (!P.block_offsets && P.nblocks == 1)
-        return e;
-    if (linear_total_blocks(P) > 0)
-        e = P.bf16 ? launch_mode<bf16, MODE>(P, st) : launch_mode<float, MODE>(P, st);
-    if (e != hipSuccess)
-        return e;
-    const int pieces = P.dk * P.dv / (4 * NT);
-    const dim3 grid((unsigned)((long)P.N * P.H * pieces)), block(NT);
-    hipLaunchKernelGGL((linear_join_kernel<REV>), grid, block, 0, st, P, pieces);
+template <typename T> static hipError_t launch_own(const LinearParams &P, hipStream_t st) {
+    const dim3 grid((unsigned)(linear_total_blocks(P) * P.H * 2)), block(NT);
+#define KDN_CASE(DK_, DV_)                                                       \
+    hipLaunchKernelGGL((linear_own_kernel<T, DK_, DV_>), grid, block, 0, st, P); \
     return hipGetLastError();
+    KDN_LINEAR_SIZES(P.dk, P.dv, KDN_CASE)
+#undef KDN_CASE
+    return hipErrorInvalidValue;
 }
 
 }  // namespace lin
 
-hipError_t launch_linear_states(const LinearParams &P, hipStream_t st) {
-    return lin::launch_states<false>(P, st);
-}
-
-hipError_t launch_linear_reverse_states(const LinearParams &P, hipStream_t st) {
-    return lin::launch_states<true>(P, st);
+hipError_t launch_linear_own(const LinearParams &P, hipStream_t st) {
+    return P.bf16 ? lin::launch_own<bf16>(P, st) : lin::launch_own<float>(P, st);
 }
 
 hipError_t launch_linear_chunk_states(const LinearParams &P, hipStream_t st) {
@@ -545,8 +491,22 @@ hipError_t launch_linear_chunk_states(const LinearParams &P, hipStream_t st) {
 hipError_t launch_linear_prefill(const LinearParams &P, hipStream_t st) {
     if (P.N == 0 || P.H == 0)
         return hipSuccess;
-    const hipError_t e = launch_linear_states(P, st);
-    if (e != hipSuccess || linear_total_blocks(P) == 0)
+    const bool any = linear_total_blocks(P) > 0;
+    hipError_t e = hipSuccess;
+    if (P.block_offsets || P.nblocks != 1) {
+        // the blocks' own contributions and their join, where a sequence may
+        // have more than one; the join also passes on the states of empty ones
+        if (any)
+            e = P.bf16 ? lin::launch_mode<bf16, lin::OWN>(P, st)
+                       : lin::launch_mode<float, lin::OWN>(P, st);
+        if (e == hipSuccess) {
+            const int pieces = P.dk * P.dv / (4 * lin::JOIN_NT);
+            hipLaunchKernelGGL(lin::linear_join_kernel, dim3((unsigned)((long)P.N * P.H * pieces)),
+                               dim3(lin::JOIN_NT), 0, st, P, pieces);
+            e = hipGetLastError();
+        }
+    }
+    if (e != hipSuccess || !any)
         return e;
     return P.bf16 ? lin::launch_mode<bf16, lin::OUT>(P, st) : lin::launch_mode<float, lin::OUT>(P, st);
 }

@@ -48,8 +48,8 @@ kdn_status linear_shape(kdn::LinearParams &P, int dtype, int N, int T, int H, in
         P.pool = N;
     }
     const long long blocks = packed ? P.nblocks : (long long)N * P.nblocks;
-    if (tokens * H * (d_k > d_v ? d_k : d_v) >= (1LL << 40) || blocks * H > INT_MAX ||
-        (long long)N * H > INT_MAX / 16 || P.pool * H >= (1LL << 40))
+    if (tokens * H * (d_k > d_v ? d_k : d_v) >= (1LL << 40) || 2 * blocks * H > INT_MAX ||
+        (long long)N * H > INT_MAX / 64 || P.pool * H >= (1LL << 40))
         return KDN_ERR_SHAPE;
     if (!kdn::valid_dim(d_k) || !kdn::valid_dim(d_v))
         return KDN_ERR_UNSUPPORTED;
@@ -107,7 +107,9 @@ bool clash(const Range *outs, int no, const Range *ins, int ni) {
 kdn_status packed_tables(kdn::LinearParams &P, const kdn_packed *packed) {
     if (!packed)
         return KDN_OK;
-    if (P.N > 0 && (!packed->block_offsets || (P.nblocks > 0 && !packed->blocks)))
+    if (P.N + P.tokens > 0 && !packed->block_offsets)
+        return KDN_ERR_NULL;
+    if (P.nblocks > 0 && !packed->blocks)
         return KDN_ERR_NULL;
     if (!aligned(packed->blocks, 16) || !aligned(packed->block_offsets, 4) ||
         !aligned(packed->slots, 4))

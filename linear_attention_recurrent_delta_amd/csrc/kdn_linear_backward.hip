@@ -442,9 +442,11 @@ __global__ __launch_bounds__((GradShape<T, DK, DV>::NT)) void linear_grad_kernel
         grad_walk<T, DK, DV, 2>(P, B, b, h, L);
 }
 
-// Rows behind the last sequence of a packed batch: zero gradients.
-constexpr int TNT = 256;
-template <typename T> __global__ __launch_bounds__(TNT) void linear_tail_kernel(LinearParams P) {
+// Joins of the forward and of the reverse states, and zero gradients for the
+// rows behind the last sequence of a packed batch, by the workgroups' numbers.
+constexpr int TNT = 256, TAIL_WGS = 64;
+template <typename T>
+__device__ __forceinline__ void clear_tail(const LinearParams &P, long wg) {
     const int nb = P.block_offsets[P.N];
     long end = 0;
     if (nb > 0 && nb <= P.nblocks) {
@@ -453,8 +455,8 @@ template <typename T> __global__ __launch_bounds__(TNT) void linear_tail_kernel(
     }
     if (end < 0 || end >= P.tokens)
         return;
-    const long rows = P.tokens - end, stride = (long)gridDim.x * TNT;
-    const long id = (long)blockIdx.x * TNT + threadIdx.x;
+    const long rows = P.tokens - end, stride = (long)TAIL_WGS * TNT;
+    const long id = wg * TNT + threadIdx.x;
     const f32x4 zero = {0.f, 0.f, 0.f, 0.f};
     auto clear = [&](void *out, float *part, int heads, int d) {
         const long row = (long)(part ? P.H : heads) * d;
@@ -469,21 +471,45 @@ template <typename T> __global__ __launch_bounds__(TNT) void linear_tail_kernel(
             static_cast<T *>(P.dla)[end * P.H + i] = from_f32<T>(0.f);
 }
 
-// Gradient of a shared head: the sum over the states that read it, in order.
 template <typename T>
-__global__ __launch_bounds__(TNT) void linear_share_kernel(const float *part, T *out, long n,
-                                                           int row, int d, int group) {
-    // n: groups of 4 values of `out`; row: values of a token in `out`
-    const long i = ((long)blockIdx.x * TNT + threadIdx.x) * 4;
-    if (i >= n * 4)
-        return;
-    const long t = i / row;
-    const int c = i % row, hh = c / d;
-    const float *p = part + t * row * group + (long)hh * group * d + c % d;
-    f32x4 x = *reinterpret_cast<const f32x4 *>(p);
-    for (int j = 1; j < group; ++j)
-        x += *reinterpret_cast<const f32x4 *>(p + (long)j * d);
-    store4<T>(out, nullptr, i, x);
+__global__ __launch_bounds__(TNT) void linear_grad_join_kernel(LinearParams P, int pieces,
+                                                               long joins) {
+    static_assert(TNT == JOIN_NT, "one launch for both");
+    const long id = blockIdx.x;
+    if (id >= 2 * joins)
+        clear_tail<T>(P, id - 2 * joins);
+    else if (id & 1)
+        join_blocks<true>(P, id >> 1, pieces);
+    else
+        join_blocks<false>(P, id >> 1, pieces);
+}
+
+// Gradient of a shared head: the sum over the states that read it, in order.
+// n groups of 4 values of `out`, `row` values of a token in it.
+template <typename T> struct Share {
+    const float *part;
+    T *out;
+    long n;
+    int row, d, group;
+    __device__ __forceinline__ void sum(long g) const {
+        const long i = g * 4, t = i / row;
+        const int c = i % row, hh = c / d;
+        const float *p = part + t * row * group + (long)hh * group * d + c % d;
+        f32x4 x = *reinterpret_cast<const f32x4 *>(p);
+        for (int j = 1; j < group; ++j)
+            x += *reinterpret_cast<const f32x4 *>(p + (long)j * d);
+        store4<T>(out, nullptr, i, x);
+    }
+};
+template <typename T>
+__global__ __launch_bounds__(TNT) void linear_share_kernel(Share<T> q, Share<T> k, Share<T> v) {
+    long i = (long)blockIdx.x * TNT + threadIdx.x;
+    if (i < q.n)
+        return q.sum(i);
+    if ((i -= q.n) < k.n)
+        return k.sum(i);
+    if ((i -= k.n) < v.n)
+        v.sum(i);
 }
 
 // One decay per head: the sum over the blocks, in 64 bits in a fixed order.
@@ -501,20 +527,28 @@ __global__ __launch_bounds__(WAVE) void linear_gate_sum_kernel(LinearParams P, l
 }
 
 template <typename T>
-static hipError_t share(const float *part, void *out, long tokens, int H, int heads, int d,
-                        hipStream_t st) {
-    const long n = tokens * heads * d / 4;
-    if (!part || n == 0)
-        return hipSuccess;
-    hipLaunchKernelGGL(linear_share_kernel<T>, dim3((unsigned)((n + TNT - 1) / TNT)), dim3(TNT), 0,
-                       st, part, static_cast<T *>(out), n, heads * d, d, H / heads);
-    return hipGetLastError();
+static Share<T> share(const LinearParams &P, const float *part, void *out, int heads, int d) {
+    return Share<T>{part, static_cast<T *>(out), part ? P.tokens * heads * d / 4 : 0, heads * d, d,
+                    P.H / (heads ? heads : 1)};
 }
 
 template <typename T> static hipError_t launch_grad(const LinearParams &P, hipStream_t st) {
     const long blocks = linear_total_blocks(P);
     hipError_t e = hipSuccess;
-    if (blocks > 0) {
+    const bool several = P.block_offsets || P.nblocks != 1;     // blocks in a sequence, or none
+    if (several && blocks > 0)
+        e = launch_linear_own(P, st);
+    const int pieces = P.dk * P.dv / (4 * TNT);
+    const long joins = several ? (long)P.N * P.H * pieces : 0;
+    const long tail = P.block_offsets && P.tokens > 0 ? TAIL_WGS : 0;
+    if (e == hipSuccess && joins + tail > 0) {
+        hipLaunchKernelGGL(linear_grad_join_kernel<T>, dim3((unsigned)(2 * joins + tail)), dim3(TNT),
+                           0, st, P, pieces, joins);
+        e = hipGetLastError();
+    }
+    if (e == hipSuccess && blocks > 0)
+        e = launch_linear_chunk_states(P, st);
+    if (e == hipSuccess && blocks > 0) {
         const dim3 grid((unsigned)(blocks * P.H));
 #define KDN_LGRAD(DK_, DV_)                                                                  \
         if (P.dk == DK_ && P.dv == DV_)                                                      \
@@ -527,16 +561,15 @@ template <typename T> static hipError_t launch_grad(const LinearParams &P, hipSt
 #undef KDN_LGRAD
         e = hipGetLastError();
     }
-    if (e == hipSuccess && P.block_offsets && P.tokens > 0) {
-        hipLaunchKernelGGL(linear_tail_kernel<T>, dim3(256), dim3(TNT), 0, st, P);
+    const Share<T> q = share<T>(P, P.ws_dq, P.dq, P.Hq, P.dk);
+    const Share<T> k = share<T>(P, P.ws_dk, P.dk_, P.Hk, P.dk);
+    const Share<T> v = share<T>(P, P.ws_dv, P.dv_, P.Hv, P.dv);
+    const long n = q.n + k.n + v.n;
+    if (e == hipSuccess && n > 0) {
+        hipLaunchKernelGGL(linear_share_kernel<T>, dim3((unsigned)((n + TNT - 1) / TNT)), dim3(TNT),
+                           0, st, q, k, v);
         e = hipGetLastError();
     }
-    if (e == hipSuccess)
-        e = share<T>(P.ws_dq, P.dq, P.tokens, P.H, P.Hq, P.dk, st);
-    if (e == hipSuccess)
-        e = share<T>(P.ws_dk, P.dk_, P.tokens, P.H, P.Hk, P.dk, st);
-    if (e == hipSuccess)
-        e = share<T>(P.ws_dv, P.dv_, P.tokens, P.H, P.Hv, P.dv, st);
     if (e == hipSuccess && P.dla && P.gate == KDN_GATE_HEAD) {
         hipLaunchKernelGGL(linear_gate_sum_kernel<T>, dim3((unsigned)P.H), dim3(WAVE), 0, st, P,
                            blocks);
@@ -550,17 +583,6 @@ template <typename T> static hipError_t launch_grad(const LinearParams &P, hipSt
 hipError_t launch_linear_backward(const LinearParams &P, hipStream_t st) {
     if (P.H == 0)
         return hipSuccess;
-    hipError_t e = hipSuccess;
-    if (P.N > 0) {
-        if (linear_total_blocks(P) > 0)
-            e = launch_linear_states(P, st);
-        if (e == hipSuccess)
-            e = launch_linear_reverse_states(P, st);
-        if (e == hipSuccess && linear_total_blocks(P) > 0)
-            e = launch_linear_chunk_states(P, st);
-    }
-    if (e != hipSuccess)
-        return e;
     return P.bf16 ? lin::launch_grad<bf16>(P, st) : lin::launch_grad<float>(P, st);
 }
 

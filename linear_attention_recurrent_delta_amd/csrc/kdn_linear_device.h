@@ -434,5 +434,66 @@ template <typename T, int ROWS, int COLS, int NT> struct TileRegs {
     }
 };
 
+// ---------------------------------------------------------------------------
+// Join of the blocks along each sequence: block b's own contribution U_b in
+// ws_state becomes the state at its start (REV: in ws_rstate, the reverse
+// state behind its end, blocks last to first).  One thread holds 4 values of S
+// of one (sequence, head); the blocks' values are loaded JOIN ahead.  A
+// sequence of one block has nothing to join, one without tokens passes its
+// state on.
+// ---------------------------------------------------------------------------
+constexpr int JOIN = 8, JOIN_NT = 256;
+
+template <bool REV>
+__device__ __forceinline__ void join_blocks(const LinearParams &P, long id, int pieces) {
+    const int piece = id % pieces;
+    const int h = (id / pieces) % P.H;
+    const int seq = id / ((long)pieces * P.H);
+    const int e = (piece * JOIN_NT + threadIdx.x) * 4;
+    const long size = (long)P.dk * P.dv;
+    long b0 = (long)seq * P.nblocks, b1 = b0 + P.nblocks, slot = seq;
+    if (P.block_offsets) {
+        b0 = P.block_offsets[seq];
+        b1 = P.block_offsets[seq + 1];
+        slot = P.slots ? P.slots[seq] : seq;
+        if (b0 < 0 || b1 > P.nblocks || slot < 0 || slot >= P.pool)
+            return;
+    }
+    const long nb = b1 - b0;
+    if (nb == 1)
+        return;
+    const float *first = REV ? P.dS_out : P.S0;
+    float *pass = REV ? P.dS0 : P.S_out;
+    float *ws = REV ? P.ws_rstate : P.ws_state;
+    const float *decay = REV ? P.ws_rdecay : P.ws_decay;
+    const long at = (slot * P.H + h) * size + e;
+    f32x4 s = {0.f, 0.f, 0.f, 0.f};
+    if (first)
+        s = *reinterpret_cast<const f32x4 *>(first + at);
+    if (nb <= 0) {
+        if (pass && pass != first)
+            *reinterpret_cast<f32x4 *>(pass + at) = s;
+        return;
+    }
+    auto block = [&](long i) { return (REV ? b1 - 1 - i : b0 + i) * P.H + h; };
+    for (long j = 0; j < nb; j += JOIN) {
+        f32x4 u[JOIN];
+        float a[JOIN];
+#pragma unroll
+        for (int i = 0; i < JOIN; ++i)
+            if (j + i < nb - 1) {
+                u[i] = *reinterpret_cast<const f32x4 *>(ws + block(j + i) * size + e);
+                a[i] = decay[block(j + i)];
+            }
+#pragma unroll
+        for (int i = 0; i < JOIN; ++i)
+            if (j + i < nb) {
+                *reinterpret_cast<f32x4 *>(ws + block(j + i) * size + e) = s;
+                if (j + i < nb - 1)
+                    s = s * a[i] + u[i];
+            }
+    }
+}
+
 }  // namespace lin
 }  // namespace kdn
