@@ -247,7 +247,7 @@ __device__ __forceinline__ void linear_walk(
             float d[2][8];
 #pragma unroll
             for (int u = 0; u < 2; ++u)
-                decay_between<T, C>(dc, dc.hi[i], dc.lo[i], i, 32 * jt + 16 * u + 8 * hf, d[u]);
+                decay_between<T>(dc, dc.hi[i], dc.lo[i], i, 32 * jt + 16 * u + 8 * hf, d[u]);
             mma_rows<T, DK, 8>(p, Ks + (32 * jt + cn) * PK + 8 * hf, Qs + i * PK + 8 * hf);
 #pragma unroll
             for (int u = 0; u < 2; ++u) {

@@ -36,7 +36,7 @@ template <typename T, int DK, int DV> struct GradShape {
     static constexpr int IT = C / 32;          // token tiles
     static constexpr int KT = DK / 32, VT = DV / 32;       // channel tiles
     static constexpr int TR = KT * VT / W;     // row tiles of R in a wave
-    static constexpr int KS = C / 16;
+    static constexpr int KS = C / 16;          // steps, and 16-token tiles
     static constexpr int PK = lds_pitch<T>(DK), PV = lds_pitch<T>(DV), PP = lds_pitch<T>(C);
 
     struct Lds {
@@ -48,8 +48,8 @@ template <typename T, int DK, int DV> struct GradShape {
         __attribute__((aligned(16))) T Ys[C * PP];
         __attribute__((aligned(16))) T Rs[DV * PK];      // R^T
         __attribute__((aligned(16))) Decays<C> D[2];
-        // sums of X over a tile's keys, and over 16 of a tile's queries
-        __attribute__((aligned(16))) float rowx[IT][C], colx[2 * IT][C];
+        // sums of X over a tile's keys, and over a tile's queries
+        __attribute__((aligned(16))) float rowx[KS][C], colx[KS][C];
         float xs[KT][C], ys[KT][C], zs[KT];
     };
 };
@@ -183,6 +183,11 @@ __device__ __forceinline__ void grad_walk(const LinearParams &P, const Block &B,
     if (w == GW)
         chunk_decays<C>(D[0], gate_value(la0, nchunk - 1), lane);
     share_state();
+    // P and Y right of the diagonal inside the 32 x 32 tiles: never written
+    for (int i = tid; i < C * PP; i += NT) {
+        Ps[i] = from_f32<T>(0.f);
+        Ys[i] = from_f32<T>(0.f);
+    }
     double gsum = 0.;               // wave GW: sum of the block's d log_alpha (this lane's)
 
     for (int step = 0; step < nchunk; ++step) {
@@ -195,64 +200,91 @@ __device__ __forceinline__ void grad_walk(const LinearParams &P, const Block &B,
         orr.template store<PV>(Os, tid);
         __syncthreads();
 
-        // tiles of P^T and Y^T on and below the diagonal, and of X's sums: lane n
-        // has query i = 32 it + n, registers 0-7 and 8-15 eight keys each
-        if (w < IT * (IT + 1) / 2) {
-            const int it = w > 0, jt = w > 1;
-            const int i = 32 * it + n;
-            f32x16 p = zero16(), y = zero16();
-            mma_rows<T, DK, 4>(p, Ks + (32 * jt + cn) * PK + 8 * hf, Qs + i * PK + 8 * hf);
-            mma_rows<T, DV, 4>(y, Vs + (32 * jt + cn) * PV + 8 * hf, Os + i * PV + 8 * hf);
-            float sum = 0.f;
+        // 16 x 16 tiles of P^T and Y^T on and below the diagonal (small ones:
+        // 10 tiles keep 8 waves busy, 3 of 32 x 32 would not), and X's sums.
+        // Lane m has query i = 16 it + m and 4 keys.
+        for (int t = w; t < KS * (KS + 1) / 2; t += W) {
+            int it = 0, jt = t;
+            while (jt > it)
+                jt -= ++it;
+            const int m = lane & 15, g = lane >> 4;
+            const int i = 16 * it + m, j = 16 * jt + 4 * g;
+            f32x4 p = {0.f, 0.f, 0.f, 0.f}, y = p;
+            {
+                FragV<T> a[DK / 32], x[DK / 32];
 #pragma unroll
-            for (int u = 0; u < 2; ++u) {
-                const int j = 32 * jt + 16 * u + 8 * hf;
-                float d[8], pf[8], yf[8], x[8];
-                decay_between<T, C>(dc, dc.hi[i], dc.lo[i], i, j, d);
-#pragma unroll
-                for (int r = 0; r < 8; ++r) {
-                    pf[r] = p[8 * u + r] * d[r];
-                    yf[r] = y[8 * u + r] * d[r];
-                    // X without its diagonal, which no log-decay is between
-                    x[r] = j + r < i ? pf[r] * y[8 * u + r] : 0.f;
+                for (int s = 0; s < DK / 32; ++s) {
+                    a[s] = frag_row(Ks + (16 * jt + m) * PK + 32 * s + 8 * g);
+                    x[s] = frag_row(Qs + i * PK + 32 * s + 8 * g);
                 }
-                lds_st8(Ps + i * PP + j, pf);
-                lds_st8(Ys + i * PP + j, yf);
-                if (P.dla) {
+                FragV<T> e[DV / 32], f[DV / 32];
 #pragma unroll
-                    for (int r = 0; r < 8; ++r) {
-                        sum += x[r];
-                        x[r] = row16_sum_last(x[r]);
-                    }
-                    if ((n & 15) == 15)
-                        lds_st8(&colx[2 * it + (n >> 4)][j], x);
+                for (int s = 0; s < DV / 32; ++s) {
+                    e[s] = frag_row(Vs + (16 * jt + m) * PV + 32 * s + 8 * g);
+                    f[s] = frag_row(Os + i * PV + 32 * s + 8 * g);
                 }
+                if (sizeof(T) == 2)
+                    __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+                for (int s = 0; s < DK / 32; ++s)
+                    mma(p, a[s], x[s]);
+#pragma unroll
+                for (int s = 0; s < DV / 32; ++s)
+                    mma(y, e[s], f[s]);
             }
-            if (P.dla) {
-                sum += __shfl_xor(sum, 32, WAVE);
-                if (hf == 0)
-                    rowx[jt][i] = sum;
+            float d[4], pf[4], yf[4], row = 0.f;
+            decay_between<T>(dc, dc.hi[i], dc.lo[i], i, j, d);
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+                pf[r] = p[r] * d[r];
+                yf[r] = y[r] * d[r];
+                // X without its diagonal, which no log-decay is between
+                float x = j + r < i ? pf[r] * y[r] : 0.f;
+                row += x;
+                x = row16_sum_last(x);
+                if (m == 15)
+                    colx[it][j + r] = x;
             }
+            lds_stn<4>(Ps + i * PP + j, pf);
+            lds_stn<4>(Ys + i * PP + j, yf);
+            row += __shfl_xor(row, 16, WAVE);
+            row += __shfl_xor(row, 32, WAVE);
+            if (g == 0)
+                rowx[jt][i] = row;
         }
 
-        // what comes from S and R, scaled to each token
+        // What comes from S and R, scaled to each token.  Operands are read a
+        // few steps at a time, so that their latency is paid once for all.
+        // (sched_barrier: what a phase reads is not read in the phase before,
+        // whose registers it would need.)
+        __builtin_amdgcn_sched_barrier(0);
+        constexpr int G = sizeof(T) == 2 && DK + DV < 256 ? 4 : 2;   // registers of 128 x 128
         f32x16 aq = zero16(), ak = zero16(), av = zero16();
         if (qt < IT) {
             const int i = 32 * qt + n;
-            float z = 0.f;
+            const bool want_z = P.dla && qt == 0;
+            f32x16 z = zero16();         // S R^T of this wave's channels: its diagonal
 #pragma unroll
-            for (int s = 0; s < DV / 16; ++s) {
-                const FragV<T> rf = frag_cols<PK, true, true>(Rs + 16 * s * PK + 32 * qc, lane);
-                if (P.dla && qt == 0) {
+            for (int s0 = 0; s0 < DV / 16; s0 += G) {
+                FragV<T> rf[G], of[G], vf[G];
 #pragma unroll
-                    for (int e = 0; e < 8; ++e)
-                        z += to_f32(sf[s][e]) * to_f32(rf[e]);
+                for (int s = 0; s < G; ++s) {
+                    rf[s] = frag_cols<PK, true, true>(Rs + 16 * (s0 + s) * PK + 32 * qc, lane);
+                    of[s] = frag_row_perm(Os + i * PV + 16 * (s0 + s) + 4 * hf);
+                    vf[s] = frag_row_perm(Vs + i * PV + 16 * (s0 + s) + 4 * hf);
                 }
-                mma(aq, sf[s], frag_row_perm(Os + i * PV + 16 * s + 4 * hf));
-                mma(ak, rf, frag_row_perm(Vs + i * PV + 16 * s + 4 * hf));
+                __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+                for (int s = 0; s < G; ++s) {
+                    mma(aq, sf[s0 + s], of[s]);
+                    mma(ak, rf[s], vf[s]);
+                }
+                if (want_z) {
+#pragma unroll
+                    for (int s = 0; s < G; ++s)
+                        mma(z, sf[s0 + s], rf[s]);
+                }
             }
-            if (step + 1 < nchunk)
-                load_state(c - 1);
             aq *= dc.in[i];
             ak *= dc.out[i];
             if (P.dla) {
@@ -274,22 +306,38 @@ __device__ __forceinline__ void grad_walk(const LinearParams &P, const Block &B,
                     xs[qc][i] = x;
                     ys[qc][i] = y;
                 }
-                if (qt == 0) {
-                    z = wave_sum(z);
+                if (want_z) {
+                    float zd = 0.f;
+#pragma unroll
+                    for (int r = 0; r < 16; ++r)
+                        zd += 8 * (r / 4) + 4 * hf + r % 4 == n ? z[r] : 0.f;
+                    zd = wave_sum(zd);
                     if (lane == 0)
-                        zs[qc] = z;
+                        zs[qc] = zd;
                 }
             }
         }
+        __builtin_amdgcn_sched_barrier(0);
+        if (qt < IT && step + 1 < nchunk)
+            load_state(c - 1);
         if (vt < IT) {
             const int i = 32 * vt + n;
 #pragma unroll
-            for (int s = 0; s < DK / 16; ++s)
-                mma(av, frag_row(Rs + (32 * vc + cn) * PK + 16 * s + 8 * hf),
-                    frag_row(Ks + i * PK + 16 * s + 8 * hf));
+            for (int s0 = 0; s0 < DK / 16; s0 += G) {
+                FragV<T> rf[G], kf[G];
+#pragma unroll
+                for (int s = 0; s < G; ++s) {
+                    rf[s] = frag_row(Rs + (32 * vc + cn) * PK + 16 * (s0 + s) + 8 * hf);
+                    kf[s] = frag_row(Ks + i * PK + 16 * (s0 + s) + 8 * hf);
+                }
+                __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+                for (int s = 0; s < G; ++s)
+                    mma(av, rf[s], kf[s]);
+            }
             av *= dc.out[i];
         }
-        const float la = gate_value(la0, c);     // wave GW: this chunk's log-decays
+        const float la = gate_value(la0, c);      // wave GW: this chunk's log-decays
         if (w == GW) {
             if (step + 1 < nchunk)
                 chunk_decays<C>(D[(step + 1) & 1], gate_value(la1, c - 1), lane);
@@ -298,88 +346,116 @@ __device__ __forceinline__ void grad_walk(const LinearParams &P, const Block &B,
                 gate(la1, c - 2);
         }
         __syncthreads();            // P, Y and the sums
-        if (step + 1 < nchunk)
-            load_chunk(c - 1);
 
         if (w == GW && P.dla) {
-            const bool live = lane < C && lane < cnt;
+            // opaque: the addresses below are made here, not held over the loop
+            int tok = lane;
+            asm volatile("" : "+v"(tok));
+            const bool live = tok < C && tok < cnt;
             float u = 0.f, y = 0.f, zz = 0.f;
-            if (live) {
-                const int t = lane / 32;
-                for (int j = 0; j <= t; ++j)
-                    u += rowx[j][lane];
-                for (int i = 2 * t; i < 2 * IT; ++i)
-                    u -= colx[i][lane];
+            if (tok < C) {
+                const int t = tok / 16;
+#pragma unroll
+                for (int j = 0; j < KS; ++j)
+                    u += (j <= t ? rowx[j][tok] : 0.f) - (j >= t ? colx[j][tok] : 0.f);
 #pragma unroll
                 for (int i = 0; i < KT; ++i) {
-                    u += xs[i][lane];
-                    y += ys[i][lane];
+                    u += xs[i][tok];
+                    y += ys[i][tok];
                 }
+                u -= y;
             }
 #pragma unroll
             for (int i = 0; i < KT; ++i)
                 zz += zs[i];
-            // suffix sums of u, prefix sums of y before the token
-            float before = y;
-#pragma unroll
-            for (int off = 1; off < C; off <<= 1) {
-                const float a = __shfl_down(u, off, WAVE), bb = __shfl_up(before, off, WAVE);
-                if (lane + off < C)
-                    u += a;
-                if (lane >= off)
-                    before += bb;
-            }
-            before -= y;
-            float dg = u + before + dc.all * zz;
+            // with u = row - col + x - y: sum_{i >= s} (u_i + y_i) + sum_{j < s} y_j
+            // is all of y and what of u is not before s
+            const double past = prefix_sum((double)u), ally = prefix_sum((double)y);
+            float dg = (float)(lane_value(past, WAVE - 1) - past + (double)u +
+                               lane_value(ally, WAVE - 1)) +
+                       dc.all * zz;
             if (log2_decay(la) <= (double)RESET2)
                 dg = 0.f;           // a reset lets nothing past
             if (live) {
                 if (dla)
-                    dla[(B.first + (long)c * C + lane) * P.H + h] = from_f32<T>(dg);
+                    dla[(B.first + (long)c * C + tok) * P.H + h] = from_f32<T>(dg);
                 gsum += dg;
             }
         }
 
-        // what comes from the chunk's own tokens
+        __builtin_amdgcn_sched_barrier(0);
+        // what comes from the chunk's own tokens: operands first
         if (qt < IT) {
+            FragV<T> x[KS], y[KS];
 #pragma unroll
-            for (int s = 0; s < KS; ++s) {
-                if (s / 2 <= qt)        // dq_i: j <= i
-                    mma(aq, frag_cols<PK, true>(Ks + 16 * s * PK + 32 * qc, lane),
-                        frag_row(Ys + (32 * qt + n) * PP + 16 * s + 8 * hf));
-                if (s / 2 >= qt)        // dk_j: i >= j
-                    mma(ak, frag_cols<PK, true>(Qs + 16 * s * PK + 32 * qc, lane),
-                        frag_cols<PP, false>(Ys + 16 * s * PP + 32 * qt, lane));
+            for (int s = 0; s < KS; ++s)
+                if (s / 2 <= qt) {      // dq_i: j <= i
+                    x[s] = frag_cols<PK, true>(Ks + 16 * s * PK + 32 * qc, lane);
+                    y[s] = frag_row(Ys + (32 * qt + n) * PP + 16 * s + 8 * hf);
+                }
+#pragma unroll
+            for (int s = 0; s < KS; ++s)
+                if (s / 2 <= qt)
+                    mma(aq, x[s], y[s]);
+            __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+            for (int s = 0; s < KS; ++s)
+                if (s / 2 >= qt) {      // dk_j: i >= j
+                    x[s] = frag_cols<PK, true>(Qs + 16 * s * PK + 32 * qc, lane);
+                    y[s] = frag_cols<PP, false>(Ys + 16 * s * PP + 32 * qt, lane);
+                }
+#pragma unroll
+            for (int s = 0; s < KS; ++s)
+                if (s / 2 >= qt)
+                    mma(ak, x[s], y[s]);
+        }
+        __builtin_amdgcn_sched_barrier(0);
+        if (qt < IT && 32 * qt + n < cnt) {
+            const long t0 = (long)c * C + 32 * qt + n;
+#pragma unroll
+            for (int u = 0; u < 2; ++u) {
+                const int c0 = 32 * qc + 16 * u + 8 * hf;
+                float x[8], y[8];
+#pragma unroll
+                for (int r = 0; r < 8; ++r) {
+                    x[r] = aq[8 * u + r];
+                    y[r] = ak[8 * u + r];
+                }
+                store8<T>(P.dq, P.ws_dq, qat + t0 * qrow + c0, x);
+                store8<T>(P.dk_, P.ws_dk, kat + t0 * krow + c0, y);
             }
-            const int i = 32 * qt + n;
-            if (i < cnt) {
-                const long t0 = (long)c * C + i;
+        }
+        __builtin_amdgcn_sched_barrier(0);
+        FragV<T> of[KS];
+#pragma unroll
+        for (int s = 0; s < KS; ++s)
+            of[s] = frag_cols<PV, true>(Os + 16 * s * PV + 32 * vc, lane);
+        if (step + 1 < nchunk)
+            load_chunk(c - 1);
+        if (vt < IT) {
+            FragV<T> pc[KS];
+#pragma unroll
+            for (int s = 0; s < KS; ++s)
+                if (s / 2 >= vt)
+                    pc[s] = frag_cols<PP, false>(Ps + 16 * s * PP + 32 * vt, lane);
+#pragma unroll
+            for (int s = 0; s < KS; ++s)
+                if (s / 2 >= vt)
+                    mma(av, of[s], pc[s]);
+            if (32 * vt + n < cnt) {
+                const long t0 = (long)c * C + 32 * vt + n;
 #pragma unroll
                 for (int u = 0; u < 2; ++u) {
-                    const int c0 = 32 * qc + 16 * u + 8 * hf;
-                    float x[8], y[8];
+                    float x[8];
 #pragma unroll
-                    for (int r = 0; r < 8; ++r) {
-                        x[r] = aq[8 * u + r];
-                        y[r] = ak[8 * u + r];
-                    }
-                    store8<T>(P.dq, P.ws_dq, qat + t0 * qrow + c0, x);
-                    store8<T>(P.dk_, P.ws_dk, kat + t0 * krow + c0, y);
+                    for (int r = 0; r < 8; ++r)
+                        x[r] = av[8 * u + r];
+                    store8<T>(P.dv_, P.ws_dv, vat + t0 * vrow + 32 * vc + 16 * u + 8 * hf, x);
                 }
             }
         }
-        // and R <- all R + q^T (in (.) do)
-        const float all = dc.all;
-#pragma unroll
-        for (int i = 0; i < TR; ++i)
-            R[i] *= all;
-        FragV<T> of[KS];
-#pragma unroll
-        for (int s = 0; s < KS; ++s) {
-            of[s] = frag_cols<PV, true>(Os + 16 * s * PV + 32 * vc, lane);
-            if (vt < IT && s / 2 >= vt)
-                mma(av, of[s], frag_cols<PP, false>(Ps + 16 * s * PP + 32 * vt, lane));
-        }
+        __builtin_amdgcn_sched_barrier(0);
+        // R <- all R + q^T (in (.) do)
         auto rows = [&](int s, int i) {
             return frag_cols<PK, false>(Qs + 16 * s * PK + 32 * (vt * TR + i), lane);
         };
@@ -390,21 +466,14 @@ __device__ __forceinline__ void grad_walk(const LinearParams &P, const Block &B,
 #pragma unroll
         for (int i = 0; i < TR; ++i)
             rq[i] = rows(0, i);
+        const float all = dc.all;
+#pragma unroll
+        for (int i = 0; i < TR; ++i)
+            R[i] *= all;
 #pragma unroll
         for (int i = 0; i < 4 * Split<T, PARTS>::PARTS; ++i)
             split.step(i, of[0], wt);
         update_state<T, PARTS>(R, of, dc.in, hf, split, rq, rows, [](int, int) {});
-        if (vt < IT && 32 * vt + n < cnt) {
-            const long t0 = (long)c * C + 32 * vt + n;
-#pragma unroll
-            for (int u = 0; u < 2; ++u) {
-                float x[8];
-#pragma unroll
-                for (int r = 0; r < 8; ++r)
-                    x[r] = av[8 * u + r];
-                store8<T>(P.dv_, P.ws_dv, vat + t0 * vrow + 32 * vc + 16 * u + 8 * hf, x);
-            }
-        }
         share_state();              // Rs was read before the barrier above
         __syncthreads();            // the chunk's tiles have been read
     }

@@ -104,6 +104,18 @@ __device__ __forceinline__ void mma(f32x16 &acc, f32x8 a, f32x8 b) {
         acc = __builtin_amdgcn_mfma_f32_32x32x2f32(a[s], b[s], acc, 0, 0, 0);
 }
 
+// 16 x 16 tiles, for products that are shared out among waves in smaller
+// pieces: row or column lane & 15, the lane's 8 of 32 contraction elements from
+// 8 (lane >> 4); accumulator register r: row 4 (lane >> 4) + r.
+__device__ __forceinline__ void mma(f32x4 &acc, bf16x8 a, bf16x8 b) {
+    acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b, acc, 0, 0, 0);
+}
+__device__ __forceinline__ void mma(f32x4 &acc, f32x8 a, f32x8 b) {
+#pragma unroll
+    for (int s = 0; s < 8; ++s)
+        acc = __builtin_amdgcn_mfma_f32_16x16x4f32(a[s], b[s], acc, 0, 0, 0);
+}
+
 // p: this lane's row at its 8 consecutive elements (contraction 8 h + e).
 __device__ __forceinline__ bf16x8 frag_row(const bf16 *p) {
     return *reinterpret_cast<const bf16x8 *>(p);
@@ -296,21 +308,28 @@ template <int CTRL, int ROWS> __device__ __forceinline__ double add_dpp(double x
     return x + __builtin_bit_cast(double, (uint64_t)hi << 32 | lo);
 }
 
-// One wave: lane j < C holds the log-decay (natural) of token j, 0 behind the
-// end.  Returns the base-2 prefix sum of the chunk.
-template <int C>
-__device__ __forceinline__ double chunk_decays(Decays<C> &D, float la, int lane) {
-    double x = log2_decay(la);
+// Inclusive prefix sums over the lanes, and the value of a lane.
+__device__ __forceinline__ double prefix_sum(double x) {
     x = add_dpp<0x111, 0xf>(x);      // the lane before, 2, 4 and 8 before (rows of 16)
     x = add_dpp<0x112, 0xf>(x);
     x = add_dpp<0x114, 0xf>(x);
     x = add_dpp<0x118, 0xf>(x);
     x = add_dpp<0x142, 0xa>(x);      // the end of the row before, to rows 1 and 3
-    x = add_dpp<0x143, 0xc>(x);      // lane 31, to rows 2 and 3
-    const double all = __builtin_bit_cast(
-        double, (uint64_t)(uint32_t)__builtin_amdgcn_readlane(
-                    (int)(__builtin_bit_cast(uint64_t, x) >> 32), C - 1) << 32 |
-                    (uint32_t)__builtin_amdgcn_readlane((int)__builtin_bit_cast(uint64_t, x), C - 1));
+    return add_dpp<0x143, 0xc>(x);   // lane 31, to rows 2 and 3
+}
+__device__ __forceinline__ double lane_value(double x, int lane) {
+    const uint64_t b = __builtin_bit_cast(uint64_t, x);
+    const uint32_t lo = __builtin_amdgcn_readlane((int)(uint32_t)b, lane);
+    const uint32_t hi = __builtin_amdgcn_readlane((int)(uint32_t)(b >> 32), lane);
+    return __builtin_bit_cast(double, (uint64_t)hi << 32 | lo);
+}
+
+// One wave: lane j < C holds the log-decay (natural) of token j, 0 behind the
+// end.  Returns the base-2 sum of the chunk.
+template <int C>
+__device__ __forceinline__ double chunk_decays(Decays<C> &D, float la, int lane) {
+    const double x = prefix_sum(log2_decay(la));
+    const double all = lane_value(x, C - 1);
     if (lane < C) {
         const float hi = (float)x;
         D.hi[lane] = hi;
@@ -323,28 +342,23 @@ __device__ __forceinline__ double chunk_decays(Decays<C> &D, float la, int lane)
     return all;
 }
 
-// 2^(G_i - G_j) of 8 consecutive j, 0 right of the diagonal (j > i)
-template <typename T, int C>
+// 2^(G_i - G_j) of N (a multiple of 4) consecutive j, 0 right of the diagonal
+// (j > i)
+template <typename T, int C, int N>
 __device__ __forceinline__ void decay_between(const Decays<C> &D, float hi_i, float lo_i, int i,
-                                              int j, float (&d)[8]) {
-    float x[8];
-    lds_ld8(D.hi + j, x);
+                                              int j, float (&d)[N]) {
 #pragma unroll
-    for (int r = 0; r < 8; ++r)
-        x[r] = hi_i - x[r];
-    // bfloat16 products: the low parts (2^-24 of a prefix sum) are far below
-    // their rounding
-    if (sizeof(T) == 4) {
-        float lo[8];
-        lds_ld8(D.lo + j, lo);
+    for (int q = 0; q < N; q += 4) {
+        f32x4 x = hi_i - *reinterpret_cast<const f32x4 *>(D.hi + j + q);
+        // bfloat16 products: the low parts (2^-24 of a prefix sum) are far
+        // below their rounding
+        if (sizeof(T) == 4)
+            x += lo_i - *reinterpret_cast<const f32x4 *>(D.lo + j + q);
 #pragma unroll
-        for (int r = 0; r < 8; ++r)
-            x[r] += lo_i - lo[r];
-    }
-#pragma unroll
-    for (int r = 0; r < 8; ++r) {
-        const float y = exp2_fast(x[r]);
-        d[r] = j + r <= i ? y : 0.f;
+        for (int r = 0; r < 4; ++r) {
+            const float y = exp2_fast(x[r]);
+            d[q + r] = j + q + r <= i ? y : 0.f;
+        }
     }
 }
 
