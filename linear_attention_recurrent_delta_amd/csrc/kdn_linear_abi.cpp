@@ -20,10 +20,32 @@ struct Range {
 
 long long up256(long long n) { return (n + 255) / 256 * 256; }
 
+// Workgroups that the 256 CUs hold at once: two each of the prefill's kernels,
+// one of the gradients' (LDS).
+constexpr int PREFILL_WGS = 512, GRAD_WGS = 256;
+
+// Tokens of a block: as many blocks as workgroups run at once.  Below that the
+// longest chain counts: the chunks of a block twice (its own state and its
+// outputs, 3.5 us a chunk of 64 each) and the join over the sequence's blocks
+// (1.5 us for 8), least at a block of about sqrt(2 tokens); up to 256 tokens
+// one block is as quick as three launches.
+int dense_block(int tokens, int N, int H, int wgs) {
+    const long long full = ((long long)tokens * H + wgs - 1) / wgs;
+    const long long len = N > 0 ? tokens / N : 0;
+    long long chain = 64;
+    while (chain * chain < 2 * len)
+        chain += 64;
+    if (len <= 256)
+        chain = 256;
+    const long long block = ((full > chain ? full : chain) + 63) / 64 * 64;
+    return (int)(block > (1 << 30) ? (1 << 30) : block);
+}
+
 // Sizes common to the prefill and its gradients; fills the sizes of P.
 // `heads` is false for the workspace query of the prefill, which has none.
+// `wgs`: the workgroups that run at once, which dense blocks are cut for.
 kdn_status linear_shape(kdn::LinearParams &P, int dtype, int N, int T, int H, int Hq, int Hk,
-                        int Hv, int d_k, int d_v, int gate, const kdn_packed *packed) {
+                        int Hv, int d_k, int d_v, int gate, const kdn_packed *packed, int wgs) {
     if (!kdn::valid_dtype(dtype) || (gate != KDN_GATE_TOKEN && gate != KDN_GATE_HEAD))
         return KDN_ERR_UNSUPPORTED;
     if (N < 0 || T < 0 || H < 0 || Hq < 0 || Hk < 0 || Hv < 0 || d_k <= 0 || d_v <= 0)
@@ -43,7 +65,7 @@ kdn_status linear_shape(kdn::LinearParams &P, int dtype, int N, int T, int H, in
         P.nblocks = packed->max_blocks;
         P.pool = packed->pool;
     } else {
-        P.block = kdn_linear_block((int)tokens, N, H);
+        P.block = dense_block((int)tokens, N, H, wgs);
         P.nblocks = T == 0 ? 0 : (T - 1) / P.block + 1;
         P.pool = N;
     }
@@ -137,20 +159,7 @@ int kdn_sequence_max_blocks(int N, int tokens, int block) {
 int kdn_linear_block(int tokens, int N, int H) {
     if (tokens < 0 || N < 0 || H < 0)
         return -1;
-    // Two workgroups for each of the 256 CUs, all at once.  Below that the
-    // longest chain counts: the chunks of a block twice (its own state and its
-    // outputs, 3.5 us a chunk of 64 each) and the join over the sequence's blocks
-    // (1.5 us for 8), least at a block of about sqrt(2 tokens); up to 256 tokens
-    // one block is as quick as three launches.
-    const long long full = ((long long)tokens * H + 511) / 512;
-    const long long len = N > 0 ? tokens / N : 0;
-    long long chain = 64;
-    while (chain * chain < 2 * len)
-        chain += 64;
-    if (len <= 256)
-        chain = 256;
-    const long long block = ((full > chain ? full : chain) + 63) / 64 * 64;
-    return (int)(block > (1 << 30) ? (1 << 30) : block);
+    return dense_block(tokens, N, H, PREFILL_WGS);
 }
 
 kdn_status kdn_sequence_tables(int N, int tokens, int block, int max_blocks, const int *lengths,
@@ -188,7 +197,8 @@ unsigned long long kdn_linear_prefill_workspace_size(kdn_dtype dtype, int N, int
                                                      int d_k, int d_v, const kdn_packed *packed,
                                                      kdn_status *status) {
     kdn::LinearParams P;
-    const kdn_status st = linear_shape(P, dtype, N, T, H, H, H, H, d_k, d_v, KDN_GATE_TOKEN, packed);
+    const kdn_status st = linear_shape(P, dtype, N, T, H, H, H, H, d_k, d_v, KDN_GATE_TOKEN, packed,
+                                       PREFILL_WGS);
     if (status)
         *status = st;
     return st == KDN_OK ? (unsigned long long)state_sections(P, packed != nullptr, nullptr) : 0;
@@ -202,7 +212,8 @@ kdn_status kdn_linear_prefill(kdn_dtype dtype, int N, int T, int H, int Hq, int 
                               void *workspace, unsigned long long workspace_bytes,
                               void *stream) {
     kdn::LinearParams P;
-    if (kdn_status st = linear_shape(P, dtype, N, T, H, Hq, Hk, Hv, d_k, d_v, gate, packed))
+    if (kdn_status st = linear_shape(P, dtype, N, T, H, Hq, Hk, Hv, d_k, d_v, gate, packed,
+                                         PREFILL_WGS))
         return st;
     const long long es = P.bf16 ? 2 : 4, tok = P.tokens;
     if (kdn_status st = token_stride(q_stride, (long long)Hq * d_k, es, &P.q_stride)) return st;
@@ -254,7 +265,8 @@ kdn_status kdn_linear_decode(kdn_dtype dtype, int N, int H, int Hq, int Hk, int 
                              const void *log_alpha, const int *slots, int pool, float *S,
                              void *o, void *stream) {
     kdn::LinearParams L;
-    if (kdn_status st = linear_shape(L, dtype, N, 1, H, Hq, Hk, Hv, d_k, d_v, gate, nullptr))
+    if (kdn_status st = linear_shape(L, dtype, N, 1, H, Hq, Hk, Hv, d_k, d_v, gate, nullptr,
+                                         PREFILL_WGS))
         return st;
     if (pool < 0 || (!slots && pool < N) || (long long)pool * H >= (1LL << 40))
         return KDN_ERR_SHAPE;
@@ -334,7 +346,8 @@ unsigned long long kdn_linear_prefill_backward_workspace_size(
     kdn_dtype dtype, int N, int T, int H, int Hq, int Hk, int Hv, int d_k, int d_v, kdn_gate gate,
     const kdn_packed *packed, kdn_status *status) {
     kdn::LinearParams P;
-    const kdn_status st = linear_shape(P, dtype, N, T, H, Hq, Hk, Hv, d_k, d_v, gate, packed);
+    const kdn_status st = linear_shape(P, dtype, N, T, H, Hq, Hk, Hv, d_k, d_v, gate, packed,
+                                         GRAD_WGS);
     if (status)
         *status = st;
     return st == KDN_OK ? (unsigned long long)grad_ws(P, packed != nullptr).total : 0;
@@ -350,7 +363,8 @@ kdn_status kdn_linear_prefill_backward(kdn_dtype dtype, int N, int T, int H, int
                                        const kdn_packed *packed, void *workspace,
                                        unsigned long long workspace_bytes, void *stream) {
     kdn::LinearParams P;
-    if (kdn_status st = linear_shape(P, dtype, N, T, H, Hq, Hk, Hv, d_k, d_v, gate, packed))
+    if (kdn_status st = linear_shape(P, dtype, N, T, H, Hq, Hk, Hv, d_k, d_v, gate, packed,
+                                         GRAD_WGS))
         return st;
     const long long es = P.bf16 ? 2 : 4, tok = P.tokens;
     if (kdn_status st = token_stride(q_stride, (long long)Hq * d_k, es, &P.q_stride)) return st;
