@@ -40,6 +40,8 @@ struct LinearParams {
     // and its decay, replaced by the state at the block's start.
     float *ws_state;        // [blocks][H][dk * dv]
     float *ws_decay;        // [blocks][H]
+    int *ws_order;          // [nblocks] of a packed batch, the order of its blocks in
+                            // time (null: as they are)
     // Gradients.
     const void *d_o;        // [tokens, H, dv]
     const float *dS_out;    // [pool, H, dk, dv], may be null (zero)

@@ -35,7 +35,9 @@ enum Mode { OWN = 0, OUT = 1, CHUNKS = 2, ROWN = 3 };
 
 constexpr int NT = 256;
 
-template <typename T, int DK, int DV> struct Shape {
+// NH heads of DV / NH columns share a workgroup.
+template <typename T, int DK, int DV, int NH = 1> struct Shape {
+    static constexpr int HD = DV / NH;         // d_v
     static constexpr int C = linear_chunk(sizeof(T) == 2);
     static constexpr int PK = lds_pitch<T>(DK), PV = lds_pitch<T>(DV), PP = lds_pitch<T>(C);
     static constexpr int NCT = DV / 32;        // column tiles
@@ -50,16 +52,16 @@ template <typename T, int DK, int DV> struct Shape {
         __attribute__((aligned(16))) T Ks[C * PK];
         __attribute__((aligned(16))) T Vs[C * PV];
         __attribute__((aligned(16))) T Qs[MODE == OUT ? C * PK : 1];
-        __attribute__((aligned(16))) T Ps[MODE == OUT ? C * PP : 1];
+        __attribute__((aligned(16))) T Ps[NH][MODE == OUT ? C * PP : 1];
         __attribute__((aligned(16))) T Ss[SHARED ? DV * PK : 1];
-        __attribute__((aligned(16))) Decays<C> D[2];
+        __attribute__((aligned(16))) Decays<C> D[2][NH];
     };
 };
 
 // The part of the state of one wave: row tiles t TK .. + TK - 1 of column tile
 // ct (t = w / NCT, ct = w % NCT), column n at channel chan(n).
-template <typename T, int DK, int DV> struct StateAcc {
-    using SH = Shape<T, DK, DV>;
+template <typename T, int DK, int DV, int NH> struct StateAcc {
+    using SH = Shape<T, DK, DV, NH>;
     f32x16 t[SH::TK];
     int row0, col;                             // of this lane
 
@@ -69,6 +71,10 @@ template <typename T, int DK, int DV> struct StateAcc {
     }
     __device__ __forceinline__ int row(int i, int r) const {
         return row0 + 32 * i + 8 * (r / 4) + r % 4;
+    }
+    // element (row, col) of the heads' matrices [NH][DK][HD]
+    __device__ __forceinline__ int at(int i, int r) const {
+        return col / SH::HD * (DK * SH::HD) + row(i, r) * SH::HD + col % SH::HD;
     }
     __device__ __forceinline__ void zero() {
 #pragma unroll
@@ -80,7 +86,7 @@ template <typename T, int DK, int DV> struct StateAcc {
         for (int i = 0; i < SH::TK; ++i)
 #pragma unroll
             for (int r = 0; r < 16; ++r)
-                t[i][r] = S[row(i, r) * DV + col];
+                t[i][r] = S[at(i, r)];
     }
     // from the transposed matrix [DV][DK]
     __device__ __forceinline__ void load_t(const float *S) {
@@ -99,7 +105,7 @@ template <typename T, int DK, int DV> struct StateAcc {
         for (int i = 0; i < SH::TK; ++i)
 #pragma unroll
             for (int r = 0; r < 16; ++r)
-                S[row(i, r) * DV + col] = t[i][r];
+                S[at(i, r)] = t[i][r];
     }
     // operand fragments [column tile][16 rows][lane], rounded to T: the
     // products that read them round the same state in the prefill
@@ -125,22 +131,25 @@ template <typename T, int DK, int DV> struct StateAcc {
 };
 
 // PARTS: of the split operands in the update of S (Split).
-template <typename T, int DK, int DV, int MODE, int PARTS>
+template <typename T, int DK, int DV, int NH, int MODE, int PARTS>
 __device__ __forceinline__ void linear_walk(
     const LinearParams &P, const Block &B, long b, int h,
-    typename Shape<T, DK, DV>::template Lds<MODE> &L) {
-    using SH = Shape<T, DK, DV>;
+    typename Shape<T, DK, DV, NH>::template Lds<MODE> &L) {
+    using SH = Shape<T, DK, DV, NH>;
     constexpr int C = SH::C, TK = SH::TK, KS = SH::KS, IT = SH::IT, OT = SH::OT, TW = SH::TW;
     constexpr int NCT = SH::NCT, PK = SH::PK, PV = SH::PV, PP = SH::PP;
     constexpr bool SHARED = SH::template Lds<MODE>::SHARED;
 
-    T *const Ks = L.Ks, *const Vs = L.Vs, *const Qs = L.Qs, *const Ps = L.Ps, *const Ss = L.Ss;
+    T *const Ks = L.Ks, *const Vs = L.Vs, *const Qs = L.Qs, *const Ss = L.Ss;
     auto &D = L.D;
+    constexpr int HD = SH::HD;
 
     const int tid = threadIdx.x, lane = tid & (WAVE - 1), w = wave_id();
     const int hf = lane >> 5, n = lane & 31, cn = chan(n);
     const int ct = w % NCT, tw = w / NCT;
-    constexpr int HK = MODE == CHUNKS ? DV : DK, HV = MODE == CHUNKS ? DK : DV;
+    const int eh = ct / (NCT / NH);     // head of this wave's columns
+    T *const Ps = L.Ps[eh];
+    constexpr int HK = MODE == CHUNKS ? DV : DK, HV = MODE == CHUNKS ? DK : HD;
     const T *q = static_cast<const T *>(P.q) + B.first * P.q_stride + (h / (P.H / P.Hq)) * HK;
     const T *k = static_cast<const T *>(P.k) + B.first * P.k_stride + (h / (P.H / P.Hk)) * HK;
     const T *v = static_cast<const T *>(P.v) + B.first * P.v_stride + (h / (P.H / P.Hv)) * HV;
@@ -156,7 +165,7 @@ __device__ __forceinline__ void linear_walk(
         k = q;
         ks = P.q_stride;
         vs = P.o_stride;
-        v = static_cast<const T *>(P.d_o) + B.first * vs + h * DV;
+        v = static_cast<const T *>(P.d_o) + B.first * vs + h * HD;
     }
 
     TileRegs<T, C, DK, NT> qr, kr;
@@ -164,14 +173,25 @@ __device__ __forceinline__ void linear_walk(
     const int nchunk = (B.count + C - 1) / C;
     // the wave that sums the decays: not one of those with a tile of P
     constexpr int GW = NT / WAVE - 1;
-    const float head = P.gate == KDN_GATE_HEAD ? static_cast<const float *>(P.la)[h] : 0.f;
-    GateReg<T> la0, la1;            // this lane's token of the next chunks
-    auto gate = [&](GateReg<T> &x, int c) {
-        x.template load<C>(P, B.first + (long)c * C, B.count - c * C, h, lane);
+    float head[NH];
+    GateReg<T> la[NH];              // this lane's token of the next chunk
+    auto gate = [&](int c) {
+#pragma unroll
+        for (int e = 0; e < NH; ++e)
+            la[e].template load<C>(P, B.first + (long)c * C, B.count - c * C, h + e, lane);
     };
-    auto gate_value = [&](const GateReg<T> &x, int c) {
-        return x.value(P, head, lane < C && c * C + lane < B.count);
+    double total[NH];               // base-2 log of the block's decay (wave GW)
+    auto decays = [&](int c, int buffer) {
+#pragma unroll
+        for (int e = 0; e < NH; ++e)
+            total[e] += chunk_decays<C>(
+                D[buffer][e], la[e].value(P, head[e], lane < C && c * C + lane < B.count), lane);
     };
+#pragma unroll
+    for (int e = 0; e < NH; ++e) {
+        head[e] = P.gate == KDN_GATE_HEAD ? static_cast<const float *>(P.la)[h + e] : 0.f;
+        total[e] = 0.;
+    }
     typedef TileRegs<T, C, DK, NT> KT;
     typedef TileRegs<T, C, DV, NT> VT;
     // part i of n of chunk c's loads of k and v, and its loads of q (a chunk
@@ -195,19 +215,16 @@ __device__ __forceinline__ void linear_walk(
     };
     // the chunk of step i
     auto chunk = [&](int i) { return MODE == ROWN ? nchunk - 1 - i : i; };
-    if (w == GW) {
-        gate(la0, chunk(0));
-        if (nchunk > 1)
-            gate(la1, chunk(1));
-    }
+    if (w == GW)
+        gate(chunk(0));
     load_kv(chunk(0), 0, 1);
     load_q(chunk(0));
 
-    StateAcc<T, DK, DV> S(w, lane);
-    const long sidx = (b * P.H + h) * (long)(DK * DV);
+    StateAcc<T, DK, DV, NH> S(w, lane);
+    const long sidx = (b * P.H + h) * (long)(DK * HD);
     const float *start = B.single ? P.S0 : P.ws_state;
     if (start)
-        start += B.single ? (B.slot * P.H + h) * (long)(DK * DV) : sidx;
+        start += B.single ? (B.slot * P.H + h) * (long)(DK * HD) : sidx;
     if (MODE == OWN || MODE == ROWN || !start)
         S.zero();
     else if (MODE == CHUNKS)
@@ -215,15 +232,17 @@ __device__ __forceinline__ void linear_walk(
     else
         S.load(start);
 
-    double total = 0.;              // base-2 log of the block's decay (wave GW)
-    if (w == GW)
-        total = chunk_decays<C>(D[0], gate_value(la0, chunk(0)), lane);
+    if (w == GW) {
+        decays(chunk(0), 0);
+        if (nchunk > 1)
+            gate(chunk(1));
+    }
     if (SHARED)
         S.share(Ss, PK);
 
     for (int step = 0; step < nchunk; ++step) {
         const int c = chunk(step);
-        const Decays<C> &dc = D[step & 1];
+        const Decays<C> &dc = D[step & 1][eh];
         const int cnt = B.count - c * C;       // tokens from here on
         kr.template store<PK>(Ks, tid);
         vr.template store<PV>(Vs, tid);
@@ -235,7 +254,7 @@ __device__ __forceinline__ void linear_walk(
 
         if (MODE == CHUNKS)
             S.store_frags(static_cast<T *>(P.ws_chunk) +
-                              (chunk_slot(b, B.first, c, C) * P.H + h) * (long)(DK * DV),
+                              (chunk_slot(b, B.first, c, C) * P.H + h) * (long)(DK * HD),
                           w, lane);
 
         if (MODE == OUT && w < IT * (IT + 1) / 2) {
@@ -244,21 +263,27 @@ __device__ __forceinline__ void linear_walk(
             const int it = w > 0, jt = w > 1;
             const int i = 32 * it + n;
             f32x16 p = zero16();
-            float d[2][8];
+            float d[NH][2][8];
 #pragma unroll
-            for (int u = 0; u < 2; ++u)
-                decay_between<T>(dc, dc.hi[i], dc.lo[i], i, 32 * jt + 16 * u + 8 * hf, d[u]);
+            for (int e = 0; e < NH; ++e)
+#pragma unroll
+                for (int u = 0; u < 2; ++u) {
+                    const Decays<C> &de = D[step & 1][e];
+                    decay_between<T>(de, de.hi[i], de.lo[i], i, 32 * jt + 16 * u + 8 * hf, d[e][u]);
+                }
             mma_rows<T, DK, 8>(p, Ks + (32 * jt + cn) * PK + 8 * hf, Qs + i * PK + 8 * hf);
 #pragma unroll
-            for (int u = 0; u < 2; ++u) {
-                // rounded to the operand type: P feeds one product whose
-                // result is rounded to the same type
-                float x[8];
+            for (int e = 0; e < NH; ++e)
 #pragma unroll
-                for (int r = 0; r < 8; ++r)
-                    x[r] = p[8 * u + r] * d[u][r];
-                lds_st8(Ps + i * PP + 32 * jt + 16 * u + 8 * hf, x);
-            }
+                for (int u = 0; u < 2; ++u) {
+                    // rounded to the operand type: P feeds one product whose
+                    // result is rounded to the same type
+                    float x[8];
+#pragma unroll
+                    for (int r = 0; r < 8; ++r)
+                        x[r] = p[8 * u + r] * d[e][u][r];
+                    lds_st8(L.Ps[e] + i * PP + 32 * jt + 16 * u + 8 * hf, x);
+                }
         }
 
         // operands of the state's update, S <- all S + k^T (out (.) v)
@@ -352,9 +377,9 @@ __device__ __forceinline__ void linear_walk(
         });
         if (w == GW) {              // the next chunk's decays
             if (step + 1 < nchunk)
-                total += chunk_decays<C>(D[(step + 1) & 1], gate_value(la1, chunk(step + 1)), lane);
+                decays(chunk(step + 1), (step + 1) & 1);
             if (step + 2 < nchunk)
-                gate(la1, chunk(step + 2));
+                gate(chunk(step + 2));
         }
         // P is whole, and q, k and v have been read: what follows reads P and
         // registers only, and the next chunk's tiles may be stored
@@ -382,8 +407,8 @@ __device__ __forceinline__ void linear_walk(
             for (int t = 0; t < OT; ++t) {
                 const int it = t * TW + tw, i = 32 * it + n;
                 if (it < IT && i < cnt) {
-                    T *dst = static_cast<T *>(P.o) + ((B.first + (long)c * C) * P.H + h) * DV +
-                             (unsigned)i * (unsigned)(P.H * DV) + (unsigned)(32 * ct + 8 * hf);
+                    T *dst = static_cast<T *>(P.o) + ((B.first + (long)c * C) * P.H + h) * HD +
+                             (unsigned)i * (unsigned)(P.H * HD) + (unsigned)(32 * ct + 8 * hf);
 #pragma unroll
                     for (int u = 0; u < 2; ++u) {
                         float x[8];
@@ -400,34 +425,41 @@ __device__ __forceinline__ void linear_walk(
     }
     if (MODE == OWN || MODE == ROWN) {
         S.store((MODE == OWN ? P.ws_state : P.ws_rstate) + sidx);
-        if (w == GW && lane == 0)
-            (MODE == OWN ? P.ws_decay : P.ws_rdecay)[b * P.H + h] = exp2_fast((float)total);
+        if (w == GW && lane == 0) {
+#pragma unroll
+            for (int e = 0; e < NH; ++e)
+                (MODE == OWN ? P.ws_decay : P.ws_rdecay)[b * P.H + h + e] =
+                    exp2_fast((float)total[e]);
+        }
     }
     if (MODE == OUT && B.last && P.S_out)
-        S.store(P.S_out + (B.slot * P.H + h) * (long)(DK * DV));
+        S.store(P.S_out + (B.slot * P.H + h) * (long)(DK * HD));
 }
 
-// One (block, head) of a mode.  Three parts for a state that is returned and
-// for what goes into one: the last block's in the prefill and the blocks' own
-// (the forward ones of the gradient call excepted, which are only read rounded).
-template <typename T, int DK, int DV, int MODE, bool GRAD>
-__device__ __forceinline__ void linear_block_head(
-    const LinearParams &P, long id, typename Shape<T, DK, DV>::template Lds<MODE> &L) {
-    const long b = id / P.H;
-    const int h = id % P.H;
+// One block and NH heads of a mode.  Three parts for a state that is returned
+// and for what goes into one: the last block's in the prefill and the blocks'
+// own (the forward ones of the gradient call excepted, which are only read
+// rounded).
+template <typename T, int DK, int DV, int NH, int MODE, bool GRAD>
+__device__ __forceinline__ void linear_block_heads(
+    const LinearParams &P, long id, typename Shape<T, DK, DV, NH>::template Lds<MODE> &L) {
+    const int groups = P.H / NH;
+    // the order is made with the joins, which the blocks' own states precede
+    const long b = MODE == OUT || MODE == CHUNKS ? block_at(P, id / groups) : id / groups;
+    const int h = id % groups * NH;
     const Block B = get_block(P, b);
     if (B.count == 0 || B.slot < 0 || (MODE == OWN && B.last) || (MODE == ROWN && B.index == 0))
         return;
     if (MODE == OUT ? B.last : MODE == ROWN || (MODE == OWN && !GRAD))
-        linear_walk<T, DK, DV, MODE, 3>(P, B, b, h, L);
+        linear_walk<T, DK, DV, NH, MODE, 3>(P, B, b, h, L);
     else if (MODE == OUT || MODE == CHUNKS || GRAD)
-        linear_walk<T, DK, DV, MODE, 2>(P, B, b, h, L);
+        linear_walk<T, DK, DV, NH, MODE, 2>(P, B, b, h, L);
 }
 
-template <typename T, int DK, int DV, int MODE>
+template <typename T, int DK, int DV, int NH, int MODE>
 __global__ __launch_bounds__(NT, 2) void linear_kernel(LinearParams P) {
-    __shared__ typename Shape<T, DK, DV>::template Lds<MODE> L;
-    linear_block_head<T, DK, DV, MODE, false>(P, blockIdx.x, L);
+    __shared__ typename Shape<T, DK, DV, NH>::template Lds<MODE> L;
+    linear_block_heads<T, DK, DV, NH, MODE, false>(P, blockIdx.x, L);
 }
 
 // The blocks' own contributions to both recurrences of the gradient call, in
@@ -439,13 +471,16 @@ __global__ __launch_bounds__(NT, 2) void linear_own_kernel(LinearParams P) {
         typename Shape<T, DK, DV>::template Lds<ROWN> r;
     } L;
     if (blockIdx.x & 1)
-        linear_block_head<T, DK, DV, ROWN, true>(P, blockIdx.x >> 1, L.r);
+        linear_block_heads<T, DK, DV, 1, ROWN, true>(P, blockIdx.x >> 1, L.r);
     else
-        linear_block_head<T, DK, DV, OWN, true>(P, blockIdx.x >> 1, L.f);
+        linear_block_heads<T, DK, DV, 1, OWN, true>(P, blockIdx.x >> 1, L.f);
 }
 
 __global__ __launch_bounds__(JOIN_NT) void linear_join_kernel(LinearParams P, int pieces) {
-    join_blocks<false>(P, blockIdx.x, pieces);
+    if (blockIdx.x == (unsigned long)P.N * P.H * pieces)
+        order_blocks(P);
+    else
+        join_blocks<false>(P, blockIdx.x, pieces);
 }
 
 #define KDN_LINEAR_SIZES(rows, cols, CASE)         \
@@ -460,11 +495,34 @@ static hipError_t launch_mode(const LinearParams &P, hipStream_t st) {
     // rows and columns of the state the mode works on
     const int rows = MODE == CHUNKS ? P.dv : P.dk, cols = MODE == CHUNKS ? P.dk : P.dv;
 #define KDN_CASE(DK_, DV_)                                                         \
-    hipLaunchKernelGGL((linear_kernel<T, DK_, DV_, MODE>), grid, block, 0, st, P); \
+    hipLaunchKernelGGL((linear_kernel<T, DK_, DV_, 1, MODE>), grid, block, 0, st, P); \
     return hipGetLastError();
     KDN_LINEAR_SIZES(rows, cols, KDN_CASE)
 #undef KDN_CASE
     return hipErrorInvalidValue;
+}
+
+// Two heads of d_v = 64 in a workgroup, where two neighbours have the same q
+// and k and v of their own: q and k are read and q k^T is made once for both,
+// and their columns fill the four waves.  Only where single heads would be
+// more workgroups than run at once (2 a CU), since one alone takes longer for
+// two: B1 H8 T1000 of 128 x 64, bf16, 22 against 19 us; B1 H16 T4000 36
+// against 39; B4 H32 T16384 439 against 489 (float32 38 against 31, 71 against
+// 91, 1450 against 1968).
+inline bool pairs(const LinearParams &P) {
+    return P.dv == 64 && P.Hv == P.H && P.H / P.Hq % 2 == 0 && P.H / P.Hk % 2 == 0 &&
+           linear_total_blocks(P) * P.H >= 512;
+}
+template <typename T, int MODE>
+static hipError_t launch_prefill_mode(const LinearParams &P, hipStream_t st) {
+    if (!pairs(P))
+        return launch_mode<T, MODE>(P, st);
+    const dim3 grid((unsigned)(linear_total_blocks(P) * (P.H / 2))), block(NT);
+    if (P.dk == 64)
+        hipLaunchKernelGGL((linear_kernel<T, 64, 128, 2, MODE>), grid, block, 0, st, P);
+    else
+        hipLaunchKernelGGL((linear_kernel<T, 128, 128, 2, MODE>), grid, block, 0, st, P);
+    return hipGetLastError();
 }
 
 template <typename T> static hipError_t launch_own(const LinearParams &P, hipStream_t st) {
@@ -488,27 +546,31 @@ hipError_t launch_linear_chunk_states(const LinearParams &P, hipStream_t st) {
                   : lin::launch_mode<float, lin::CHUNKS>(P, st);
 }
 
-hipError_t launch_linear_prefill(const LinearParams &P, hipStream_t st) {
+hipError_t launch_linear_prefill(const LinearParams &call, hipStream_t st) {
+    LinearParams P = call;
     if (P.N == 0 || P.H == 0)
         return hipSuccess;
-    const bool any = linear_total_blocks(P) > 0;
+    const bool any = linear_total_blocks(P) > 0, sort = lin::ordered(P);
+    if (!sort)
+        P.ws_order = nullptr;
     hipError_t e = hipSuccess;
     if (P.block_offsets || P.nblocks != 1) {
         // the blocks' own contributions and their join, where a sequence may
         // have more than one; the join also passes on the states of empty ones
         if (any)
-            e = P.bf16 ? lin::launch_mode<bf16, lin::OWN>(P, st)
-                       : lin::launch_mode<float, lin::OWN>(P, st);
+            e = P.bf16 ? lin::launch_prefill_mode<bf16, lin::OWN>(P, st)
+                       : lin::launch_prefill_mode<float, lin::OWN>(P, st);
         if (e == hipSuccess) {
             const int pieces = P.dk * P.dv / (4 * lin::JOIN_NT);
-            hipLaunchKernelGGL(lin::linear_join_kernel, dim3((unsigned)((long)P.N * P.H * pieces)),
+            hipLaunchKernelGGL(lin::linear_join_kernel, dim3((unsigned)((long)P.N * P.H * pieces + sort)),
                                dim3(lin::JOIN_NT), 0, st, P, pieces);
             e = hipGetLastError();
         }
     }
     if (e != hipSuccess || !any)
         return e;
-    return P.bf16 ? lin::launch_mode<bf16, lin::OUT>(P, st) : lin::launch_mode<float, lin::OUT>(P, st);
+    return P.bf16 ? lin::launch_prefill_mode<bf16, lin::OUT>(P, st)
+                  : lin::launch_prefill_mode<float, lin::OUT>(P, st);
 }
 
 }  // namespace kdn

@@ -100,16 +100,16 @@ long long span(long long rows, long stride, long long row, long long es) {
     return rows > 0 ? ((rows - 1) * stride + row) * es : 0;
 }
 
-// Workspace sections: states at the blocks' starts and the blocks' decays;
-// nothing where every sequence is known to be one block.
+// Workspace sections: states at the blocks' starts, and the blocks' decays with
+// a packed batch's order behind them; nothing where every sequence is known to
+// be one block.
 long long state_sections(const kdn::LinearParams &P, bool packed, long long *decay) {
     const long long blocks = packed ? P.nblocks : (long long)P.N * P.nblocks;
     if (!packed && P.nblocks <= 1)
         return 0;
     const long long n = up256(blocks * P.H * P.dk * P.dv * 4);
-    if (decay)
-        *decay = n;
-    return n + up256(blocks * P.H * 4);
+    *decay = n;
+    return n + up256(blocks * (P.H + packed) * 4);
 }
 
 // Outputs overlap no input and no other output.
@@ -201,7 +201,8 @@ unsigned long long kdn_linear_prefill_workspace_size(kdn_dtype dtype, int N, int
                                        PREFILL_WGS);
     if (status)
         *status = st;
-    return st == KDN_OK ? (unsigned long long)state_sections(P, packed != nullptr, nullptr) : 0;
+    long long decay;
+    return st == KDN_OK ? (unsigned long long)state_sections(P, packed != nullptr, &decay) : 0;
 }
 
 kdn_status kdn_linear_prefill(kdn_dtype dtype, int N, int T, int H, int Hq, int Hk, int Hv,
@@ -252,6 +253,8 @@ kdn_status kdn_linear_prefill(kdn_dtype dtype, int N, int T, int H, int Hq, int 
             return KDN_ERR_ALIAS;
         P.ws_state = static_cast<float *>(workspace);
         P.ws_decay = reinterpret_cast<float *>(static_cast<char *>(workspace) + decay);
+        if (packed)
+            P.ws_order = reinterpret_cast<int *>(P.ws_decay + (long)P.nblocks * H);
     }
     P.q = q; P.k = k; P.v = v; P.la = log_alpha;
     P.S0 = S0; P.o = o; P.S_out = S_out;
@@ -304,9 +307,9 @@ kdn_status kdn_linear_decode(kdn_dtype dtype, int N, int H, int Hq, int Hk, int 
 // ---------------------------------------------------------------------------
 namespace {
 // Workspace, sections 256-byte aligned: the forward and the reverse states at
-// the blocks' ends with the blocks' decays (sequences of several blocks), the
-// state at every chunk's start, float32 gradients of shared heads before their
-// sum, and for one decay per head each block's sum.
+// the blocks' ends with the blocks' decays (sequences of several blocks; a
+// packed batch's order behind the decays), the state at every chunk's start, float32 gradients of
+// shared heads before their sum, and for one decay per head each block's sum.
 struct GradWs {
     long long state, decay, rstate, rdecay, chunk, dq, dk, dv, dla, total;
 };
@@ -324,7 +327,7 @@ GradWs grad_ws(const kdn::LinearParams &P, bool packed) {
     };
     if (packed || P.nblocks > 1) {
         w.state = take(blocks * P.H * n_S * 4);
-        w.decay = take(blocks * P.H * 4);
+        w.decay = take(blocks * (P.H + packed) * 4);
         w.rstate = take(blocks * P.H * n_S * 4);
         w.rdecay = take(blocks * P.H * 4);
     }
@@ -416,6 +419,8 @@ kdn_status kdn_linear_prefill_backward(kdn_dtype dtype, int N, int T, int H, int
             P.ws_decay = f32(w.decay);
             P.ws_rstate = f32(w.rstate);
             P.ws_rdecay = f32(w.rdecay);
+            if (packed)
+                P.ws_order = reinterpret_cast<int *>(P.ws_decay + (long)P.nblocks * H);
         }
         P.ws_chunk = base + w.chunk;
         P.ws_dq = Hq != H ? f32(w.dq) : nullptr;

@@ -496,7 +496,7 @@ __device__ __forceinline__ void grad_walk(const LinearParams &P, const Block &B,
 
 template <typename T, int DK, int DV>
 __global__ __launch_bounds__((GradShape<T, DK, DV>::NT)) void linear_grad_kernel(LinearParams P) {
-    const long b = blockIdx.x / P.H;
+    const long b = block_at(P, blockIdx.x / P.H);
     const int h = blockIdx.x % P.H;
     const Block B = get_block(P, b);
     if (P.ws_dla && (B.count == 0 || B.slot < 0) && threadIdx.x == 0)
@@ -511,8 +511,9 @@ __global__ __launch_bounds__((GradShape<T, DK, DV>::NT)) void linear_grad_kernel
         grad_walk<T, DK, DV, 2>(P, B, b, h, L);
 }
 
-// Joins of the forward and of the reverse states, and zero gradients for the
-// rows behind the last sequence of a packed batch, by the workgroups' numbers.
+// Joins of the forward and of the reverse states, zero gradients for the rows
+// behind the last sequence of a packed batch, and the order of its blocks, by
+// the workgroups' numbers.
 constexpr int TNT = 256, TAIL_WGS = 64;
 template <typename T>
 __device__ __forceinline__ void clear_tail(const LinearParams &P, long wg) {
@@ -542,10 +543,12 @@ __device__ __forceinline__ void clear_tail(const LinearParams &P, long wg) {
 
 template <typename T>
 __global__ __launch_bounds__(TNT) void linear_grad_join_kernel(LinearParams P, int pieces,
-                                                               long joins) {
+                                                               long joins, long tail) {
     static_assert(TNT == JOIN_NT, "one launch for both");
     const long id = blockIdx.x;
-    if (id >= 2 * joins)
+    if (id >= 2 * joins + tail)
+        order_blocks(P);
+    else if (id >= 2 * joins)
         clear_tail<T>(P, id - 2 * joins);
     else if (id & 1)
         join_blocks<true>(P, id >> 1, pieces);
@@ -601,8 +604,12 @@ static Share<T> share(const LinearParams &P, const float *part, void *out, int h
                     P.H / (heads ? heads : 1)};
 }
 
-template <typename T> static hipError_t launch_grad(const LinearParams &P, hipStream_t st) {
+template <typename T> static hipError_t launch_grad(const LinearParams &call, hipStream_t st) {
+    LinearParams P = call;
     const long blocks = linear_total_blocks(P);
+    const bool sort = ordered(P);
+    if (!sort)
+        P.ws_order = nullptr;
     hipError_t e = hipSuccess;
     const bool several = P.block_offsets || P.nblocks != 1;     // blocks in a sequence, or none
     if (several && blocks > 0)
@@ -610,9 +617,10 @@ template <typename T> static hipError_t launch_grad(const LinearParams &P, hipSt
     const int pieces = P.dk * P.dv / (4 * TNT);
     const long joins = several ? (long)P.N * P.H * pieces : 0;
     const long tail = P.block_offsets && P.tokens > 0 ? TAIL_WGS : 0;
-    if (e == hipSuccess && joins + tail > 0) {
-        hipLaunchKernelGGL(linear_grad_join_kernel<T>, dim3((unsigned)(2 * joins + tail)), dim3(TNT),
-                           0, st, P, pieces, joins);
+    if (e == hipSuccess && joins + tail + sort > 0) {
+        hipLaunchKernelGGL(linear_grad_join_kernel<T>, 
+                           dim3((unsigned)(2 * joins + tail + sort)), dim3(TNT), 0, st, P, pieces,
+                           joins, tail);
         e = hipGetLastError();
     }
     if (e == hipSuccess && blocks > 0)

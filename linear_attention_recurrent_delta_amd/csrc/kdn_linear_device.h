@@ -509,5 +509,53 @@ __device__ __forceinline__ void join_blocks(const LinearParams &P, long id, int 
     }
 }
 
+// Order of a packed batch's blocks in time: the longest first, so that the
+// workgroups that start last are short ones.  Worth it where there are more
+// workgroups than run at once; with very many blocks the differences even out
+// (and one workgroup sorts).  B = 37 sequences of 700 tokens at the mean, bf16,
+// the prefill: H32 of 128 x 64 in blocks of 1664 257 -> 196 us, H16 of 128 x 128
+// in blocks of 832 186 -> 178 us.
+constexpr int ORDER_BINS = 512, ORDER_MAX = 4096;
+inline bool ordered(const LinearParams &P) {
+    return P.ws_order && P.nblocks <= ORDER_MAX && (long)P.nblocks * P.H > 256;
+}
+// By one workgroup of JOIN_NT threads: a counting sort by length.  Which of two
+// blocks of about the same length is first may change, results do not.
+__device__ __forceinline__ void order_blocks(const LinearParams &P) {
+    static_assert(ORDER_BINS == 2 * JOIN_NT, "two bins a thread");
+    __shared__ int count[ORDER_BINS], wave[JOIN_NT / WAVE];
+    const int tid = threadIdx.x, lane = tid & (WAVE - 1);
+    count[tid] = count[tid + JOIN_NT] = 0;
+    __syncthreads();
+    // bin 0: the longest
+    auto bin = [&](int b) {
+        const int n = min(max(P.blocks[4l * b + 1], 0), P.block);
+        return ORDER_BINS - 1 - (int)((long)n * (ORDER_BINS - 1) / P.block);
+    };
+    for (int b = tid; b < P.nblocks; b += JOIN_NT)
+        atomicAdd(&count[bin(b)], 1);
+    __syncthreads();
+    const int x = count[2 * tid], y = count[2 * tid + 1];
+    int sum = x + y;
+    for (int off = 1; off < WAVE; off *= 2) {
+        const int below = __shfl_up(sum, off, WAVE);
+        sum += lane >= off ? below : 0;
+    }
+    if (lane == WAVE - 1)
+        wave[tid / WAVE] = sum;
+    __syncthreads();
+    for (int i = 0; i < tid / WAVE; ++i)
+        sum += wave[i];
+    count[2 * tid] = sum - x - y;
+    count[2 * tid + 1] = sum - y;
+    __syncthreads();
+    for (int b = tid; b < P.nblocks; b += JOIN_NT)
+        P.ws_order[atomicAdd(&count[bin(b)], 1)] = b;
+}
+// The block of the i-th place.
+__device__ __forceinline__ long block_at(const LinearParams &P, long i) {
+    return P.ws_order ? __builtin_amdgcn_readfirstlane(P.ws_order[i]) : i;
+}
+
 }  // namespace lin
 }  // namespace kdn

@@ -84,6 +84,35 @@ def test_prefill_shared_heads_and_strides(Hq, Hk, Hv, H, dtype):
     check_dense(q, k, v, la, S0, o, S, H)
 
 
+@pytest.mark.parametrize("Hq,Hk,H", [(1, 1, 2), (2, 1, 4), (3, 3, 6), (1, 2, 4), (2, 2, 6)])
+@pytest.mark.parametrize("dk", [64, 128])
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("gate", ["token", "head"])
+def test_prefill_neighbours_with_the_same_q_and_k(Hq, Hk, H, dk, dtype, gate):
+    """Heads of 64 columns, whose neighbours have q and k in common: outputs,
+    states, and the blocks of a cut sequence, each head with its own decay."""
+    q, k, v, la = make((2, 330), Hq, Hk, H, H, dk, 64, dtype, gate, seed=H + dk, fused=True)
+    if gate == "token":
+        la[:, 100, 1::2] = -math.inf
+    S0 = state(2, H, dk, 64)
+    o, S = kdn.linear_prefill(q, k, v, la, S0=S0)
+    check_dense(q, k, v, la, S0, o, S, H)
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+def test_prefill_neighbours_keep_their_infinities(dtype):
+    """A value, a start or a decay that is not finite stays in its head."""
+    q, k, v, la = make((1, 600), 2, 2, 4, 4, 128, 64, dtype, seed=21)
+    S0 = state(1, 4, 128, 64)
+    o, S = kdn.linear_prefill(q, k, v, la, S0=S0)
+    v[:, 70, 1], la[:, 90, 2], S0[:, 3] = math.inf, math.nan, math.nan
+    o2, S2 = kdn.linear_prefill(q, k, v, la, S0=S0)
+    assert torch.equal(o[:, :, 0], o2[:, :, 0]) and torch.equal(S[:, 0], S2[:, 0])
+    assert torch.equal(o[:, :64, 1:3], o2[:, :64, 1:3])
+    assert not torch.isfinite(S2[:, 1:]).flatten(2).all(-1).any()
+    assert o2[:, :, 3].isnan().all()
+
+
 @pytest.mark.parametrize("dtype", [BF, F32])
 @pytest.mark.parametrize("value", [-math.inf, -1e30, -120.0, -7.0, 0.0])
 @pytest.mark.parametrize("share", [0.03, 0.5, 1.0])
@@ -212,6 +241,43 @@ def test_packed(lengths, dtype, block, inplace):
 
 
 @pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("dv", [64, 128])
+def test_packed_many_blocks(dtype, dv):
+    """More workgroups than run at once: the blocks are taken longest first.
+    Neighbouring heads share q and k, sequences are cut, empty or skipped."""
+    lengths = [(37 * n * n + 11 * n) % 331 for n in range(40)]
+    lengths[7] = lengths[8] = 0
+    H, total = 8, sum(lengths) + 9
+    slots = [(7 * n + 3) % 41 for n in range(40)]
+    slots[5] = -1
+    q, k, v, la = make((total,), 2, 4, H, H, 64, dv, dtype, seed=91)
+    t = kdn.sequence_tables(i32(lengths), total, 128, slots=i32(slots))
+    assert t.blocks.shape[0] * H > 512
+    S = state(41, H, 64, dv)
+    keep = S.clone()
+    o = torch.full(v.shape, 7.0, dtype=dtype, device="cuda")
+    ob = o.clone()
+    kdn.linear_prefill(q, k, v, la, S0=S, tables=t, out=(o, S))
+    wide = [x.repeat_interleave(H // x.shape[1], 1) for x in (q, k)]
+    check_packed(*wide, v, la, lengths, slots, keep, o, S, keep, ob)
+
+
+def test_packed_thousands_of_blocks():
+    """So many blocks that they are taken as they come, the same bits as in a
+    batch of their first sequences, which are sorted."""
+    lengths = [1 + n % 3 for n in range(4200)]
+    total, few = sum(lengths), 300
+    q, k, v, la, t = packed_case(lengths, 0, 2, 64, 64, BF, 95, 64)
+    assert t.blocks.shape[0] > 4096
+    o, S = kdn.linear_prefill(q, k, v, la, tables=t)
+    rows = sum(lengths[:few])
+    t2 = kdn.sequence_tables(i32(lengths[:few]), rows, 64)
+    o2, S2 = kdn.linear_prefill(q[:rows], k[:rows], v[:rows], la[:rows], tables=t2)
+    assert torch.equal(o[:rows], o2) and torch.equal(S[:few], S2)
+    check_packed(q[:rows], k[:rows], v[:rows], la[:rows], lengths[:few], None, None, o2, S2, S2, o2)
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
 def test_packed_skips_sequences_without_a_slot(dtype):
     lengths, slots = [70, 130, 0, 400, 3], [2, -1, 7, 6, 0]       # pool of 6: -1, 7, 6 are none
     q, k, v, la, t = packed_case(lengths, 2, 2, 64, 128, dtype, 31, 128, slots)
@@ -254,6 +320,22 @@ def test_packed_rows_that_do_not_fit_are_skipped():
         kdn.linear_prefill(q, k, v, la, tables=t2, out=(o, S))
         torch.cuda.synchronize()
         assert torch.equal(o[:164], good[:164]) and (o[164:] == 7.0).all()
+
+
+def test_packed_rows_of_any_length_are_sorted():
+    """Lengths that no table has: the rows are skipped, the others computed."""
+    lengths = [40] * 150
+    q, k, v, la, t = packed_case(lengths, 0, 2, 64, 64, F32, 52, 64)
+    good, _ = kdn.linear_prefill(q, k, v, la, tables=t)
+    for n, bad in ((3, -2 ** 31), (9, 2 ** 31 - 1), (20, -1), (149, 65)):
+        t.blocks[n, 1] = bad
+    o = torch.full(v.shape, 7.0, device="cuda")
+    S = torch.zeros(150, 2, 64, 64, device="cuda")
+    kdn.linear_prefill(q, k, v, la, tables=t, out=(o, S))
+    skipped = torch.zeros(150, 40, dtype=torch.bool, device="cuda")
+    skipped[[3, 9, 20, 149]] = True
+    skipped = skipped.flatten()
+    assert torch.equal(o[~skipped], good[~skipped]) and (o[skipped] == 7.0).all()
 
 
 # ---------------------------------------------------------------------------

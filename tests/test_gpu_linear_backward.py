@@ -169,6 +169,22 @@ def test_packed(lengths, dtype, block, Hk):
         assert not got["dS0"][p].any()
 
 
+@pytest.mark.parametrize("dtype", [BF, F32])
+def test_packed_many_blocks(dtype):
+    """More workgroups than run at once: the blocks are taken longest first."""
+    lengths, H, tail = [(23 * n * n + 5 * n) % 211 for n in range(44)], 6, 4
+    total = sum(lengths) + tail
+    q, k, v, la = make((total,), 2, 3, H, H, 64, 64, dtype, seed=44)
+    do = randn((total, H, 64), dtype, 3)
+    S0, dS = state(44, H, 64, 64), state(44, H, 64, 64, seed=2)
+    t = kdn.sequence_tables(i32(lengths), total, 64)
+    assert t.blocks.shape[0] * H > 256
+    got = kdn.linear_prefill_backward(q, k, v, do, la, S0=S0, dS_out=dS, tables=t)
+    ends = torch.tensor(lengths).cumsum(0).tolist()
+    check(q, k, v, la, do, S0, dS, got, [slice(e - n, e) for e, n in zip(ends, lengths)],
+          list(range(44)))
+
+
 def test_wanted_outputs_only():
     """Without d log_alpha and dS0, into given tensors, the same bits."""
     H, T = 2, 300
