@@ -360,7 +360,8 @@ unsigned long long kdn_chunk_prefill_backward_workspace_size(kdn_variant variant
  *   - q, k and v may be slices of wider rows, such as one projection's output:
  *     q_stride, k_stride and v_stride are the elements from one token to the
  *     next (0: contiguous, heads * d), at least heads * d, and whole 16-byte
- *     pieces.  The heads of a token are contiguous.  o is contiguous.
+ *     pieces.  The heads of a token are contiguous.  o is contiguous.  A
+ *     token's row of q, k, v (its stride) and of o is less than 64 MiB.
  *   - dense batches: N sequences of T tokens, rows n * T + t, state n of S0 and
  *     S_out.  Packed batches (`packed` not NULL): N sequences of any lengths
  *     one behind the other, described by kdn_sequence_tables; T is 0; rows

@@ -220,6 +220,7 @@ kdn_status kdn_linear_prefill(kdn_dtype dtype, int N, int T, int H, int Hq, int 
     if (kdn_status st = token_stride(q_stride, (long long)Hq * d_k, es, &P.q_stride)) return st;
     if (kdn_status st = token_stride(k_stride, (long long)Hk * d_k, es, &P.k_stride)) return st;
     if (kdn_status st = token_stride(v_stride, (long long)Hv * d_v, es, &P.v_stride)) return st;
+    if (kdn_status st = token_stride(0, (long long)H * d_v, es, &P.o_stride)) return st;
     if (tok * H > 0 && (!q || !k || !v || !log_alpha || !o))
         return KDN_ERR_NULL;
     if (kdn_status st = packed_tables(P, packed))

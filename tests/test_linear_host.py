@@ -44,6 +44,8 @@ def prefill(lib, dtype=BF16, N=2, T=100, H=4, Hq=4, Hk=4, Hv=4, dk=64, dv=64, ga
     (dict(gate=1, la=A + 3 * MB + 2), EALIGN),
     (dict(o=A), EALIAS), (dict(o=A + 2 * MB + 16), EALIAS), (dict(S=A + 4 * MB + 16), EALIAS),
     (dict(S=A + 6 * MB), EALIAS), (dict(o=A + 4 * MB), EALIAS),
+    # rows of o of 64 MiB: a chunk of them would pass 2^32 bytes
+    (dict(N=1, T=1, H=1 << 19, Hv=1, dv=64), ESHAPE), (dict(N=1, T=1, H=1 << 18, Hv=1, dv=64, dtype=F32), ESHAPE),
     # o inside the wide rows that v is a slice of
     (dict(vs=4096, o=A + 2 * MB + 199 * 4096 * 2), EALIAS),
     (dict(T=1000, ws=None), EWS), (dict(T=1000, wsb=100), EWS), (dict(T=1000, ws=A + 12 * MB + 64), EALIGN),
