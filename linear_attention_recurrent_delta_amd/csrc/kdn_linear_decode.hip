@@ -1,11 +1,15 @@
 // kdn_linear_decode.hip -- one token of linear attention with a decay for
 // each head for every row of a batch (gfx950):
 //   S <- e^g S + k v^T,   o = S^T q.
-// Bound by one read and one write of S.  The columns of S are independent, so
-// a workgroup of 256 threads owns CW of the d_v columns of one (row, head);
-// thread (rg, cg) holds rows [rg * RPT, + RPT) of 4 columns in registers, and
-// the partial outputs of the row groups are summed by lane exchanges, then
-// across the waves in LDS (a fixed order: results are the same every time).
+// Bound by one read and one write of S: 8192 states of 128 x 128 (1.07 GB) in
+// 192 us, 5.6 TB/s, above what a large copy reaches (4.9); a step of a few
+// states by the launch and the latency of one load and one store, 3.3 us.  S
+// passes the caches (non-temporal): nothing of it is read twice in a step.
+// The columns of S are independent, so a workgroup of 256 threads owns CW of
+// the d_v columns of one (row, head); thread (rg, cg) holds rows
+// [rg * RPT, + RPT) of 4 columns in registers, and the partial outputs of the
+// row groups are summed by lane exchanges, then across the waves in LDS (a
+// fixed order: results are the same every time).
 #include "kdn_linear_device.h"
 
 namespace kdn {
@@ -80,11 +84,14 @@ static hipError_t launch_decode_t(const LinearDecodeParams &P, hipStream_t st) {
                            dim3((unsigned)(nh * (DV_ / CW_))), dim3(DNT), 0, st, P);        \
         return hipGetLastError();                                                           \
     }
-    // few states: a quarter of the columns each, so that more CUs share one
-    if (nh < 1024) {
-        KDN_LDEC(64, 64, 16)
+    // No more states than CUs: 32 columns (whole cache lines) each, so that more
+    // CUs share a state.  bf16, us, split against whole: 8 states of 128 x 128
+    // 3.3 / 5.6, 256 7.2 / 8.0, 512 14.0 / 13.2; 256 of 128 x 64 4.8 / 5.2, 512
+    // 7.1 / 7.1; 256 of 64 x 64 3.8 / 3.9.
+    if (nh <= 256) {
+        KDN_LDEC(64, 64, 32)
         KDN_LDEC(64, 128, 32)
-        KDN_LDEC(128, 64, 16)
+        KDN_LDEC(128, 64, 32)
         KDN_LDEC(128, 128, 32)
     }
     KDN_LDEC(64, 64, 64)
