@@ -21,6 +21,17 @@
 // q k^T is computed once, a tile per wave, and shared through LDS.  q, k and v
 // of the next chunk are in flight (in registers) while one is worked on, and
 // two workgroups share a CU.
+//
+// Tiles are 32 x 32 because the operands come from LDS: 16 x 16 tiles read
+// every operand twice as often for the same products.
+//
+// Measured (bf16, 128 x 128): B2 H16 T16384 in blocks of 1024, constant decays,
+// 207 us a call (own states 69-88 us, join 13, outputs 127-151: the clock falls
+// in long runs).  It moves 805 MB where 537 are needed (k and v twice), at
+// 3.9 TB/s of the 4.9 that a large copy reaches; what holds it is that a
+// workgroup's LDS reads, splitting and MFMAs (40, 30 and 25 % of the time)
+// follow one another and a CU has two workgroups to overlap.  B1 H16 T190
+// 14.3 us, three chunks one after the other.
 #include "kdn_linear_device.h"
 
 namespace kdn {
@@ -146,6 +157,7 @@ __device__ __forceinline__ void linear_walk(
 
     const int tid = threadIdx.x, lane = tid & (WAVE - 1), w = wave_id();
     const int hf = lane >> 5, n = lane & 31, cn = chan(n);
+    const int rn = lds_row(n), rcn = lds_row(cn);   // their places in a tile
     const int ct = w % NCT, tw = w / NCT;
     const int eh = ct / (NCT / NH);     // head of this wave's columns
     T *const Ps = L.Ps[eh];
@@ -271,7 +283,8 @@ __device__ __forceinline__ void linear_walk(
                     const Decays<C> &de = D[step & 1][e];
                     decay_between<T>(de, de.hi[i], de.lo[i], i, 32 * jt + 16 * u + 8 * hf, d[e][u]);
                 }
-            mma_rows<T, DK, 8>(p, Ks + (32 * jt + cn) * PK + 8 * hf, Qs + i * PK + 8 * hf);
+            mma_rows<T, DK, 8>(p, Ks + (32 * jt + rcn) * PK + 8 * hf,
+                               Qs + (32 * it + rn) * PK + 8 * hf);
 #pragma unroll
             for (int e = 0; e < NH; ++e)
 #pragma unroll
@@ -307,7 +320,7 @@ __device__ __forceinline__ void linear_walk(
             // operands of its update
             constexpr int NS = DK / 16, U = NS * OT;
             auto read_q = [&](int s, int t) {
-                const int i = 32 * (t * TW + (IT >= TW ? tw : 0)) + n;
+                const int i = 32 * (t * TW + (IT >= TW ? tw : 0)) + rn;
                 return SHARED ? frag_row(Qs + i * PK + 16 * s + 8 * hf)
                               : frag_row_perm(Qs + i * PK + 16 * s + 4 * hf);
             };

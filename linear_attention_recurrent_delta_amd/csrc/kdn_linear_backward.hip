@@ -24,6 +24,15 @@
 // 32 x 32 tile (channels x tokens) of dq, dk and dv and its tiles of R.  All
 // products are computed transposed, so that a lane ends with runs of 8
 // consecutive channels of a token.
+//
+// Measured (bf16, 128 x 128): B4 H16 T4096 302 us a call: own states of both
+// directions 68-79 us, joins 13, states at the chunks' starts 64-72 (268 MB,
+// 4 TB/s), the walk below 174-197.  It moves 940 MB where 470 are needed.  The
+// walk holds q, k, v, do, P, Y and R of a chunk in 141 KB of LDS, so one
+// workgroup has a CU; its phases (P and Y; dq, dk, dv; R; d log_alpha) follow
+// one another behind barriers, and none of LDS, MFMA and VALU is busy for more
+// than half of the time.  The walk of the chunks' states split into two
+// workgroups of 64 columns each took 71 us for 68.
 #include "kdn_linear_device.h"
 
 namespace kdn {
@@ -90,6 +99,7 @@ __device__ __forceinline__ void grad_walk(const LinearParams &P, const Block &B,
 
     const int tid = threadIdx.x, lane = tid & (WAVE - 1), w = wave_id();
     const int hf = lane >> 5, n = lane & 31, cn = chan(n);
+    const int rn = lds_row(n), rcn = lds_row(cn);   // their places in a tile
     const int qc = w % KT, qt = w / KT;     // channel and token tile of dq and dk
     const int vc = w % VT, vt = w / VT;     // of dv; and column tile and row group of R
     const int hq = h / (P.H / P.Hq), hk = h / (P.H / P.Hk), hv = h / (P.H / P.Hv);
@@ -158,7 +168,7 @@ __device__ __forceinline__ void grad_walk(const LinearParams &P, const Block &B,
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
                 const float f[4] = {R[i][4 * j], R[i][4 * j + 1], R[i][4 * j + 2], R[i][4 * j + 3]};
-                lds_stn<4>(Rs + col * PK + row(i, 4 * j), f);
+                lds_stn<4>(Rs + (32 * vc + rcn) * PK + row(i, 4 * j), f);
             }
     };
     const long hs = (long)DK * DV;
@@ -209,19 +219,20 @@ __device__ __forceinline__ void grad_walk(const LinearParams &P, const Block &B,
                 jt -= ++it;
             const int m = lane & 15, g = lane >> 4;
             const int i = 16 * it + m, j = 16 * jt + 4 * g;
+            const int ri = lds_row(i), rk = 16 * jt + lds_row(m);
             f32x4 p = {0.f, 0.f, 0.f, 0.f}, y = p;
             {
                 FragV<T> a[DK / 32], x[DK / 32];
 #pragma unroll
                 for (int s = 0; s < DK / 32; ++s) {
-                    a[s] = frag_row(Ks + (16 * jt + m) * PK + 32 * s + 8 * g);
-                    x[s] = frag_row(Qs + i * PK + 32 * s + 8 * g);
+                    a[s] = frag_row(Ks + rk * PK + 32 * s + 8 * g);
+                    x[s] = frag_row(Qs + ri * PK + 32 * s + 8 * g);
                 }
                 FragV<T> e[DV / 32], f[DV / 32];
 #pragma unroll
                 for (int s = 0; s < DV / 32; ++s) {
-                    e[s] = frag_row(Vs + (16 * jt + m) * PV + 32 * s + 8 * g);
-                    f[s] = frag_row(Os + i * PV + 32 * s + 8 * g);
+                    e[s] = frag_row(Vs + rk * PV + 32 * s + 8 * g);
+                    f[s] = frag_row(Os + ri * PV + 32 * s + 8 * g);
                 }
                 if (sizeof(T) == 2)
                     __builtin_amdgcn_sched_barrier(0);
@@ -245,8 +256,8 @@ __device__ __forceinline__ void grad_walk(const LinearParams &P, const Block &B,
                 if (m == 15)
                     colx[it][j + r] = x;
             }
-            lds_stn<4>(Ps + i * PP + j, pf);
-            lds_stn<4>(Ys + i * PP + j, yf);
+            lds_stn<4>(Ps + ri * PP + j, pf);
+            lds_stn<4>(Ys + ri * PP + j, yf);
             row += __shfl_xor(row, 16, WAVE);
             row += __shfl_xor(row, 32, WAVE);
             if (g == 0)
@@ -261,7 +272,7 @@ __device__ __forceinline__ void grad_walk(const LinearParams &P, const Block &B,
         constexpr int G = sizeof(T) == 2 && DK + DV < 256 ? 4 : 2;   // registers of 128 x 128
         f32x16 aq = zero16(), ak = zero16(), av = zero16();
         if (qt < IT) {
-            const int i = 32 * qt + n;
+            const int i = 32 * qt + n, ri = 32 * qt + rn;
             const bool want_z = P.dla && qt == 0;
             f32x16 z = zero16();         // S R^T of this wave's channels: its diagonal
 #pragma unroll
@@ -270,8 +281,8 @@ __device__ __forceinline__ void grad_walk(const LinearParams &P, const Block &B,
 #pragma unroll
                 for (int s = 0; s < G; ++s) {
                     rf[s] = frag_cols<PK, true, true>(Rs + 16 * (s0 + s) * PK + 32 * qc, lane);
-                    of[s] = frag_row_perm(Os + i * PV + 16 * (s0 + s) + 4 * hf);
-                    vf[s] = frag_row_perm(Vs + i * PV + 16 * (s0 + s) + 4 * hf);
+                    of[s] = frag_row_perm(Os + ri * PV + 16 * (s0 + s) + 4 * hf);
+                    vf[s] = frag_row_perm(Vs + ri * PV + 16 * (s0 + s) + 4 * hf);
                 }
                 __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
@@ -292,8 +303,8 @@ __device__ __forceinline__ void grad_walk(const LinearParams &P, const Block &B,
 #pragma unroll
                 for (int u = 0; u < 2; ++u) {
                     float qx[8], kx[8];
-                    lds_ld8(Qs + i * PK + 32 * qc + 16 * u + 8 * hf, qx);
-                    lds_ld8(Ks + i * PK + 32 * qc + 16 * u + 8 * hf, kx);
+                    lds_ld8(Qs + ri * PK + 32 * qc + 16 * u + 8 * hf, qx);
+                    lds_ld8(Ks + ri * PK + 32 * qc + 16 * u + 8 * hf, kx);
 #pragma unroll
                     for (int r = 0; r < 8; ++r) {
                         x += aq[8 * u + r] * qx[r];
@@ -327,8 +338,8 @@ __device__ __forceinline__ void grad_walk(const LinearParams &P, const Block &B,
                 FragV<T> rf[G], kf[G];
 #pragma unroll
                 for (int s = 0; s < G; ++s) {
-                    rf[s] = frag_row(Rs + (32 * vc + cn) * PK + 16 * (s0 + s) + 8 * hf);
-                    kf[s] = frag_row(Ks + i * PK + 16 * (s0 + s) + 8 * hf);
+                    rf[s] = frag_row(Rs + (32 * vc + rcn) * PK + 16 * (s0 + s) + 8 * hf);
+                    kf[s] = frag_row(Ks + (32 * vt + rn) * PK + 16 * (s0 + s) + 8 * hf);
                 }
                 __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
@@ -391,7 +402,7 @@ __device__ __forceinline__ void grad_walk(const LinearParams &P, const Block &B,
             for (int s = 0; s < KS; ++s)
                 if (s / 2 <= qt) {      // dq_i: j <= i
                     x[s] = frag_cols<PK, true>(Ks + 16 * s * PK + 32 * qc, lane);
-                    y[s] = frag_row(Ys + (32 * qt + n) * PP + 16 * s + 8 * hf);
+                    y[s] = frag_row(Ys + (32 * qt + rn) * PP + 16 * s + 8 * hf);
                 }
 #pragma unroll
             for (int s = 0; s < KS; ++s)

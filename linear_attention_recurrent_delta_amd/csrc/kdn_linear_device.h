@@ -155,7 +155,16 @@ __device__ __forceinline__ int chan(int n) {
     return 4 * ((q & 4) | ((q & 1) << 1) | ((q >> 1) & 1)) + (n & 3);
 }
 
-// Transposed read of a tile [token][channel]: tokens 8 h + e (PERM: 4 h .. + 3
+// Place of row r of an LDS tile: within each 16 rows the 4 x 4 transpose.  A
+// transposed read takes 4 neighbouring rows, 16 banks of each; at the pitches of
+// lds_pitch rows 4 places apart are the ones that fill the 64 banks (next to
+// each other, half of the read's cycles were conflicts), and 16 neighbouring
+// rows at the same column still fall into 16 different groups of 4.
+__device__ __forceinline__ int lds_row(int r) {
+    return (r & ~15) | ((r & 3) << 2) | ((r >> 2) & 3);
+}
+
+// Transposed read of a tile [token][channel], rows as in lds_row: tokens 8 h + e (PERM: 4 h .. + 3
 // and 8 + 4 h .. + 3) of the 16 behind `m`, channel n of the 32 behind `m` (CH:
 // in the order of chan()).  bfloat16: ds_read_b64_tr_b16 gives lane i of a
 // group of 16 column i of the 4 rows x 16 columns whose 8-byte pieces the
@@ -163,20 +172,20 @@ __device__ __forceinline__ int chan(int n) {
 template <int PITCH, bool CH, bool PERM = false>
 __device__ __forceinline__ bf16x8 frag_cols(const bf16 *m, int lane) {
     const int i = lane & 15, h = lane >> 5, q = 4 * ((lane >> 4) & 1) + (i & 3);
-    const bf16 *p = m + ((PERM ? 4 : 8) * h + (i >> 2)) * PITCH + (CH ? chan(4 * q) : 4 * q);
+    const bf16 *p = m + (4 * (i >> 2) + (PERM ? 1 : 2) * h) * PITCH + (CH ? chan(4 * q) : 4 * q);
     union { s16x4 s[2]; bf16x8 v; } u;
     u.s[0] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4 *)p);
-    u.s[1] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4 *)(p + (PERM ? 8 : 4) * PITCH));
+    u.s[1] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4 *)(p + (PERM ? 2 : 1) * PITCH));
     return u.v;
 }
 template <int PITCH, bool CH, bool PERM = false>
 __device__ __forceinline__ f32x8 frag_cols(const float *m, int lane) {
     const int n = lane & 31, h = lane >> 5;
-    const float *p = m + (PERM ? 4 : 8) * h * PITCH + (CH ? chan(n) : n);
+    const float *p = m + (PERM ? 1 : 2) * h * PITCH + (CH ? chan(n) : n);
     f32x8 f;
 #pragma unroll
     for (int e = 0; e < 8; ++e)
-        f[e] = p[(e + (PERM && e >= 4 ? 4 : 0)) * PITCH];
+        f[e] = p[(4 * (e % 4) + (PERM ? 2 : 1) * (e / 4)) * PITCH];
     return f;
 }
 
@@ -399,11 +408,11 @@ template <typename T> struct GateReg {
     }
 };
 
-// Elements between the rows of an LDS tile of D columns.  Rows n = 0 .. 15 at
-// the same 16 bytes (frag_row) have to fall into different groups of 4 banks
-// (the pitch an odd multiple of 4 of the 64), and 4 rows of 8 banks each
-// (frag_cols) next to each other: 76 and 36 banks for bfloat16 (68 doubled the
-// cycles of every transposed read), one group more than the row for float32.
+// Elements between the rows of an LDS tile of D columns.  16 rows at the same
+// 16 bytes (frag_row) have to fall into different groups of 4 banks (the pitch
+// an odd multiple of 4 of the 64), and the 4 rows of a transposed read, 4 places
+// apart (lds_row), 16 banks from each other: 76 and 36 banks for bfloat16, one
+// group more than the row for float32.
 template <typename T> constexpr int lds_pitch(int d) {
     return sizeof(T) == 4 ? d + 4 : (d == 128 ? 152 : d + 8);
 }
@@ -444,7 +453,7 @@ template <typename T, int ROWS, int COLS, int NT> struct TileRegs {
         const int row = tid / PER_ROW, c = (tid % PER_ROW) * VEC;
 #pragma unroll
         for (int i = 0; i < N; ++i)
-            *reinterpret_cast<f32x4 *>(lds + (row + i * STEP) * PITCH + c) = r[i];
+            *reinterpret_cast<f32x4 *>(lds + lds_row(row + i * STEP) * PITCH + c) = r[i];
     }
 };
 
@@ -452,9 +461,9 @@ template <typename T, int ROWS, int COLS, int NT> struct TileRegs {
 // Join of the blocks along each sequence: block b's own contribution U_b in
 // ws_state becomes the state at its start (REV: in ws_rstate, the reverse
 // state behind its end, blocks last to first).  One thread holds 4 values of S
-// of one (sequence, head); the blocks' values are loaded JOIN ahead.  A
-// sequence of one block has nothing to join, one without tokens passes its
-// state on.
+// of one (sequence, head); the blocks' values are loaded JOIN ahead (B2 H16, 16
+// blocks of 128 x 128: 67 MB in 13 us).  A sequence of one block has nothing to
+// join, one without tokens passes its state on.
 // ---------------------------------------------------------------------------
 constexpr int JOIN = 8, JOIN_NT = 256;
 
@@ -512,7 +521,7 @@ __device__ __forceinline__ void join_blocks(const LinearParams &P, long id, int 
 // Order of a packed batch's blocks in time: the longest first, so that the
 // workgroups that start last are short ones.  Worth it where there are more
 // workgroups than run at once; with very many blocks the differences even out
-// (and one workgroup sorts).  B = 37 sequences of 700 tokens at the mean, bf16,
+// (and one workgroup sorts).  37 sequences of 700 tokens at the mean, bf16,
 // the prefill: H32 of 128 x 64 in blocks of 1664 257 -> 196 us, H16 of 128 x 128
 // in blocks of 832 186 -> 178 us.
 constexpr int ORDER_BINS = 512, ORDER_MAX = 4096;
