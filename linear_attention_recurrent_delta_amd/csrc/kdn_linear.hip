@@ -70,18 +70,19 @@ template <typename T, int DK, int DV, int NH = 1> struct Shape {
 };
 
 // The part of the state of one wave: row tiles t TK .. + TK - 1 of column tile
-// ct (t = w / NCT, ct = w % NCT), column n at channel chan(n).
+// ct (t = w / NCT, ct = w % NCT), rows and columns in the order of chan(): a lane
+// has one column and of each 32 rows twice 8 neighbours.
 template <typename T, int DK, int DV, int NH> struct StateAcc {
     using SH = Shape<T, DK, DV, NH>;
     f32x16 t[SH::TK];
     int row0, col;                             // of this lane
 
     __device__ __forceinline__ StateAcc(int w, int lane) {
-        row0 = w / SH::NCT * SH::TK * 32 + 4 * (lane >> 5);
+        row0 = w / SH::NCT * SH::TK * 32 + 8 * (lane >> 5);
         col = w % SH::NCT * 32 + chan(lane & 31);
     }
     __device__ __forceinline__ int row(int i, int r) const {
-        return row0 + 32 * i + 8 * (r / 4) + r % 4;
+        return row0 + 32 * i + 16 * (r / 8) + r % 8;
     }
     // element (row, col) of the heads' matrices [NH][DK][HD]
     __device__ __forceinline__ int at(int i, int r) const {
@@ -134,9 +135,12 @@ template <typename T, int DK, int DV, int NH> struct StateAcc {
 #pragma unroll
         for (int i = 0; i < SH::TK; ++i)
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const float f[4] = {t[i][4 * j], t[i][4 * j + 1], t[i][4 * j + 2], t[i][4 * j + 3]};
-                lds_stn<4>(Ss + col * pitch + row(i, 4 * j), f);
+            for (int j = 0; j < 2; ++j) {
+                float f[8];
+#pragma unroll
+                for (int r = 0; r < 8; ++r)
+                    f[r] = t[i][8 * j + r];
+                lds_st8(Ss + col * pitch + row(i, 8 * j), f);
             }
     }
 };
@@ -303,7 +307,7 @@ __device__ __forceinline__ void linear_walk(
         const float all = dc.all;
         const float *weight = MODE == ROWN ? dc.in : dc.out;
         auto rows = [&](int s, int i) {
-            return frag_cols<PK, false>(Ks + 16 * s * PK + 32 * (tw * TK + i), lane);
+            return frag_cols<PK, true>(Ks + 16 * s * PK + 32 * (tw * TK + i), lane);
         };
         FragV<T> vf[KS], kf[TK];
         Split<T, PARTS> split;
@@ -321,8 +325,7 @@ __device__ __forceinline__ void linear_walk(
             constexpr int NS = DK / 16, U = NS * OT;
             auto read_q = [&](int s, int t) {
                 const int i = 32 * (t * TW + (IT >= TW ? tw : 0)) + rn;
-                return SHARED ? frag_row(Qs + i * PK + 16 * s + 8 * hf)
-                              : frag_row_perm(Qs + i * PK + 16 * s + 4 * hf);
+                return frag_row(Qs + i * PK + 16 * s + 8 * hf);
             };
             auto read_s = [&](int s) {
                 if constexpr (SHARED)

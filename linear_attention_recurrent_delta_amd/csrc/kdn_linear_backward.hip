@@ -160,15 +160,18 @@ __device__ __forceinline__ void grad_walk(const LinearParams &P, const Block &B,
 
     // R: rows row(i, r), column col of this lane
     f32x16 R[TR];
-    const int col = 32 * vc + cn, row0 = vt * TR * 32 + 4 * hf;
-    auto row = [&](int i, int r) { return row0 + 32 * i + 8 * (r / 4) + r % 4; };
+    const int col = 32 * vc + cn, row0 = vt * TR * 32 + 8 * hf;
+    auto row = [&](int i, int r) { return row0 + 32 * i + 16 * (r / 8) + r % 8; };
     auto share_state = [&]() {
 #pragma unroll
         for (int i = 0; i < TR; ++i)
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const float f[4] = {R[i][4 * j], R[i][4 * j + 1], R[i][4 * j + 2], R[i][4 * j + 3]};
-                lds_stn<4>(Rs + (32 * vc + rcn) * PK + row(i, 4 * j), f);
+            for (int j = 0; j < 2; ++j) {
+                float f[8];
+#pragma unroll
+                for (int r = 0; r < 8; ++r)
+                    f[r] = R[i][8 * j + r];
+                lds_st8(Rs + (32 * vc + rcn) * PK + row(i, 8 * j), f);
             }
     };
     const long hs = (long)DK * DV;
@@ -280,9 +283,9 @@ __device__ __forceinline__ void grad_walk(const LinearParams &P, const Block &B,
                 FragV<T> rf[G], of[G], vf[G];
 #pragma unroll
                 for (int s = 0; s < G; ++s) {
-                    rf[s] = frag_cols<PK, true, true>(Rs + 16 * (s0 + s) * PK + 32 * qc, lane);
-                    of[s] = frag_row_perm(Os + ri * PV + 16 * (s0 + s) + 4 * hf);
-                    vf[s] = frag_row_perm(Vs + ri * PV + 16 * (s0 + s) + 4 * hf);
+                    rf[s] = frag_cols<PK, true>(Rs + 16 * (s0 + s) * PK + 32 * qc, lane);
+                    of[s] = frag_row(Os + ri * PV + 16 * (s0 + s) + 8 * hf);
+                    vf[s] = frag_row(Vs + ri * PV + 16 * (s0 + s) + 8 * hf);
                 }
                 __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
@@ -468,7 +471,7 @@ __device__ __forceinline__ void grad_walk(const LinearParams &P, const Block &B,
         __builtin_amdgcn_sched_barrier(0);
         // R <- all R + q^T (in (.) do)
         auto rows = [&](int s, int i) {
-            return frag_cols<PK, false>(Qs + 16 * s * PK + 32 * (vt * TR + i), lane);
+            return frag_cols<PK, true>(Qs + 16 * s * PK + 32 * (vt * TR + i), lane);
         };
         FragV<T> rq[TR];
         Split<T, PARTS> split;

@@ -125,20 +125,8 @@ __device__ __forceinline__ f32x8 frag_row(const float *p) {
     const f32x4 b = *reinterpret_cast<const f32x4 *>(p + 4);
     return __builtin_shufflevector(a, b, 0, 1, 2, 3, 4, 5, 6, 7);
 }
-// p: this lane's row at 4 h; elements 4 h .. + 3 and 8 + 4 h .. + 3, the order
-// of an accumulator's rows (frag_acc).
-__device__ __forceinline__ bf16x8 frag_row_perm(const bf16 *p) {
-    const bf16x4 a = *reinterpret_cast<const bf16x4 *>(p);
-    const bf16x4 b = *reinterpret_cast<const bf16x4 *>(p + 8);
-    return __builtin_shufflevector(a, b, 0, 1, 2, 3, 4, 5, 6, 7);
-}
-__device__ __forceinline__ f32x8 frag_row_perm(const float *p) {
-    const f32x4 a = *reinterpret_cast<const f32x4 *>(p);
-    const f32x4 b = *reinterpret_cast<const f32x4 *>(p + 8);
-    return __builtin_shufflevector(a, b, 0, 1, 2, 3, 4, 5, 6, 7);
-}
-// Rows 16 b .. + 15 of an accumulator tile as the fragment whose contraction
-// runs over them.
+// Rows 16 b .. + 15 of an accumulator tile, whose row operand was read in the
+// order of chan(), as the fragment whose contraction runs over them.
 template <typename T> __device__ __forceinline__ FragV<T> frag_acc(const f32x16 &a, int b) {
     FragV<T> f;
 #pragma unroll
@@ -164,28 +152,28 @@ __device__ __forceinline__ int lds_row(int r) {
     return (r & ~15) | ((r & 3) << 2) | ((r >> 2) & 3);
 }
 
-// Transposed read of a tile [token][channel], rows as in lds_row: tokens 8 h + e (PERM: 4 h .. + 3
-// and 8 + 4 h .. + 3) of the 16 behind `m`, channel n of the 32 behind `m` (CH:
-// in the order of chan()).  bfloat16: ds_read_b64_tr_b16 gives lane i of a
-// group of 16 column i of the 4 rows x 16 columns whose 8-byte pieces the
-// lanes point to (lane i: row i / 4, columns 4 (i % 4) .. + 3).
-template <int PITCH, bool CH, bool PERM = false>
+// Transposed read of a tile [token][channel], rows as in lds_row: tokens 8 h + e
+// of the 16 behind `m`, channel n of the 32 behind `m` (CH: in the order of
+// chan()).  bfloat16: ds_read_b64_tr_b16 gives lane i of a group of 16 column i
+// of the 4 rows x 16 columns whose 8-byte pieces the lanes point to (lane i: row
+// i / 4, columns 4 (i % 4) .. + 3).
+template <int PITCH, bool CH>
 __device__ __forceinline__ bf16x8 frag_cols(const bf16 *m, int lane) {
     const int i = lane & 15, h = lane >> 5, q = 4 * ((lane >> 4) & 1) + (i & 3);
-    const bf16 *p = m + (4 * (i >> 2) + (PERM ? 1 : 2) * h) * PITCH + (CH ? chan(4 * q) : 4 * q);
+    const bf16 *p = m + (4 * (i >> 2) + 2 * h) * PITCH + (CH ? chan(4 * q) : 4 * q);
     union { s16x4 s[2]; bf16x8 v; } u;
     u.s[0] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4 *)p);
-    u.s[1] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4 *)(p + (PERM ? 2 : 1) * PITCH));
+    u.s[1] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4 *)(p + PITCH));
     return u.v;
 }
-template <int PITCH, bool CH, bool PERM = false>
+template <int PITCH, bool CH>
 __device__ __forceinline__ f32x8 frag_cols(const float *m, int lane) {
     const int n = lane & 31, h = lane >> 5;
-    const float *p = m + (PERM ? 1 : 2) * h * PITCH + (CH ? chan(n) : n);
+    const float *p = m + 2 * h * PITCH + (CH ? chan(n) : n);
     f32x8 f;
 #pragma unroll
     for (int e = 0; e < 8; ++e)
-        f[e] = p[(4 * (e % 4) + (PERM ? 2 : 1) * (e / 4)) * PITCH];
+        f[e] = p[(4 * (e % 4) + e / 4) * PITCH];
     return f;
 }
 
