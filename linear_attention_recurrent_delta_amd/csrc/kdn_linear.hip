@@ -26,12 +26,12 @@
 // every operand twice as often for the same products.
 //
 // Measured (bf16, 128 x 128): B2 H16 T16384 in blocks of 1024, constant decays,
-// 207 us a call (own states 69-88 us, join 13, outputs 127-151: the clock falls
-// in long runs).  It moves 805 MB where 537 are needed (k and v twice), at
-// 3.9 TB/s of the 4.9 that a large copy reaches; what holds it is that a
-// workgroup's LDS reads, splitting and MFMAs (40, 30 and 25 % of the time)
-// follow one another and a CU has two workgroups to overlap.  B1 H16 T190
-// 14.3 us, three chunks one after the other.
+// @@LONG@@ us a call (own states 69-79 us, join 12, outputs 123-140: the clock falls
+// in long runs).  It moves 920 MB where 539 are needed (k and v twice, and the
+// blocks' states).  LDS is busy for 47 % of the outputs' time, VALU 30, MFMA 28:
+// a workgroup's reads, splitting and products follow one another, and a CU has
+// two workgroups to overlap them.  B1 H16 T190 14.3 us, three chunks one after
+// the other.
 #include "kdn_linear_device.h"
 
 namespace kdn {

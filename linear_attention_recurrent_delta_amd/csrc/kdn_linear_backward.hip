@@ -25,14 +25,17 @@
 // products are computed transposed, so that a lane ends with runs of 8
 // consecutive channels of a token.
 //
-// Measured (bf16, 128 x 128): B4 H16 T4096 302 us a call: own states of both
-// directions 68-79 us, joins 13, states at the chunks' starts 64-72 (268 MB,
-// 4 TB/s), the walk below 174-197.  It moves 940 MB where 470 are needed.  The
-// walk holds q, k, v, do, P, Y and R of a chunk in 141 KB of LDS, so one
-// workgroup has a CU; its phases (P and Y; dq, dk, dv; R; d log_alpha) follow
-// one another behind barriers, and none of LDS, MFMA and VALU is busy for more
-// than half of the time.  The walk of the chunks' states split into two
-// workgroups of 64 columns each took 71 us for 68.
+// P, Y, S and R are read rounded to the operand type, once each: bfloat16
+// gradients carry about one such rounding beside their own (dlog_alpha two where
+// <S, R> is most of it); sums over tokens are float32, of log-decays 64 bits.
+//
+// Measured (bf16, 128 x 128): B4 H16 T4096 @@GRAD@@ us a call: own states of both
+// directions 67-76 us, joins 14, states at the chunks' starts 63-69 (290 MB),
+// the walk below 166-187.  It moves 1230 MB where 483 are needed.  The walk holds
+// q, k, v, do, P, Y and R of a chunk in 141 KB of LDS, so one workgroup has a CU;
+// its phases (P and Y; dq, dk, dv; R; d log_alpha) follow one another behind
+// barriers: LDS is busy 42 % of the time, VALU 29, MFMA 18.  The walk of the
+// chunks' states split into two workgroups of 64 columns each took 71 us for 68.
 #include "kdn_linear_device.h"
 
 namespace kdn {
@@ -272,7 +275,8 @@ __device__ __forceinline__ void grad_walk(const LinearParams &P, const Block &B,
         // (sched_barrier: what a phase reads is not read in the phase before,
         // whose registers it would need.)
         __builtin_amdgcn_sched_barrier(0);
-        constexpr int G = sizeof(T) == 2 && DK + DV < 256 ? 4 : 2;   // registers of 128 x 128
+        // as the registers allow
+        constexpr int G = DK + DV < 256 ? (sizeof(T) == 2 ? 4 : 2) : (sizeof(T) == 2 ? 2 : 1);
         f32x16 aq = zero16(), ak = zero16(), av = zero16();
         if (qt < IT) {
             const int i = 32 * qt + n, ri = 32 * qt + rn;
