@@ -29,13 +29,14 @@
 // gradients carry about one such rounding beside their own (dlog_alpha two where
 // <S, R> is most of it); sums over tokens are float32, of log-decays 64 bits.
 //
-// Measured (bf16, 128 x 128): B4 H16 T4096 @@GRAD@@ us a call: own states of both
-// directions 67-76 us, joins 14, states at the chunks' starts 63-69 (290 MB),
-// the walk below 166-187.  It moves 1230 MB where 483 are needed.  The walk holds
-// q, k, v, do, P, Y and R of a chunk in 141 KB of LDS, so one workgroup has a CU;
-// its phases (P and Y; dq, dk, dv; R; d log_alpha) follow one another behind
-// barriers: LDS is busy 42 % of the time, VALU 29, MFMA 18.  The walk of the
-// chunks' states split into two workgroups of 64 columns each took 71 us for 68.
+// Measured (bf16, 128 x 128): B4 H16 T4096 305 us a call: own states of both
+// directions 67-79 us, joins 14, states at the chunks' starts 63-72 (290 MB),
+// the walk below 166-195.  It moves 1231 MB where 483 are needed, at 4.0 TB/s, 82 %
+// of the rate of a large copy.  The walk holds q, k, v, do, P, Y and R of a chunk
+// in 141 KB of LDS, so one workgroup has a CU; its phases (P and Y; dq, dk, dv; R;
+// d log_alpha) follow one another behind barriers: LDS is busy 35 % of the time,
+// VALU 29, MFMA 18.  The walk of the chunks' states split into two workgroups of
+// 64 columns each took 71 us for 68.
 #include "kdn_linear_device.h"
 
 namespace kdn {
