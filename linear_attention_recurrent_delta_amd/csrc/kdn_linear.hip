@@ -576,7 +576,7 @@ hipError_t launch_linear_prefill(const LinearParams &call, hipStream_t st) {
             e = P.bf16 ? lin::launch_prefill_mode<bf16, lin::OWN>(P, st)
                        : lin::launch_prefill_mode<float, lin::OWN>(P, st);
         if (e == hipSuccess) {
-            const int pieces = P.dk * P.dv / (4 * lin::JOIN_NT);
+            const int pieces = lin::join_pieces(P);
             hipLaunchKernelGGL(lin::linear_join_kernel, dim3((unsigned)((long)P.N * P.H * pieces + sort)),
                                dim3(lin::JOIN_NT), 0, st, P, pieces);
             e = hipGetLastError();

@@ -633,7 +633,7 @@ template <typename T> static hipError_t launch_grad(const LinearParams &call, hi
     const bool several = P.block_offsets || P.nblocks != 1;     // blocks in a sequence, or none
     if (several && blocks > 0)
         e = launch_linear_own(P, st);
-    const int pieces = P.dk * P.dv / (4 * TNT);
+    const int pieces = join_pieces(P);
     const long joins = several ? (long)P.N * P.H * pieces : 0;
     const long tail = P.block_offsets && P.tokens > 0 ? TAIL_WGS : 0;
     if (e == hipSuccess && joins + tail + sort > 0) {

@@ -262,6 +262,26 @@ def test_packed_many_blocks(dtype, dv):
     check_packed(*wide, v, la, lengths, slots, keep, o, S, keep, ob)
 
 
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("dk,dv", [(64, 64), (128, 128)])
+def test_packed_many_states(dtype, dk, dv):
+    """So many states that a workgroup joins the whole of one: cut sequences,
+    whole ones, empty ones that pass theirs on, skipped ones."""
+    lengths = [(53 * n) % 190 if n % 6 else 0 for n in range(172)]
+    H, total = 6, sum(lengths) + 3
+    slots = [(5 * n + 3) % 173 for n in range(172)]
+    slots[9] = slots[12] = -1
+    q, k, v, la = make((total,), H, H, H, H, dk, dv, dtype, seed=92)
+    t = kdn.sequence_tables(i32(lengths), total, 64, slots=i32(slots))
+    S0 = state(173, H, dk, dv)
+    S = torch.full_like(S0, 3.0)
+    before = S.clone()
+    o = torch.full(v.shape, 7.0, dtype=dtype, device="cuda")
+    ob = o.clone()
+    kdn.linear_prefill(q, k, v, la, S0=S0, tables=t, out=(o, S))
+    check_packed(q, k, v, la, lengths, slots, S0, o, S, before, ob)
+
+
 def test_packed_thousands_of_blocks():
     """So many blocks that they are taken as they come, the same bits as in a
     batch of their first sequences, which are sorted."""

@@ -185,6 +185,20 @@ def test_packed_many_blocks(dtype):
           list(range(44)))
 
 
+def test_packed_many_states():
+    """So many states that a workgroup joins the whole of one."""
+    lengths, H = [(31 * n) % 140 if n % 7 else 0 for n in range(260)], 4
+    total = sum(lengths)
+    q, k, v, la = make((total,), H, H, H, H, 64, 128, BF, seed=45)
+    do = randn((total, H, 128), BF, 3)
+    S0, dS = state(260, H, 64, 128), state(260, H, 64, 128, seed=2)
+    t = kdn.sequence_tables(i32(lengths), total, 64)
+    got = kdn.linear_prefill_backward(q, k, v, do, la, S0=S0, dS_out=dS, tables=t)
+    ends = torch.tensor(lengths).cumsum(0).tolist()
+    check(q, k, v, la, do, S0, dS, got, [slice(e - n, e) for e, n in zip(ends, lengths)],
+          list(range(260)))
+
+
 def test_wanted_outputs_only():
     """Without d log_alpha and dS0, into given tensors, the same bits."""
     H, T = 2, 300
