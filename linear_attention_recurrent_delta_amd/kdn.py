@@ -667,7 +667,8 @@ def linear_prefill(q, k, v, log_alpha, S0=None, tables=None, out=None, workspace
     if dt not in DTYPES:
         raise ValueError(f"kdn: q has dtype {dt}, expected float32 or bfloat16")
     lead, N, T, pool = _linear_sizes(q, tables, S0, out[1] if out is not None else None)
-    qs, ks, vs = (_rows(n, x, lead, dt, dev) for n, x in (("q", q), ("k", k), ("v", v)))
+    qs, ks = _rows("q", q, lead, dt, dev), _rows("k", k, lead, dt, dev)
+    vs = _rows("v", v, lead, dt, dev)
     H = _linear_heads(q, k, v, log_alpha)
     dk, dv, f32 = q.shape[-1], v.shape[-1], torch.float32
     gate = _gate(log_alpha, lead, H, dt, dev)
@@ -741,7 +742,8 @@ def linear_decode(q, k, v, log_alpha, S, slots=None, o=None, stream=None):
     if q.dim() != 3:
         raise ValueError(f"kdn: q has shape {tuple(q.shape)}, expected [N, heads, d_k]")
     N, lead = q.shape[0], (q.shape[0],)
-    qs, ks, vs = (_rows(n, x, lead, dt, dev) for n, x in (("q", q), ("k", k), ("v", v)))
+    qs, ks = _rows("q", q, lead, dt, dev), _rows("k", k, lead, dt, dev)
+    vs = _rows("v", v, lead, dt, dev)
     H = _linear_heads(q, k, v, log_alpha)
     dk, dv = q.shape[-1], v.shape[-1]
     gate = _gate(log_alpha, lead, H, dt, dev)
@@ -756,8 +758,8 @@ def linear_decode(q, k, v, log_alpha, S, slots=None, o=None, stream=None):
     _same("o", o, (N, H, dv), dt, dev)
     _same("slots", slots, (N,), torch.int32, dev)
     _call(lib.kdn_linear_decode, dev, stream, DTYPES[dt], N, H, q.shape[-2], k.shape[-2],
-          v.shape[-2], dk, dv, gate, qs, ks, vs, _p(q), _p(k), _p(v), _p(log_alpha), _p(slots),
-          pool, _p(S), _p(o))
+          v.shape[-2], dk, dv, gate, qs, ks, vs, q.data_ptr(), k.data_ptr(), v.data_ptr(),
+          log_alpha.data_ptr(), _p(slots), pool, S.data_ptr(), o.data_ptr())
     return o
 
 
