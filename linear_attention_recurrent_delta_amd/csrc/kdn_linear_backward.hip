@@ -37,6 +37,8 @@
 // d log_alpha) follow one another behind barriers: LDS is busy 35 % of the time,
 // VALU 29, MFMA 18.  The walk of the chunks' states split into two workgroups of
 // 64 columns each took 71 us for 68.
+#include <type_traits>
+
 #include "kdn_linear_device.h"
 
 namespace kdn {
@@ -104,7 +106,14 @@ __device__ __forceinline__ void grad_walk(const LinearParams &P, const Block &B,
     const int tid = threadIdx.x, lane = tid & (WAVE - 1), w = wave_id();
     const int hf = lane >> 5, n = lane & 31, cn = chan(n);
     const int rn = lds_row(n), rcn = lds_row(cn);   // their places in a tile
-    const int qc = w % KT, qt = w / KT;     // channel and token tile of dq and dk
+    // channel and token tile of dq and dk; where there are waves for both (float32,
+    // and d_k < d_v), dq and dk have waves of their own, and so has <S, R>
+    constexpr int ROLES = W / KT / IT;
+    constexpr bool APART = ROLES >= 2;
+    const int qc = w % KT, qt = w / KT % IT, role = w / KT / IT;
+    const bool do_q = role == 0, do_k = role == (APART ? 1 : 0);
+    constexpr int ZROLE = ROLES > 2 ? 2 : ROLES - 1;
+    const bool do_z = role == ZROLE && qt == 0;
     const int vc = w % VT, vt = w / VT;     // of dv; and column tile and row group of R
     const int hq = h / (P.H / P.Hq), hk = h / (P.H / P.Hk), hv = h / (P.H / P.Hv);
     // outputs: rows of the shared heads' partials have all H heads
@@ -195,7 +204,7 @@ __device__ __forceinline__ void grad_walk(const LinearParams &P, const Block &B,
         for (int s = 0; s < DV / 16; ++s)
             sf[s] = src[(qc * (DV / 16) + s) * WAVE + lane];
     };
-    if (qt < IT)
+    if (do_q || do_z)
         load_state(nchunk - 1);
     if (w == GW)
         chunk_decays<C>(D[0], gate_value(la0, nchunk - 1), lane);
@@ -279,51 +288,68 @@ __device__ __forceinline__ void grad_walk(const LinearParams &P, const Block &B,
         // as the registers allow
         constexpr int G = DK + DV < 256 ? (sizeof(T) == 2 ? 4 : 2) : (sizeof(T) == 2 ? 2 : 1);
         f32x16 aq = zero16(), ak = zero16(), av = zero16();
-        if (qt < IT) {
+        auto channels = [&](auto dq, auto dk, auto dz) {    // which of them: compile-time
+            constexpr bool Q = decltype(dq)::value, K = decltype(dk)::value, Z = decltype(dz)::value;
             const int i = 32 * qt + n, ri = 32 * qt + rn;
-            const bool want_z = P.dla && qt == 0;
+            const bool want_z = Z && P.dla && do_z;
             f32x16 z = zero16();         // S R^T of this wave's channels: its diagonal
 #pragma unroll
             for (int s0 = 0; s0 < DV / 16; s0 += G) {
                 FragV<T> rf[G], of[G], vf[G];
 #pragma unroll
                 for (int s = 0; s < G; ++s) {
-                    rf[s] = frag_cols<PK, true>(Rs + 16 * (s0 + s) * PK + 32 * qc, lane);
-                    of[s] = frag_row(Os + ri * PV + 16 * (s0 + s) + 8 * hf);
-                    vf[s] = frag_row(Vs + ri * PV + 16 * (s0 + s) + 8 * hf);
+                    if constexpr (K || Z)
+                        rf[s] = frag_cols<PK, true>(Rs + 16 * (s0 + s) * PK + 32 * qc, lane);
+                    if constexpr (Q)
+                        of[s] = frag_row(Os + ri * PV + 16 * (s0 + s) + 8 * hf);
+                    if constexpr (K)
+                        vf[s] = frag_row(Vs + ri * PV + 16 * (s0 + s) + 8 * hf);
                 }
                 __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
                 for (int s = 0; s < G; ++s) {
-                    mma(aq, sf[s0 + s], of[s]);
-                    mma(ak, rf[s], vf[s]);
+                    if constexpr (Q)
+                        mma(aq, sf[s0 + s], of[s]);
+                    if constexpr (K)
+                        mma(ak, rf[s], vf[s]);
                 }
-                if (want_z) {
+                if constexpr (Z)
+                    if (want_z) {
 #pragma unroll
-                    for (int s = 0; s < G; ++s)
-                        mma(z, sf[s0 + s], rf[s]);
-                }
+                        for (int s = 0; s < G; ++s)
+                            mma(z, sf[s0 + s], rf[s]);
+                    }
             }
-            aq *= dc.in[i];
-            ak *= dc.out[i];
+            if constexpr (Q)
+                aq *= dc.in[i];
+            if constexpr (K)
+                ak *= dc.out[i];
             if (P.dla) {
                 float x = 0.f, y = 0.f;
 #pragma unroll
                 for (int u = 0; u < 2; ++u) {
                     float qx[8], kx[8];
-                    lds_ld8(Qs + ri * PK + 32 * qc + 16 * u + 8 * hf, qx);
-                    lds_ld8(Ks + ri * PK + 32 * qc + 16 * u + 8 * hf, kx);
+                    if constexpr (Q)
+                        lds_ld8(Qs + ri * PK + 32 * qc + 16 * u + 8 * hf, qx);
+                    if constexpr (K)
+                        lds_ld8(Ks + ri * PK + 32 * qc + 16 * u + 8 * hf, kx);
 #pragma unroll
                     for (int r = 0; r < 8; ++r) {
-                        x += aq[8 * u + r] * qx[r];
-                        y += ak[8 * u + r] * kx[r];
+                        if constexpr (Q)
+                            x += aq[8 * u + r] * qx[r];
+                        if constexpr (K)
+                            y += ak[8 * u + r] * kx[r];
                     }
                 }
-                x += __shfl_xor(x, 32, WAVE);
-                y += __shfl_xor(y, 32, WAVE);
+                if constexpr (Q)
+                    x += __shfl_xor(x, 32, WAVE);
+                if constexpr (K)
+                    y += __shfl_xor(y, 32, WAVE);
                 if (hf == 0) {
-                    xs[qc][i] = x;
-                    ys[qc][i] = y;
+                    if constexpr (Q)
+                        xs[qc][i] = x;
+                    if constexpr (K)
+                        ys[qc][i] = y;
                 }
                 if (want_z) {
                     float zd = 0.f;
@@ -335,9 +361,22 @@ __device__ __forceinline__ void grad_walk(const LinearParams &P, const Block &B,
                         zs[qc] = zd;
                 }
             }
+        };
+        typedef std::true_type Yes;
+        typedef std::false_type No;
+        if constexpr (!APART) {
+            if (do_q)
+                channels(Yes{}, Yes{}, Yes{});
+        } else {
+            if (do_q)
+                channels(Yes{}, No{}, No{});
+            else if (do_k)
+                channels(No{}, Yes{}, std::bool_constant<ZROLE == 1>{});
+            else if (ZROLE == 2 && do_z)
+                channels(No{}, No{}, Yes{});
         }
         __builtin_amdgcn_sched_barrier(0);
-        if (qt < IT && step + 1 < nchunk)
+        if ((do_q || do_z) && step + 1 < nchunk)
             load_state(c - 1);
         if (vt < IT) {
             const int i = 32 * vt + n;
@@ -404,7 +443,7 @@ __device__ __forceinline__ void grad_walk(const LinearParams &P, const Block &B,
 
         __builtin_amdgcn_sched_barrier(0);
         // what comes from the chunk's own tokens: operands first
-        if (qt < IT) {
+        auto own_q = [&]() {
             FragV<T> x[KS], y[KS];
 #pragma unroll
             for (int s = 0; s < KS; ++s)
@@ -416,7 +455,9 @@ __device__ __forceinline__ void grad_walk(const LinearParams &P, const Block &B,
             for (int s = 0; s < KS; ++s)
                 if (s / 2 <= qt)
                     mma(aq, x[s], y[s]);
-            __builtin_amdgcn_sched_barrier(0);
+        };
+        auto own_k = [&]() {
+            FragV<T> x[KS], y[KS];
 #pragma unroll
             for (int s = 0; s < KS; ++s)
                 if (s / 2 >= qt) {      // dk_j: i >= j
@@ -427,22 +468,32 @@ __device__ __forceinline__ void grad_walk(const LinearParams &P, const Block &B,
             for (int s = 0; s < KS; ++s)
                 if (s / 2 >= qt)
                     mma(ak, x[s], y[s]);
-        }
-        __builtin_amdgcn_sched_barrier(0);
-        if (qt < IT && 32 * qt + n < cnt) {
+        };
+        auto store_channels = [&](const f32x16 &a, void *out, float *part, long at, long pitch) {
+            if (32 * qt + n >= cnt)
+                return;
             const long t0 = (long)c * C + 32 * qt + n;
 #pragma unroll
             for (int u = 0; u < 2; ++u) {
-                const int c0 = 32 * qc + 16 * u + 8 * hf;
-                float x[8], y[8];
+                float x[8];
 #pragma unroll
-                for (int r = 0; r < 8; ++r) {
-                    x[r] = aq[8 * u + r];
-                    y[r] = ak[8 * u + r];
-                }
-                store8<T>(P.dq, P.ws_dq, qat + t0 * qrow + c0, x);
-                store8<T>(P.dk_, P.ws_dk, kat + t0 * krow + c0, y);
+                for (int r = 0; r < 8; ++r)
+                    x[r] = a[8 * u + r];
+                store8<T>(out, part, at + t0 * pitch + 32 * qc + 16 * u + 8 * hf, x);
             }
+        };
+        if (do_q) {
+            own_q();
+            if constexpr (!APART) {
+                __builtin_amdgcn_sched_barrier(0);
+                own_k();
+                __builtin_amdgcn_sched_barrier(0);
+                store_channels(ak, P.dk_, P.ws_dk, kat, krow);
+            }
+            store_channels(aq, P.dq, P.ws_dq, qat, qrow);
+        } else if (APART && do_k) {
+            own_k();
+            store_channels(ak, P.dk_, P.ws_dk, kat, krow);
         }
         __builtin_amdgcn_sched_barrier(0);
         FragV<T> of[KS];
