@@ -499,7 +499,9 @@ kdn_status kdn_linear_decode(kdn_dtype dtype, int N, int H, int Hq, int Hk, int 
  *               sequence are left as they were
  *   workspace   as for kdn_linear_prefill, of at least
  *               kdn_linear_prefill_backward_workspace_size bytes
- * Outputs overlap no input and no other output.
+ * Outputs overlap no input and no other output.  bfloat16 products round
+ * q k^T, do v^T and the states of both directions to bfloat16 once; the states
+ * themselves and dS0 are float32.
  */
 kdn_status kdn_linear_prefill_backward(kdn_dtype dtype, int N, int T, int H, int Hq, int Hk,
                                        int Hv, int d_k, int d_v, kdn_gate gate,

@@ -11,7 +11,8 @@
 namespace kdn {
 
 // Tokens of one chunk of the chunked form: 64 bfloat16 or 32 float32 rows of
-// q, k and v (d = 128) are 48 KB of LDS, so that two workgroups share a CU.
+// q, k and v (d = 128) are 48 KB, 70 KB of LDS with their pitch and P, so that
+// two workgroups share a CU.
 __host__ __device__ constexpr int linear_chunk(bool bf16) { return bf16 ? 64 : 32; }
 
 struct LinearParams {
