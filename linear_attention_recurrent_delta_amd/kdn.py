@@ -663,6 +663,8 @@ def linear_prefill(q, k, v, log_alpha, S0=None, tables=None, out=None, workspace
     S0 itself, updated in place.  Rows of o behind the last sequence are left
     as they were.  Returns (o, S_out)."""
     lib = load()
+    if not isinstance(q, torch.Tensor):
+        raise TypeError("kdn: q must be a tensor")
     dt, dev = q.dtype, q.device
     if dt not in DTYPES:
         raise ValueError(f"kdn: q has dtype {dt}, expected float32 or bfloat16")
@@ -736,6 +738,8 @@ def linear_decode(q, k, v, log_alpha, S, slots=None, o=None, stream=None):
     row's state (None: row n).  A row whose slot is not in the pool is skipped,
     its o left as it was (zero in a new o).  Returns o [N,H,dv]."""
     lib = load()
+    if not isinstance(q, torch.Tensor):
+        raise TypeError("kdn: q must be a tensor")
     dt, dev = q.dtype, q.device
     if dt not in DTYPES:
         raise ValueError(f"kdn: q has dtype {dt}, expected float32 or bfloat16")

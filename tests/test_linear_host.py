@@ -275,3 +275,11 @@ def test_reference_gradients_against_differences():
             up, down = (loss(dict(x, **{n: x[n] + e * way})) for e in (1e-5, -1e-5))
             want = (grads[name] * way).sum().item()
             assert abs((up - down) / 2e-5 - want) <= 1e-7 * (1 + abs(want)) * 10
+
+
+def test_binding_q_must_be_a_tensor():
+    x, la = z(2, 8, 4, 64), z(2, 8, 4)
+    for call in (lambda: kdn.linear_prefill(None, x, x, la), lambda: kdn.linear_decode([1.0], x, x, la, x),
+                 lambda: kdn.linear_prefill_backward(None, x, x, x, la)):
+        with pytest.raises(TypeError, match="q must be"):
+            call()
