@@ -80,7 +80,8 @@ __global__ __launch_bounds__(NT) void tables_kernel(TableParams P, int tok_share
             start[i] = (int)min(at, (long long)P.tokens);
             at += len[i];
             const int stop = (int)min(at, (long long)P.tokens);
-            nb[i] = (stop - start[i] + P.block - 1) / P.block;
+            // (len + block - 1 would pass 32 bits: blocks may be any length)
+            nb[i] = stop > start[i] ? (stop - start[i] - 1) / P.block + 1 : 0;
             bown += nb[i];
         }
         int ball;

@@ -1,0 +1,69 @@
+"""Linear attention and the packed batch's tables on the GPU at the ends of their
+ranges, against the recurrence in 64 bits (tests/linear_ref.py)."""
+import pytest
+import torch
+
+import linear_ref as ref
+from linear_attention_recurrent_delta_amd import kdn
+from test_gpu_linear import BF, F32, check_packed, i32, make, packed_case, state
+from test_gpu_linear_backward import check as check_gradients, randn
+
+pytestmark = pytest.mark.gpu
+NEVER_CUT = 2 ** 31 - 64         # the longest block there is
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _lib():
+    assert torch.cuda.is_available()
+    kdn.ensure_built()
+
+
+# ---------------------------------------------------------------------------
+# Blocks of any length.
+# ---------------------------------------------------------------------------
+def block_tables(lengths, tokens, block):
+    """offsets, block_offsets and blocks in plain Python, for any number of tokens."""
+    offsets, block_offsets, blocks = [0], [0], []
+    for n, length in enumerate(lengths):
+        first = offsets[-1]
+        end = min(first + max(length, 0), tokens)
+        for i, at in enumerate(range(first, end, block)):
+            blocks.append([at, min(block, end - at), n, i])
+        offsets.append(end)
+        block_offsets.append(len(blocks))
+    rows = min(tokens, tokens // block + len(lengths))
+    return offsets, block_offsets, blocks + [[0, 0, -1, 0]] * (rows - len(blocks))
+
+
+@pytest.mark.parametrize("lengths,tokens,block", [
+    ([65], 65, NEVER_CUT), ([64], 64, NEVER_CUT), ([1], 1, NEVER_CUT), ([100, 0, 70, 1, 64], 300, NEVER_CUT),
+    ([2 ** 31 - 1, 5], 1000, NEVER_CUT), ([300] * 4097, 300 * 4097, NEVER_CUT),
+    ([2 ** 31 - 6, 5], 2 ** 31 - 1, NEVER_CUT), ([2 ** 31 - 6, 5], 2 ** 31 - 1, 2 ** 30),
+    ([2 ** 30 + 1, 2 ** 30 - 3], 2 ** 31 - 1, 2 ** 30), ([2 ** 30, 2 ** 30 - 1], 2 ** 31 - 1, 2 ** 20)])
+def test_tables_with_long_blocks(lengths, tokens, block):
+    t = kdn.sequence_tables(i32(lengths), tokens, block)
+    for name, got, want in zip(("offsets", "block_offsets", "blocks"),
+                               (t.offsets, t.block_offsets, t.blocks),
+                               block_tables(lengths, tokens, block)):
+        same = got.tolist() == want          # no diff of long lists
+        assert same, name
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+def test_packed_never_cut(dtype):
+    """Every sequence one block, whatever its length: outputs, states, gradients."""
+    lengths, H, d = [65, 0, 300, 1, 64], 2, 64
+    q, k, v, la, t = packed_case(lengths, 3, H, d, d, dtype, 17, NEVER_CUT)
+    assert t.block_offsets.tolist() == [0, 1, 1, 2, 3, 4]
+    S0 = state(5, H, d, d)
+    S, o = torch.full_like(S0, 3.0), torch.full(v.shape, 7.0, dtype=dtype, device="cuda")
+    before, o_before = S.clone(), o.clone()
+    kdn.linear_prefill(q, k, v, la, S0=S0, tables=t, out=(o, S))
+    check_packed(q, k, v, la, lengths, None, S0, o, S, before, o_before)
+    do, dS = randn(v.shape, dtype, 3), state(5, H, d, d, seed=2)
+    got = kdn.linear_prefill_backward(q, k, v, do, la, S0=S0, dS_out=dS, tables=t)
+    for x in (q, k, v, la, do):
+        x[-3:] = 0
+    ends = torch.tensor(lengths).cumsum(0).tolist()
+    check_gradients(q, k, v, la, do, S0, dS, got, [slice(e - n, e) for e, n in zip(ends, lengths)],
+                    list(range(5)))
