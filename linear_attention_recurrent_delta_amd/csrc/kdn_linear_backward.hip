@@ -127,15 +127,16 @@ __device__ __forceinline__ void grad_walk(const LinearParams &P, const Block &B,
     T *dla = static_cast<T *>(P.gate == KDN_GATE_TOKEN ? P.dla : nullptr);
     if (B.slot < 0) {               // a skipped sequence: zero
         const f32x4 zero = {0.f, 0.f, 0.f, 0.f};
-        for (int i = tid; i < B.count * (DK / 4); i += NT) {
-            const int r = i / (DK / 4), c = i % (DK / 4) * 4;
+        // 64 bits: a block may have 2^26 tokens and more
+        for (long i = tid; i < (long)B.count * (DK / 4); i += NT) {
+            const long r = i / (DK / 4), c = i % (DK / 4) * 4;
             store4<T>(P.dq, P.ws_dq, qat + r * qrow + c, zero);
             store4<T>(P.dk_, P.ws_dk, kat + r * krow + c, zero);
         }
-        for (int i = tid; i < B.count * (DV / 4); i += NT)
+        for (long i = tid; i < (long)B.count * (DV / 4); i += NT)
             store4<T>(P.dv_, P.ws_dv, vat + i / (DV / 4) * vrow + i % (DV / 4) * 4, zero);
         if (dla)
-            for (int i = tid; i < B.count; i += NT)
+            for (long i = tid; i < B.count; i += NT)
                 dla[(B.first + i) * P.H + h] = from_f32<T>(0.f);
         return;
     }

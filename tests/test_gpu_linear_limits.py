@@ -67,3 +67,29 @@ def test_packed_never_cut(dtype):
     ends = torch.tensor(lengths).cumsum(0).tolist()
     check_gradients(q, k, v, la, do, S0, dS, got, [slice(e - n, e) for e, n in zip(ends, lengths)],
                     list(range(5)))
+
+
+def test_gradients_of_a_long_skipped_sequence():
+    """A sequence of 2^26 tokens without a slot has zero gradients (its groups of
+    4 channels pass 2^31); the one behind it has its own."""
+    long, n, dk, dv = 2 ** 26 + 5, 70, 128, 64
+    rows = long + n
+    x = make((n,), 1, 1, 1, 1, dk, dv, BF, seed=5)
+    do, S0 = randn((n, 1, dv), BF, 6), state(1, 1, dk, dv)
+    want = kdn.linear_prefill_backward(
+        x[0], x[0], x[0][..., :dv], do, x[3], S0=S0,
+        tables=kdn.sequence_tables(i32([n]), n, NEVER_CUT, slots=i32([0])))
+    q, la, d = (torch.empty((rows, 1) + s, dtype=BF, device="cuda") for s in ((dk,), (), (dv,)))
+    for big, small in ((q, x[0]), (la, x[3]), (d, do)):
+        big[long:] = small
+    out = {name: torch.full((rows, 1) + s, 7.0, dtype=BF, device="cuda")
+           for name, s in (("dq", (dk,)), ("dk", (dk,)), ("dv", (dv,)), ("dlog_alpha", ()))}
+    out["dS0"] = torch.full_like(S0, 7.0)
+    t = kdn.sequence_tables(i32([long, n]), rows, NEVER_CUT, slots=i32([-1, 0]))
+    kdn.linear_prefill_backward(q, q, q[..., :dv], d, la, S0=S0, tables=t, out=out)
+    for name in ("dq", "dk", "dv", "dlog_alpha"):
+        assert not out[name][:long].any(), name
+        assert torch.equal(out[name][long:], want[name]), name
+    assert torch.equal(out["dS0"], want["dS0"])
+    del q, la, d, out, big
+    torch.cuda.empty_cache()
