@@ -64,7 +64,7 @@ template <typename T, int DK, int DV, int NH = 1> struct Shape {
         __attribute__((aligned(16))) T Qs[MODE == OUT ? C * PK : 1];
         __attribute__((aligned(16))) T Ps[NH][MODE == OUT ? C * PP : 1];
         __attribute__((aligned(16))) T Ss[SHARED ? DV * PK : 1];
-        __attribute__((aligned(16))) Decays<C> D[2][NH];
+        Decays<C> D[2][NH];
     };
 };
 
@@ -303,7 +303,7 @@ __device__ __forceinline__ void linear_walk(
         }
 
         // operands of the state's update, S <- all S + k^T (out (.) v)
-        const float all = dc.all;
+        const float all = dc.all();
         const float *weight = MODE == ROWN ? dc.in : dc.out;
         auto rows = [&](int s, int i) {
             return frag_cols<PK, true>(Ks + 16 * s * PK + 32 * (tw * TK + i), lane);
@@ -474,6 +474,7 @@ __device__ __forceinline__ void linear_block_heads(
 template <typename T, int DK, int DV, int NH, int MODE>
 __global__ __launch_bounds__(NT, 2) void linear_kernel(LinearParams P) {
     __shared__ typename Shape<T, DK, DV, NH>::template Lds<MODE> L;
+    static_assert(sizeof(L) <= 80 * 1024, "two workgroups share a CU");
     linear_block_heads<T, DK, DV, NH, MODE, false>(P, blockIdx.x, L);
 }
 

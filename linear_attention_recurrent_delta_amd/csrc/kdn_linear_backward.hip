@@ -63,7 +63,7 @@ template <typename T, int DK, int DV> struct GradShape {
         __attribute__((aligned(16))) T Ps[C * PP];
         __attribute__((aligned(16))) T Ys[C * PP];
         __attribute__((aligned(16))) T Rs[DV * PK];      // R^T
-        __attribute__((aligned(16))) Decays<C> D[2];
+        Decays<C> D[2];
         // sums of X over a tile's keys, and over a tile's queries
         __attribute__((aligned(16))) float rowx[KS][C], colx[KS][C];
         float xs[KT][C], ys[KT][C], zs[KT];
@@ -433,7 +433,7 @@ __device__ __forceinline__ void grad_walk(const LinearParams &P, const Block &B,
             const double past = prefix_sum((double)u), ally = prefix_sum((double)y);
             float dg = (float)(lane_value(past, WAVE - 1) - past + (double)u +
                                lane_value(ally, WAVE - 1)) +
-                       dc.all * zz;
+                       dc.all() * zz;
             if (log2_decay(la) <= (double)RESET2)
                 dg = 0.f;           // a reset lets nothing past
             if (live) {
@@ -538,7 +538,7 @@ __device__ __forceinline__ void grad_walk(const LinearParams &P, const Block &B,
 #pragma unroll
         for (int i = 0; i < TR; ++i)
             rq[i] = rows(0, i);
-        const float all = dc.all;
+        const float all = dc.all();
 #pragma unroll
         for (int i = 0; i < TR; ++i)
             R[i] *= all;

@@ -278,12 +278,17 @@ __device__ __forceinline__ void mma_rows(f32x16 &acc, const T *a, const T *b) {
 // strong decays.  A log-decay below -152 (base 2) counts as -152, whose power
 // is 0 in float32 as that of -infinity is, so that a reset costs no NaN.
 // ---------------------------------------------------------------------------
-template <int C> struct Decays {
+// Aligned, since it is read 16 bytes at a time and stands in arrays.  Tokens
+// behind the end decay by nothing, so the last one's 2^G_i is 2^G_C.
+template <int C> struct alignas(16) Decays {
     float hi[C], lo[C];   // prefix sum G_i in two floats
     float in[C];          // 2^G_i: from the chunk's start through token i
     float out[C];         // 2^(G_C - G_j): behind token j to the chunk's end
-    float all;            // 2^G_C
+    __device__ __forceinline__ float all() const { return in[C - 1]; }     // 2^G_C
 };
+static_assert(sizeof(Decays<32>) == 4 * 32 * sizeof(float) &&
+                  sizeof(Decays<64>) == 4 * 64 * sizeof(float),
+              "no padding, every element of an array aligned");
 
 constexpr float LOG2E = 1.4426950408889634f;
 constexpr float RESET2 = -152.f;
@@ -333,8 +338,6 @@ __device__ __forceinline__ double chunk_decays(Decays<C> &D, float la, int lane)
         D.lo[lane] = (float)(x - (double)hi);
         D.in[lane] = exp2_fast((float)x);
         D.out[lane] = exp2_fast((float)(all - x));
-        if (lane == 0)
-            D.all = exp2_fast((float)all);
     }
     return all;
 }
