@@ -362,6 +362,10 @@ unsigned long long kdn_chunk_prefill_backward_workspace_size(kdn_variant variant
  *     next (0: contiguous, heads * d), at least heads * d, and whole 16-byte
  *     pieces.  The heads of a token are contiguous.  o is contiguous.  A
  *     token's row of q, k, v (its stride) and of o is less than 64 MiB.
+ *   - A call whose launches would have 2^32 work-items or more is refused
+ *     (KDN_ERR_SHAPE).  None has where sequences times H and blocks times H (a
+ *     dense sequence has one block at least) are below 2^24 - 1 and, for
+ *     gradients, below 2^22 with less than 2^34 values in dq, dk and dv.
  *   - dense batches: N sequences of T tokens, rows n * T + t, state n of S0 and
  *     S_out.  Packed batches (`packed` not NULL): N sequences of any lengths
  *     one behind the other, described by kdn_sequence_tables; T is 0; rows
@@ -442,11 +446,11 @@ int kdn_linear_block(int tokens, int N, int H);
  *               bytes (KDN_ERR_WORKSPACE), 256-byte aligned, overlapping no
  *               other argument; NULL if that size is 0.  Scratch.
  * (tokens = N * T for a dense batch.)  Supported: d_k, d_v in {64, 128};
- * KDN_F32 or KDN_BF16; any N, T, tokens >= 0 with N * T < 2^31.  A prefill of
- * one token per sequence is a decode step with S0 kept; several are the check
- * of draft tokens.  o overlaps no input and not S_out.  bfloat16 products
- * round q k^T and the state they read to bfloat16 once, and keep the state
- * itself to float32.
+ * KDN_F32 or KDN_BF16; any N, T, tokens >= 0 with N * T < 2^31 and
+ * launches as above.  A prefill of one token per sequence is a decode step
+ * with S0 kept; several are the check of draft tokens.  o overlaps no input
+ * and not S_out.  bfloat16 products round q k^T and the state they read to
+ * bfloat16 once, and keep the state itself to float32.
  */
 kdn_status kdn_linear_prefill(kdn_dtype dtype, int N, int T, int H, int Hq, int Hk, int Hv,
                               int d_k, int d_v, kdn_gate gate,

@@ -87,6 +87,18 @@ inline long linear_total_blocks(const LinearParams &P) {
     return P.block_offsets ? (long)P.nblocks : (long)P.N * P.nblocks;
 }
 
+// Two heads of d_v = 64 in a workgroup, where two neighbours have the same q
+// and k and v of their own: q and k are read and q k^T is made once for both,
+// and their columns fill the four waves.  Only where single heads would be
+// more workgroups than run at once (2 a CU), since one alone takes longer for
+// two: B1 H8 T1000 of 128 x 64, bf16, 22 against 19 us; B1 H16 T4000 36
+// against 39; B4 H32 T16384 439 against 489 (float32 38 against 31, 71 against
+// 91, 1450 against 1968).
+inline bool linear_pairs(const LinearParams &P) {
+    return P.H > 0 && P.dv == 64 && P.Hv == P.H && P.H / P.Hq % 2 == 0 && P.H / P.Hk % 2 == 0 &&
+           linear_total_blocks(P) * P.H >= 512;
+}
+
 hipError_t launch_linear_prefill(const LinearParams &P, hipStream_t stream);
 hipError_t launch_linear_decode(const LinearDecodeParams &P, hipStream_t stream);
 hipError_t launch_linear_backward(const LinearParams &P, hipStream_t stream);

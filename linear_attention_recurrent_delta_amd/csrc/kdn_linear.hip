@@ -518,20 +518,9 @@ static hipError_t launch_mode(const LinearParams &P, hipStream_t st) {
     return hipErrorInvalidValue;
 }
 
-// Two heads of d_v = 64 in a workgroup, where two neighbours have the same q
-// and k and v of their own: q and k are read and q k^T is made once for both,
-// and their columns fill the four waves.  Only where single heads would be
-// more workgroups than run at once (2 a CU), since one alone takes longer for
-// two: B1 H8 T1000 of 128 x 64, bf16, 22 against 19 us; B1 H16 T4000 36
-// against 39; B4 H32 T16384 439 against 489 (float32 38 against 31, 71 against
-// 91, 1450 against 1968).
-inline bool pairs(const LinearParams &P) {
-    return P.dv == 64 && P.Hv == P.H && P.H / P.Hq % 2 == 0 && P.H / P.Hk % 2 == 0 &&
-           linear_total_blocks(P) * P.H >= 512;
-}
 template <typename T, int MODE>
 static hipError_t launch_prefill_mode(const LinearParams &P, hipStream_t st) {
-    if (!pairs(P))
+    if (!linear_pairs(P))
         return launch_mode<T, MODE>(P, st);
     const dim3 grid((unsigned)(linear_total_blocks(P) * (P.H / 2))), block(NT);
     if (P.dk == 64)

@@ -82,6 +82,10 @@ kdn_status linear_shape(kdn::LinearParams &P, int dtype, int N, int T, int H, in
     return KDN_OK;
 }
 
+// A launch has less than 2^32 work-items: of more the runtime starts what their
+// low 32 bits say, and reports no error.
+bool launchable(long long workgroups, int threads) { return workgroups * threads < (1LL << 32); }
+
 // Elements between tokens (0: contiguous), or an error.
 kdn_status token_stride(long long given, long long row, long long es, long *out) {
     if (given == 0)
@@ -225,6 +229,11 @@ kdn_status kdn_linear_prefill(kdn_dtype dtype, int N, int T, int H, int Hq, int 
         return KDN_ERR_NULL;
     if (kdn_status st = packed_tables(P, packed))
         return st;
+    // the walks; sequences of several blocks (or none): the joins
+    const bool several = packed || P.nblocks != 1;
+    const long long wgs = kdn::linear_total_blocks(P) * H / (kdn::linear_pairs(P) ? 2 : 1);
+    if (!launchable(wgs, 256) || (several && !launchable((long long)N * H + 1, 256)))
+        return KDN_ERR_SHAPE;
     for (const void *x : {q, k, v, (const void *)S0, (const void *)o, (const void *)S_out})
         if (!aligned(x, 16))
             return KDN_ERR_ALIGN;
@@ -272,9 +281,10 @@ kdn_status kdn_linear_decode(kdn_dtype dtype, int N, int H, int Hq, int Hk, int 
     if (kdn_status st = linear_shape(L, dtype, N, 1, H, Hq, Hk, Hv, d_k, d_v, gate, nullptr,
                                          PREFILL_WGS))
         return st;
-    if (pool < 0 || (!slots && pool < N) || (long long)pool * H >= (1LL << 40))
-        return KDN_ERR_SHAPE;
     const long long es = L.bf16 ? 2 : 4, nh = (long long)N * H;
+    if (pool < 0 || (!slots && pool < N) || (long long)pool * H >= (1LL << 40) ||
+        !launchable(nh, 256))
+        return KDN_ERR_SHAPE;
     if (kdn_status st = token_stride(q_stride, (long long)Hq * d_k, es, &L.q_stride)) return st;
     if (kdn_status st = token_stride(k_stride, (long long)Hk * d_k, es, &L.k_stride)) return st;
     if (kdn_status st = token_stride(v_stride, (long long)Hv * d_v, es, &L.v_stride)) return st;
@@ -379,6 +389,16 @@ kdn_status kdn_linear_prefill_backward(kdn_dtype dtype, int N, int T, int H, int
         return KDN_ERR_NULL;
     if (kdn_status st = packed_tables(P, packed))
         return st;
+    // the walk; sequences of several blocks (or none): the blocks' own states and
+    // the joins, both directions, with the packed tail; the shared heads' sums
+    const long long wgs = kdn::linear_total_blocks(P) * H;
+    const bool several = packed || P.nblocks != 1;
+    const long long shared = tok * ((Hq != H ? (long long)Hq * d_k : 0) +
+                                    (Hk != H ? (long long)Hk * d_k : 0) +
+                                    (Hv != H ? (long long)Hv * d_v : 0)) / 4;
+    if (!launchable(wgs, 4 * (d_k > d_v ? d_k : d_v)) || (several && !launchable(2 * wgs, 256)) ||
+        (several && !launchable(2LL * N * H + 128, 256)) || !launchable(shared / 256 + 1, 256))
+        return KDN_ERR_SHAPE;
     for (const void *x : {q, k, v, (const void *)S0, d_o, (const void *)dS_out, (const void *)dq,
                           (const void *)dk, (const void *)dv, (const void *)dS0})
         if (!aligned(x, 16))

@@ -93,3 +93,33 @@ def test_gradients_of_a_long_skipped_sequence():
     assert torch.equal(out["dS0"], want["dS0"])
     del q, la, d, out, big
     torch.cuda.empty_cache()
+
+
+# ---------------------------------------------------------------------------
+# The largest launches.
+# ---------------------------------------------------------------------------
+def test_largest_launches():
+    """2^24 - 16 workgroups run; of 2^24 and more the runtime would start some
+    only, and they are refused."""
+    H, d = 16, 64
+    for N in (2 ** 20 - 1, 2 ** 20, 2 ** 20 + 64):
+        q = randn((N, 1, 1, d), BF, 4)
+        la = torch.zeros(N, 1, H, dtype=BF, device="cuda")
+        o = torch.full((N, 1, H, d), 7.0, dtype=BF, device="cuda")
+        S = torch.zeros(1, H, d, d, device="cuda")
+        slots = torch.full((N,), -1, dtype=torch.int32, device="cuda")
+        slots[-1] = 0
+        calls = (lambda: kdn.linear_prefill(q, q, q, la, out=(o, None)),
+                 lambda: kdn.linear_decode(q[:, 0], q[:, 0], q[:, 0], la[:, 0], S, slots=slots))
+        if N >= 2 ** 20:
+            for call in calls:
+                with pytest.raises(kdn.KdnError, match="SHAPE"):
+                    call()
+            continue
+        calls[0]()
+        # one token from nothing: o = (q . k) v, with q k^T and o rounded to bf16,
+        # and float32 sums of 64 channels
+        want = q.double().square().sum(-1, keepdim=True) * q.double()
+        near = lambda x, y: ((x.double() - y).abs() <= 2.02 * 2.0 ** -8 * y.abs()).all()
+        assert near(o, want)
+        assert near(calls[1]()[-1], want[-1, 0])

@@ -1,0 +1,52 @@
+"""Sizes at which the linear-attention entry points have to refuse a call, on the
+host (no GPU needed): fake addresses, none of which is ever read."""
+import pytest
+
+from linear_attention_recurrent_delta_amd import kdn
+from test_linear_host import BF16, ESHAPE, F32, backward, decode, packed, prefill
+
+M = 1 << 20
+
+
+@pytest.fixture(scope="module")
+def lib():
+    return kdn.ensure_built()
+
+
+# A launch has less than 2^32 work-items, 2^24 workgroups of 256.
+@pytest.mark.parametrize("kw", [
+    dict(N=16 * M, T=1, H=1, Hq=1, Hk=1, Hv=1), dict(N=M, T=1, H=16, Hq=16, Hk=16, Hv=16),
+    dict(N=M + 64, T=1, H=16, Hq=1, Hk=1, Hv=1), dict(N=2 * M, T=1, H=16, Hq=1, Hk=1, Hv=16),
+    dict(N=M, T=0, H=16, Hq=16, Hk=16, Hv=16), dict(dtype=F32, N=16 * M, T=7, H=1, Hq=1, Hk=1, Hv=1)])
+def test_prefill_past_one_launch(lib, kw):
+    assert prefill(lib, **kw) == ESHAPE
+
+
+def test_packed_prefill_past_one_launch(lib):
+    heads = dict(H=16, Hq=16, Hk=16, Hv=16)
+    assert prefill(lib, N=M, T=0, pk=packed(tokens=64 * M, N=M), **heads) == ESHAPE
+    # few blocks, but a state of each sequence to pass on
+    assert prefill(lib, N=M, T=0, pk=packed(tokens=100, N=M), **heads) == ESHAPE
+
+
+@pytest.mark.parametrize("kw", [
+    dict(N=16 * M, H=1, Hq=1, Hk=1, Hv=1), dict(N=M + 64, H=16, Hq=16, Hk=16, Hv=16)])
+def test_decode_past_one_launch(lib, kw):
+    assert decode(lib, **kw) == ESHAPE
+
+
+@pytest.mark.parametrize("kw", [
+    dict(N=16 * M, T=1, H=1, Hq=1, Hk=1, Hv=1),                              # the walk, 4 waves
+    dict(N=8 * M, T=1, H=1, Hq=1, Hk=1, Hv=1, dk=128),                       # 8 waves
+    dict(N=8 * M, T=0, H=1, Hq=1, Hk=1, Hv=1),                               # the joins
+    dict(N=1, T=90 * M, H=2, Hq=1, Hk=1, Hv=1, dtype=BF16),                  # the shared heads' sums
+])
+def test_gradients_past_one_launch(lib, kw):
+    assert backward(lib, **kw) == ESHAPE
+
+
+def test_no_heads(lib):
+    """No states: nothing to do, in every form."""
+    none = dict(H=0, Hq=0, Hk=0, Hv=0)
+    assert prefill(lib, **none) == 0 and backward(lib, **none) == 0 and decode(lib, **none) == 0
+    assert prefill(lib, N=4, T=0, pk=packed(), **none) == 0
