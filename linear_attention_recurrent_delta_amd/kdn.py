@@ -600,7 +600,6 @@ def sequence_tables(lengths, tokens, block, slots=None, context=None, maps=False
         out = SequenceTables(tokens, block, parts[1], parts[2], parts[0].view(rows, 4), slots,
                              parts[3] if maps else None, parts[4] if maps else None)
     else:
-        out.tokens, out.block, out.slots = tokens, block, slots
         for name, x, shape in (("offsets", out.offsets, (N + 1,)),
                                ("block_offsets", out.block_offsets, (N + 1,)),
                                ("blocks", out.blocks, (rows, 4)),
@@ -610,6 +609,8 @@ def sequence_tables(lengths, tokens, block, slots=None, context=None, maps=False
     _call(lib.kdn_sequence_tables, dev, stream, N, tokens, block, rows, _p(lengths), _p(slots),
           _p(context), _p(out.offsets), _p(out.block_offsets), _p(out.blocks), _p(out.slot_map),
           _p(out.positions))
+    # a refused call leaves `out` describing the tables it holds
+    out.tokens, out.block, out.slots = tokens, block, slots
     return out
 
 

@@ -123,3 +123,17 @@ def test_largest_launches():
         near = lambda x, y: ((x.double() - y).abs() <= 2.02 * 2.0 ** -8 * y.abs()).all()
         assert near(o, want)
         assert near(calls[1]()[-1], want[-1, 0])
+
+
+def test_refused_tables_keep_their_description():
+    lengths, slots = i32([30, 0, 70]), i32([2, 0, 1])
+    t = kdn.sequence_tables(lengths, 100, 64, slots=slots, maps=True)
+    want = [x.clone() for x in (t.offsets, t.block_offsets, t.blocks, t.slot_map, t.positions)]
+    for args in ((i32([1, 2]), 100, 64), (lengths, 300, 64), (lengths, 101, 64)):
+        with pytest.raises(ValueError):
+            kdn.sequence_tables(*args, out=t)
+    assert (t.tokens, t.block) == (100, 64) and t.slots is slots
+    for x, y in zip((t.offsets, t.block_offsets, t.blocks, t.slot_map, t.positions), want):
+        assert torch.equal(x, y)
+    assert kdn.sequence_tables(i32([0, 5, 9]), 100, 64, out=t) is t and t.slots is None
+    assert t.offsets.tolist() == [0, 0, 5, 14]

@@ -1,6 +1,7 @@
 """Sizes at which the linear-attention entry points have to refuse a call, on the
 host (no GPU needed): fake addresses, none of which is ever read."""
 import pytest
+import torch
 
 from linear_attention_recurrent_delta_amd import kdn
 from test_linear_host import BF16, ESHAPE, F32, backward, decode, packed, prefill
@@ -50,3 +51,21 @@ def test_no_heads(lib):
     none = dict(H=0, Hq=0, Hk=0, Hv=0)
     assert prefill(lib, **none) == 0 and backward(lib, **none) == 0 and decode(lib, **none) == 0
     assert prefill(lib, N=4, T=0, pk=packed(), **none) == 0
+
+
+@pytest.mark.parametrize("N,tokens,block", [(4, 10, 64), (3, 200, 64), (3, 10, 128)])
+def test_refused_tables_keep_their_description(lib, monkeypatch, N, tokens, block):
+    """sequence_tables into given tables: what a refused call was to make is not
+    written into them, whether a size does not fit or the call itself fails (the
+    last case: its tensors are not in GPU memory)."""
+    def same(name, x, shape, dtype, dev):
+        if x is not None and x.shape != shape:
+            raise ValueError(name)
+
+    monkeypatch.setattr(kdn, "_same", same)      # host tensors pass, wrong sizes do not
+    i32 = lambda *shape: torch.zeros(shape, dtype=torch.int32)
+    slots = i32(3)
+    t = kdn.SequenceTables(10, 64, i32(4), i32(4), i32(3, 4), slots, i32(10), i32(10))
+    with pytest.raises(ValueError):
+        kdn.sequence_tables(i32(N), tokens, block, slots=i32(N), out=t)
+    assert (t.tokens, t.block) == (10, 64) and t.slots is slots
