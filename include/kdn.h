@@ -383,7 +383,8 @@ unsigned long long kdn_chunk_prefill_backward_workspace_size(kdn_variant variant
  */
 typedef enum kdn_gate {
     KDN_GATE_TOKEN = 0,
-    KDN_GATE_HEAD = 1
+    KDN_GATE_HEAD = 1,
+    KDN_GATE_HEAD_F32 = 2      /* gradients only: KDN_GATE_HEAD, dlog_alpha float32 */
 } kdn_gate;
 
 typedef struct kdn_packed {
@@ -498,7 +499,9 @@ kdn_status kdn_linear_decode(kdn_dtype dtype, int N, int H, int Hq, int Hk, int 
  * head; contiguous):
  *   dq [tokens, Hq, d_k], dk [tokens, Hk, d_k], dv [tokens, Hv, d_v]
  *   dlog_alpha  shaped as log_alpha (KDN_GATE_HEAD: [H], the sum over all
- *               tokens), 0 at a reset; may be NULL (not wanted)
+ *               tokens), 0 at a reset; may be NULL (not wanted).  With
+ *               KDN_GATE_HEAD_F32 it is float32 as log_alpha itself is, the
+ *               sum rounded once (in bfloat16 it keeps 8 bits of it)
  *   dS0         shaped as S0, float32, or NULL (not wanted); states without a
  *               sequence are left as they were
  *   workspace   as for kdn_linear_prefill, of at least

@@ -48,6 +48,7 @@ struct LinearParams {
     const float *dS_out;    // [pool, H, dk, dv], may be null (zero)
     void *dq, *dk_, *dv_;   // contiguous [tokens, heads, d], call dtype
     void *dla;              // [tokens, H] or [H], call dtype, may be null
+    int dla_f32;            // [H] in float32 whatever the call's dtype
     float *dS0;             // may be null
     float *ws_rstate;       // [blocks][H][dk * dv], the reverse recurrence's
     float *ws_rdecay;       // [blocks][H]

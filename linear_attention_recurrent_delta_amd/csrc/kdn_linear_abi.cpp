@@ -359,6 +359,8 @@ GradWs grad_ws(const kdn::LinearParams &P, bool packed) {
 unsigned long long kdn_linear_prefill_backward_workspace_size(
     kdn_dtype dtype, int N, int T, int H, int Hq, int Hk, int Hv, int d_k, int d_v, kdn_gate gate,
     const kdn_packed *packed, kdn_status *status) {
+    if (gate == KDN_GATE_HEAD_F32)
+        gate = KDN_GATE_HEAD;
     kdn::LinearParams P;
     const kdn_status st = linear_shape(P, dtype, N, T, H, Hq, Hk, Hv, d_k, d_v, gate, packed,
                                          GRAD_WGS);
@@ -376,6 +378,9 @@ kdn_status kdn_linear_prefill_backward(kdn_dtype dtype, int N, int T, int H, int
                                        void *dv, void *dlog_alpha, float *dS0,
                                        const kdn_packed *packed, void *workspace,
                                        unsigned long long workspace_bytes, void *stream) {
+    const bool dla_f32 = gate == KDN_GATE_HEAD_F32;
+    if (dla_f32)
+        gate = KDN_GATE_HEAD;
     kdn::LinearParams P;
     if (kdn_status st = linear_shape(P, dtype, N, T, H, Hq, Hk, Hv, d_k, d_v, gate, packed,
                                          GRAD_WGS))
@@ -403,7 +408,8 @@ kdn_status kdn_linear_prefill_backward(kdn_dtype dtype, int N, int T, int H, int
                           (const void *)dk, (const void *)dv, (const void *)dS0})
         if (!aligned(x, 16))
             return KDN_ERR_ALIGN;
-    if (!aligned(log_alpha, gate == KDN_GATE_HEAD ? 4 : es) || !aligned(dlog_alpha, es))
+    if (!aligned(log_alpha, gate == KDN_GATE_HEAD ? 4 : es) ||
+        !aligned(dlog_alpha, dla_f32 ? 4 : es))
         return KDN_ERR_ALIGN;
     const long long n_S = P.pool * H * d_k * d_v * 4;
     const long long n_la = gate == KDN_GATE_HEAD ? 4LL * H : tok * H * es;
@@ -420,7 +426,7 @@ kdn_status kdn_linear_prefill_backward(kdn_dtype dtype, int N, int T, int H, int
     const Range outs[] = {{dq, tok * Hq * d_k * es},
                           {dk, tok * Hk * d_k * es},
                           {dv, tok * Hv * d_v * es},
-                          {dlog_alpha, gate == KDN_GATE_HEAD ? H * es : tok * H * es},
+                          {dlog_alpha, gate == KDN_GATE_HEAD ? H * (dla_f32 ? 4 : es) : tok * H * es},
                           {dS0, n_S}};
     if (clash(outs, 5, ins, 10))
         return KDN_ERR_ALIAS;
@@ -451,7 +457,7 @@ kdn_status kdn_linear_prefill_backward(kdn_dtype dtype, int N, int T, int H, int
     }
     P.q = q; P.k = k; P.v = v; P.la = log_alpha;
     P.S0 = S0; P.d_o = d_o; P.dS_out = dS_out;
-    P.dq = dq; P.dk_ = dk; P.dv_ = dv; P.dla = dlog_alpha; P.dS0 = dS0;
+    P.dq = dq; P.dk_ = dk; P.dv_ = dv; P.dla = dlog_alpha; P.dla_f32 = dla_f32; P.dS0 = dS0;
     const hipError_t e = kdn::launch_linear_backward(P, static_cast<hipStream_t>(stream));
     return e == hipSuccess ? KDN_OK : KDN_ERR_HIP;
 }

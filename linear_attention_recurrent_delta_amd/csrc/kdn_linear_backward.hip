@@ -666,8 +666,12 @@ __global__ __launch_bounds__(WAVE) void linear_gate_sum_kernel(LinearParams P, l
 #pragma unroll
     for (int off = 32; off >= 1; off >>= 1)
         x += __shfl_xor(x, off, WAVE);
-    if (lane == 0)
-        static_cast<T *>(P.dla)[h] = from_f32<T>((float)x);
+    if (lane == 0) {
+        if (P.dla_f32)
+            static_cast<float *>(P.dla)[h] = (float)x;
+        else
+            static_cast<T *>(P.dla)[h] = from_f32<T>((float)x);
+    }
 }
 
 template <typename T>

@@ -36,7 +36,7 @@ STATUS = {0: "KDN_OK", 1: "KDN_ERR_NULL", 2: "KDN_ERR_SHAPE",
           6: "KDN_ERR_HIP", 7: "KDN_ERR_WORKSPACE", 8: "KDN_ERR_SCRATCH"}
 
 # kdn_gate values
-GATE_TOKEN, GATE_HEAD = 0, 1
+GATE_TOKEN, GATE_HEAD, GATE_HEAD_F32 = 0, 1, 2
 
 
 class Packed(ctypes.Structure):
@@ -776,8 +776,10 @@ def linear_prefill_backward(q, k, v, d_o, log_alpha, S0=None, dS_out=None, table
     decay per head) in q's dtype, and dS0 float32.  A head that several states
     share gets the sum of their gradients; rows behind the last sequence of a
     packed batch get zero, and so do states of dS0 without a sequence.  ``out``
-    may pass such a dict (dlog_alpha and dS0 may be None: not wanted; in a
-    given dS0 states without a sequence are left as they were).
+    may pass such a dict (dlog_alpha and dS0 may be None: not wanted; a given
+    dlog_alpha [H] may be float32 as log_alpha [H] is, which keeps all bits of
+    the sum in a bf16 call; in a given dS0 states without a sequence are left
+    as they were).
     ``workspace``: a uint8 tensor of at least the queried size, or None to
     allocate one.  A packed batch without any of S0, dS_out and out["dS0"] has
     no pool: dS0 is by sequence and slots are not looked at."""
@@ -798,20 +800,23 @@ def linear_prefill_backward(q, k, v, d_o, log_alpha, S0=None, dS_out=None, table
     if tables is not None:
         pk, N = _packed(tables, pool, dev)
         pool = N if pool is None else pool
-    la_shape = (H,) if gate == GATE_HEAD else lead + (H,)
+    la_shape, la_dt = (H,) if gate == GATE_HEAD else lead + (H,), dt
     s_shape = (pool, H, dk, dv)
     if out is None:
         new = lambda *shape: _new(shape, dt, dev, stream)
         out = dict(dq=new(*lead, Hq, dk), dk=new(*lead, Hk, dk), dv=new(*lead, Hv, dv),
                    dlog_alpha=new(*la_shape),
                    dS0=_new(s_shape, f32, dev, stream, zero=tables is not None))
+    elif gate == GATE_HEAD and isinstance(out["dlog_alpha"], torch.Tensor) \
+            and out["dlog_alpha"].dtype is f32:
+        gate, la_dt = GATE_HEAD_F32, f32
     if k.shape[-1] != dk:
         _same("k", k, lead + (Hk, dk), dt, dev)
     for name, x, shape, t in (("d_o", d_o, lead + (H, dv), dt), ("S0", S0, s_shape, f32),
                               ("dS_out", dS_out, s_shape, f32), ("dq", out["dq"], lead + (Hq, dk), dt),
                               ("dk", out["dk"], lead + (Hk, dk), dt),
                               ("dv", out["dv"], lead + (Hv, dv), dt),
-                              ("dlog_alpha", out["dlog_alpha"], la_shape, dt),
+                              ("dlog_alpha", out["dlog_alpha"], la_shape, la_dt),
                               ("dS0", out["dS0"], s_shape, f32)):
         _same(name, x, shape, t, dev)
     if workspace is None:

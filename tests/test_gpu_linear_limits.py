@@ -137,3 +137,31 @@ def test_refused_tables_keep_their_description():
         assert torch.equal(x, y)
     assert kdn.sequence_tables(i32([0, 5, 9]), 100, 64, out=t) is t and t.slots is None
     assert t.offsets.tolist() == [0, 0, 5, 14]
+
+
+# ---------------------------------------------------------------------------
+# The gradient of one decay per head in float32.
+# ---------------------------------------------------------------------------
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("cut", [False, True])
+def test_float32_gate_gradient(dtype, cut):
+    """The same sum rounded once to float32: its bf16 rounding is what the call's
+    type gives, and the sum itself has more bits."""
+    H, d = 5, 64
+    q, k, v, la = make((2, 500 if cut else 90), H, H, H, H, d, d, dtype, "head", seed=6)
+    do, S0 = randn(v.shape, dtype, 3), state(2, H, d, d)
+    want = kdn.linear_prefill_backward(q, k, v, do, la, S0=S0)
+    out = {n: torch.full_like(x, 7.0) for n, x in want.items()}
+    out["dlog_alpha"] = torch.full((H,), 7.0, device="cuda")
+    got = kdn.linear_prefill_backward(q, k, v, do, la, S0=S0, out=out)
+    assert got["dlog_alpha"] is out["dlog_alpha"] and want["dlog_alpha"].dtype == dtype
+    assert torch.equal(got["dlog_alpha"].to(dtype), want["dlog_alpha"])
+    if dtype == BF:
+        assert (got["dlog_alpha"] != want["dlog_alpha"].float()).any()
+    for n in ("dq", "dk", "dv", "dS0"):
+        assert torch.equal(got[n], want[n]), n
+    B, T = q.shape[:2]
+    flat = lambda x: x.flatten(0, 1)
+    check_gradients(flat(q), flat(k), flat(v), la, flat(do), S0, None,
+                    {n: x if n in ("dlog_alpha", "dS0") else flat(x) for n, x in got.items()},
+                    [slice(b * T, b * T + T) for b in range(B)], list(range(B)))

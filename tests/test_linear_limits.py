@@ -4,7 +4,8 @@ import pytest
 import torch
 
 from linear_attention_recurrent_delta_amd import kdn
-from test_linear_host import BF16, ESHAPE, F32, backward, decode, packed, prefill
+from test_linear_host import (A, BF16, EALIAS, EALIGN, ESHAPE, EUNSUP, EWS, F32, MB, backward, decode,
+                              packed, prefill)
 
 M = 1 << 20
 
@@ -69,3 +70,23 @@ def test_refused_tables_keep_their_description(lib, monkeypatch, N, tokens, bloc
     with pytest.raises(ValueError):
         kdn.sequence_tables(i32(N), tokens, block, slots=i32(N), out=t)
     assert (t.tokens, t.block) == (10, 64) and t.slots is slots
+
+
+# ---------------------------------------------------------------------------
+# The gradient of one decay per head in float32.
+# ---------------------------------------------------------------------------
+@pytest.mark.parametrize("kw,want", [
+    (dict(gate=3), EUNSUP), (dict(gate=2, dla=A + 13 * MB + 2), EALIGN),
+    (dict(gate=2, la=A + 3 * MB + 2), EALIGN),
+    # 4 heads: 8 bytes in bfloat16, 16 in float32
+    (dict(gate=1, dla=A + 14 * MB - 8, wsb=0), EWS), (dict(gate=2, dla=A + 14 * MB - 16, wsb=0), EWS),
+    (dict(gate=2, dla=A + 14 * MB - 8, wsb=0), EALIAS)])
+def test_float32_gate_gradient_refusals(lib, kw, want):
+    assert backward(lib, **kw) == want
+
+
+def test_float32_gate_gradient_sizes_and_forward(lib):
+    size = lambda gate: lib.kdn_linear_prefill_backward_workspace_size(
+        BF16, 2, 300, 4, 4, 2, 4, 64, 64, gate, None, None)
+    assert size(kdn.GATE_HEAD_F32) == size(kdn.GATE_HEAD) > size(kdn.GATE_TOKEN)
+    assert prefill(lib, gate=kdn.GATE_HEAD_F32) == EUNSUP and decode(lib, gate=kdn.GATE_HEAD_F32) == EUNSUP
