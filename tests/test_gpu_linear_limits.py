@@ -4,6 +4,7 @@ import pytest
 import torch
 
 import linear_ref as ref
+import linear_tight as tight
 from linear_attention_recurrent_delta_amd import kdn
 from test_gpu_linear import BF, F32, check_packed, i32, make, packed_case, state
 from test_gpu_linear_backward import check as check_gradients, randn
@@ -165,3 +166,92 @@ def test_float32_gate_gradient(dtype, cut):
     check_gradients(flat(q), flat(k), flat(v), la, flat(do), S0, None,
                     {n: x if n in ("dlog_alpha", "dS0") else flat(x) for n, x in got.items()},
                     [slice(b * T, b * T + T) for b in range(B)], list(range(B)))
+
+
+# ---------------------------------------------------------------------------
+# Returned states are float32.
+# ---------------------------------------------------------------------------
+@pytest.mark.parametrize("size", range(len(tight.SIZES)))
+@pytest.mark.parametrize("dk,dv", [(64, 64), (64, 128), (128, 64), (128, 128)])
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("shared", [False, True])
+def test_returned_states_keep_24_bits(size, dk, dv, dtype, shared):
+    T, live, block, chunks, blocks = tight.SIZES[size]
+    if dtype == F32:
+        chunks = sum(-(-min(block, T - at) // 32) for at in range(0, T, block))
+    H = 4
+    x = tight.case(T, live, H, dk, dv, dtype, seed=size)
+    if shared:                         # neighbours with the same q and k
+        for y in x[:2]:
+            y[:] = y[:, :1]
+    S, M, R, MR = tight.wanted(*x)
+    q, k, v, la, do, S0, dS = (y.cuda() for y in x)
+    N = 1
+    if shared:                         # as many as make them share a workgroup
+        q, k, N = q[:, :1], k[:, :1], 130
+    q, k, v, la, do = (y.repeat(N, *[1] * (y.dim() - 1)) for y in (q, k, v, la, do))
+    S0, dS = S0.repeat(N, 1, 1, 1), dS.repeat(N, 1, 1, 1)
+    t = kdn.sequence_tables(i32([T] * N), N * T, block)
+    assert t.block_offsets[:2].tolist() == [0, blocks]
+    got = kdn.linear_prefill(q, k, v, la, S0=S0.clone(), tables=t)[1]
+    ref.close("S", got[0], S, tight.bound(M, len(live), chunks, blocks))
+    assert (got == got[0]).all()
+    got = kdn.linear_prefill_backward(q, k, v, do, la, S0=S0, dS_out=dS, tables=t)["dS0"]
+    ref.close("dS0", got[0], R, tight.bound(MR, len(live), chunks, blocks))
+    assert (got == got[0]).all()
+
+
+# ---------------------------------------------------------------------------
+# Packed batches with one decay per head, in a workspace that holds anything.
+# ---------------------------------------------------------------------------
+def junk(n):
+    """A workspace whose floats are all NaN."""
+    return torch.full((n,), 255, dtype=torch.uint8, device="cuda")
+
+
+@pytest.mark.parametrize("lengths", [[1], [5, 0, 64, 1, 129, 0], [300, 2, 500, 65], [0, 0, 700, 0],
+                                     [(23 * n * n + 5 * n) % 211 for n in range(44)]],
+                         ids=lambda x: f"{len(x)}x{sum(x)}")
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("block", [64, 256])
+@pytest.mark.parametrize("Hk", [2, 1])
+def test_packed_constant_decays(lengths, dtype, block, Hk):
+    """Empty sequences, skipped ones and rows behind the last: none adds to the
+    decays' gradient, and nothing is read from the workspace that was not
+    written."""
+    N, H, d, tail = len(lengths), 2, 64, 3
+    P, total = N + 3, sum(lengths) + tail
+    slots = [P - 1 - n for n in range(N)]
+    if N > 3:
+        slots[1], slots[3] = -1, P
+    q, k, v, la = make((total,), H, Hk, H, H, d, d, dtype, "head", seed=N)
+    do = randn(v.shape, dtype, 3)
+    for x in (q, k, v, do):
+        x[total - tail:] = float("nan")
+    ends = torch.tensor(lengths).cumsum(0).tolist()
+    spans = [slice(e - n, e) for e, n in zip(ends, lengths)]
+    if N > 3:
+        q[spans[1]] = float("nan")
+    S0, dS = state(P, H, d, d), state(P, H, d, d, seed=2)
+    t = kdn.sequence_tables(i32(lengths), total, block, slots=i32(slots))
+    pk, _ = kdn._packed(t, P, q.device)
+    lib, kind = kdn.load(), kdn.DTYPES[dtype]
+
+    S, o = S0.clone(), torch.full(v.shape, 7.0, dtype=dtype, device="cuda")
+    o_before = o.clone()
+    ws = junk(lib.kdn_linear_prefill_workspace_size(kind, N, 0, H, d, d, pk, None))
+    kdn.linear_prefill(q, k, v, la, S0=S, tables=t, out=(o, S), workspace=ws)
+    wide = [x.repeat_interleave(H // x.shape[1], 1) for x in (q, k)]
+    check_packed(*wide, v, la.expand(total, H), lengths, slots, S0, o, S, S0, o_before)
+
+    ws = junk(lib.kdn_linear_prefill_backward_workspace_size(kind, N, 0, H, H, Hk, H, d, d,
+                                                             kdn.GATE_HEAD, pk, None))
+    got = kdn.linear_prefill_backward(q, k, v, do, la, S0=S0, dS_out=dS, tables=t, workspace=ws)
+    for x in (q, k, v, do):
+        x[total - tail:] = 0
+    if N > 3:
+        q[spans[1]] = 0
+    live = [s if 0 <= s < P else -1 for s in slots]
+    check_gradients(q, k, v, la, do, S0, dS, got, spans, live)
+    for p in set(range(P)) - set(live):
+        assert not got["dS0"][p].any()

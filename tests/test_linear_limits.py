@@ -3,6 +3,7 @@ host (no GPU needed): fake addresses, none of which is ever read."""
 import pytest
 import torch
 
+import linear_tight as tight
 from linear_attention_recurrent_delta_amd import kdn
 from test_linear_host import (A, BF16, EALIAS, EALIGN, ESHAPE, EUNSUP, EWS, F32, MB, backward, decode,
                               packed, prefill)
@@ -90,3 +91,16 @@ def test_float32_gate_gradient_sizes_and_forward(lib):
         BF16, 2, 300, 4, 4, 2, 4, 64, 64, gate, None, None)
     assert size(kdn.GATE_HEAD_F32) == size(kdn.GATE_HEAD) > size(kdn.GATE_TOKEN)
     assert prefill(lib, gate=kdn.GATE_HEAD_F32) == EUNSUP and decode(lib, gate=kdn.GATE_HEAD_F32) == EUNSUP
+
+
+@pytest.mark.parametrize("size", range(len(tight.SIZES)))
+def test_bound_of_returned_states_tells_two_parts_from_three(size):
+    """What test_gpu_linear_limits.py holds returned states to: three parts are
+    inside, two are not, in either direction."""
+    T, live, _, chunks, blocks = tight.SIZES[size]
+    x = tight.case(T, live, 4, 64, 128, torch.bfloat16, seed=size)
+    S, M, R, MR = tight.wanted(*x)
+    for parts in (2, 3):
+        for got, want, m in zip(tight.planted(*x, parts), (S, R), (M, MR)):
+            inside = ((got - want).abs() <= tight.bound(m, len(live), chunks, blocks)).all()
+            assert inside == (parts == 3)
