@@ -63,8 +63,9 @@ __global__ __launch_bounds__(NT) void tables_kernel(TableParams P, int tok_share
     const long r0 = (long)blockIdx.x * row_share, r1 = min(r0 + row_share, (long)P.max_blocks);
     long long sum = 0;               // tokens and blocks before the tile
     int end = 0, blk = 0;
-    for (int n0 = 0; n0 < P.N; n0 += TILE) {
-        const int m = min(TILE, P.N - n0);
+    // by what is left: N + TILE may pass 32 bits
+    for (int left = P.N; left > 0; left -= TILE) {
+        const int n0 = P.N - left, m = min(TILE, left);
         long long len[PER], own = 0;
 #pragma unroll
         for (int i = 0; i < PER; ++i) {

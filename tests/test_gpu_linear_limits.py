@@ -255,3 +255,27 @@ def test_packed_constant_decays(lengths, dtype, block, Hk):
     check_gradients(q, k, v, la, do, S0, dS, got, spans, live)
     for p in set(range(P)) - set(live):
         assert not got["dS0"][p].any()
+
+
+def test_tables_of_the_most_sequences():
+    """2^31 - 1 sequences: the tiles of the scan end at the last one (a 32-bit
+    counter of them would pass 2^31 and start again before the first)."""
+    N, tokens = 2 ** 31 - 1, 1000
+    live = {5: 70, 4096: 1, N - 4097: 64, N - 4095: 130, N - 2: 3}
+    lengths = torch.zeros(N, dtype=torch.int32, device="cuda")
+    for n, length in live.items():
+        lengths[n] = length
+    t = kdn.sequence_tables(lengths, tokens, 64, maps=True)
+    at, blocks = 0, []
+    for n, length in live.items():
+        assert t.offsets[n].item() == at and t.block_offsets[n].item() == len(blocks)
+        assert (t.slot_map[at:at + length] == n).all()
+        assert t.positions[at:at + length].tolist() == list(range(length))
+        blocks += [[at + i, min(64, length - i), n, i // 64] for i in range(0, length, 64)]
+        at += length
+        assert t.offsets[n + 1].item() == at and t.block_offsets[n + 1].item() == len(blocks)
+    assert t.offsets[N].item() == at and t.block_offsets[N].item() == len(blocks)
+    assert t.blocks[:len(blocks)].tolist() == blocks
+    assert (t.blocks[len(blocks):] == i32([0, 0, -1, 0])).all() and (t.slot_map[at:] == -1).all()
+    del t, lengths
+    torch.cuda.empty_cache()
