@@ -562,10 +562,18 @@ def _linear_heads(q, k, v, log_alpha):
     return H
 
 
+def _int32(name, x):
+    """x as an int the library can take (ctypes would pass its low 32 bits)."""
+    x = int(x)
+    if not -2 ** 31 <= x < 2 ** 31:
+        raise KdnError(2, f"{name} {x} does not fit 32 bits")
+    return x
+
+
 def linear_block(tokens, N, H):
     """Tokens of a block for :func:`sequence_tables` of N sequences with
     ``tokens`` rows in all and H states each."""
-    n = int(load().kdn_linear_block(int(tokens), int(N), int(H)))
+    n = int(load().kdn_linear_block(_int32("tokens", tokens), _int32("N", N), _int32("H", H)))
     if n < 0:
         raise KdnError(2, kdn_status_string(2))
     return n
@@ -583,8 +591,8 @@ def sequence_tables(lengths, tokens, block, slots=None, context=None, maps=False
     lib = load()
     if not isinstance(lengths, torch.Tensor) or lengths.dim() != 1:
         raise ValueError("kdn: lengths must be a tensor [N]")
-    N, dev, i32 = lengths.shape[0], lengths.device, torch.int32
-    tokens, block = int(tokens), int(block)
+    N, dev, i32 = _int32("N", lengths.shape[0]), lengths.device, torch.int32
+    tokens, block = _int32("tokens", tokens), _int32("block", block)
     rows = lib.kdn_sequence_max_blocks(N, tokens, block)
     if rows < 0:
         raise KdnError(2, f"tokens {tokens} must not be negative, block {block} a positive "

@@ -104,3 +104,15 @@ def test_bound_of_returned_states_tells_two_parts_from_three(size):
         for got, want, m in zip(tight.planted(*x, parts), (S, R), (M, MR)):
             inside = ((got - want).abs() <= tight.bound(m, len(live), chunks, blocks)).all()
             assert inside == (parts == 3)
+
+
+@pytest.mark.parametrize("x", [2 ** 32 + 64, 2 ** 31, -2 ** 32 + 64])
+def test_sizes_of_more_than_32_bits(lib, x):
+    """The library takes 32-bit sizes: what does not fit is refused, not cut off."""
+    lengths = torch.zeros(3, dtype=torch.int32)
+    for call in (lambda: kdn.sequence_tables(lengths, x, 64), lambda: kdn.sequence_tables(lengths, 64, x),
+                 lambda: kdn.linear_block(x, 3, 4), lambda: kdn.linear_block(64, x, 4),
+                 lambda: kdn.linear_block(64, 3, x),
+                 lambda: kdn.sequence_tables(lengths[:1].expand(abs(x)), 64, 64)):
+        with pytest.raises(kdn.KdnError, match="SHAPE"):
+            call()
