@@ -508,7 +508,9 @@ kdn_status kdn_linear_decode(kdn_dtype dtype, int N, int H, int Hq, int Hk, int 
  *               kdn_linear_prefill_backward_workspace_size bytes
  * Outputs overlap no input and no other output.  bfloat16 products round
  * q k^T, do v^T and the states of both directions to bfloat16 once; the states
- * themselves and dS0 are float32.
+ * themselves and dS0 are float32.  The sum over tokens of one decay per head,
+ * and dlog_alpha of dense sequences of up to 64 tokens, have the states to 16
+ * bits.
  */
 kdn_status kdn_linear_prefill_backward(kdn_dtype dtype, int N, int T, int H, int Hq, int Hk,
                                        int Hv, int d_k, int d_v, kdn_gate gate,

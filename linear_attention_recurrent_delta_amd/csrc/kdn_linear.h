@@ -54,6 +54,8 @@ struct LinearParams {
     float *ws_rdecay;       // [blocks][H]
     void *ws_chunk;         // [chunk slots][H][dk * dv] state at every chunk's start,
                             // call dtype, in fragment order (chunk_slot)
+    void *ws_chunk_lo;      // what the rounding of ws_chunk leaves, the same way, for
+                            // d log_alpha (null: not wanted)
     float *ws_dq, *ws_dk, *ws_dv;   // [tokens, H, d] of shared heads (else null)
     double *ws_dla;         // [blocks][H] sums of d log_alpha (one decay per head)
 };

@@ -119,8 +119,9 @@ template <typename T, int DK, int DV, int NH> struct StateAcc {
                 S[at(i, r)] = t[i][r];
     }
     // operand fragments [column tile][16 rows][lane], rounded to T: the
-    // products that read them round the same state in the prefill
-    __device__ __forceinline__ void store_frags(T *S, int w, int lane) const {
+    // products that read them round the same state in the prefill.  `rest`: what
+    // the rounding leaves, where wanted.
+    __device__ __forceinline__ void store_frags(T *S, T *rest, int w, int lane) const {
         const int first = (w % SH::NCT * (DK / 32) + w / SH::NCT * SH::TK) * 2;
 #pragma unroll
         for (int i = 0; i < SH::TK; ++i)
@@ -128,6 +129,14 @@ template <typename T, int DK, int DV, int NH> struct StateAcc {
             for (int b = 0; b < 2; ++b)
                 reinterpret_cast<FragV<T> *>(S)[(first + 2 * i + b) * WAVE + lane] =
                     frag_acc<T>(t[i], b);
+        if (sizeof(T) == 2 && rest) {
+#pragma unroll
+            for (int i = 0; i < SH::TK; ++i)
+#pragma unroll
+                for (int b = 0; b < 2; ++b)
+                    reinterpret_cast<FragV<T> *>(rest)[(first + 2 * i + b) * WAVE + lane] =
+                        frag_rest<T>(t[i], b);
+        }
     }
     // to LDS, transposed [DV][pitch], in the operand type
     __device__ __forceinline__ void share(T *Ss, int pitch) const {
@@ -267,10 +276,11 @@ __device__ __forceinline__ void linear_walk(
         if (MODE != OUT)                // OUT: later, its registers are taken here
             load_kv(chunk(step + 1), 0, 1);
 
-        if (MODE == CHUNKS)
-            S.store_frags(static_cast<T *>(P.ws_chunk) +
-                              (chunk_slot(b, B.first, c, C) * P.H + h) * (long)(DK * HD),
-                          w, lane);
+        if (MODE == CHUNKS) {
+            const long at = (chunk_slot(b, B.first, c, C) * P.H + h) * (long)(DK * HD);
+            T *const rest = static_cast<T *>(P.ws_chunk_lo);
+            S.store_frags(static_cast<T *>(P.ws_chunk) + at, rest ? rest + at : nullptr, w, lane);
+        }
 
         if (MODE == OUT && w < IT * (IT + 1) / 2) {
             // tiles of P^T on and below the diagonal: lane n has query

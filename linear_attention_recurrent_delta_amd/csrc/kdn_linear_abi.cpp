@@ -319,10 +319,18 @@ kdn_status kdn_linear_decode(kdn_dtype dtype, int N, int H, int Hq, int Hk, int 
 namespace {
 // Workspace, sections 256-byte aligned: the forward and the reverse states at
 // the blocks' ends with the blocks' decays (sequences of several blocks; a
-// packed batch's order behind the decays), the state at every chunk's start, float32 gradients of
-// shared heads before their sum, and for one decay per head each block's sum.
+// packed batch's order behind the decays), the state at every chunk's start
+// (where `fine`: what its rounding leaves, too), float32 gradients of shared
+// heads before their sum, and for one decay per head each block's sum.
+//
+// fine: d log_alpha of a bfloat16 call beyond its operands' rounding, for the sum
+// over tokens of one decay per head and for dense sequences of one chunk
+// (kdn_linear_backward.hip).
+bool fine(const kdn::LinearParams &P, bool packed) {
+    return P.bf16 && (P.gate == KDN_GATE_HEAD || (!packed && P.T <= kdn::linear_chunk(true)));
+}
 struct GradWs {
-    long long state, decay, rstate, rdecay, chunk, dq, dk, dv, dla, total;
+    long long state, decay, rstate, rdecay, chunk, chunk_lo, dq, dk, dv, dla, total;
 };
 GradWs grad_ws(const kdn::LinearParams &P, bool packed) {
     GradWs w{};
@@ -342,7 +350,11 @@ GradWs grad_ws(const kdn::LinearParams &P, bool packed) {
         w.rstate = take(blocks * P.H * n_S * 4);
         w.rdecay = take(blocks * P.H * 4);
     }
-    w.chunk = take(kdn::chunk_slots(P.tokens, blocks, kdn::linear_chunk(P.bf16)) * P.H * n_S * es);
+    const long long n_chunk =
+        kdn::chunk_slots(P.tokens, blocks, kdn::linear_chunk(P.bf16)) * P.H * n_S * es;
+    w.chunk = take(n_chunk);
+    if (fine(P, packed))
+        w.chunk_lo = take(n_chunk);
     if (P.Hq != P.H)
         w.dq = take(P.tokens * P.H * P.dk * 4);
     if (P.Hk != P.H)
@@ -450,6 +462,9 @@ kdn_status kdn_linear_prefill_backward(kdn_dtype dtype, int N, int T, int H, int
                 P.ws_order = reinterpret_cast<int *>(P.ws_decay + (long)P.nblocks * H);
         }
         P.ws_chunk = base + w.chunk;
+        // without states a single chunk has neither x nor y nor z
+        if (w.chunk_lo && dlog_alpha && (gate == KDN_GATE_HEAD || S0 || dS_out))
+            P.ws_chunk_lo = base + w.chunk_lo;
         P.ws_dq = Hq != H ? f32(w.dq) : nullptr;
         P.ws_dk = Hk != H ? f32(w.dk) : nullptr;
         P.ws_dv = Hv != H ? f32(w.dv) : nullptr;

@@ -26,8 +26,21 @@
 // consecutive channels of a token.
 //
 // P, Y, S and R are read rounded to the operand type, once each: bfloat16
-// gradients carry about one such rounding beside their own (dlog_alpha two where
-// <S, R> is most of it); sums over tokens are float32, of log-decays 64 bits.
+// gradients carry about one such rounding beside their own; sums over tokens are
+// float32, of log-decays 64 bits.
+//
+// With one decay per head the sum of d log_alpha over all tokens cancels while
+// these roundings add up (B3 H3 T186 with states: 1.2e-2 of the sum, computed in
+// float32 7e-4, its own rounding).  FINE keeps both out of it: what the rounding
+// of S leaves is saved beside it and multiplied too, what that of R leaves is
+// multiplied from the accumulators (x and y to 2^-16 of a term), and <S, R> is a
+// product only at the block's last chunk: from there on it is the sum of the x
+// and y that it passes, exact enough for a sum over all tokens, not for a token's
+// own value where later ones are far larger.  B4 H16 T4096 of 128 x 128 388 us
+// against 320 with decays per token, B2 H16 T4096 of 64 x 64 94 against 87.
+// Sequences of one chunk with states take it with decays per token as well: of
+// few tokens x, y and z are most of d log_alpha, there is no sum over chunks, and
+// the errors were up to twice those of a sum in float32.
 //
 // Measured (bf16, 128 x 128): B4 H16 T4096 305 us a call: own states of both
 // directions 67-79 us, joins 14, states at the chunks' starts 63-72 (290 MB),
@@ -45,7 +58,8 @@
 namespace kdn {
 namespace lin {
 
-template <typename T, int DK, int DV> struct GradShape {
+// FINE: what the roundings of S and R leave goes into d log_alpha.
+template <typename T, int DK, int DV, bool FINE = false> struct GradShape {
     static constexpr int C = linear_chunk(sizeof(T) == 2);
     static constexpr int W = (DK > DV ? DK : DV) / 16;     // waves
     static constexpr int NT = W * WAVE;
@@ -67,6 +81,8 @@ template <typename T, int DK, int DV> struct GradShape {
         // sums of X over a tile's keys, and over a tile's queries
         __attribute__((aligned(16))) float rowx[KS][C], colx[KS][C];
         float xs[KT][C], ys[KT][C], zs[KT];
+        float ylo[FINE ? W : 1][C];         // a wave's part of y from the rest of R
+        double flow[FINE ? W : 1];          // and of <S, R> at the block's last chunk
     };
 };
 
@@ -89,10 +105,10 @@ __device__ __forceinline__ void store4(void *out, float *part, long at, f32x4 x)
 }
 
 // PARTS: of the split operands in the update of R (Split).
-template <typename T, int DK, int DV, int PARTS>
+template <typename T, int DK, int DV, int PARTS, bool FINE>
 __device__ __forceinline__ void grad_walk(const LinearParams &P, const Block &B, long b, int h,
-                                          typename GradShape<T, DK, DV>::Lds &L) {
-    using SH = GradShape<T, DK, DV>;
+                                          typename GradShape<T, DK, DV, FINE>::Lds &L) {
+    using SH = GradShape<T, DK, DV, FINE>;
     constexpr int C = SH::C, W = SH::W, NT = SH::NT, TR = SH::TR, KT = SH::KT, VT = SH::VT;
     constexpr int IT = SH::IT, KS = SH::KS, PK = SH::PK, PV = SH::PV, PP = SH::PP;
 
@@ -199,15 +215,38 @@ __device__ __forceinline__ void grad_walk(const LinearParams &P, const Block &B,
         for (int r = 0; r < 16; ++r)
             R[i][r] = rstart ? rstart[row(i, r) * DV + col] : 0.f;
     FragV<T> sf[DV / 16];           // rows of S of this wave, a chunk ahead
-    auto load_state = [&](int c) {
-        const FragV<T> *src = reinterpret_cast<const FragV<T> *>(
-            static_cast<const T *>(P.ws_chunk) + (chunk_slot(b, B.first, c, C) * P.H + h) * hs);
+    auto state_of = [&](const void *ws, int c) {
+        return reinterpret_cast<const FragV<T> *>(
+            static_cast<const T *>(ws) + (chunk_slot(b, B.first, c, C) * P.H + h) * hs);
+    };
+    auto load_state = [&](const void *ws, int c) {
+        const FragV<T> *src = state_of(ws, c);
 #pragma unroll
         for (int s = 0; s < DV / 16; ++s)
             sf[s] = src[(qc * (DV / 16) + s) * WAVE + lane];
     };
-    if (do_q || do_z)
-        load_state(nchunk - 1);
+    if (do_q || (do_z && !FINE))
+        load_state(P.ws_chunk, nchunk - 1);
+    if constexpr (FINE) {
+        // <S, R> of the block's last chunk, R as it is and S in both its parts:
+        // a piece is 8 neighbours of a row of S
+        float z = 0.f;
+        if (rstart) {
+            const FragV<T> *hi = state_of(P.ws_chunk, nchunk - 1);
+            const FragV<T> *lo = state_of(P.ws_chunk_lo, nchunk - 1);
+            for (int i = tid; i < DK * DV / 8; i += NT) {
+                const int l = i % WAVE, s = i / WAVE % (DV / 16), t = i / WAVE / (DV / 16);
+                const float *r = rstart + (32 * t + chan(l & 31)) * DV + 16 * s + 8 * (l >> 5);
+                const FragV<T> x = hi[i], y = lo[i];
+#pragma unroll
+                for (int e = 0; e < 8; ++e)
+                    z += (to_f32(x[e]) + to_f32(y[e])) * r[e];
+            }
+        }
+        z = wave_sum(z);
+        if (lane == 0)
+            L.flow[w] = z;
+    }
     if (w == GW)
         chunk_decays<C>(D[0], gate_value(la0, nchunk - 1), lane);
     share_state();
@@ -217,6 +256,7 @@ __device__ __forceinline__ void grad_walk(const LinearParams &P, const Block &B,
         Ys[i] = from_f32<T>(0.f);
     }
     double gsum = 0.;               // wave GW: sum of the block's d log_alpha (this lane's)
+    double flow = 0.;               // FINE: <S, R> between two chunks
 
     for (int step = 0; step < nchunk; ++step) {
         const int c = nchunk - 1 - step;
@@ -368,18 +408,21 @@ __device__ __forceinline__ void grad_walk(const LinearParams &P, const Block &B,
         typedef std::false_type No;
         if constexpr (!APART) {
             if (do_q)
-                channels(Yes{}, Yes{}, Yes{});
+                channels(Yes{}, Yes{}, std::bool_constant<!FINE>{});
         } else {
             if (do_q)
                 channels(Yes{}, No{}, No{});
             else if (do_k)
-                channels(No{}, Yes{}, std::bool_constant<ZROLE == 1>{});
-            else if (ZROLE == 2 && do_z)
+                channels(No{}, Yes{}, std::bool_constant<ZROLE == 1 && !FINE>{});
+            else if (ZROLE == 2 && do_z && !FINE)
                 channels(No{}, No{}, Yes{});
         }
         __builtin_amdgcn_sched_barrier(0);
-        if ((do_q || do_z) && step + 1 < nchunk)
-            load_state(c - 1);
+        if constexpr (FINE) {
+            if (do_q)
+                load_state(P.ws_chunk_lo, c);
+        } else if ((do_q || do_z) && step + 1 < nchunk)
+            load_state(P.ws_chunk, c - 1);
         if (vt < IT) {
             const int i = 32 * vt + n;
 #pragma unroll
@@ -397,6 +440,56 @@ __device__ __forceinline__ void grad_walk(const LinearParams &P, const Block &B,
             }
             av *= dc.out[i];
         }
+        if constexpr (FINE) {
+            // what the roundings of R and S leave of y and x: this wave's tiles of
+            // R, as they are in its registers, on all tokens (y_j = v_j . R^T k_j),
+            // and the rest of its channels of S
+            __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+            for (int it = 0; it < IT; ++it) {
+                const int i = 32 * it + n, ri = 32 * it + rn;
+                f32x16 a = zero16();
+#pragma unroll
+                for (int s = 0; s < 2 * TR; ++s)
+                    mma(a, frag_rest<T>(R[s / 2], s % 2),
+                        frag_row(Ks + ri * PK + 32 * vt * TR + 16 * s + 8 * hf));
+                float y = 0.f;
+#pragma unroll
+                for (int u = 0; u < 2; ++u) {
+                    float vx[8];
+                    lds_ld8(Vs + ri * PV + 32 * vc + 16 * u + 8 * hf, vx);
+#pragma unroll
+                    for (int r = 0; r < 8; ++r)
+                        y += a[8 * u + r] * vx[r];
+                }
+                y += __shfl_xor(y, 32, WAVE);
+                if (hf == 0)
+                    L.ylo[w][i] = y * dc.out[i];
+                __builtin_amdgcn_sched_barrier(0);
+            }
+            if (do_q) {
+                const int i = 32 * qt + n, ri = 32 * qt + rn;
+                f32x16 a = zero16();
+#pragma unroll
+                for (int s = 0; s < DV / 16; ++s)
+                    mma(a, sf[s], frag_row(Os + ri * PV + 16 * s + 8 * hf));
+                float x = 0.f;
+#pragma unroll
+                for (int u = 0; u < 2; ++u) {
+                    float qx[8];
+                    lds_ld8(Qs + ri * PK + 32 * qc + 16 * u + 8 * hf, qx);
+#pragma unroll
+                    for (int r = 0; r < 8; ++r)
+                        x += a[8 * u + r] * qx[r];
+                }
+                x += __shfl_xor(x, 32, WAVE);
+                if (hf == 0)
+                    xs[qc][i] += x * dc.in[i];      // which this lane wrote
+                __builtin_amdgcn_sched_barrier(0);
+                if (step + 1 < nchunk)
+                    load_state(P.ws_chunk, c - 1);
+            }
+        }
         const float la = gate_value(la0, c);      // wave GW: this chunk's log-decays
         if (w == GW) {
             if (step + 1 < nchunk)
@@ -412,7 +505,7 @@ __device__ __forceinline__ void grad_walk(const LinearParams &P, const Block &B,
             int tok = lane;
             asm volatile("" : "+v"(tok));
             const bool live = tok < C && tok < cnt;
-            float u = 0.f, y = 0.f, zz = 0.f;
+            float u = 0.f, x = 0.f, y = 0.f, zz = 0.f;
             if (tok < C) {
                 const int t = tok / 16;
 #pragma unroll
@@ -420,25 +513,47 @@ __device__ __forceinline__ void grad_walk(const LinearParams &P, const Block &B,
                     u += (j <= t ? rowx[j][tok] : 0.f) - (j >= t ? colx[j][tok] : 0.f);
 #pragma unroll
                 for (int i = 0; i < KT; ++i) {
-                    u += xs[i][tok];
+                    x += xs[i][tok];
                     y += ys[i][tok];
                 }
+                if constexpr (FINE)
+#pragma unroll
+                    for (int i = 0; i < W; ++i)
+                        y += L.ylo[i][tok];
+                u += x;
                 u -= y;
             }
+            if (!FINE) {
 #pragma unroll
-            for (int i = 0; i < KT; ++i)
-                zz += zs[i];
+                for (int i = 0; i < KT; ++i)
+                    zz += zs[i];
+            }
             // with u = row - col + x - y: sum_{i >= s} (u_i + y_i) + sum_{j < s} y_j
             // is all of y and what of u is not before s
-            const double past = prefix_sum((double)u), ally = prefix_sum((double)y);
-            float dg = (float)(lane_value(past, WAVE - 1) - past + (double)u +
-                               lane_value(ally, WAVE - 1)) +
-                       dc.all() * zz;
+            const double past = prefix_sum((double)u);
+            const double ally = lane_value(prefix_sum((double)y), WAVE - 1);
+            double dg = lane_value(past, WAVE - 1) - past + (double)u + ally;
+            if constexpr (FINE) {
+                // <S, R> at the chunk's end is z and all of y, at its start z and all
+                // of x: only the last chunk's is a product
+                double z = flow - ally;
+                if (step == 0) {
+                    z = 0.;
+#pragma unroll
+                    for (int i = 0; i < W; ++i)
+                        z += L.flow[i];
+                    z *= (double)dc.all();
+                }
+                flow = z + lane_value(prefix_sum((double)x), WAVE - 1);
+                dg += z;
+            } else {
+                dg = (float)dg + dc.all() * zz;
+            }
             if (log2_decay(la) <= (double)RESET2)
-                dg = 0.f;           // a reset lets nothing past
+                dg = 0.;            // a reset lets nothing past
             if (live) {
                 if (dla)
-                    dla[(B.first + (long)c * C + tok) * P.H + h] = from_f32<T>(dg);
+                    dla[(B.first + (long)c * C + tok) * P.H + h] = from_f32<T>((float)dg);
                 gsum += dg;
             }
         }
@@ -566,7 +681,7 @@ __device__ __forceinline__ void grad_walk(const LinearParams &P, const Block &B,
     }
 }
 
-template <typename T, int DK, int DV>
+template <typename T, int DK, int DV, bool FINE>
 __global__ __launch_bounds__((GradShape<T, DK, DV>::NT)) void linear_grad_kernel(LinearParams P) {
     const long b = block_at(P, blockIdx.x / P.H);
     const int h = blockIdx.x % P.H;
@@ -575,12 +690,12 @@ __global__ __launch_bounds__((GradShape<T, DK, DV>::NT)) void linear_grad_kernel
         P.ws_dla[b * P.H + h] = 0.;
     if (B.count == 0)
         return;
-    __shared__ typename GradShape<T, DK, DV>::Lds L;
+    __shared__ typename GradShape<T, DK, DV, FINE>::Lds L;
     // three parts where R ends as dS0
     if (B.index == 0)
-        grad_walk<T, DK, DV, 3>(P, B, b, h, L);
+        grad_walk<T, DK, DV, 3, FINE>(P, B, b, h, L);
     else
-        grad_walk<T, DK, DV, 2>(P, B, b, h, L);
+        grad_walk<T, DK, DV, 2, FINE>(P, B, b, h, L);
 }
 
 // Joins of the forward and of the reverse states, zero gradients for the rows
@@ -703,15 +818,25 @@ template <typename T> static hipError_t launch_grad(const LinearParams &call, hi
         e = launch_linear_chunk_states(P, st);
     if (e == hipSuccess && blocks > 0) {
         const dim3 grid((unsigned)(blocks * P.H));
+        auto walk = [&](auto fine) {
 #define KDN_LGRAD(DK_, DV_)                                                                  \
-        if (P.dk == DK_ && P.dv == DV_)                                                      \
-            hipLaunchKernelGGL((linear_grad_kernel<T, DK_, DV_>), grid,                      \
-                               dim3(GradShape<T, DK_, DV_>::NT), 0, st, P);
-        KDN_LGRAD(64, 64)
-        KDN_LGRAD(64, 128)
-        KDN_LGRAD(128, 64)
-        KDN_LGRAD(128, 128)
+            if (P.dk == DK_ && P.dv == DV_)                                                  \
+                hipLaunchKernelGGL((linear_grad_kernel<T, DK_, DV_, decltype(fine)::value>), \
+                                   grid, dim3(GradShape<T, DK_, DV_>::NT), 0, st, P);
+            KDN_LGRAD(64, 64)
+            KDN_LGRAD(64, 128)
+            KDN_LGRAD(128, 64)
+            KDN_LGRAD(128, 128)
 #undef KDN_LGRAD
+        };
+        if constexpr (sizeof(T) == 2) {
+            if (P.ws_chunk_lo)
+                walk(std::true_type{});
+            else
+                walk(std::false_type{});
+        } else {
+            walk(std::false_type{});
+        }
         e = hipGetLastError();
     }
     const Share<T> q = share<T>(P, P.ws_dq, P.dq, P.Hq, P.dk);

@@ -135,6 +135,15 @@ template <typename T> __device__ __forceinline__ FragV<T> frag_acc(const f32x16 
     return f;
 }
 
+// What that rounding leaves, to T.
+template <typename T> __device__ __forceinline__ FragV<T> frag_rest(const f32x16 &a, int b) {
+    FragV<T> f;
+#pragma unroll
+    for (int e = 0; e < 8; ++e)
+        f[e] = from_f32<T>(a[8 * b + e] - to_f32(from_f32<T>(a[8 * b + e])));
+    return f;
+}
+
 // Channel of row or column n of a 32-channel tile.  The middle bits of the
 // groups of 4 change places, so that accumulator registers 0-7 and 8-15 of a
 // lane are 8 consecutive channels each, from 8 h and 16 + 8 h.

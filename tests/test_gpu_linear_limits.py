@@ -279,3 +279,63 @@ def test_tables_of_the_most_sequences():
     assert (t.blocks[len(blocks):] == i32([0, 0, -1, 0])).all() and (t.slot_map[at:] == -1).all()
     del t, lengths
     torch.cuda.empty_cache()
+
+
+# ---------------------------------------------------------------------------
+# d log_alpha beyond the rounding of its operands.
+# ---------------------------------------------------------------------------
+def flow_call(x, dk, dv, block, per_head):
+    q, k, v, la, do, S0, dS = (y.cuda() for y in x)
+    T, H = do.shape[:2]
+    out = dict(dq=torch.empty_like(q), dk=torch.empty_like(k), dv=torch.empty_like(v),
+               dlog_alpha=torch.full_like(la, 7.0), dS0=torch.empty_like(S0)[None])
+    rows, tables = [q, k, v, do], None
+    if block:
+        tables = kdn.sequence_tables(i32([T]), T, block)
+    else:
+        rows = [y[None] for y in rows]
+        for n in ("dq", "dk", "dv") if per_head else ("dq", "dk", "dv", "dlog_alpha"):
+            out[n] = out[n][None]
+        la = la if per_head else la[None]
+    kdn.linear_prefill_backward(*rows, la, S0=S0[None], dS_out=dS[None], tables=tables, out=out)
+    return out["dlog_alpha"] if per_head or block else out["dlog_alpha"][0]
+
+
+def flow_wanted(x):
+    q, k, v, la, do, S0, dS = x
+    T, H = q.shape[:2]
+    a = torch.exp(la.double()).expand(T, H)
+    w, m = ref.backward(*(y.double() for y in (q, k, v)), a, do.double(), S0.double(), dS.double())
+    return w["dlog_alpha"], tight.flow_bound(w["dlog_alpha"], m, q, k)
+
+
+@pytest.mark.parametrize("dk,dv", [(64, 64), (64, 128), (128, 64), (128, 128)])
+@pytest.mark.parametrize("T,block", [(1, 0), (40, 0), (64, 0), (200, 0), (300, 0), (150, 64), (300, 512)])
+def test_sum_over_tokens_is_not_of_rounded_states(dk, dv, T, block):
+    """One decay per head, dense (one block or several) and packed."""
+    x = tight.flow_case(T, 8, dk, dv, True, seed=T)
+    w, bound = flow_wanted(x)
+    got = flow_call(x, dk, dv, block, True)
+    ref.close("dlog_alpha", got, w.sum(0), 2.0 ** -24 * w.sum(0).abs() + bound.sum(0))
+
+
+@pytest.mark.parametrize("dk,dv", [(64, 64), (64, 128), (128, 64), (128, 128)])
+@pytest.mark.parametrize("T", [1, 2, 40, 64])
+def test_flows_of_one_chunk_are_not_of_rounded_states(dk, dv, T):
+    """Decays per token, sequences of one chunk: the values' own rounding, 2^-8."""
+    x = tight.flow_case(T, 8, dk, dv, False, seed=T)
+    w, bound = flow_wanted(x)
+    ref.close("dlog_alpha", flow_call(x, dk, dv, 0, False), w, 2.0 ** -8 * w.abs() + 1.01 * bound)
+
+
+@pytest.mark.parametrize("dk,dv", [(64, 64), (64, 128), (128, 64), (128, 128)])
+@pytest.mark.parametrize("T,block", [(1, 0), (50, 0), (186, 0), (300, 0), (300, 128)])
+def test_sum_over_tokens_of_any_inputs(dk, dv, T, block):
+    """All channels live, sums that cancel: the same bound, over absolute values."""
+    H = 3
+    q, k, v, la = make((T,), H, H, H, H, dk, dv, BF, "head", seed=T)
+    x = (q, k, v, la, randn(v.shape, BF, 3), state(1, H, dk, dv)[0], 0.2 * state(1, H, dk, dv, seed=2)[0])
+    x = [y.cpu() for y in x]
+    w, bound = flow_wanted(x)
+    got = flow_call(x, dk, dv, block, True)
+    ref.close("dlog_alpha", got, w.sum(0), 2.0 ** -24 * w.sum(0).abs() + bound.sum(0))

@@ -3,6 +3,7 @@ host (no GPU needed): fake addresses, none of which is ever read."""
 import pytest
 import torch
 
+import linear_ref as ref
 import linear_tight as tight
 from linear_attention_recurrent_delta_amd import kdn
 from test_linear_host import (A, BF16, EALIAS, EALIGN, ESHAPE, EUNSUP, EWS, F32, MB, backward, decode,
@@ -116,3 +117,22 @@ def test_sizes_of_more_than_32_bits(lib, x):
                  lambda: kdn.sequence_tables(lengths[:1].expand(abs(x)), 64, 64)):
         with pytest.raises(kdn.KdnError, match="SHAPE"):
             call()
+
+
+@pytest.mark.parametrize("T,per_head", [(1, True), (40, True), (300, True), (1, False), (40, False)])
+def test_bound_of_flows_tells_one_part_from_two(T, per_head):
+    """What test_gpu_linear_limits.py holds d log_alpha to, as a sum over tokens or
+    a token's own: two bf16 parts of the states are inside, one is not."""
+    x = tight.flow_case(T, 8, 64, 128, per_head, seed=T)
+    q, k, v, la, do, S0, dS = x
+    a = torch.exp(la.double()).expand(T, 8)
+    w, m = ref.backward(*(y.double() for y in (q, k, v)), a, do.double(), S0.double(), dS.double())
+    bound = tight.flow_bound(w["dlog_alpha"], m, q, k)
+    assert (tight.flow_in_parts(*x, 8) - w["dlog_alpha"]).abs().max() <= 1e-12 * m["dlog_alpha"].max()
+    for parts in (1, 2):
+        off = tight.flow_in_parts(*x, parts) - w["dlog_alpha"]
+        if per_head:
+            assert (off.sum(0).abs() <= bound.sum(0)).all() == (parts == 2)
+            assert (off.sum(0).abs() > bound.sum(0)).all() == (parts == 1)
+        else:
+            assert (off.abs() <= bound).all() == (parts == 2)
