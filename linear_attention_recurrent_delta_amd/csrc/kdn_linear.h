@@ -11,8 +11,9 @@
 namespace kdn {
 
 // Tokens of one chunk of the chunked form: 64 bfloat16 or 32 float32 rows of
-// q, k and v (d = 128) are 48 KB, 70 KB of LDS with their pitch and P, so that
-// two workgroups share a CU.
+// q, k and v (d = 128) are 48 KB, 68 or 55 KB of LDS with their pitch and P, at
+// most 80 KB where the state passes through LDS too (d_v = 64), so that two
+// workgroups share a CU.
 __host__ __device__ constexpr int linear_chunk(bool bf16) { return bf16 ? 64 : 32; }
 
 struct LinearParams {
@@ -94,9 +95,9 @@ inline long linear_total_blocks(const LinearParams &P) {
 // and k and v of their own: q and k are read and q k^T is made once for both,
 // and their columns fill the four waves.  Only where single heads would be
 // more workgroups than run at once (2 a CU), since one alone takes longer for
-// two: B1 H8 T1000 of 128 x 64, bf16, 22 against 19 us; B1 H16 T4000 36
-// against 39; B4 H32 T16384 439 against 489 (float32 38 against 31, 71 against
-// 91, 1450 against 1968).
+// two: B1 H8 T1000 of 128 x 64, bf16, 22 against 19 us; B1 H16 T4000 34
+// against 37; B4 H32 T16384 418 against 474 (float32 38 against 31, 70 against
+// 79, 1396 against 1598).
 inline bool linear_pairs(const LinearParams &P) {
     return P.H > 0 && P.dv == 64 && P.Hv == P.H && P.H / P.Hq % 2 == 0 && P.H / P.Hk % 2 == 0 &&
            linear_total_blocks(P) * P.H >= 512;

@@ -26,11 +26,11 @@
 // every operand twice as often for the same products.
 //
 // Measured (bf16, 128 x 128): B2 H16 T16384 in blocks of 1024, constant decays,
-// 208 us a call (own states 70-84 us, join 12, outputs 125-143: the clock falls
+// 207 us a call (own states 68-88 us, join 12, outputs 120-153: the clock falls
 // in long runs).  It moves 924 MB where 539 are needed (k and v twice, and the
 // blocks' states), at 4.4 TB/s, 91 % of the rate of a large copy.  In the outputs
-// LDS is busy for 37 % of the time, VALU 31, MFMA 28, and a third is waiting.  B1
-// H16 T190 takes 14.3 us, three chunks one after the other.
+// LDS is busy for 23 % of the time, VALU 32, MFMA 29, and 29 % is waiting.  B1
+// H16 T190 takes 13.7 us, three chunks one after the other.
 #include "kdn_linear_device.h"
 
 namespace kdn {

@@ -20,15 +20,21 @@ struct Range {
 
 long long up256(long long n) { return (n + 255) / 256 * 256; }
 
-// Workgroups that the 256 CUs hold at once: two each of the prefill's kernels,
-// one of the gradients' (LDS).
+// Workgroups that dense blocks are cut for: the 256 CUs hold two each of the
+// prefill's kernels (LDS), and one of the gradients' walk (of 128 x 128 registers
+// and LDS; of 64 x 64 two would fit).
 constexpr int PREFILL_WGS = 512, GRAD_WGS = 256;
 
 // Tokens of a block: as many blocks as workgroups run at once.  Below that the
 // longest chain counts: the chunks of a block twice (its own state and its
 // outputs, 3.5 us a chunk of 64 each) and the join over the sequence's blocks
-// (1.5 us for 8), least at a block of about sqrt(2 tokens); up to 256 tokens
-// one block is as quick as three launches.
+// (1.5 us for 8), least at a block of about sqrt(2 tokens); up to 256 tokens a
+// bfloat16 prefill is as quick in one block as in three launches.
+// The rule is the bfloat16 prefill's.  us a call of 256 tokens (one block) and of
+// 257 (blocks of 64), H4, 64 x 64 / 128 x 128: bf16 prefill 11.2 / 16.2 and 16.9 /
+// 17.3; float32 prefill, in chunks of 32, 32 / 62 and 20 / 32; gradients bf16 33 /
+// 43 and 35 / 35, float32 66 / 153 and 35 / 62.  float32 calls would be quicker cut
+// from about 128 tokens on, bf16 gradients from about 192.
 int dense_block(int tokens, int N, int H, int wgs) {
     const long long full = ((long long)tokens * H + wgs - 1) / wgs;
     const long long len = N > 0 ? tokens / N : 0;
@@ -41,9 +47,8 @@ int dense_block(int tokens, int N, int H, int wgs) {
     return (int)(block > (1 << 30) ? (1 << 30) : block);
 }
 
-// Sizes common to the prefill and its gradients; fills the sizes of P.
-// `heads` is false for the workspace query of the prefill, which has none.
-// `wgs`: the workgroups that run at once, which dense blocks are cut for.
+// Sizes common to the prefill and its gradients; fills the sizes of P.  `wgs`: the
+// workgroups that dense blocks are cut for.
 kdn_status linear_shape(kdn::LinearParams &P, int dtype, int N, int T, int H, int Hq, int Hk,
                         int Hv, int d_k, int d_v, int gate, const kdn_packed *packed, int wgs) {
     if (!kdn::valid_dtype(dtype) || (gate != KDN_GATE_TOKEN && gate != KDN_GATE_HEAD))

@@ -42,14 +42,18 @@
 // few tokens x, y and z are most of d log_alpha, there is no sum over chunks, and
 // the errors were up to twice those of a sum in float32.
 //
-// Measured (bf16, 128 x 128): B4 H16 T4096 305 us a call: own states of both
-// directions 67-79 us, joins 14, states at the chunks' starts 63-72 (290 MB),
-// the walk below 166-195.  It moves 1231 MB where 483 are needed, at 4.0 TB/s, 82 %
-// of the rate of a large copy.  The walk holds q, k, v, do, P, Y and R of a chunk
-// in 141 KB of LDS, so one workgroup has a CU; its phases (P and Y; dq, dk, dv; R;
-// d log_alpha) follow one another behind barriers: LDS is busy 35 % of the time,
-// VALU 29, MFMA 18.  The walk of the chunks' states split into two workgroups of
-// 64 columns each took 71 us for 68.  B1 H4 T333 of 64 x 64 float32: 33 us of
+// Measured (bf16, 128 x 128): B4 H16 T4096 302 us a call: own states of both
+// directions 66-79 us, joins 14, states at the chunks' starts 60-71 (290 MB), the
+// walk below 167-196.  It moves 1231 MB where 483 are needed, at 4.1 TB/s, 83 % of
+// the rate of a large copy.  One workgroup has a CU: 512 threads of 256 registers
+// each fill its registers, and q, k, v, do, P, Y and R of a chunk are 141 KB of
+// LDS.  (64 x 64 has 4 waves and 70 KB, so that two fit.)  The walk's phases (P and
+// Y; dq, dk, dv; R; d log_alpha) follow one another behind barriers: LDS is busy
+// 27 % of the time, VALU 30, MFMA 18, 42 % is waiting; of its LDS cycles 18 % are
+// bank conflicts, the row reads of the 16 x 16 tiles.  about 200 scalars are
+// spilled to lanes of vector registers (strides, addresses and descriptors live
+// over the loop).  The walk of the chunks' states split into two workgroups of 64
+// columns each took 71 us for 68.  B1 H4 T333 of 64 x 64 float32: 33 us of
 // kernels, the walk 17 (22 with dq and dk in the same waves).
 #include <type_traits>
 
@@ -181,7 +185,7 @@ __device__ __forceinline__ void grad_walk(const LinearParams &P, const Block &B,
         vr.load(v + (long)c * C * P.v_stride, P.v_stride, cnt, tid);
         orr.load(od + (long)c * C * ostride, ostride, cnt, tid);
     };
-    constexpr int GW = W - 1;       // the wave of the decays: not one with a tile of P
+    constexpr int GW = W - 1;       // the wave of the decays: the fewest tiles of P
     if (w == GW) {
         gate(la0, nchunk - 1);
         if (nchunk > 1)

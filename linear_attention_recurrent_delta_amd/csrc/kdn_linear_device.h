@@ -359,8 +359,9 @@ __device__ __forceinline__ void decay_between(const Decays<C> &D, float hi_i, fl
 #pragma unroll
     for (int q = 0; q < N; q += 4) {
         f32x4 x = hi_i - *reinterpret_cast<const f32x4 *>(D.hi + j + q);
-        // bfloat16 products: the low parts (2^-24 of a prefix sum) are far
-        // below their rounding
+        // bfloat16 products: the low parts are 2^-24 of a prefix sum, of at most
+        // 64 resets (2^14) 7e-4 of the factor, a sixth of the product's rounding,
+        // and of common decays nothing of it
         if (sizeof(T) == 4)
             x += lo_i - *reinterpret_cast<const f32x4 *>(D.lo + j + q);
 #pragma unroll
@@ -412,7 +413,8 @@ template <typename T> struct GateReg {
 // 16 bytes (frag_row) have to fall into different groups of 4 banks (the pitch
 // an odd multiple of 4 of the 64), and the 4 rows of a transposed read, 4 places
 // apart (lds_row), 16 banks from each other: 76 and 36 banks for bfloat16, one
-// group more than the row for float32.
+// group more than the row for float32.  (Row reads of 16 x 16 tiles lose 4 cycles
+// of 12 to conflicts at any such pitch.)
 template <typename T> constexpr int lds_pitch(int d) {
     return sizeof(T) == 4 ? d + 4 : (d == 128 ? 152 : d + 8);
 }
@@ -537,8 +539,8 @@ __device__ __forceinline__ void join_blocks(const LinearParams &P, long id, int 
 // workgroups that start last are short ones.  Worth it where there are more
 // workgroups than run at once; with very many blocks the differences even out
 // (and one workgroup sorts).  37 sequences of 700 tokens at the mean, bf16,
-// the prefill: H32 of 128 x 64 in blocks of 1664 257 -> 196 us, H16 of 128 x 128
-// in blocks of 832 186 -> 178 us.
+// the prefill: H32 of 128 x 64 in blocks of 1664 149 -> 140 us, H16 of 128 x 128
+// in blocks of 832 205 -> 187 us.
 constexpr int ORDER_BINS = 512, ORDER_MAX = 4096;
 inline bool ordered(const LinearParams &P) {
     return P.ws_order && P.nblocks <= ORDER_MAX && (long)P.nblocks * P.H > 256;

@@ -3,7 +3,7 @@
 // workgroup scans all lengths (a tile of TILE at a time, N int32 from the L2)
 // and fills its own share of the tokens and of the block rows by binary
 // searches in the tile's offsets.  Bound by the launch and the chain of scan,
-// search and write: 48 sequences, 8192 tokens 7.8 us with the maps; 8000
+// search and write: 48 sequences, 8192 tokens 7.7 us with the maps; 8000
 // sequences, 2^20 tokens 18 us (8.7 MB written: 2 us of them at the rate of a
 // copy, the rest two tiles of scans and searches of 12 steps in LDS).
 #include "kdn_device.h"
