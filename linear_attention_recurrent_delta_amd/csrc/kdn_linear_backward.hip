@@ -36,8 +36,8 @@
 // multiplied from the accumulators (x and y to 2^-16 of a term), and <S, R> is a
 // product only at the block's last chunk: from there on it is the sum of the x
 // and y that it passes, exact enough for a sum over all tokens, not for a token's
-// own value where later ones are far larger.  B4 H16 T4096 of 128 x 128 388 us
-// against 320 with decays per token, B2 H16 T4096 of 64 x 64 94 against 87.
+// own value where later ones are far larger.  B4 H16 T4096 of 128 x 128 378 us
+// against 302 with decays per token, B2 H16 T4096 of 64 x 64 94 against 87.
 // Sequences of one chunk with states take it with decays per token as well: of
 // few tokens x, y and z are most of d log_alpha, there is no sum over chunks, and
 // the errors were up to twice those of a sum in float32.
