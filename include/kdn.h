@@ -526,6 +526,156 @@ unsigned long long kdn_linear_prefill_backward_workspace_size(
     kdn_dtype dtype, int N, int T, int H, int Hq, int Hk, int Hv, int d_k, int d_v,
     kdn_gate gate, const kdn_packed *packed, kdn_status *status);
 
+/*
+ * ---------------------------------------------------------------------------
+ * Around a recurrence: the short causal convolution in front of it, a selective
+ * state space scan as the recurrence itself, and the norms behind and before it.
+ *
+ * Conventions of these entry points, beside those at the top of this file:
+ *   - Parameters (weights, biases, A, D, scales) and their gradients are float32
+ *     always; per-token tensors have the call's dtype.
+ *   - Rows may be slices of wider rows: a stride is the elements from one token
+ *     to the next (0: contiguous), at least the row and below 2^28.  Any channel
+ *     count, stride and element-aligned address is taken; rows of whole 16-byte
+ *     pieces on such boundaries are quickest.  Outputs are contiguous.
+ *   - Dense and packed batches, pools, slots and what is skipped are as for
+ *     linear attention, and the same tables serve all of them: T is 0 where
+ *     `packed` is not NULL, a sequence whose slot is not in [0, pool) is skipped
+ *     (its outputs and states are left as they were, its gradients are zero), rows
+ *     behind the last sequence are not read, their outputs are left as they were
+ *     and their gradients are zero.  A sequence without tokens passes its state on.
+ *     Two sequences may share a slot only where no state is written.
+ *   - Sums over tokens (gradients of parameters) are made in parts in a fixed
+ *     order, the parts' sums in 64 bits: results are the same every time.
+ *   - Non-finite values propagate along their own channel or row, and through the
+ *     sums that they are part of; never to another sequence's outputs.
+ */
+typedef enum kdn_activation {
+    KDN_ACT_NONE = 0,
+    KDN_ACT_SILU = 1,          /* x sigmoid(x) */
+    KDN_ACT_SIGMOID = 2        /* gates only */
+} kdn_activation;
+
+/*
+ * Short causal convolution, each channel by itself, with W taps:
+ *     s_t = bias + sum_j weight_j x_{t-W+1+j},   y_t = act(s_t).
+ * The rows before a sequence are its state, the last W - 1 rows of x, oldest
+ * first, in the call's dtype (they are the inputs themselves).
+ *
+ *   x           [tokens, C] dtype, rows by stride
+ *   weight      [C, W] float32, W in {2, 3, 4};  bias [C] float32 or NULL (zero)
+ *   act         KDN_ACT_NONE or KDN_ACT_SILU
+ *   state0      [N or pool, W - 1, C] dtype, or NULL (zero)
+ *   y           [tokens, C] dtype (output)
+ *   state_out   shaped as state0 (output), or NULL (not wanted); may be exactly
+ *               state0, must not overlap it otherwise
+ * C below 2^26; sizes whose launches would have 2^32 work-items are refused
+ * (none has with less than 2^35 values in whole tiles of 64 x 64).
+ */
+kdn_status kdn_causal_conv(kdn_dtype dtype, int N, int T, int C, int W, kdn_activation act,
+                           long long x_stride, const void *x, const float *weight,
+                           const float *bias, const void *state0, void *y, void *state_out,
+                           const kdn_packed *packed, void *stream);
+
+/*
+ * One token for N rows from a pool of states, updated in place.  x [N, C] by
+ * stride, y [N, C]; slots [N] int32 or NULL (row n), pool states of `state`
+ * [pool, W - 1, C].  A row whose slot is not in [0, pool) is skipped and its y left
+ * as it was.  Two rows may not share a slot.
+ */
+kdn_status kdn_causal_conv_decode(kdn_dtype dtype, int N, int C, int W, kdn_activation act,
+                                  long long x_stride, const void *x, const float *weight,
+                                  const float *bias, const int *slots, int pool, void *state,
+                                  void *y, void *stream);
+
+/*
+ * Gradients of kdn_causal_conv for the cotangents d_y [tokens, C] and dstate_out
+ * (shaped as state0; NULL: zero).  Outputs: dx [tokens, C] and dstate0 (shaped as
+ * state0, or NULL; states without a sequence are left as they were) in the call's
+ * dtype, dweight [C, W] and dbias [C] (or NULL) float32.  workspace: device memory
+ * of at least the queried size, 256-byte aligned, overlapping no argument; NULL if
+ * that is 0.
+ */
+kdn_status kdn_causal_conv_backward(kdn_dtype dtype, int N, int T, int C, int W,
+                                    kdn_activation act, long long x_stride, const void *x,
+                                    const float *weight, const float *bias, const void *state0,
+                                    const void *d_y, const void *dstate_out, void *dx,
+                                    float *dweight, float *dbias, void *dstate0,
+                                    const kdn_packed *packed, void *workspace,
+                                    unsigned long long workspace_bytes, void *stream);
+
+/* Bytes of workspace, or 0 with *status set when the sizes are invalid (status may
+ * be NULL).  Of `packed` only tokens, block and max_blocks are read. */
+unsigned long long kdn_causal_conv_backward_workspace_size(kdn_dtype dtype, int N, int T, int C,
+                                                           int W, const kdn_packed *packed,
+                                                           kdn_status *status);
+
+/*
+ * Gated RMS norm of each head's d values, r(u) = (mean(u^2) + eps)^(-1/2):
+ *   KDN_NORM_GATE:  y = x r(x) weight act(z)
+ *   KDN_GATE_NORM:  y = u r(u) weight,  u = x act(z)
+ *
+ *   x, z        [tokens, H, d] dtype, tokens by stride, heads contiguous; z may be
+ *               NULL (no gate)
+ *   weight      [d] float32 for all heads, or [H, d] (per_head)
+ *   y           [tokens, H, d] dtype (output); may overlap no input
+ *   eps         positive and finite, else KDN_ERR_UNSUPPORTED
+ * 1 <= d <= 16384, else KDN_ERR_UNSUPPORTED; tokens * H < 2^31, H < 2^16.
+ */
+typedef enum kdn_norm_order { KDN_NORM_GATE = 0, KDN_GATE_NORM = 1 } kdn_norm_order;
+
+kdn_status kdn_gated_norm(kdn_dtype dtype, int tokens, int H, int d, kdn_norm_order order,
+                          kdn_activation act, int per_head, float eps, long long x_stride,
+                          long long z_stride, const void *x, const float *weight, const void *z,
+                          void *y, void *stream);
+
+/* Its gradients for d_y [tokens, H, d]: dx and dz (NULL where z is) in the call's
+ * dtype, dweight float32 shaped as weight. */
+kdn_status kdn_gated_norm_backward(kdn_dtype dtype, int tokens, int H, int d,
+                                   kdn_norm_order order, kdn_activation act, int per_head,
+                                   float eps, long long x_stride, long long z_stride,
+                                   const void *x, const float *weight, const void *z,
+                                   const void *d_y, void *dx, void *dz, float *dweight,
+                                   void *workspace, unsigned long long workspace_bytes,
+                                   void *stream);
+unsigned long long kdn_gated_norm_backward_workspace_size(int tokens, int H, int d, int per_head,
+                                                          kdn_status *status);
+
+/*
+ * Residual stream and the RMS norm before the next block:
+ *     h = residual + scale x,   y = h r(h) weight
+ * (the norm is of h before its rounding).
+ *
+ *   x           [tokens, D] dtype, residual [tokens, D] stream_dtype, by strides;
+ *               stream_dtype is dtype or KDN_F32
+ *   weight      [D] float32;  scale [scale_n] float32, scale_n 0 (NULL: one), 1 or D
+ *   y           [tokens, D] dtype, h [tokens, D] stream_dtype (outputs); h may be
+ *               exactly a contiguous residual
+ * 1 <= D <= 16384 and eps as above.
+ */
+kdn_status kdn_residual_norm(kdn_dtype dtype, kdn_dtype stream_dtype, int tokens, int D,
+                             int scale_n, float eps, long long x_stride, long long residual_stride,
+                             const void *x, const void *residual, const float *weight,
+                             const float *scale, void *y, void *h, void *stream);
+
+/*
+ * Its gradients from h (the output, rows by stride) for d_y [tokens, D] dtype and
+ * d_h [tokens, D] stream_dtype (NULL: zero):
+ *   dresidual [tokens, D] stream_dtype: d_h + the norm's gradient
+ *   dx [tokens, D] dtype: scale dresidual, or NULL (not wanted)
+ *   dweight [D], dscale [scale_n] float32 (NULL: not wanted; NULL where scale is)
+ * x is read for dscale only and may be NULL without it.
+ */
+kdn_status kdn_residual_norm_backward(kdn_dtype dtype, kdn_dtype stream_dtype, int tokens, int D,
+                                      int scale_n, float eps, long long x_stride,
+                                      long long h_stride, const void *x, const void *h,
+                                      const float *weight, const float *scale, const void *d_y,
+                                      const void *d_h, void *dx, void *dresidual, float *dweight,
+                                      float *dscale, void *workspace,
+                                      unsigned long long workspace_bytes, void *stream);
+unsigned long long kdn_residual_norm_backward_workspace_size(int tokens, int D, int scale_n,
+                                                             kdn_status *status);
+
 /* Static, NUL-terminated description of a status code. */
 const char *kdn_status_string(kdn_status status);
 

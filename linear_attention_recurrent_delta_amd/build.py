@@ -48,7 +48,11 @@ UNITS += [("kdn_prefill.hip", ["-DKDN_PREFILL_DISPATCH"], "kdn_prefill_dispatch.
           ("kdn_linear_backward.hip", ["-mllvm", "-amdgpu-mfma-vgpr-form"],
            "kdn_linear_backward.o"),
           ("kdn_linear_decode.hip", [], "kdn_linear_decode.o"),
-          ("kdn_tables.hip", [], "kdn_tables.o")]
+          ("kdn_tables.hip", [], "kdn_tables.o"),
+          ("kdn_conv_abi.cpp", [], "kdn_conv_abi.o"),
+          ("kdn_conv.hip", [], "kdn_conv.o"),
+          ("kdn_norm_abi.cpp", [], "kdn_norm_abi.o"),
+          ("kdn_norm.hip", [], "kdn_norm.o")]
 
 
 def hipcc() -> str:

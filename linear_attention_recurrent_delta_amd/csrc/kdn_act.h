@@ -1,0 +1,85 @@
+// kdn_act.h -- device-side activations (silu, sigmoid) and element packs of a
+// chosen width, shared by the convolution, norm and scan kernels.
+#pragma once
+
+#include "kdn_device.h"
+
+namespace kdn {
+
+// e^x.  v_exp_f32 is off by an ulp; the rounding of x log2(e) adds |x| 2^-24 to it
+// (with the constant's own rounding as much again), which float32 calls (FINE)
+// take back by the part that the product lost.
+template <bool FINE> __device__ __forceinline__ float exp_f32(float x) {
+    constexpr float L = 1.44269504f, L_LO = 1.92596299e-8f;
+    const float t = x * L;
+    float e = __builtin_amdgcn_exp2f(t);
+    if constexpr (FINE) {
+        const float lo = fmaf(x, L, -t) + x * L_LO;
+        // past the ends of float32 e is 0 or infinite and stays so
+        if (fabsf(t) < 126.f)
+            e = fmaf(e, lo * 0.693147181f, e);
+    }
+    return e;
+}
+
+// sigmoid(x) and 1 - sigmoid(x), both without cancellation (and where e^-x is
+// infinite, with g zero).
+template <bool FINE>
+__device__ __forceinline__ void sigmoid2(float x, float &g, float &rest) {
+    const float e = exp_f32<FINE>(-x);
+    g = FINE ? 1.f / (1.f + e) : fast_rcp(1.f + e);
+    rest = e > 1e37f ? 1.f : e * g;       // NaN stays NaN
+}
+template <bool FINE> __device__ __forceinline__ float sigmoid_f32(float x) {
+    float g, rest;
+    sigmoid2<FINE>(x, g, rest);
+    return g;
+}
+template <bool FINE> __device__ __forceinline__ float silu_f32(float x) {
+    return x * sigmoid_f32<FINE>(x);
+}
+// silu(x) and its derivative
+template <bool FINE>
+__device__ __forceinline__ void silu_grad(float x, float &y, float &dy) {
+    float g, rest;
+    sigmoid2<FINE>(x, g, rest);
+    y = x * g;
+    dy = fmaf(y, rest, g);
+}
+
+// V consecutive elements as they lie in memory, on any element's boundary (global
+// memory takes wide accesses there), of which the first n are there.
+template <typename T, int V> struct Pack {
+    typedef T Vec __attribute__((ext_vector_type(V)));
+    typedef Vec Raw __attribute__((aligned(sizeof(T))));
+    Vec r;
+    __device__ __forceinline__ void zero() { r = (Vec)(T)0.f; }
+    __device__ __forceinline__ void load(const T *p) { r = *reinterpret_cast<const Raw *>(p); }
+    __device__ __forceinline__ void store(T *p) const { *reinterpret_cast<Raw *>(p) = r; }
+    // elements past n: zero, not written
+    __device__ __forceinline__ void load(const T *p, int n) {
+        if (n >= V) {
+            load(p);
+        } else {
+            zero();
+#pragma unroll
+            for (int i = 0; i < V - 1; ++i)
+                if (i < n)
+                    r[i] = p[i];
+        }
+    }
+    __device__ __forceinline__ void store(T *p, int n) const {
+        if (n >= V) {
+            store(p);
+        } else {
+#pragma unroll
+            for (int i = 0; i < V - 1; ++i)
+                if (i < n)
+                    p[i] = r[i];
+        }
+    }
+    __device__ __forceinline__ float get(int i) const { return to_f32(r[i]); }
+    __device__ __forceinline__ void set(int i, float x) { r[i] = from_f32<T>(x); }
+};
+
+}  // namespace kdn

@@ -1,0 +1,449 @@
+// kdn_conv.hip -- the short causal convolution in front of a recurrence (gfx950):
+//   s_t = bias + sum_j w_j x_{t-W+1+j},   y_t = s_t sigmoid(s_t)   (or s_t),
+// per channel, W <= 4 taps.  The rows before a sequence are its state, the last
+// W - 1 rows of x, kept in the call's type: they are the inputs themselves.
+// Bound by memory: x read and y written once.  A lane owns VEC neighbouring
+// channels (16 bytes) of RT consecutive tokens, so that a wave reads whole lines
+// and every row is read (RT + W - 1) / RT times, the second time from the caches;
+// all rows of a lane are requested before the first is used.
+#include "kdn_act.h"
+#include "kdn_batch_device.h"
+#include "kdn_conv.h"
+
+namespace kdn {
+namespace conv {
+
+constexpr int NT = 256, NW = NT / WAVE;
+
+// Where a workgroup is: tile of tokens and 64 * VEC channels, or (behind the
+// tiles) one sequence.
+struct Place {
+    long tile;
+    int chunk;
+};
+__device__ __forceinline__ Place place(int chunks) {
+    return Place{(long)blockIdx.x / chunks, (int)(blockIdx.x % chunks)};
+}
+
+// Weights of VEC channels, tap j of channel e in w[j][e], and the bias.
+template <int VEC, int W>
+__device__ __forceinline__ void load_weights(const float *weight, const float *bias, long c, int n,
+                                             float (&w)[W][VEC], float (&b)[VEC]) {
+    Pack<float, W> taps;
+    Pack<float, VEC> first;
+    first.zero();
+    if (bias)
+        first.load(bias + c, n);
+#pragma unroll
+    for (int e = 0; e < VEC; ++e) {
+        taps.zero();
+        if (e < n)
+            taps.load(weight + (c + e) * W);
+#pragma unroll
+        for (int j = 0; j < W; ++j)
+            w[j][e] = taps.get(j);
+        b[e] = first.get(e);
+    }
+}
+
+template <typename T, int VEC, int W, int RT>
+__global__ __launch_bounds__(NT) void conv_kernel(ConvParams P, int chunks, int sub, long tiles) {
+    constexpr bool FINE = sizeof(T) == 4;
+    constexpr int H = W - 1, TT = NW * RT;
+    const int lane = threadIdx.x & (WAVE - 1);
+    const Place at = place(chunks);
+    const long c = ((long)at.chunk * WAVE + lane) * VEC;
+    T *state_out = static_cast<T *>(P.state_out);
+    const T *state0 = static_cast<const T *>(P.state0);
+    const int nc = (int)min((long)VEC, P.C - c);     // channels of this lane
+    typedef Pack<T, VEC> V;
+    if (at.tile >= tiles) {
+        // a sequence without tokens passes its state on
+        if (at.chunk > 0 || !state_out || state_out == state0)
+            return;
+        const long slot = empty_slot(P, (int)(at.tile - tiles));
+        if (slot < 0)
+            return;
+        for (long i = threadIdx.x; i < (long)H * P.C; i += NT)
+            state_out[slot * H * P.C + i] = state0 ? state0[slot * H * P.C + i] : from_f32<T>(0.f);
+        return;
+    }
+    const Block B = get_block(P, at.tile / sub);
+    const int t0 = (int)(at.tile % sub) * TT + wave_id() * RT;
+    if (t0 >= B.count || B.slot < 0 || c >= P.C)
+        return;
+    const bool start = B.index == 0 && t0 == 0;
+    const T *x = static_cast<const T *>(P.x) + B.first * P.x_stride + c;
+    V rows[RT + H], old[H];
+#pragma unroll
+    for (int i = 0; i < RT + H; ++i) {
+        rows[i].zero();
+        const int t = t0 - H + i;
+        if (t < B.count && (i >= H || !start) && (i >= H || B.first + t >= 0))
+            rows[i].load(x + (long)t * P.x_stride, nc);
+    }
+    if (start) {
+        const long at0 = B.slot * H * P.C + c;
+#pragma unroll
+        for (int i = 0; i < H; ++i) {
+            old[i].zero();
+            if (state0)
+                old[i].load(state0 + at0 + (long)i * P.C, nc);
+            rows[i] = old[i];
+        }
+        if (state_out) {
+            // the last W - 1 of the sequence's rows with its state before them; the
+            // state has been read, and no other thread reads or writes it
+            const long n = tokens_left(P, B);
+#pragma unroll
+            for (int i = 0; i < H; ++i) {
+                V last;
+                last.zero();
+                if (n + i >= H)
+                    last.load(x + (n + i - H) * P.x_stride, nc);
+#pragma unroll
+                for (int j = 1; j < H; ++j)
+                    if (n + i == j)
+                        last = old[j];
+                last.store(state_out + at0 + (long)i * P.C, nc);
+            }
+        }
+    }
+    float w[W][VEC], b[VEC];
+    load_weights<VEC, W>(P.weight, P.bias, c, nc, w, b);
+    T *y = static_cast<T *>(P.y) + (B.first + t0) * P.C + c;
+#pragma unroll
+    for (int i = 0; i < RT; ++i) {
+        V out;
+#pragma unroll
+        for (int e = 0; e < VEC; ++e) {
+            float s = b[e];
+#pragma unroll
+            for (int j = 0; j < W; ++j)
+                s = fmaf(w[j][e], rows[i + j].get(e), s);
+            out.set(e, P.silu ? silu_f32<FINE>(s) : s);
+        }
+        if (t0 + i < B.count)
+            out.store(y + (long)i * P.C, nc);
+    }
+}
+
+// ---------------------------------------------------------------------------
+// Single tokens: a thread shifts the state of VEC channels of one row.
+// ---------------------------------------------------------------------------
+template <typename T, int VEC, int W>
+__global__ __launch_bounds__(WAVE) void conv_decode_kernel(ConvDecodeParams P, int chunks) {
+    constexpr bool FINE = sizeof(T) == 4;
+    constexpr int H = W - 1;
+    const Place at = place(chunks);
+    const long c = ((long)at.chunk * WAVE + threadIdx.x) * VEC;
+    const long slot = P.slots ? P.slots[at.tile] : at.tile;
+    if (slot < 0 || slot >= P.pool || c >= P.C)
+        return;
+    T *state = static_cast<T *>(P.state) + slot * H * P.C + c;
+    const int nc = (int)min((long)VEC, P.C - c);
+    Pack<T, VEC> rows[W];
+    rows[H].load(static_cast<const T *>(P.x) + at.tile * P.x_stride + c, nc);
+#pragma unroll
+    for (int i = 0; i < H; ++i)
+        rows[i].load(state + (long)i * P.C, nc);
+    float w[W][VEC], b[VEC];
+    load_weights<VEC, W>(P.weight, P.bias, c, nc, w, b);
+#pragma unroll
+    for (int i = 0; i < H; ++i)
+        rows[i + 1].store(state + (long)i * P.C, nc);
+    Pack<T, VEC> out;
+#pragma unroll
+    for (int e = 0; e < VEC; ++e) {
+        float s = b[e];
+#pragma unroll
+        for (int j = 0; j < W; ++j)
+            s = fmaf(w[j][e], rows[j].get(e), s);
+        out.set(e, P.silu ? silu_f32<FINE>(s) : s);
+    }
+    out.store(static_cast<T *>(P.y) + at.tile * P.C + c, nc);
+}
+
+// ---------------------------------------------------------------------------
+// Gradients: with ds_t = dy_t act'(s_t) (s made again from x),
+//   dx_t = sum_j w_j ds_{t+W-1-j},  dw_j = sum_t ds_t x_{t-W+1+j},  db = sum_t ds_t,
+// the same sum for the rows of the state before the sequence, and what reaches
+// the state behind it added to its last rows.  Bound by memory: x and dy read, dx
+// written.  A lane walks RT tokens and the W - 1 behind them, whose ds it makes
+// again.  A workgroup keeps the sums of its channels over all its tiles (every
+// `parts`-th) in registers and writes them once; a second kernel adds the parts
+// in order, in 64 bits.
+// ---------------------------------------------------------------------------
+template <typename T, int VEC, int W>
+__global__ __launch_bounds__(NT) void conv_grad_kernel(ConvParams P, int chunks, int sub,
+                                                       long tiles) {
+    constexpr bool FINE = sizeof(T) == 4;
+    constexpr int H = W - 1, RT = CONV_GRAD_TILE / NW;
+    const int lane = threadIdx.x & (WAVE - 1), wv = wave_id();
+    const int chunk = blockIdx.x % chunks, part = blockIdx.x / chunks;
+    const long c = ((long)chunk * WAVE + lane) * VEC;
+    const bool live = c < P.C;
+    const int nc = (int)min((long)VEC, P.C - c);     // channels of this lane
+    typedef Pack<T, VEC> V;
+    float w[W][VEC], b[VEC], dw[W + 1][VEC];
+#pragma unroll
+    for (int j = 0; j <= W; ++j)
+#pragma unroll
+        for (int e = 0; e < VEC; ++e)
+            dw[j][e] = 0.f;
+    if (live)
+        load_weights<VEC, W>(P.weight, P.bias, c, nc, w, b);
+    for (long tile = part; tile < tiles && live; tile += P.parts) {
+        const Block B = get_block(P, tile / sub);
+        const int t0 = (int)(tile % sub) * CONV_GRAD_TILE + wv * RT;
+        if (t0 >= B.count)
+            continue;
+        T *dx = static_cast<T *>(P.dx) + (B.first + t0) * P.C + c;
+        const int n = min(RT, B.count - t0);      // own tokens
+        if (B.slot < 0) {
+            V none;
+            none.zero();
+            for (int i = 0; i < n; ++i)
+                none.store(dx + (long)i * P.C, nc);
+            continue;
+        }
+        const long left = tokens_left(P, B) - t0;     // tokens to the sequence's end
+        const bool start = B.index == 0 && t0 == 0;
+        const T *x = static_cast<const T *>(P.x) + (B.first + t0) * P.x_stride + c;
+        const T *dy = static_cast<const T *>(P.d_y) + (B.first + t0) * P.C + c;
+        const T *state0 = static_cast<const T *>(P.state0);
+        const T *dlast = static_cast<const T *>(P.dstate_out);
+        const long at0 = B.slot * H * P.C + c;
+        // rows t0 - H .. t0 + RT + H - 1 of x and t0 .. of dy
+        V xs[RT + 2 * H], g[RT + H];
+#pragma unroll
+        for (int i = 0; i < RT + 2 * H; ++i) {
+            xs[i].zero();
+            if (i < H && start) {
+                if (state0)
+                    xs[i].load(state0 + at0 + (long)i * P.C, nc);
+            } else if (i - H < left && B.first + t0 - H + i >= 0) {
+                xs[i].load(x + (long)(i - H) * P.x_stride, nc);
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < RT + H; ++i) {
+            g[i].zero();
+            if (i < left)
+                g[i].load(dy + (long)i * P.C, nc);
+        }
+        // near[k] = ds of token i - H + 1 + k
+        float near[W][VEC];
+#pragma unroll
+        for (int k = 0; k < W; ++k)
+#pragma unroll
+            for (int e = 0; e < VEC; ++e)
+                near[k][e] = 0.f;
+#pragma unroll
+        for (int i = 0; i < RT + H; ++i) {
+            V out;
+#pragma unroll
+            for (int e = 0; e < VEC; ++e) {
+#pragma unroll
+                for (int k = 0; k < H; ++k)
+                    near[k][e] = near[k + 1][e];
+                float d = g[i].get(e);
+                if (P.silu) {
+                    float s = b[e], y, dact;
+#pragma unroll
+                    for (int j = 0; j < W; ++j)
+                        s = fmaf(w[j][e], xs[i + j].get(e), s);
+                    silu_grad<FINE>(s, y, dact);
+                    d *= dact;
+                }
+                // tokens behind the sequence have no gradient, whatever s was
+                d = i < left ? d : 0.f;
+                near[H][e] = d;
+                if (i < n) {
+#pragma unroll
+                    for (int j = 0; j < W; ++j)
+                        dw[j][e] = fmaf(d, xs[i + j].get(e), dw[j][e]);
+                    dw[W][e] += d;
+                }
+                // the row H before: dx_t = sum_k w_{H-k} ds_{t+k}
+                float sum = 0.f;
+#pragma unroll
+                for (int k = 0; k < W; ++k)
+                    sum = fmaf(w[H - k][e], near[k][e], sum);
+                out.set(e, sum);
+            }
+            // row t0 + i - H, of the sequence or of the state before it
+            const int t = i - H;
+            if (t >= 0 ? t < n : start && P.dstate0) {
+                if (dlast && left - t <= H) {
+                    V last;
+                    last.load(dlast + at0 + (long)(H + t - left) * P.C, nc);
+#pragma unroll
+                    for (int e = 0; e < VEC; ++e) {
+                        float sum = 0.f;
+#pragma unroll
+                        for (int k = 0; k < W; ++k)
+                            sum = fmaf(w[H - k][e], near[k][e], sum);
+                        out.set(e, sum + last.get(e));
+                    }
+                }
+                if (t >= 0)
+                    out.store(dx + (long)t * P.C, nc);
+                else
+                    out.store(static_cast<T *>(P.dstate0) + at0 + (long)i * P.C, nc);
+            }
+        }
+    }
+    // sums over the four waves, in order
+    __shared__ float sums[NW][W + 1][WAVE * VEC];
+#pragma unroll
+    for (int j = 0; j <= W; ++j)
+#pragma unroll
+        for (int e = 0; e < VEC; ++e)
+            sums[wv][j][lane * VEC + e] = dw[j][e];
+    __syncthreads();
+    for (int i = threadIdx.x; i < (W + 1) * WAVE * VEC; i += NT) {
+        const int j = i / (WAVE * VEC), k = i % (WAVE * VEC);
+        const long cc = (long)chunk * WAVE * VEC + k;
+        if (cc < P.C) {
+            float s = sums[0][j][k];
+#pragma unroll
+            for (int q = 1; q < NW; ++q)
+                s += sums[q][j][k];
+            P.ws[((long)part * (W + 1) + j) * P.C + cc] = s;
+        }
+    }
+}
+
+// The parts' sums, 64 channels a workgroup; behind those workgroups: zero
+// gradients of the rows behind the last sequence, and the states' of sequences
+// without tokens.
+constexpr int TAIL_WGS = 64;
+template <typename T>
+__global__ __launch_bounds__(NT) void conv_sum_kernel(ConvParams P, int chunks) {
+    const int W = P.W, lane = threadIdx.x & (WAVE - 1), wv = threadIdx.x / WAVE;
+    const long id = blockIdx.x;
+    if (id < (long)chunks * (W + 1)) {
+        const int j = (int)(id % (W + 1));
+        const long c = id / (W + 1) * WAVE + lane;
+        double s = 0.;
+        if (c < P.C)
+            for (int p = wv; p < P.parts; p += NW)
+                s += (double)P.ws[((long)p * (W + 1) + j) * P.C + c];
+        __shared__ double sums[NW][WAVE];
+        sums[wv][lane] = s;
+        __syncthreads();
+        if (wv == 0 && c < P.C) {
+            for (int q = 1; q < NW; ++q)
+                s += sums[q][lane];
+            if (j < W)
+                P.dweight[c * W + j] = (float)s;
+            else if (P.dbias)
+                P.dbias[c] = (float)s;
+        }
+        return;
+    }
+    const long wg = id - (long)chunks * (W + 1);
+    if (wg < TAIL_WGS) {
+        if (!P.block_offsets)
+            return;
+        const long first = tail_start(P);
+        for (long i = first * P.C + wg * NT + threadIdx.x; i < P.tokens * P.C;
+             i += (long)TAIL_WGS * NT)
+            static_cast<T *>(P.dx)[i] = from_f32<T>(0.f);
+        return;
+    }
+    if (!P.dstate0)
+        return;
+    const long slot = empty_slot(P, (int)(wg - TAIL_WGS)), size = (long)(W - 1) * P.C;
+    if (slot < 0)
+        return;
+    const T *dlast = static_cast<const T *>(P.dstate_out);
+    for (long i = threadIdx.x; i < size; i += NT)
+        static_cast<T *>(P.dstate0)[slot * size + i] = dlast ? dlast[slot * size + i]
+                                                             : from_f32<T>(0.f);
+}
+
+template <typename T, int VEC, int W>
+hipError_t launch_conv_fwd_t(const ConvParams &P, hipStream_t st) {
+    constexpr int RT = 16, TT = NW * RT;
+    const int chunks = conv_chunks(P.C, VEC), sub = P.block_offsets ? (int)((P.block + TT - 1l) / TT) : 1;
+    ConvParams Q = P;
+    if (!P.block_offsets) {          // dense: a block is a tile
+        Q.block = TT;
+        Q.nblocks = (int)((P.T + TT - 1l) / TT);
+    }
+    const long tiles = conv_tiles(Q, TT);
+    const long empty = P.state_out && P.state_out != P.state0 && (P.block_offsets || P.T == 0) ? P.N : 0;
+    if (tiles + empty == 0)
+        return hipSuccess;
+    hipLaunchKernelGGL((conv_kernel<T, VEC, W, RT>), dim3((unsigned)((tiles + empty) * chunks)),
+                       dim3(NT), 0, st, Q, chunks, sub, tiles);
+    return hipGetLastError();
+}
+
+template <typename T, int VEC, int W>
+hipError_t launch_conv_decode_t(const ConvDecodeParams &P, hipStream_t st) {
+    const int chunks = conv_chunks(P.C, VEC);
+    hipLaunchKernelGGL((conv_decode_kernel<T, VEC, W>), dim3((unsigned)((long)P.N * chunks)),
+                       dim3(WAVE), 0, st, P, chunks);
+    return hipGetLastError();
+}
+
+template <typename T, int VEC, int W>
+hipError_t launch_conv_grad_t(const ConvParams &P, hipStream_t st) {
+    constexpr int TT = CONV_GRAD_TILE;
+    const int chunks = conv_chunks(P.C, VEC), sub = P.block_offsets ? (int)((P.block + TT - 1l) / TT) : 1;
+    ConvParams Q = P;
+    if (!P.block_offsets) {
+        Q.block = TT;
+        Q.nblocks = (int)((P.T + TT - 1l) / TT);
+    }
+    const long tiles = conv_tiles(Q, TT);
+    if (P.parts > 0) {
+        hipLaunchKernelGGL((conv_grad_kernel<T, VEC, W>), dim3((unsigned)(chunks * (long)P.parts)),
+                           dim3(NT), 0, st, Q, chunks, sub, tiles);
+        const hipError_t e = hipGetLastError();
+        if (e != hipSuccess)
+            return e;
+    }
+    const int wide = (P.C + WAVE - 1) / WAVE;
+    const long empty = P.dstate0 && (P.block_offsets || P.T == 0) ? P.N : 0;
+    hipLaunchKernelGGL((conv_sum_kernel<T>), dim3((unsigned)((long)wide * (W + 1) + TAIL_WGS + empty)),
+                       dim3(NT), 0, st, Q, wide);
+    return hipGetLastError();
+}
+
+}  // namespace conv
+
+#define KDN_CONV(fn, T_, V_)                              \
+    switch (P.W) {                                        \
+    case 2: return conv::fn<T_, V_, 2>(P, stream);        \
+    case 3: return conv::fn<T_, V_, 3>(P, stream);        \
+    default: return conv::fn<T_, V_, 4>(P, stream);       \
+    }
+
+hipError_t launch_conv(const ConvParams &P, hipStream_t stream) {
+    if (P.bf16)
+        KDN_CONV(launch_conv_fwd_t, bf16, 8)
+    KDN_CONV(launch_conv_fwd_t, float, 4)
+}
+
+hipError_t launch_conv_decode(const ConvDecodeParams &P, hipStream_t stream) {
+    if ((long)P.N * P.C == 0)
+        return hipSuccess;
+    if (P.bf16)
+        KDN_CONV(launch_conv_decode_t, bf16, 8)
+    KDN_CONV(launch_conv_decode_t, float, 4)
+}
+
+hipError_t launch_conv_backward(const ConvParams &P, hipStream_t stream) {
+    if (P.C == 0)
+        return hipSuccess;
+    if (P.bf16)
+        KDN_CONV(launch_conv_grad_t, bf16, 4)
+    KDN_CONV(launch_conv_grad_t, float, 2)
+}
+#undef KDN_CONV
+
+}  // namespace kdn

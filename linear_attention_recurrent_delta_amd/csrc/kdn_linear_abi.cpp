@@ -9,16 +9,14 @@
 #include <limits.h>
 
 using kdn::aligned;
+using kdn::clash;
+using kdn::launchable;
 using kdn::overlap;
+using kdn::Range;
+using kdn::span;
+using kdn::up256;
 
 namespace {
-
-struct Range {
-    const void *p;
-    long long n;
-};
-
-long long up256(long long n) { return (n + 255) / 256 * 256; }
 
 // Workgroups that dense blocks are cut for: the 256 CUs hold two each of the
 // prefill's kernels (LDS), and one of the gradients' walk (of 128 x 128 registers
@@ -87,10 +85,6 @@ kdn_status linear_shape(kdn::LinearParams &P, int dtype, int N, int T, int H, in
     return KDN_OK;
 }
 
-// A launch has less than 2^32 work-items: of more the runtime starts what their
-// low 32 bits say, and reports no error.
-bool launchable(long long workgroups, int threads) { return workgroups * threads < (1LL << 32); }
-
 // Elements between tokens (0: contiguous), or an error.
 kdn_status token_stride(long long given, long long row, long long es, long *out) {
     if (given == 0)
@@ -104,11 +98,6 @@ kdn_status token_stride(long long given, long long row, long long es, long *out)
     return KDN_OK;
 }
 
-// Bytes from the first to the last element of `rows` strided rows.
-long long span(long long rows, long stride, long long row, long long es) {
-    return rows > 0 ? ((rows - 1) * stride + row) * es : 0;
-}
-
 // Workspace sections: states at the blocks' starts, and the blocks' decays with
 // a packed batch's order behind them; nothing where every sequence is known to
 // be one block.
@@ -119,19 +108,6 @@ long long state_sections(const kdn::LinearParams &P, bool packed, long long *dec
     const long long n = up256(blocks * P.H * P.dk * P.dv * 4);
     *decay = n;
     return n + up256(blocks * (P.H + packed) * 4);
-}
-
-// Outputs overlap no input and no other output.
-bool clash(const Range *outs, int no, const Range *ins, int ni) {
-    for (int i = 0; i < no; ++i) {
-        for (int j = 0; j < ni; ++j)
-            if (overlap(outs[i].p, outs[i].n, ins[j].p, ins[j].n))
-                return true;
-        for (int j = i + 1; j < no; ++j)
-            if (overlap(outs[i].p, outs[i].n, outs[j].p, outs[j].n))
-                return true;
-    }
-    return false;
 }
 
 // The packed tables' pointers.

@@ -3,7 +3,7 @@
 // chunk.
 #pragma once
 
-#include "kdn_device.h"
+#include "kdn_batch_device.h"
 #include "kdn_linear.h"
 
 namespace kdn {
@@ -12,65 +12,6 @@ namespace lin {
 typedef float f32x8 __attribute__((ext_vector_type(8)));
 typedef short s16x4 __attribute__((ext_vector_type(4)));
 typedef __attribute__((address_space(3))) s16x4 lds_s16x4;
-
-// The wave's number as a scalar: what depends on it are branches of the whole
-// wave.  (A vector condition may become an EXEC mask without a branch, which
-// an MFMA under it does not heed.)
-__device__ __forceinline__ int wave_id() {
-    return __builtin_amdgcn_readfirstlane((int)threadIdx.x / WAVE);
-}
-
-// ---------------------------------------------------------------------------
-// The block of a workgroup.
-// ---------------------------------------------------------------------------
-struct Block {
-    long first;      // first token row
-    int count;       // tokens (0: nothing to do)
-    int seq;         // sequence
-    int index, last; // index in the sequence; 1 if it is the sequence's last
-    int single;      // 1: the sequence has this block only
-    long slot;       // state of the sequence, -1: the sequence is skipped
-};
-
-// Row b of the blocks.  Packed tables are device data that the host cannot
-// check: a row that does not fit the call's sizes owns no tokens.
-__device__ __forceinline__ Block get_block(const LinearParams &P, long b) {
-    Block B;
-    B.count = 0;
-    if (!P.block_offsets) {
-        B.seq = (int)(b / P.nblocks);
-        B.index = (int)(b - (long)B.seq * P.nblocks);
-        const int t0 = B.index * P.block;
-        B.first = (long)B.seq * P.T + t0;
-        B.count = min(P.block, P.T - t0);
-        B.last = B.index + 1 == P.nblocks;
-        B.single = P.nblocks == 1;
-        B.slot = B.seq;
-        return B;
-    }
-    int4 r = reinterpret_cast<const int4 *>(P.blocks)[b];
-    r.x = __builtin_amdgcn_readfirstlane(r.x);      // the same in every lane: scalars
-    r.y = __builtin_amdgcn_readfirstlane(r.y);
-    r.z = __builtin_amdgcn_readfirstlane(r.z);
-    r.w = __builtin_amdgcn_readfirstlane(r.w);
-    if (r.z < 0 || r.z >= P.N || r.x < 0 || r.y <= 0 || r.y > P.block ||
-        (long)r.x + r.y > P.tokens || r.w < 0)
-        return B;
-    const int b0 = __builtin_amdgcn_readfirstlane(P.block_offsets[r.z]);
-    const int b1 = __builtin_amdgcn_readfirstlane(P.block_offsets[r.z + 1]);
-    if (b0 < 0 || b1 > P.nblocks || (long)b0 + r.w != b || b1 <= b)
-        return B;
-    B.slot = P.slots ? __builtin_amdgcn_readfirstlane(P.slots[r.z]) : r.z;
-    if (B.slot >= P.pool)
-        B.slot = -1;
-    B.first = r.x;
-    B.seq = r.z;
-    B.index = r.w;
-    B.last = b + 1 == b1;
-    B.single = b1 - b0 == 1;
-    B.count = r.y;
-    return B;
-}
 
 // ---------------------------------------------------------------------------
 // Fragments of 32 x 32 tiles: the 8 contraction elements of one lane for a

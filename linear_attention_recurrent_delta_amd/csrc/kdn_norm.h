@@ -1,0 +1,70 @@
+// kdn_norm.h -- launch parameters and launchers of the gated norm and of the norm
+// of the residual stream.  The C ABI (kdn_norm_abi.cpp) validates arguments and
+// fills these.
+#pragma once
+
+#include <hip/hip_runtime.h>
+
+#include "kdn.h"
+
+namespace kdn {
+
+constexpr int NORM_DIM = 16384;     // channels of a norm at most
+
+struct GatedNormParams {
+    int bf16;
+    long tokens;
+    int H, d;               // heads of a token, channels of a head
+    int per_head;           // weight [H, d], else [d]
+    int gate_first;         // kdn_norm_order
+    int act;                // kdn_activation
+    float eps;
+    long x_stride, z_stride;    // elements between tokens
+    const void *x, *z;      // z may be null
+    const float *weight;
+    void *y;                // [tokens, H, d]
+    // Gradients.
+    const void *d_y;
+    void *dx, *dz;
+    float *dweight;
+    float *ws;              // [parts][heads of weight][d]
+    int parts;
+};
+
+struct ResidualNormParams {
+    int bf16, stream_bf16;  // types of x and y, of the residual stream
+    long tokens;
+    int D;
+    int scale_n;            // 0, 1 or D
+    float eps;
+    long x_stride, r_stride;    // elements between tokens
+    const void *x, *residual;
+    const float *weight, *scale;
+    void *y, *h;            // [tokens, D]
+    // Gradients (residual holds h).
+    const void *d_y, *d_h;  // d_h may be null (zero)
+    void *dx, *dresidual;   // dx may be null (not wanted)
+    float *dweight, *dscale;    // dscale may be null
+    float *ws;              // [parts][D] of dweight, [parts][D or 1] of dscale
+    int parts;
+};
+
+// Parts that the sums over tokens are made in: workgroups that run at once.
+constexpr int NORM_PARTS = 1024;
+
+// Threads of a row of n elements: one for each 16 bytes, a power of two, up to a
+// whole workgroup.
+inline int norm_row_threads(int n, bool bf16) {
+    const int v = bf16 ? 8 : 4;
+    int t = 1;
+    while (t < (n + v - 1) / v && t < 1024)
+        t *= 2;
+    return t;
+}
+
+hipError_t launch_gated_norm(const GatedNormParams &P, hipStream_t stream);
+hipError_t launch_gated_norm_backward(const GatedNormParams &P, hipStream_t stream);
+hipError_t launch_residual_norm(const ResidualNormParams &P, hipStream_t stream);
+hipError_t launch_residual_norm_backward(const ResidualNormParams &P, hipStream_t stream);
+
+}  // namespace kdn

@@ -1,0 +1,563 @@
+// kdn_norm.hip -- RMS norms around a block (gfx950), r(u) = (mean(u^2) + eps)^(-1/2):
+// of a recurrence's outputs with their gate, each head by itself,
+//   y = x r(x) w act(z)   or   u = x act(z), y = u r(u) w,
+// and of the residual stream before the next block,
+//   h = residual + scale x,   y = h r(h) w;
+// with their gradients: for u, n = u r and t = dn w,
+//   du = r (t - n mean(t n)),   dw = sum over rows of dn n.
+// Bound by memory: every row is read and written once, from and to registers.
+// A row is TPR threads (a power of two, as few as hold it in IT pieces of VEC
+// elements each), so that short heads share a wave and long rows a workgroup.
+// The sum of squares is kept in 64 bits: two instructions for each element, which
+// memory hides, and no row of finite values is lost to an overflow.
+#include "kdn_act.h"
+#include "kdn_norm.h"
+
+namespace kdn {
+namespace norm {
+
+constexpr int NT = 256, NT_MAX = 1024;
+
+// Sum over the TPR threads of a row; every thread gets it.  Rows of several waves
+// meet in LDS, so that all threads of the workgroup have to come here.
+__device__ __forceinline__ double row_sum(double x, int tpr, double *lds) {
+    const int n = tpr < WAVE ? tpr : WAVE;
+    for (int off = n >> 1; off >= 1; off >>= 1)
+        x += __shfl_xor(x, off, WAVE);
+    if (tpr > WAVE) {
+        __syncthreads();             // the sums before have been read
+        if ((threadIdx.x & (WAVE - 1)) == 0)
+            lds[threadIdx.x / WAVE] = x;
+        __syncthreads();
+        const double *row = lds + threadIdx.x / tpr * (tpr / WAVE);
+        x = row[0];
+        for (int i = 1; i < tpr / WAVE; ++i)
+            x += row[i];
+    }
+    return x;
+}
+
+// (m)^(-1/2) of a positive m in float32's range of roots: m is brought near 1 by
+// an even power of two, for v_rsq_f32 (an ulp); float32 calls add a Newton step.
+template <bool FINE> __device__ __forceinline__ float inv_sqrt(double m) {
+    const int k = __builtin_amdgcn_frexp_exp(m) >> 1;
+    const double s = __builtin_amdgcn_ldexp(m, -2 * k);
+    float r = __builtin_amdgcn_rsqf((float)s);
+    if constexpr (FINE) {
+        const double y = r;
+        if (r > 0.f && r < 3e38f)
+            r = (float)(y * (1.5 - 0.5 * s * y * y));
+    }
+    return __builtin_amdgcn_ldexpf(r, -k);
+}
+
+template <bool FINE> __device__ __forceinline__ float act_f32(int act, float z) {
+    if (act == KDN_ACT_NONE)
+        return z;
+    const float g = sigmoid_f32<FINE>(z);
+    return act == KDN_ACT_SILU ? z * g : g;
+}
+template <bool FINE>
+__device__ __forceinline__ void act_grad(int act, float z, float &y, float &dy) {
+    float g, rest;
+    if (act == KDN_ACT_NONE) {
+        y = z;
+        dy = 1.f;
+        return;
+    }
+    sigmoid2<FINE>(z, g, rest);
+    y = act == KDN_ACT_SILU ? z * g : g;
+    dy = act == KDN_ACT_SILU ? fmaf(y, rest, g) : g * rest;
+}
+
+// Where a thread is: its row's slot in the workgroup, its first element of piece i.
+struct Lane {
+    int tpr, slot, lane;
+    __device__ __forceinline__ Lane(int tpr_) : tpr(tpr_) {
+        slot = threadIdx.x / tpr;
+        lane = threadIdx.x % tpr;
+    }
+    template <int VEC> __device__ __forceinline__ int at(int i) const {
+        return (i * tpr + lane) * VEC;
+    }
+};
+
+template <typename T, int VEC, int IT>
+__global__ __launch_bounds__(NT_MAX) void gated_norm_kernel(GatedNormParams P, int tpr) {
+    constexpr bool FINE = sizeof(T) == 4;
+    __shared__ double lds[NT_MAX / WAVE];
+    const Lane L(tpr);
+    const long row = (long)blockIdx.x * (blockDim.x / tpr) + L.slot, rows = P.tokens * P.H;
+    const bool in = row < rows;
+    const long t = in ? row / P.H : 0;
+    const int h = in ? (int)(row - t * P.H) : 0;
+    const T *x = static_cast<const T *>(P.x) + t * P.x_stride + (long)h * P.d;
+    const T *z = static_cast<const T *>(P.z) + t * P.z_stride + (long)h * P.d;
+    const float *w = P.weight + (P.per_head ? (long)h * P.d : 0);
+    Pack<T, VEC> xs[IT], zs[IT];
+    Pack<float, VEC> ws[IT];
+#pragma unroll
+    for (int i = 0; i < IT; ++i) {
+        const int at = L.at<VEC>(i);
+        xs[i].zero();
+        zs[i].zero();
+        ws[i].zero();
+        if (in && at < P.d) {
+            xs[i].load(x + at, P.d - at);
+            if (P.z)
+                zs[i].load(z + at, P.d - at);
+            ws[i].load(w + at, P.d - at);
+        }
+    }
+    float u[IT][VEC];
+    double sum = 0.;
+#pragma unroll
+    for (int i = 0; i < IT; ++i)
+#pragma unroll
+        for (int e = 0; e < VEC; ++e) {
+            u[i][e] = xs[i].get(e);
+            if (P.z && P.gate_first)
+                u[i][e] *= act_f32<FINE>(P.act, zs[i].get(e));
+            sum = fma((double)u[i][e], (double)u[i][e], sum);
+        }
+    const float r = inv_sqrt<FINE>(row_sum(sum, tpr, lds) / P.d + (double)P.eps);
+    T *y = static_cast<T *>(P.y) + row * P.d;
+#pragma unroll
+    for (int i = 0; i < IT; ++i) {
+        Pack<T, VEC> out;
+#pragma unroll
+        for (int e = 0; e < VEC; ++e) {
+            float v = u[i][e] * r * ws[i].get(e);
+            if (P.z && !P.gate_first)
+                v *= act_f32<FINE>(P.act, zs[i].get(e));
+            out.set(e, v);
+        }
+        const int at = L.at<VEC>(i);
+        if (in && at < P.d)
+            out.store(y + at, P.d - at);
+    }
+}
+
+// A workgroup's sums of N values of each column over its rows, in the order of the
+// rows' slots, into ws[column].
+template <int VEC, int IT>
+__device__ __forceinline__ void column_sums(const float (&v)[IT][VEC], const Lane &L, int d,
+                                            float *lds, float *out) {
+    const int slots = blockDim.x / L.tpr;
+#pragma unroll
+    for (int i = 0; i < IT; ++i)
+#pragma unroll
+        for (int e = 0; e < VEC; ++e) {
+            float s = v[i][e];
+            if (slots > 1) {
+                __syncthreads();
+                lds[threadIdx.x] = s;
+                __syncthreads();
+                if (L.slot == 0)
+                    for (int q = 1; q < slots; ++q)
+                        s += lds[q * L.tpr + L.lane];
+            }
+            const int at = L.at<VEC>(i) + e;
+            if (L.slot == 0 && at < d)
+                out[at] = s;
+        }
+}
+
+template <typename T, int VEC, int IT>
+__global__ __launch_bounds__(NT_MAX) void gated_norm_grad_kernel(GatedNormParams P, int tpr) {
+    constexpr bool FINE = sizeof(T) == 4;
+    __shared__ double lds[NT_MAX / WAVE];
+    __shared__ float cols[NT_MAX];
+    const Lane L(tpr);
+    const int slots = blockDim.x / tpr;
+    // weight by head: a workgroup has one head's rows; else rows of all heads
+    const int head = P.per_head ? blockIdx.y : 0, heads = P.per_head ? 1 : P.H;
+    const long rows = P.tokens * heads;
+    const float *w = P.weight + (long)head * P.d;
+    Pack<float, VEC> ws[IT];
+    float dw[IT][VEC];
+#pragma unroll
+    for (int i = 0; i < IT; ++i) {
+        ws[i].zero();
+        if (L.at<VEC>(i) < P.d)
+            ws[i].load(w + L.at<VEC>(i), P.d - L.at<VEC>(i));
+#pragma unroll
+        for (int e = 0; e < VEC; ++e)
+            dw[i][e] = 0.f;
+    }
+    // the same number of rounds for every thread: they meet in row_sum
+    for (long first = (long)blockIdx.x * slots; first < rows; first += (long)P.parts * slots) {
+        const long row = first + L.slot;
+        const bool in = row < rows;
+        const long t = in ? row / heads : 0;
+        const int h = head + (in ? (int)(row - t * heads) : 0);
+        const T *x = static_cast<const T *>(P.x) + t * P.x_stride + (long)h * P.d;
+        const T *z = static_cast<const T *>(P.z) + t * P.z_stride + (long)h * P.d;
+        const long out = (t * P.H + h) * P.d;
+        const T *dy = static_cast<const T *>(P.d_y) + out;
+        Pack<T, VEC> xs[IT], zs[IT], gs[IT];
+#pragma unroll
+        for (int i = 0; i < IT; ++i) {
+            const int at = L.at<VEC>(i);
+            xs[i].zero();
+            zs[i].zero();
+            gs[i].zero();
+            if (in && at < P.d) {
+                xs[i].load(x + at, P.d - at);
+                gs[i].load(dy + at, P.d - at);
+                if (P.z)
+                    zs[i].load(z + at, P.d - at);
+            }
+        }
+        // u, the gradient of the norm's output dn, the gate and its derivative
+        double sq = 0., dot = 0.;
+#pragma unroll
+        for (int i = 0; i < IT; ++i)
+#pragma unroll
+            for (int e = 0; e < VEC; ++e) {
+                float u = xs[i].get(e), dn = gs[i].get(e);
+                if (P.z) {
+                    const float a = act_f32<FINE>(P.act, zs[i].get(e));
+                    if (P.gate_first)
+                        u *= a;
+                    else
+                        dn *= a;
+                }
+                sq = fma((double)u, (double)u, sq);
+                dot = fma((double)(dn * ws[i].get(e)), (double)u, dot);
+            }
+        const float r = inv_sqrt<FINE>(row_sum(sq, tpr, lds) / P.d + (double)P.eps);
+        // mean(t n)
+        const float m = (float)(row_sum(dot, tpr, lds) * (double)r / P.d);
+#pragma unroll
+        for (int i = 0; i < IT; ++i) {
+            Pack<T, VEC> dx, dz;
+            const int at = L.at<VEC>(i);
+#pragma unroll
+            for (int e = 0; e < VEC; ++e) {
+                const float xe = xs[i].get(e), ge = gs[i].get(e), we = ws[i].get(e);
+                float a = 1.f, da = 0.f;
+                if (P.z)
+                    act_grad<FINE>(P.act, zs[i].get(e), a, da);
+                const float n = (P.z && P.gate_first ? xe * a : xe) * r;
+                const float dn = P.z && !P.gate_first ? ge * a : ge;
+                const float du = r * (dn * we - n * m);
+                if (in && at < P.d)
+                    dw[i][e] = fmaf(dn, n, dw[i][e]);
+                dx.set(e, P.z && P.gate_first ? du * a : du);
+                dz.set(e, P.gate_first ? du * xe * da : ge * n * we * da);
+            }
+            if (in && at < P.d) {
+                dx.store(static_cast<T *>(P.dx) + out + at, P.d - at);
+                if (P.z)
+                    dz.store(static_cast<T *>(P.dz) + out + at, P.d - at);
+            }
+        }
+    }
+    column_sums<VEC, IT>(dw, L, P.d, cols,
+                         P.ws + ((long)blockIdx.x * gridDim.y + head) * P.d);
+}
+
+template <typename T, typename S, int VEC, int IT>
+__global__ __launch_bounds__(NT_MAX) void residual_norm_kernel(ResidualNormParams P, int tpr) {
+    constexpr bool FINE = sizeof(T) == 4;
+    __shared__ double lds[NT_MAX / WAVE];
+    const Lane L(tpr);
+    const long row = (long)blockIdx.x * (blockDim.x / tpr) + L.slot;
+    const bool in = row < P.tokens;
+    const T *x = static_cast<const T *>(P.x) + (in ? row : 0) * P.x_stride;
+    const S *res = static_cast<const S *>(P.residual) + (in ? row : 0) * P.r_stride;
+    Pack<T, VEC> xs[IT];
+    Pack<S, VEC> rs[IT];
+    Pack<float, VEC> ws[IT];
+#pragma unroll
+    for (int i = 0; i < IT; ++i) {
+        const int at = L.at<VEC>(i);
+        xs[i].zero();
+        rs[i].zero();
+        ws[i].zero();
+        if (in && at < P.D) {
+            xs[i].load(x + at, P.D - at);
+            rs[i].load(res + at, P.D - at);
+            ws[i].load(P.weight + at, P.D - at);
+        }
+    }
+    float h[IT][VEC];
+    double sum = 0.;
+#pragma unroll
+    for (int i = 0; i < IT; ++i) {
+        const int at = L.at<VEC>(i);
+        Pack<float, VEC> sc;
+        sc.zero();
+        if (P.scale_n > 1 && at < P.D)
+            sc.load(P.scale + at, P.D - at);
+        Pack<S, VEC> out;
+#pragma unroll
+        for (int e = 0; e < VEC; ++e) {
+            const float s = P.scale_n == 0 ? 1.f : (P.scale_n == 1 ? P.scale[0] : sc.get(e));
+            h[i][e] = fmaf(s, xs[i].get(e), rs[i].get(e));
+            sum = fma((double)h[i][e], (double)h[i][e], sum);
+            out.set(e, h[i][e]);
+        }
+        if (in && at < P.D)
+            out.store(static_cast<S *>(P.h) + row * P.D + at, P.D - at);
+    }
+    const float r = inv_sqrt<FINE>(row_sum(sum, tpr, lds) / P.D + (double)P.eps);
+#pragma unroll
+    for (int i = 0; i < IT; ++i) {
+        const int at = L.at<VEC>(i);
+        Pack<T, VEC> out;
+#pragma unroll
+        for (int e = 0; e < VEC; ++e)
+            out.set(e, h[i][e] * r * ws[i].get(e));
+        if (in && at < P.D)
+            out.store(static_cast<T *>(P.y) + row * P.D + at, P.D - at);
+    }
+}
+
+template <typename T, typename S, int VEC, int IT>
+__global__ __launch_bounds__(NT_MAX) void residual_norm_grad_kernel(ResidualNormParams P, int tpr) {
+    constexpr bool FINE = sizeof(T) == 4;
+    __shared__ double lds[NT_MAX / WAVE];
+    __shared__ float cols[NT_MAX];
+    const Lane L(tpr);
+    const int slots = blockDim.x / tpr;
+    Pack<float, VEC> ws[IT], sc[IT];
+    float dw[IT][VEC], ds[IT][VEC];
+    const float one = P.scale_n == 1 ? P.scale[0] : 1.f;
+#pragma unroll
+    for (int i = 0; i < IT; ++i) {
+        const int at = L.at<VEC>(i);
+        ws[i].zero();
+        sc[i].zero();
+        if (at < P.D) {
+            ws[i].load(P.weight + at, P.D - at);
+            if (P.scale_n > 1)
+                sc[i].load(P.scale + at, P.D - at);
+        }
+#pragma unroll
+        for (int e = 0; e < VEC; ++e)
+            dw[i][e] = ds[i][e] = 0.f;
+    }
+    for (long first = (long)blockIdx.x * slots; first < P.tokens; first += (long)P.parts * slots) {
+        const long row = first + L.slot;
+        const bool in = row < P.tokens;
+        const S *hrow = static_cast<const S *>(P.residual) + (in ? row : 0) * P.r_stride;
+        const T *x = static_cast<const T *>(P.x) + (in ? row : 0) * P.x_stride;
+        const long out = (in ? row : 0) * P.D;
+        Pack<S, VEC> hs[IT], dh[IT];
+        Pack<T, VEC> gs[IT], xs[IT];
+#pragma unroll
+        for (int i = 0; i < IT; ++i) {
+            const int at = L.at<VEC>(i);
+            hs[i].zero();
+            dh[i].zero();
+            gs[i].zero();
+            xs[i].zero();
+            if (in && at < P.D) {
+                hs[i].load(hrow + at, P.D - at);
+                gs[i].load(static_cast<const T *>(P.d_y) + out + at, P.D - at);
+                if (P.d_h)
+                    dh[i].load(static_cast<const S *>(P.d_h) + out + at, P.D - at);
+                if (P.dscale)
+                    xs[i].load(x + at, P.D - at);
+            }
+        }
+        double sq = 0., dot = 0.;
+#pragma unroll
+        for (int i = 0; i < IT; ++i)
+#pragma unroll
+            for (int e = 0; e < VEC; ++e) {
+                const double u = hs[i].get(e);
+                sq = fma(u, u, sq);
+                dot = fma((double)(gs[i].get(e) * ws[i].get(e)), u, dot);
+            }
+        const float r = inv_sqrt<FINE>(row_sum(sq, tpr, lds) / P.D + (double)P.eps);
+        const float m = (float)(row_sum(dot, tpr, lds) * (double)r / P.D);
+#pragma unroll
+        for (int i = 0; i < IT; ++i) {
+            Pack<S, VEC> dres;
+            Pack<T, VEC> dx;
+            const int at = L.at<VEC>(i);
+#pragma unroll
+            for (int e = 0; e < VEC; ++e) {
+                const float g = gs[i].get(e), n = hs[i].get(e) * r;
+                const float d = fmaf(r, g * ws[i].get(e) - n * m, dh[i].get(e));
+                if (in && at < P.D) {
+                    dw[i][e] = fmaf(g, n, dw[i][e]);
+                    ds[i][e] = fmaf(d, xs[i].get(e), ds[i][e]);
+                }
+                dres.set(e, d);
+                dx.set(e, d * (P.scale_n > 1 ? sc[i].get(e) : one));
+            }
+            if (in && at < P.D) {
+                dres.store(static_cast<S *>(P.dresidual) + out + at, P.D - at);
+                if (P.dx)
+                    dx.store(static_cast<T *>(P.dx) + out + at, P.D - at);
+            }
+        }
+    }
+    column_sums<VEC, IT>(dw, L, P.D, cols, P.ws + (long)blockIdx.x * P.D);
+    if (!P.dscale)
+        return;
+    float *part = P.ws + (long)P.parts * P.D;
+    if (P.scale_n > 1) {
+        column_sums<VEC, IT>(ds, L, P.D, cols, part + (long)blockIdx.x * P.D);
+        return;
+    }
+    // one scale: its sum over the workgroup's columns and rows
+    float s = 0.f;
+#pragma unroll
+    for (int i = 0; i < IT; ++i)
+#pragma unroll
+        for (int e = 0; e < VEC; ++e)
+            s += ds[i][e];
+    __syncthreads();
+    cols[threadIdx.x] = s;
+    __syncthreads();
+    for (int n = blockDim.x / 2; n >= 1; n >>= 1) {
+        if ((int)threadIdx.x < n)
+            cols[threadIdx.x] += cols[threadIdx.x + n];
+        __syncthreads();
+    }
+    if (threadIdx.x == 0)
+        part[blockIdx.x] = cols[0];
+}
+
+// out[c] = sum over parts of ws[part][c], in order, in 64 bits; 64 columns a
+// workgroup.  Two arrays in one launch: those of ws2 behind those of ws.
+struct Sums {
+    const float *ws, *ws2;
+    float *out, *out2;
+    long n, n2;
+    int parts;
+};
+__global__ __launch_bounds__(NT_MAX) void sum_parts_kernel(Sums S) {
+    const int lane = threadIdx.x & (WAVE - 1), wv = threadIdx.x / WAVE, nw = NT_MAX / WAVE;
+    const long wide = (S.n + WAVE - 1) / WAVE;
+    const bool second = blockIdx.x >= wide;
+    const float *ws = second ? S.ws2 : S.ws;
+    const long n = second ? S.n2 : S.n;
+    const long c = ((long)blockIdx.x - (second ? wide : 0)) * WAVE + lane;
+    double s = 0.;
+    if (c < n)
+        for (int p = wv; p < S.parts; p += nw)
+            s += (double)ws[(long)p * n + c];
+    __shared__ double sums[NT_MAX / WAVE][WAVE];
+    sums[wv][lane] = s;
+    __syncthreads();
+    if (wv == 0 && c < n) {
+        for (int q = 1; q < nw; ++q)
+            s += sums[q][lane];
+        (second ? S.out2 : S.out)[c] = (float)s;
+    }
+}
+
+hipError_t sum_parts(const Sums &S, hipStream_t st) {
+    const long wgs = (S.n + WAVE - 1) / WAVE + (S.n2 + WAVE - 1) / WAVE;
+    if (wgs == 0)
+        return hipSuccess;
+    hipLaunchKernelGGL(sum_parts_kernel, dim3((unsigned)wgs), dim3(NT_MAX), 0, st, S);
+    return hipGetLastError();
+}
+
+}  // namespace norm
+
+// FN(IT) for a row of `width` elements in pieces of V.
+#define KDN_NORM_IT(FN, width)                                                         \
+    {                                                                                  \
+        const int pieces = (width + V - 1) / V, tpr = norm_row_threads(width, V == 8);\
+        const int threads = tpr < norm::NT ? norm::NT : tpr;                           \
+        const int it = (pieces + tpr - 1) / tpr;                                       \
+        if (it <= 1)                                                                   \
+            FN(1)                                                                      \
+        if (it <= 2)                                                                   \
+            FN(2)                                                                      \
+        if constexpr (V < 8)                                                           \
+            FN(4)                                                                      \
+    }
+
+template <typename T>
+static hipError_t gated_norm_t(const GatedNormParams &P, hipStream_t st, bool back) {
+    constexpr int V = 16 / sizeof(T);
+#define KDN_GATED(IT_)                                                                      \
+    {                                                                                           \
+        const long slots = threads / tpr, rows = P.tokens * P.H;                                \
+        if (!back)                                                                              \
+            hipLaunchKernelGGL((norm::gated_norm_kernel<T, V, IT_>),                           \
+                               dim3((unsigned)((rows + slots - 1) / slots)), dim3(threads), 0,  \
+                               st, P, tpr);                                                     \
+        else                                                                                    \
+            hipLaunchKernelGGL((norm::gated_norm_grad_kernel<T, V, IT_>),                      \
+                               dim3((unsigned)P.parts, P.per_head ? P.H : 1), dim3(threads), 0, \
+                               st, P, tpr);                                                     \
+        return hipGetLastError();                                                               \
+    }
+    KDN_NORM_IT(KDN_GATED, P.d)
+#undef KDN_GATED
+    return hipErrorInvalidValue;
+}
+
+template <typename T, typename S>
+static hipError_t residual_norm_t(const ResidualNormParams &P, hipStream_t st, bool back) {
+    constexpr int V = 16 / sizeof(T);
+#define KDN_RESIDUAL(IT_)                                                                   \
+    {                                                                                           \
+        const long slots = threads / tpr;                                                       \
+        if (!back)                                                                              \
+            hipLaunchKernelGGL((norm::residual_norm_kernel<T, S, V, IT_>),                     \
+                               dim3((unsigned)((P.tokens + slots - 1) / slots)), dim3(threads), \
+                               0, st, P, tpr);                                                  \
+        else                                                                                    \
+            hipLaunchKernelGGL((norm::residual_norm_grad_kernel<T, S, V, IT_>),                \
+                               dim3((unsigned)P.parts), dim3(threads), 0, st, P, tpr);          \
+        return hipGetLastError();                                                               \
+    }
+    KDN_NORM_IT(KDN_RESIDUAL, P.D)
+#undef KDN_RESIDUAL
+    return hipErrorInvalidValue;
+}
+#undef KDN_NORM_IT
+
+hipError_t launch_gated_norm(const GatedNormParams &P, hipStream_t st) {
+    if (P.tokens * P.H * P.d == 0)
+        return hipSuccess;
+    return P.bf16 ? gated_norm_t<bf16>(P, st, false) : gated_norm_t<float>(P, st, false);
+}
+
+hipError_t launch_gated_norm_backward(const GatedNormParams &P, hipStream_t st) {
+    if ((long)P.H * P.d == 0)
+        return hipSuccess;
+    if (P.parts > 0) {
+        const hipError_t e = P.bf16 ? gated_norm_t<bf16>(P, st, true) : gated_norm_t<float>(P, st, true);
+        if (e != hipSuccess)
+            return e;
+    }
+    const long n = (long)(P.per_head ? P.H : 1) * P.d;
+    return norm::sum_parts(norm::Sums{P.ws, nullptr, P.dweight, nullptr, n, 0, P.parts}, st);
+}
+
+static hipError_t residual(const ResidualNormParams &P, hipStream_t st, bool back) {
+    if (P.bf16)
+        return P.stream_bf16 ? residual_norm_t<bf16, bf16>(P, st, back)
+                             : residual_norm_t<bf16, float>(P, st, back);
+    return residual_norm_t<float, float>(P, st, back);
+}
+
+hipError_t launch_residual_norm(const ResidualNormParams &P, hipStream_t st) {
+    return P.tokens * P.D == 0 ? hipSuccess : residual(P, st, false);
+}
+
+hipError_t launch_residual_norm_backward(const ResidualNormParams &P, hipStream_t st) {
+    if (P.D == 0)
+        return hipSuccess;
+    if (P.parts > 0) {
+        const hipError_t e = residual(P, st, true);
+        if (e != hipSuccess)
+            return e;
+    }
+    return norm::sum_parts(norm::Sums{P.ws, P.ws + (long)P.parts * P.D, P.dweight, P.dscale, P.D,
+                                      P.dscale ? P.scale_n : 0, P.parts}, st);
+}
+
+}  // namespace kdn

@@ -35,6 +35,9 @@ STATUS = {0: "KDN_OK", 1: "KDN_ERR_NULL", 2: "KDN_ERR_SHAPE",
           3: "KDN_ERR_UNSUPPORTED", 4: "KDN_ERR_ALIGN", 5: "KDN_ERR_ALIAS",
           6: "KDN_ERR_HIP", 7: "KDN_ERR_WORKSPACE", 8: "KDN_ERR_SCRATCH"}
 
+# kdn_activation and kdn_norm_order values
+ACTIVATIONS = {None: 0, "silu": 1, "sigmoid": 2}
+NORM_ORDERS = {"norm_gate": 0, "gate_norm": 1}
 # kdn_gate values
 GATE_TOKEN, GATE_HEAD, GATE_HEAD_F32 = 0, 1, 2
 
@@ -99,6 +102,27 @@ def load(path: str = LIB_PATH):
     lib.kdn_linear_prefill_backward_workspace_size.argtypes = [i] * 10 + [pk, ctypes.POINTER(i)]
     lib.kdn_linear_decode.restype = i
     lib.kdn_linear_decode.argtypes = [i] * 9 + [ll] * 3 + [vp] * 5 + [i] + [vp] * 3
+    ip = ctypes.POINTER(i)
+    lib.kdn_causal_conv.restype = i
+    lib.kdn_causal_conv.argtypes = [i] * 6 + [ll] + [vp] * 6 + [pk, vp]
+    lib.kdn_causal_conv_decode.restype = i
+    lib.kdn_causal_conv_decode.argtypes = [i] * 5 + [ll] + [vp] * 4 + [i] + [vp] * 3
+    lib.kdn_causal_conv_backward.restype = i
+    lib.kdn_causal_conv_backward.argtypes = [i] * 6 + [ll] + [vp] * 10 + [pk, vp, u64, vp]
+    lib.kdn_causal_conv_backward_workspace_size.restype = u64
+    lib.kdn_causal_conv_backward_workspace_size.argtypes = [i] * 5 + [pk, ip]
+    lib.kdn_gated_norm.restype = i
+    lib.kdn_gated_norm.argtypes = [i] * 7 + [f, ll, ll] + [vp] * 5
+    lib.kdn_gated_norm_backward.restype = i
+    lib.kdn_gated_norm_backward.argtypes = [i] * 7 + [f, ll, ll] + [vp] * 8 + [u64, vp]
+    lib.kdn_gated_norm_backward_workspace_size.restype = u64
+    lib.kdn_gated_norm_backward_workspace_size.argtypes = [i] * 4 + [ip]
+    lib.kdn_residual_norm.restype = i
+    lib.kdn_residual_norm.argtypes = [i] * 5 + [f, ll, ll] + [vp] * 7
+    lib.kdn_residual_norm_backward.restype = i
+    lib.kdn_residual_norm_backward.argtypes = [i] * 5 + [f, ll, ll] + [vp] * 11 + [u64, vp]
+    lib.kdn_residual_norm_backward_workspace_size.restype = u64
+    lib.kdn_residual_norm_backward_workspace_size.argtypes = [i] * 3 + [ip]
     lib.kdn_status_string.restype = ctypes.c_char_p
     lib.kdn_status_string.argtypes = [i]
     lib.kdn_chunk_prefill_chunk_size.restype = i
@@ -841,4 +865,353 @@ def linear_prefill_backward(q, k, v, d_o, log_alpha, S0=None, dS_out=None, table
           gate, qs, ks, vs, _p(q), _p(k), _p(v), _p(log_alpha), _p(S0), _p(d_o), _p(dS_out),
           _p(out["dq"]), _p(out["dk"]), _p(out["dv"]), _p(out["dlog_alpha"]), _p(out["dS0"]), pk,
           _p(workspace), nws)
+    return out
+
+
+# ---------------------------------------------------------------------------
+# Around a recurrence: the short causal convolution in front of it, the norms
+# behind and before it.
+# ---------------------------------------------------------------------------
+_f32 = torch.float32
+
+
+def _dtype(name, x):
+    """dtype and device of a call's first per-token tensor."""
+    if not isinstance(x, torch.Tensor):
+        raise TypeError(f"kdn: {name} must be a tensor")
+    if x.dtype not in DTYPES:
+        raise ValueError(f"kdn: {name} has dtype {x.dtype}, expected float32 or bfloat16")
+    return x.dtype, x.device
+
+
+def _strided(name, x, lead, tail, dtype, dev):
+    """Checks of a per-token tensor [*lead, *tail] whose rows may be slices of
+    wider ones; returns the elements between tokens (0: contiguous)."""
+    if not isinstance(x, torch.Tensor):
+        raise TypeError(f"kdn: {name} must be a tensor")
+    if x.shape != lead + tail:
+        raise ValueError(f"kdn: {name} has shape {tuple(x.shape)}, expected {lead + tail}")
+    if x.dtype is not dtype:
+        raise ValueError(f"kdn: {name} has dtype {x.dtype}, expected {dtype}")
+    if x.device != dev:
+        raise ValueError(f"kdn: {name} is on {x.device}, the other tensors on {dev}")
+    if x.is_contiguous():
+        return 0
+    if x.numel() == 0:
+        return 0
+    n, st, row = len(lead), x.stride(), 1
+    for size, step in zip(reversed(tail), reversed(st[n:])):
+        if size > 1 and step != row:
+            raise ValueError(f"kdn: {name} must have contiguous rows")
+        row *= size
+    # one distance between all tokens; dimensions of one element have none
+    dist, tokens = None, 1
+    for size, step in zip(reversed(lead), reversed(st[:n])):
+        if size > 1:
+            if dist is None:
+                if step % tokens:
+                    raise ValueError(f"kdn: {name} must have rows at one distance")
+                dist = step // tokens
+            elif step != dist * tokens:
+                raise ValueError(f"kdn: {name} must have rows at one distance")
+        tokens *= size
+    if dist is None:
+        return 0
+    if dist < row:
+        raise ValueError(f"kdn: {name} must have rows that do not overlap")
+    return dist
+
+
+def _activation(activation, among):
+    if activation not in among:
+        raise ValueError(f"kdn: activation must be one of {among}, not {activation!r}")
+    return ACTIVATIONS[activation]
+
+
+def _batch(x, tables, states, ndim, what):
+    """(lead, N, T, kdn_packed or None, pool) of a dense or packed batch whose
+    per-token tensors have ``ndim`` dimensions behind the tokens; the pool is that of
+    the first of ``states`` which is given."""
+    if tables is None:
+        if x.dim() != 2 + ndim:
+            raise ValueError(f"kdn: {what} has shape {tuple(x.shape)}, expected [B, T, ..]")
+        B, T = x.shape[:2]
+        return (B, T), _int32("B", B), _int32("T", T), None, B
+    if x.dim() != 1 + ndim:
+        raise ValueError(f"kdn: {what} has shape {tuple(x.shape)}, expected [tokens, ..]")
+    if x.shape[0] != tables.tokens:
+        raise ValueError(f"kdn: {what} has {x.shape[0]} rows, the tables {tables.tokens}")
+    pool = next((_int32("pool", s.shape[0]) for s in states
+                 if isinstance(s, torch.Tensor) and s.dim() > 0), None)
+    pk, N = _packed(tables, pool, x.device)
+    return (x.shape[0],), N, 0, pk, N if pool is None else pool
+
+
+def _workspace(n, workspace, dev, stream):
+    """A workspace of n bytes if none is given, and its size."""
+    if workspace is None:
+        workspace = _new((n,), torch.uint8, dev, stream) if n else None
+    if workspace is None:
+        return None, 0
+    _same("workspace", workspace, (workspace.numel(),), torch.uint8, dev)
+    return workspace, workspace.numel()
+
+
+def _taps(weight, C):
+    if not isinstance(weight, torch.Tensor) or weight.dim() != 2:
+        raise ValueError("kdn: weight must be a tensor [C, W]")
+    return _int32("W", weight.shape[1])
+
+
+def causal_conv(x, weight, bias=None, state0=None, tables=None, activation="silu", out=None,
+                stream=None):
+    """Short causal convolution of each channel and its activation ("silu" or
+    None): s_t = bias + sum_j weight[:, j] x_{t-W+1+j}, y = s sigmoid(s).
+
+    Dense: x [B,T,C] (float32 or bf16, rows may be slices of one wider tensor);
+    packed (``tables`` from :func:`sequence_tables`): x [tokens,C].  weight [C,W]
+    float32, W 2 to 4, bias [C] float32 or None.  ``state0`` [B or pool,W-1,C] in
+    x's dtype holds the rows before each sequence (None: zeros).  ``out`` may pass
+    (y, state_out); state_out may be state0 (in place) or None (not wanted).
+    Without it state_out is new, and for a packed batch with state0 the pool state0
+    itself, updated in place.  Rows of y behind the last sequence are left as they
+    were.  Returns (y, state_out)."""
+    lib = load()
+    dt, dev = _dtype("x", x)
+    act = _activation(activation, (None, "silu"))
+    lead, N, T, pk, pool = _batch(x, tables, (state0, out[1] if out is not None else None), 1, "x")
+    C = _int32("C", x.shape[-1])
+    W = _taps(weight, C)
+    xs = _strided("x", x, lead, (C,), dt, dev)
+    s_shape = (pool, W - 1, C)
+    if out is None:
+        y = _new(lead + (C,), dt, dev, stream)
+        if tables is not None and state0 is not None:
+            S = state0
+        elif tables is not None and tables.slots is not None:
+            raise ValueError("kdn: a pool for the tables' slots must be given (state0 or out)")
+        else:
+            S = _new((pool, max(W - 1, 0), C), dt, dev, stream)
+    else:
+        y, S = out
+    _same("weight", weight, (C, W), _f32, dev)
+    _same("bias", bias, (C,), _f32, dev)
+    _same("state0", state0, s_shape, dt, dev)
+    _same("y", y, lead + (C,), dt, dev)
+    _same("state_out", S, s_shape, dt, dev)
+    _call(lib.kdn_causal_conv, dev, stream, DTYPES[dt], N, T, C, W, act, xs, _p(x), _p(weight),
+          _p(bias), _p(state0), _p(y), _p(S), pk)
+    return y, S
+
+
+def causal_conv_decode(x, weight, state, bias=None, activation="silu", slots=None, y=None,
+                       stream=None):
+    """One token of :func:`causal_conv` for N rows x [N,C].  ``state`` [P,W-1,C] in
+    x's dtype is a pool of states, updated in place; ``slots`` [N] int32 is each
+    row's state (None: row n).  A row whose slot is not in the pool is skipped, its y
+    left as it was (zero in a new y).  Returns y [N,C]."""
+    lib = load()
+    dt, dev = _dtype("x", x)
+    act = _activation(activation, (None, "silu"))
+    if x.dim() != 2:
+        raise ValueError(f"kdn: x has shape {tuple(x.shape)}, expected [N, C]")
+    N, C = _int32("N", x.shape[0]), _int32("C", x.shape[1])
+    W = _taps(weight, C)
+    xs = _strided("x", x, (N,), (C,), dt, dev)
+    if not isinstance(state, torch.Tensor) or state.dim() != 3:
+        raise ValueError("kdn: state must be a tensor [P, W - 1, C]")
+    pool = _int32("pool", state.shape[0])
+    if y is None:
+        y = _new((N, C), dt, dev, stream, zero=slots is not None)
+    _same("weight", weight, (C, W), _f32, dev)
+    _same("bias", bias, (C,), _f32, dev)
+    _same("state", state, (pool, W - 1, C), dt, dev)
+    _same("y", y, (N, C), dt, dev)
+    _same("slots", slots, (N,), torch.int32, dev)
+    _call(lib.kdn_causal_conv_decode, dev, stream, DTYPES[dt], N, C, W, act, xs, _p(x), _p(weight),
+          _p(bias), _p(slots), pool, _p(state), _p(y))
+    return y
+
+
+def causal_conv_backward(x, weight, d_y, bias=None, state0=None, dstate_out=None, tables=None,
+                         activation="silu", out=None, workspace=None, stream=None):
+    """Gradients of :func:`causal_conv` for the cotangents d_y (shaped as y) and
+    dstate_out (shaped as state_out; None: zero).  Returns a dict of dx and dstate0
+    in x's dtype, dweight and dbias float32.  Rows behind the last sequence of a
+    packed batch get zero, and so do states of dstate0 without a sequence.  ``out``
+    may pass such a dict (dbias and dstate0 may be None: not wanted; in a given
+    dstate0 states without a sequence are left as they were).  A packed batch
+    without any of state0, dstate_out and out["dstate0"] has no pool: dstate0 is by
+    sequence and slots are not looked at."""
+    lib = load()
+    dt, dev = _dtype("x", x)
+    act = _activation(activation, (None, "silu"))
+    lead, N, T, pk, pool = _batch(x, tables, (state0, dstate_out, (out or {}).get("dstate0")), 1, "x")
+    C = _int32("C", x.shape[-1])
+    W = _taps(weight, C)
+    xs = _strided("x", x, lead, (C,), dt, dev)
+    s_shape = (pool, W - 1, C)
+    if out is None:
+        out = dict(dx=_new(lead + (C,), dt, dev, stream), dweight=_new((C, W), _f32, dev, stream),
+                   dbias=None if bias is None else _new((C,), _f32, dev, stream),
+                   dstate0=_new((pool, max(W - 1, 0), C), dt, dev, stream, zero=tables is not None))
+    for name, t, shape, kind in (("weight", weight, (C, W), _f32), ("bias", bias, (C,), _f32),
+                                 ("d_y", d_y, lead + (C,), dt), ("state0", state0, s_shape, dt),
+                                 ("dstate_out", dstate_out, s_shape, dt),
+                                 ("dx", out["dx"], lead + (C,), dt),
+                                 ("dweight", out["dweight"], (C, W), _f32),
+                                 ("dbias", out["dbias"], (C,), _f32),
+                                 ("dstate0", out["dstate0"], s_shape, dt)):
+        _same(name, t, shape, kind, dev)
+    st = ctypes.c_int(0)
+    n = lib.kdn_causal_conv_backward_workspace_size(DTYPES[dt], N, T, C, W, pk, ctypes.byref(st))
+    _check(lib, st.value)
+    workspace, n = _workspace(n, workspace, dev, stream)
+    _call(lib.kdn_causal_conv_backward, dev, stream, DTYPES[dt], N, T, C, W, act, xs, _p(x),
+          _p(weight), _p(bias), _p(state0), _p(d_y), _p(dstate_out), _p(out["dx"]),
+          _p(out["dweight"]), _p(out["dbias"]), _p(out["dstate0"]), pk, _p(workspace), n)
+    return out
+
+
+def _heads(x, weight, gate, order, activation):
+    """Sizes and codes of a gated norm."""
+    dt, dev = _dtype("x", x)
+    if x.dim() < 2:
+        raise ValueError(f"kdn: x has shape {tuple(x.shape)}, expected [.., H, d]")
+    if order not in NORM_ORDERS:
+        raise ValueError(f"kdn: order must be one of {tuple(NORM_ORDERS)}, not {order!r}")
+    act = _activation(activation, (None, "silu", "sigmoid"))
+    lead, (H, d) = x.shape[:-2], x.shape[-2:]
+    if not isinstance(weight, torch.Tensor) or weight.dim() not in (1, 2):
+        raise ValueError("kdn: weight must be a tensor [d] or [H, d]")
+    per_head = weight.dim() == 2
+    _same("weight", weight, (H, d) if per_head else (d,), _f32, dev)
+    tokens = 1
+    for n in lead:
+        tokens *= n
+    xs = _strided("x", x, lead, (H, d), dt, dev)
+    zs = 0 if gate is None else _strided("gate", gate, lead, (H, d), dt, dev)
+    return (dt, dev, _int32("tokens", tokens), _int32("H", H), _int32("d", d), NORM_ORDERS[order],
+            act, int(per_head), xs, zs)
+
+
+def gated_norm(x, weight, gate=None, eps=1e-5, order="norm_gate", activation="silu", out=None,
+               stream=None):
+    """RMS norm of each head's d values with its gate, r(u) = (mean(u^2) + eps)^-1/2:
+    order "norm_gate": y = x r(x) weight act(gate); "gate_norm": u = x act(gate),
+    y = u r(u) weight.  x and gate [..,H,d] (float32 or bf16; rows [H,d] may be
+    slices of wider ones), weight [d] float32 for all heads or [H,d]; activation
+    "silu", "sigmoid" or None; gate None: no gate.  Returns y [..,H,d] (``out`` if
+    given)."""
+    lib = load()
+    dt, dev, tokens, H, d, order, act, per_head, xs, zs = _heads(x, weight, gate, order, activation)
+    if out is None:
+        out = _new(x.shape, dt, dev, stream)
+    _same("out", out, x.shape, dt, dev)
+    _call(lib.kdn_gated_norm, dev, stream, DTYPES[dt], tokens, H, d, order, act, per_head,
+          float(eps), xs, zs, _p(x), _p(weight), _p(gate), _p(out))
+    return out
+
+
+def gated_norm_backward(x, weight, d_y, gate=None, eps=1e-5, order="norm_gate", activation="silu",
+                        out=None, workspace=None, stream=None):
+    """Gradients of :func:`gated_norm` for d_y [..,H,d]: a dict of dx and dgate (None
+    without a gate) in x's dtype and dweight float32, or ``out``, such a dict."""
+    lib = load()
+    dt, dev, tokens, H, d, order, act, per_head, xs, zs = _heads(x, weight, gate, order, activation)
+    if out is None:
+        out = dict(dx=_new(x.shape, dt, dev, stream),
+                   dgate=None if gate is None else _new(x.shape, dt, dev, stream),
+                   dweight=_new(weight.shape, _f32, dev, stream))
+    for name, t, shape, kind in (("d_y", d_y, x.shape, dt), ("dx", out["dx"], x.shape, dt),
+                                 ("dgate", out["dgate"], x.shape, dt),
+                                 ("dweight", out["dweight"], weight.shape, _f32)):
+        _same(name, t, shape, kind, dev)
+    st = ctypes.c_int(0)
+    n = lib.kdn_gated_norm_backward_workspace_size(tokens, H, d, per_head, ctypes.byref(st))
+    _check(lib, st.value)
+    workspace, n = _workspace(n, workspace, dev, stream)
+    _call(lib.kdn_gated_norm_backward, dev, stream, DTYPES[dt], tokens, H, d, order, act, per_head,
+          float(eps), xs, zs, _p(x), _p(weight), _p(gate), _p(d_y), _p(out["dx"]),
+          _p(out["dgate"]), _p(out["dweight"]), _p(workspace), n)
+    return out
+
+
+def _residual(x, residual, weight, scale):
+    """Sizes and checks common to the residual norm and its gradients; x may be None
+    (the stream's type then stands for it)."""
+    sdt, dev = _dtype("residual", residual)
+    dt = sdt if x is None else _dtype("x", x)[0]
+    if residual.dim() < 1:
+        raise ValueError("kdn: residual must be a tensor [.., D]")
+    lead, D = residual.shape[:-1], residual.shape[-1]
+    tokens = 1
+    for n in lead:
+        tokens *= n
+    rs = _strided("residual", residual, lead, (D,), sdt, dev)
+    xs = 0 if x is None else _strided("x", x, lead, (D,), dt, dev)
+    _same("weight", weight, (D,), _f32, dev)
+    if weight is None:
+        raise TypeError("kdn: weight must be a tensor [D]")
+    scale_n = 0
+    if scale is not None:
+        if not isinstance(scale, torch.Tensor):
+            raise TypeError("kdn: scale must be a tensor [1] or [D] or None")
+        scale_n = 1 if scale.shape == (1,) else D
+        _same("scale", scale, (scale_n,), _f32, dev)
+    return dt, sdt, dev, _int32("tokens", tokens), _int32("D", D), scale_n, xs, rs
+
+
+def residual_norm(x, residual, weight, scale=None, eps=1e-5, out=None, stream=None):
+    """The residual stream and the RMS norm before the next block:
+    h = residual + scale x, y = h (mean(h^2) + eps)^-1/2 weight.  x [..,D] (float32
+    or bf16), residual [..,D] in x's dtype or float32, weight [D] float32, scale [1]
+    or [D] float32 (None: one); rows of x and residual may be slices of wider ones.
+    ``out`` may pass (y, h); h may be a contiguous residual itself (in place).
+    Returns (y, h): y in x's dtype, h in the residual's."""
+    lib = load()
+    dt, sdt, dev, tokens, D, scale_n, xs, rs = _residual(x, residual, weight, scale)
+    if x is None:
+        raise TypeError("kdn: x must be a tensor")
+    y, h = out if out is not None else (_new(x.shape, dt, dev, stream),
+                                        _new(x.shape, sdt, dev, stream))
+    for name, t, kind in (("y", y, dt), ("h", h, sdt)):
+        if t is None:
+            raise TypeError(f"kdn: {name} must be a tensor")
+        _same(name, t, x.shape, kind, dev)
+    _call(lib.kdn_residual_norm, dev, stream, DTYPES[dt], DTYPES[sdt], tokens, D, scale_n,
+          float(eps), xs, rs, _p(x), _p(residual), _p(weight), _p(scale), _p(y), _p(h))
+    return y, h
+
+
+def residual_norm_backward(x, h, weight, d_y, d_h=None, scale=None, eps=1e-5, out=None,
+                           workspace=None, stream=None):
+    """Gradients of :func:`residual_norm` from h, its second output, for d_y (x's
+    dtype) and d_h (h's dtype; None: zero): a dict of dx (x's dtype), dresidual (h's),
+    dweight and dscale (float32; None without a scale), or ``out``, such a dict (dx
+    and dscale may be None: not wanted).  x may be None where dscale is not wanted."""
+    lib = load()
+    dt, sdt, dev, tokens, D, scale_n, xs, rs = _residual(x, h, weight, scale)
+    if not isinstance(d_y, torch.Tensor):
+        raise TypeError("kdn: d_y must be a tensor")
+    if x is None:
+        dt, _ = _dtype("d_y", d_y)
+    if out is None:
+        out = dict(dx=_new(h.shape, dt, dev, stream), dresidual=_new(h.shape, sdt, dev, stream),
+                   dweight=_new((D,), _f32, dev, stream),
+                   dscale=None if scale is None or x is None else _new((scale_n,), _f32, dev, stream))
+    for name, t, shape, kind in (("d_y", d_y, h.shape, dt), ("d_h", d_h, h.shape, sdt),
+                                 ("dx", out["dx"], h.shape, dt),
+                                 ("dresidual", out["dresidual"], h.shape, sdt),
+                                 ("dweight", out["dweight"], (D,), _f32),
+                                 ("dscale", out["dscale"], (scale_n,), _f32)):
+        _same(name, t, shape, kind, dev)
+    st = ctypes.c_int(0)
+    n = lib.kdn_residual_norm_backward_workspace_size(tokens, D, scale_n, ctypes.byref(st))
+    _check(lib, st.value)
+    workspace, n = _workspace(n, workspace, dev, stream)
+    _call(lib.kdn_residual_norm_backward, dev, stream, DTYPES[dt], DTYPES[sdt], tokens, D, scale_n,
+          float(eps), xs, rs, _p(x), _p(h), _p(weight), _p(scale), _p(d_y), _p(d_h),
+          _p(out["dx"]), _p(out["dresidual"]), _p(out["dweight"]), _p(out["dscale"]),
+          _p(workspace), n)
     return out
