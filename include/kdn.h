@@ -611,6 +611,78 @@ unsigned long long kdn_causal_conv_backward_workspace_size(kdn_dtype dtype, int 
                                                            kdn_status *status);
 
 /*
+ * Selective state space scan, per channel c with S states n:
+ *     dt_t = softplus(delta_t + delta_bias)   (softplus = 0: delta_t + delta_bias)
+ *     h_t = exp(dt_t A) h_{t-1} + dt_t x_t B_t
+ *     y_t = (sum_n C_t h_t + D x_t) silu(z_t)
+ * (A < 0, not checked).  G groups of C / G consecutive channels share B and C.
+ *
+ *   x, delta    [tokens, C] dtype;  z [tokens, C] dtype or NULL (no gate)
+ *   B, C        [tokens, G, S] dtype, rows by stride as all of these
+ *   A           [C, S] float32;  D, delta_bias [C] float32 or NULL (zero)
+ *   S0          [N or pool, C, S] float32, or NULL (zero)
+ *   y           [tokens, C] dtype (output)
+ *   S_out       shaped as S0 (output), or NULL (not wanted); may be exactly S0, must
+ *               not overlap it otherwise
+ *   workspace   device memory of at least the queried size, 256-byte aligned,
+ *               overlapping no other argument; NULL if that is 0
+ * A, S0 and S_out on 16-byte boundaries.  S in {8, 16, 32}; C below 2^24; sizes whose
+ * launches would have 2^32 work-items are refused (KDN_ERR_SHAPE).  States are
+ * float32.  A packed batch's sequences are cut where its blocks cut them: tables with
+ * blocks of kdn_selective_block tokens are quickest, any do.
+ */
+kdn_status kdn_selective_scan(kdn_dtype dtype, int N, int T, int C, int S, int G, int softplus,
+                              long long x_stride, long long delta_stride, long long z_stride,
+                              long long B_stride, long long C_stride, const void *x,
+                              const void *delta, const float *A, const void *B, const void *Cm,
+                              const float *D, const void *z, const float *delta_bias,
+                              const float *S0, void *y, float *S_out, const kdn_packed *packed,
+                              void *workspace, unsigned long long workspace_bytes, void *stream);
+unsigned long long kdn_selective_scan_workspace_size(kdn_dtype dtype, int N, int T, int C, int S,
+                                                     int G, const kdn_packed *packed,
+                                                     kdn_status *status);
+
+/* A good block length for a packed batch of N sequences, `tokens` rows and C channels
+ * of S states; -1 if the sizes are invalid. */
+int kdn_selective_block(int tokens, int N, int C, int S);
+
+/*
+ * One token for N rows from a pool of states, updated in place: x, delta, z [N, C],
+ * B, C [N, G, S] by strides, y [N, C]; slots [N] int32 or NULL (row n), pool states of
+ * `state` [pool, C, S] float32.  A row whose slot is not in [0, pool) is skipped and
+ * its y left as it was.  Two rows may not share a slot.
+ */
+kdn_status kdn_selective_decode(kdn_dtype dtype, int N, int C, int S, int G, int softplus,
+                                long long x_stride, long long delta_stride, long long z_stride,
+                                long long B_stride, long long C_stride, const void *x,
+                                const void *delta, const float *A, const void *B, const void *Cm,
+                                const float *D, const void *z, const float *delta_bias,
+                                const int *slots, int pool, float *state, void *y, void *stream);
+
+/*
+ * Gradients of kdn_selective_scan for the cotangents d_y [tokens, C] and dS_out (shaped
+ * as S0; NULL: zero).  Outputs: dx, ddelta, dz (NULL where z is) [tokens, C], dB, dC
+ * [tokens, G, S] in the call's dtype; dA [C, S], dD [C], ddelta_bias [C] (the last two
+ * may be NULL) and dS0 (shaped as S0, or NULL; states without a sequence are left as
+ * they were) float32.  dS_out and dS0 on 16-byte boundaries.  workspace as above.
+ */
+kdn_status kdn_selective_scan_backward(kdn_dtype dtype, int N, int T, int C, int S, int G,
+                                       int softplus, long long x_stride, long long delta_stride,
+                                       long long z_stride, long long B_stride, long long C_stride,
+                                       const void *x, const void *delta, const float *A,
+                                       const void *B, const void *Cm, const float *D,
+                                       const void *z, const float *delta_bias, const float *S0,
+                                       const void *d_y, const float *dS_out, void *dx,
+                                       void *ddelta, float *dA, void *dB, void *dC, float *dD,
+                                       void *dz, float *ddelta_bias, float *dS0,
+                                       const kdn_packed *packed, void *workspace,
+                                       unsigned long long workspace_bytes, void *stream);
+unsigned long long kdn_selective_scan_backward_workspace_size(kdn_dtype dtype, int N, int T, int C,
+                                                              int S, int G,
+                                                              const kdn_packed *packed,
+                                                              kdn_status *status);
+
+/*
  * Gated RMS norm of each head's d values, r(u) = (mean(u^2) + eps)^(-1/2):
  *   KDN_NORM_GATE:  y = x r(x) weight act(z)
  *   KDN_GATE_NORM:  y = u r(u) weight,  u = x act(z)

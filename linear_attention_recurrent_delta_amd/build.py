@@ -51,6 +51,9 @@ UNITS += [("kdn_prefill.hip", ["-DKDN_PREFILL_DISPATCH"], "kdn_prefill_dispatch.
           ("kdn_tables.hip", [], "kdn_tables.o"),
           ("kdn_conv_abi.cpp", [], "kdn_conv_abi.o"),
           ("kdn_conv.hip", [], "kdn_conv.o"),
+          ("kdn_scan_abi.cpp", [], "kdn_scan_abi.o"),
+          ("kdn_scan.hip", [], "kdn_scan.o"),
+          ("kdn_scan_backward.hip", [], "kdn_scan_backward.o"),
           ("kdn_norm_abi.cpp", [], "kdn_norm_abi.o"),
           ("kdn_norm.hip", [], "kdn_norm.o")]
 

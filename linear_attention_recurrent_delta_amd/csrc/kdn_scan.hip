@@ -1,0 +1,516 @@
+// kdn_scan.hip -- the selective state space scan (gfx950), per channel with S states:
+//   dt_t = softplus(delta_t + bias),   h_t = exp(dt_t A) h_{t-1} + dt_t x_t B_t,
+//   y_t = (C_t . h_t + D x_t) silu(z_t).
+// Every token needs an exponential for each channel and state, so the scan is bound
+// by the vector units: a product, an exponential (two instructions' time), a product
+// and two sums for each state.  No matrix product is in it: the decays differ for
+// each channel and state.
+#include "kdn_scan_device.h"
+
+namespace kdn {
+namespace scan {
+
+// Tokens that a wave takes at a time: their decays and inputs stay in registers
+// between the two passes over them.
+template <int SPL> constexpr int steps() { return SPL <= 4 ? 16 : 8; }
+
+// Per-token values of a wave's channels: lane 4 k + j has tokens 4 i + j.
+template <typename T, int K> struct TokenRows {
+    T x[K / 4], d[K / 4], z[K / 4];
+    // tokens first .. + K of which `count` are there
+    __device__ __forceinline__ void load(const ScanParams &P, const Channels &ch, long first,
+                                         int count) {
+        const int j = threadIdx.x & 3;
+        const uint32_t lx = lane_at<T>(j, P.x_stride, ch.c), ld = lane_at<T>(j, P.d_stride, ch.c);
+        const uint32_t lz = lane_at<T>(j, P.z_stride, ch.c);
+#pragma unroll
+        for (int i = 0; i < K / 4; ++i) {
+            x[i] = d[i] = z[i] = from_f32<T>(0.f);
+            if (4 * i + j < count) {
+                x[i] = *row_at<T>(P.x, first + 4 * i, P.x_stride, lx);
+                d[i] = *row_at<T>(P.delta, first + 4 * i, P.d_stride, ld);
+                if (P.z)
+                    z[i] = *row_at<T>(P.z, first + 4 * i, P.z_stride, lz);
+            }
+        }
+    }
+    // time step of token 4 i + j (0 of one that is not there, which leaves the state as
+    // it is)
+    template <bool FINE>
+    __device__ __forceinline__ float step(const ScanParams &P, float bias, int i,
+                                          int count) const {
+        const float v = to_f32(d[i]) + bias;
+        const float dt = P.softplus ? softplus<FINE>(v) : v;
+        return 4 * i + ((int)threadIdx.x & 3) < count ? dt : 0.f;
+    }
+};
+
+// ---------------------------------------------------------------------------
+// Outputs.  NW waves of a workgroup walk one block, K tokens each at a time: every
+// wave scans its tokens from nothing, hands its end and its decay to the others
+// through LDS, folds those before it into its start and goes through its tokens
+// again, with their decays and inputs from registers (one more product and sum for
+// a state than a walk by one wave, which NW = 1 is).
+// ---------------------------------------------------------------------------
+template <typename T, int SPL, int NW>
+__global__ __launch_bounds__(NW == 1 ? 256 : NW *WAVE, 2) void scan_kernel(ScanParams P,
+                                                                           int groups,
+                                                                           long units) {
+    constexpr bool FINE = sizeof(T) == 4;
+    constexpr int S = 4 * SPL, K = steps<SPL>(), WAVES = NW == 1 ? 4 : NW;
+    __shared__ float bc[WAVES][2][K][S];
+    __shared__ float ends[NW == 1 ? 1 : 2][2][NW == 1 ? 1 : NW][WAVE * SPL];
+    const int lane = threadIdx.x & (WAVE - 1), j = lane & 3, w = wave_id();
+    const int seg = NW == 1 ? 0 : w;
+    // NW = 1: each wave has a run of channels of its own
+    const long unit = NW == 1 ? (long)blockIdx.x * WAVES + w : xcd_unit(blockIdx.x, units);
+    if (unit >= units)
+        return;
+    const int runs = groups * P.G;
+    const long b = unit / runs;
+    const Channels ch(P, (int)(unit % runs), groups);
+    const Block B = get_block(P, b);
+    if (B.count <= 0 || B.slot < 0 || (!B.single && !P.ws_state))
+        return;
+    const long at = (B.slot * P.C + ch.c) * S + j * SPL;
+    float A2[SPL], h[SPL];
+    load_A<SPL>(P, ch.c, j, A2);
+    const float bias = P.bias ? P.bias[ch.c] : 0.f, D = P.D ? P.D[ch.c] : 0.f;
+    if (!B.single)
+        load_states<SPL>(P.ws_state + (tile_slot(b, B.first, 0, S) * P.C + ch.c) * S + j * SPL, h);
+    else if (P.S0)
+        load_states<SPL>(P.S0 + at, h);
+    else
+#pragma unroll
+        for (int s = 0; s < SPL; ++s)
+            h[s] = 0.f;
+
+    TokenRows<T, K> rows;
+    GroupRows<T, S, K> group;
+    rows.load(P, ch, B.first + seg * K, B.count - seg * K);
+    group.load(P, ch.g, B.first + seg * K, B.count - seg * K);
+    // the state is here before the first barrier: S_out, which a wave may write behind
+    // it, may be S0
+#pragma unroll
+    for (int s = 0; s < SPL; ++s)
+        asm volatile("" : "+v"(h[s]));
+    const uint32_t ly = lane_at<T>(j, P.C, ch.c);
+    int buf = 0;
+    for (int t0 = 0; t0 < B.count; t0 += NW * K, buf ^= 1) {
+        const int own = t0 + seg * K, count = B.count - own;
+        // this round's values; the next round's are requested before the work on them
+        const TokenRows<T, K> now = rows;
+        group.put(bc[w]);
+        if (t0 + NW * K < B.count) {
+            rows.load(P, ch, B.first + own + NW * K, count - NW * K);
+            group.load(P, ch.g, B.first + own + NW * K, count - NW * K);
+        }
+        float dt[K / 4], in[K / 4], sum = 0.f;
+#pragma unroll
+        for (int i = 0; i < K / 4; ++i) {
+            dt[i] = now.template step<FINE>(P, bias, i, count);
+            in[i] = dt[i] * to_f32(now.x[i]);
+            sum += dt[i];
+        }
+        float a[K][SPL], u[K][SPL], end[SPL];
+#pragma unroll
+        for (int s = 0; s < SPL; ++s)
+            end[s] = 0.f;
+        unrolled<K>([&](auto I) {
+            constexpr int i = I;
+            const float d = quad_lane<i % 4>(dt[i / 4]), v = quad_lane<i % 4>(in[i / 4]);
+            float Bt[SPL];
+            load_states<SPL>(&bc[w][0][i][j * SPL], Bt);
+#pragma unroll
+            for (int s = 0; s < SPL; ++s) {
+                a[i][s] = __builtin_amdgcn_exp2f(d * A2[s]);
+                u[i][s] = v * Bt[s];
+                if constexpr (NW > 1)
+                    end[s] = fmaf(a[i][s], end[s], u[i][s]);
+            }
+        });
+        float next[SPL];
+        if constexpr (NW > 1) {
+            sum = quad_sum(sum);
+            float all[SPL];
+#pragma unroll
+            for (int s = 0; s < SPL; ++s)
+                all[s] = __builtin_amdgcn_exp2f(sum * A2[s]);
+            store_states<SPL>(&ends[buf][0][seg][lane * SPL], all);
+            store_states<SPL>(&ends[buf][1][seg][lane * SPL], end);
+            __syncthreads();
+#pragma unroll
+            for (int s = 0; s < SPL; ++s)
+                next[s] = h[s];
+#pragma unroll
+            for (int q = 0; q < NW; ++q) {
+                load_states<SPL>(&ends[buf][0][q][lane * SPL], all);
+                load_states<SPL>(&ends[buf][1][q][lane * SPL], end);
+#pragma unroll
+                for (int s = 0; s < SPL; ++s) {
+                    if (q == seg)
+                        h[s] = next[s];
+                    next[s] = fmaf(all[s], next[s], end[s]);
+                }
+            }
+        }
+        float part[4];
+        unrolled<K>([&](auto I) {
+            constexpr int i = I;
+            float Ct[SPL], y = 0.f;
+            load_states<SPL>(&bc[w][1][i][j * SPL], Ct);
+#pragma unroll
+            for (int s = 0; s < SPL; ++s) {
+                h[s] = fmaf(a[i][s], h[s], u[i][s]);
+                y = fmaf(Ct[s], h[s], y);
+            }
+            part[i % 4] = y;
+            if constexpr (i % 4 == 3) {
+                float out = fmaf(D, to_f32(now.x[i / 4]), quad_sums(part, j));
+                if (P.z)
+                    out *= silu_f32<FINE>(to_f32(now.z[i / 4]));
+                if (i - 3 + j < count && ch.live)
+                    *row_at<T>(P.y, B.first + own + i - 3, P.C, ly) = from_f32<T>(out);
+            }
+        });
+        if constexpr (NW > 1)
+#pragma unroll
+            for (int s = 0; s < SPL; ++s)
+                h[s] = next[s];
+    }
+    if (P.S_out && B.last && seg == 0 && ch.live)
+        store_states<SPL>(P.S_out + at, h);
+}
+
+// ---------------------------------------------------------------------------
+// A tile's own contribution to the state from nothing, U = sum_t (decay behind t)
+// dt_t x_t B_t, the sum of its time steps, and with REV what its tokens hand to the
+// reverse recurrence, Q = sum_t (decay up to and with t) dy'_t C_t, dy' = dy silu(z).
+// A workgroup has a block and run of 16 channels, a wave every fourth of its tiles,
+// token by token.
+// ---------------------------------------------------------------------------
+constexpr int OWN_WAVES = 4;
+template <typename T, int SPL, bool REV>
+__global__ __launch_bounds__(OWN_WAVES *WAVE) void scan_own_kernel(ScanParams P, int groups,
+                                                                   long units) {
+    constexpr bool FINE = sizeof(T) == 4;
+    constexpr int S = 4 * SPL, K = steps<SPL>(), TILE = scan_tile(S);
+    __shared__ float bc[OWN_WAVES][2][K][S];
+    const int lane = threadIdx.x & (WAVE - 1), j = lane & 3, w = wave_id();
+    const int runs = groups * P.G;
+    const long unit = xcd_unit(blockIdx.x, units), b = unit / runs;
+    const Channels ch(P, (int)(unit % runs), groups);
+    const Block B = get_block(P, b);
+    if (B.count <= 0 || B.slot < 0 || (!REV && B.single))
+        return;
+    // the outputs alone do not need the last tile's
+    const int stop = !REV && B.last ? (B.count - 1) / TILE * TILE : B.count;
+    float A2[SPL];
+    load_A<SPL>(P, ch.c, j, A2);
+    const float bias = P.bias ? P.bias[ch.c] : 0.f;
+    for (int t1 = w * TILE; t1 < stop; t1 += OWN_WAVES * TILE) {
+        const int n = min(TILE, B.count - t1);
+        float end[SPL], back[SPL], all[SPL];
+#pragma unroll
+        for (int s = 0; s < SPL; ++s) {
+            end[s] = back[s] = 0.f;
+            all[s] = 1.f;
+        }
+        float sum = 0.f;
+        for (int t0 = 0; t0 < n; t0 += K) {
+            TokenRows<T, K> rows;
+            GroupRows<T, S, K> group;
+            const long first = B.first + t1 + t0;
+            rows.load(P, ch, first, n - t0);
+            group.load(P, ch.g, first, n - t0);
+            float dt[K / 4], in[K / 4], g[K / 4];
+#pragma unroll
+            for (int i = 0; i < K / 4; ++i) {
+                g[i] = 0.f;
+                if (REV && 4 * i + j < n - t0)
+                    g[i] = to_f32(*row_at<T>(P.d_y, first + 4 * i, P.C, lane_at<T>(j, P.C, ch.c)));
+            }
+            group.put(bc[w]);
+#pragma unroll
+            for (int i = 0; i < K / 4; ++i) {
+                dt[i] = rows.template step<FINE>(P, bias, i, n - t0);
+                in[i] = dt[i] * to_f32(rows.x[i]);
+                sum += dt[i];
+                if (REV && P.z)
+                    g[i] *= silu_f32<FINE>(to_f32(rows.z[i]));
+            }
+            unrolled<K>([&](auto I) {
+                constexpr int i = I;
+                const float d = quad_lane<i % 4>(dt[i / 4]), v = quad_lane<i % 4>(in[i / 4]);
+                const float e = quad_lane<i % 4>(g[i / 4]);
+                float Bt[SPL], Ct[SPL];
+                load_states<SPL>(&bc[w][0][i][j * SPL], Bt);
+                if constexpr (REV)
+                    load_states<SPL>(&bc[w][1][i][j * SPL], Ct);
+#pragma unroll
+                for (int s = 0; s < SPL; ++s) {
+                    const float a = __builtin_amdgcn_exp2f(d * A2[s]);
+                    end[s] = fmaf(a, end[s], v * Bt[s]);
+                    if constexpr (REV) {
+                        all[s] *= a;
+                        back[s] = fmaf(all[s], e * Ct[s], back[s]);
+                    }
+                }
+            });
+        }
+        sum = quad_sum(sum);
+        const long slot = tile_slot(b, B.first, t1 / TILE, S) * P.C + ch.c;
+        if (ch.live) {
+            store_states<SPL>(P.ws_state + slot * S + j * SPL, end);
+            if constexpr (REV)
+                store_states<SPL>(P.ws_rstate + slot * S + j * SPL, back);
+            if (j == 0)
+                P.ws_dt[slot] = sum;
+        }
+    }
+}
+
+// ---------------------------------------------------------------------------
+// Join of the tiles along each sequence: a tile's own contribution U becomes the
+// state at its start, h <- 2^(A2 sum dt) h + U; reverse (tiles last to first): Q
+// becomes the reverse state behind its end, and behind the first tile is dS0.  One
+// thread holds 4 states of a channel; JOIN tiles are requested ahead.
+// ---------------------------------------------------------------------------
+constexpr int JOIN = 8, JOIN_NT = 256;
+template <bool REV>
+__device__ __forceinline__ void join(const ScanParams &P, int seq, long quad, bool all) {
+    const long size = (long)P.C * P.S, e = 4 * quad;
+    long b0 = (long)seq * P.nblocks, b1 = b0 + P.nblocks, slot = seq, first, n;
+    if (P.block_offsets) {
+        b0 = P.block_offsets[seq];
+        b1 = P.block_offsets[seq + 1];
+        slot = P.slots ? P.slots[seq] : seq;
+        if (b0 < 0 || b1 > P.nblocks || slot < 0 || slot >= P.pool)
+            return;
+    }
+    const float *from = REV ? P.dS_out : P.S0;
+    float *pass = REV ? P.dS0 : P.S_out;
+    f32x4 h = {0.f, 0.f, 0.f, 0.f};
+    if (from)
+        h = *reinterpret_cast<const f32x4 *>(from + slot * size + e);
+    if (b1 <= b0) {                  // no tokens: the state passes on
+        if (pass && pass != from)
+            *reinterpret_cast<f32x4 *>(pass + slot * size + e) = h;
+        return;
+    }
+    if (b1 - b0 == 1 && !all)
+        return;
+    first = (long)seq * P.T;
+    n = P.T;
+    if (P.block_offsets) {
+        const int4 r0 = reinterpret_cast<const int4 *>(P.blocks)[b0];
+        const int4 r1 = reinterpret_cast<const int4 *>(P.blocks)[b1 - 1];
+        first = r0.x;
+        n = (b1 - b0 - 1) * P.block + r1.y;
+    }
+    const int tile = scan_tile(P.S);
+    const long tiles = (n + tile - 1) / tile, per = P.block / tile;
+    // blocks but the last are whole tiles: tile i has slot first / tile + b0 + i + i / per
+    const long base = first / tile + b0;
+    float *ws = REV ? P.ws_rstate : P.ws_state;
+    if (!ws || first < 0 || n <= 0 || base + tiles - 1 + (tiles - 1) / per >= P.tile_slots)
+        return;
+    const f32x4 A = *reinterpret_cast<const f32x4 *>(P.A + e);
+    const long c = e / P.S;
+    auto place = [&](long i) {
+        const long t = REV ? tiles - 1 - i : i;
+        return base + t + t / per;
+    };
+    const long need = REV ? tiles : tiles - 1;      // own contributions that are used
+    for (long i = 0; i < tiles; i += JOIN) {
+        f32x4 u[JOIN];
+        float d[JOIN];
+#pragma unroll
+        for (int k = 0; k < JOIN; ++k)
+            if (i + k < need) {
+                u[k] = *reinterpret_cast<const f32x4 *>(ws + place(i + k) * size + e);
+                d[k] = P.ws_dt[place(i + k) * P.C + c];
+            }
+#pragma unroll
+        for (int k = 0; k < JOIN; ++k)
+            if (i + k < tiles) {
+                *reinterpret_cast<f32x4 *>(ws + place(i + k) * size + e) = h;
+                if (i + k < need)
+#pragma unroll
+                    for (int q = 0; q < 4; ++q)
+                        h[q] = fmaf(__builtin_amdgcn_exp2f(d[k] * LOG2E * A[q]), h[q], u[k][q]);
+            }
+    }
+    if (REV && pass)
+        *reinterpret_cast<f32x4 *>(pass + slot * size + e) = h;
+}
+
+template <bool REV>
+__global__ __launch_bounds__(JOIN_NT) void scan_join_kernel(ScanParams P, int pieces) {
+    long id = blockIdx.x;
+    bool reverse = false;
+    if (REV) {
+        reverse = id & 1;
+        id >>= 1;
+    }
+    const long quad = (id % pieces) * JOIN_NT + threadIdx.x;
+    const int seq = (int)(id / pieces);
+    if (quad >= (long)P.C * P.S / 4)
+        return;
+    if (REV && reverse)
+        join<true>(P, seq, quad, true);
+    else
+        join<false>(P, seq, quad, REV);
+}
+
+// ---------------------------------------------------------------------------
+// Single tokens.  Bound by one read and one write of the states.  Four lanes a
+// channel, as above; no state is read twice, so they pass the caches.
+// ---------------------------------------------------------------------------
+template <typename T, int SPL>
+__global__ __launch_bounds__(256) void scan_decode_kernel(ScanDecodeParams P, int chunks) {
+    constexpr bool FINE = sizeof(T) == 4;
+    constexpr int S = 4 * SPL;
+    const int j = threadIdx.x & 3;
+    const long n = blockIdx.x / chunks;
+    const int in = (int)(blockIdx.x % chunks) * 64 + (threadIdx.x >> 2);
+    const long slot = P.slots ? P.slots[n] : n;
+    if (slot < 0 || slot >= P.pool)
+        return;
+    const bool live = in < P.C;
+    const int c = live ? in : P.C - 1, g = c / (P.C / P.G);
+    float *state = P.state + (slot * P.C + c) * S + j * SPL;
+    float h[SPL], A[SPL], y = 0.f;
+    typedef float V __attribute__((ext_vector_type(SPL < 4 ? SPL : 4)));
+    constexpr int VN = SPL < 4 ? SPL : 4;
+#pragma unroll
+    for (int s = 0; s < SPL; s += VN) {
+        const V v = __builtin_nontemporal_load(reinterpret_cast<const V *>(state + s));
+#pragma unroll
+        for (int e = 0; e < VN; ++e)
+            h[s + e] = v[e];
+    }
+    load_states<SPL>(P.A + (long)c * S + j * SPL, A);
+    const float x = to_f32(static_cast<const T *>(P.x)[n * P.x_stride + c]);
+    float dt = to_f32(static_cast<const T *>(P.delta)[n * P.d_stride + c]) +
+               (P.bias ? P.bias[c] : 0.f);
+    if (P.softplus)
+        dt = softplus<FINE>(dt);
+    const T *B = static_cast<const T *>(P.B) + n * P.b_stride + (long)g * S + j * SPL;
+    const T *Cm = static_cast<const T *>(P.Cm) + n * P.c_stride + (long)g * S + j * SPL;
+    Pack<T, SPL> Bt, Ct;
+    Bt.load(B);
+    Ct.load(Cm);
+    const float in_x = dt * x;
+#pragma unroll
+    for (int s = 0; s < SPL; ++s) {
+        h[s] = fmaf(exp_f32<FINE>(dt * A[s]), h[s], in_x * Bt.get(s));
+        y = fmaf(Ct.get(s), h[s], y);
+    }
+    if (live)
+#pragma unroll
+        for (int s = 0; s < SPL; s += VN) {
+            V v;
+#pragma unroll
+            for (int e = 0; e < VN; ++e)
+                v[e] = h[s + e];
+            __builtin_nontemporal_store(v, reinterpret_cast<V *>(state + s));
+        }
+    y = quad_sum(y);
+    if (j == 0 && live) {
+        y = fmaf(P.D ? P.D[c] : 0.f, x, y);
+        if (P.z)
+            y *= silu_f32<FINE>(to_f32(static_cast<const T *>(P.z)[n * P.z_stride + c]));
+        static_cast<T *>(P.y)[n * P.C + c] = from_f32<T>(y);
+    }
+}
+
+template <typename T, int SPL>
+hipError_t launch_t(const ScanParams &P, hipStream_t st) {
+    constexpr int NW = 8;
+    const int groups = scan_groups(P.C, P.G);
+    const long units = scan_total_blocks(P) * groups * P.G;
+    if (units == 0)
+        return hipSuccess;
+    hipLaunchKernelGGL((scan_kernel<T, SPL, NW>), dim3((unsigned)units), dim3(NW * WAVE), 0, st, P,
+                       groups, units);
+    return hipGetLastError();
+}
+
+template <typename T, int SPL>
+hipError_t launch_own_t(const ScanParams &P, bool reverse, hipStream_t st) {
+    const int groups = scan_groups(P.C, P.G);
+    const long units = scan_total_blocks(P) * groups * P.G;
+    if (units == 0)
+        return hipSuccess;
+    const dim3 grid((unsigned)units), block(OWN_WAVES * WAVE);
+    if (reverse)
+        hipLaunchKernelGGL((scan_own_kernel<T, SPL, true>), grid, block, 0, st, P, groups, units);
+    else
+        hipLaunchKernelGGL((scan_own_kernel<T, SPL, false>), grid, block, 0, st, P, groups, units);
+    return hipGetLastError();
+}
+
+template <typename T, int SPL>
+hipError_t launch_decode_t(const ScanDecodeParams &P, hipStream_t st) {
+    const int chunks = (P.C + 63) / 64;
+    hipLaunchKernelGGL((scan_decode_kernel<T, SPL>), dim3((unsigned)((long)P.N * chunks)), dim3(256),
+                       0, st, P, chunks);
+    return hipGetLastError();
+}
+
+}  // namespace scan
+
+#define KDN_SCAN(fn, ...)                                        \
+    switch (P.S) {                                               \
+    case 8: return P.bf16 ? scan::fn<bf16, 2>(__VA_ARGS__)       \
+                          : scan::fn<float, 2>(__VA_ARGS__);     \
+    case 16: return P.bf16 ? scan::fn<bf16, 4>(__VA_ARGS__)      \
+                           : scan::fn<float, 4>(__VA_ARGS__);    \
+    default: return P.bf16 ? scan::fn<bf16, 8>(__VA_ARGS__)      \
+                           : scan::fn<float, 8>(__VA_ARGS__);    \
+    }
+
+static hipError_t outputs(const ScanParams &P, hipStream_t st) { KDN_SCAN(launch_t, P, st) }
+static hipError_t own(const ScanParams &P, bool reverse, hipStream_t st) {
+    KDN_SCAN(launch_own_t, P, reverse, st)
+}
+
+static hipError_t joins(const ScanParams &P, bool reverse, hipStream_t st) {
+    if (P.N == 0)
+        return hipSuccess;
+    const long quads = (long)P.C * P.S / 4;
+    const int pieces = (int)((quads + scan::JOIN_NT - 1) / scan::JOIN_NT);
+    if (reverse)
+        hipLaunchKernelGGL((scan::scan_join_kernel<true>), dim3((unsigned)(2l * P.N * pieces)),
+                           dim3(scan::JOIN_NT), 0, st, P, pieces);
+    else
+        hipLaunchKernelGGL((scan::scan_join_kernel<false>), dim3((unsigned)((long)P.N * pieces)),
+                           dim3(scan::JOIN_NT), 0, st, P, pieces);
+    return hipGetLastError();
+}
+
+hipError_t launch_scan_states(const ScanParams &P, bool reverse, hipStream_t st) {
+    const hipError_t e = own(P, reverse, st);
+    return e == hipSuccess ? joins(P, reverse, st) : e;
+}
+
+hipError_t launch_scan(const ScanParams &P, bool several, hipStream_t st) {
+    if (P.C == 0)
+        return hipSuccess;
+    // sequences of several blocks: their states first; sequences without tokens: the
+    // joins pass their state on
+    const bool empty = (P.block_offsets || P.T == 0) && P.S_out && P.S_out != P.S0;
+    const hipError_t e = several ? launch_scan_states(P, false, st)
+                                 : (empty ? joins(P, false, st) : hipSuccess);
+    return e == hipSuccess ? outputs(P, st) : e;
+}
+
+hipError_t launch_scan_decode(const ScanDecodeParams &P, hipStream_t st) {
+    if ((long)P.N * P.C == 0)
+        return hipSuccess;
+    KDN_SCAN(launch_decode_t, P, st)
+}
+#undef KDN_SCAN
+
+}  // namespace kdn

@@ -111,6 +111,18 @@ def load(path: str = LIB_PATH):
     lib.kdn_causal_conv_backward.argtypes = [i] * 6 + [ll] + [vp] * 10 + [pk, vp, u64, vp]
     lib.kdn_causal_conv_backward_workspace_size.restype = u64
     lib.kdn_causal_conv_backward_workspace_size.argtypes = [i] * 5 + [pk, ip]
+    lib.kdn_selective_block.restype = i
+    lib.kdn_selective_block.argtypes = [i] * 4
+    lib.kdn_selective_scan.restype = i
+    lib.kdn_selective_scan.argtypes = [i] * 7 + [ll] * 5 + [vp] * 11 + [pk, vp, u64, vp]
+    lib.kdn_selective_scan_workspace_size.restype = u64
+    lib.kdn_selective_scan_workspace_size.argtypes = [i] * 6 + [pk, ip]
+    lib.kdn_selective_decode.restype = i
+    lib.kdn_selective_decode.argtypes = [i] * 5 + [i] + [ll] * 5 + [vp] * 9 + [i] + [vp] * 3
+    lib.kdn_selective_scan_backward.restype = i
+    lib.kdn_selective_scan_backward.argtypes = [i] * 7 + [ll] * 5 + [vp] * 20 + [pk, vp, u64, vp]
+    lib.kdn_selective_scan_backward_workspace_size.restype = u64
+    lib.kdn_selective_scan_backward_workspace_size.argtypes = [i] * 6 + [pk, ip]
     lib.kdn_gated_norm.restype = i
     lib.kdn_gated_norm.argtypes = [i] * 7 + [f, ll, ll] + [vp] * 5
     lib.kdn_gated_norm_backward.restype = i
@@ -1070,6 +1082,158 @@ def causal_conv_backward(x, weight, d_y, bias=None, state0=None, dstate_out=None
     _call(lib.kdn_causal_conv_backward, dev, stream, DTYPES[dt], N, T, C, W, act, xs, _p(x),
           _p(weight), _p(bias), _p(state0), _p(d_y), _p(dstate_out), _p(out["dx"]),
           _p(out["dweight"]), _p(out["dbias"]), _p(out["dstate0"]), pk, _p(workspace), n)
+    return out
+
+
+def selective_block(tokens, N, C, S):
+    """Tokens of a block for :func:`sequence_tables` of N sequences with ``tokens``
+    rows in all and C channels of S states."""
+    n = int(load().kdn_selective_block(_int32("tokens", tokens), _int32("N", N), _int32("C", C),
+                                       _int32("S", S)))
+    if n < 0:
+        raise KdnError(2, kdn_status_string(2))
+    return n
+
+
+def _scan_inputs(x, delta, A, B, C, D, z, delta_bias, lead):
+    """Checks of a scan's inputs: (channels, states, groups, strides)."""
+    dt, dev = x.dtype, x.device
+    n = len(lead)
+    if not isinstance(A, torch.Tensor) or A.dim() != 2:
+        raise ValueError("kdn: A must be a tensor [C, S]")
+    if not isinstance(B, torch.Tensor) or B.dim() != n + 2:
+        raise ValueError("kdn: B must be a tensor [.., G, S]")
+    c, s, g = _int32("C", x.shape[-1]), _int32("S", A.shape[1]), _int32("G", B.shape[-2])
+    strides = (_strided("x", x, lead, (c,), dt, dev), _strided("delta", delta, lead, (c,), dt, dev),
+               0 if z is None else _strided("z", z, lead, (c,), dt, dev),
+               _strided("B", B, lead, (g, s), dt, dev), _strided("C", C, lead, (g, s), dt, dev))
+    _same("A", A, (c, s), _f32, dev)
+    _same("D", D, (c,), _f32, dev)
+    _same("delta_bias", delta_bias, (c,), _f32, dev)
+    return c, s, g, strides
+
+
+def selective_scan(x, delta, A, B, C, D=None, z=None, delta_bias=None, softplus=True, S0=None,
+                   tables=None, out=None, workspace="auto", stream=None):
+    """Selective state space scan of each channel with S states:
+    dt = softplus(delta + delta_bias) (or without softplus), h_t = exp(dt_t A) h_{t-1} +
+    dt_t x_t B_t, y_t = (C_t . h_t + D x_t) silu(z_t).
+
+    Dense: x, delta, z [B,T,C], B and C [B,T,G,S] (float32 or bf16, rows may be slices
+    of wider ones; G groups of channels share B and C), A [C,S], D and delta_bias [C]
+    float32 (None: zero), z None: no gate, S0 [B,C,S] float32 or None (zeros).
+    Packed (``tables`` from :func:`sequence_tables`, blocks of :func:`selective_block`):
+    the same without the batch, rows [tokens, ..]; S0 and S_out are pools [P,C,S] of
+    states by slot.  ``out`` may pass (y, S_out); S_out may be S0 (in place) or None
+    (not wanted).  Without it S_out is new, and for a packed batch with S0 the pool S0
+    itself, updated in place.  Rows of y behind the last sequence are left as they
+    were.  Returns (y, S_out)."""
+    lib = load()
+    dt, dev = _dtype("x", x)
+    lead, N, T, pk, pool = _batch(x, tables, (S0, out[1] if out is not None else None), 1, "x")
+    c, s, g, strides = _scan_inputs(x, delta, A, B, C, D, z, delta_bias, lead)
+    if out is None:
+        y = _new(lead + (c,), dt, dev, stream)
+        if tables is not None and S0 is not None:
+            S = S0
+        elif tables is not None and tables.slots is not None:
+            raise ValueError("kdn: a pool for the tables' slots must be given (S0 or out)")
+        else:
+            S = _new((pool, c, s), _f32, dev, stream)
+    else:
+        y, S = out
+    _same("S0", S0, (pool, c, s), _f32, dev)
+    _same("y", y, lead + (c,), dt, dev)
+    _same("S_out", S, (pool, c, s), _f32, dev)
+    if isinstance(workspace, str):
+        if workspace != "auto":
+            raise ValueError(f"kdn: workspace must be 'auto', None or a tensor, not {workspace!r}")
+        workspace = _scan_workspace(DTYPES[dt], N, T, c, s, g, pk, dev, stream)
+    nws = 0
+    if workspace is not None:
+        nws = workspace.numel()
+        _same("workspace", workspace, (nws,), torch.uint8, dev)
+    _call(lib.kdn_selective_scan, dev, stream, DTYPES[dt], N, T, c, s, g, int(bool(softplus)),
+          *strides, _p(x), _p(delta), _p(A), _p(B), _p(C), _p(D), _p(z), _p(delta_bias), _p(S0),
+          _p(y), _p(S), pk, _p(workspace), nws)
+    return y, S
+
+
+def _scan_workspace(dtype, N, T, C, S, G, pk, dev, stream):
+    st = ctypes.c_int(0)
+    n = load().kdn_selective_scan_workspace_size(dtype, N, T, C, S, G, pk, ctypes.byref(st))
+    _check(_lib, st.value)
+    return _new((n,), torch.uint8, dev, stream) if n else None
+
+
+def selective_decode(x, delta, A, B, C, S, D=None, z=None, delta_bias=None, softplus=True,
+                     slots=None, y=None, stream=None):
+    """One token of :func:`selective_scan` for N rows: x, delta, z [N,C], B, C [N,G,S].
+    S [P,C,S] float32 is a pool of states, updated in place; ``slots`` [N] int32 is each
+    row's state (None: row n).  A row whose slot is not in the pool is skipped, its y
+    left as it was (zero in a new y).  Returns y [N,C]."""
+    lib = load()
+    dt, dev = _dtype("x", x)
+    if x.dim() != 2:
+        raise ValueError(f"kdn: x has shape {tuple(x.shape)}, expected [N, C]")
+    N = _int32("N", x.shape[0])
+    c, s, g, strides = _scan_inputs(x, delta, A, B, C, D, z, delta_bias, (N,))
+    if not isinstance(S, torch.Tensor) or S.dim() != 3:
+        raise ValueError("kdn: S must be a tensor [P, C, S]")
+    pool = _int32("pool", S.shape[0])
+    if y is None:
+        y = _new((N, c), dt, dev, stream, zero=slots is not None)
+    _same("S", S, (pool, c, s), _f32, dev)
+    _same("y", y, (N, c), dt, dev)
+    _same("slots", slots, (N,), torch.int32, dev)
+    _call(lib.kdn_selective_decode, dev, stream, DTYPES[dt], N, c, s, g, int(bool(softplus)),
+          *strides, _p(x), _p(delta), _p(A), _p(B), _p(C), _p(D), _p(z), _p(delta_bias), _p(slots),
+          pool, _p(S), _p(y))
+    return y
+
+
+def selective_scan_backward(x, delta, A, B, C, d_y, D=None, z=None, delta_bias=None, softplus=True,
+                            S0=None, dS_out=None, tables=None, out=None, workspace=None,
+                            stream=None):
+    """Gradients of :func:`selective_scan` for the cotangents d_y (shaped as y) and dS_out
+    (shaped as S_out; None: zero).  Returns a dict of dx, ddelta, dz (None without z), dB,
+    dC in x's dtype and dA, dD, ddelta_bias (None where their parameter is), dS0 float32.
+    Rows behind the last sequence of a packed batch get zero, and so do states of dS0
+    without a sequence.  ``out`` may pass such a dict (dD, ddelta_bias and dS0 may be None:
+    not wanted; in a given dS0 states without a sequence are left as they were).  A packed
+    batch without any of S0, dS_out and out["dS0"] has no pool: dS0 is by sequence and
+    slots are not looked at."""
+    lib = load()
+    dt, dev = _dtype("x", x)
+    lead, N, T, pk, pool = _batch(x, tables, (S0, dS_out, (out or {}).get("dS0")), 1, "x")
+    c, s, g, strides = _scan_inputs(x, delta, A, B, C, D, z, delta_bias, lead)
+    if out is None:
+        new = lambda *shape: _new(lead + shape, dt, dev, stream)  # noqa: E731
+        par = lambda *shape: _new(shape, _f32, dev, stream)  # noqa: E731
+        out = dict(dx=new(c), ddelta=new(c), dz=None if z is None else new(c), dB=new(g, s),
+                   dC=new(g, s), dA=par(c, s), dD=None if D is None else par(c),
+                   ddelta_bias=None if delta_bias is None else par(c),
+                   dS0=_new((pool, c, s), _f32, dev, stream, zero=tables is not None))
+    for name, t, shape, kind in (("d_y", d_y, lead + (c,), dt), ("S0", S0, (pool, c, s), _f32),
+                                 ("dS_out", dS_out, (pool, c, s), _f32),
+                                 ("dx", out["dx"], lead + (c,), dt),
+                                 ("ddelta", out["ddelta"], lead + (c,), dt),
+                                 ("dz", out["dz"], lead + (c,), dt),
+                                 ("dB", out["dB"], lead + (g, s), dt),
+                                 ("dC", out["dC"], lead + (g, s), dt),
+                                 ("dA", out["dA"], (c, s), _f32), ("dD", out["dD"], (c,), _f32),
+                                 ("ddelta_bias", out["ddelta_bias"], (c,), _f32),
+                                 ("dS0", out["dS0"], (pool, c, s), _f32)):
+        _same(name, t, shape, kind, dev)
+    st = ctypes.c_int(0)
+    n = lib.kdn_selective_scan_backward_workspace_size(DTYPES[dt], N, T, c, s, g, pk, ctypes.byref(st))
+    _check(lib, st.value)
+    workspace, n = _workspace(n, workspace, dev, stream)
+    _call(lib.kdn_selective_scan_backward, dev, stream, DTYPES[dt], N, T, c, s, g,
+          int(bool(softplus)), *strides, _p(x), _p(delta), _p(A), _p(B), _p(C), _p(D), _p(z),
+          _p(delta_bias), _p(S0), _p(d_y), _p(dS_out), _p(out["dx"]), _p(out["ddelta"]),
+          _p(out["dA"]), _p(out["dB"]), _p(out["dC"]), _p(out["dD"]), _p(out["dz"]),
+          _p(out["ddelta_bias"]), _p(out["dS0"]), pk, _p(workspace), n)
     return out
 
 

@@ -178,3 +178,131 @@ def residual_grad(x, h, w, scale, dy, dh, eps, dtype, stream):
              dx=1.01 * (HALF[dtype] * dx.abs() + (off + U * dres.abs()) * (s if scale is None else s.abs())),
              dweight=1.01 * 12 * U * (dy * n).abs(),
              dscale=None if x is None else 1.01 * off * x.abs())
+
+
+# ---------------------------------------------------------------------------
+# Selective scan: one sequence, float64; x, delta, z [T, C], B, C [T, G, S].
+# ---------------------------------------------------------------------------
+def step(delta, bias, softplus):
+    v = delta if bias is None else delta + bias
+    return torch.logaddexp(v, torch.zeros_like(v)) if softplus else v
+
+
+def step_slack(delta, bias, softplus, dtype):
+    """Relative error of a time step in units of u: the sum with the bias (what it moves
+    e^v by), the exponential, and the series with its reciprocal and its rest (2^-18 of
+    it in bf16 calls)."""
+    v = delta if bias is None else delta + bias
+    m = delta.abs() + (0 if bias is None else bias.abs())
+    if not softplus:
+        return m / v.abs().clamp(min=1e-300)
+    s = 2 * m + 14 + 2 * v.abs() * (1.45 if dtype == torch.bfloat16 else 0)
+    return s + (64 if dtype == torch.bfloat16 else 0)
+
+
+def heads(m, C):
+    return m.repeat_interleave(C // m.shape[1], 1)
+
+
+def scan(x, delta, A, B, Cm, D, z, bias, softplus, S0, dtype):
+    """y, S and their bounds.  M is the state over absolute values, E a bound of what the
+    state is off by, in units of u: every decay is off by its exponential and by what the
+    time step and the argument's roundings move it by."""
+    T, C = x.shape
+    dt, ds = step(delta, bias, softplus), step_slack(delta, bias, softplus, dtype)
+    Bh, Ch = heads(B, C), heads(Cm, C)
+    S, M, E = S0.clone(), S0.abs(), torch.zeros_like(S0)
+    y, by = torch.zeros_like(x), torch.zeros_like(x)
+    for t in range(T):
+        arg = dt[t][:, None] * A
+        a = torch.exp(arg)
+        off = 3 + arg.abs() * (ds[t][:, None] + 4)            # relative, of a
+        u = (dt[t] * x[t])[:, None] * Bh[t]
+        E = a * (E + off * M) + u.abs() * (ds[t][:, None] + 3)
+        S = a * S + u
+        M = a * M + u.abs()
+        E = E + 2 * M                                          # sums, and parts of the scan joined
+        y[t] = (S * Ch[t]).sum(-1)
+        by[t] = ((E + (S.shape[-1] + 4) * M) * Ch[t].abs()).sum(-1)
+    if D is not None:
+        by = by + 2 * (D * x).abs()
+        y = y + D * x
+    out, bound = y, U * by
+    if z is not None:
+        g = silu(z)
+        out = y * g
+        bound = bound * g.abs() + out.abs() * U * (act_slack(z, dtype) + 2)
+    return out, S, 1.02 * (HALF[dtype] * out.abs() + bound), 1.02 * U * E
+
+
+def scan_grad(x, delta, A, B, Cm, D, z, bias, softplus, S0, dy, dS, dtype):
+    """Gradients and their bounds (parameters': of this sequence's part)."""
+    T, C = x.shape
+    G, per = B.shape[1], C // B.shape[1]
+    dt, ds = step(delta, bias, softplus), step_slack(delta, bias, softplus, dtype)
+    Bh, Ch = heads(B, C), heads(Cm, C)
+    gz = torch.ones_like(x) if z is None else silu(z)
+    dp = dy * gz
+    ep = dp.abs() * (1.0 if z is None else act_slack(z, dtype) + 2)
+    S, M, E = S0.clone(), S0.abs(), torch.zeros_like(S0)
+    before, y, ey = [], torch.zeros_like(x), torch.zeros_like(x)
+    dC, mC = torch.zeros(T, C, B.shape[2]).double(), torch.zeros(T, C, B.shape[2]).double()
+    rel = []
+    for t in range(T):
+        before.append((S, M, E))
+        arg = dt[t][:, None] * A
+        a, off = torch.exp(arg), 3 + arg.abs() * (ds[t][:, None] + 4)
+        rel.append((a, off))
+        u = (dt[t] * x[t])[:, None] * Bh[t]
+        E = a * (E + off * M) + u.abs() * (ds[t][:, None] + 3) + 2 * (a * M + u.abs())
+        S, M = a * S + u, a * M + u.abs()
+        y[t], ey[t] = (S * Ch[t]).sum(-1), ((E + (S.shape[-1] + 4) * M) * Ch[t].abs()).sum(-1)
+        dC[t], mC[t] = dp[t][:, None] * S, dp[t].abs()[:, None] * (E + 2 * M) + ep[t][:, None] * M
+    skip = 0 if D is None else D * x
+    y = y + skip
+    ey = ey + 2 * (skip if D is None else skip.abs())
+    R, Mr, Er = dS.clone(), dS.abs(), torch.zeros_like(dS)
+    zero = torch.zeros_like(x)
+    dx, ex, dd, ed = zero.clone(), zero.clone(), zero.clone(), zero.clone()
+    dB, mB = torch.zeros_like(dC), torch.zeros_like(dC)
+    dA, mA = torch.zeros_like(A), torch.zeros_like(A)
+    N = A.shape[1] + 6
+    for t in range(T - 1, -1, -1):
+        a, off = rel[t]
+        g = R + dp[t][:, None] * Ch[t]
+        mg = Mr + dp[t].abs()[:, None] * Ch[t].abs()
+        eg = Er + ep[t][:, None] * Ch[t].abs() + 3 * mg
+        v = dt[t] * x[t]
+        dB[t], mB[t] = v[:, None] * g, v.abs()[:, None] * (eg + (ds[t][:, None] + 3) * mg)
+        own, mown = (g * Bh[t]).sum(-1), ((eg + N * mg) * Bh[t].abs()).sum(-1)
+        bown = (mg * Bh[t].abs()).sum(-1)
+        R, Mr, Er = a * g, a * mg, a * (eg + (off + 1) * mg)
+        Sb, Mb, Eb = before[t]
+        w, ew = R * Sb, Er * Mb + Mr * Eb + 2 * Mr * Mb
+        wA, ewA = (w * A).sum(-1), ((ew + N * Mr * Mb) * A.abs()).sum(-1)
+        dx[t] = dt[t] * own + (0 if D is None else D * dp[t])
+        ex[t] = dt[t].abs() * (mown + (ds[t] + 2) * bown) + (0 if D is None else D.abs() * (ep[t] + 2 * dp[t].abs()))
+        dd[t], ed[t] = wA + x[t] * own, ewA + x[t].abs() * mown + 2 * (wA.abs() + (x[t] * own).abs())
+        dA = dA + w * dt[t][:, None]
+        mA = mA + (ew + (24 + ds[t][:, None]) * Mr * Mb) * dt[t].abs()[:, None]
+    if softplus:
+        v = delta if bias is None else delta + bias
+        s = torch.sigmoid(v)
+        m = delta.abs() + (0 if bias is None else bias.abs())
+        ed = ed * s + dd.abs() * s * (act_slack(v, dtype) + 2 + 2 * m)
+        dd = dd * s
+    h = HALF[dtype]
+    share = lambda m: m.unflatten(1, (G, per)).sum(2)  # noqa: E731
+    grads = dict(dx=dx, ddelta=dd, dB=share(dB), dC=share(dC), dA=dA, dS0=R, dD=(dp * x).sum(0),
+                 ddelta_bias=dd.sum(0))
+    # sums over channels: 16 lanes, runs of a set and the sets
+    many = per / 16 + 10
+    bounds = dict(dx=ex, ddelta=ed, dB=share(mB + many * dB.abs()), dC=share(mC + many * dC.abs()), dA=mA, dS0=Er,
+                  dD=((ep + 24 * dp.abs()) * x.abs()).sum(0), ddelta_bias=(ed + 24 * dd.abs()).sum(0))
+    if z is not None:
+        sg = torch.sigmoid(z)
+        slope = sg + (z * sg * (1 - sg)).abs()
+        grads["dz"] = dy * y * dsilu(z)
+        bounds["dz"] = dy.abs() * (ey + y.abs() * (2 * act_slack(z, dtype) + 6)) * slope
+    low = ("dx", "ddelta", "dB", "dC", "dz")
+    return grads, {k: 1.02 * (U * b + (h if k in low else U) * grads[k].abs()) for k, b in bounds.items()}
