@@ -49,11 +49,11 @@ template <typename Params> inline kdn_status batch_tables(Params &P, const kdn_p
 }
 
 // Elements between tokens (0: contiguous rows of `row` elements), any number of
-// them from `row` to 2^28.
+// them from `row` to 2^25.
 inline kdn_status row_stride(long long given, long long row, long *out) {
     if (given == 0)
         given = row;
-    if (given < row || given >= (1LL << 28))
+    if (given < row || given >= (1LL << 25))
         return KDN_ERR_SHAPE;
     *out = given;
     return KDN_OK;

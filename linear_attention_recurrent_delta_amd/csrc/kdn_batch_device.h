@@ -13,6 +13,13 @@ __device__ __forceinline__ int wave_id() {
     return __builtin_amdgcn_readfirstlane((int)threadIdx.x / WAVE);
 }
 
+// Descriptor of `bytes` bytes from `base` (the same in every lane): loads at or past
+// their end return 0, stores there are dropped.
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t buf_rsrc(const void *base, unsigned bytes) {
+    return __builtin_amdgcn_make_buffer_rsrc(const_cast<void *>(base), (short)0, (int)bytes,
+                                             0x00020000);
+}
+
 // ---------------------------------------------------------------------------
 // The block of a workgroup.
 // ---------------------------------------------------------------------------

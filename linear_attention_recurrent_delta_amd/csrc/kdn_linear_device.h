@@ -318,10 +318,6 @@ __device__ __forceinline__ void decay_between(const Decays<C> &D, float hi_i, fl
 // return 0 without a branch.  (A guarded and an unguarded load path that meet
 // make the compiler wait for the loads in flight on each of them.)
 // ---------------------------------------------------------------------------
-__device__ __forceinline__ __amdgpu_buffer_rsrc_t buf_rsrc(const void *base, unsigned bytes) {
-    return __builtin_amdgcn_make_buffer_rsrc(const_cast<void *>(base), (short)0, (int)bytes,
-                                             0x00020000);
-}
 
 // The log-decays of a chunk, one per lane, on their way: the bits as they were
 // loaded, made a float only where they are used.

@@ -10,6 +10,8 @@
 namespace kdn {
 namespace scan {
 
+constexpr long SCAN_MANY = 2048;
+
 // Tokens that a wave takes at a time: their decays and inputs stay in registers
 // between the two passes over them.
 template <int SPL> constexpr int steps() { return SPL <= 4 ? 16 : 8; }
@@ -21,17 +23,14 @@ template <typename T, int K> struct TokenRows {
     __device__ __forceinline__ void load(const ScanParams &P, const Channels &ch, long first,
                                          int count) {
         const int j = threadIdx.x & 3;
-        const uint32_t lx = lane_at<T>(j, P.x_stride, ch.c), ld = lane_at<T>(j, P.d_stride, ch.c);
-        const uint32_t lz = lane_at<T>(j, P.z_stride, ch.c);
+        const Rows<T, K> rx(P.x, first, P.x_stride, P.C, count);
+        const Rows<T, K> rd(P.delta, first, P.d_stride, P.C, count);
+        const Rows<T, K> rz(P.z, first, P.z_stride, P.C, P.z ? count : 0);
 #pragma unroll
         for (int i = 0; i < K / 4; ++i) {
-            x[i] = d[i] = z[i] = from_f32<T>(0.f);
-            if (4 * i + j < count) {
-                x[i] = *row_at<T>(P.x, first + 4 * i, P.x_stride, lx);
-                d[i] = *row_at<T>(P.delta, first + 4 * i, P.d_stride, ld);
-                if (P.z)
-                    z[i] = *row_at<T>(P.z, first + 4 * i, P.z_stride, lz);
-            }
+            x[i] = rx.load(rx.at(4 * i + j, P.x_stride, ch.c, true));
+            d[i] = rd.load(rd.at(4 * i + j, P.d_stride, ch.c, true));
+            z[i] = rz.load(rz.at(4 * i + j, P.z_stride, ch.c, true));
         }
     }
     // time step of token 4 i + j (0 of one that is not there, which leaves the state as
@@ -94,7 +93,6 @@ __global__ __launch_bounds__(NW == 1 ? 256 : NW *WAVE, 2) void scan_kernel(ScanP
 #pragma unroll
     for (int s = 0; s < SPL; ++s)
         asm volatile("" : "+v"(h[s]));
-    const uint32_t ly = lane_at<T>(j, P.C, ch.c);
     int buf = 0;
     for (int t0 = 0; t0 < B.count; t0 += NW * K, buf ^= 1) {
         const int own = t0 + seg * K, count = B.count - own;
@@ -112,27 +110,52 @@ __global__ __launch_bounds__(NW == 1 ? 256 : NW *WAVE, 2) void scan_kernel(ScanP
             in[i] = dt[i] * to_f32(now.x[i]);
             sum += dt[i];
         }
-        float a[K][SPL], u[K][SPL], end[SPL];
-#pragma unroll
-        for (int s = 0; s < SPL; ++s)
-            end[s] = 0.f;
-        unrolled<K>([&](auto I) {
+        // outputs of four tokens at a time, each by the lane that has its x and z
+        const Rows<T, K> ry(P.y, B.first + own, P.C, P.C, count);
+        float part[4];
+        auto output = [&](auto I) {
             constexpr int i = I;
-            const float d = quad_lane<i % 4>(dt[i / 4]), v = quad_lane<i % 4>(in[i / 4]);
-            float Bt[SPL];
-            load_states<SPL>(&bc[w][0][i][j * SPL], Bt);
-#pragma unroll
-            for (int s = 0; s < SPL; ++s) {
-                a[i][s] = __builtin_amdgcn_exp2f(d * A2[s]);
-                u[i][s] = v * Bt[s];
-                if constexpr (NW > 1)
-                    end[s] = fmaf(a[i][s], end[s], u[i][s]);
+            if constexpr (i % 4 == 3) {
+                float out = fmaf(D, to_f32(now.x[i / 4]), quad_sums(part, j));
+                if (P.z)
+                    out *= silu_f32<FINE>(to_f32(now.z[i / 4]));
+                ry.store(from_f32<T>(out), ry.at(i - 3 + j, P.C, ch.c, ch.live));
             }
-        });
-        float next[SPL];
-        if constexpr (NW > 1) {
+        };
+        if constexpr (NW == 1) {
+            unrolled<K>([&](auto I) {
+                constexpr int i = I;
+                const float d = quad_lane<i % 4>(dt[i / 4]), v = quad_lane<i % 4>(in[i / 4]);
+                float Bt[SPL], Ct[SPL], y = 0.f;
+                load_states<SPL>(&bc[w][0][i][j * SPL], Bt);
+                load_states<SPL>(&bc[w][1][i][j * SPL], Ct);
+#pragma unroll
+                for (int s = 0; s < SPL; ++s) {
+                    h[s] = fmaf(__builtin_amdgcn_exp2f(d * A2[s]), h[s], v * Bt[s]);
+                    y = fmaf(Ct[s], h[s], y);
+                }
+                part[i % 4] = y;
+                output(I);
+            });
+        } else {
+            float a[K][SPL], u[K][SPL], end[SPL];
+#pragma unroll
+            for (int s = 0; s < SPL; ++s)
+                end[s] = 0.f;
+            unrolled<K>([&](auto I) {
+                constexpr int i = I;
+                const float d = quad_lane<i % 4>(dt[i / 4]), v = quad_lane<i % 4>(in[i / 4]);
+                float Bt[SPL];
+                load_states<SPL>(&bc[w][0][i][j * SPL], Bt);
+#pragma unroll
+                for (int s = 0; s < SPL; ++s) {
+                    a[i][s] = __builtin_amdgcn_exp2f(d * A2[s]);
+                    u[i][s] = v * Bt[s];
+                    end[s] = fmaf(a[i][s], end[s], u[i][s]);
+                }
+            });
             sum = quad_sum(sum);
-            float all[SPL];
+            float all[SPL], next[SPL];
 #pragma unroll
             for (int s = 0; s < SPL; ++s)
                 all[s] = __builtin_amdgcn_exp2f(sum * A2[s]);
@@ -146,37 +169,30 @@ __global__ __launch_bounds__(NW == 1 ? 256 : NW *WAVE, 2) void scan_kernel(ScanP
             for (int q = 0; q < NW; ++q) {
                 load_states<SPL>(&ends[buf][0][q][lane * SPL], all);
                 load_states<SPL>(&ends[buf][1][q][lane * SPL], end);
+                if (q == seg)
+#pragma unroll
+                    for (int s = 0; s < SPL; ++s)
+                        h[s] = next[s];
+#pragma unroll
+                for (int s = 0; s < SPL; ++s)
+                    next[s] = fmaf(all[s], next[s], end[s]);
+            }
+            unrolled<K>([&](auto I) {
+                constexpr int i = I;
+                float Ct[SPL], y = 0.f;
+                load_states<SPL>(&bc[w][1][i][j * SPL], Ct);
 #pragma unroll
                 for (int s = 0; s < SPL; ++s) {
-                    if (q == seg)
-                        h[s] = next[s];
-                    next[s] = fmaf(all[s], next[s], end[s]);
+                    h[s] = fmaf(a[i][s], h[s], u[i][s]);
+                    y = fmaf(Ct[s], h[s], y);
                 }
-            }
-        }
-        float part[4];
-        unrolled<K>([&](auto I) {
-            constexpr int i = I;
-            float Ct[SPL], y = 0.f;
-            load_states<SPL>(&bc[w][1][i][j * SPL], Ct);
-#pragma unroll
-            for (int s = 0; s < SPL; ++s) {
-                h[s] = fmaf(a[i][s], h[s], u[i][s]);
-                y = fmaf(Ct[s], h[s], y);
-            }
-            part[i % 4] = y;
-            if constexpr (i % 4 == 3) {
-                float out = fmaf(D, to_f32(now.x[i / 4]), quad_sums(part, j));
-                if (P.z)
-                    out *= silu_f32<FINE>(to_f32(now.z[i / 4]));
-                if (i - 3 + j < count && ch.live)
-                    *row_at<T>(P.y, B.first + own + i - 3, P.C, ly) = from_f32<T>(out);
-            }
-        });
-        if constexpr (NW > 1)
+                part[i % 4] = y;
+                output(I);
+            });
 #pragma unroll
             for (int s = 0; s < SPL; ++s)
                 h[s] = next[s];
+        }
     }
     if (P.S_out && B.last && seg == 0 && ch.live)
         store_states<SPL>(P.S_out + at, h);
@@ -224,12 +240,10 @@ __global__ __launch_bounds__(OWN_WAVES *WAVE) void scan_own_kernel(ScanParams P,
             rows.load(P, ch, first, n - t0);
             group.load(P, ch.g, first, n - t0);
             float dt[K / 4], in[K / 4], g[K / 4];
+            const Rows<T, K> ry(P.d_y, first, P.C, P.C, REV ? n - t0 : 0);
 #pragma unroll
-            for (int i = 0; i < K / 4; ++i) {
-                g[i] = 0.f;
-                if (REV && 4 * i + j < n - t0)
-                    g[i] = to_f32(*row_at<T>(P.d_y, first + 4 * i, P.C, lane_at<T>(j, P.C, ch.c)));
-            }
+            for (int i = 0; i < K / 4; ++i)
+                g[i] = REV ? to_f32(ry.load(ry.at(4 * i + j, P.C, ch.c, true))) : 0.f;
             group.put(bc[w]);
 #pragma unroll
             for (int i = 0; i < K / 4; ++i) {
@@ -432,8 +446,12 @@ hipError_t launch_t(const ScanParams &P, hipStream_t st) {
     const long units = scan_total_blocks(P) * groups * P.G;
     if (units == 0)
         return hipSuccess;
-    hipLaunchKernelGGL((scan_kernel<T, SPL, NW>), dim3((unsigned)units), dim3(NW * WAVE), 0, st, P,
-                       groups, units);
+    if (units >= SCAN_MANY)
+        hipLaunchKernelGGL((scan_kernel<T, SPL, 1>), dim3((unsigned)((units + 3) / 4)), dim3(256), 0,
+                           st, P, groups, units);
+    else
+        hipLaunchKernelGGL((scan_kernel<T, SPL, NW>), dim3((unsigned)units), dim3(NW * WAVE), 0, st,
+                           P, groups, units);
     return hipGetLastError();
 }
 

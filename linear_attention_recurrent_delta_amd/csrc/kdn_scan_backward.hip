@@ -32,19 +32,18 @@ template <typename T, int SPL, int K> struct Run {
                                          int count, long slot) {
         constexpr int S = 4 * SPL;
         const int j = threadIdx.x & 3;
-        const uint32_t lx = lane_at<T>(j, P.x_stride, ch.c), ld = lane_at<T>(j, P.d_stride, ch.c);
-        const uint32_t lz = lane_at<T>(j, P.z_stride, ch.c), lg = lane_at<T>(j, P.C, ch.c);
+        const Rows<T, K> rx(P.x, first, P.x_stride, P.C, count);
+        const Rows<T, K> rd(P.delta, first, P.d_stride, P.C, count);
+        const Rows<T, K> rz(P.z, first, P.z_stride, P.C, P.z ? count : 0);
+        const Rows<T, K> rg(P.d_y, first, P.C, P.C, count);
 #pragma unroll
         for (int i = 0; i < K / 4; ++i) {
-            x[i] = d[i] = z[i] = g[i] = from_f32<T>(0.f);
             // lanes behind the last channel: x = dy = 0, nothing of them in dB and dC
-            if (4 * i + j < count && ch.live) {
-                x[i] = *row_at<T>(P.x, first + 4 * i, P.x_stride, lx);
-                d[i] = *row_at<T>(P.delta, first + 4 * i, P.d_stride, ld);
-                g[i] = *row_at<T>(P.d_y, first + 4 * i, P.C, lg);
-                if (P.z)
-                    z[i] = *row_at<T>(P.z, first + 4 * i, P.z_stride, lz);
-            }
+            const int t = 4 * i + j;
+            x[i] = rx.load(rx.at(t, P.x_stride, ch.c, ch.live));
+            d[i] = rd.load(rd.at(t, P.d_stride, ch.c, ch.live));
+            z[i] = rz.load(rz.at(t, P.z_stride, ch.c, ch.live));
+            g[i] = rg.load(rg.at(t, P.C, ch.c, ch.live));
         }
         load_A<SPL>(P, ch.c, j, A2);
         const long at = (slot * P.C + ch.c) * S + j * SPL;
@@ -258,6 +257,9 @@ __global__ __launch_bounds__(grad_waves<SPL>() * WAVE) void scan_grad_kernel(Sca
                         }
                     });
                     float dD = 0.f, dbias = 0.f;
+                    const Rows<T, K> rx(P.dx, first, P.C, P.C, count);
+                    const Rows<T, K> rd(P.ddelta, first, P.C, P.C, count);
+                    const Rows<T, K> rz(P.dz, first, P.C, P.C, P.z ? count : 0);
 #pragma unroll
                     for (int i = 0; i < K / 4; ++i) {
                         const float x = to_f32(now.x[i]), v = to_f32(now.d[i]) + now.bias;
@@ -274,14 +276,11 @@ __global__ __launch_bounds__(grad_waves<SPL>() * WAVE) void scan_grad_kernel(Sca
                         if (4 * i + j < count) {
                             dD = fmaf(dp[i], x, dD);
                             dbias += dd;
-                            if (ch.live) {
-                                const uint32_t lg = lane_at<T>(j, P.C, ch.c);
-                                *row_at<T>(P.dx, first + 4 * i, P.C, lg) = from_f32<T>(dx);
-                                *row_at<T>(P.ddelta, first + 4 * i, P.C, lg) = from_f32<T>(dd);
-                                if (P.z)
-                                    *row_at<T>(P.dz, first + 4 * i, P.C, lg) = from_f32<T>(dz[i]);
-                            }
                         }
+                        const int at = rx.at(4 * i + j, P.C, ch.c, ch.live);
+                        rx.store(from_f32<T>(dx), at);
+                        rd.store(from_f32<T>(dd), at);
+                        rz.store(from_f32<T>(dz[i]), at);
                     }
                     float old[SPL];
                     load_states<SPL>(&sum_A[k][w][lane * SPL], old);

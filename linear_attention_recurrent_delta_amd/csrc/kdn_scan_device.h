@@ -91,37 +91,52 @@ struct Channels {
     }
 };
 
-// Element `lane` (in bytes) of the row `row` of a per-token tensor: the row, the same for
-// all lanes, in scalars, and 32 bits that differ.  Four rows of less than 2^28 elements
-// and a channel stay below 2^32 bytes.
-template <typename T>
-__device__ __forceinline__ const T *row_at(const void *p, long row, long stride, uint32_t lane) {
-    return reinterpret_cast<const T *>(reinterpret_cast<const char *>(static_cast<const T *>(p) + row * stride) + lane);
-}
-template <typename T>
-__device__ __forceinline__ T *row_at(void *p, long row, long stride, uint32_t lane) {
-    return reinterpret_cast<T *>(reinterpret_cast<char *>(static_cast<T *>(p) + row * stride) + lane);
-}
-template <typename T> __device__ __forceinline__ uint32_t lane_at(int j, long stride, int c) {
-    return ((uint32_t)j * (uint32_t)stride + (uint32_t)c) * (uint32_t)sizeof(T);
-}
+// Rows of a per-token tensor of C channels, K of them at a time through a descriptor
+// that ends with the last that is there: rows behind it read 0 and are not written,
+// without a branch.  Strides are below 2^25 elements, K rows below 2^32 bytes.
+template <typename T, int K> struct Rows {
+    __amdgpu_buffer_rsrc_t d;
+    // rows first .. of which `count` are there (the same in every lane)
+    __device__ __forceinline__ Rows(const void *p, long first, long stride, int C, int count) {
+        const int rows = min(count, K);
+        d = buf_rsrc(static_cast<const T *>(p) + first * stride,
+                     rows > 0 ? ((rows - 1) * (unsigned)stride + (unsigned)C) * (unsigned)sizeof(T) : 0u);
+    }
+    // row t, channel c, for lanes that take part in it
+    __device__ __forceinline__ static int at(int t, long stride, int c, bool live) {
+        return live ? (int)(((unsigned)t * (unsigned)stride + (unsigned)c) * (unsigned)sizeof(T)) : -1;
+    }
+    __device__ __forceinline__ T load(int at) const {
+        if constexpr (sizeof(T) == 2)
+            return __builtin_bit_cast(T, __builtin_amdgcn_raw_buffer_load_b16(d, at, 0, 0));
+        else
+            return __builtin_bit_cast(T, __builtin_amdgcn_raw_buffer_load_b32(d, at, 0, 0));
+    }
+    __device__ __forceinline__ void store(T x, int at) const {
+        if constexpr (sizeof(T) == 2)
+            __builtin_amdgcn_raw_buffer_store_b16(__builtin_bit_cast(unsigned short, x), d, at, 0, 0);
+        else
+            __builtin_amdgcn_raw_buffer_store_b32(__builtin_bit_cast(unsigned, x), d, at, 0, 0);
+    }
+};
 
 // B and C of K consecutive tokens of a group, float32 in LDS, written and read by one
 // wave.
 template <typename T, int S, int K> struct GroupRows {
     static constexpr int EPL = 2 * K * S / WAVE;      // elements of a lane
     Pack<T, EPL> r;
-    // rows first .. + K of which `count` are there
+    bool there;
+    // rows first .. + K of which `count` are there (none or less: first + count is the
+    // end of the rows): in the place of one behind them the last is read
     __device__ __forceinline__ void load(const ScanParams &P, int g, long first, int count) {
         const int lane = threadIdx.x & (WAVE - 1), e = (lane & 31) * EPL;
-        const int row = e / S, col = e % S;
-        r.zero();
-        if (row < count) {
-            const T *p = lane < 32 ? static_cast<const T *>(P.B) + (first + row) * P.b_stride
-                                   : static_cast<const T *>(P.Cm) + (first + row) * P.c_stride;
-            r.load(p + (long)g * S + col);
-        }
+        const int row = min(e / S, count - 1), col = e % S;
+        there = e / S < count;
+        const T *p = lane < 32 ? static_cast<const T *>(P.B) + (first + row) * P.b_stride
+                               : static_cast<const T *>(P.Cm) + (first + row) * P.c_stride;
+        r.load(p + (long)g * S + col);
     }
+    __device__ __forceinline__ float get(int i) const { return there ? r.get(i) : 0.f; }
     // to[0]: B, to[1]: C
     __device__ __forceinline__ void put(float (*to)[K][S]) const {
         const int lane = threadIdx.x & (WAVE - 1), e = (lane & 31) * EPL;
@@ -130,7 +145,7 @@ template <typename T, int S, int K> struct GroupRows {
 #pragma unroll
         for (int i = 0; i < EPL; i += 4)
             *reinterpret_cast<f32x4 *>(p + i) =
-                f32x4{r.get(i), r.get(i + 1), r.get(i + 2), r.get(i + 3)};
+                f32x4{get(i), get(i + 1), get(i + 2), get(i + 3)};
         order();
     }
     // what a wave's lanes read from each other through LDS stays in order
