@@ -44,6 +44,19 @@ template <typename T, int K> struct TokenRows {
     }
 };
 
+// Block number p of a packed batch by length, the longest first (of equal ones the
+// first), for up to 64 blocks: each lane ranks one.
+__device__ __forceinline__ int by_length(const ScanParams &P, int p) {
+    const int lane = threadIdx.x & (WAVE - 1), n = P.nblocks;
+    const int count = lane < n ? P.blocks[4 * lane + 1] : 0;
+    int rank = 0;
+    for (int k = 0; k < n; ++k) {
+        const int other = __builtin_amdgcn_readlane(count, k);
+        rank += other > count || (other == count && k < lane);
+    }
+    return __builtin_ctzll(__ballot(lane < n && rank == p));
+}
+
 // ---------------------------------------------------------------------------
 // Outputs.  NW waves of a workgroup walk one block, K tokens each at a time: every
 // wave scans its tokens from nothing, hands its end and its decay to the others
@@ -66,7 +79,9 @@ __global__ __launch_bounds__(NW == 1 ? 256 : NW *WAVE, 2) void scan_kernel(ScanP
     if (unit >= units)
         return;
     const int runs = groups * P.G;
-    const long b = unit / runs;
+    long b = unit / runs;
+    if (NW == 1 && P.block_offsets && P.nblocks <= WAVE)
+        b = by_length(P, (int)b);
     const Channels ch(P, (int)(unit % runs), groups);
     const Block B = get_block(P, b);
     if (B.count <= 0 || B.slot < 0 || (!B.single && !P.ws_state))
