@@ -21,16 +21,14 @@ namespace scan {
 
 // Tokens of a wave, and waves: registers hold two values and two sums for each state
 // and token.
-template <int SPL> constexpr int grad_steps() { return SPL == 2 ? 16 : (SPL == 4 ? 8 : 4); }
+template <int SPL> constexpr int grad_steps() { return SPL <= 4 ? 8 : 4; }
 template <int SPL> constexpr int grad_waves() { return scan_tile(4 * SPL) / grad_steps<SPL>(); }
 
-// What a wave needs of one run of channels, requested while it works on another.
-template <typename T, int SPL, int K> struct Run {
+// A wave's tokens of one run of channels, requested while it works on another.
+template <typename T, int K> struct Run {
     T x[K / 4], d[K / 4], z[K / 4], g[K / 4];
-    float A2[SPL], h[SPL], r[SPL], bias, D;
     __device__ __forceinline__ void load(const ScanParams &P, const Channels &ch, long first,
-                                         int count, long slot) {
-        constexpr int S = 4 * SPL;
+                                         int count) {
         const int j = threadIdx.x & 3;
         const Rows<T, K> rx(P.x, first, P.x_stride, P.C, count);
         const Rows<T, K> rd(P.delta, first, P.d_stride, P.C, count);
@@ -45,12 +43,6 @@ template <typename T, int SPL, int K> struct Run {
             z[i] = rz.load(rz.at(t, P.z_stride, ch.c, ch.live));
             g[i] = rg.load(rg.at(t, P.C, ch.c, ch.live));
         }
-        load_A<SPL>(P, ch.c, j, A2);
-        const long at = (slot * P.C + ch.c) * S + j * SPL;
-        load_states<SPL>(P.ws_state + at, h);
-        load_states<SPL>(P.ws_rstate + at, r);
-        bias = P.bias ? P.bias[ch.c] : 0.f;
-        D = P.D ? P.D[ch.c] : 0.f;
     }
 };
 
@@ -60,42 +52,45 @@ __device__ __forceinline__ float swap_add(float a, float b, bool half) {
     return __uint_as_float(p[0]) + __uint_as_float(p[1]);
 }
 
-// Sums over the 16 channels of a wave of 64 values f: lane 4 k + j gets in v the four
-// sums of lanes j of f[4 x .. + 4], x = 4 (k & 3) + 2 ((k >> 2) & 1) + (k >> 3).  Two
+// Sums over the 16 channels of a wave of M = 16 V values f: lane 4 k + j gets in v the
+// sums over lanes j of f[V x .. + V], x = 4 (k & 3) + 2 ((k >> 2) & 1) + (k >> 3).  Two
 // steps swap halves of registers (each leaves half as many), two add within 16 lanes.
-__device__ __forceinline__ void channel_sums(const float (&f)[64], float (&v)[4]) {
-    float a[32], b[16];
+template <int V>
+__device__ __forceinline__ void channel_sums(const float (&f)[16 * V], float (&v)[V]) {
+    float a[8 * V], b[4 * V];
 #pragma unroll
-    for (int m = 0; m < 32; ++m) {
-        // place 2 m and 2 m + 1 of the order 16 q + 4 i + e, f index 4 (4 q + e) + i
+    for (int m = 0; m < 8 * V; ++m) {
+        // places 2 m and 2 m + 1 of the order 4 V q + 4 i + e, f index V (4 q + e) + i
         const int p0 = 2 * m, p1 = p0 + 1;
-        const int f0 = 4 * (4 * (p0 / 16) + p0 % 4) + p0 % 16 / 4;
-        const int f1 = 4 * (4 * (p1 / 16) + p1 % 4) + p1 % 16 / 4;
+        const int f0 = V * (4 * (p0 / (4 * V)) + p0 % 4) + p0 % (4 * V) / 4;
+        const int f1 = V * (4 * (p1 / (4 * V)) + p1 % 4) + p1 % (4 * V) / 4;
         a[m] = swap_add(f[f0], f[f1], true);
     }
 #pragma unroll
-    for (int m = 0; m < 16; ++m) {
+    for (int m = 0; m < 4 * V; ++m) {
         b[m] = swap_add(a[2 * m], a[2 * m + 1], false);
         b[m] += dpp<0x128>(b[m]);            // row_ror:8
         b[m] += dpp<0x124>(b[m]);            // row_ror:4
     }
     const int q = (threadIdx.x >> 2) & 3;
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
-        v[i] = q & 2 ? (q & 1 ? b[12 + i] : b[8 + i]) : (q & 1 ? b[4 + i] : b[i]);
+    for (int i = 0; i < V; ++i)
+        v[i] = q & 2 ? (q & 1 ? b[3 * V + i] : b[2 * V + i]) : (q & 1 ? b[V + i] : b[i]);
 }
 
 template <typename T, int SPL>
-__global__ __launch_bounds__(grad_waves<SPL>() * WAVE) void scan_grad_kernel(ScanParams P,
+__global__ __launch_bounds__(grad_waves<SPL>() * WAVE, 2) void scan_grad_kernel(ScanParams P,
                                                                               int groups,
                                                                               int sets,
                                                                               long blocks) {
     constexpr bool FINE = sizeof(T) == 4;
     constexpr int S = 4 * SPL, K = grad_steps<SPL>(), NW = grad_waves<SPL>(), TILE = NW * K;
+    constexpr int M = 2 * K * SPL, V = M / 16;     // sums of a lane, and after the exchange
     __shared__ float bc[NW][2][K][S];
     __shared__ float ends[2][3][NW][WAVE * SPL];
     __shared__ float sum_A[scan_per_set(S)][NW][WAVE * SPL];
-    __shared__ float sum_D[scan_per_set(S)][2][NW][WAVE];
+    __shared__ float sum_D[scan_per_set(S)][2][NW][SCAN_CHANNELS];
+    __shared__ float par_A[scan_per_set(S)][WAVE * SPL], par[scan_per_set(S)][2][SCAN_CHANNELS];
     const int lane = threadIdx.x & (WAVE - 1), j = lane & 3, w = wave_id();
     const int set = blockIdx.x % sets, g = (int)(blockIdx.x / sets) % P.G;
     const int part = (int)(blockIdx.x / sets) / P.G;
@@ -103,8 +98,17 @@ __global__ __launch_bounds__(grad_waves<SPL>() * WAVE) void scan_grad_kernel(Sca
     for (int k = 0; k < runs; ++k) {         // a wave's own place: no barrier
         const float zero[SPL] = {};
         store_states<SPL>(&sum_A[k][w][lane * SPL], zero);
-        sum_D[k][0][w][lane] = sum_D[k][1][w][lane] = 0.f;
+        sum_D[k][j & 1][w][lane >> 2] = 0.f;
+        if (k % NW == w) {                   // A, delta's bias and D, for all waves
+            const Channels ch(P, g * groups + run0 + k, groups);
+            float A2[SPL];
+            load_A<SPL>(P, ch.c, j, A2);
+            store_states<SPL>(&par_A[k][lane * SPL], A2);
+            const float *from = j & 1 ? P.D : P.bias;
+            par[k][j & 1][lane >> 2] = from ? from[ch.c] : 0.f;
+        }
     }
+    __syncthreads();
     int buf = 0;
     for (long u = part; u < blocks * P.classes; u += P.parts) {
         const long b = u / P.classes;
@@ -113,9 +117,9 @@ __global__ __launch_bounds__(grad_waves<SPL>() * WAVE) void scan_grad_kernel(Sca
             const int count = B.count - t1 - w * K;          // of the wave's tokens
             const long first = B.first + t1 + w * K;
             float *rows_bc = P.ws_bc + ((set * P.tokens + first) * P.G + g) * (2 * S);
-            float acc[64];
+            float acc[M];
 #pragma unroll
-            for (int i = 0; i < 64; ++i)
+            for (int i = 0; i < M; ++i)
                 acc[i] = 0.f;
             if (B.slot < 0) {
                 // a skipped sequence has no gradients
@@ -133,20 +137,25 @@ __global__ __launch_bounds__(grad_waves<SPL>() * WAVE) void scan_grad_kernel(Sca
             } else {
                 const long slot = tile_slot(b, B.first, t1 / TILE, S);
                 GroupRows<T, S, K> group;
-                Run<T, SPL, K> next;
+                Run<T, K> next;
                 group.load(P, g, first, count);
-                next.load(P, Channels(P, g * groups + run0, groups), first, count, slot);
+                next.load(P, Channels(P, g * groups + run0, groups), first, count);
                 group.put(bc[w]);
                 for (int k = 0; k < runs; ++k, buf ^= 1) {
                     const Channels ch(P, g * groups + run0 + k, groups);
-                    const Run<T, SPL, K> now = next;
+                    const Run<T, K> now = next;
+                    float A2[SPL], hs[SPL], r[SPL];
+                    const long at = (slot * P.C + ch.c) * S + j * SPL;
+                    load_states<SPL>(P.ws_state + at, hs);
+                    load_states<SPL>(P.ws_rstate + at, r);
                     if (k + 1 < runs)
-                        next.load(P, Channels(P, g * groups + run0 + k + 1, groups), first, count,
-                                  slot);
+                        next.load(P, Channels(P, g * groups + run0 + k + 1, groups), first, count);
+                    load_states<SPL>(&par_A[k][lane * SPL], A2);
+                    const float bias = par[k][0][lane >> 2], D = par[k][1][lane >> 2];
                     float dt[K / 4], in[K / 4], dp[K / 4], sum = 0.f;
 #pragma unroll
                     for (int i = 0; i < K / 4; ++i) {
-                        const float v = to_f32(now.d[i]) + now.bias;
+                        const float v = to_f32(now.d[i]) + bias;
                         dt[i] = 4 * i + j < count ? (P.softplus ? softplus<FINE>(v) : v) : 0.f;
                         in[i] = dt[i] * to_f32(now.x[i]);
                         dp[i] = to_f32(now.g[i]);
@@ -165,7 +174,7 @@ __global__ __launch_bounds__(grad_waves<SPL>() * WAVE) void scan_grad_kernel(Sca
                         load_states<SPL>(&bc[w][0][i][j * SPL], Bt);
 #pragma unroll
                         for (int s = 0; s < SPL; ++s) {
-                            a[i][s] = __builtin_amdgcn_exp2f(d * now.A2[s]);
+                            a[i][s] = __builtin_amdgcn_exp2f(d * A2[s]);
                             h[i][s] = v * Bt[s];
                             end[s] = fmaf(a[i][s], end[s], h[i][s]);
                         }
@@ -182,31 +191,42 @@ __global__ __launch_bounds__(grad_waves<SPL>() * WAVE) void scan_grad_kernel(Sca
                     sum = quad_sum(sum);
 #pragma unroll
                     for (int s = 0; s < SPL; ++s)
-                        all[s] = __builtin_amdgcn_exp2f(sum * now.A2[s]);
+                        all[s] = __builtin_amdgcn_exp2f(sum * A2[s]);
                     store_states<SPL>(&ends[buf][0][w][lane * SPL], all);
                     store_states<SPL>(&ends[buf][1][w][lane * SPL], end);
                     store_states<SPL>(&ends[buf][2][w][lane * SPL], back);
                     __syncthreads();
-                    // the states in front of the wave's tokens and behind them
-                    float hs[SPL], r[SPL];
+                    // the states in front of the wave's tokens and behind them; the next
+                    // wave's are on their way while one's are used
+                    if (w > 0) {
+                        load_states<SPL>(&ends[buf][0][0][lane * SPL], all);
+                        load_states<SPL>(&ends[buf][1][0][lane * SPL], end);
+                        for (int q = 1; q <= w; ++q) {
+                            float a1[SPL], e1[SPL];
+                            load_states<SPL>(&ends[buf][0][q][lane * SPL], a1);
+                            load_states<SPL>(&ends[buf][1][q][lane * SPL], e1);
 #pragma unroll
-                    for (int s = 0; s < SPL; ++s) {
-                        hs[s] = now.h[s];
-                        r[s] = now.r[s];
+                            for (int s = 0; s < SPL; ++s) {
+                                hs[s] = fmaf(all[s], hs[s], end[s]);
+                                all[s] = a1[s];
+                                end[s] = e1[s];
+                            }
+                        }
                     }
-                    for (int q = 0; q < w; ++q) {
-                        load_states<SPL>(&ends[buf][0][q][lane * SPL], all);
-                        load_states<SPL>(&ends[buf][1][q][lane * SPL], end);
+                    if (w < NW - 1) {
+                        load_states<SPL>(&ends[buf][0][NW - 1][lane * SPL], all);
+                        load_states<SPL>(&ends[buf][2][NW - 1][lane * SPL], back);
+                        for (int q = NW - 2; q >= w; --q) {
+                            float a1[SPL], e1[SPL];
+                            load_states<SPL>(&ends[buf][0][q][lane * SPL], a1);
+                            load_states<SPL>(&ends[buf][2][q][lane * SPL], e1);
 #pragma unroll
-                        for (int s = 0; s < SPL; ++s)
-                            hs[s] = fmaf(all[s], hs[s], end[s]);
-                    }
-                    for (int q = NW - 1; q > w; --q) {
-                        load_states<SPL>(&ends[buf][0][q][lane * SPL], all);
-                        load_states<SPL>(&ends[buf][2][q][lane * SPL], back);
-#pragma unroll
-                        for (int s = 0; s < SPL; ++s)
-                            r[s] = fmaf(all[s], r[s], back[s]);
+                            for (int s = 0; s < SPL; ++s) {
+                                r[s] = fmaf(all[s], r[s], back[s]);
+                                all[s] = a1[s];
+                                back[s] = e1[s];
+                            }
+                        }
                     }
                     // forwards: h[i] becomes the state before token i
                     float part[4], y[K / 4], dz[K / 4];
@@ -246,7 +266,7 @@ __global__ __launch_bounds__(grad_waves<SPL>() * WAVE) void scan_grad_kernel(Sca
                             gb = fmaf(gs, Bt[s], gb);
                             r[s] = a[i][s] * gs;
                             const float ws = r[s] * h[i][s];
-                            wa = fmaf(ws, now.A2[s], wa);
+                            wa = fmaf(ws, A2[s], wa);
                             dA[s] = fmaf(ws, d, dA[s]);
                         }
                         part[i % 4] = gb;
@@ -262,8 +282,8 @@ __global__ __launch_bounds__(grad_waves<SPL>() * WAVE) void scan_grad_kernel(Sca
                     const Rows<T, K> rz(P.dz, first, P.C, P.C, P.z ? count : 0);
 #pragma unroll
                     for (int i = 0; i < K / 4; ++i) {
-                        const float x = to_f32(now.x[i]), v = to_f32(now.d[i]) + now.bias;
-                        const float dx = fmaf(dt[i], sum_B[i], now.D * dp[i]);
+                        const float x = to_f32(now.x[i]), v = to_f32(now.d[i]) + bias;
+                        const float dx = fmaf(dt[i], sum_B[i], D * dp[i]);
                         float dd = fmaf(x, sum_B[i], sum_w[i] * (1.f / LOG2E));
                         if (P.softplus)
                             dd *= sigmoid_f32<FINE>(v);
@@ -271,7 +291,7 @@ __global__ __launch_bounds__(grad_waves<SPL>() * WAVE) void scan_grad_kernel(Sca
                         if (P.z) {
                             float act, slope;
                             silu_grad<FINE>(to_f32(now.z[i]), act, slope);
-                            dz[i] = to_f32(now.g[i]) * fmaf(now.D, x, y[i]) * slope;
+                            dz[i] = to_f32(now.g[i]) * fmaf(D, x, y[i]) * slope;
                         }
                         if (4 * i + j < count) {
                             dD = fmaf(dp[i], x, dD);
@@ -288,25 +308,18 @@ __global__ __launch_bounds__(grad_waves<SPL>() * WAVE) void scan_grad_kernel(Sca
                     for (int s = 0; s < SPL; ++s)
                         old[s] += dA[s];
                     store_states<SPL>(&sum_A[k][w][lane * SPL], old);
-                    sum_D[k][0][w][lane] += dD;
-                    sum_D[k][1][w][lane] += dbias;
+                    dD = quad_sum(dD);
+                    dbias = quad_sum(dbias);
+                    if (j < 2)
+                        sum_D[k][j][w][lane >> 2] += j ? dbias : dD;
                 }
             }
-            float v[4];
-            channel_sums(acc, v);
-            const int x = 4 * (((lane >> 2) & 3)) + 2 * ((lane >> 4) & 1) + (lane >> 5);
-            const int t = 4 * x / (2 * SPL);
-            if (t < count) {
-                float *to = rows_bc + (long)t * P.G * (2 * S);
-                const int rest = 4 * x % (2 * SPL);          // tensor and state
-                if constexpr (SPL == 2) {
-                    *reinterpret_cast<float2 *>(to + j * SPL) = make_float2(v[0], v[1]);
-                    *reinterpret_cast<float2 *>(to + S + j * SPL) = make_float2(v[2], v[3]);
-                } else {
-                    *reinterpret_cast<f32x4 *>(to + rest / SPL * S + j * SPL + rest % SPL) =
-                        f32x4{v[0], v[1], v[2], v[3]};
-                }
-            }
+            float v[V];
+            channel_sums<V>(acc, v);
+            const int x = 4 * ((lane >> 2) & 3) + 2 * ((lane >> 4) & 1) + (lane >> 5);
+            const int t = V * x / (2 * SPL), rest = V * x % (2 * SPL);   // token; tensor and state
+            if (t < count)
+                store_states<V>(rows_bc + (long)t * P.G * (2 * S) + rest / SPL * S + j * SPL + rest % SPL, v);
         }
     }
     // the waves' sums, in order
@@ -322,8 +335,7 @@ __global__ __launch_bounds__(grad_waves<SPL>() * WAVE) void scan_grad_kernel(Sca
                 if (n < S) {
                     s += sum_A[k][q][(4 * cl + n / SPL) * SPL + n % SPL];
                 } else {
-                    const float *d = &sum_D[k][n - S][q][4 * cl];
-                    s += (d[0] + d[1]) + (d[2] + d[3]);
+                    s += sum_D[k][n - S][q][cl];
                 }
             }
             P.ws_sum[((long)part * P.C + (long)g * per + in0 + cl) * (S + 2) + n] = s;

@@ -142,10 +142,14 @@ template <typename T, int S, int K> struct GroupRows {
         const int lane = threadIdx.x & (WAVE - 1), e = (lane & 31) * EPL;
         float *p = &to[lane >> 5][0][0] + e;
         order();
+        if constexpr (EPL == 2) {
+            *reinterpret_cast<float2 *>(p) = make_float2(get(0), get(1));
+        } else {
 #pragma unroll
-        for (int i = 0; i < EPL; i += 4)
-            *reinterpret_cast<f32x4 *>(p + i) =
-                f32x4{get(i), get(i + 1), get(i + 2), get(i + 3)};
+            for (int i = 0; i < EPL; i += 4)
+                *reinterpret_cast<f32x4 *>(p + i) =
+                    f32x4{get(i), get(i + 1), get(i + 2), get(i + 3)};
+        }
         order();
     }
     // what a wave's lanes read from each other through LDS stays in order
