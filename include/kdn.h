@@ -535,7 +535,7 @@ unsigned long long kdn_linear_prefill_backward_workspace_size(
  *   - Parameters (weights, biases, A, D, scales) and their gradients are float32
  *     always; per-token tensors have the call's dtype.
  *   - Rows may be slices of wider rows: a stride is the elements from one token
- *     to the next (0: contiguous), at least the row and below 2^25.  Any channel
+ *     to the next (0: contiguous), at least the row and below 2^28 (the scan's: 2^25).  Any channel
  *     count, stride and element-aligned address is taken; rows of whole 16-byte
  *     pieces on such boundaries are quickest.  Outputs are contiguous.
  *   - Dense and packed batches, pools, slots and what is skipped are as for

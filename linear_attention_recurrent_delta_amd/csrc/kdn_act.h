@@ -82,4 +82,38 @@ template <typename T, int V> struct Pack {
     __device__ __forceinline__ void set(int i, float x) { r[i] = from_f32<T>(x); }
 };
 
+// Sums over `parts` rows of 16 columns of ws [parts][n], in 64 bits in a fixed order, by a
+// workgroup of NT threads: thread r * 16 + c adds every NT / 16-th row of column c, many
+// loads at once; the first 16 threads get the sums of columns first .. + 16.
+template <int NT>
+__device__ __forceinline__ double part_sums(const float *ws, long n, int parts, long first,
+                                            double (*lds)[16]) {
+    constexpr int STEP = NT / 16, AHEAD = 8;
+    const int c = threadIdx.x & 15, r = threadIdx.x >> 4;
+    const bool live = first + c < n;
+    double s = 0.;
+    for (int p = r; p < parts; p += AHEAD * STEP) {
+        float v[AHEAD];
+#pragma unroll
+        for (int i = 0; i < AHEAD; ++i) {
+            v[i] = 0.f;
+            if (live && p + i * STEP < parts)
+                v[i] = ws[(long)(p + i * STEP) * n + first + c];
+        }
+#pragma unroll
+        for (int i = 0; i < AHEAD; ++i)
+            s += (double)v[i];
+    }
+    s += __shfl_xor(s, 16, WAVE);
+    s += __shfl_xor(s, 32, WAVE);
+    if ((threadIdx.x & (WAVE - 1)) < 16)
+        lds[threadIdx.x / WAVE][c] = s;
+    __syncthreads();
+    s = lds[0][c];
+#pragma unroll
+    for (int i = 1; i < NT / WAVE; ++i)
+        s += lds[i][c];
+    return s;
+}
+
 }  // namespace kdn

@@ -49,11 +49,12 @@ template <typename Params> inline kdn_status batch_tables(Params &P, const kdn_p
 }
 
 // Elements between tokens (0: contiguous rows of `row` elements), any number of
-// them from `row` to 2^25.
-inline kdn_status row_stride(long long given, long long row, long *out) {
+// them from `row` to below 2^28 or the kernel's own limit.
+inline kdn_status row_stride(long long given, long long row, long *out,
+                             long long limit = 1LL << 28) {
     if (given == 0)
         given = row;
-    if (given < row || given >= (1LL << 25))
+    if (given < row || given >= limit)
         return KDN_ERR_SHAPE;
     *out = given;
     return KDN_OK;

@@ -315,35 +315,31 @@ __global__ __launch_bounds__(NT) void conv_grad_kernel(ConvParams P, int chunks,
     }
 }
 
-// The parts' sums, 64 channels a workgroup; behind those workgroups: zero
-// gradients of the rows behind the last sequence, and the states' of sequences
-// without tokens.
+// The parts' sums, 16 columns a workgroup; behind those workgroups: zero gradients of
+// the rows behind the last sequence, and the states' of sequences without tokens.
 constexpr int TAIL_WGS = 64;
 template <typename T>
-__global__ __launch_bounds__(NT) void conv_sum_kernel(ConvParams P, int chunks) {
-    const int W = P.W, lane = threadIdx.x & (WAVE - 1), wv = threadIdx.x / WAVE;
+__global__ __launch_bounds__(NT) void conv_sum_kernel(ConvParams P, long wide) {
+    const int W = P.W;
     const long id = blockIdx.x;
-    if (id < (long)chunks * (W + 1)) {
-        const int j = (int)(id % (W + 1));
-        const long c = id / (W + 1) * WAVE + lane;
-        double s = 0.;
-        if (c < P.C)
-            for (int p = wv; p < P.parts; p += NW)
-                s += (double)P.ws[((long)p * (W + 1) + j) * P.C + c];
-        __shared__ double sums[NW][WAVE];
-        sums[wv][lane] = s;
-        __syncthreads();
-        if (wv == 0 && c < P.C) {
-            for (int q = 1; q < NW; ++q)
-                s += sums[q][lane];
-            if (j < W)
-                P.dweight[c * W + j] = (float)s;
-            else if (P.dbias)
-                P.dbias[c] = (float)s;
+    if (id < wide) {
+        __shared__ double lds[NW][16];
+        const long n = (long)(W + 1) * P.C;
+        for (long first = id * 16; first < n; first += wide * 16) {
+            const long i = first + threadIdx.x;
+            const double s = part_sums<NT>(P.ws, n, P.parts, first, lds);
+            if (threadIdx.x < 16 && i < n) {
+                const long j = i / P.C, c = i - j * P.C;
+                if (j < W)
+                    P.dweight[c * W + j] = (float)s;
+                else if (P.dbias)
+                    P.dbias[c] = (float)s;
+            }
+            __syncthreads();             // the sums have been read
         }
         return;
     }
-    const long wg = id - (long)chunks * (W + 1);
+    const long wg = id - wide;
     if (wg < TAIL_WGS) {
         if (!P.block_offsets)
             return;
@@ -407,9 +403,9 @@ hipError_t launch_conv_grad_t(const ConvParams &P, hipStream_t st) {
         if (e != hipSuccess)
             return e;
     }
-    const int wide = (P.C + WAVE - 1) / WAVE;
+    const long wide = min(((long)(W + 1) * P.C + 15) / 16, 65536l);
     const long empty = P.dstate0 && (P.block_offsets || P.T == 0) ? P.N : 0;
-    hipLaunchKernelGGL((conv_sum_kernel<T>), dim3((unsigned)((long)wide * (W + 1) + TAIL_WGS + empty)),
+    hipLaunchKernelGGL((conv_sum_kernel<T>), dim3((unsigned)(wide + TAIL_WGS + empty)),
                        dim3(NT), 0, st, Q, wide);
     return hipGetLastError();
 }

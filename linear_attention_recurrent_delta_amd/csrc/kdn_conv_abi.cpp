@@ -146,7 +146,7 @@ kdn_status kdn_causal_conv_backward(kdn_dtype dtype, int N, int T, int C, int W,
     kdn::ConvParams P;
     if (kdn_status st = conv_shape(P, dtype, N, T, C, W, act, x_stride, packed))
         return st;
-    if (!launchable((C + 63LL) / 64 * (W + 1) + 64 + N, 256))
+    if (!launchable(65536LL + 64 + N, 256))
         return KDN_ERR_SHAPE;
     const long long es = P.bf16 ? 2 : 4, tok = P.tokens;
     if ((tok * C > 0 && (!x || !d_y || !dx)) || (C > 0 && (!weight || !dweight)))

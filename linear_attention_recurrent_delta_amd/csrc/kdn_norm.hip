@@ -424,8 +424,8 @@ __global__ __launch_bounds__(NT_MAX) void residual_norm_grad_kernel(ResidualNorm
         part[blockIdx.x] = cols[0];
 }
 
-// out[c] = sum over parts of ws[part][c], in order, in 64 bits; 64 columns a
-// workgroup.  Two arrays in one launch: those of ws2 behind those of ws.
+// out[c] = sum over parts of ws[part][c], 16 columns a workgroup.  Two arrays in one
+// launch: those of ws2 behind those of ws.
 struct Sums {
     const float *ws, *ws2;
     float *out, *out2;
@@ -433,28 +433,17 @@ struct Sums {
     int parts;
 };
 __global__ __launch_bounds__(NT_MAX) void sum_parts_kernel(Sums S) {
-    const int lane = threadIdx.x & (WAVE - 1), wv = threadIdx.x / WAVE, nw = NT_MAX / WAVE;
-    const long wide = (S.n + WAVE - 1) / WAVE;
+    __shared__ double lds[NT_MAX / WAVE][16];
+    const long wide = (S.n + 15) / 16;
     const bool second = blockIdx.x >= wide;
-    const float *ws = second ? S.ws2 : S.ws;
-    const long n = second ? S.n2 : S.n;
-    const long c = ((long)blockIdx.x - (second ? wide : 0)) * WAVE + lane;
-    double s = 0.;
-    if (c < n)
-        for (int p = wv; p < S.parts; p += nw)
-            s += (double)ws[(long)p * n + c];
-    __shared__ double sums[NT_MAX / WAVE][WAVE];
-    sums[wv][lane] = s;
-    __syncthreads();
-    if (wv == 0 && c < n) {
-        for (int q = 1; q < nw; ++q)
-            s += sums[q][lane];
-        (second ? S.out2 : S.out)[c] = (float)s;
-    }
+    const long n = second ? S.n2 : S.n, first = ((long)blockIdx.x - (second ? wide : 0)) * 16;
+    const double s = part_sums<NT_MAX>(second ? S.ws2 : S.ws, n, S.parts, first, lds);
+    if (threadIdx.x < 16 && first + threadIdx.x < n)
+        (second ? S.out2 : S.out)[first + threadIdx.x] = (float)s;
 }
 
 hipError_t sum_parts(const Sums &S, hipStream_t st) {
-    const long wgs = (S.n + WAVE - 1) / WAVE + (S.n2 + WAVE - 1) / WAVE;
+    const long wgs = (S.n + 15) / 16 + (S.n2 + 15) / 16;
     if (wgs == 0)
         return hipSuccess;
     hipLaunchKernelGGL(sum_parts_kernel, dim3((unsigned)wgs), dim3(NT_MAX), 0, st, S);

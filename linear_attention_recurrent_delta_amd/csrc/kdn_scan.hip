@@ -10,7 +10,7 @@
 namespace kdn {
 namespace scan {
 
-constexpr long SCAN_MANY = 2048;
+constexpr long SCAN_MANY = 2048, SCAN_OWN_WGS = 4096;
 
 // Tokens that a wave takes at a time: their decays and inputs stay in registers
 // between the two passes over them.
@@ -217,19 +217,20 @@ __global__ __launch_bounds__(NW == 1 ? 256 : NW *WAVE, 2) void scan_kernel(ScanP
 // A tile's own contribution to the state from nothing, U = sum_t (decay behind t)
 // dt_t x_t B_t, the sum of its time steps, and with REV what its tokens hand to the
 // reverse recurrence, Q = sum_t (decay up to and with t) dy'_t C_t, dy' = dy silu(z).
-// A workgroup has a block and run of 16 channels, a wave every fourth of its tiles,
-// token by token.
+// A workgroup has a run of 16 channels and a share of a block: its waves take every
+// fourth of every `classes`-th four tiles, token by token.
 // ---------------------------------------------------------------------------
 constexpr int OWN_WAVES = 4;
 template <typename T, int SPL, bool REV>
 __global__ __launch_bounds__(OWN_WAVES *WAVE) void scan_own_kernel(ScanParams P, int groups,
-                                                                   long units) {
+                                                                   int classes, long units) {
     constexpr bool FINE = sizeof(T) == 4;
     constexpr int S = 4 * SPL, K = steps<SPL>(), TILE = scan_tile(S);
     __shared__ float bc[OWN_WAVES][2][K][S];
     const int lane = threadIdx.x & (WAVE - 1), j = lane & 3, w = wave_id();
     const int runs = groups * P.G;
-    const long unit = xcd_unit(blockIdx.x, units), b = unit / runs;
+    const long unit = xcd_unit(blockIdx.x, units), b = unit / runs / classes;
+    const int share = (int)(unit / runs % classes);
     const Channels ch(P, (int)(unit % runs), groups);
     const Block B = get_block(P, b);
     if (B.count <= 0 || B.slot < 0 || (!REV && B.single))
@@ -239,7 +240,7 @@ __global__ __launch_bounds__(OWN_WAVES *WAVE) void scan_own_kernel(ScanParams P,
     float A2[SPL];
     load_A<SPL>(P, ch.c, j, A2);
     const float bias = P.bias ? P.bias[ch.c] : 0.f;
-    for (int t1 = w * TILE; t1 < stop; t1 += OWN_WAVES * TILE) {
+    for (int t1 = (share * OWN_WAVES + w) * TILE; t1 < stop; t1 += classes * OWN_WAVES * TILE) {
         const int n = min(TILE, B.count - t1);
         float end[SPL], back[SPL], all[SPL];
 #pragma unroll
@@ -302,13 +303,14 @@ __global__ __launch_bounds__(OWN_WAVES *WAVE) void scan_own_kernel(ScanParams P,
 // ---------------------------------------------------------------------------
 // Join of the tiles along each sequence: a tile's own contribution U becomes the
 // state at its start, h <- 2^(A2 sum dt) h + U; reverse (tiles last to first): Q
-// becomes the reverse state behind its end, and behind the first tile is dS0.  One
-// thread holds 4 states of a channel; JOIN tiles are requested ahead.
+// becomes the reverse state behind its end, and behind the first tile is dS0.  A
+// thread holds two states of a channel; the next JOIN tiles are on their way while as
+// many are joined.
 // ---------------------------------------------------------------------------
 constexpr int JOIN = 8, JOIN_NT = 256;
 template <bool REV>
-__device__ __forceinline__ void join(const ScanParams &P, int seq, long quad, bool all) {
-    const long size = (long)P.C * P.S, e = 4 * quad;
+__device__ __forceinline__ void join(const ScanParams &P, int seq, long e, bool all) {
+    const long size = (long)P.C * P.S;
     long b0 = (long)seq * P.nblocks, b1 = b0 + P.nblocks, slot = seq, first, n;
     if (P.block_offsets) {
         b0 = P.block_offsets[seq];
@@ -319,12 +321,12 @@ __device__ __forceinline__ void join(const ScanParams &P, int seq, long quad, bo
     }
     const float *from = REV ? P.dS_out : P.S0;
     float *pass = REV ? P.dS0 : P.S_out;
-    f32x4 h = {0.f, 0.f, 0.f, 0.f};
+    float2 h = make_float2(0.f, 0.f);
     if (from)
-        h = *reinterpret_cast<const f32x4 *>(from + slot * size + e);
+        h = *reinterpret_cast<const float2 *>(from + slot * size + e);
     if (b1 <= b0) {                  // no tokens: the state passes on
         if (pass && pass != from)
-            *reinterpret_cast<f32x4 *>(pass + slot * size + e) = h;
+            *reinterpret_cast<float2 *>(pass + slot * size + e) = h;
         return;
     }
     if (b1 - b0 == 1 && !all)
@@ -344,34 +346,56 @@ __device__ __forceinline__ void join(const ScanParams &P, int seq, long quad, bo
     float *ws = REV ? P.ws_rstate : P.ws_state;
     if (!ws || first < 0 || n <= 0 || base + tiles - 1 + (tiles - 1) / per >= P.tile_slots)
         return;
-    const f32x4 A = *reinterpret_cast<const f32x4 *>(P.A + e);
+    const float2 A = *reinterpret_cast<const float2 *>(P.A + e);
     const long c = e / P.S;
-    auto place = [&](long i) {
-        const long t = REV ? tiles - 1 - i : i;
-        return base + t + t / per;
+    // the tiles in the order of the join
+    struct Place {
+        long slot, in;               // slot, and index in the block
     };
+    auto next = [&](Place &p) {
+        if (REV ? p.in == 0 : p.in + 1 == per) {
+            p.in = REV ? per - 1 : 0;
+            p.slot += REV ? -2 : 2;
+        } else {
+            p.in += REV ? -1 : 1;
+            p.slot += REV ? -1 : 1;
+        }
+    };
+    const long t0 = REV ? tiles - 1 : 0;
+    Place at{base + t0 + t0 / per, t0 % per}, ahead = at;
     const long need = REV ? tiles : tiles - 1;      // own contributions that are used
-    for (long i = 0; i < tiles; i += JOIN) {
-        f32x4 u[JOIN];
-        float d[JOIN];
+    float2 u[JOIN], u1[JOIN];
+    float d[JOIN], d1[JOIN];
+    auto load = [&](long i, float2(&v)[JOIN], float(&t)[JOIN]) {
 #pragma unroll
         for (int k = 0; k < JOIN; ++k)
             if (i + k < need) {
-                u[k] = *reinterpret_cast<const f32x4 *>(ws + place(i + k) * size + e);
-                d[k] = P.ws_dt[place(i + k) * P.C + c];
+                v[k] = *reinterpret_cast<const float2 *>(ws + ahead.slot * size + e);
+                t[k] = P.ws_dt[ahead.slot * P.C + c];
+                next(ahead);
             }
+    };
+    auto step = [&](long i, const float2(&v)[JOIN], const float(&t)[JOIN]) {
 #pragma unroll
         for (int k = 0; k < JOIN; ++k)
             if (i + k < tiles) {
-                *reinterpret_cast<f32x4 *>(ws + place(i + k) * size + e) = h;
-                if (i + k < need)
-#pragma unroll
-                    for (int q = 0; q < 4; ++q)
-                        h[q] = fmaf(__builtin_amdgcn_exp2f(d[k] * LOG2E * A[q]), h[q], u[k][q]);
+                *reinterpret_cast<float2 *>(ws + at.slot * size + e) = h;
+                next(at);
+                if (i + k < need) {
+                    h.x = fmaf(__builtin_amdgcn_exp2f(t[k] * LOG2E * A.x), h.x, v[k].x);
+                    h.y = fmaf(__builtin_amdgcn_exp2f(t[k] * LOG2E * A.y), h.y, v[k].y);
+                }
             }
+    };
+    load(0, u, d);
+    for (long i = 0; i < tiles; i += 2 * JOIN) {
+        load(i + JOIN, u1, d1);
+        step(i, u, d);
+        load(i + 2 * JOIN, u, d);
+        step(i + JOIN, u1, d1);
     }
     if (REV && pass)
-        *reinterpret_cast<f32x4 *>(pass + slot * size + e) = h;
+        *reinterpret_cast<float2 *>(pass + slot * size + e) = h;
 }
 
 template <bool REV>
@@ -382,14 +406,14 @@ __global__ __launch_bounds__(JOIN_NT) void scan_join_kernel(ScanParams P, int pi
         reverse = id & 1;
         id >>= 1;
     }
-    const long quad = (id % pieces) * JOIN_NT + threadIdx.x;
+    const long e = 2 * ((id % pieces) * JOIN_NT + threadIdx.x);
     const int seq = (int)(id / pieces);
-    if (quad >= (long)P.C * P.S / 4)
+    if (e >= (long)P.C * P.S)
         return;
     if (REV && reverse)
-        join<true>(P, seq, quad, true);
+        join<true>(P, seq, e, true);
     else
-        join<false>(P, seq, quad, REV);
+        join<false>(P, seq, e, REV);
 }
 
 // ---------------------------------------------------------------------------
@@ -473,14 +497,19 @@ hipError_t launch_t(const ScanParams &P, hipStream_t st) {
 template <typename T, int SPL>
 hipError_t launch_own_t(const ScanParams &P, bool reverse, hipStream_t st) {
     const int groups = scan_groups(P.C, P.G);
-    const long units = scan_total_blocks(P) * groups * P.G;
-    if (units == 0)
+    const long blocks = scan_total_blocks(P), runs = (long)groups * P.G;
+    if (blocks * runs == 0)
         return hipSuccess;
+    // blocks of many tiles are shared out where they are few
+    constexpr int FOUR = OWN_WAVES * scan_tile(4 * SPL);
+    const long most = min((long)P.block, P.tokens), fours = (most + FOUR - 1) / FOUR;
+    const int classes = (int)max(1l, min(fours, (SCAN_OWN_WGS + blocks * runs - 1) / (blocks * runs)));
+    const long units = blocks * classes * runs;
     const dim3 grid((unsigned)units), block(OWN_WAVES * WAVE);
     if (reverse)
-        hipLaunchKernelGGL((scan_own_kernel<T, SPL, true>), grid, block, 0, st, P, groups, units);
+        hipLaunchKernelGGL((scan_own_kernel<T, SPL, true>), grid, block, 0, st, P, groups, classes, units);
     else
-        hipLaunchKernelGGL((scan_own_kernel<T, SPL, false>), grid, block, 0, st, P, groups, units);
+        hipLaunchKernelGGL((scan_own_kernel<T, SPL, false>), grid, block, 0, st, P, groups, classes, units);
     return hipGetLastError();
 }
 
@@ -512,8 +541,7 @@ static hipError_t own(const ScanParams &P, bool reverse, hipStream_t st) {
 static hipError_t joins(const ScanParams &P, bool reverse, hipStream_t st) {
     if (P.N == 0)
         return hipSuccess;
-    const long quads = (long)P.C * P.S / 4;
-    const int pieces = (int)((quads + scan::JOIN_NT - 1) / scan::JOIN_NT);
+    const int pieces = (int)(((long)P.C * P.S / 2 + scan::JOIN_NT - 1) / scan::JOIN_NT);
     if (reverse)
         hipLaunchKernelGGL((scan::scan_join_kernel<true>), dim3((unsigned)(2l * P.N * pieces)),
                            dim3(scan::JOIN_NT), 0, st, P, pieces);

@@ -37,6 +37,9 @@ struct Strides {
     long long x, delta, z, B, C;
 };
 
+// Elements of a row: 16 rows are below 2^32 bytes.
+constexpr long long ROW = 1LL << 25;
+
 kdn_status scan_shape(kdn::ScanParams &P, int dtype, int N, int T, int C, int S, int G,
                       const Strides &st, const kdn_packed *packed) {
     if (!kdn::valid_dtype(dtype))
@@ -50,11 +53,11 @@ kdn_status scan_shape(kdn::ScanParams &P, int dtype, int N, int T, int C, int S,
         return e;
     P.bf16 = dtype == KDN_BF16;
     P.C = C; P.S = S; P.G = std::max(G, 1);
-    if (kdn_status e = kdn::row_stride(st.x, C, &P.x_stride)) return e;
-    if (kdn_status e = kdn::row_stride(st.delta, C, &P.d_stride)) return e;
-    if (kdn_status e = kdn::row_stride(st.z, C, &P.z_stride)) return e;
-    if (kdn_status e = kdn::row_stride(st.B, (long long)G * S, &P.b_stride)) return e;
-    if (kdn_status e = kdn::row_stride(st.C, (long long)G * S, &P.c_stride)) return e;
+    if (kdn_status e = kdn::row_stride(st.x, C, &P.x_stride, ROW)) return e;
+    if (kdn_status e = kdn::row_stride(st.delta, C, &P.d_stride, ROW)) return e;
+    if (kdn_status e = kdn::row_stride(st.z, C, &P.z_stride, ROW)) return e;
+    if (kdn_status e = kdn::row_stride(st.B, (long long)G * S, &P.b_stride, ROW)) return e;
+    if (kdn_status e = kdn::row_stride(st.C, (long long)G * S, &P.c_stride, ROW)) return e;
     if (P.pool * C >= (1LL << 40))
         return KDN_ERR_SHAPE;
     return KDN_OK;
@@ -69,7 +72,7 @@ kdn_status scan_blocks(kdn::ScanParams &P, bool packed, int block) {
     const long long blocks = packed ? P.nblocks : (long long)P.N * P.nblocks;
     const long long runs = P.C > 0 ? (long long)kdn::scan_groups(P.C, P.G) * P.G : 0;
     P.tile_slots = kdn::tile_slots(P.tokens, blocks, P.S);
-    const long long pieces = ((long long)P.C * P.S / 4 + 255) / 256;
+    const long long pieces = ((long long)P.C * P.S + 255) / 256;
     if (blocks >= (1LL << 32) || !launchable(blocks * runs, 512) ||
         !launchable(2LL * P.N * pieces, 256) || P.tile_slots * P.C >= (1LL << 40))
         return KDN_ERR_SHAPE;
@@ -105,7 +108,7 @@ void grad_shares(kdn::ScanParams &P, bool packed) {
     const long long sets = groups > 0 ? (long long)kdn::scan_sets(P) * P.G : 0;
     const long long in_block = std::min<long long>(P.block, std::max<long long>(P.tokens, 1));
     const long long per_block = (in_block + tile - 1) / tile;
-    long long parts = sets > 0 ? std::max(1LL, (GRAD_WGS + sets - 1) / sets) : 0;
+    long long parts = sets > 0 ? std::max(1LL, GRAD_WGS / sets) : 0;
     P.classes = (int)std::min(per_block, blocks > 0 ? (4 * parts + blocks - 1) / blocks : 1);
     P.parts = (int)std::min(parts, blocks * P.classes);
 }
