@@ -29,7 +29,10 @@ template <typename T, int K> struct Run {
     T x[K / 4], d[K / 4], z[K / 4], g[K / 4];
     __device__ __forceinline__ void load(const ScanParams &P, const Channels &ch, long first,
                                          int count) {
-        const int j = threadIdx.x & 3;
+        // the rows' offsets are made again for every run: kept over the runs they would
+        // not fit the registers, and a reload waits for all loads before it
+        int j = threadIdx.x & 3;
+        asm volatile("" : "+v"(j));
         const Rows<T, K> rx(P.x, first, P.x_stride, P.C, count);
         const Rows<T, K> rd(P.delta, first, P.d_stride, P.C, count);
         const Rows<T, K> rz(P.z, first, P.z_stride, P.C, P.z ? count : 0);
@@ -148,8 +151,10 @@ __global__ __launch_bounds__(grad_waves<SPL>() * WAVE, 2) void scan_grad_kernel(
                     const long at = (slot * P.C + ch.c) * S + j * SPL;
                     load_states<SPL>(P.ws_state + at, hs);
                     load_states<SPL>(P.ws_rstate + at, r);
-                    if (k + 1 < runs)
-                        next.load(P, Channels(P, g * groups + run0 + k + 1, groups), first, count);
+                    // behind the last run nothing is read, but without a branch, behind
+                    // which all loads would be waited for
+                    next.load(P, Channels(P, g * groups + run0 + min(k + 1, runs - 1), groups),
+                              first, k + 1 < runs ? count : 0);
                     load_states<SPL>(&par_A[k][lane * SPL], A2);
                     const float bias = par[k][0][lane >> 2], D = par[k][1][lane >> 2];
                     float dt[K / 4], in[K / 4], dp[K / 4], sum = 0.f;
@@ -277,6 +282,8 @@ __global__ __launch_bounds__(grad_waves<SPL>() * WAVE, 2) void scan_grad_kernel(
                         }
                     });
                     float dD = 0.f, dbias = 0.f;
+                    int j1 = j;
+                    asm volatile("" : "+v"(j1));
                     const Rows<T, K> rx(P.dx, first, P.C, P.C, count);
                     const Rows<T, K> rd(P.ddelta, first, P.C, P.C, count);
                     const Rows<T, K> rz(P.dz, first, P.C, P.C, P.z ? count : 0);
@@ -297,7 +304,7 @@ __global__ __launch_bounds__(grad_waves<SPL>() * WAVE, 2) void scan_grad_kernel(
                             dD = fmaf(dp[i], x, dD);
                             dbias += dd;
                         }
-                        const int at = rx.at(4 * i + j, P.C, ch.c, ch.live);
+                        const int at = rx.at(4 * i + j1, P.C, ch.c, ch.live);
                         rx.store(from_f32<T>(dx), at);
                         rd.store(from_f32<T>(dd), at);
                         rz.store(from_f32<T>(dz[i]), at);
