@@ -90,14 +90,17 @@ __global__ __launch_bounds__(grad_waves<SPL>() * WAVE, 2) void scan_grad_kernel(
     constexpr int S = 4 * SPL, K = grad_steps<SPL>(), NW = grad_waves<SPL>(), TILE = NW * K;
     constexpr int M = 2 * K * SPL, V = M / 16;     // sums of a lane, and after the exchange
     __shared__ float bc[NW][2][K][S];
-    __shared__ float ends[2][3][NW][WAVE * SPL];
+    // each wave's decay, and its ends of both recurrences from nothing, which the fold
+    // makes the states in front of its tokens and behind them
+    __shared__ float ends[3][NW][WAVE * SPL];
+    constexpr int ITEMS = 2 * WAVE * SPL / NW, ROUNDS = (ITEMS + WAVE - 1) / WAVE;
     __shared__ float sum_A[scan_per_set(S)][NW][WAVE * SPL];
     __shared__ float sum_D[scan_per_set(S)][2][NW][SCAN_CHANNELS];
     __shared__ float par_A[scan_per_set(S)][WAVE * SPL], par[scan_per_set(S)][2][SCAN_CHANNELS];
     const int lane = threadIdx.x & (WAVE - 1), j = lane & 3, w = wave_id();
     const int set = blockIdx.x % sets, g = (int)(blockIdx.x / sets) % P.G;
     const int part = (int)(blockIdx.x / sets) / P.G;
-    const int run0 = set * P.per_set, runs = min(P.per_set, groups - run0);
+    const int run0 = set * P.per_set, runs = min(P.per_set, groups - run0), per = P.C / P.G;
     for (int k = 0; k < runs; ++k) {         // a wave's own place: no barrier
         const float zero[SPL] = {};
         store_states<SPL>(&sum_A[k][w][lane * SPL], zero);
@@ -112,7 +115,6 @@ __global__ __launch_bounds__(grad_waves<SPL>() * WAVE, 2) void scan_grad_kernel(
         }
     }
     __syncthreads();
-    int buf = 0;
     for (long u = part; u < blocks * P.classes; u += P.parts) {
         const long b = u / P.classes;
         const Block B = get_block(P, b);
@@ -144,13 +146,25 @@ __global__ __launch_bounds__(grad_waves<SPL>() * WAVE, 2) void scan_grad_kernel(
                 group.load(P, g, first, count);
                 next.load(P, Channels(P, g * groups + run0, groups), first, count);
                 group.put(bc[w]);
-                for (int k = 0; k < runs; ++k, buf ^= 1) {
+                for (int k = 0; k < runs; ++k) {
                     const Channels ch(P, g * groups + run0 + k, groups);
                     const Run<T, K> now = next;
                     float A2[SPL], hs[SPL], r[SPL];
-                    const long at = (slot * P.C + ch.c) * S + j * SPL;
-                    load_states<SPL>(P.ws_state + at, hs);
-                    load_states<SPL>(P.ws_rstate + at, r);
+                    // the tile's states that this lane folds: its waves have 1 / NW of
+                    // the run's 16 S each, forward ones and then reverse ones
+                    float state[ROUNDS];
+                    const long run_at = (slot * P.C + (long)g * per + (run0 + k) * SCAN_CHANNELS) * S;
+#pragma unroll
+                    for (int n = 0; n < ROUNDS; ++n) {
+                        int it = lane + n * WAVE;
+                        if constexpr (SPL == 4)
+                            asm volatile("" : "+v"(it));
+                        const int e = w * (ITEMS / 2) + it % (ITEMS / 2);
+                        const int behind = (per - (run0 + k) * SCAN_CHANNELS) * S - 1;
+                        state[n] = 0.f;
+                        if (it < ITEMS)
+                            state[n] = (it < ITEMS / 2 ? P.ws_state : P.ws_rstate)[run_at + min(e, behind)];
+                    }
                     // behind the last run nothing is read, but without a branch, behind
                     // which all loads would be waited for
                     next.load(P, Channels(P, g * groups + run0 + min(k + 1, runs - 1), groups),
@@ -197,42 +211,39 @@ __global__ __launch_bounds__(grad_waves<SPL>() * WAVE, 2) void scan_grad_kernel(
 #pragma unroll
                     for (int s = 0; s < SPL; ++s)
                         all[s] = __builtin_amdgcn_exp2f(sum * A2[s]);
-                    store_states<SPL>(&ends[buf][0][w][lane * SPL], all);
-                    store_states<SPL>(&ends[buf][1][w][lane * SPL], end);
-                    store_states<SPL>(&ends[buf][2][w][lane * SPL], back);
+                    store_states<SPL>(&ends[0][w][lane * SPL], all);
+                    store_states<SPL>(&ends[1][w][lane * SPL], end);
+                    store_states<SPL>(&ends[2][w][lane * SPL], back);
                     __syncthreads();
-                    // the states in front of the wave's tokens and behind them; the next
-                    // wave's are on their way while one's are used
-                    if (w > 0) {
-                        load_states<SPL>(&ends[buf][0][0][lane * SPL], all);
-                        load_states<SPL>(&ends[buf][1][0][lane * SPL], end);
-                        for (int q = 1; q <= w; ++q) {
-                            float a1[SPL], e1[SPL];
-                            load_states<SPL>(&ends[buf][0][q][lane * SPL], a1);
-                            load_states<SPL>(&ends[buf][1][q][lane * SPL], e1);
 #pragma unroll
-                            for (int s = 0; s < SPL; ++s) {
-                                hs[s] = fmaf(all[s], hs[s], end[s]);
-                                all[s] = a1[s];
-                                end[s] = e1[s];
+                    for (int n = 0; n < ROUNDS; ++n) {
+                        // (where registers are short, places are made again, as the rows' offsets)
+                        int it = lane + n * WAVE;
+                        if constexpr (SPL == 4)
+                            asm volatile("" : "+v"(it));
+                        const int e = w * (ITEMS / 2) + it % (ITEMS / 2);
+                        if (it < ITEMS) {
+                            // the waves in their order, or from the last one
+                            const bool rev = it >= ITEMS / 2;
+                            const int step = rev ? -WAVE * SPL : WAVE * SPL;
+                            const float *pa = &ends[0][rev ? NW - 1 : 0][e];
+                            float *pe = &ends[rev ? 2 : 1][rev ? NW - 1 : 0][e];
+                            float va[NW], ve[NW], v = state[n];
+#pragma unroll
+                            for (int q = 0; q < NW; ++q) {
+                                va[q] = pa[q * step];
+                                ve[q] = pe[q * step];
+                            }
+#pragma unroll
+                            for (int q = 0; q < NW; ++q) {
+                                pe[q * step] = v;
+                                v = fmaf(va[q], v, ve[q]);
                             }
                         }
                     }
-                    if (w < NW - 1) {
-                        load_states<SPL>(&ends[buf][0][NW - 1][lane * SPL], all);
-                        load_states<SPL>(&ends[buf][2][NW - 1][lane * SPL], back);
-                        for (int q = NW - 2; q >= w; --q) {
-                            float a1[SPL], e1[SPL];
-                            load_states<SPL>(&ends[buf][0][q][lane * SPL], a1);
-                            load_states<SPL>(&ends[buf][2][q][lane * SPL], e1);
-#pragma unroll
-                            for (int s = 0; s < SPL; ++s) {
-                                r[s] = fmaf(all[s], r[s], back[s]);
-                                all[s] = a1[s];
-                                back[s] = e1[s];
-                            }
-                        }
-                    }
+                    __syncthreads();
+                    load_states<SPL>(&ends[1][w][lane * SPL], hs);
+                    load_states<SPL>(&ends[2][w][lane * SPL], r);
                     // forwards: h[i] becomes the state before token i
                     float part[4], y[K / 4], dz[K / 4];
                     unrolled<K>([&](auto I) {
@@ -332,7 +343,7 @@ __global__ __launch_bounds__(grad_waves<SPL>() * WAVE, 2) void scan_grad_kernel(
     // the waves' sums, in order
     __syncthreads();
     for (int k = 0; k < runs; ++k) {
-        const int per = P.C / P.G, in0 = (run0 + k) * SCAN_CHANNELS;
+        const int in0 = (run0 + k) * SCAN_CHANNELS;
         for (int i = threadIdx.x; i < SCAN_CHANNELS * (S + 2); i += NW * WAVE) {
             const int cl = i / (S + 2), n = i % (S + 2);
             if (in0 + cl >= per)
