@@ -59,10 +59,11 @@ __device__ __forceinline__ int by_length(const ScanParams &P, int p) {
 
 // ---------------------------------------------------------------------------
 // Outputs.  NW waves of a workgroup walk one block, K tokens each at a time: every
-// wave scans its tokens from nothing, hands its end and its decay to the others
-// through LDS, folds those before it into its start and goes through its tokens
-// again, with their decays and inputs from registers (one more product and sum for
-// a state than a walk by one wave, which NW = 1 is).
+// wave scans its tokens from nothing and puts its end and its decay into LDS; the
+// lanes, one for each of the run's 16 S states, fold the waves' ends into the states
+// in front of their tokens and carry the last on; and every wave goes through its
+// tokens again, with their decays and inputs from registers (one more product and sum
+// for a state than a walk by one wave, which NW = 1 is).
 // ---------------------------------------------------------------------------
 template <typename T, int SPL, int NW>
 __global__ __launch_bounds__(NW == 1 ? 256 : NW *WAVE, 2) void scan_kernel(ScanParams P,
@@ -71,7 +72,9 @@ __global__ __launch_bounds__(NW == 1 ? 256 : NW *WAVE, 2) void scan_kernel(ScanP
     constexpr bool FINE = sizeof(T) == 4;
     constexpr int S = 4 * SPL, K = steps<SPL>(), WAVES = NW == 1 ? 4 : NW;
     __shared__ float bc[WAVES][2][K][S];
-    __shared__ float ends[NW == 1 ? 1 : 2][2][NW == 1 ? 1 : NW][WAVE * SPL];
+    // each wave's decay; its end from nothing, and then the state in front of its tokens
+    __shared__ float ends[2][NW][NW == 1 ? 1 : WAVE * SPL];
+    constexpr int FOLD = WAVE * SPL / NW;            // states that a wave's lanes fold
     const int lane = threadIdx.x & (WAVE - 1), j = lane & 3, w = wave_id();
     const int seg = NW == 1 ? 0 : w;
     // NW = 1: each wave has a run of channels of its own
@@ -90,26 +93,27 @@ __global__ __launch_bounds__(NW == 1 ? 256 : NW *WAVE, 2) void scan_kernel(ScanP
     float A2[SPL], h[SPL];
     load_A<SPL>(P, ch.c, j, A2);
     const float bias = P.bias ? P.bias[ch.c] : 0.f, D = P.D ? P.D[ch.c] : 0.f;
-    if (!B.single)
-        load_states<SPL>(P.ws_state + (tile_slot(b, B.first, 0, S) * P.C + ch.c) * S + j * SPL, h);
-    else if (P.S0)
-        load_states<SPL>(P.S0 + at, h);
-    else
+    // the state in front of the block: the lane's own states, or the one that it folds
+    const float *from = B.single ? P.S0 : P.ws_state;
+    const long from_slot = B.single ? B.slot : tile_slot(b, B.first, 0, S);
+    const int per = P.C / P.G, run = (int)(unit % runs) % groups;
+    const int fold = w * FOLD + lane, channels = min(SCAN_CHANNELS, per - run * SCAN_CHANNELS);
+    const bool folds = NW > 1 && lane < FOLD && fold < channels * S;
+    const long fold_at = ((long)ch.g * per + run * SCAN_CHANNELS) * S + fold;
+    float carry = 0.f;
 #pragma unroll
-        for (int s = 0; s < SPL; ++s)
-            h[s] = 0.f;
+    for (int s = 0; s < SPL; ++s)
+        h[s] = 0.f;
+    if (NW > 1 && from && folds)
+        carry = from[from_slot * P.C * S + fold_at];
+    if (NW == 1 && from)
+        load_states<SPL>(from + (from_slot * P.C + ch.c) * S + j * SPL, h);
 
     TokenRows<T, K> rows;
     GroupRows<T, S, K> group;
     rows.load(P, ch, B.first + seg * K, B.count - seg * K);
     group.load(P, ch.g, B.first + seg * K, B.count - seg * K);
-    // the state is here before the first barrier: S_out, which a wave may write behind
-    // it, may be S0
-#pragma unroll
-    for (int s = 0; s < SPL; ++s)
-        asm volatile("" : "+v"(h[s]));
-    int buf = 0;
-    for (int t0 = 0; t0 < B.count; t0 += NW * K, buf ^= 1) {
+    for (int t0 = 0; t0 < B.count; t0 += NW * K) {
         const int own = t0 + seg * K, count = B.count - own;
         // this round's values; the next round's are requested before the work on them
         const TokenRows<T, K> now = rows;
@@ -170,28 +174,28 @@ __global__ __launch_bounds__(NW == 1 ? 256 : NW *WAVE, 2) void scan_kernel(ScanP
                 }
             });
             sum = quad_sum(sum);
-            float all[SPL], next[SPL];
+            float all[SPL];
 #pragma unroll
             for (int s = 0; s < SPL; ++s)
                 all[s] = __builtin_amdgcn_exp2f(sum * A2[s]);
-            store_states<SPL>(&ends[buf][0][seg][lane * SPL], all);
-            store_states<SPL>(&ends[buf][1][seg][lane * SPL], end);
+            store_states<SPL>(&ends[0][seg][lane * SPL], all);
+            store_states<SPL>(&ends[1][seg][lane * SPL], end);
             __syncthreads();
+            if (lane < FOLD) {
+                float va[NW], ve[NW];
 #pragma unroll
-            for (int s = 0; s < SPL; ++s)
-                next[s] = h[s];
+                for (int q = 0; q < NW; ++q) {
+                    va[q] = ends[0][q][fold];
+                    ve[q] = ends[1][q][fold];
+                }
 #pragma unroll
-            for (int q = 0; q < NW; ++q) {
-                load_states<SPL>(&ends[buf][0][q][lane * SPL], all);
-                load_states<SPL>(&ends[buf][1][q][lane * SPL], end);
-                if (q == seg)
-#pragma unroll
-                    for (int s = 0; s < SPL; ++s)
-                        h[s] = next[s];
-#pragma unroll
-                for (int s = 0; s < SPL; ++s)
-                    next[s] = fmaf(all[s], next[s], end[s]);
+                for (int q = 0; q < NW; ++q) {
+                    ends[1][q][fold] = carry;
+                    carry = fmaf(va[q], carry, ve[q]);
+                }
             }
+            __syncthreads();
+            load_states<SPL>(&ends[1][seg][lane * SPL], h);
             unrolled<K>([&](auto I) {
                 constexpr int i = I;
                 float Ct[SPL], y = 0.f;
@@ -204,13 +208,15 @@ __global__ __launch_bounds__(NW == 1 ? 256 : NW *WAVE, 2) void scan_kernel(ScanP
                 part[i % 4] = y;
                 output(I);
             });
-#pragma unroll
-            for (int s = 0; s < SPL; ++s)
-                h[s] = next[s];
         }
     }
-    if (P.S_out && B.last && seg == 0 && ch.live)
-        store_states<SPL>(P.S_out + at, h);
+    // (where S_out is S0: a state is read and written by the same lane)
+    if (P.S_out && B.last) {
+        if (NW == 1 && ch.live)
+            store_states<SPL>(P.S_out + at, h);
+        if (NW > 1 && folds)
+            P.S_out[B.slot * P.C * S + fold_at] = carry;
+    }
 }
 
 // ---------------------------------------------------------------------------
