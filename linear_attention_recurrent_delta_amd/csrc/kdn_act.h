@@ -56,16 +56,20 @@ template <typename T, int V> struct Pack {
     __device__ __forceinline__ void zero() { r = (Vec)(T)0.f; }
     __device__ __forceinline__ void load(const T *p) { r = *reinterpret_cast<const Raw *>(p); }
     __device__ __forceinline__ void store(T *p) const { *reinterpret_cast<Raw *>(p) = r; }
-    // elements past n: zero, not written
+    // elements past n (1 at least): zero (the last one is read in their place, so that
+    // all loads are on their way together), not written
     __device__ __forceinline__ void load(const T *p, int n) {
         if (n >= V) {
             load(p);
         } else {
+            T v[V - 1];
+#pragma unroll
+            for (int i = 0; i < V - 1; ++i)
+                v[i] = p[i < n ? i : n - 1];
             zero();
 #pragma unroll
             for (int i = 0; i < V - 1; ++i)
-                if (i < n)
-                    r[i] = p[i];
+                r[i] = i < n ? v[i] : r[i];
         }
     }
     __device__ __forceinline__ void store(T *p, int n) const {

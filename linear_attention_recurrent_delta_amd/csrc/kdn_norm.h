@@ -19,6 +19,7 @@ struct GatedNormParams {
     int gate_first;         // kdn_norm_order
     int act;                // kdn_activation
     float eps;
+    double inv_d;           // 1 / d
     long x_stride, z_stride;    // elements between tokens
     const void *x, *z;      // z may be null
     const float *weight;
@@ -37,6 +38,7 @@ struct ResidualNormParams {
     int D;
     int scale_n;            // 0, 1 or D
     float eps;
+    double inv_d;           // 1 / D
     long x_stride, r_stride;    // elements between tokens
     const void *x, *residual;
     const float *weight, *scale;

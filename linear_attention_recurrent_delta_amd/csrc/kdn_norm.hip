@@ -18,23 +18,65 @@ namespace norm {
 
 constexpr int NT = 256, NT_MAX = 1024;
 
-// Sum over the TPR threads of a row; every thread gets it.  Rows of several waves
-// meet in LDS, so that all threads of the workgroup have to come here.
-__device__ __forceinline__ double row_sum(double x, int tpr, double *lds) {
-    const int n = tpr < WAVE ? tpr : WAVE;
-    for (int off = n >> 1; off >= 1; off >>= 1)
-        x += __shfl_xor(x, off, WAVE);
-    if (tpr > WAVE) {
-        __syncthreads();             // the sums before have been read
-        if ((threadIdx.x & (WAVE - 1)) == 0)
-            lds[threadIdx.x / WAVE] = x;
-        __syncthreads();
-        const double *row = lds + threadIdx.x / tpr * (tpr / WAVE);
-        x = row[0];
-        for (int i = 1; i < tpr / WAVE; ++i)
-            x += row[i];
-    }
+// The value of the lane that CTRL names, in 64 bits.
+template <int CTRL> __device__ __forceinline__ double dpp64(double x) {
+    const uint64_t b = __builtin_bit_cast(uint64_t, x);
+    const unsigned lo = __builtin_amdgcn_update_dpp(0, (int)b, CTRL, 0xf, 0xf, true);
+    const unsigned hi = __builtin_amdgcn_update_dpp(0, (int)(b >> 32), CTRL, 0xf, 0xf, true);
+    return __builtin_bit_cast(double, (uint64_t)hi << 32 | lo);
+}
+// x + that of the lane 16 (or 32) away.
+template <bool FAR> __device__ __forceinline__ double swap64(double x) {
+    const uint64_t b = __builtin_bit_cast(uint64_t, x);
+    const unsigned lo = (unsigned)b, hi = (unsigned)(b >> 32);
+    const auto l = FAR ? __builtin_amdgcn_permlane32_swap(lo, lo, false, false)
+                       : __builtin_amdgcn_permlane16_swap(lo, lo, false, false);
+    const auto h = FAR ? __builtin_amdgcn_permlane32_swap(hi, hi, false, false)
+                       : __builtin_amdgcn_permlane16_swap(hi, hi, false, false);
+    return __builtin_bit_cast(double, (uint64_t)h[0] << 32 | l[0]) +
+           __builtin_bit_cast(double, (uint64_t)h[1] << 32 | l[1]);
+}
+// Sum over groups of tpr lanes (a power of two up to 64) within the registers; every
+// lane gets it.  A mirror is as good as an exchange once the lanes of each half agree.
+__device__ __forceinline__ double lane_sum(double x, int tpr) {
+    if (tpr > 1)
+        x += dpp64<0xB1>(x);             // the neighbour
+    if (tpr > 2)
+        x += dpp64<0x4E>(x);             // two away
+    if (tpr > 4)
+        x += dpp64<0x141>(x);            // the mirror of 8
+    if (tpr > 8)
+        x += dpp64<0x140>(x);            // the mirror of 16
+    if (tpr > 16)
+        x = swap64<false>(x);
+    if (tpr > 32)
+        x = swap64<true>(x);
     return x;
+}
+
+// Sums of N values over the TPR threads of a row; every thread gets them.  Rows of
+// several waves meet in LDS, so that all threads of the workgroup have to come here;
+// calls that follow each other take the two buffers in turn.
+template <int N>
+__device__ __forceinline__ void row_sums(double (&x)[N], int tpr, double (*lds)[N]) {
+#pragma unroll
+    for (int n = 0; n < N; ++n)
+        x[n] = lane_sum(x[n], tpr);
+    if (tpr <= WAVE)
+        return;
+    if ((threadIdx.x & (WAVE - 1)) == 0)
+#pragma unroll
+        for (int n = 0; n < N; ++n)
+            lds[threadIdx.x / WAVE][n] = x[n];
+    __syncthreads();
+    const int first = threadIdx.x / tpr * (tpr / WAVE);
+#pragma unroll
+    for (int n = 0; n < N; ++n)
+        x[n] = lds[first][n];
+    for (int i = 1; i < tpr / WAVE; ++i)
+#pragma unroll
+        for (int n = 0; n < N; ++n)
+            x[n] += lds[first + i][n];
 }
 
 // (m)^(-1/2) of a positive m in float32's range of roots: m is brought near 1 by
@@ -85,7 +127,7 @@ struct Lane {
 template <typename T, int VEC, int IT>
 __global__ __launch_bounds__(NT_MAX) void gated_norm_kernel(GatedNormParams P, int tpr) {
     constexpr bool FINE = sizeof(T) == 4;
-    __shared__ double lds[NT_MAX / WAVE];
+    __shared__ double lds[NT_MAX / WAVE][1];
     const Lane L(tpr);
     const long row = (long)blockIdx.x * (blockDim.x / tpr) + L.slot, rows = P.tokens * P.H;
     const bool in = row < rows;
@@ -110,7 +152,7 @@ __global__ __launch_bounds__(NT_MAX) void gated_norm_kernel(GatedNormParams P, i
         }
     }
     float u[IT][VEC];
-    double sum = 0.;
+    double sum[1] = {0.};
 #pragma unroll
     for (int i = 0; i < IT; ++i)
 #pragma unroll
@@ -118,9 +160,10 @@ __global__ __launch_bounds__(NT_MAX) void gated_norm_kernel(GatedNormParams P, i
             u[i][e] = xs[i].get(e);
             if (P.z && P.gate_first)
                 u[i][e] *= act_f32<FINE>(P.act, zs[i].get(e));
-            sum = fma((double)u[i][e], (double)u[i][e], sum);
+            sum[0] = fma((double)u[i][e], (double)u[i][e], sum[0]);
         }
-    const float r = inv_sqrt<FINE>(row_sum(sum, tpr, lds) / P.d + (double)P.eps);
+    row_sums(sum, tpr, lds);
+    const float r = inv_sqrt<FINE>(sum[0] * P.inv_d + (double)P.eps);
     T *y = static_cast<T *>(P.y) + row * P.d;
 #pragma unroll
     for (int i = 0; i < IT; ++i) {
@@ -166,7 +209,7 @@ __device__ __forceinline__ void column_sums(const float (&v)[IT][VEC], const Lan
 template <typename T, int VEC, int IT>
 __global__ __launch_bounds__(NT_MAX) void gated_norm_grad_kernel(GatedNormParams P, int tpr) {
     constexpr bool FINE = sizeof(T) == 4;
-    __shared__ double lds[NT_MAX / WAVE];
+    __shared__ double lds[2][NT_MAX / WAVE][2];
     __shared__ float cols[NT_MAX];
     const Lane L(tpr);
     const int slots = blockDim.x / tpr;
@@ -185,32 +228,49 @@ __global__ __launch_bounds__(NT_MAX) void gated_norm_grad_kernel(GatedNormParams
         for (int e = 0; e < VEC; ++e)
             dw[i][e] = 0.f;
     }
-    // the same number of rounds for every thread: they meet in row_sum
-    for (long first = (long)blockIdx.x * slots; first < rows; first += (long)P.parts * slots) {
-        const long row = first + L.slot;
+    // a row's values, requested while the row before is worked on
+    Pack<T, VEC> x1[IT], z1[IT], g1[IT];
+    auto load = [&](long row) {
         const bool in = row < rows;
         const long t = in ? row / heads : 0;
         const int h = head + (in ? (int)(row - t * heads) : 0);
         const T *x = static_cast<const T *>(P.x) + t * P.x_stride + (long)h * P.d;
         const T *z = static_cast<const T *>(P.z) + t * P.z_stride + (long)h * P.d;
-        const long out = (t * P.H + h) * P.d;
-        const T *dy = static_cast<const T *>(P.d_y) + out;
-        Pack<T, VEC> xs[IT], zs[IT], gs[IT];
+        const T *dy = static_cast<const T *>(P.d_y) + (t * P.H + h) * P.d;
 #pragma unroll
         for (int i = 0; i < IT; ++i) {
             const int at = L.at<VEC>(i);
-            xs[i].zero();
-            zs[i].zero();
-            gs[i].zero();
+            x1[i].zero();
+            z1[i].zero();
+            g1[i].zero();
             if (in && at < P.d) {
-                xs[i].load(x + at, P.d - at);
-                gs[i].load(dy + at, P.d - at);
+                x1[i].load(x + at, P.d - at);
+                g1[i].load(dy + at, P.d - at);
                 if (P.z)
-                    zs[i].load(z + at, P.d - at);
+                    z1[i].load(z + at, P.d - at);
             }
         }
+    };
+    load((long)blockIdx.x * slots + L.slot);
+    int buf = 0;
+    // the same number of rounds for every thread: they meet in row_sums
+    for (long first = (long)blockIdx.x * slots; first < rows;
+         first += (long)P.parts * slots, buf ^= 1) {
+        const long row = first + L.slot;
+        const bool in = row < rows;
+        const long t = in ? row / heads : 0;
+        const int h = head + (in ? (int)(row - t * heads) : 0);
+        const long out = (t * P.H + h) * P.d;
+        Pack<T, VEC> xs[IT], zs[IT], gs[IT];
+#pragma unroll
+        for (int i = 0; i < IT; ++i) {
+            xs[i] = x1[i];
+            zs[i] = z1[i];
+            gs[i] = g1[i];
+        }
+        load(row + (long)P.parts * slots);
         // u, the gradient of the norm's output dn, the gate and its derivative
-        double sq = 0., dot = 0.;
+        double sums[2] = {0., 0.};       // of u^2 and of t u
 #pragma unroll
         for (int i = 0; i < IT; ++i)
 #pragma unroll
@@ -223,12 +283,13 @@ __global__ __launch_bounds__(NT_MAX) void gated_norm_grad_kernel(GatedNormParams
                     else
                         dn *= a;
                 }
-                sq = fma((double)u, (double)u, sq);
-                dot = fma((double)(dn * ws[i].get(e)), (double)u, dot);
+                sums[0] = fma((double)u, (double)u, sums[0]);
+                sums[1] = fma((double)(dn * ws[i].get(e)), (double)u, sums[1]);
             }
-        const float r = inv_sqrt<FINE>(row_sum(sq, tpr, lds) / P.d + (double)P.eps);
+        row_sums(sums, tpr, lds[buf]);
+        const float r = inv_sqrt<FINE>(sums[0] * P.inv_d + (double)P.eps);
         // mean(t n)
-        const float m = (float)(row_sum(dot, tpr, lds) * (double)r / P.d);
+        const float m = (float)(sums[1] * (double)r * P.inv_d);
 #pragma unroll
         for (int i = 0; i < IT; ++i) {
             Pack<T, VEC> dx, dz;
@@ -261,7 +322,7 @@ __global__ __launch_bounds__(NT_MAX) void gated_norm_grad_kernel(GatedNormParams
 template <typename T, typename S, int VEC, int IT>
 __global__ __launch_bounds__(NT_MAX) void residual_norm_kernel(ResidualNormParams P, int tpr) {
     constexpr bool FINE = sizeof(T) == 4;
-    __shared__ double lds[NT_MAX / WAVE];
+    __shared__ double lds[NT_MAX / WAVE][1];
     const Lane L(tpr);
     const long row = (long)blockIdx.x * (blockDim.x / tpr) + L.slot;
     const bool in = row < P.tokens;
@@ -283,7 +344,7 @@ __global__ __launch_bounds__(NT_MAX) void residual_norm_kernel(ResidualNormParam
         }
     }
     float h[IT][VEC];
-    double sum = 0.;
+    double sum[1] = {0.};
 #pragma unroll
     for (int i = 0; i < IT; ++i) {
         const int at = L.at<VEC>(i);
@@ -296,13 +357,14 @@ __global__ __launch_bounds__(NT_MAX) void residual_norm_kernel(ResidualNormParam
         for (int e = 0; e < VEC; ++e) {
             const float s = P.scale_n == 0 ? 1.f : (P.scale_n == 1 ? P.scale[0] : sc.get(e));
             h[i][e] = fmaf(s, xs[i].get(e), rs[i].get(e));
-            sum = fma((double)h[i][e], (double)h[i][e], sum);
+            sum[0] = fma((double)h[i][e], (double)h[i][e], sum[0]);
             out.set(e, h[i][e]);
         }
         if (in && at < P.D)
             out.store(static_cast<S *>(P.h) + row * P.D + at, P.D - at);
     }
-    const float r = inv_sqrt<FINE>(row_sum(sum, tpr, lds) / P.D + (double)P.eps);
+    row_sums(sum, tpr, lds);
+    const float r = inv_sqrt<FINE>(sum[0] * P.inv_d + (double)P.eps);
 #pragma unroll
     for (int i = 0; i < IT; ++i) {
         const int at = L.at<VEC>(i);
@@ -318,7 +380,7 @@ __global__ __launch_bounds__(NT_MAX) void residual_norm_kernel(ResidualNormParam
 template <typename T, typename S, int VEC, int IT>
 __global__ __launch_bounds__(NT_MAX) void residual_norm_grad_kernel(ResidualNormParams P, int tpr) {
     constexpr bool FINE = sizeof(T) == 4;
-    __shared__ double lds[NT_MAX / WAVE];
+    __shared__ double lds[2][NT_MAX / WAVE][2];
     __shared__ float cols[NT_MAX];
     const Lane L(tpr);
     const int slots = blockDim.x / tpr;
@@ -339,41 +401,60 @@ __global__ __launch_bounds__(NT_MAX) void residual_norm_grad_kernel(ResidualNorm
         for (int e = 0; e < VEC; ++e)
             dw[i][e] = ds[i][e] = 0.f;
     }
-    for (long first = (long)blockIdx.x * slots; first < P.tokens; first += (long)P.parts * slots) {
-        const long row = first + L.slot;
+    // a row's values, requested while the row before is worked on
+    Pack<S, VEC> h1[IT], dh1[IT];
+    Pack<T, VEC> g1[IT], x1[IT];
+    auto load = [&](long row) {
         const bool in = row < P.tokens;
         const S *hrow = static_cast<const S *>(P.residual) + (in ? row : 0) * P.r_stride;
         const T *x = static_cast<const T *>(P.x) + (in ? row : 0) * P.x_stride;
+        const long out = (in ? row : 0) * P.D;
+#pragma unroll
+        for (int i = 0; i < IT; ++i) {
+            const int at = L.at<VEC>(i);
+            h1[i].zero();
+            dh1[i].zero();
+            g1[i].zero();
+            x1[i].zero();
+            if (in && at < P.D) {
+                h1[i].load(hrow + at, P.D - at);
+                g1[i].load(static_cast<const T *>(P.d_y) + out + at, P.D - at);
+                if (P.d_h)
+                    dh1[i].load(static_cast<const S *>(P.d_h) + out + at, P.D - at);
+                if (P.dscale)
+                    x1[i].load(x + at, P.D - at);
+            }
+        }
+    };
+    load((long)blockIdx.x * slots + L.slot);
+    int buf = 0;
+    for (long first = (long)blockIdx.x * slots; first < P.tokens;
+         first += (long)P.parts * slots, buf ^= 1) {
+        const long row = first + L.slot;
+        const bool in = row < P.tokens;
         const long out = (in ? row : 0) * P.D;
         Pack<S, VEC> hs[IT], dh[IT];
         Pack<T, VEC> gs[IT], xs[IT];
 #pragma unroll
         for (int i = 0; i < IT; ++i) {
-            const int at = L.at<VEC>(i);
-            hs[i].zero();
-            dh[i].zero();
-            gs[i].zero();
-            xs[i].zero();
-            if (in && at < P.D) {
-                hs[i].load(hrow + at, P.D - at);
-                gs[i].load(static_cast<const T *>(P.d_y) + out + at, P.D - at);
-                if (P.d_h)
-                    dh[i].load(static_cast<const S *>(P.d_h) + out + at, P.D - at);
-                if (P.dscale)
-                    xs[i].load(x + at, P.D - at);
-            }
+            hs[i] = h1[i];
+            dh[i] = dh1[i];
+            gs[i] = g1[i];
+            xs[i] = x1[i];
         }
-        double sq = 0., dot = 0.;
+        load(row + (long)P.parts * slots);
+        double sums[2] = {0., 0.};       // of u^2 and of t u
 #pragma unroll
         for (int i = 0; i < IT; ++i)
 #pragma unroll
             for (int e = 0; e < VEC; ++e) {
                 const double u = hs[i].get(e);
-                sq = fma(u, u, sq);
-                dot = fma((double)(gs[i].get(e) * ws[i].get(e)), u, dot);
+                sums[0] = fma(u, u, sums[0]);
+                sums[1] = fma((double)(gs[i].get(e) * ws[i].get(e)), u, sums[1]);
             }
-        const float r = inv_sqrt<FINE>(row_sum(sq, tpr, lds) / P.D + (double)P.eps);
-        const float m = (float)(row_sum(dot, tpr, lds) * (double)r / P.D);
+        row_sums(sums, tpr, lds[buf]);
+        const float r = inv_sqrt<FINE>(sums[0] * P.inv_d + (double)P.eps);
+        const float m = (float)(sums[1] * (double)r * P.inv_d);
 #pragma unroll
         for (int i = 0; i < IT; ++i) {
             Pack<S, VEC> dres;

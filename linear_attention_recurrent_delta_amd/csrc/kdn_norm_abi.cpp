@@ -29,7 +29,7 @@ kdn_status gated_shape(kdn::GatedNormParams &P, int dtype, int tokens, int H, in
     P = kdn::GatedNormParams{};
     P.bf16 = dtype == KDN_BF16;
     P.tokens = tokens; P.H = H; P.d = d;
-    P.per_head = per_head != 0; P.gate_first = order == KDN_GATE_NORM; P.act = act; P.eps = eps;
+    P.per_head = per_head != 0; P.gate_first = order == KDN_GATE_NORM; P.act = act; P.eps = eps; P.inv_d = 1. / d;
     if (kdn_status st = kdn::row_stride(x_stride, (long long)H * d, &P.x_stride)) return st;
     if (kdn_status st = kdn::row_stride(z_stride, (long long)H * d, &P.z_stride)) return st;
     // a row has a thread for 16 bytes at most: a workgroup a row, at the largest
@@ -56,7 +56,7 @@ kdn_status residual_shape(kdn::ResidualNormParams &P, int dtype, int stream_dtyp
         return KDN_ERR_UNSUPPORTED;
     P = kdn::ResidualNormParams{};
     P.bf16 = dtype == KDN_BF16; P.stream_bf16 = stream_dtype == KDN_BF16;
-    P.tokens = tokens; P.D = D; P.scale_n = scale_n; P.eps = eps;
+    P.tokens = tokens; P.D = D; P.scale_n = scale_n; P.eps = eps; P.inv_d = 1. / D;
     if (kdn_status st = kdn::row_stride(x_stride, D, &P.x_stride)) return st;
     if (kdn_status st = kdn::row_stride(r_stride, D, &P.r_stride)) return st;
     const int tpr = kdn::norm_row_threads(D, P.bf16);

@@ -500,6 +500,10 @@ _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
     lambda index: torch.cuda.current_stream(index).cuda_stream)
 
 
+# the current device's index; tensors in GPU memory are there, so it is initialised
+_current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
+
+
 def _call(fn, dev, stream, *args):
     """Call fn(*args, stream) with the tensors' device current.  These calls
     are short on the GPU too, so their checks take the quickest way that says
@@ -510,7 +514,7 @@ def _call(fn, dev, stream, *args):
         stream = _raw_stream(dev.index)
     elif not isinstance(stream, int):
         stream = stream.cuda_stream
-    if dev.index == torch.cuda.current_device():
+    if dev.index == _current_device():
         st = fn(*args, stream)
     else:
         with torch.cuda.device(dev):
@@ -522,7 +526,7 @@ def _call(fn, dev, stream, *args):
 def _same(name, x, shape, dtype, dev):
     """x is None or a contiguous GPU tensor of this shape, dtype and device."""
     if x is None or (isinstance(x, torch.Tensor) and x.shape == shape and x.dtype is dtype
-                     and x.is_cuda and x.device == dev and x.is_contiguous()):
+                     and x.get_device() == dev.index and x.is_contiguous()):
         return
     _expect([(name, x, shape, dtype)], dev)
 
@@ -901,14 +905,14 @@ def _strided(name, x, lead, tail, dtype, dev):
     wider ones; returns the elements between tokens (0: contiguous)."""
     if not isinstance(x, torch.Tensor):
         raise TypeError(f"kdn: {name} must be a tensor")
+    if x.shape == lead + tail and x.dtype is dtype and x.device == dev and x.is_contiguous():
+        return 0
     if x.shape != lead + tail:
         raise ValueError(f"kdn: {name} has shape {tuple(x.shape)}, expected {lead + tail}")
     if x.dtype is not dtype:
         raise ValueError(f"kdn: {name} has dtype {x.dtype}, expected {dtype}")
     if x.device != dev:
         raise ValueError(f"kdn: {name} is on {x.device}, the other tensors on {dev}")
-    if x.is_contiguous():
-        return 0
     if x.numel() == 0:
         return 0
     n, st, row = len(lead), x.stride(), 1
