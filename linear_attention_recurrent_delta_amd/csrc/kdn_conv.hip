@@ -10,6 +10,8 @@
 #include "kdn_batch_device.h"
 #include "kdn_conv.h"
 
+#include <initializer_list>
+
 namespace kdn {
 namespace conv {
 
@@ -24,6 +26,59 @@ struct Place {
 __device__ __forceinline__ Place place(int chunks) {
     return Place{(long)blockIdx.x / chunks, (int)(blockIdx.x % chunks)};
 }
+
+// Rows of VEC channels of a lane, n of them there (the same in every lane).  WHOLE: rows of
+// whole pieces on their boundaries, through a descriptor that ends with the last row, so
+// that rows behind it read 0 and are not written without a branch; else by the pieces'
+// elements.
+template <typename T, int VEC, bool WHOLE> struct Lines {
+    typedef Pack<T, VEC> V;
+    __amdgpu_buffer_rsrc_t d;
+    T *p;
+    long pitch;
+    unsigned lane, step;
+    int n, nc;
+    // base: the first row (the same in every lane); c, nc: the lane's first channel and
+    // how many of its VEC are there
+    __device__ __forceinline__ Lines(const void *base, long pitch_, int C, long n_, long c, int nc_) {
+        n = (int)(n_ < 0 ? 0 : (n_ > 64 ? 64 : n_));
+        nc = nc_;
+        pitch = pitch_;
+        p = static_cast<T *>(const_cast<void *>(base)) + c;
+        if constexpr (WHOLE) {
+            step = (unsigned)pitch * sizeof(T);
+            lane = (unsigned)c * sizeof(T);
+            d = buf_rsrc(base, n > 0 ? (n - 1) * step + (unsigned)C * sizeof(T) : 0u);
+        }
+    }
+    __device__ __forceinline__ void load(V &v, int i) const {
+        if constexpr (WHOLE) {
+            const int at = (int)(lane + (unsigned)i * step);
+            if constexpr (VEC * sizeof(T) == 16)
+                v.r = __builtin_bit_cast(typename V::Vec, __builtin_amdgcn_raw_buffer_load_b128(d, at, 0, 0));
+            else
+                v.r = __builtin_bit_cast(typename V::Vec, __builtin_amdgcn_raw_buffer_load_b64(d, at, 0, 0));
+        } else {
+            v.zero();
+            if (i < n)
+                v.load(p + (long)i * pitch, nc);
+        }
+    }
+    __device__ __forceinline__ void store(const V &v, int i) const {
+        if constexpr (WHOLE) {
+            const int at = (int)(lane + (unsigned)i * step);
+            if constexpr (VEC * sizeof(T) == 16)
+                __builtin_amdgcn_raw_buffer_store_b128(
+                    __builtin_bit_cast(__attribute__((ext_vector_type(4))) unsigned, v.r), d, at, 0, 0);
+            else
+                __builtin_amdgcn_raw_buffer_store_b64(
+                    __builtin_bit_cast(__attribute__((ext_vector_type(2))) unsigned, v.r), d, at, 0, 0);
+        } else {
+            if (i < n)
+                v.store(p + (long)i * pitch, nc);
+        }
+    }
+};
 
 // Weights of VEC channels, tap j of channel e in w[j][e], and the bias.
 template <int VEC, int W>
@@ -46,7 +101,7 @@ __device__ __forceinline__ void load_weights(const float *weight, const float *b
     }
 }
 
-template <typename T, int VEC, int W, int RT>
+template <typename T, int VEC, int W, int RT, bool WHOLE>
 __global__ __launch_bounds__(NT) void conv_kernel(ConvParams P, int chunks, int sub, long tiles) {
     constexpr bool FINE = sizeof(T) == 4;
     constexpr int H = W - 1, TT = NW * RT;
@@ -73,24 +128,22 @@ __global__ __launch_bounds__(NT) void conv_kernel(ConvParams P, int chunks, int 
     if (t0 >= B.count || B.slot < 0 || c >= P.C)
         return;
     const bool start = B.index == 0 && t0 == 0;
+    typedef Lines<T, VEC, WHOLE> L;
     const T *x = static_cast<const T *>(P.x) + B.first * P.x_stride + c;
-    V rows[RT + H], old[H];
+    const T *x0 = static_cast<const T *>(P.x) + (B.first + t0) * P.x_stride;
+    // the tokens' rows and the H before them (of a sequence's start: the state's)
+    const L here(x0, P.x_stride, P.C, B.count - t0, c, nc);
+    const L before(start ? state0 + B.slot * H * P.C : x0 - H * P.x_stride, start ? P.C : P.x_stride, P.C,
+                   start ? (state0 ? H : 0) : (B.first + t0 >= H ? H : 0), c, nc);
+    V rows[RT + H];
 #pragma unroll
-    for (int i = 0; i < RT + H; ++i) {
-        rows[i].zero();
-        const int t = t0 - H + i;
-        if (t < B.count && (i >= H || !start) && (i >= H || B.first + t >= 0))
-            rows[i].load(x + (long)t * P.x_stride, nc);
-    }
+    for (int i = 0; i < RT; ++i)
+        here.load(rows[H + i], i);
+#pragma unroll
+    for (int i = 0; i < H; ++i)
+        before.load(rows[i], i);
     if (start) {
         const long at0 = B.slot * H * P.C + c;
-#pragma unroll
-        for (int i = 0; i < H; ++i) {
-            old[i].zero();
-            if (state0)
-                old[i].load(state0 + at0 + (long)i * P.C, nc);
-            rows[i] = old[i];
-        }
         if (state_out) {
             // the last W - 1 of the sequence's rows with its state before them; the
             // state has been read, and no other thread reads or writes it
@@ -104,14 +157,14 @@ __global__ __launch_bounds__(NT) void conv_kernel(ConvParams P, int chunks, int 
 #pragma unroll
                 for (int j = 1; j < H; ++j)
                     if (n + i == j)
-                        last = old[j];
+                        last = rows[j];
                 last.store(state_out + at0 + (long)i * P.C, nc);
             }
         }
     }
     float w[W][VEC], b[VEC];
     load_weights<VEC, W>(P.weight, P.bias, c, nc, w, b);
-    T *y = static_cast<T *>(P.y) + (B.first + t0) * P.C + c;
+    const L y(static_cast<T *>(P.y) + (B.first + t0) * P.C, P.C, P.C, B.count - t0, c, nc);
 #pragma unroll
     for (int i = 0; i < RT; ++i) {
         V out;
@@ -123,8 +176,7 @@ __global__ __launch_bounds__(NT) void conv_kernel(ConvParams P, int chunks, int 
                 s = fmaf(w[j][e], rows[i + j].get(e), s);
             out.set(e, P.silu ? silu_f32<FINE>(s) : s);
         }
-        if (t0 + i < B.count)
-            out.store(y + (long)i * P.C, nc);
+        y.store(out, i);
     }
 }
 
@@ -174,7 +226,7 @@ __global__ __launch_bounds__(WAVE) void conv_decode_kernel(ConvDecodeParams P, i
 // `parts`-th) in registers and writes them once; a second kernel adds the parts
 // in order, in 64 bits.
 // ---------------------------------------------------------------------------
-template <typename T, int VEC, int W>
+template <typename T, int VEC, int W, bool WHOLE>
 __global__ __launch_bounds__(NT) void conv_grad_kernel(ConvParams P, int chunks, int sub,
                                                        long tiles) {
     constexpr bool FINE = sizeof(T) == 4;
@@ -198,39 +250,36 @@ __global__ __launch_bounds__(NT) void conv_grad_kernel(ConvParams P, int chunks,
         const int t0 = (int)(tile % sub) * CONV_GRAD_TILE + wv * RT;
         if (t0 >= B.count)
             continue;
-        T *dx = static_cast<T *>(P.dx) + (B.first + t0) * P.C + c;
+        typedef Lines<T, VEC, WHOLE> L;
         const int n = min(RT, B.count - t0);      // own tokens
+        const L dx(static_cast<T *>(P.dx) + (B.first + t0) * P.C, P.C, P.C, n, c, nc);
         if (B.slot < 0) {
             V none;
             none.zero();
             for (int i = 0; i < n; ++i)
-                none.store(dx + (long)i * P.C, nc);
+                dx.store(none, i);
             continue;
         }
         const long left = tokens_left(P, B) - t0;     // tokens to the sequence's end
         const bool start = B.index == 0 && t0 == 0;
-        const T *x = static_cast<const T *>(P.x) + (B.first + t0) * P.x_stride + c;
-        const T *dy = static_cast<const T *>(P.d_y) + (B.first + t0) * P.C + c;
         const T *state0 = static_cast<const T *>(P.state0);
         const T *dlast = static_cast<const T *>(P.dstate_out);
         const long at0 = B.slot * H * P.C + c;
-        // rows t0 - H .. t0 + RT + H - 1 of x and t0 .. of dy
+        // rows t0 - H .. t0 + RT + H - 1 of x and t0 .. of dy, those of the sequence
+        const T *x0 = static_cast<const T *>(P.x) + (B.first + t0) * P.x_stride;
+        const L here(x0, P.x_stride, P.C, left, c, nc);
+        const L before(start ? state0 + B.slot * H * P.C : x0 - H * P.x_stride,
+                       start ? P.C : P.x_stride, P.C,
+                       start ? (state0 ? H : 0) : (B.first + t0 >= H ? H : 0), c, nc);
+        const L dy(static_cast<const T *>(P.d_y) + (B.first + t0) * P.C, P.C, P.C, left, c, nc);
         V xs[RT + 2 * H], g[RT + H];
 #pragma unroll
-        for (int i = 0; i < RT + 2 * H; ++i) {
-            xs[i].zero();
-            if (i < H && start) {
-                if (state0)
-                    xs[i].load(state0 + at0 + (long)i * P.C, nc);
-            } else if (i - H < left && B.first + t0 - H + i >= 0) {
-                xs[i].load(x + (long)(i - H) * P.x_stride, nc);
-            }
-        }
+        for (int i = 0; i < H; ++i)
+            before.load(xs[i], i);
 #pragma unroll
         for (int i = 0; i < RT + H; ++i) {
-            g[i].zero();
-            if (i < left)
-                g[i].load(dy + (long)i * P.C, nc);
+            here.load(xs[H + i], i);
+            dy.load(g[i], i);
         }
         // near[k] = ds of token i - H + 1 + k
         float near[W][VEC];
@@ -288,7 +337,7 @@ __global__ __launch_bounds__(NT) void conv_grad_kernel(ConvParams P, int chunks,
                     }
                 }
                 if (t >= 0)
-                    out.store(dx + (long)t * P.C, nc);
+                    dx.store(out, t);
                 else
                     out.store(static_cast<T *>(P.dstate0) + at0 + (long)i * P.C, nc);
             }
@@ -360,6 +409,14 @@ __global__ __launch_bounds__(NT) void conv_sum_kernel(ConvParams P, long wide) {
                                                              : from_f32<T>(0.f);
 }
 
+// Rows of whole pieces of `bytes` bytes on such boundaries, near enough for 32 bits.
+bool whole(int C, long stride, int es, int bytes, std::initializer_list<const void *> p) {
+    bool ok = C * (long)es % bytes == 0 && stride * es % bytes == 0 && stride < (1l << 24);
+    for (const void *x : p)
+        ok = ok && (reinterpret_cast<uintptr_t>(x) & (bytes - 1)) == 0;
+    return ok;
+}
+
 template <typename T, int VEC, int W>
 hipError_t launch_conv_fwd_t(const ConvParams &P, hipStream_t st) {
     constexpr int RT = 16, TT = NW * RT;
@@ -373,8 +430,11 @@ hipError_t launch_conv_fwd_t(const ConvParams &P, hipStream_t st) {
     const long empty = P.state_out && P.state_out != P.state0 && (P.block_offsets || P.T == 0) ? P.N : 0;
     if (tiles + empty == 0)
         return hipSuccess;
-    hipLaunchKernelGGL((conv_kernel<T, VEC, W, RT>), dim3((unsigned)((tiles + empty) * chunks)),
-                       dim3(NT), 0, st, Q, chunks, sub, tiles);
+    const dim3 grid((unsigned)((tiles + empty) * chunks)), block(NT);
+    if (whole(P.C, P.x_stride, sizeof(T), VEC * sizeof(T), {P.x, P.y, P.state0, P.state_out}))
+        hipLaunchKernelGGL((conv_kernel<T, VEC, W, RT, true>), grid, block, 0, st, Q, chunks, sub, tiles);
+    else
+        hipLaunchKernelGGL((conv_kernel<T, VEC, W, RT, false>), grid, block, 0, st, Q, chunks, sub, tiles);
     return hipGetLastError();
 }
 
@@ -397,8 +457,11 @@ hipError_t launch_conv_grad_t(const ConvParams &P, hipStream_t st) {
     }
     const long tiles = conv_tiles(Q, TT);
     if (P.parts > 0) {
-        hipLaunchKernelGGL((conv_grad_kernel<T, VEC, W>), dim3((unsigned)(chunks * (long)P.parts)),
-                           dim3(NT), 0, st, Q, chunks, sub, tiles);
+        const dim3 grid((unsigned)(chunks * (long)P.parts)), block(NT);
+        if (whole(P.C, P.x_stride, sizeof(T), VEC * sizeof(T), {P.x, P.d_y, P.dx, P.state0}))
+            hipLaunchKernelGGL((conv_grad_kernel<T, VEC, W, true>), grid, block, 0, st, Q, chunks, sub, tiles);
+        else
+            hipLaunchKernelGGL((conv_grad_kernel<T, VEC, W, false>), grid, block, 0, st, Q, chunks, sub, tiles);
         const hipError_t e = hipGetLastError();
         if (e != hipSuccess)
             return e;
