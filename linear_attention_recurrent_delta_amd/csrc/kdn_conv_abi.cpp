@@ -43,8 +43,8 @@ kdn_status conv_shape(kdn::ConvParams &P, int dtype, int N, int T, int C, int W,
 }
 
 // Parts that the sums over tokens are made in: as many workgroups as run at once
-// (three a CU), each over all the tiles it takes.
-constexpr int GRAD_WGS = 768;
+// (two a CU, by their registers), each over all the tiles it takes.
+constexpr int GRAD_WGS = 512;
 int grad_parts(const kdn::ConvParams &P, bool packed) {
     const long long tiles = packed ? (long long)P.nblocks * ((P.block + 63LL) / 64)
                                    : (long long)P.N * ((P.T + 63LL) / 64);

@@ -83,7 +83,7 @@ def test_conv_workspace_size(lib):
     size = lambda *a: (lib.kdn_causal_conv_backward_workspace_size(*a, None, ctypes.byref(st)), st.value)
     assert size(BF16, 2, 100, 64, 4) == (4 * 4 * 5 * 64, OK)         # a part for each of 2 x 2 tiles
     assert size(BF16, 2, 0, 64, 4) == (0, OK)
-    assert size(BF16, 4, 4096, 2048, 4) == (4 * (768 // 8) * 5 * 2048, OK)
+    assert size(BF16, 4, 4096, 2048, 4) == (4 * (512 // 8) * 5 * 2048, OK)
     assert size(BF16, 4, 4096, 2048, 9)[1] == EUNSUP and size(BF16, -4, 4096, 2048, 4)[1] == ESHAPE
 
 
