@@ -124,15 +124,41 @@ struct Lane {
     }
 };
 
-template <typename T, int VEC, int IT>
+// A piece of a row, n elements of it there.  FULL: rows are whole pieces.
+template <bool FULL, typename Piece, typename T>
+__device__ __forceinline__ void get_piece(Piece &v, const T *p, int n) {
+    if constexpr (FULL)
+        v.load(p);
+    else
+        v.load(p, n);
+}
+template <bool FULL, typename Piece, typename T>
+__device__ __forceinline__ void put_piece(const Piece &v, T *p, int n) {
+    if constexpr (FULL)
+        v.store(p);
+    else
+        v.store(p, n);
+}
+
+// What a gated norm's kernel knows of its gate: silu in either order, or nothing.
+enum Kind { NORM_SILU, SILU_NORM, ANY };
+template <Kind KIND> struct Gate {
+    bool there, first;
+    int act;
+    __device__ __forceinline__ Gate(const GatedNormParams &P)
+        : there(KIND != ANY || P.z), first(KIND == ANY ? P.z && P.gate_first : KIND == SILU_NORM),
+          act(KIND == ANY ? P.act : (int)KDN_ACT_SILU) {}
+};
+
+template <typename T, int VEC, int IT, bool FULL, Kind KIND>
 __global__ __launch_bounds__(NT_MAX) void gated_norm_kernel(GatedNormParams P, int tpr) {
     constexpr bool FINE = sizeof(T) == 4;
     __shared__ double lds[NT_MAX / WAVE][1];
     const Lane L(tpr);
+    const Gate<KIND> gate(P);
     const long row = (long)blockIdx.x * (blockDim.x / tpr) + L.slot, rows = P.tokens * P.H;
     const bool in = row < rows;
-    const long t = in ? row / P.H : 0;
-    const int h = in ? (int)(row - t * P.H) : 0;
+    const unsigned at_row = in ? (unsigned)row : 0u, t = at_row / (unsigned)P.H, h = at_row - t * P.H;
     const T *x = static_cast<const T *>(P.x) + t * P.x_stride + (long)h * P.d;
     const T *z = static_cast<const T *>(P.z) + t * P.z_stride + (long)h * P.d;
     const float *w = P.weight + (P.per_head ? (long)h * P.d : 0);
@@ -145,10 +171,10 @@ __global__ __launch_bounds__(NT_MAX) void gated_norm_kernel(GatedNormParams P, i
         zs[i].zero();
         ws[i].zero();
         if (in && at < P.d) {
-            xs[i].load(x + at, P.d - at);
-            if (P.z)
-                zs[i].load(z + at, P.d - at);
-            ws[i].load(w + at, P.d - at);
+            get_piece<FULL>(xs[i], x + at, P.d - at);
+            if (gate.there)
+                get_piece<FULL>(zs[i], z + at, P.d - at);
+            get_piece<FULL>(ws[i], w + at, P.d - at);
         }
     }
     float u[IT][VEC];
@@ -158,8 +184,8 @@ __global__ __launch_bounds__(NT_MAX) void gated_norm_kernel(GatedNormParams P, i
 #pragma unroll
         for (int e = 0; e < VEC; ++e) {
             u[i][e] = xs[i].get(e);
-            if (P.z && P.gate_first)
-                u[i][e] *= act_f32<FINE>(P.act, zs[i].get(e));
+            if (gate.first)
+                u[i][e] *= act_f32<FINE>(gate.act, zs[i].get(e));
             sum[0] = fma((double)u[i][e], (double)u[i][e], sum[0]);
         }
     row_sums(sum, tpr, lds);
@@ -171,13 +197,13 @@ __global__ __launch_bounds__(NT_MAX) void gated_norm_kernel(GatedNormParams P, i
 #pragma unroll
         for (int e = 0; e < VEC; ++e) {
             float v = u[i][e] * r * ws[i].get(e);
-            if (P.z && !P.gate_first)
-                v *= act_f32<FINE>(P.act, zs[i].get(e));
+            if (gate.there && !gate.first)
+                v *= act_f32<FINE>(gate.act, zs[i].get(e));
             out.set(e, v);
         }
         const int at = L.at<VEC>(i);
         if (in && at < P.d)
-            out.store(y + at, P.d - at);
+            put_piece<FULL>(out, y + at, P.d - at);
     }
 }
 
@@ -206,82 +232,66 @@ __device__ __forceinline__ void column_sums(const float (&v)[IT][VEC], const Lan
         }
 }
 
-template <typename T, int VEC, int IT>
+template <typename T, int VEC, int IT, bool FULL, Kind KIND>
 __global__ __launch_bounds__(NT_MAX) void gated_norm_grad_kernel(GatedNormParams P, int tpr) {
     constexpr bool FINE = sizeof(T) == 4;
     __shared__ double lds[2][NT_MAX / WAVE][2];
     __shared__ float cols[NT_MAX];
     const Lane L(tpr);
+    const Gate<KIND> gate(P);
     const int slots = blockDim.x / tpr;
     // weight by head: a workgroup has one head's rows; else rows of all heads
-    const int head = P.per_head ? blockIdx.y : 0, heads = P.per_head ? 1 : P.H;
-    const long rows = P.tokens * heads;
+    const unsigned head = P.per_head ? blockIdx.y : 0, heads = P.per_head ? 1 : P.H;
+    const unsigned rows = (unsigned)(P.tokens * heads), step = (unsigned)P.parts * slots;
     const float *w = P.weight + (long)head * P.d;
     Pack<float, VEC> ws[IT];
     float dw[IT][VEC];
 #pragma unroll
     for (int i = 0; i < IT; ++i) {
+        const int at = L.at<VEC>(i);
         ws[i].zero();
-        if (L.at<VEC>(i) < P.d)
-            ws[i].load(w + L.at<VEC>(i), P.d - L.at<VEC>(i));
+        if (at < P.d)
+            get_piece<FULL>(ws[i], w + at, P.d - at);
 #pragma unroll
         for (int e = 0; e < VEC; ++e)
             dw[i][e] = 0.f;
     }
-    // a row's values, requested while the row before is worked on
-    Pack<T, VEC> x1[IT], z1[IT], g1[IT];
-    auto load = [&](long row) {
-        const bool in = row < rows;
-        const long t = in ? row / heads : 0;
-        const int h = head + (in ? (int)(row - t * heads) : 0);
-        const T *x = static_cast<const T *>(P.x) + t * P.x_stride + (long)h * P.d;
-        const T *z = static_cast<const T *>(P.z) + t * P.z_stride + (long)h * P.d;
-        const T *dy = static_cast<const T *>(P.d_y) + (t * P.H + h) * P.d;
-#pragma unroll
-        for (int i = 0; i < IT; ++i) {
-            const int at = L.at<VEC>(i);
-            x1[i].zero();
-            z1[i].zero();
-            g1[i].zero();
-            if (in && at < P.d) {
-                x1[i].load(x + at, P.d - at);
-                g1[i].load(dy + at, P.d - at);
-                if (P.z)
-                    z1[i].load(z + at, P.d - at);
-            }
-        }
-    };
-    load((long)blockIdx.x * slots + L.slot);
+    // the row's token and head, and the steps of both (a division once a row would cost a
+    // tenth of the row's work)
+    unsigned row = blockIdx.x * slots + L.slot, t = row / heads, h = row - t * heads;
+    const unsigned dt = step / heads, dh = step - dt * heads;
     int buf = 0;
     // the same number of rounds for every thread: they meet in row_sums
-    for (long first = (long)blockIdx.x * slots; first < rows;
-         first += (long)P.parts * slots, buf ^= 1) {
-        const long row = first + L.slot;
+    for (long first = (long)blockIdx.x * slots; first < rows; first += step, buf ^= 1) {
         const bool in = row < rows;
-        const long t = in ? row / heads : 0;
-        const int h = head + (in ? (int)(row - t * heads) : 0);
-        const long out = (t * P.H + h) * P.d;
+        const T *x = static_cast<const T *>(P.x) + t * P.x_stride + (long)(head + h) * P.d;
+        const T *z = static_cast<const T *>(P.z) + t * P.z_stride + (long)(head + h) * P.d;
+        const long out = ((long)t * P.H + head + h) * P.d;
+        const T *dy = static_cast<const T *>(P.d_y) + out;
         Pack<T, VEC> xs[IT], zs[IT], gs[IT];
 #pragma unroll
         for (int i = 0; i < IT; ++i) {
-            xs[i] = x1[i];
-            zs[i] = z1[i];
-            gs[i] = g1[i];
+            const int at = L.at<VEC>(i);
+            xs[i].zero();
+            zs[i].zero();
+            gs[i].zero();
+            if (in && at < P.d) {
+                get_piece<FULL>(xs[i], x + at, P.d - at);
+                get_piece<FULL>(gs[i], dy + at, P.d - at);
+                if (gate.there)
+                    get_piece<FULL>(zs[i], z + at, P.d - at);
+            }
         }
-        load(row + (long)P.parts * slots);
-        // u, the gradient of the norm's output dn, the gate and its derivative
         double sums[2] = {0., 0.};       // of u^2 and of t u
 #pragma unroll
         for (int i = 0; i < IT; ++i)
 #pragma unroll
             for (int e = 0; e < VEC; ++e) {
                 float u = xs[i].get(e), dn = gs[i].get(e);
-                if (P.z) {
-                    const float a = act_f32<FINE>(P.act, zs[i].get(e));
-                    if (P.gate_first)
-                        u *= a;
-                    else
-                        dn *= a;
+                if (gate.there) {
+                    const float a = act_f32<FINE>(gate.act, zs[i].get(e));
+                    u = gate.first ? u * a : u;
+                    dn = gate.first ? dn : dn * a;
                 }
                 sums[0] = fma((double)u, (double)u, sums[0]);
                 sums[1] = fma((double)(dn * ws[i].get(e)), (double)u, sums[1]);
@@ -298,28 +308,35 @@ __global__ __launch_bounds__(NT_MAX) void gated_norm_grad_kernel(GatedNormParams
             for (int e = 0; e < VEC; ++e) {
                 const float xe = xs[i].get(e), ge = gs[i].get(e), we = ws[i].get(e);
                 float a = 1.f, da = 0.f;
-                if (P.z)
-                    act_grad<FINE>(P.act, zs[i].get(e), a, da);
-                const float n = (P.z && P.gate_first ? xe * a : xe) * r;
-                const float dn = P.z && !P.gate_first ? ge * a : ge;
+                if (gate.there)
+                    act_grad<FINE>(gate.act, zs[i].get(e), a, da);
+                const float n = (gate.first ? xe * a : xe) * r;
+                const float dn = gate.first ? ge : ge * a;
                 const float du = r * (dn * we - n * m);
-                if (in && at < P.d)
-                    dw[i][e] = fmaf(dn, n, dw[i][e]);
-                dx.set(e, P.z && P.gate_first ? du * a : du);
-                dz.set(e, P.gate_first ? du * xe * da : ge * n * we * da);
+                // (what lies behind the rows and the row is zero)
+                dw[i][e] = fmaf(dn, n, dw[i][e]);
+                dx.set(e, gate.first ? du * a : du);
+                dz.set(e, gate.first ? du * xe * da : ge * n * we * da);
             }
             if (in && at < P.d) {
-                dx.store(static_cast<T *>(P.dx) + out + at, P.d - at);
-                if (P.z)
-                    dz.store(static_cast<T *>(P.dz) + out + at, P.d - at);
+                put_piece<FULL>(dx, static_cast<T *>(P.dx) + out + at, P.d - at);
+                if (gate.there)
+                    put_piece<FULL>(dz, static_cast<T *>(P.dz) + out + at, P.d - at);
             }
+        }
+        row += step;
+        t += dt;
+        h += dh;
+        if (h >= heads) {
+            h -= heads;
+            ++t;
         }
     }
     column_sums<VEC, IT>(dw, L, P.d, cols,
                          P.ws + ((long)blockIdx.x * gridDim.y + head) * P.d);
 }
 
-template <typename T, typename S, int VEC, int IT>
+template <typename T, typename S, int VEC, int IT, bool FULL>
 __global__ __launch_bounds__(NT_MAX) void residual_norm_kernel(ResidualNormParams P, int tpr) {
     constexpr bool FINE = sizeof(T) == 4;
     __shared__ double lds[NT_MAX / WAVE][1];
@@ -338,9 +355,9 @@ __global__ __launch_bounds__(NT_MAX) void residual_norm_kernel(ResidualNormParam
         rs[i].zero();
         ws[i].zero();
         if (in && at < P.D) {
-            xs[i].load(x + at, P.D - at);
-            rs[i].load(res + at, P.D - at);
-            ws[i].load(P.weight + at, P.D - at);
+            get_piece<FULL>(xs[i], x + at, P.D - at);
+            get_piece<FULL>(rs[i], res + at, P.D - at);
+            get_piece<FULL>(ws[i], P.weight + at, P.D - at);
         }
     }
     float h[IT][VEC];
@@ -351,7 +368,7 @@ __global__ __launch_bounds__(NT_MAX) void residual_norm_kernel(ResidualNormParam
         Pack<float, VEC> sc;
         sc.zero();
         if (P.scale_n > 1 && at < P.D)
-            sc.load(P.scale + at, P.D - at);
+            get_piece<FULL>(sc, P.scale + at, P.D - at);
         Pack<S, VEC> out;
 #pragma unroll
         for (int e = 0; e < VEC; ++e) {
@@ -361,7 +378,7 @@ __global__ __launch_bounds__(NT_MAX) void residual_norm_kernel(ResidualNormParam
             out.set(e, h[i][e]);
         }
         if (in && at < P.D)
-            out.store(static_cast<S *>(P.h) + row * P.D + at, P.D - at);
+            put_piece<FULL>(out, static_cast<S *>(P.h) + row * P.D + at, P.D - at);
     }
     row_sums(sum, tpr, lds);
     const float r = inv_sqrt<FINE>(sum[0] * P.inv_d + (double)P.eps);
@@ -373,11 +390,11 @@ __global__ __launch_bounds__(NT_MAX) void residual_norm_kernel(ResidualNormParam
         for (int e = 0; e < VEC; ++e)
             out.set(e, h[i][e] * r * ws[i].get(e));
         if (in && at < P.D)
-            out.store(static_cast<T *>(P.y) + row * P.D + at, P.D - at);
+            put_piece<FULL>(out, static_cast<T *>(P.y) + row * P.D + at, P.D - at);
     }
 }
 
-template <typename T, typename S, int VEC, int IT>
+template <typename T, typename S, int VEC, int IT, bool FULL>
 __global__ __launch_bounds__(NT_MAX) void residual_norm_grad_kernel(ResidualNormParams P, int tpr) {
     constexpr bool FINE = sizeof(T) == 4;
     __shared__ double lds[2][NT_MAX / WAVE][2];
@@ -393,9 +410,9 @@ __global__ __launch_bounds__(NT_MAX) void residual_norm_grad_kernel(ResidualNorm
         ws[i].zero();
         sc[i].zero();
         if (at < P.D) {
-            ws[i].load(P.weight + at, P.D - at);
+            get_piece<FULL>(ws[i], P.weight + at, P.D - at);
             if (P.scale_n > 1)
-                sc[i].load(P.scale + at, P.D - at);
+                get_piece<FULL>(sc[i], P.scale + at, P.D - at);
         }
 #pragma unroll
         for (int e = 0; e < VEC; ++e)
@@ -417,12 +434,12 @@ __global__ __launch_bounds__(NT_MAX) void residual_norm_grad_kernel(ResidualNorm
             g1[i].zero();
             x1[i].zero();
             if (in && at < P.D) {
-                h1[i].load(hrow + at, P.D - at);
-                g1[i].load(static_cast<const T *>(P.d_y) + out + at, P.D - at);
+                get_piece<FULL>(h1[i], hrow + at, P.D - at);
+                get_piece<FULL>(g1[i], static_cast<const T *>(P.d_y) + out + at, P.D - at);
                 if (P.d_h)
-                    dh1[i].load(static_cast<const S *>(P.d_h) + out + at, P.D - at);
+                    get_piece<FULL>(dh1[i], static_cast<const S *>(P.d_h) + out + at, P.D - at);
                 if (P.dscale)
-                    x1[i].load(x + at, P.D - at);
+                    get_piece<FULL>(x1[i], x + at, P.D - at);
             }
         }
     };
@@ -464,17 +481,15 @@ __global__ __launch_bounds__(NT_MAX) void residual_norm_grad_kernel(ResidualNorm
             for (int e = 0; e < VEC; ++e) {
                 const float g = gs[i].get(e), n = hs[i].get(e) * r;
                 const float d = fmaf(r, g * ws[i].get(e) - n * m, dh[i].get(e));
-                if (in && at < P.D) {
-                    dw[i][e] = fmaf(g, n, dw[i][e]);
-                    ds[i][e] = fmaf(d, xs[i].get(e), ds[i][e]);
-                }
+                dw[i][e] = fmaf(g, n, dw[i][e]);
+                ds[i][e] = fmaf(d, xs[i].get(e), ds[i][e]);
                 dres.set(e, d);
                 dx.set(e, d * (P.scale_n > 1 ? sc[i].get(e) : one));
             }
             if (in && at < P.D) {
-                dres.store(static_cast<S *>(P.dresidual) + out + at, P.D - at);
+                put_piece<FULL>(dres, static_cast<S *>(P.dresidual) + out + at, P.D - at);
                 if (P.dx)
-                    dx.store(static_cast<T *>(P.dx) + out + at, P.D - at);
+                    put_piece<FULL>(dx, static_cast<T *>(P.dx) + out + at, P.D - at);
             }
         }
     }
@@ -547,20 +562,17 @@ hipError_t sum_parts(const Sums &S, hipStream_t st) {
             FN(4)                                                                      \
     }
 
-template <typename T>
-static hipError_t gated_norm_t(const GatedNormParams &P, hipStream_t st, bool back) {
+template <typename T, bool FULL, norm::Kind KIND>
+static hipError_t gated_norm_k(const GatedNormParams &P, hipStream_t st, bool back) {
     constexpr int V = 16 / sizeof(T);
 #define KDN_GATED(IT_)                                                                      \
     {                                                                                           \
         const long slots = threads / tpr, rows = P.tokens * P.H;                                \
-        if (!back)                                                                              \
-            hipLaunchKernelGGL((norm::gated_norm_kernel<T, V, IT_>),                           \
-                               dim3((unsigned)((rows + slots - 1) / slots)), dim3(threads), 0,  \
-                               st, P, tpr);                                                     \
-        else                                                                                    \
-            hipLaunchKernelGGL((norm::gated_norm_grad_kernel<T, V, IT_>),                      \
-                               dim3((unsigned)P.parts, P.per_head ? P.H : 1), dim3(threads), 0, \
-                               st, P, tpr);                                                     \
+        const dim3 grid = back ? dim3((unsigned)P.parts, P.per_head ? P.H : 1)                  \
+                               : dim3((unsigned)((rows + slots - 1) / slots));                  \
+        auto kernel = back ? norm::gated_norm_grad_kernel<T, V, IT_, FULL, KIND>                \
+                           : norm::gated_norm_kernel<T, V, IT_, FULL, KIND>;                    \
+        hipLaunchKernelGGL(kernel, grid, dim3(threads), 0, st, P, tpr);                         \
         return hipGetLastError();                                                               \
     }
     KDN_NORM_IT(KDN_GATED, P.d)
@@ -568,19 +580,16 @@ static hipError_t gated_norm_t(const GatedNormParams &P, hipStream_t st, bool ba
     return hipErrorInvalidValue;
 }
 
-template <typename T, typename S>
-static hipError_t residual_norm_t(const ResidualNormParams &P, hipStream_t st, bool back) {
+template <typename T, typename S, bool FULL>
+static hipError_t residual_norm_k(const ResidualNormParams &P, hipStream_t st, bool back) {
     constexpr int V = 16 / sizeof(T);
 #define KDN_RESIDUAL(IT_)                                                                   \
     {                                                                                           \
         const long slots = threads / tpr;                                                       \
-        if (!back)                                                                              \
-            hipLaunchKernelGGL((norm::residual_norm_kernel<T, S, V, IT_>),                     \
-                               dim3((unsigned)((P.tokens + slots - 1) / slots)), dim3(threads), \
-                               0, st, P, tpr);                                                  \
-        else                                                                                    \
-            hipLaunchKernelGGL((norm::residual_norm_grad_kernel<T, S, V, IT_>),                \
-                               dim3((unsigned)P.parts), dim3(threads), 0, st, P, tpr);          \
+        const dim3 grid((unsigned)(back ? P.parts : (P.tokens + slots - 1) / slots));           \
+        auto kernel = back ? norm::residual_norm_grad_kernel<T, S, V, IT_, FULL>                \
+                           : norm::residual_norm_kernel<T, S, V, IT_, FULL>;                    \
+        hipLaunchKernelGGL(kernel, grid, dim3(threads), 0, st, P, tpr);                         \
         return hipGetLastError();                                                               \
     }
     KDN_NORM_IT(KDN_RESIDUAL, P.D)
@@ -588,6 +597,24 @@ static hipError_t residual_norm_t(const ResidualNormParams &P, hipStream_t st, b
     return hipErrorInvalidValue;
 }
 #undef KDN_NORM_IT
+
+template <typename T, bool FULL>
+static hipError_t gated_norm_f(const GatedNormParams &P, hipStream_t st, bool back) {
+    if (!P.z || P.act != KDN_ACT_SILU)
+        return gated_norm_k<T, FULL, norm::ANY>(P, st, back);
+    return P.gate_first ? gated_norm_k<T, FULL, norm::SILU_NORM>(P, st, back)
+                        : gated_norm_k<T, FULL, norm::NORM_SILU>(P, st, back);
+}
+template <typename T>
+static hipError_t gated_norm_t(const GatedNormParams &P, hipStream_t st, bool back) {
+    return P.d % (16 / sizeof(T)) == 0 ? gated_norm_f<T, true>(P, st, back)
+                                       : gated_norm_f<T, false>(P, st, back);
+}
+template <typename T, typename S>
+static hipError_t residual_norm_t(const ResidualNormParams &P, hipStream_t st, bool back) {
+    return P.D % (16 / sizeof(T)) == 0 ? residual_norm_k<T, S, true>(P, st, back)
+                                       : residual_norm_k<T, S, false>(P, st, back);
+}
 
 hipError_t launch_gated_norm(const GatedNormParams &P, hipStream_t st) {
     if (P.tokens * P.H * P.d == 0)
