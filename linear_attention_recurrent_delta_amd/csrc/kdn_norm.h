@@ -51,8 +51,9 @@ struct ResidualNormParams {
     int parts;
 };
 
-// Parts that the sums over tokens are made in: workgroups that run at once.
-constexpr int NORM_PARTS = 1024;
+// Parts that the sums over tokens are made in: workgroups that run at once (of 256 and
+// of 512 threads).
+constexpr int NORM_PARTS = 1024, RESIDUAL_PARTS = 512;
 
 // Threads of a row of n elements: one for each 16 bytes, a power of two, up to a
 // whole workgroup.

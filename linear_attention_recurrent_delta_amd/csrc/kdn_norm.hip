@@ -119,26 +119,49 @@ struct Lane {
         slot = threadIdx.x / tpr;
         lane = threadIdx.x % tpr;
     }
-    template <int VEC> __device__ __forceinline__ int at(int i) const {
-        return (i * tpr + lane) * VEC;
-    }
 };
 
-// A piece of a row, n elements of it there.  FULL: rows are whole pieces.
-template <bool FULL, typename Piece, typename T>
-__device__ __forceinline__ void get_piece(Piece &v, const T *p, int n) {
-    if constexpr (FULL)
-        v.load(p);
-    else
-        v.load(p, n);
-}
-template <bool FULL, typename Piece, typename T>
-__device__ __forceinline__ void put_piece(const Piece &v, T *p, int n) {
-    if constexpr (FULL)
-        v.store(p);
-    else
-        v.store(p, n);
-}
+// Piece i of a thread: VEC elements of a row of d from `at` on, of which those from `skip`
+// on are its own; none where `there` is false.  A row's last piece ends with the row and
+// has elements of the piece before it in front (a load of fewer elements would be waited
+// for at once); a row shorter than a piece is loaded by its elements.  FULL: rows are
+// whole pieces.
+template <int VEC, bool FULL> struct Piece {
+    int at, skip, n;
+    bool there, whole;
+    __device__ __forceinline__ Piece(const Lane &L, int i, int d) {
+        at = (i * L.tpr + L.lane) * VEC;
+        skip = 0;
+        there = at < d;
+        n = VEC;
+        whole = true;
+        if constexpr (!FULL) {
+            if (there && at + VEC > d) {
+                n = d - at;
+                whole = d >= VEC;
+                skip = whole ? VEC - n : 0;
+                at = whole ? d - VEC : at;
+            }
+        }
+    }
+    __device__ __forceinline__ bool own(int e) const { return FULL || e >= skip; }
+    template <typename T> __device__ __forceinline__ void load(Pack<T, VEC> &v, const T *row) const {
+        if (FULL || whole)
+            v.load(row + at);
+        else
+            v.load(row + at, n);
+    }
+    template <typename T> __device__ __forceinline__ void store(const Pack<T, VEC> &v, T *row) const {
+        if (FULL || n == VEC) {
+            v.store(row + at);
+        } else {
+#pragma unroll
+            for (int e = 0; e < VEC; ++e)
+                if (e >= skip && e < skip + n)
+                    row[at + e] = v.r[e];
+        }
+    }
+};
 
 // What a gated norm's kernel knows of its gate: silu in either order, or nothing.
 enum Kind { NORM_SILU, SILU_NORM, ANY };
@@ -166,28 +189,31 @@ __global__ __launch_bounds__(NT_MAX) void gated_norm_kernel(GatedNormParams P, i
     Pack<float, VEC> ws[IT];
 #pragma unroll
     for (int i = 0; i < IT; ++i) {
-        const int at = L.at<VEC>(i);
+        const Piece<VEC, FULL> piece(L, i, P.d);
         xs[i].zero();
         zs[i].zero();
         ws[i].zero();
-        if (in && at < P.d) {
-            get_piece<FULL>(xs[i], x + at, P.d - at);
+        if (in && piece.there) {
+            piece.load(xs[i], x);
             if (gate.there)
-                get_piece<FULL>(zs[i], z + at, P.d - at);
-            get_piece<FULL>(ws[i], w + at, P.d - at);
+                piece.load(zs[i], z);
+            piece.load(ws[i], w);
         }
     }
     float u[IT][VEC];
     double sum[1] = {0.};
 #pragma unroll
-    for (int i = 0; i < IT; ++i)
+    for (int i = 0; i < IT; ++i) {
+        const Piece<VEC, FULL> piece(L, i, P.d);
 #pragma unroll
         for (int e = 0; e < VEC; ++e) {
             u[i][e] = xs[i].get(e);
             if (gate.first)
                 u[i][e] *= act_f32<FINE>(gate.act, zs[i].get(e));
-            sum[0] = fma((double)u[i][e], (double)u[i][e], sum[0]);
+            const float own = piece.own(e) ? u[i][e] : 0.f;
+            sum[0] = fma((double)own, (double)own, sum[0]);
         }
+    }
     row_sums(sum, tpr, lds);
     const float r = inv_sqrt<FINE>(sum[0] * P.inv_d + (double)P.eps);
     T *y = static_cast<T *>(P.y) + row * P.d;
@@ -201,20 +227,21 @@ __global__ __launch_bounds__(NT_MAX) void gated_norm_kernel(GatedNormParams P, i
                 v *= act_f32<FINE>(gate.act, zs[i].get(e));
             out.set(e, v);
         }
-        const int at = L.at<VEC>(i);
-        if (in && at < P.d)
-            put_piece<FULL>(out, y + at, P.d - at);
+        const Piece<VEC, FULL> piece(L, i, P.d);
+        if (in && piece.there)
+            piece.store(out, y);
     }
 }
 
-// A workgroup's sums of N values of each column over its rows, in the order of the
-// rows' slots, into ws[column].
-template <int VEC, int IT>
+// A workgroup's sums of the values of each column over its rows, in the order of the
+// rows' slots, into out[column].
+template <int VEC, int IT, bool FULL>
 __device__ __forceinline__ void column_sums(const float (&v)[IT][VEC], const Lane &L, int d,
                                             float *lds, float *out) {
     const int slots = blockDim.x / L.tpr;
 #pragma unroll
-    for (int i = 0; i < IT; ++i)
+    for (int i = 0; i < IT; ++i) {
+        const Piece<VEC, FULL> piece(L, i, d);
 #pragma unroll
         for (int e = 0; e < VEC; ++e) {
             float s = v[i][e];
@@ -226,10 +253,10 @@ __device__ __forceinline__ void column_sums(const float (&v)[IT][VEC], const Lan
                     for (int q = 1; q < slots; ++q)
                         s += lds[q * L.tpr + L.lane];
             }
-            const int at = L.at<VEC>(i) + e;
-            if (L.slot == 0 && at < d)
-                out[at] = s;
+            if (L.slot == 0 && piece.there && piece.own(e) && piece.at + e < d)
+                out[piece.at + e] = s;
         }
+    }
 }
 
 template <typename T, int VEC, int IT, bool FULL, Kind KIND>
@@ -248,10 +275,10 @@ __global__ __launch_bounds__(NT_MAX) void gated_norm_grad_kernel(GatedNormParams
     float dw[IT][VEC];
 #pragma unroll
     for (int i = 0; i < IT; ++i) {
-        const int at = L.at<VEC>(i);
+        const Piece<VEC, FULL> piece(L, i, P.d);
         ws[i].zero();
-        if (at < P.d)
-            get_piece<FULL>(ws[i], w + at, P.d - at);
+        if (piece.there)
+            piece.load(ws[i], w);
 #pragma unroll
         for (int e = 0; e < VEC; ++e)
             dw[i][e] = 0.f;
@@ -271,20 +298,21 @@ __global__ __launch_bounds__(NT_MAX) void gated_norm_grad_kernel(GatedNormParams
         Pack<T, VEC> xs[IT], zs[IT], gs[IT];
 #pragma unroll
         for (int i = 0; i < IT; ++i) {
-            const int at = L.at<VEC>(i);
+            const Piece<VEC, FULL> piece(L, i, P.d);
             xs[i].zero();
             zs[i].zero();
             gs[i].zero();
-            if (in && at < P.d) {
-                get_piece<FULL>(xs[i], x + at, P.d - at);
-                get_piece<FULL>(gs[i], dy + at, P.d - at);
+            if (in && piece.there) {
+                piece.load(xs[i], x);
+                piece.load(gs[i], dy);
                 if (gate.there)
-                    get_piece<FULL>(zs[i], z + at, P.d - at);
+                    piece.load(zs[i], z);
             }
         }
         double sums[2] = {0., 0.};       // of u^2 and of t u
 #pragma unroll
-        for (int i = 0; i < IT; ++i)
+        for (int i = 0; i < IT; ++i) {
+            const Piece<VEC, FULL> piece(L, i, P.d);
 #pragma unroll
             for (int e = 0; e < VEC; ++e) {
                 float u = xs[i].get(e), dn = gs[i].get(e);
@@ -293,9 +321,12 @@ __global__ __launch_bounds__(NT_MAX) void gated_norm_grad_kernel(GatedNormParams
                     u = gate.first ? u * a : u;
                     dn = gate.first ? dn : dn * a;
                 }
+                u = piece.own(e) ? u : 0.f;
+                dn = piece.own(e) ? dn * ws[i].get(e) : 0.f;
                 sums[0] = fma((double)u, (double)u, sums[0]);
-                sums[1] = fma((double)(dn * ws[i].get(e)), (double)u, sums[1]);
+                sums[1] = fma((double)dn, (double)u, sums[1]);
             }
+        }
         row_sums(sums, tpr, lds[buf]);
         const float r = inv_sqrt<FINE>(sums[0] * P.inv_d + (double)P.eps);
         // mean(t n)
@@ -303,7 +334,7 @@ __global__ __launch_bounds__(NT_MAX) void gated_norm_grad_kernel(GatedNormParams
 #pragma unroll
         for (int i = 0; i < IT; ++i) {
             Pack<T, VEC> dx, dz;
-            const int at = L.at<VEC>(i);
+            const Piece<VEC, FULL> piece(L, i, P.d);
 #pragma unroll
             for (int e = 0; e < VEC; ++e) {
                 const float xe = xs[i].get(e), ge = gs[i].get(e), we = ws[i].get(e);
@@ -313,15 +344,16 @@ __global__ __launch_bounds__(NT_MAX) void gated_norm_grad_kernel(GatedNormParams
                 const float n = (gate.first ? xe * a : xe) * r;
                 const float dn = gate.first ? ge : ge * a;
                 const float du = r * (dn * we - n * m);
-                // (what lies behind the rows and the row is zero)
+                // (what lies behind the rows and the row is zero; a piece's elements that are not
+                // its own are left out of the columns' sums)
                 dw[i][e] = fmaf(dn, n, dw[i][e]);
                 dx.set(e, gate.first ? du * a : du);
                 dz.set(e, gate.first ? du * xe * da : ge * n * we * da);
             }
-            if (in && at < P.d) {
-                put_piece<FULL>(dx, static_cast<T *>(P.dx) + out + at, P.d - at);
+            if (in && piece.there) {
+                piece.store(dx, static_cast<T *>(P.dx) + out);
                 if (gate.there)
-                    put_piece<FULL>(dz, static_cast<T *>(P.dz) + out + at, P.d - at);
+                    piece.store(dz, static_cast<T *>(P.dz) + out);
             }
         }
         row += step;
@@ -332,7 +364,7 @@ __global__ __launch_bounds__(NT_MAX) void gated_norm_grad_kernel(GatedNormParams
             ++t;
         }
     }
-    column_sums<VEC, IT>(dw, L, P.d, cols,
+    column_sums<VEC, IT, FULL>(dw, L, P.d, cols,
                          P.ws + ((long)blockIdx.x * gridDim.y + head) * P.d);
 }
 
@@ -350,47 +382,48 @@ __global__ __launch_bounds__(NT_MAX) void residual_norm_kernel(ResidualNormParam
     Pack<float, VEC> ws[IT];
 #pragma unroll
     for (int i = 0; i < IT; ++i) {
-        const int at = L.at<VEC>(i);
+        const Piece<VEC, FULL> piece(L, i, P.D);
         xs[i].zero();
         rs[i].zero();
         ws[i].zero();
-        if (in && at < P.D) {
-            get_piece<FULL>(xs[i], x + at, P.D - at);
-            get_piece<FULL>(rs[i], res + at, P.D - at);
-            get_piece<FULL>(ws[i], P.weight + at, P.D - at);
+        if (in && piece.there) {
+            piece.load(xs[i], x);
+            piece.load(rs[i], res);
+            piece.load(ws[i], P.weight);
         }
     }
     float h[IT][VEC];
     double sum[1] = {0.};
 #pragma unroll
     for (int i = 0; i < IT; ++i) {
-        const int at = L.at<VEC>(i);
+        const Piece<VEC, FULL> piece(L, i, P.D);
         Pack<float, VEC> sc;
         sc.zero();
-        if (P.scale_n > 1 && at < P.D)
-            get_piece<FULL>(sc, P.scale + at, P.D - at);
+        if (P.scale_n > 1 && piece.there)
+            piece.load(sc, P.scale);
         Pack<S, VEC> out;
 #pragma unroll
         for (int e = 0; e < VEC; ++e) {
             const float s = P.scale_n == 0 ? 1.f : (P.scale_n == 1 ? P.scale[0] : sc.get(e));
             h[i][e] = fmaf(s, xs[i].get(e), rs[i].get(e));
-            sum[0] = fma((double)h[i][e], (double)h[i][e], sum[0]);
+            const float own = piece.own(e) ? h[i][e] : 0.f;
+            sum[0] = fma((double)own, (double)own, sum[0]);
             out.set(e, h[i][e]);
         }
-        if (in && at < P.D)
-            put_piece<FULL>(out, static_cast<S *>(P.h) + row * P.D + at, P.D - at);
+        if (in && piece.there)
+            piece.store(out, static_cast<S *>(P.h) + row * P.D);
     }
     row_sums(sum, tpr, lds);
     const float r = inv_sqrt<FINE>(sum[0] * P.inv_d + (double)P.eps);
 #pragma unroll
     for (int i = 0; i < IT; ++i) {
-        const int at = L.at<VEC>(i);
+        const Piece<VEC, FULL> piece(L, i, P.D);
         Pack<T, VEC> out;
 #pragma unroll
         for (int e = 0; e < VEC; ++e)
             out.set(e, h[i][e] * r * ws[i].get(e));
-        if (in && at < P.D)
-            put_piece<FULL>(out, static_cast<T *>(P.y) + row * P.D + at, P.D - at);
+        if (in && piece.there)
+            piece.store(out, static_cast<T *>(P.y) + row * P.D);
     }
 }
 
@@ -406,13 +439,13 @@ __global__ __launch_bounds__(NT_MAX) void residual_norm_grad_kernel(ResidualNorm
     const float one = P.scale_n == 1 ? P.scale[0] : 1.f;
 #pragma unroll
     for (int i = 0; i < IT; ++i) {
-        const int at = L.at<VEC>(i);
+        const Piece<VEC, FULL> piece(L, i, P.D);
         ws[i].zero();
         sc[i].zero();
-        if (at < P.D) {
-            get_piece<FULL>(ws[i], P.weight + at, P.D - at);
+        if (piece.there) {
+            piece.load(ws[i], P.weight);
             if (P.scale_n > 1)
-                get_piece<FULL>(sc[i], P.scale + at, P.D - at);
+                piece.load(sc[i], P.scale);
         }
 #pragma unroll
         for (int e = 0; e < VEC; ++e)
@@ -428,18 +461,18 @@ __global__ __launch_bounds__(NT_MAX) void residual_norm_grad_kernel(ResidualNorm
         const long out = (in ? row : 0) * P.D;
 #pragma unroll
         for (int i = 0; i < IT; ++i) {
-            const int at = L.at<VEC>(i);
+            const Piece<VEC, FULL> piece(L, i, P.D);
             h1[i].zero();
             dh1[i].zero();
             g1[i].zero();
             x1[i].zero();
-            if (in && at < P.D) {
-                get_piece<FULL>(h1[i], hrow + at, P.D - at);
-                get_piece<FULL>(g1[i], static_cast<const T *>(P.d_y) + out + at, P.D - at);
+            if (in && piece.there) {
+                piece.load(h1[i], hrow);
+                piece.load(g1[i], static_cast<const T *>(P.d_y) + out);
                 if (P.d_h)
-                    get_piece<FULL>(dh1[i], static_cast<const S *>(P.d_h) + out + at, P.D - at);
+                    piece.load(dh1[i], static_cast<const S *>(P.d_h) + out);
                 if (P.dscale)
-                    get_piece<FULL>(x1[i], x + at, P.D - at);
+                    piece.load(x1[i], x);
             }
         }
     };
@@ -462,13 +495,16 @@ __global__ __launch_bounds__(NT_MAX) void residual_norm_grad_kernel(ResidualNorm
         load(row + (long)P.parts * slots);
         double sums[2] = {0., 0.};       // of u^2 and of t u
 #pragma unroll
-        for (int i = 0; i < IT; ++i)
+        for (int i = 0; i < IT; ++i) {
+            const Piece<VEC, FULL> piece(L, i, P.D);
 #pragma unroll
             for (int e = 0; e < VEC; ++e) {
-                const double u = hs[i].get(e);
+                const double u = piece.own(e) ? hs[i].get(e) : 0.f;
+                const float t = piece.own(e) ? gs[i].get(e) * ws[i].get(e) : 0.f;
                 sums[0] = fma(u, u, sums[0]);
-                sums[1] = fma((double)(gs[i].get(e) * ws[i].get(e)), u, sums[1]);
+                sums[1] = fma((double)t, u, sums[1]);
             }
+        }
         row_sums(sums, tpr, lds[buf]);
         const float r = inv_sqrt<FINE>(sums[0] * P.inv_d + (double)P.eps);
         const float m = (float)(sums[1] * (double)r * P.inv_d);
@@ -476,7 +512,7 @@ __global__ __launch_bounds__(NT_MAX) void residual_norm_grad_kernel(ResidualNorm
         for (int i = 0; i < IT; ++i) {
             Pack<S, VEC> dres;
             Pack<T, VEC> dx;
-            const int at = L.at<VEC>(i);
+            const Piece<VEC, FULL> piece(L, i, P.D);
 #pragma unroll
             for (int e = 0; e < VEC; ++e) {
                 const float g = gs[i].get(e), n = hs[i].get(e) * r;
@@ -486,28 +522,30 @@ __global__ __launch_bounds__(NT_MAX) void residual_norm_grad_kernel(ResidualNorm
                 dres.set(e, d);
                 dx.set(e, d * (P.scale_n > 1 ? sc[i].get(e) : one));
             }
-            if (in && at < P.D) {
-                put_piece<FULL>(dres, static_cast<S *>(P.dresidual) + out + at, P.D - at);
+            if (in && piece.there) {
+                piece.store(dres, static_cast<S *>(P.dresidual) + out);
                 if (P.dx)
-                    put_piece<FULL>(dx, static_cast<T *>(P.dx) + out + at, P.D - at);
+                    piece.store(dx, static_cast<T *>(P.dx) + out);
             }
         }
     }
-    column_sums<VEC, IT>(dw, L, P.D, cols, P.ws + (long)blockIdx.x * P.D);
+    column_sums<VEC, IT, FULL>(dw, L, P.D, cols, P.ws + (long)blockIdx.x * P.D);
     if (!P.dscale)
         return;
     float *part = P.ws + (long)P.parts * P.D;
     if (P.scale_n > 1) {
-        column_sums<VEC, IT>(ds, L, P.D, cols, part + (long)blockIdx.x * P.D);
+        column_sums<VEC, IT, FULL>(ds, L, P.D, cols, part + (long)blockIdx.x * P.D);
         return;
     }
     // one scale: its sum over the workgroup's columns and rows
     float s = 0.f;
 #pragma unroll
-    for (int i = 0; i < IT; ++i)
+    for (int i = 0; i < IT; ++i) {
+        const Piece<VEC, FULL> piece(L, i, P.D);
 #pragma unroll
         for (int e = 0; e < VEC; ++e)
-            s += ds[i][e];
+            s += piece.own(e) ? ds[i][e] : 0.f;
+    }
     __syncthreads();
     cols[threadIdx.x] = s;
     __syncthreads();
@@ -585,11 +623,13 @@ static hipError_t residual_norm_k(const ResidualNormParams &P, hipStream_t st, b
     constexpr int V = 16 / sizeof(T);
 #define KDN_RESIDUAL(IT_)                                                                   \
     {                                                                                           \
-        const long slots = threads / tpr;                                                       \
+        /* gradients: half as many parts, whose sums and their reading count */             \
+        const int wide = back && threads < 512 ? 512 : threads;                                 \
+        const long slots = wide / tpr;                                                          \
         const dim3 grid((unsigned)(back ? P.parts : (P.tokens + slots - 1) / slots));           \
         auto kernel = back ? norm::residual_norm_grad_kernel<T, S, V, IT_, FULL>                \
                            : norm::residual_norm_kernel<T, S, V, IT_, FULL>;                    \
-        hipLaunchKernelGGL(kernel, grid, dim3(threads), 0, st, P, tpr);                         \
+        hipLaunchKernelGGL(kernel, grid, dim3(wide), 0, st, P, tpr);                         \
         return hipGetLastError();                                                               \
     }
     KDN_NORM_IT(KDN_RESIDUAL, P.D)

@@ -186,7 +186,7 @@ unsigned long long kdn_residual_norm_backward_workspace_size(int tokens, int D, 
     const kdn_status st = residual_shape(P, KDN_F32, KDN_F32, tokens, D, scale_n, 1.f, 0, 0);
     if (status)
         *status = st;
-    return st == KDN_OK ? 4ull * std::min(tokens, kdn::NORM_PARTS) * (D + scale_n) : 0;
+    return st == KDN_OK ? 4ull * std::min(tokens, kdn::RESIDUAL_PARTS) * (D + scale_n) : 0;
 }
 
 kdn_status kdn_residual_norm_backward(kdn_dtype dtype, kdn_dtype stream_dtype, int tokens, int D,
@@ -217,7 +217,7 @@ kdn_status kdn_residual_norm_backward(kdn_dtype dtype, kdn_dtype stream_dtype, i
     const Range outs[] = {{dx, n * es}, {dresidual, n * rs}, {dweight, 4LL * D}, {dscale, 4LL * scale_n}};
     if (clash(outs, 4, ins, 6))
         return KDN_ERR_ALIAS;
-    P.parts = std::min(tokens, kdn::NORM_PARTS);
+    P.parts = std::min(tokens, kdn::RESIDUAL_PARTS);
     const long long n_ws = 4LL * P.parts * (D + (dscale ? scale_n : 0));
     if (kdn_status st = workspace_ok(workspace, workspace_bytes, n_ws, ins, 6, outs, 4))
         return st;

@@ -245,7 +245,7 @@ def test_norm_workspace_sizes(lib):
     assert g(1 << 20, 4, 64, 0) == (4 * 1024 * 64, OK) and g(1 << 20, 4, 64, 1) == (4 * 256 * 256, OK)
     assert g(0, 4, 64, 0) == (0, OK) and g(-1, 4, 64, 0)[1] == ESHAPE and g(1, 1, 20000, 0)[1] == EUNSUP
     r = lambda *a: (lib.kdn_residual_norm_backward_workspace_size(*a, ctypes.byref(st)), st.value)
-    assert r(10, 64, 0) == (4 * 640, OK) and r(5000, 64, 64) == (4 * 1024 * 128, OK) and r(10, 64, 7)[1] == ESHAPE
+    assert r(10, 64, 0) == (4 * 640, OK) and r(5000, 64, 64) == (4 * 512 * 128, OK) and r(10, 64, 7)[1] == ESHAPE
 
 
 # ---------------------------------------------------------------------------
