@@ -10,7 +10,16 @@
 namespace kdn {
 namespace scan {
 
-constexpr long SCAN_MANY = 2048, SCAN_OWN_WGS = 4096;
+// Blocks times runs of channels from which each has one wave and not eight: the one
+// wave needs three quarters of the work, and there are enough to fill the CUs.  bf16, 16
+// states, eight waves and one, in us:
+//     tokens    512 runs    1024       2048        4096
+//       300     26   35    49   37    95   54    185   89
+//      1000     62  114   121  117   229  159
+//      4000    221  426   463  430   894  610   1786 1157
+constexpr long SCAN_MANY = 1024;
+// Workgroups that the pass over tiles' own states is shared out to.
+constexpr long SCAN_OWN_WGS = 4096;
 
 // Tokens that a wave takes at a time: their decays and inputs stay in registers
 // between the two passes over them.
@@ -68,7 +77,7 @@ __device__ __forceinline__ int by_length(const ScanParams &P, int p) {
 template <typename T, int SPL, int NW>
 __global__ __launch_bounds__(NW == 1 ? 256 : NW *WAVE, 2) void scan_kernel(ScanParams P,
                                                                            int groups,
-                                                                           long units) {
+                                                                           long blocks) {
     constexpr bool FINE = sizeof(T) == 4;
     constexpr int S = 4 * SPL, K = steps<SPL>(), WAVES = NW == 1 ? 4 : NW;
     __shared__ float bc[WAVES][2][K][S];
@@ -77,15 +86,15 @@ __global__ __launch_bounds__(NW == 1 ? 256 : NW *WAVE, 2) void scan_kernel(ScanP
     constexpr int FOLD = WAVE * SPL / NW;            // states that a wave's lanes fold
     const int lane = threadIdx.x & (WAVE - 1), j = lane & 3, w = wave_id();
     const int seg = NW == 1 ? 0 : w;
-    // NW = 1: each wave has a run of channels of its own
-    const long unit = NW == 1 ? (long)blockIdx.x * WAVES + w : xcd_unit(blockIdx.x, units);
-    if (unit >= units)
+    const int runs = groups * P.G, fours = (runs + 3) / 4;
+    long b = blockIdx.x / fours;
+    int run = (int)(blockIdx.x % fours) * 4 + w;     // NW = 1: one for each wave
+    if (NW == 1 ? run >= runs : !four_unit(blockIdx.x, blocks, runs, b, run))
         return;
-    const int runs = groups * P.G;
-    long b = unit / runs;
-    if (NW == 1 && P.block_offsets && P.nblocks <= WAVE)
+    // of a packed batch the longest sequences go first
+    if (P.block_offsets && P.nblocks <= WAVE)
         b = by_length(P, (int)b);
-    const Channels ch(P, (int)(unit % runs), groups);
+    const Channels ch(P, run, groups);
     const Block B = get_block(P, b);
     if (B.count <= 0 || B.slot < 0 || (!B.single && !P.ws_state))
         return;
@@ -96,10 +105,10 @@ __global__ __launch_bounds__(NW == 1 ? 256 : NW *WAVE, 2) void scan_kernel(ScanP
     // the state in front of the block: the lane's own states, or the one that it folds
     const float *from = B.single ? P.S0 : P.ws_state;
     const long from_slot = B.single ? B.slot : tile_slot(b, B.first, 0, S);
-    const int per = P.C / P.G, run = (int)(unit % runs) % groups;
-    const int fold = w * FOLD + lane, channels = min(SCAN_CHANNELS, per - run * SCAN_CHANNELS);
+    const int per = P.C / P.G, first_c = run % groups * SCAN_CHANNELS;
+    const int fold = w * FOLD + lane, channels = min(SCAN_CHANNELS, per - first_c);
     const bool folds = NW > 1 && lane < FOLD && fold < channels * S;
-    const long fold_at = ((long)ch.g * per + run * SCAN_CHANNELS) * S + fold;
+    const long fold_at = ((long)ch.g * per + first_c) * S + fold;
     float carry = 0.f;
 #pragma unroll
     for (int s = 0; s < SPL; ++s)
@@ -229,15 +238,18 @@ __global__ __launch_bounds__(NW == 1 ? 256 : NW *WAVE, 2) void scan_kernel(ScanP
 constexpr int OWN_WAVES = 4;
 template <typename T, int SPL, bool REV>
 __global__ __launch_bounds__(OWN_WAVES *WAVE) void scan_own_kernel(ScanParams P, int groups,
-                                                                   int classes, long units) {
+                                                                   int classes, long shares) {
     constexpr bool FINE = sizeof(T) == 4;
     constexpr int S = 4 * SPL, K = steps<SPL>(), TILE = scan_tile(S);
     __shared__ float bc[OWN_WAVES][2][K][S];
     const int lane = threadIdx.x & (WAVE - 1), j = lane & 3, w = wave_id();
-    const int runs = groups * P.G;
-    const long unit = xcd_unit(blockIdx.x, units), b = unit / runs / classes;
-    const int share = (int)(unit / runs % classes);
-    const Channels ch(P, (int)(unit % runs), groups);
+    long outer;
+    int run;
+    if (!four_unit(blockIdx.x, shares, groups * P.G, outer, run))
+        return;
+    const long b = outer / classes;
+    const int share = (int)(outer % classes);
+    const Channels ch(P, run, groups);
     const Block B = get_block(P, b);
     if (B.count <= 0 || B.slot < 0 || (!REV && B.single))
         return;
@@ -488,15 +500,16 @@ template <typename T, int SPL>
 hipError_t launch_t(const ScanParams &P, hipStream_t st) {
     constexpr int NW = 8;
     const int groups = scan_groups(P.C, P.G);
-    const long units = scan_total_blocks(P) * groups * P.G;
-    if (units == 0)
+    const long blocks = scan_total_blocks(P), runs = (long)groups * P.G;
+    if (blocks * runs == 0)
         return hipSuccess;
-    if (units >= SCAN_MANY)
-        hipLaunchKernelGGL((scan_kernel<T, SPL, 1>), dim3((unsigned)((units + 3) / 4)), dim3(256), 0,
-                           st, P, groups, units);
+    if (blocks * runs >= SCAN_MANY)
+        hipLaunchKernelGGL((scan_kernel<T, SPL, 1>), dim3((unsigned)(blocks * ((runs + 3) / 4))), dim3(256), 0, st, P,
+                           groups, blocks);
     else
-        hipLaunchKernelGGL((scan_kernel<T, SPL, NW>), dim3((unsigned)units), dim3(NW * WAVE), 0, st,
-                           P, groups, units);
+        hipLaunchKernelGGL((scan_kernel<T, SPL, NW>),
+                           dim3((unsigned)four_grid(blocks, runs)), dim3(NW * WAVE), 0, st, P,
+                           groups, blocks);
     return hipGetLastError();
 }
 
@@ -510,12 +523,12 @@ hipError_t launch_own_t(const ScanParams &P, bool reverse, hipStream_t st) {
     constexpr int FOUR = OWN_WAVES * scan_tile(4 * SPL);
     const long most = min((long)P.block, P.tokens), fours = (most + FOUR - 1) / FOUR;
     const int classes = (int)max(1l, min(fours, (SCAN_OWN_WGS + blocks * runs - 1) / (blocks * runs)));
-    const long units = blocks * classes * runs;
-    const dim3 grid((unsigned)units), block(OWN_WAVES * WAVE);
+    const long shares = blocks * classes;
+    const dim3 grid((unsigned)four_grid(shares, runs)), block(OWN_WAVES * WAVE);
     if (reverse)
-        hipLaunchKernelGGL((scan_own_kernel<T, SPL, true>), grid, block, 0, st, P, groups, classes, units);
+        hipLaunchKernelGGL((scan_own_kernel<T, SPL, true>), grid, block, 0, st, P, groups, classes, shares);
     else
-        hipLaunchKernelGGL((scan_own_kernel<T, SPL, false>), grid, block, 0, st, P, groups, classes, units);
+        hipLaunchKernelGGL((scan_own_kernel<T, SPL, false>), grid, block, 0, st, P, groups, classes, shares);
     return hipGetLastError();
 }
 

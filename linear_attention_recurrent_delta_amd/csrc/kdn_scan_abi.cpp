@@ -15,20 +15,26 @@ using kdn::up256;
 
 namespace {
 
-// Workgroups of the outputs' kernel that run at once: two a CU.
-constexpr int SCAN_WGS = 512;
+// Workgroups of the outputs' kernel that run at once: one a CU, by its registers.
+constexpr int SCAN_WGS = 256;
 // Tokens that a workgroup of the outputs' kernel takes at a time.
 constexpr int SCAN_STEP = 128;
 
-// Tokens of a block.  A workgroup walks a block for 16 channels; sequences are cut
-// where there would be fewer workgroups than half of those that run at once, at the
-// price of another pass (its time is 0.7 of the outputs') and two launches.
+// Tokens of a block.  A workgroup walks a block for 16 channels, and sequences are cut
+// into as many blocks as run at once, where the walk becomes shorter by more than the
+// price: another pass of half the work and two launches, together some 4 steps.  bf16,
+// 16 states, whole and cut, in us:
+//     tokens   16 runs of channels    64          128
+//      1000     30    22               29   24     31   34
+//      4000    100    31              110   61    112   99
+//     16000    390    90              415  204    418  357
 int scan_block(long long tokens, int N, int C) {
     const long long runs = (C + kdn::SCAN_CHANNELS - 1) / kdn::SCAN_CHANNELS;
     long long block = tokens;
     const long long len = N > 0 ? (tokens + N - 1) / N : 0;
-    if (runs * N < SCAN_WGS / 2 && len > 8 * SCAN_STEP)
-        block = std::max((tokens * runs + SCAN_WGS - 1) / SCAN_WGS, 2LL * SCAN_STEP);
+    const long long blocks = runs * N > 0 ? SCAN_WGS / (runs * N) : 1;
+    if (blocks >= 2 && len * (2 * blocks - 3) > 8 * SCAN_STEP * blocks)
+        block = std::max((len + blocks - 1) / blocks, (long long)SCAN_STEP);
     block = (std::max(block, 1LL) + 63) / 64 * 64;
     return (int)std::min(block, 1LL << 30);
 }
@@ -70,10 +76,11 @@ kdn_status scan_blocks(kdn::ScanParams &P, bool packed, int block) {
         P.nblocks = P.T == 0 ? 0 : (P.T - 1) / block + 1;
     }
     const long long blocks = packed ? P.nblocks : (long long)P.N * P.nblocks;
-    const long long runs = P.C > 0 ? (long long)kdn::scan_groups(P.C, P.G) * P.G : 0;
+    // (grids have fours of runs)
+    const long long runs = P.C > 0 ? ((long long)kdn::scan_groups(P.C, P.G) * P.G + 3) / 4 * 4 : 0;
     P.tile_slots = kdn::tile_slots(P.tokens, blocks, P.S);
     const long long pieces = ((long long)P.C * P.S + 255) / 256;
-    if (blocks >= (1LL << 32) || !launchable(blocks * runs, 512) ||
+    if (blocks >= (1LL << 32) || !launchable(blocks * runs + 32, 512) ||
         !launchable(2LL * P.N * pieces, 256) || P.tile_slots * P.C >= (1LL << 40))
         return KDN_ERR_SHAPE;
     return KDN_OK;

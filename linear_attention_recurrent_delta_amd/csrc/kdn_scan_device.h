@@ -71,11 +71,20 @@ template <bool FINE> __device__ __forceinline__ float softplus(float x) {
     return fmaf(2.f, p, x < 0.f ? 0.f : x);
 }
 
-// Consecutive units of work on one XCD, whose L2 then has the lines that neighbouring
-// runs of channels share: workgroups go to the 8 XCDs in turn.
-__device__ __forceinline__ long xcd_unit(long id, long total) {
-    const long q = total / 8, r = total % 8, x = id % 8;
-    return x * q + (x < r ? x : r) + id / 8;
+constexpr int XCDS = 8;
+
+// Workgroup `id` of a grid over (outer, run of channels): four runs share the lines of
+// a row and are neighbours on an XCD; fours go over the XCDs in turn, so that each has
+// its part of every sequence.
+__host__ __device__ __forceinline__ long four_grid(long outers, long runs) {
+    return (outers * ((runs + 3) / 4) + XCDS - 1) / XCDS * XCDS * 4;
+}
+__device__ __forceinline__ bool four_unit(long id, long outers, int runs, long &outer, int &run) {
+    const int fours = (runs + 3) / 4;
+    const long k = id / XCDS, four = k / 4 * XCDS + id % XCDS;
+    outer = four / fours;
+    run = (int)(four % fours * 4 + k % 4);
+    return outer < outers && run < runs;
 }
 
 // A wave's 16 channels: run k of the channels of group g.
