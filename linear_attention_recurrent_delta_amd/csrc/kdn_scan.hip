@@ -4,7 +4,10 @@
 // Every token needs an exponential for each channel and state, so the scan is bound
 // by the vector units: a product, an exponential (two instructions' time), a product
 // and two sums for each state.  No matrix product is in it: the decays differ for
-// each channel and state.
+// each channel and state.  A wave has 16 channels, four lanes each, with S / 4 states
+// in a lane's registers: a token's 16 values are 32 or 64 bytes of a row, B and C of a
+// token come from LDS once for four channels' lanes, and the sum over states is two
+// steps within four lanes.
 #include "kdn_scan_device.h"
 
 namespace kdn {
@@ -18,7 +21,9 @@ namespace scan {
 //      1000     62  114   121  117   229  159
 //      4000    221  426   463  430   894  610   1786 1157
 constexpr long SCAN_MANY = 1024;
-// Workgroups that the pass over tiles' own states is shared out to.
+// Workgroups that the pass over tiles' own states is shared out to.  With 1024, 4096
+// and 16384: one sequence of 16000 tokens and 1024 channels 214, 209 and 209 us,
+// gradients of 11 packed sequences of 518 channels, float32, 209, 204 and 215.
 constexpr long SCAN_OWN_WGS = 4096;
 
 // Tokens that a wave takes at a time: their decays and inputs stay in registers
@@ -72,7 +77,11 @@ __device__ __forceinline__ int by_length(const ScanParams &P, int p) {
 // lanes, one for each of the run's 16 S states, fold the waves' ends into the states
 // in front of their tokens and carry the last on; and every wave goes through its
 // tokens again, with their decays and inputs from registers (one more product and sum
-// for a state than a walk by one wave, which NW = 1 is).
+// for a state than a walk by one wave, which NW = 1 is).  The chain along a sequence
+// is then an eighth as long.  37 packed prompts (22 thousand tokens) of 4096 channels,
+// 16 states, bf16: 350 us with the vector units busy all the time (six instructions'
+// time for a state are 245; B and C from LDS, softplus, gate and sums over states the
+// rest), 2.1 TB/s; a prompt of 190 tokens and 2048 channels: 11 us.
 // ---------------------------------------------------------------------------
 template <typename T, int SPL, int NW>
 __global__ __launch_bounds__(NW == 1 ? 256 : NW *WAVE, 2) void scan_kernel(ScanParams P,
@@ -233,7 +242,8 @@ __global__ __launch_bounds__(NW == 1 ? 256 : NW *WAVE, 2) void scan_kernel(ScanP
 // dt_t x_t B_t, the sum of its time steps, and with REV what its tokens hand to the
 // reverse recurrence, Q = sum_t (decay up to and with t) dy'_t C_t, dy' = dy silu(z).
 // A workgroup has a run of 16 channels and a share of a block: its waves take every
-// fourth of every `classes`-th four tiles, token by token.
+// fourth of every `classes`-th four tiles, token by token.  Bound by the vector units
+// as the outputs are: B2 T4096, 2048 channels, 16 states, bf16, both ways 88 us.
 // ---------------------------------------------------------------------------
 constexpr int OWN_WAVES = 4;
 template <typename T, int SPL, bool REV>
@@ -323,7 +333,10 @@ __global__ __launch_bounds__(OWN_WAVES *WAVE) void scan_own_kernel(ScanParams P,
 // state at its start, h <- 2^(A2 sum dt) h + U; reverse (tiles last to first): Q
 // becomes the reverse state behind its end, and behind the first tile is dS0.  A
 // thread holds two states of a channel; the next JOIN tiles are on their way while as
-// many are joined.
+// many are joined (4, 8 and 16: one sequence of 16000 tokens and 1024 channels 212, 208
+// and 205 us, gradients of B2 T4096 398, 393 and 396).  Bound by a chain of as many
+// loads as there are tiles: 16 us for two of 64 both ways, 2048 channels (27 with one
+// state a thread and no tiles on their way).
 // ---------------------------------------------------------------------------
 constexpr int JOIN = 8, JOIN_NT = 256;
 template <bool REV>
@@ -436,7 +449,8 @@ __global__ __launch_bounds__(JOIN_NT) void scan_join_kernel(ScanParams P, int pi
 
 // ---------------------------------------------------------------------------
 // Single tokens.  Bound by one read and one write of the states.  Four lanes a
-// channel, as above; no state is read twice, so they pass the caches.
+// channel, as above; no state is read twice, so they pass the caches.  256 sequences,
+// 4096 channels, 16 states, bf16: 30 us, 4.8 TB/s.
 // ---------------------------------------------------------------------------
 template <typename T, int SPL>
 __global__ __launch_bounds__(256) void scan_decode_kernel(ScanDecodeParams P, int chunks) {

