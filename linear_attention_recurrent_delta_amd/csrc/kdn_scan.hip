@@ -5,9 +5,9 @@
 // by the vector units: a product, an exponential (two instructions' time), a product
 // and two sums for each state.  No matrix product is in it: the decays differ for
 // each channel and state.  A wave has 16 channels, four lanes each, with S / 4 states
-// in a lane's registers: a token's 16 values are 32 or 64 bytes of a row, B and C of a
-// token come from LDS once for four channels' lanes, and the sum over states is two
-// steps within four lanes.
+// in a lane's registers: a token's 16 values are 32 or 64 bytes of a row, one read from
+// LDS brings B and C of a token to all 16 channels, and the sum over states is two steps
+// within four lanes.
 #include "kdn_scan_device.h"
 
 namespace kdn {

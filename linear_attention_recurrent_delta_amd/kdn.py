@@ -973,6 +973,17 @@ def _workspace(n, workspace, dev, stream):
     return workspace, workspace.numel()
 
 
+def _outputs(out, specs, dev, stream):
+    """A call's outputs (name, shape, dtype, whether wanted or "zero"): those of ``out``,
+    checked, or new ones."""
+    if out is None:
+        return {name: _new(shape, kind, dev, stream, zero=want == "zero") if want else None
+                for name, shape, kind, want in specs}
+    for name, shape, kind, _ in specs:
+        _same(name, out[name], shape, kind, dev)
+    return out
+
+
 def _taps(weight, C):
     if not isinstance(weight, torch.Tensor) or weight.dim() != 2:
         raise ValueError("kdn: weight must be a tensor [C, W]")
@@ -1067,18 +1078,15 @@ def causal_conv_backward(x, weight, d_y, bias=None, state0=None, dstate_out=None
     W = _taps(weight, C)
     xs = _strided("x", x, lead, (C,), dt, dev)
     s_shape = (pool, W - 1, C)
-    if out is None:
-        out = dict(dx=_new(lead + (C,), dt, dev, stream), dweight=_new((C, W), _f32, dev, stream),
-                   dbias=None if bias is None else _new((C,), _f32, dev, stream),
-                   dstate0=_new((pool, max(W - 1, 0), C), dt, dev, stream, zero=tables is not None))
-    for name, t, shape, kind in (("weight", weight, (C, W), _f32), ("bias", bias, (C,), _f32),
-                                 ("d_y", d_y, lead + (C,), dt), ("state0", state0, s_shape, dt),
-                                 ("dstate_out", dstate_out, s_shape, dt),
-                                 ("dx", out["dx"], lead + (C,), dt),
-                                 ("dweight", out["dweight"], (C, W), _f32),
-                                 ("dbias", out["dbias"], (C,), _f32),
-                                 ("dstate0", out["dstate0"], s_shape, dt)):
-        _same(name, t, shape, kind, dev)
+    out = _outputs(out, (("dx", lead + (C,), dt, True), ("dweight", (C, W), _f32, True),
+                         ("dbias", (C,), _f32, bias is not None),
+                         ("dstate0", (pool, max(W - 1, 0), C), dt,
+                          True if tables is None else "zero")), dev, stream)
+    _same("weight", weight, (C, W), _f32, dev)
+    _same("bias", bias, (C,), _f32, dev)
+    _same("d_y", d_y, lead + (C,), dt, dev)
+    _same("state0", state0, s_shape, dt, dev)
+    _same("dstate_out", dstate_out, s_shape, dt, dev)
     st = ctypes.c_int(0)
     n = lib.kdn_causal_conv_backward_workspace_size(DTYPES[dt], N, T, C, W, pk, ctypes.byref(st))
     _check(lib, st.value)
@@ -1211,24 +1219,16 @@ def selective_scan_backward(x, delta, A, B, C, d_y, D=None, z=None, delta_bias=N
     dt, dev = _dtype("x", x)
     lead, N, T, pk, pool = _batch(x, tables, (S0, dS_out, (out or {}).get("dS0")), 1, "x")
     c, s, g, strides = _scan_inputs(x, delta, A, B, C, D, z, delta_bias, lead)
-    if out is None:
-        new = lambda *shape: _new(lead + shape, dt, dev, stream)  # noqa: E731
-        par = lambda *shape: _new(shape, _f32, dev, stream)  # noqa: E731
-        out = dict(dx=new(c), ddelta=new(c), dz=None if z is None else new(c), dB=new(g, s),
-                   dC=new(g, s), dA=par(c, s), dD=None if D is None else par(c),
-                   ddelta_bias=None if delta_bias is None else par(c),
-                   dS0=_new((pool, c, s), _f32, dev, stream, zero=tables is not None))
-    for name, t, shape, kind in (("d_y", d_y, lead + (c,), dt), ("S0", S0, (pool, c, s), _f32),
-                                 ("dS_out", dS_out, (pool, c, s), _f32),
-                                 ("dx", out["dx"], lead + (c,), dt),
-                                 ("ddelta", out["ddelta"], lead + (c,), dt),
-                                 ("dz", out["dz"], lead + (c,), dt),
-                                 ("dB", out["dB"], lead + (g, s), dt),
-                                 ("dC", out["dC"], lead + (g, s), dt),
-                                 ("dA", out["dA"], (c, s), _f32), ("dD", out["dD"], (c,), _f32),
-                                 ("ddelta_bias", out["ddelta_bias"], (c,), _f32),
-                                 ("dS0", out["dS0"], (pool, c, s), _f32)):
-        _same(name, t, shape, kind, dev)
+    out = _outputs(out, (("dx", lead + (c,), dt, True), ("ddelta", lead + (c,), dt, True),
+                         ("dz", lead + (c,), dt, z is not None), ("dB", lead + (g, s), dt, True),
+                         ("dC", lead + (g, s), dt, True), ("dA", (c, s), _f32, True),
+                         ("dD", (c,), _f32, D is not None),
+                         ("ddelta_bias", (c,), _f32, delta_bias is not None),
+                         ("dS0", (pool, c, s), _f32, True if tables is None else "zero")),
+                   dev, stream)
+    _same("d_y", d_y, lead + (c,), dt, dev)
+    _same("S0", S0, (pool, c, s), _f32, dev)
+    _same("dS_out", dS_out, (pool, c, s), _f32, dev)
     st = ctypes.c_int(0)
     n = lib.kdn_selective_scan_backward_workspace_size(DTYPES[dt], N, T, c, s, g, pk, ctypes.byref(st))
     _check(lib, st.value)
@@ -1287,14 +1287,9 @@ def gated_norm_backward(x, weight, d_y, gate=None, eps=1e-5, order="norm_gate", 
     without a gate) in x's dtype and dweight float32, or ``out``, such a dict."""
     lib = load()
     dt, dev, tokens, H, d, order, act, per_head, xs, zs = _heads(x, weight, gate, order, activation)
-    if out is None:
-        out = dict(dx=_new(x.shape, dt, dev, stream),
-                   dgate=None if gate is None else _new(x.shape, dt, dev, stream),
-                   dweight=_new(weight.shape, _f32, dev, stream))
-    for name, t, shape, kind in (("d_y", d_y, x.shape, dt), ("dx", out["dx"], x.shape, dt),
-                                 ("dgate", out["dgate"], x.shape, dt),
-                                 ("dweight", out["dweight"], weight.shape, _f32)):
-        _same(name, t, shape, kind, dev)
+    out = _outputs(out, (("dx", x.shape, dt, True), ("dgate", x.shape, dt, gate is not None),
+                         ("dweight", weight.shape, _f32, True)), dev, stream)
+    _same("d_y", d_y, x.shape, dt, dev)
     st = ctypes.c_int(0)
     n = lib.kdn_gated_norm_backward_workspace_size(tokens, H, d, per_head, ctypes.byref(st))
     _check(lib, st.value)
@@ -1364,16 +1359,12 @@ def residual_norm_backward(x, h, weight, d_y, d_h=None, scale=None, eps=1e-5, ou
         raise TypeError("kdn: d_y must be a tensor")
     if x is None:
         dt, _ = _dtype("d_y", d_y)
-    if out is None:
-        out = dict(dx=_new(h.shape, dt, dev, stream), dresidual=_new(h.shape, sdt, dev, stream),
-                   dweight=_new((D,), _f32, dev, stream),
-                   dscale=None if scale is None or x is None else _new((scale_n,), _f32, dev, stream))
-    for name, t, shape, kind in (("d_y", d_y, h.shape, dt), ("d_h", d_h, h.shape, sdt),
-                                 ("dx", out["dx"], h.shape, dt),
-                                 ("dresidual", out["dresidual"], h.shape, sdt),
-                                 ("dweight", out["dweight"], (D,), _f32),
-                                 ("dscale", out["dscale"], (scale_n,), _f32)):
-        _same(name, t, shape, kind, dev)
+    out = _outputs(out, (("dx", h.shape, dt, True), ("dresidual", h.shape, sdt, True),
+                         ("dweight", (D,), _f32, True),
+                         ("dscale", (scale_n,), _f32, scale is not None and x is not None)),
+                   dev, stream)
+    _same("d_y", d_y, h.shape, dt, dev)
+    _same("d_h", d_h, h.shape, sdt, dev)
     st = ctypes.c_int(0)
     n = lib.kdn_residual_norm_backward_workspace_size(tokens, D, scale_n, ctypes.byref(st))
     _check(lib, st.value)
