@@ -191,6 +191,48 @@ def test_packed(dtype, S, G, lengths, behind, block):
 
 
 @pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("S,G,C", [(16, 1, 80), (8, 5, 35), (32, 2, 150)])
+def test_many_sequences(dtype, S, G, C):
+    """More runs of channels than the GPU has waves for, fives of them and not fours: a wave a run."""
+    B, T = 300, 37
+    args, kw = case((B, T), C, S, G, dtype, seed=S)
+    S0 = randn((B, C, S), F32, 9)
+    y, last = kdn.selective_scan(*args, S0=S0, **kw)
+    a, k = flat(args, kw)
+    some = (0, 1, 2, 150, 298, 299)
+    check(a, k, S0, y.view(-1, C), last, [slice(n * T, n * T + T) for n in some], some)
+    keep = S0.clone()
+    y2, _ = kdn.selective_scan(*args, S0=keep, out=(torch.empty_like(y), keep), **kw)
+    assert torch.equal(y, y2) and torch.equal(keep, last)
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("n,C,block", [(40, 430, 256), (40, 430, 64), (63, 300, 64), (300, 80, 64), (5, 330, 1024),
+                                       (3, 40, 128)])
+def test_uneven_packed_sequences(dtype, n, C, block):
+    """Lengths from none to hundreds, few and many runs, blocks by length and not; skipped
+    sequences and rows behind the last are left alone."""
+    S, G = 16, 2
+    lengths = [(7 * i * i) % 41 if i % 9 else 130 * (i % 5) for i in range(n)]
+    total = sum(lengths) + 19
+    args, kw = case((total,), C, S, G, dtype, seed=n)
+    slots = [n + 3 - i for i in range(n)]
+    slots[1] = -1
+    tables = kdn.sequence_tables(i32(lengths), total, block, slots=i32(slots))
+    S0 = randn((n + 5, C, S), F32, 9)
+    y0 = randn((total, C), dtype, 10)
+    y, last = kdn.selective_scan(*args, S0=S0, tables=tables, out=(y0.clone(), S0.clone()), **kw)
+    first = [sum(lengths[:i]) for i in range(n + 1)]
+    on = [i for i in range(n) if slots[i] >= 0]
+    some = sorted(set(on[:4] + on[::max(1, n // 12)] + on[-4:]))
+    check(args, kw, S0, y, last, [slice(first[i], first[i + 1]) for i in some if lengths[i]],
+          [slots[i] for i in some if lengths[i]])
+    assert torch.equal(y[first[1]:first[2]], y0[first[1]:first[2]]) and torch.equal(y[first[n]:], y0[first[n]:])
+    left = [i for i in range(n + 5) if i not in slots] + [slots[i] for i in on if not lengths[i]]
+    assert torch.equal(last[left], S0[left])
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
 @pytest.mark.parametrize("C,S,G", [(5, 8, 1), (100, 16, 2), (64, 32, 1)])
 def test_decode(dtype, C, S, G):
     N, pool = 6, 9
