@@ -12,9 +12,11 @@
 // the decays and the states in registers.  Bound by the vector units: 18 instructions'
 // time for each token, channel and state, an exponential's two among them (140 us for
 // B2 T4096, 2048 channels, 16 states), and as much again for B and C from LDS, the
-// exchanges between lanes and the tokens' own functions.  That call, bf16: 320 us, the
-// vector units busy 74 % of the time, two waves a SIMD by their registers; 693 MB moved,
-// where the inputs and gradients are 236.
+// exchanges between lanes and the tokens' own functions.  That call, bf16: 290 us, the
+// vector units busy 82 % of the time, two waves a SIMD by their registers; the call moves
+// 607 MB, where its inputs and gradients are 236.  Softplus, the gate and their slopes are
+// made once, in front, and take fewer registers than the inputs that they replace (made
+// again behind the scans: 323 us, with 20 registers spilled).
 // dB and dC are sums over channels: a lane adds those of its runs in registers, so
 // that only their sum goes through the exchanges between lanes, once for each set of
 // runs; the sets' sums are added by another kernel.
@@ -175,15 +177,23 @@ __global__ __launch_bounds__(grad_waves<SPL>() * WAVE, 2) void scan_grad_kernel(
                               first, k + 1 < runs ? count : 0);
                     load_states<SPL>(&par_A[k][lane * SPL], A2);
                     const float bias = par[k][0][lane >> 2], D = par[k][1][lane >> 2];
-                    float dt[K / 4], in[K / 4], dp[K / 4], sum = 0.f;
+                    // slope: of softplus; dz: dy silu'(z), the gate's gradient without its p
+                    float dt[K / 4], in[K / 4], dp[K / 4], slope[K / 4], dz[K / 4], sum = 0.f;
 #pragma unroll
                     for (int i = 0; i < K / 4; ++i) {
-                        const float v = to_f32(now.d[i]) + bias;
-                        dt[i] = 4 * i + j < count ? (P.softplus ? softplus<FINE>(v) : v) : 0.f;
+                        dt[i] = to_f32(now.d[i]) + bias;
+                        slope[i] = 1.f;
+                        if (P.softplus)
+                            softplus_grad<FINE>(dt[i], dt[i], slope[i]);
+                        dt[i] = 4 * i + j < count ? dt[i] : 0.f;
                         in[i] = dt[i] * to_f32(now.x[i]);
-                        dp[i] = to_f32(now.g[i]);
-                        if (P.z)
-                            dp[i] *= silu_f32<FINE>(to_f32(now.z[i]));
+                        dp[i] = dz[i] = to_f32(now.g[i]);
+                        if (P.z) {
+                            float act, dact;
+                            silu_grad<FINE>(to_f32(now.z[i]), act, dact);
+                            dp[i] *= act;
+                            dz[i] *= dact;
+                        }
                         sum += dt[i];
                     }
                     float a[K][SPL], h[K][SPL], end[SPL], back[SPL], all[SPL];
@@ -249,7 +259,7 @@ __global__ __launch_bounds__(grad_waves<SPL>() * WAVE, 2) void scan_grad_kernel(
                     load_states<SPL>(&ends[1][w][lane * SPL], hs);
                     load_states<SPL>(&ends[2][w][lane * SPL], r);
                     // forwards: h[i] becomes the state before token i
-                    float part[4], y[K / 4], dz[K / 4];
+                    float part[4], y[K / 4];
                     unrolled<K>([&](auto I) {
                         constexpr int i = I;
                         const float e = quad_lane<i % 4>(dp[i / 4]);
@@ -304,17 +314,9 @@ __global__ __launch_bounds__(grad_waves<SPL>() * WAVE, 2) void scan_grad_kernel(
                     const Rows<T, K> rz(P.dz, first, P.C, P.C, P.z ? count : 0);
 #pragma unroll
                     for (int i = 0; i < K / 4; ++i) {
-                        const float x = to_f32(now.x[i]), v = to_f32(now.d[i]) + bias;
+                        const float x = to_f32(now.x[i]);
                         const float dx = fmaf(dt[i], sum_B[i], D * dp[i]);
-                        float dd = fmaf(x, sum_B[i], sum_w[i] * (1.f / LOG2E));
-                        if (P.softplus)
-                            dd *= sigmoid_f32<FINE>(v);
-                        dz[i] = 0.f;
-                        if (P.z) {
-                            float act, slope;
-                            silu_grad<FINE>(to_f32(now.z[i]), act, slope);
-                            dz[i] = to_f32(now.g[i]) * fmaf(D, x, y[i]) * slope;
-                        }
+                        const float dd = slope[i] * fmaf(x, sum_B[i], sum_w[i] * (1.f / LOG2E));
                         if (4 * i + j < count) {
                             dD = fmaf(dp[i], x, dD);
                             dbias += dd;
@@ -322,7 +324,7 @@ __global__ __launch_bounds__(grad_waves<SPL>() * WAVE, 2) void scan_grad_kernel(
                         const int at = rx.at(4 * i + j1, P.C, ch.c, ch.live);
                         rx.store(from_f32<T>(dx), at);
                         rd.store(from_f32<T>(dd), at);
-                        rz.store(from_f32<T>(dz[i]), at);
+                        rz.store(from_f32<T>(dz[i] * fmaf(D, x, y[i])), at);
                     }
                     float old[SPL];
                     load_states<SPL>(&sum_A[k][w][lane * SPL], old);

@@ -51,8 +51,7 @@ __device__ __forceinline__ float quad_sums(const float (&v)[4], int j) {
 // log(1 + w) = 2 (s + s^3 / 3 + s^5 / 5 ..), s = w / (2 + w) <= 1/3: no cancellation,
 // so that small time steps keep their relative precision.  The terms left out are
 // below 2^-18 of the sum in bfloat16 calls, 2^-26 in float32 ones.
-template <bool FINE> __device__ __forceinline__ float softplus(float x) {
-    const float w = exp_f32<FINE>(-fabsf(x));
+template <bool FINE> __device__ __forceinline__ float softplus(float x, float w) {
     const float s = FINE ? w / (2.f + w) : w * fast_rcp(2.f + w);
     const float q = s * s;
     float p;
@@ -69,6 +68,16 @@ template <bool FINE> __device__ __forceinline__ float softplus(float x) {
     p = fmaf(p * q, s, s);
     // NaN stays NaN: no fmaxf
     return fmaf(2.f, p, x < 0.f ? 0.f : x);
+}
+template <bool FINE> __device__ __forceinline__ float softplus(float x) {
+    return softplus<FINE>(x, exp_f32<FINE>(-fabsf(x)));
+}
+// softplus(x) and its derivative, 1 / (1 + e^-x), from the same exponential
+template <bool FINE>
+__device__ __forceinline__ void softplus_grad(float x, float &y, float &dy) {
+    const float w = exp_f32<FINE>(-fabsf(x)), n = x < 0.f ? w : 1.f;
+    y = softplus<FINE>(x, w);
+    dy = FINE ? n / (1.f + w) : n * fast_rcp(1.f + w);
 }
 
 constexpr int XCDS = 8;
