@@ -10,6 +10,7 @@ from __future__ import annotations
 
 import ctypes
 import dataclasses
+import math
 import os
 
 import torch
@@ -973,14 +974,25 @@ def _workspace(n, workspace, dev, stream):
     return workspace, workspace.numel()
 
 
+def _like(x, dtype, dev, stream):
+    """New memory for a contiguous tensor of x's shape, the quickest way."""
+    if stream is None and x.dtype is dtype and dev.type == "cuda" and x.is_contiguous():
+        return torch.empty_like(x)
+    return _new(x.shape, dtype, dev, stream)
+
+
 def _outputs(out, specs, dev, stream):
-    """A call's outputs (name, shape, dtype, whether wanted or "zero"): those of ``out``,
-    checked, or new ones."""
+    """A call's outputs (name, shape of or tensor like it, dtype, whether wanted or "zero"):
+    those of ``out``, checked, or new ones."""
     if out is None:
-        return {name: _new(shape, kind, dev, stream, zero=want == "zero") if want else None
+        return {name: None if not want else _like(shape, kind, dev, stream)
+                if isinstance(shape, torch.Tensor)
+                else _new(shape, kind, dev, stream, zero=want == "zero")
                 for name, shape, kind, want in specs}
-    for name, shape, kind, _ in specs:
-        _same(name, out[name], shape, kind, dev)
+    for name, shape, kind, want in specs:
+        if out[name] is not None:
+            _same(name, out[name], shape.shape if isinstance(shape, torch.Tensor) else shape,
+                  kind, dev)
     return out
 
 
@@ -1012,7 +1024,7 @@ def causal_conv(x, weight, bias=None, state0=None, tables=None, activation="silu
     xs = _strided("x", x, lead, (C,), dt, dev)
     s_shape = (pool, W - 1, C)
     if out is None:
-        y = _new(lead + (C,), dt, dev, stream)
+        y = _like(x, dt, dev, stream)
         if tables is not None and state0 is not None:
             S = state0
         elif tables is not None and tables.slots is not None:
@@ -1078,12 +1090,12 @@ def causal_conv_backward(x, weight, d_y, bias=None, state0=None, dstate_out=None
     W = _taps(weight, C)
     xs = _strided("x", x, lead, (C,), dt, dev)
     s_shape = (pool, W - 1, C)
-    out = _outputs(out, (("dx", lead + (C,), dt, True), ("dweight", (C, W), _f32, True),
+    _same("weight", weight, (C, W), _f32, dev)
+    _same("bias", bias, (C,), _f32, dev)
+    out = _outputs(out, (("dx", x, dt, True), ("dweight", weight, _f32, True),
                          ("dbias", (C,), _f32, bias is not None),
                          ("dstate0", (pool, max(W - 1, 0), C), dt,
                           True if tables is None else "zero")), dev, stream)
-    _same("weight", weight, (C, W), _f32, dev)
-    _same("bias", bias, (C,), _f32, dev)
     _same("d_y", d_y, lead + (C,), dt, dev)
     _same("state0", state0, s_shape, dt, dev)
     _same("dstate_out", dstate_out, s_shape, dt, dev)
@@ -1145,7 +1157,7 @@ def selective_scan(x, delta, A, B, C, D=None, z=None, delta_bias=None, softplus=
     lead, N, T, pk, pool = _batch(x, tables, (S0, out[1] if out is not None else None), 1, "x")
     c, s, g, strides = _scan_inputs(x, delta, A, B, C, D, z, delta_bias, lead)
     if out is None:
-        y = _new(lead + (c,), dt, dev, stream)
+        y = _like(x, dt, dev, stream)
         if tables is not None and S0 is not None:
             S = S0
         elif tables is not None and tables.slots is not None:
@@ -1219,9 +1231,9 @@ def selective_scan_backward(x, delta, A, B, C, d_y, D=None, z=None, delta_bias=N
     dt, dev = _dtype("x", x)
     lead, N, T, pk, pool = _batch(x, tables, (S0, dS_out, (out or {}).get("dS0")), 1, "x")
     c, s, g, strides = _scan_inputs(x, delta, A, B, C, D, z, delta_bias, lead)
-    out = _outputs(out, (("dx", lead + (c,), dt, True), ("ddelta", lead + (c,), dt, True),
-                         ("dz", lead + (c,), dt, z is not None), ("dB", lead + (g, s), dt, True),
-                         ("dC", lead + (g, s), dt, True), ("dA", (c, s), _f32, True),
+    out = _outputs(out, (("dx", x, dt, True), ("ddelta", x, dt, True),
+                         ("dz", x, dt, z is not None), ("dB", B, dt, True), ("dC", B, dt, True),
+                         ("dA", A, _f32, True),
                          ("dD", (c,), _f32, D is not None),
                          ("ddelta_bias", (c,), _f32, delta_bias is not None),
                          ("dS0", (pool, c, s), _f32, True if tables is None else "zero")),
@@ -1249,16 +1261,19 @@ def _heads(x, weight, gate, order, activation):
     if order not in NORM_ORDERS:
         raise ValueError(f"kdn: order must be one of {tuple(NORM_ORDERS)}, not {order!r}")
     act = _activation(activation, (None, "silu", "sigmoid"))
-    lead, (H, d) = x.shape[:-2], x.shape[-2:]
+    shape = x.shape
+    lead, H, d = shape[:-2], shape[-2], shape[-1]
     if not isinstance(weight, torch.Tensor) or weight.dim() not in (1, 2):
         raise ValueError("kdn: weight must be a tensor [d] or [H, d]")
     per_head = weight.dim() == 2
     _same("weight", weight, (H, d) if per_head else (d,), _f32, dev)
-    tokens = 1
-    for n in lead:
-        tokens *= n
-    xs = _strided("x", x, lead, (H, d), dt, dev)
-    zs = 0 if gate is None else _strided("gate", gate, lead, (H, d), dt, dev)
+    tokens = math.prod(lead)
+    xs = 0 if x.is_contiguous() else _strided("x", x, lead, (H, d), dt, dev)
+    zs = 0
+    if gate is not None and not (isinstance(gate, torch.Tensor) and gate.shape == shape and
+                                 gate.dtype is dt and gate.get_device() == dev.index and
+                                 gate.is_contiguous()):
+        zs = _strided("gate", gate, lead, (H, d), dt, dev)
     return (dt, dev, _int32("tokens", tokens), _int32("H", H), _int32("d", d), NORM_ORDERS[order],
             act, int(per_head), xs, zs)
 
@@ -1274,8 +1289,9 @@ def gated_norm(x, weight, gate=None, eps=1e-5, order="norm_gate", activation="si
     lib = load()
     dt, dev, tokens, H, d, order, act, per_head, xs, zs = _heads(x, weight, gate, order, activation)
     if out is None:
-        out = _new(x.shape, dt, dev, stream)
-    _same("out", out, x.shape, dt, dev)
+        out = _like(x, dt, dev, stream)
+    else:
+        _same("out", out, x.shape, dt, dev)
     _call(lib.kdn_gated_norm, dev, stream, DTYPES[dt], tokens, H, d, order, act, per_head,
           float(eps), xs, zs, _p(x), _p(weight), _p(gate), _p(out))
     return out
@@ -1287,8 +1303,8 @@ def gated_norm_backward(x, weight, d_y, gate=None, eps=1e-5, order="norm_gate", 
     without a gate) in x's dtype and dweight float32, or ``out``, such a dict."""
     lib = load()
     dt, dev, tokens, H, d, order, act, per_head, xs, zs = _heads(x, weight, gate, order, activation)
-    out = _outputs(out, (("dx", x.shape, dt, True), ("dgate", x.shape, dt, gate is not None),
-                         ("dweight", weight.shape, _f32, True)), dev, stream)
+    out = _outputs(out, (("dx", x, dt, True), ("dgate", x, dt, gate is not None),
+                         ("dweight", weight, _f32, True)), dev, stream)
     _same("d_y", d_y, x.shape, dt, dev)
     st = ctypes.c_int(0)
     n = lib.kdn_gated_norm_backward_workspace_size(tokens, H, d, per_head, ctypes.byref(st))
@@ -1308,9 +1324,7 @@ def _residual(x, residual, weight, scale):
     if residual.dim() < 1:
         raise ValueError("kdn: residual must be a tensor [.., D]")
     lead, D = residual.shape[:-1], residual.shape[-1]
-    tokens = 1
-    for n in lead:
-        tokens *= n
+    tokens = math.prod(lead)
     rs = _strided("residual", residual, lead, (D,), sdt, dev)
     xs = 0 if x is None else _strided("x", x, lead, (D,), dt, dev)
     _same("weight", weight, (D,), _f32, dev)
@@ -1336,8 +1350,8 @@ def residual_norm(x, residual, weight, scale=None, eps=1e-5, out=None, stream=No
     dt, sdt, dev, tokens, D, scale_n, xs, rs = _residual(x, residual, weight, scale)
     if x is None:
         raise TypeError("kdn: x must be a tensor")
-    y, h = out if out is not None else (_new(x.shape, dt, dev, stream),
-                                        _new(x.shape, sdt, dev, stream))
+    y, h = out if out is not None else (_like(x, dt, dev, stream),
+                                        _like(residual, sdt, dev, stream))
     for name, t, kind in (("y", y, dt), ("h", h, sdt)):
         if t is None:
             raise TypeError(f"kdn: {name} must be a tensor")
@@ -1359,11 +1373,11 @@ def residual_norm_backward(x, h, weight, d_y, d_h=None, scale=None, eps=1e-5, ou
         raise TypeError("kdn: d_y must be a tensor")
     if x is None:
         dt, _ = _dtype("d_y", d_y)
-    out = _outputs(out, (("dx", h.shape, dt, True), ("dresidual", h.shape, sdt, True),
-                         ("dweight", (D,), _f32, True),
+    _same("d_y", d_y, h.shape, dt, dev)
+    out = _outputs(out, (("dx", h if dt is sdt else d_y, dt, True), ("dresidual", h, sdt, True),
+                         ("dweight", weight, _f32, True),
                          ("dscale", (scale_n,), _f32, scale is not None and x is not None)),
                    dev, stream)
-    _same("d_y", d_y, h.shape, dt, dev)
     _same("d_h", d_h, h.shape, sdt, dev)
     st = ctypes.c_int(0)
     n = lib.kdn_residual_norm_backward_workspace_size(tokens, D, scale_n, ctypes.byref(st))
