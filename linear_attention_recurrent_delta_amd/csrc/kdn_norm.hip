@@ -16,7 +16,7 @@
 // gate's kind and whole rows known to the compiler; 91 without), and the parts' sums 5;
 // of the residual norm of 2500 x 1543 bf16 20 us and 4, where rows start on no boundary
 // and a row takes 256 threads of which 193 work; one token of 16 heads of 128 2 us of
-// the call's 11, which its launch takes.
+// the call's 9, which binding and launch take.
 #include "kdn_act.h"
 #include "kdn_norm.h"
 
