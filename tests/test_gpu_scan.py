@@ -346,6 +346,25 @@ def test_packed_gradients(dtype, S, G, lengths, behind, block):
     assert (d["dS0"][untouched] == 7).all()
 
 
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("S,G,C", [(16, 1, 80), (8, 5, 35), (32, 2, 70)])
+def test_gradients_of_many_sequences(dtype, S, G, C):
+    """Short sequences, dense and packed, many more than workgroups of a set of channels."""
+    B, T = 300, 5
+    args, kw = case((B, T), C, S, G, dtype, seed=S)
+    dense_grad(args, kw, randn((B, C, S), F32, 9), randn((B, T, C), dtype, 11), randn((B, C, S), F32, 10))
+    lengths = [(7 * i * i) % 23 for i in range(150)]
+    args, kw, t, pool, spans, live, slots, untouched, skip = packed(lengths, 7, 64, C, S, G, dtype)
+    S0, dS = randn((pool, C, S), F32, 2), randn((pool, C, S), F32, 3)
+    dy = randn((sum(lengths) + 7, C), dtype, 4)
+    dy[-7:] = math.nan
+    d = kdn.selective_scan_backward(*args, dy, S0=S0, dS_out=dS, tables=t, **kw)
+    check_grad(args, kw, S0, dy, dS, d, [spans[n] for n in live], slots)
+    for k in ("dx", "ddelta", "dz", "dB", "dC"):
+        assert not d[k][-7:].any() and not d[k][spans[skip]].any(), k
+    assert not d["dS0"][untouched].any()
+
+
 def test_gradient_against_differences():
     """The 64-bit gradient itself against central differences of the 64-bit form."""
     T, C, S, G = 5, 4, 8, 2
