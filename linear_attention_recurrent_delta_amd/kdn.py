@@ -1325,8 +1325,11 @@ def _residual(x, residual, weight, scale):
         raise ValueError("kdn: residual must be a tensor [.., D]")
     lead, D = residual.shape[:-1], residual.shape[-1]
     tokens = math.prod(lead)
-    rs = _strided("residual", residual, lead, (D,), sdt, dev)
-    xs = 0 if x is None else _strided("x", x, lead, (D,), dt, dev)
+    rs = 0 if residual.is_contiguous() else _strided("residual", residual, lead, (D,), sdt, dev)
+    xs = 0
+    if x is not None and not (x.shape == residual.shape and x.get_device() == dev.index and
+                              x.is_contiguous()):
+        xs = _strided("x", x, lead, (D,), dt, dev)
     _same("weight", weight, (D,), _f32, dev)
     if weight is None:
         raise TypeError("kdn: weight must be a tensor [D]")
@@ -1350,12 +1353,14 @@ def residual_norm(x, residual, weight, scale=None, eps=1e-5, out=None, stream=No
     dt, sdt, dev, tokens, D, scale_n, xs, rs = _residual(x, residual, weight, scale)
     if x is None:
         raise TypeError("kdn: x must be a tensor")
-    y, h = out if out is not None else (_like(x, dt, dev, stream),
-                                        _like(residual, sdt, dev, stream))
-    for name, t, kind in (("y", y, dt), ("h", h, sdt)):
-        if t is None:
-            raise TypeError(f"kdn: {name} must be a tensor")
-        _same(name, t, x.shape, kind, dev)
+    if out is None:
+        y, h = _like(x, dt, dev, stream), _like(residual, sdt, dev, stream)
+    else:
+        y, h = out
+        for name, t, kind in (("y", y, dt), ("h", h, sdt)):
+            if t is None:
+                raise TypeError(f"kdn: {name} must be a tensor")
+            _same(name, t, x.shape, kind, dev)
     _call(lib.kdn_residual_norm, dev, stream, DTYPES[dt], DTYPES[sdt], tokens, D, scale_n,
           float(eps), xs, rs, _p(x), _p(residual), _p(weight), _p(scale), _p(y), _p(h))
     return y, h
