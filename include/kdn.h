@@ -569,8 +569,9 @@ typedef enum kdn_activation {
  *   y           [tokens, C] dtype (output)
  *   state_out   shaped as state0 (output), or NULL (not wanted); may be exactly
  *               state0, must not overlap it otherwise
- * C below 2^26; sizes whose launches would have 2^32 work-items are refused
- * (none has with less than 2^35 values in whole tiles of 64 x 64).
+ * C below 2^26; sizes whose launches would have 2^32 work-items are refused: those of
+ * 2^24 tiles of 64 tokens of a sequence and 512 channels (float32: 256), with a tile more
+ * for each sequence or block and up to a quarter more for a packed batch.
  */
 kdn_status kdn_causal_conv(kdn_dtype dtype, int N, int T, int C, int W, kdn_activation act,
                            long long x_stride, const void *x, const float *weight,

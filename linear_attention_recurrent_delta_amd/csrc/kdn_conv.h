@@ -50,12 +50,32 @@ struct ConvDecodeParams {
     void *y;                // [N, C]
 };
 
-// Tokens of a workgroup's tile in the gradient kernel, whose 64 lanes take 8 bytes
-// of a row each.
-constexpr int CONV_GRAD_TILE = 64;
-inline long conv_tiles(const ConvParams &P, int tile) {
-    return P.block_offsets ? (long)P.nblocks * (((long)P.block + tile - 1) / tile)
-                           : (long)P.N * (((long)P.T + tile - 1) / tile);
+// Tokens of a workgroup's tile; channels of a lane (16 bytes of a row, gradients 8).
+constexpr int CONV_TILE = 64;
+inline int conv_vec(bool bf16, bool grad) { return (bf16 ? 8 : 4) / (grad ? 2 : 1); }
+
+// Tiles of a packed batch that are found by their number (kdn_conv.hip): blocks may end
+// with a part of a tile, so each adds at most one to the tiles before it.
+inline long conv_found_tiles(const ConvParams &P) {
+    return P.nblocks > 0 ? P.tokens / CONV_TILE + P.nblocks : 0;
+}
+// Tiles of a block where each block has room for as many as its length may need.
+inline long conv_block_tiles(const ConvParams &P) {
+    return ((long)P.block + CONV_TILE - 1) / CONV_TILE;
+}
+// Tiles of a launch.  `packed`: P.block and P.nblocks are the tables'.  Looking for a tile
+// costs a gradient workgroup two loads in front of each of its tiles, a tile without tokens
+// a workgroup or a round.  Room in every block and found, bf16, forward and gradients in us:
+//     sequences, tokens, channels, block      room / found
+//     37 of 590               6144    256         1.05        108  230    109  240
+//     256 of 1 to 511, 63569  4096    256         1.35        237  510    203  462
+//     256 of 1 to 31, 4225    4096    256         3.2          68  263     28   93
+//     37 of 590               6144  21888        34           265  523    105  211
+inline long conv_tiles(const ConvParams &P, bool packed) {
+    if (!packed)
+        return (long)P.N * (((long)P.T + CONV_TILE - 1) / CONV_TILE);
+    const long room = P.nblocks * conv_block_tiles(P), found = conv_found_tiles(P);
+    return 4 * room <= 5 * found ? room : found;
 }
 inline int conv_chunks(int C, int vec) { return (C + 64 * vec - 1) / (64 * vec); }
 

@@ -29,6 +29,38 @@ __device__ __forceinline__ Place place(int chunks) {
     return Place{(long)blockIdx.x / chunks, (int)(blockIdx.x % chunks)};
 }
 
+// Tile `id` of a batch: its block, and in t0 the tile's first token in it (a block without
+// tokens where there is no such tile).  sub > 0: tile id % sub of block id / sub.  sub 0:
+// tile j of block b has the number first / CONV_TILE + b + j, so that there are as many
+// numbers as tokens and blocks need, however long a block may be; the block is the last
+// whose first number is not behind id, which the wave's 64 lanes look for together (all of
+// them have to come here): 37 packed prompts (21830 tokens) of 6144 channels in a table of
+// one block a sequence 105 us, as with blocks of 256.
+__device__ __forceinline__ Block tile_block(const ConvParams &P, long id, int sub, int &t0) {
+    if (sub > 0) {
+        t0 = (int)(id % sub) * CONV_TILE;
+        return get_block(P, id / sub);
+    }
+    const int lane = threadIdx.x & (WAVE - 1);
+    // rows of the table that hold blocks; device data, so kept within the table
+    long lo = 0, hi = min(max(__builtin_amdgcn_readfirstlane(P.block_offsets[P.N]), 0), P.nblocks);
+    while (hi - lo > 1) {
+        const long step = (hi - lo + WAVE - 1) / WAVE, row = lo + lane * step;
+        const bool before = row < hi && P.blocks[4 * row] / CONV_TILE + row <= id;
+        const int n = __builtin_popcountll(__ballot(before));
+        lo += (n > 1 ? n - 1 : 0) * step;
+        hi = min(hi, lo + step);
+    }
+    Block B = get_block(P, lo);
+    const long t = B.count > 0 ? (id - B.first / CONV_TILE - lo) * CONV_TILE : 0;
+    t0 = 0;
+    if (t < 0 || t >= B.count)
+        B.count = 0;
+    else
+        t0 = (int)t;
+    return B;
+}
+
 // Rows of VEC channels of a lane, n of them there (the same in every lane).  WHOLE: rows of
 // whole pieces on their boundaries, through a descriptor that ends with the last row, so
 // that rows behind it read 0 and are not written without a branch; else by the pieces'
@@ -106,7 +138,8 @@ __device__ __forceinline__ void load_weights(const float *weight, const float *b
 template <typename T, int VEC, int W, int RT, bool WHOLE>
 __global__ __launch_bounds__(NT) void conv_kernel(ConvParams P, int chunks, int sub, long tiles) {
     constexpr bool FINE = sizeof(T) == 4;
-    constexpr int H = W - 1, TT = NW * RT;
+    constexpr int H = W - 1;
+    static_assert(NW * RT == CONV_TILE, "a workgroup's tokens");
     const int lane = threadIdx.x & (WAVE - 1);
     const Place at = place(chunks);
     const long c = ((long)at.chunk * WAVE + lane) * VEC;
@@ -125,8 +158,9 @@ __global__ __launch_bounds__(NT) void conv_kernel(ConvParams P, int chunks, int 
             state_out[slot * H * P.C + i] = state0 ? state0[slot * H * P.C + i] : from_f32<T>(0.f);
         return;
     }
-    const Block B = get_block(P, at.tile / sub);
-    const int t0 = (int)(at.tile % sub) * TT + wave_id() * RT;
+    int t0;
+    const Block B = tile_block(P, at.tile, sub, t0);
+    t0 += wave_id() * RT;
     if (t0 >= B.count || B.slot < 0 || c >= P.C)
         return;
     const bool start = B.index == 0 && t0 == 0;
@@ -238,7 +272,7 @@ template <typename T, int VEC, int W, bool WHOLE>
 __global__ __launch_bounds__(NT) void conv_grad_kernel(ConvParams P, int chunks, int sub,
                                                        long tiles) {
     constexpr bool FINE = sizeof(T) == 4;
-    constexpr int H = W - 1, RT = CONV_GRAD_TILE / NW;
+    constexpr int H = W - 1, RT = CONV_TILE / NW;
     const int lane = threadIdx.x & (WAVE - 1), wv = wave_id();
     const int chunk = blockIdx.x % chunks, part = blockIdx.x / chunks;
     const long c = ((long)chunk * WAVE + lane) * VEC;
@@ -253,10 +287,11 @@ __global__ __launch_bounds__(NT) void conv_grad_kernel(ConvParams P, int chunks,
             dw[j][e] = 0.f;
     if (live)
         load_weights<VEC, W>(P.weight, P.bias, c, nc, w, b);
-    for (long tile = part; tile < tiles && live; tile += P.parts) {
-        const Block B = get_block(P, tile / sub);
-        const int t0 = (int)(tile % sub) * CONV_GRAD_TILE + wv * RT;
-        if (t0 >= B.count)
+    for (long tile = part; tile < tiles; tile += P.parts) {
+        int t0;
+        const Block B = tile_block(P, tile, sub, t0);     // (every lane takes part in it)
+        t0 += wv * RT;
+        if (t0 >= B.count || !live)
             continue;
         typedef Lines<T, VEC, WHOLE> L;
         const int n = min(RT, B.count - t0);      // own tokens
@@ -427,25 +462,35 @@ bool whole(int C, long stride, int es, int bytes, std::initializer_list<const vo
     return ok;
 }
 
+// Blocks and tiles of a launch: of a dense batch a block is a tile.
+struct Tiles {
+    ConvParams P;
+    long n;
+    int sub;
+    explicit Tiles(const ConvParams &P_) : P(P_), n(conv_tiles(P_, P_.block_offsets)), sub(1) {
+        if (!P.block_offsets) {
+            P.block = CONV_TILE;
+            P.nblocks = (int)((P.T + CONV_TILE - 1l) / CONV_TILE);
+        } else {
+            sub = n == P.nblocks * conv_block_tiles(P) ? (int)conv_block_tiles(P) : 0;
+        }
+    }
+};
+
 template <typename T, int VEC, int W>
 hipError_t launch_conv_fwd_t(const ConvParams &P, hipStream_t st) {
     // tokens of a lane (8, 16 and 32: 37 packed prompts 122, 121 and 125 us)
-    constexpr int RT = 16, TT = NW * RT;
-    const int chunks = conv_chunks(P.C, VEC), sub = P.block_offsets ? (int)((P.block + TT - 1l) / TT) : 1;
-    ConvParams Q = P;
-    if (!P.block_offsets) {          // dense: a block is a tile
-        Q.block = TT;
-        Q.nblocks = (int)((P.T + TT - 1l) / TT);
-    }
-    const long tiles = conv_tiles(Q, TT);
+    constexpr int RT = CONV_TILE / NW;
+    const int chunks = conv_chunks(P.C, VEC);
+    const Tiles q(P);
     const long empty = P.state_out && P.state_out != P.state0 && (P.block_offsets || P.T == 0) ? P.N : 0;
-    if (tiles + empty == 0)
+    if (q.n + empty == 0)
         return hipSuccess;
-    const dim3 grid((unsigned)((tiles + empty) * chunks)), block(NT);
+    const dim3 grid((unsigned)((q.n + empty) * chunks)), block(NT);
     if (whole(P.C, P.x_stride, sizeof(T), VEC * sizeof(T), {P.x, P.y, P.state0, P.state_out}))
-        hipLaunchKernelGGL((conv_kernel<T, VEC, W, RT, true>), grid, block, 0, st, Q, chunks, sub, tiles);
+        hipLaunchKernelGGL((conv_kernel<T, VEC, W, RT, true>), grid, block, 0, st, q.P, chunks, q.sub, q.n);
     else
-        hipLaunchKernelGGL((conv_kernel<T, VEC, W, RT, false>), grid, block, 0, st, Q, chunks, sub, tiles);
+        hipLaunchKernelGGL((conv_kernel<T, VEC, W, RT, false>), grid, block, 0, st, q.P, chunks, q.sub, q.n);
     return hipGetLastError();
 }
 
@@ -459,20 +504,14 @@ hipError_t launch_conv_decode_t(const ConvDecodeParams &P, hipStream_t st) {
 
 template <typename T, int VEC, int W>
 hipError_t launch_conv_grad_t(const ConvParams &P, hipStream_t st) {
-    constexpr int TT = CONV_GRAD_TILE;
-    const int chunks = conv_chunks(P.C, VEC), sub = P.block_offsets ? (int)((P.block + TT - 1l) / TT) : 1;
-    ConvParams Q = P;
-    if (!P.block_offsets) {
-        Q.block = TT;
-        Q.nblocks = (int)((P.T + TT - 1l) / TT);
-    }
-    const long tiles = conv_tiles(Q, TT);
+    const int chunks = conv_chunks(P.C, VEC);
+    const Tiles q(P);
     if (P.parts > 0) {
         const dim3 grid((unsigned)(chunks * (long)P.parts)), block(NT);
         if (whole(P.C, P.x_stride, sizeof(T), VEC * sizeof(T), {P.x, P.d_y, P.dx, P.state0}))
-            hipLaunchKernelGGL((conv_grad_kernel<T, VEC, W, true>), grid, block, 0, st, Q, chunks, sub, tiles);
+            hipLaunchKernelGGL((conv_grad_kernel<T, VEC, W, true>), grid, block, 0, st, q.P, chunks, q.sub, q.n);
         else
-            hipLaunchKernelGGL((conv_grad_kernel<T, VEC, W, false>), grid, block, 0, st, Q, chunks, sub, tiles);
+            hipLaunchKernelGGL((conv_grad_kernel<T, VEC, W, false>), grid, block, 0, st, q.P, chunks, q.sub, q.n);
         const hipError_t e = hipGetLastError();
         if (e != hipSuccess)
             return e;
@@ -480,7 +519,7 @@ hipError_t launch_conv_grad_t(const ConvParams &P, hipStream_t st) {
     const long wide = min(((long)(W + 1) * P.C + 15) / 16, 65536l);
     const long empty = P.dstate0 && (P.block_offsets || P.T == 0) ? P.N : 0;
     hipLaunchKernelGGL((conv_sum_kernel<T>), dim3((unsigned)(wide + TAIL_WGS + empty)),
-                       dim3(NT), 0, st, Q, wide);
+                       dim3(NT), 0, st, P, wide);
     return hipGetLastError();
 }
 

@@ -33,12 +33,6 @@ kdn_status conv_shape(kdn::ConvParams &P, int dtype, int N, int T, int C, int W,
         return st;
     if (C >= (1 << 26) || P.pool * (W - 1) >= (1LL << 32))
         return KDN_ERR_SHAPE;
-    // tiles and, behind them, sequences, for the narrowest rows a lane takes
-    const long long tiles = packed ? (long long)P.nblocks * ((P.block + 63LL) / 64)
-                                   : (long long)N * ((T + 63LL) / 64);
-    const long long chunks = (C + 63) / 64;
-    if (chunks > 0 && tiles + N >= (1LL << 24) / chunks)
-        return KDN_ERR_SHAPE;
     return KDN_OK;
 }
 
@@ -48,9 +42,8 @@ kdn_status conv_shape(kdn::ConvParams &P, int dtype, int N, int T, int C, int W,
 // channels in float32 52, 52 and 51.
 constexpr int GRAD_WGS = 512;
 int grad_parts(const kdn::ConvParams &P, bool packed) {
-    const long long tiles = packed ? (long long)P.nblocks * ((P.block + 63LL) / 64)
-                                   : (long long)P.N * ((P.T + 63LL) / 64);
-    const int chunks = std::max(1, kdn::conv_chunks(P.C, P.bf16 ? 4 : 2));
+    const long long tiles = kdn::conv_tiles(P, packed);
+    const int chunks = std::max(1, kdn::conv_chunks(P.C, kdn::conv_vec(P.bf16, true)));
     return (int)std::min(tiles, (long long)std::max(1, GRAD_WGS / chunks));
 }
 
@@ -65,6 +58,10 @@ kdn_status kdn_causal_conv(kdn_dtype dtype, int N, int T, int C, int W, kdn_acti
     kdn::ConvParams P;
     if (kdn_status st = conv_shape(P, dtype, N, T, C, W, act, x_stride, packed))
         return st;
+    // tiles and, behind them, sequences
+    if (!launchable((kdn::conv_tiles(P, packed != nullptr) + N) *
+                    kdn::conv_chunks(C, kdn::conv_vec(P.bf16, false)), 256))
+        return KDN_ERR_SHAPE;
     const long long es = P.bf16 ? 2 : 4, tok = P.tokens;
     if (tok * C > 0 && (!x || !weight || !y))
         return KDN_ERR_NULL;
@@ -101,7 +98,8 @@ kdn_status kdn_causal_conv_decode(kdn_dtype dtype, int N, int C, int W, kdn_acti
     kdn::ConvParams L;
     if (kdn_status st = conv_shape(L, dtype, N, 1, C, W, act, x_stride, nullptr))
         return st;
-    if (pool < 0 || (!slots && pool < N) || (long long)pool * (W - 1) >= (1LL << 32))
+    if (pool < 0 || (!slots && pool < N) || (long long)pool * (W - 1) >= (1LL << 32) ||
+        !launchable((long long)N * kdn::conv_chunks(C, kdn::conv_vec(L.bf16, false)), 64))
         return KDN_ERR_SHAPE;
     const long long es = L.bf16 ? 2 : 4, n = (long long)N * C;
     if (n > 0 && (!x || !weight || !y || (pool > 0 && !state)))

@@ -1,0 +1,48 @@
+"""Sizes that the operators around a recurrence take and refuse, on the host: what is
+counted is what a call launches.  Calls go through the C ABI with an input missing, so that
+one whose sizes are taken ends at that."""
+import ctypes
+
+import pytest
+
+from linear_attention_recurrent_delta_amd import kdn
+from test_around_host import conv, decode, lib  # noqa: F401
+from test_linear_host import BF16, ENULL, ESHAPE, F32, OK, packed
+
+# sequences, tokens, channels of packed batches
+BATCHES = [(256, 65536, 4096), (512, 65536, 6144), (1024, 32768, 4096), (128, 131072, 6144), (256, 131072, 6144),
+           (1000, 100000, 6144), (37, 21815, 6144), (1, 1, 1), (4096, 4096, 8192)]
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("N,tokens,C", BATCHES)
+def test_conv_takes_the_tables_of_a_scan(lib, dtype, N, tokens, C):
+    """Tables with blocks of any length, those of selective_block among them."""
+    st = ctypes.c_int(0)
+    for block in (64, 256, lib.kdn_selective_block(tokens, N, C, 16), 1 << 20, (1 << 31) - 64):
+        pk = packed(tokens, block, pool=N, N=N)
+        size = lib.kdn_causal_conv_backward_workspace_size(dtype, N, 0, C, 4, pk, ctypes.byref(st))
+        assert st.value == OK and size > 0, block
+        assert conv(lib, dtype=dtype, N=N, T=0, C=C, pk=pk, x=None) == ENULL, block
+        # parts of what tokens and sequences need, not of what the blocks have room for
+        chunks = -(-C // (256 if dtype == BF16 else 128))
+        assert size <= 4 * 5 * C * min(max(1, 512 // chunks), tokens // 64 + N), block
+
+
+def test_conv_counts_what_it_launches(lib):
+    """2^24 workgroups: tiles of 64 tokens and 512 channels (float32: 256), and one for each sequence."""
+    sizes = lambda want, **kw: conv(lib, x=None, **kw) == want  # noqa: E731
+    assert sizes(ENULL, N=1, T=64 * (1 << 12), C=512 * 4000) and sizes(ESHAPE, N=1, T=64 * (1 << 12), C=512 * 4096)
+    assert sizes(ENULL, dtype=F32, N=1, T=64 * (1 << 12), C=256 * 4000) and sizes(ESHAPE, dtype=F32, N=1, T=64 * (1 << 12), C=256 * 4096)
+    assert sizes(ENULL, N=(1 << 23) - 1, T=1, C=512) and sizes(ESHAPE, N=1 << 23, T=1, C=512)
+    assert sizes(ENULL, N=(1 << 23) - 1, T=64, C=512) and sizes(ESHAPE, N=(1 << 23) - 1, T=65, C=512)
+    assert decode(lib, N=1 << 16, C=16384, x=None, pool=1 << 16) == ENULL
+    assert decode(lib, N=1 << 20, C=512 * 64, x=None) == ESHAPE
+
+
+def test_an_empty_table_has_no_tiles(lib):
+    """Tokens and no sequence: nothing to look for."""
+    st = ctypes.c_int(0)
+    for block in (64, 1 << 20):
+        pk = kdn.Packed(1000, block, 0, 0, None, None, None)
+        assert lib.kdn_causal_conv_backward_workspace_size(BF16, 0, 0, 64, 4, pk, ctypes.byref(st)) == 0 and st.value == OK

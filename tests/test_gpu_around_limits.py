@@ -1,0 +1,152 @@
+"""The operators around a recurrence on the GPU at the ends of their ranges: tables of any
+block length, sums over many tokens, rounds of the norms' gradients, sizes of nothing."""
+import math
+
+import pytest
+import torch
+
+import around_ref as ref
+import test_gpu_conv as tc
+import test_gpu_scan as ts
+from linear_attention_recurrent_delta_amd import kdn
+from test_gpu_conv import BF, F32, gen, i32, randn
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _lib():
+    assert torch.cuda.is_available()
+    kdn.ensure_built()
+
+
+def uneven(N, most, seed):
+    """Lengths with none, one, a tile and its neighbours among them."""
+    lengths = torch.randint(0, most, (N,), generator=gen(seed)).tolist()
+    for i, n in enumerate((0, 1, 64, 63, 65, 0, 128)):
+        lengths[(7 * i + 3) % N] = n
+    return lengths
+
+
+# sequences, longest, channels: one search step, two and three; one sequence; short ones only
+TABLES = [(1, 300, 24), (40, 200, 520), (64, 130, 40), (65, 130, 40), (300, 150, 72), (4500, 4, 8)]
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("N,most,C", TABLES)
+def test_conv_on_tables_of_any_block(dtype, N, most, C):
+    """One batch on tables of many block lengths, a scan's among them: the same bits, the
+    pool's other states, skipped sequences and rows behind the last left as they were."""
+    lengths = uneven(N, most, N) if N > 1 else [most]
+    behind, W = 5, 4
+    total = sum(lengths) + behind
+    slots = torch.randperm(N + 3, generator=gen(N)).tolist()[:N]
+    given = [-1 if n % 11 == 10 else s for n, s in enumerate(slots)]
+    x, (w, b), S0 = randn((total, C), dtype, 1), tc.params(C, W), randn((N + 3, W - 1, C), dtype, 2)
+    dy, dS = randn((total, C), dtype, 3), randn((N + 3, W - 1, C), dtype, 4)
+    x[-behind:], dy[-behind:] = math.nan, math.nan
+    ends = torch.tensor(lengths).cumsum(0).tolist()
+    first = None
+    for block in (64, 128, 4096, kdn.selective_block(total, N, C, 16), kdn.selective_block(total, N, 8192, 16), 1 << 20,
+                  (1 << 31) - 64):
+        t = kdn.sequence_tables(i32(lengths), total, block, slots=i32(given))
+        y, S = torch.full((total, C), 7.0, dtype=dtype, device="cuda"), S0.clone()
+        kdn.causal_conv(x, w, b, state0=S0, tables=t, out=(y, S))
+        keep, y2 = S0.clone(), torch.full_like(y, 7.0)
+        kdn.causal_conv(x, w, b, state0=keep, tables=t, out=(y2, keep))
+        d = kdn.causal_conv_backward(x, w, dy, b, state0=S0, dstate_out=dS, tables=t)
+        assert torch.equal(y, y2) and torch.equal(S, keep), block
+        if first is None:
+            first = y, S, d
+            on = [n for n in range(N) if given[n] >= 0]
+            some = sorted(set(on[:12] + on[::max(1, N // 12)] + on[-4:]))
+            spans = [slice(ends[n] - lengths[n], ends[n]) for n in some]
+            tc.check_forward(x, w, b, S0, "silu", y, S, spans, [slots[n] for n in some])
+            off = [n for n in range(N) if given[n] < 0]
+            for n in off:
+                assert (y[ends[n] - lengths[n]:ends[n]] == 7).all()
+            assert (y[-behind:] == 7).all() and not d["dx"][-behind:].any()
+            if N <= 300:
+                tc.check_grad(x, w, b, S0, dy, dS, "silu", d, [slice(ends[n] - lengths[n], ends[n]) for n in on],
+                              [slots[n] for n in on])
+            continue
+        assert torch.equal(y, first[0]) and torch.equal(S, first[1]), block
+        for k in ("dx", "dstate0"):
+            assert torch.equal(d[k], first[2][k]), (block, k)
+        if N <= 300:
+            tc.check_grad(x, w, b, S0, dy, dS, "silu", d, [slice(ends[n] - lengths[n], ends[n]) for n in on],
+                          [slots[n] for n in on])
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+def test_conv_and_scan_on_one_table(dtype):
+    """The table of a scan of many channels, whose block is the whole batch, for both."""
+    N, C, S = 96, 4096, 16
+    lengths = uneven(N, 40, 5)
+    total = sum(lengths)
+    block = kdn.selective_block(total, N, C, S)
+    assert block >= total
+    t = kdn.sequence_tables(i32(lengths), total, block, slots=i32(list(range(N))[::-1]))
+    args, kw = ts.case((total,), C, S, 1, dtype, seed=1)
+    w, b = tc.params(C, 4)
+    conv0, S0 = randn((N, 3, C), dtype, 2), randn((N, C, S), F32, 3)
+    u, last = kdn.causal_conv(args[0], w, b, state0=conv0, tables=t, out=(torch.empty_like(args[0]), torch.empty_like(conv0)))
+    y, Sn = kdn.selective_scan(u, *args[1:], S0=S0, tables=t, out=(torch.empty_like(u), torch.empty_like(S0)), **kw)
+    ends = torch.tensor(lengths).cumsum(0).tolist()
+    some = [n for n in range(0, N, 9)]
+    spans, slots = [slice(ends[n] - lengths[n], ends[n]) for n in some], [N - 1 - n for n in some]
+    tc.check_forward(args[0], w, b, conv0, "silu", u, last, spans, slots)
+    ts.check((u,) + args[1:], kw, S0, y, Sn, spans, slots)
+
+
+@pytest.mark.parametrize("block", [64, 1 << 20])
+def test_conv_of_no_sequence(block):
+    """Rows and no sequence: outputs left as they were, gradients zero."""
+    x, (w, b) = torch.full((700, 40), math.nan, device="cuda"), tc.params(40, 4)
+    t = kdn.sequence_tables(torch.empty(0, dtype=torch.int32, device="cuda"), 700, block)
+    y = torch.full_like(x, 7.0)
+    kdn.causal_conv(x, w, b, tables=t, out=(y, None))
+    assert (y == 7).all()
+    d = kdn.causal_conv_backward(x, w, x, b, tables=t)
+    assert not d["dx"].any() and not d["dweight"].any() and not d["dbias"].any()
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+def test_captured_conv_on_a_long_block(dtype):
+    """A captured convolution finds its tiles in tables that change between the replays."""
+    N, C, cap = 70, 72, 3000
+    x, (w, b), dy = randn((cap, C), dtype, 1), tc.params(C, 4), randn((cap, C), dtype, 2)
+    lengths, state = i32([1] * N), randn((N, 3, C), dtype, 3)
+    t = kdn.sequence_tables(lengths, cap, 1 << 20)
+    y, S = torch.zeros_like(x), torch.zeros_like(state)
+    d = dict(dx=torch.zeros_like(x), dweight=torch.zeros_like(w), dbias=torch.zeros_like(b), dstate0=torch.zeros_like(state))
+    ws = torch.empty(64 << 20, dtype=torch.uint8, device="cuda")
+
+    def step():
+        kdn.sequence_tables(lengths, cap, 1 << 20, out=t)
+        kdn.causal_conv(x, w, b, state0=state, tables=t, out=(y, S))
+        kdn.causal_conv_backward(x, w, dy, b, state0=state, tables=t, out=d, workspace=ws)
+
+    side = torch.cuda.Stream()
+    with torch.cuda.stream(side):
+        step()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        step()
+    flat = [y, S] + list(d.values())
+    for ln in ([0] * N, [cap] + [0] * (N - 1), [(5 * i * i) % 43 for i in range(N)], [0] * (N - 1) + [129]):
+        lengths.copy_(i32(ln))
+        for v in flat:
+            v.zero_()
+        step()
+        torch.cuda.synchronize()
+        want = [v.clone() for v in flat]
+        for _ in range(2):
+            for v in flat:
+                v.zero_()
+            ws.fill_(255)
+            graph.replay()
+            torch.cuda.synchronize()
+            for a, c in zip(flat, want):
+                assert torch.equal(a, c)
