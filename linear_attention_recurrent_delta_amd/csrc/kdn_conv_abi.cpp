@@ -39,12 +39,20 @@ kdn_status conv_shape(kdn::ConvParams &P, int dtype, int N, int T, int C, int W,
 // Parts that the sums over tokens are made in: as many workgroups as run at once
 // (two a CU, by their registers), each over all the tiles it takes.  With 256, 512 and
 // 1024 of them: B4 T4096 C2048 bf16 74, 56 and 59 us, 11 packed sequences of 1030
-// channels in float32 52, 52 and 51.
-constexpr int GRAD_WGS = 512;
-int grad_parts(const kdn::ConvParams &P, bool packed) {
+// channels in float32 52, 52 and 51.  A lane adds 16 tokens of a tile in float32: from
+// PART_TILES tiles a part on there are twice, three times .. as many parts, so that no sum
+// is a chain of more than 512 of them, however long the sequences are.
+constexpr int GRAD_WGS = 512, PART_TILES = 32;
+long long grad_parts(const kdn::ConvParams &P, bool packed) {
     const long long tiles = kdn::conv_tiles(P, packed);
     const int chunks = std::max(1, kdn::conv_chunks(P.C, kdn::conv_vec(P.bf16, true)));
-    return (int)std::min(tiles, (long long)std::max(1, GRAD_WGS / chunks));
+    const long long once = std::max(1, GRAD_WGS / chunks);
+    return std::min(tiles, once * std::max(1LL, (tiles - 1) / (once * PART_TILES) + 1));
+}
+// The gradients' launches: the parts' and the sums' with what follows them.
+bool grad_launchable(const kdn::ConvParams &P, bool packed) {
+    return launchable(grad_parts(P, packed) * kdn::conv_chunks(P.C, kdn::conv_vec(P.bf16, true)), 256) &&
+           launchable(65536LL + 64 + P.N, 256);
 }
 
 }  // namespace
@@ -130,10 +138,12 @@ unsigned long long kdn_causal_conv_backward_workspace_size(kdn_dtype dtype, int 
                                                            int W, const kdn_packed *packed,
                                                            kdn_status *status) {
     kdn::ConvParams P;
-    const kdn_status st = conv_shape(P, dtype, N, T, C, W, KDN_ACT_SILU, 0, packed);
+    kdn_status st = conv_shape(P, dtype, N, T, C, W, KDN_ACT_SILU, 0, packed);
+    if (st == KDN_OK && !grad_launchable(P, packed != nullptr))
+        st = KDN_ERR_SHAPE;
     if (status)
         *status = st;
-    return st == KDN_OK ? 4ull * grad_parts(P, packed != nullptr) * (W + 1) * C : 0;
+    return st == KDN_OK ? 4ull * (unsigned long long)grad_parts(P, packed != nullptr) * (W + 1) * C : 0;
 }
 
 kdn_status kdn_causal_conv_backward(kdn_dtype dtype, int N, int T, int C, int W,
@@ -146,7 +156,7 @@ kdn_status kdn_causal_conv_backward(kdn_dtype dtype, int N, int T, int C, int W,
     kdn::ConvParams P;
     if (kdn_status st = conv_shape(P, dtype, N, T, C, W, act, x_stride, packed))
         return st;
-    if (!launchable(65536LL + 64 + N, 256))
+    if (!grad_launchable(P, packed != nullptr))
         return KDN_ERR_SHAPE;
     const long long es = P.bf16 ? 2 : 4, tok = P.tokens;
     if ((tok * C > 0 && (!x || !d_y || !dx)) || (C > 0 && (!weight || !dweight)))
@@ -175,7 +185,7 @@ kdn_status kdn_causal_conv_backward(kdn_dtype dtype, int N, int T, int C, int W,
                           {dstate0, n_s}};
     if (clash(outs, 4, ins, 9))
         return KDN_ERR_ALIAS;
-    P.parts = grad_parts(P, packed != nullptr);
+    P.parts = (int)grad_parts(P, packed != nullptr);
     const long long n_ws = 4LL * P.parts * (W + 1) * C;
     if (n_ws > 0) {
         if (!workspace || workspace_bytes < (unsigned long long)n_ws)

@@ -25,8 +25,8 @@ def test_conv_takes_the_tables_of_a_scan(lib, dtype, N, tokens, C):
         assert st.value == OK and size > 0, block
         assert conv(lib, dtype=dtype, N=N, T=0, C=C, pk=pk, x=None) == ENULL, block
         # parts of what tokens and sequences need, not of what the blocks have room for
-        chunks = -(-C // (256 if dtype == BF16 else 128))
-        assert size <= 4 * 5 * C * min(max(1, 512 // chunks), tokens // 64 + N), block
+        once, tiles = max(1, 512 // -(-C // (256 if dtype == BF16 else 128))), 1.25 * (tokens // 64 + N + tokens // block)
+        assert size <= 4 * 5 * C * min(once * (1 + tiles // (32 * once)), tiles), block
 
 
 def test_conv_counts_what_it_launches(lib):
@@ -38,6 +38,13 @@ def test_conv_counts_what_it_launches(lib):
     assert sizes(ENULL, N=(1 << 23) - 1, T=64, C=512) and sizes(ESHAPE, N=(1 << 23) - 1, T=65, C=512)
     assert decode(lib, N=1 << 16, C=16384, x=None, pool=1 << 16) == ENULL
     assert decode(lib, N=1 << 20, C=512 * 64, x=None) == ESHAPE
+
+
+def test_conv_sums_in_more_parts_of_many_tokens(lib):
+    """32 tiles of 64 tokens a part at most, in whole rounds of the workgroups that run at once."""
+    size = lambda T, C: lib.kdn_causal_conv_backward_workspace_size(BF16, 1, T, C, 4, None, None) // (4 * 5 * C)  # noqa: E731
+    assert size(64 * 1024 - 1, 4096) == size(64 * 1024, 4096) == 32 and size(64 * 1024 + 1, 4096) == 64
+    assert size(1 << 20, 6144) == 21 * 25 and size(1 << 20, 1 << 18) == 512 and size(1 << 20, 64) == 512
 
 
 def test_an_empty_table_has_no_tiles(lib):

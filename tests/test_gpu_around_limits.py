@@ -150,3 +150,29 @@ def test_captured_conv_on_a_long_block(dtype):
             torch.cuda.synchronize()
             for a, c in zip(flat, want):
                 assert torch.equal(a, c)
+
+
+def spike(shape, rest, dtype=F32):
+    """Values that all count in a sum, behind one that hides each of them from a float32
+    register: what a long chain of such sums loses is `rest` a step."""
+    x = torch.full(shape, rest, dtype=dtype, device="cuda")
+    x[0] = 2.0 ** 24
+    return x
+
+
+def column_sums(x):
+    return sum(part.double().sum(0) for part in x.split(4096))
+
+
+def test_conv_sums_over_many_tokens():
+    """dweight and dbias over 768 tiles of a few wide parts.  A lane adds 16 tokens of each of at
+    most 32 tiles in float32, then four waves' sums are added, all else is 64 bits, and the
+    result is rounded: 517 roundings of the sum of absolute values at most."""
+    T, C = 64 * 768, 8192
+    x, dy, w, b = torch.ones(1, T, C, device="cuda"), spike((T, C), 0.9), torch.zeros(C, 2, device="cuda"), torch.zeros(C, device="cuda")
+    d = kdn.causal_conv_backward(x, w, dy[None], b, activation=None)
+    want = column_sums(dy)
+    for got in (d["dbias"], d["dweight"][:, 1]):
+        off = (got.double() - want).abs().max().item() / want.max().item() / ref.U
+        print(f"    {off:.0f} roundings", flush=True)
+        assert off <= 517
