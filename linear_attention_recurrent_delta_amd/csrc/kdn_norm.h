@@ -28,8 +28,8 @@ struct GatedNormParams {
     const void *d_y;
     void *dx, *dz;
     float *dweight;
-    float *ws;              // [parts][heads of weight][d]
-    int parts;
+    float *ws;              // [parts][segs][heads of weight][d]
+    int parts, segs, seg_rounds;    // workgroups; sums of each, over so many rounds of rows
 };
 
 struct ResidualNormParams {
@@ -56,6 +56,11 @@ struct ResidualNormParams {
 // bf16 72, 71 and 73 us, 98304 x 192 float32 by head 91, 82 and 84; residual 2500 x 1543
 // bf16 30, 23 and 34, 16384 x 2048 64, 67 and 71.
 constexpr int NORM_PARTS = 1024, RESIDUAL_PARTS = 512;
+// Rows of a column that a thread adds in float32: behind them a workgroup writes its sums
+// and begins anew.  (More parts in their place let workgroups that run at once work on rows
+// apart from each other: 131072 x 32 heads of 128 bf16, weight by head, 1262 us where it
+// is 1177.)
+constexpr int SEG_ROUNDS = 256;
 
 // Threads of a row of n elements: one for each 16 bytes, a power of two, up to a
 // whole workgroup.

@@ -287,93 +287,98 @@ __global__ __launch_bounds__(NT_MAX) void gated_norm_grad_kernel(GatedNormParams
         ws[i].zero();
         if (piece.there)
             piece.load(ws[i], w);
-#pragma unroll
-        for (int e = 0; e < VEC; ++e)
-            dw[i][e] = 0.f;
     }
     // the row's token and head, and the steps of both (a division once a row would cost a
     // tenth of the row's work)
     unsigned row = blockIdx.x * slots + L.slot, t = row / heads, h = row - t * heads;
     const unsigned dt = step / heads, dh = step - dt * heads;
     int buf = 0;
-    // the same number of rounds for every thread: they meet in row_sums
-    for (long first = (long)blockIdx.x * slots; first < rows; first += step, buf ^= 1) {
-        const bool in = row < rows;
-        const T *x = static_cast<const T *>(P.x) + t * P.x_stride + (long)(head + h) * P.d;
-        const T *z = static_cast<const T *>(P.z) + t * P.z_stride + (long)(head + h) * P.d;
-        const long out = ((long)t * P.H + head + h) * P.d;
-        const T *dy = static_cast<const T *>(P.d_y) + out;
-        Pack<T, VEC> xs[IT], zs[IT], gs[IT];
+    long first = (long)blockIdx.x * slots;
+    for (int seg = 0; seg < P.segs; ++seg) {
 #pragma unroll
-        for (int i = 0; i < IT; ++i) {
-            const Piece<VEC, FULL> piece(L, i, P.d);
-            xs[i].zero();
-            zs[i].zero();
-            gs[i].zero();
-            if (in && piece.there) {
-                piece.load(xs[i], x);
-                piece.load(gs[i], dy);
-                if (gate.there)
-                    piece.load(zs[i], z);
-            }
-        }
-        double sums[2] = {0., 0.};       // of u^2 and of t u
+        for (int i = 0; i < IT; ++i)
 #pragma unroll
-        for (int i = 0; i < IT; ++i) {
-            const Piece<VEC, FULL> piece(L, i, P.d);
+            for (int e = 0; e < VEC; ++e)
+                dw[i][e] = 0.f;
+        // the same number of rounds for every thread: they meet in row_sums
+        for (int k = 0; k < P.seg_rounds && first < rows; ++k, first += step, buf ^= 1) {
+            const bool in = row < rows;
+            const T *x = static_cast<const T *>(P.x) + t * P.x_stride + (long)(head + h) * P.d;
+            const T *z = static_cast<const T *>(P.z) + t * P.z_stride + (long)(head + h) * P.d;
+            const long out = ((long)t * P.H + head + h) * P.d;
+            const T *dy = static_cast<const T *>(P.d_y) + out;
+            Pack<T, VEC> xs[IT], zs[IT], gs[IT];
 #pragma unroll
-            for (int e = 0; e < VEC; ++e) {
-                float u = xs[i].get(e), dn = gs[i].get(e);
-                if (gate.there) {
-                    const float a = act_f32<FINE>(gate.act, zs[i].get(e));
-                    u = gate.first ? u * a : u;
-                    dn = gate.first ? dn : dn * a;
+            for (int i = 0; i < IT; ++i) {
+                const Piece<VEC, FULL> piece(L, i, P.d);
+                xs[i].zero();
+                zs[i].zero();
+                gs[i].zero();
+                if (in && piece.there) {
+                    piece.load(xs[i], x);
+                    piece.load(gs[i], dy);
+                    if (gate.there)
+                        piece.load(zs[i], z);
                 }
-                u = piece.own(e) ? u : 0.f;
-                dn = piece.own(e) ? dn * ws[i].get(e) : 0.f;
-                sums[0] = fma((double)u, (double)u, sums[0]);
-                sums[1] = fma((double)dn, (double)u, sums[1]);
             }
-        }
-        row_sums(sums, tpr, lds[buf]);
-        const float r = inv_sqrt<FINE>(sums[0] * P.inv_d + (double)P.eps);
-        // mean(t n)
-        const float m = (float)(sums[1] * (double)r * P.inv_d);
+            double sums[2] = {0., 0.};       // of u^2 and of t u
 #pragma unroll
-        for (int i = 0; i < IT; ++i) {
-            Pack<T, VEC> dx, dz;
-            const Piece<VEC, FULL> piece(L, i, P.d);
+            for (int i = 0; i < IT; ++i) {
+                const Piece<VEC, FULL> piece(L, i, P.d);
 #pragma unroll
-            for (int e = 0; e < VEC; ++e) {
-                const float xe = xs[i].get(e), ge = gs[i].get(e), we = ws[i].get(e);
-                float a = 1.f, da = 0.f;
-                if (gate.there)
-                    act_grad<FINE>(gate.act, zs[i].get(e), a, da);
-                const float n = (gate.first ? xe * a : xe) * r;
-                const float dn = gate.first ? ge : ge * a;
-                const float du = r * (dn * we - n * m);
-                // (what lies behind the rows and the row is zero; a piece's elements that are not
-                // its own are left out of the columns' sums)
-                dw[i][e] = fmaf(dn, n, dw[i][e]);
-                dx.set(e, gate.first ? du * a : du);
-                dz.set(e, gate.first ? du * xe * da : ge * n * we * da);
+                for (int e = 0; e < VEC; ++e) {
+                    float u = xs[i].get(e), dn = gs[i].get(e);
+                    if (gate.there) {
+                        const float a = act_f32<FINE>(gate.act, zs[i].get(e));
+                        u = gate.first ? u * a : u;
+                        dn = gate.first ? dn : dn * a;
+                    }
+                    u = piece.own(e) ? u : 0.f;
+                    dn = piece.own(e) ? dn * ws[i].get(e) : 0.f;
+                    sums[0] = fma((double)u, (double)u, sums[0]);
+                    sums[1] = fma((double)dn, (double)u, sums[1]);
+                }
             }
-            if (in && piece.there) {
-                piece.store(dx, static_cast<T *>(P.dx) + out);
-                if (gate.there)
-                    piece.store(dz, static_cast<T *>(P.dz) + out);
+            row_sums(sums, tpr, lds[buf]);
+            const float r = inv_sqrt<FINE>(sums[0] * P.inv_d + (double)P.eps);
+            // mean(t n)
+            const float m = (float)(sums[1] * (double)r * P.inv_d);
+#pragma unroll
+            for (int i = 0; i < IT; ++i) {
+                Pack<T, VEC> dx, dz;
+                const Piece<VEC, FULL> piece(L, i, P.d);
+#pragma unroll
+                for (int e = 0; e < VEC; ++e) {
+                    const float xe = xs[i].get(e), ge = gs[i].get(e), we = ws[i].get(e);
+                    float a = 1.f, da = 0.f;
+                    if (gate.there)
+                        act_grad<FINE>(gate.act, zs[i].get(e), a, da);
+                    const float n = (gate.first ? xe * a : xe) * r;
+                    const float dn = gate.first ? ge : ge * a;
+                    const float du = r * (dn * we - n * m);
+                    // (what lies behind the rows and the row is zero; a piece's elements that are not
+                    // its own are left out of the columns' sums)
+                    dw[i][e] = fmaf(dn, n, dw[i][e]);
+                    dx.set(e, gate.first ? du * a : du);
+                    dz.set(e, gate.first ? du * xe * da : ge * n * we * da);
+                }
+                if (in && piece.there) {
+                    piece.store(dx, static_cast<T *>(P.dx) + out);
+                    if (gate.there)
+                        piece.store(dz, static_cast<T *>(P.dz) + out);
+                }
+            }
+            row += step;
+            t += dt;
+            h += dh;
+            if (h >= heads) {
+                h -= heads;
+                ++t;
             }
         }
-        row += step;
-        t += dt;
-        h += dh;
-        if (h >= heads) {
-            h -= heads;
-            ++t;
-        }
+        column_sums<VEC, IT, FULL>(dw, L, P.d, cols,
+                             P.ws + (((long)blockIdx.x * P.segs + seg) * gridDim.y + head) * P.d);
     }
-    column_sums<VEC, IT, FULL>(dw, L, P.d, cols,
-                         P.ws + ((long)blockIdx.x * gridDim.y + head) * P.d);
 }
 
 template <typename T, typename S, int VEC, int IT, bool FULL>
@@ -608,6 +613,12 @@ hipError_t sum_parts(const Sums &S, hipStream_t st) {
             FN(4)                                                                      \
     }
 
+// Rounds of a segment: `step` rows a round for all workgroups together.
+static int seg_rounds(long rows, long step, int segs) {
+    const long rounds = (rows + step - 1) / step;
+    return (int)((rounds + segs - 1) / segs);
+}
+
 template <typename T, bool FULL, norm::Kind KIND>
 static hipError_t gated_norm_k(const GatedNormParams &P, hipStream_t st, bool back) {
     constexpr int V = 16 / sizeof(T);
@@ -616,9 +627,12 @@ static hipError_t gated_norm_k(const GatedNormParams &P, hipStream_t st, bool ba
         const long slots = threads / tpr, rows = P.tokens * P.H;                                \
         const dim3 grid = back ? dim3((unsigned)P.parts, P.per_head ? P.H : 1)                  \
                                : dim3((unsigned)((rows + slots - 1) / slots));                  \
+        GatedNormParams Q = P;                                                                  \
+        if (back)                                                                               \
+            Q.seg_rounds = seg_rounds(P.per_head ? P.tokens : rows, P.parts * slots, P.segs);   \
         auto kernel = back ? norm::gated_norm_grad_kernel<T, V, IT_, FULL, KIND>                \
                            : norm::gated_norm_kernel<T, V, IT_, FULL, KIND>;                    \
-        hipLaunchKernelGGL(kernel, grid, dim3(threads), 0, st, P, tpr);                         \
+        hipLaunchKernelGGL(kernel, grid, dim3(threads), 0, st, Q, tpr);                         \
         return hipGetLastError();                                                               \
     }
     KDN_NORM_IT(KDN_GATED, P.d)
@@ -679,7 +693,7 @@ hipError_t launch_gated_norm_backward(const GatedNormParams &P, hipStream_t st) 
             return e;
     }
     const long n = (long)(P.per_head ? P.H : 1) * P.d;
-    return norm::sum_parts(norm::Sums{P.ws, nullptr, P.dweight, nullptr, n, 0, P.parts}, st);
+    return norm::sum_parts(norm::Sums{P.ws, nullptr, P.dweight, nullptr, n, 0, P.parts * P.segs}, st);
 }
 
 static hipError_t residual(const ResidualNormParams &P, hipStream_t st, bool back) {

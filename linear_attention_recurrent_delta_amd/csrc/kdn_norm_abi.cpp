@@ -45,6 +45,16 @@ int gated_parts(int tokens, int H, int per_head) {
     return (int)std::min(rows, (long long)most);
 }
 
+// Sums over `rows` rows that a workgroup of `parts` writes: its threads hold as many float32
+// rows of d values at once as fit, and of bf16 rows twice as many.
+int norm_segs(long long rows, int d, int threads, int parts) {
+    const long long held = std::max(1, threads / kdn::norm_row_threads(d, false));
+    return (int)std::max(1LL, (rows - 1) / (std::max(1, parts) * held * kdn::SEG_ROUNDS) + 1);
+}
+int gated_segs(int tokens, int H, int d, int per_head) {
+    return norm_segs(per_head ? tokens : (long long)tokens * H, d, 256, gated_parts(tokens, H, per_head));
+}
+
 kdn_status residual_shape(kdn::ResidualNormParams &P, int dtype, int stream_dtype, int tokens,
                           int D, int scale_n, float eps, long long x_stride, long long r_stride) {
     if (!kdn::valid_dtype(dtype) || (stream_dtype != dtype && stream_dtype != KDN_F32) ||
@@ -114,7 +124,8 @@ unsigned long long kdn_gated_norm_backward_workspace_size(int tokens, int H, int
                                       per_head, 1.f, 0, 0);
     if (status)
         *status = st;
-    return st == KDN_OK ? 4ull * gated_parts(tokens, H, per_head) * (per_head ? H : 1) * d : 0;
+    return st == KDN_OK ? 4ull * gated_parts(tokens, H, per_head) * gated_segs(tokens, H, d, per_head) *
+                                (per_head ? H : 1) * d : 0;
 }
 
 kdn_status kdn_gated_norm_backward(kdn_dtype dtype, int tokens, int H, int d,
@@ -145,7 +156,8 @@ kdn_status kdn_gated_norm_backward(kdn_dtype dtype, int tokens, int H, int d,
     if (clash(outs, 3, ins, 4))
         return KDN_ERR_ALIAS;
     P.parts = H > 0 ? gated_parts(tokens, H, per_head) : 0;
-    if (kdn_status st = workspace_ok(workspace, workspace_bytes, 4LL * P.parts * n_w, ins, 4, outs, 3))
+    P.segs = gated_segs(tokens, H, d, per_head);
+    if (kdn_status st = workspace_ok(workspace, workspace_bytes, 4LL * P.parts * P.segs * n_w, ins, 4, outs, 3))
         return st;
     P.x = x; P.z = z; P.weight = weight; P.d_y = d_y;
     P.dx = dx; P.dz = dz; P.dweight = dweight; P.ws = static_cast<float *>(workspace);

@@ -53,3 +53,10 @@ def test_an_empty_table_has_no_tiles(lib):
     for block in (64, 1 << 20):
         pk = kdn.Packed(1000, block, 0, 0, None, None, None)
         assert lib.kdn_causal_conv_backward_workspace_size(BF16, 0, 0, 64, 4, pk, ctypes.byref(st)) == 0 and st.value == OK
+
+
+def test_gated_norm_sums_of_many_rows(lib):
+    """256 rows of a column at most in one float32 sum."""
+    size = lambda *a: lib.kdn_gated_norm_backward_workspace_size(*a, None)  # noqa: E731
+    assert size(1 << 22, 1, 64, 0) == 4 * 1024 * 64 and size((1 << 22) + 1, 1, 64, 0) == 4 * 2048 * 64
+    assert size(1 << 22, 512, 64, 1) == 4 * 2 * 512 * 512 * 64 and size(1 << 20, 8, 16384, 0) == 4 * 1024 * 32 * 16384

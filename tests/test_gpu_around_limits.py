@@ -176,3 +176,21 @@ def test_conv_sums_over_many_tokens():
         off = (got.double() - want).abs().max().item() / want.max().item() / ref.U
         print(f"    {off:.0f} roundings", flush=True)
         assert off <= 517
+
+
+@pytest.mark.parametrize("per_head,tokens,H", [(True, 24576, 512), (False, 64 * 24576, 8)])
+def test_gated_norm_sums_over_many_rows(per_head, tokens, H):
+    """dweight over 768 rows for each place of a workgroup of old.  A thread adds at most 256
+    rows in float32, then 16 rows' places; n is off by 8 roundings (its root, two products) and
+    the result by one."""
+    d = 64
+    x, dy = torch.ones(tokens, H, d, device="cuda"), spike((tokens, H, d), 0.9)
+    w = torch.ones((H, d) if per_head else (d,), device="cuda")
+    if not per_head:
+        dy[0, 1:] = 0.9
+    got = kdn.gated_norm_backward(x, w, dy)["dweight"].double()
+    n = (1.0 + torch.tensor(1e-5).double().item()) ** -0.5
+    want = n * (column_sums(dy) if per_head else column_sums(dy.view(-1, d)))
+    off = (got - want).abs().max().item() / want.max().item() / ref.U
+    print(f"    {off:.0f} roundings", flush=True)
+    assert off <= 256 + 16 + 8 + 1
