@@ -59,4 +59,4 @@ def test_gated_norm_sums_of_many_rows(lib):
     """256 rows of a column at most in one float32 sum."""
     size = lambda *a: lib.kdn_gated_norm_backward_workspace_size(*a, None)  # noqa: E731
     assert size(1 << 22, 1, 64, 0) == 4 * 1024 * 64 and size((1 << 22) + 1, 1, 64, 0) == 4 * 2048 * 64
-    assert size(1 << 22, 512, 64, 1) == 4 * 2 * 512 * 512 * 64 and size(1 << 20, 8, 16384, 0) == 4 * 1024 * 32 * 16384
+    assert size(1 << 21, 512, 64, 1) == 4 * 2 * 256 * 512 * 64 and size(1 << 20, 8, 16384, 0) == 4 * 1024 * 32 * 16384
