@@ -693,7 +693,10 @@ unsigned long long kdn_selective_scan_backward_workspace_size(kdn_dtype dtype, i
  *   weight      [d] float32 for all heads, or [H, d] (per_head)
  *   y           [tokens, H, d] dtype (output); may overlap no input
  *   eps         positive and finite, else KDN_ERR_UNSUPPORTED
- * 1 <= d <= 16384, else KDN_ERR_UNSUPPORTED; tokens * H < 2^31, H < 2^16.
+ * 1 <= d <= 16384, else KDN_ERR_UNSUPPORTED; tokens * H < 2^31, H < 2^16.  A row takes a
+ * thread for every 16 bytes (the next power of two, at most 1024); kdn_gated_norm refuses
+ * rows that would take 2^32 (KDN_ERR_SHAPE).  Its gradients have no such limit, but take
+ * less than 2^26 values of weight.
  */
 typedef enum kdn_norm_order { KDN_NORM_GATE = 0, KDN_GATE_NORM = 1 } kdn_norm_order;
 
@@ -724,7 +727,7 @@ unsigned long long kdn_gated_norm_backward_workspace_size(int tokens, int H, int
  *   weight      [D] float32;  scale [scale_n] float32, scale_n 0 (NULL: one), 1 or D
  *   y           [tokens, D] dtype, h [tokens, D] stream_dtype (outputs); h may be
  *               exactly a contiguous residual
- * 1 <= D <= 16384 and eps as above.
+ * 1 <= D <= 16384, eps and the rows' limit as above.
  */
 kdn_status kdn_residual_norm(kdn_dtype dtype, kdn_dtype stream_dtype, int tokens, int D,
                              int scale_n, float eps, long long x_stride, long long residual_stride,

@@ -32,11 +32,20 @@ kdn_status gated_shape(kdn::GatedNormParams &P, int dtype, int tokens, int H, in
     P.per_head = per_head != 0; P.gate_first = order == KDN_GATE_NORM; P.act = act; P.eps = eps; P.inv_d = 1. / d;
     if (kdn_status st = kdn::row_stride(x_stride, (long long)H * d, &P.x_stride)) return st;
     if (kdn_status st = kdn::row_stride(z_stride, (long long)H * d, &P.z_stride)) return st;
-    // a row has a thread for 16 bytes at most: a workgroup a row, at the largest
-    const long long per_wg = std::max(1, 256 / std::max(1, kdn::norm_row_threads(d, P.bf16)));
-    if (!kdn::launchable((long long)tokens * H / per_wg + 1, std::max(256, kdn::norm_row_threads(d, P.bf16))))
-        return KDN_ERR_SHAPE;
     return KDN_OK;
+}
+
+// Rows as a norm's outputs are launched: threads of a row as it has 16-byte pieces, in
+// workgroups of 256 or of one row.
+bool rows_launchable(long long rows, int d, bool bf16) {
+    const int tpr = kdn::norm_row_threads(d, bf16);
+    const int per = std::max(1, 256 / tpr);
+    return kdn::launchable((rows + per - 1) / per, std::max(256, tpr));
+}
+// Gradients' workgroups, of up to 1024 threads, and those that sum up 16 columns each.
+bool parts_launchable(long long parts, int d, long long columns) {
+    return kdn::launchable(parts, std::max(512, kdn::norm_row_threads(d, false))) &&
+           kdn::launchable((columns + 15) / 16, 1024);
 }
 
 int gated_parts(int tokens, int H, int per_head) {
@@ -55,6 +64,11 @@ int gated_segs(int tokens, int H, int d, int per_head) {
     return norm_segs(per_head ? tokens : (long long)tokens * H, d, 256, gated_parts(tokens, H, per_head));
 }
 
+bool gated_launchable(int tokens, int H, int d, int per_head) {
+    return parts_launchable((long long)gated_parts(tokens, H, per_head) * (per_head ? H : 1), d,
+                            (long long)(per_head ? H : 1) * d);
+}
+
 kdn_status residual_shape(kdn::ResidualNormParams &P, int dtype, int stream_dtype, int tokens,
                           int D, int scale_n, float eps, long long x_stride, long long r_stride) {
     if (!kdn::valid_dtype(dtype) || (stream_dtype != dtype && stream_dtype != KDN_F32) ||
@@ -69,9 +83,6 @@ kdn_status residual_shape(kdn::ResidualNormParams &P, int dtype, int stream_dtyp
     P.tokens = tokens; P.D = D; P.scale_n = scale_n; P.eps = eps; P.inv_d = 1. / D;
     if (kdn_status st = kdn::row_stride(x_stride, D, &P.x_stride)) return st;
     if (kdn_status st = kdn::row_stride(r_stride, D, &P.r_stride)) return st;
-    const int tpr = kdn::norm_row_threads(D, P.bf16);
-    if (!kdn::launchable((long long)tokens / std::max(1, 256 / tpr) + 1, std::max(256, tpr)))
-        return KDN_ERR_SHAPE;
     return KDN_OK;
 }
 
@@ -102,6 +113,8 @@ kdn_status kdn_gated_norm(kdn_dtype dtype, int tokens, int H, int d, kdn_norm_or
     if (kdn_status st = gated_shape(P, dtype, tokens, H, d, order, act, per_head, eps, x_stride,
                                     z_stride))
         return st;
+    if (!rows_launchable((long long)tokens * H, d, P.bf16))
+        return KDN_ERR_SHAPE;
     const long long es = P.bf16 ? 2 : 4, row = (long long)H * d;
     if (tokens * row > 0 && (!x || !weight || !y))
         return KDN_ERR_NULL;
@@ -120,8 +133,10 @@ kdn_status kdn_gated_norm(kdn_dtype dtype, int tokens, int H, int d, kdn_norm_or
 unsigned long long kdn_gated_norm_backward_workspace_size(int tokens, int H, int d, int per_head,
                                                           kdn_status *status) {
     kdn::GatedNormParams P;
-    const kdn_status st = gated_shape(P, KDN_F32, tokens, H, d, KDN_NORM_GATE, KDN_ACT_SILU,
-                                      per_head, 1.f, 0, 0);
+    kdn_status st = gated_shape(P, KDN_F32, tokens, H, d, KDN_NORM_GATE, KDN_ACT_SILU, per_head, 1.f,
+                                0, 0);
+    if (st == KDN_OK && !gated_launchable(tokens, H, d, per_head))
+        st = KDN_ERR_SHAPE;
     if (status)
         *status = st;
     return st == KDN_OK ? 4ull * gated_parts(tokens, H, per_head) * gated_segs(tokens, H, d, per_head) *
@@ -139,6 +154,8 @@ kdn_status kdn_gated_norm_backward(kdn_dtype dtype, int tokens, int H, int d,
     if (kdn_status st = gated_shape(P, dtype, tokens, H, d, order, act, per_head, eps, x_stride,
                                     z_stride))
         return st;
+    if (!gated_launchable(tokens, H, d, per_head))
+        return KDN_ERR_SHAPE;
     const long long es = P.bf16 ? 2 : 4, row = (long long)H * d, n_w = per_head ? row : d;
     if ((tokens * row > 0 && (!x || !weight || !d_y || !dx || (z && !dz))) || (H > 0 && !dweight) ||
         (!z && dz))
@@ -172,6 +189,8 @@ kdn_status kdn_residual_norm(kdn_dtype dtype, kdn_dtype stream_dtype, int tokens
     if (kdn_status st = residual_shape(P, dtype, stream_dtype, tokens, D, scale_n, eps, x_stride,
                                        residual_stride))
         return st;
+    if (!rows_launchable(tokens, D, P.bf16))
+        return KDN_ERR_SHAPE;
     const long long es = P.bf16 ? 2 : 4, rs = P.stream_bf16 ? 2 : 4, n = (long long)tokens * D;
     if (n > 0 && (!x || !residual || !weight || !y || !h))
         return KDN_ERR_NULL;

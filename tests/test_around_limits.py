@@ -60,3 +60,25 @@ def test_gated_norm_sums_of_many_rows(lib):
     size = lambda *a: lib.kdn_gated_norm_backward_workspace_size(*a, None)  # noqa: E731
     assert size(1 << 22, 1, 64, 0) == 4 * 1024 * 64 and size((1 << 22) + 1, 1, 64, 0) == 4 * 2048 * 64
     assert size(1 << 21, 512, 64, 1) == 4 * 2 * 256 * 512 * 64 and size(1 << 20, 8, 16384, 0) == 4 * 1024 * 32 * 16384
+
+
+def test_norm_gradients_are_not_counted_by_rows(lib):
+    """Gradients launch a workgroup a part, whatever the rows and their type; outputs a row's threads."""
+    st, big = ctypes.c_int(0), 1 << 50
+    for tokens, H, d, per_head in ((1 << 22, 32, 128, 0), (1 << 22, 32, 128, 1), (1 << 23, 1, 8192, 0), ((1 << 31) - 1, 1, 16, 0)):
+        assert lib.kdn_gated_norm_backward_workspace_size(tokens, H, d, per_head, ctypes.byref(st)) > 0 and st.value == OK
+        back = lambda dy, dt: lib.kdn_gated_norm_backward(dt, tokens, H, d, 0, 1, per_head, 1e-5, 0, 0, big, big, None, dy, big,  # noqa: E731
+                                                          None, big, None, 0, None)
+        assert back(None, BF16) == back(None, F32) == ENULL
+    for tokens, D in ((1 << 23, 2048), (1 << 22, 16384), ((1 << 31) - 1, 32)):
+        assert lib.kdn_residual_norm_backward_workspace_size(tokens, D, 1, ctypes.byref(st)) > 0 and st.value == OK
+        assert lib.kdn_residual_norm_backward(BF16, BF16, tokens, D, 0, 1e-5, 0, 0, None, None, big, None, big, None, None, big, big,
+                                              None, None, 0, None) == ENULL
+    gated = lambda dt, tokens, d: lib.kdn_gated_norm(dt, tokens, 1, d, 0, 1, 0, 1e-5, 0, 0, None, None, None, None, None)  # noqa: E731
+    assert gated(BF16, (1 << 27) - 8, 256) == ENULL and gated(BF16, (1 << 27) - 7, 256) == ESHAPE
+    assert gated(F32, (1 << 26) - 4, 256) == ENULL and gated(F32, (1 << 26) - 3, 256) == ESHAPE
+    # the sums of a weight's values, 16 a workgroup of 1024 threads
+    size = lambda H: lib.kdn_gated_norm_backward_workspace_size(1, H, 1024, 1, ctypes.byref(st))  # noqa: E731
+    assert size(65534) > 0 and st.value == OK and size(65535) > 0
+    size = lambda H: lib.kdn_gated_norm_backward_workspace_size(1, H, 4096, 1, ctypes.byref(st))  # noqa: E731
+    assert size((1 << 14) - 1) > 0 and size(1 << 14) == 0 and st.value == ESHAPE
