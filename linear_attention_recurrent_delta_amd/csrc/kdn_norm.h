@@ -47,8 +47,8 @@ struct ResidualNormParams {
     const void *d_y, *d_h;  // d_h may be null (zero)
     void *dx, *dresidual;   // dx may be null (not wanted)
     float *dweight, *dscale;    // dscale may be null
-    float *ws;              // [parts][D] of dweight, [parts][D or 1] of dscale
-    int parts;
+    float *ws, *ws_scale;   // [segs][parts][D] of dweight, [segs][parts][D or 1] of dscale
+    int parts, segs;        // workgroups of a launch, launches
 };
 
 // Parts that the sums over tokens are made in: about as many workgroups as run at once
@@ -56,8 +56,9 @@ struct ResidualNormParams {
 // bf16 72, 71 and 73 us, 98304 x 192 float32 by head 91, 82 and 84; residual 2500 x 1543
 // bf16 30, 23 and 34, 16384 x 2048 64, 67 and 71.
 constexpr int NORM_PARTS = 1024, RESIDUAL_PARTS = 512;
-// Rows of a column that a thread adds in float32: behind them a workgroup writes its sums
-// and begins anew.  (More parts in their place let workgroups that run at once work on rows
+// Rows of a column that a thread adds in float32: behind them a workgroup of the gated norm
+// writes its sums and begins anew, and of the residual norm another launch begins (as in the
+// gated norm its kernel would take 21.5 us for 2500 x 1543, where it takes 20.2).  (More parts in their place let workgroups that run at once work on rows
 // apart from each other: 131072 x 32 heads of 128 bf16, weight by head, 1262 us where it
 // is 1177.)
 constexpr int SEG_ROUNDS = 256;

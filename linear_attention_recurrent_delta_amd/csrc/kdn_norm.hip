@@ -20,6 +20,8 @@
 #include "kdn_act.h"
 #include "kdn_norm.h"
 
+#include <type_traits>
+
 namespace kdn {
 namespace norm {
 
@@ -545,7 +547,7 @@ __global__ __launch_bounds__(NT_MAX) void residual_norm_grad_kernel(ResidualNorm
     column_sums<VEC, IT, FULL>(dw, L, P.D, cols, P.ws + (long)blockIdx.x * P.D);
     if (!P.dscale)
         return;
-    float *part = P.ws + (long)P.parts * P.D;
+    float *part = P.ws_scale;
     if (P.scale_n > 1) {
         column_sums<VEC, IT, FULL>(ds, L, P.D, cols, part + (long)blockIdx.x * P.D);
         return;
@@ -707,16 +709,40 @@ hipError_t launch_residual_norm(const ResidualNormParams &P, hipStream_t st) {
     return P.tokens * P.D == 0 ? hipSuccess : residual(P, st, false);
 }
 
+// Rows `first` .. + tokens of a call.
+static ResidualNormParams rows_of(const ResidualNormParams &P, long first, long tokens) {
+    ResidualNormParams Q = P;
+    const long es = P.bf16 ? 2 : 4, rs = P.stream_bf16 ? 2 : 4;
+    auto at = [](auto *p, long bytes) {
+        typedef std::conditional_t<std::is_const_v<std::remove_pointer_t<decltype(p)>>, const char, char> Byte;
+        return p ? static_cast<decltype(p)>(static_cast<Byte *>(p) + bytes) : p;
+    };
+    Q.tokens = tokens;
+    Q.x = at(P.x, first * P.x_stride * es);
+    Q.residual = at(P.residual, first * P.r_stride * rs);
+    Q.d_y = at(P.d_y, first * P.D * es);
+    Q.d_h = at(P.d_h, first * P.D * rs);
+    Q.dx = at(P.dx, first * P.D * es);
+    Q.dresidual = at(P.dresidual, first * P.D * rs);
+    return Q;
+}
+
 hipError_t launch_residual_norm_backward(const ResidualNormParams &P, hipStream_t st) {
     if (P.D == 0)
         return hipSuccess;
-    if (P.parts > 0) {
-        const hipError_t e = residual(P, st, true);
+    const long parts = (long)P.parts * P.segs, n_scale = P.dscale ? P.scale_n : 0;
+    float *scales = P.ws + parts * P.D;
+    const long rows = parts > 0 ? (P.tokens + P.segs - 1) / P.segs : 0;
+    for (int seg = 0; parts > 0 && seg < P.segs; ++seg) {
+        const long first = min(seg * rows, P.tokens);
+        ResidualNormParams Q = rows_of(P, first, min(rows, P.tokens - first));
+        Q.ws = P.ws + seg * P.parts * (long)P.D;
+        Q.ws_scale = scales + seg * P.parts * n_scale;
+        const hipError_t e = residual(Q, st, true);
         if (e != hipSuccess)
             return e;
     }
-    return norm::sum_parts(norm::Sums{P.ws, P.ws + (long)P.parts * P.D, P.dweight, P.dscale, P.D,
-                                      P.dscale ? P.scale_n : 0, P.parts}, st);
+    return norm::sum_parts(norm::Sums{P.ws, scales, P.dweight, P.dscale, P.D, n_scale, (int)parts}, st);
 }
 
 }  // namespace kdn

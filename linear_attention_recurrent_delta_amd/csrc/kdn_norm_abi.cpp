@@ -86,6 +86,9 @@ kdn_status residual_shape(kdn::ResidualNormParams &P, int dtype, int stream_dtyp
     return KDN_OK;
 }
 
+int residual_parts(int tokens) { return std::min(tokens, kdn::RESIDUAL_PARTS); }
+int residual_segs(int tokens, int D) { return norm_segs(tokens, D, 512, residual_parts(tokens)); }
+
 // The workspace's checks, against all other arguments.
 kdn_status workspace_ok(void *workspace, unsigned long long bytes, long long need,
                         const Range *ins, int ni, const Range *outs, int no) {
@@ -217,7 +220,7 @@ unsigned long long kdn_residual_norm_backward_workspace_size(int tokens, int D, 
     const kdn_status st = residual_shape(P, KDN_F32, KDN_F32, tokens, D, scale_n, 1.f, 0, 0);
     if (status)
         *status = st;
-    return st == KDN_OK ? 4ull * std::min(tokens, kdn::RESIDUAL_PARTS) * (D + scale_n) : 0;
+    return st == KDN_OK ? 4ull * residual_parts(tokens) * residual_segs(tokens, D) * (D + scale_n) : 0;
 }
 
 kdn_status kdn_residual_norm_backward(kdn_dtype dtype, kdn_dtype stream_dtype, int tokens, int D,
@@ -248,8 +251,9 @@ kdn_status kdn_residual_norm_backward(kdn_dtype dtype, kdn_dtype stream_dtype, i
     const Range outs[] = {{dx, n * es}, {dresidual, n * rs}, {dweight, 4LL * D}, {dscale, 4LL * scale_n}};
     if (clash(outs, 4, ins, 6))
         return KDN_ERR_ALIAS;
-    P.parts = std::min(tokens, kdn::RESIDUAL_PARTS);
-    const long long n_ws = 4LL * P.parts * (D + (dscale ? scale_n : 0));
+    P.parts = residual_parts(tokens);
+    P.segs = residual_segs(tokens, D);
+    const long long n_ws = 4LL * P.parts * P.segs * (D + (dscale ? scale_n : 0));
     if (kdn_status st = workspace_ok(workspace, workspace_bytes, n_ws, ins, 6, outs, 4))
         return st;
     P.x = x; P.residual = h; P.weight = weight; P.scale = scale; P.d_y = d_y; P.d_h = d_h;

@@ -82,3 +82,10 @@ def test_norm_gradients_are_not_counted_by_rows(lib):
     assert size(65534) > 0 and st.value == OK and size(65535) > 0
     size = lambda H: lib.kdn_gated_norm_backward_workspace_size(1, H, 4096, 1, ctypes.byref(st))  # noqa: E731
     assert size((1 << 14) - 1) > 0 and size(1 << 14) == 0 and st.value == ESHAPE
+
+
+def test_residual_norm_sums_of_many_rows(lib):
+    """256 rows at most in one float32 sum."""
+    size = lambda *a: lib.kdn_residual_norm_backward_workspace_size(*a, None)  # noqa: E731
+    assert size(512 * 256, 4096, 0) == 4 * 512 * 4096 and size(512 * 256 + 1, 4096, 4096) == 4 * 1024 * 8192
+    assert size(1 << 20, 64, 1) == 4 * 512 * 65 and size(1 << 22, 2048, 1) == 4 * 512 * 32 * 2049

@@ -194,3 +194,47 @@ def test_gated_norm_sums_over_many_rows(per_head, tokens, H):
     off = (got - want).abs().max().item() / want.max().item() / ref.U
     print(f"    {off:.0f} roundings", flush=True)
     assert off <= 256 + 16 + 8 + 1
+
+
+@pytest.mark.parametrize("scale", ["one", "channel"])
+def test_residual_norm_sums_over_many_rows(scale):
+    """dweight and dscale over 768 rows a workgroup of old: a thread adds at most 256 in float32.
+    n is off by 8 roundings, the result by one; one scale adds four columns of a thread and
+    nine steps of a workgroup, too."""
+    tokens, D = 512 * 768, 2048
+    h, one = torch.ones(tokens, D, device="cuda"), torch.ones(D, device="cuda")
+    dy = spike((tokens, D), 0.9)
+    d = kdn.residual_norm_backward(None, h, one, dy, out=dict(dx=None, dresidual=torch.empty_like(h), dweight=torch.empty(D, device="cuda"),
+                                                              dscale=None))
+    want = (1.0 + torch.tensor(1e-5).double().item()) ** -0.5 * column_sums(dy)
+    off = (d["dweight"].double() - want).abs().max().item() / want.max().item() / ref.U
+    print(f"    dweight {off:.0f} roundings", flush=True)
+    assert off <= 256 + 8 + 1
+    s = torch.ones(D if scale == "channel" else 1, device="cuda")
+    got = kdn.residual_norm_backward(h, h, one, torch.zeros_like(h), dy, scale=s)["dscale"].double()
+    want = column_sums(dy) if scale == "channel" else column_sums(dy).sum().view(1)
+    off = (got - want).abs().max().item() / want.max().item() / ref.U
+    print(f"    dscale {off:.0f} roundings", flush=True)
+    assert off <= 256 + 1 + (0 if scale == "channel" else 4 + 9)
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+def test_norm_gradients_beyond_one_run_of_sums(dtype):
+    """More rows than one run of the float32 sums takes, rows as slices: each row's gradients are
+    those of its own half, bit for bit, and the sums are the halves'."""
+    d, n = 8, 512 * 256 * 256 + 12345
+    draw = lambda w: torch.rand((n, w), device="cuda", generator=torch.Generator("cuda").manual_seed(w)).to(dtype)  # noqa: E731
+    h, x, dy, w = draw(d + 3)[:, 1:1 + d], draw(d + 2)[:, 2:], draw(d), 0.5 + torch.rand(d, device="cuda")
+    assert kdn.load().kdn_residual_norm_backward_workspace_size(n, d, d, None) == 4 * 512 * 2 * 2 * d
+    assert kdn.load().kdn_gated_norm_backward_workspace_size(n, 1, d, 0, None) == 4 * 1024 * 2 * d
+    for call in (lambda r: kdn.residual_norm_backward(x[r], h[r], w, dy[r], scale=w),
+                 lambda r: kdn.gated_norm_backward(h[r].unsqueeze(1), w, dy[r].unsqueeze(1), x[r].unsqueeze(1))):
+        full = call(slice(None))
+        half = [call(slice(0, n // 2 - 77)), call(slice(n // 2 - 77, n))]
+        for k in ("dx", "dresidual", "dgate"):
+            if k in full:
+                assert torch.equal(full[k], torch.cat([a[k] for a in half])), k
+        # dy, h and w are positive and so are dweight's terms; a sum of one call is off by 256
+        # rows of a thread, 256 or 512 threads of a column and the result at most
+        want = sum(a["dweight"].double() for a in half)
+        assert ((full["dweight"].double() - want).abs() <= 2 * (256 + 512 + 1) * ref.U * want).all()
