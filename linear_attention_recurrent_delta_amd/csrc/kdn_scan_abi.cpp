@@ -102,10 +102,14 @@ constexpr int GRAD_BLOCK = 256;
 // Workgroups of the gradients' kernel that run at once: one a CU (with two of them shared
 // out B2 T4096 C2048 is 405 us where it is 397, B1 T1000 C1024 76 where it is 59).
 constexpr int GRAD_WGS = 256;
+// Tiles whose sums over tokens a wave of a workgroup adds in float32 (on average, where a
+// packed batch is uneven).
+constexpr int PART_TILES = 256;
 
 // How the gradients' work is shared out: runs of 16 channels for a workgroup, as many
 // as leave two workgroups a CU, since the sums over channels cost each set of runs the
-// same; then workgroups for the tiles of a set.
+// same; then workgroups for the tiles of a set, as many as run at once, and whole times
+// that many of long batches, so that no float32 sum is a chain that grows with the tokens.
 void grad_shares(kdn::ScanParams &P, bool packed) {
     const int tile = kdn::scan_tile(P.S);
     const long long blocks = packed ? P.nblocks : (long long)P.N * P.nblocks;
@@ -118,7 +122,8 @@ void grad_shares(kdn::ScanParams &P, bool packed) {
     const long long sets = groups > 0 ? (long long)kdn::scan_sets(P) * P.G : 0;
     const long long in_block = std::min<long long>(P.block, std::max<long long>(P.tokens, 1));
     const long long per_block = (in_block + tile - 1) / tile;
-    long long parts = sets > 0 ? std::max(1LL, GRAD_WGS / sets) : 0;
+    const long long once = sets > 0 ? std::max(1LL, GRAD_WGS / sets) : 0;
+    const long long parts = once * std::max(1LL, once > 0 ? (tiles - 1) / (once * PART_TILES) + 1 : 0);
     P.classes = (int)std::min(per_block, blocks > 0 ? (4 * parts + blocks - 1) / blocks : 1);
     P.parts = (int)std::min(parts, blocks * P.classes);
 }

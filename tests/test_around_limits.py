@@ -89,3 +89,14 @@ def test_residual_norm_sums_of_many_rows(lib):
     size = lambda *a: lib.kdn_residual_norm_backward_workspace_size(*a, None)  # noqa: E731
     assert size(512 * 256, 4096, 0) == 4 * 512 * 4096 and size(512 * 256 + 1, 4096, 4096) == 4 * 1024 * 8192
     assert size(1 << 20, 64, 1) == 4 * 512 * 65 and size(1 << 22, 2048, 1) == 4 * 512 * 32 * 2049
+
+
+def test_scan_sums_in_more_parts_of_many_tokens(lib):
+    """256 tiles a part at most: the workspace beside the tiles' states and the sums over channels."""
+    up = lambda n: -(-n // 256) * 256  # noqa: E731
+    for T, C, S, sets, parts in ((64 * 255, 32768, 8, 256, 1), (64 * 256, 32768, 8, 256, 2), (64 * 767, 32768, 8, 256, 3),
+                                 (1 << 20, 4096, 16, 32, 72), (32 * 1000, 1024, 32, 32, 8)):
+        tile = 32 if S == 32 else 64
+        tiles = T // tile + -(-T // 256) + 1
+        want = 2 * up(4 * tiles * C * S) + up(4 * tiles * C) + up(4 * sets * T * 2 * S) + up(4 * parts * C * (S + 2))
+        assert lib.kdn_selective_scan_backward_workspace_size(BF16, 1, T, C, S, 1, None, None) == want, T

@@ -238,3 +238,17 @@ def test_norm_gradients_beyond_one_run_of_sums(dtype):
         # rows of a thread, 256 or 512 threads of a column and the result at most
         want = sum(a["dweight"].double() for a in half)
         assert ((full["dweight"].double() - want).abs() <= 2 * (256 + 512 + 1) * ref.U * want).all()
+
+
+def test_scan_sums_over_many_tokens():
+    """dD over 768 tiles of one workgroup of old: a wave adds 8 tokens of each of at most 256
+    tiles in float32 (two in a lane, four lanes), then eight waves' sums are added, and the
+    result is rounded."""
+    T, C, S = 64 * 768, 32768, 8
+    x, dy = torch.ones(1, T, C, dtype=BF, device="cuda"), spike((T, C), 0.1, BF)
+    none, A = torch.zeros(1, T, 1, S, dtype=BF, device="cuda"), -torch.ones(C, S, device="cuda")
+    d = kdn.selective_scan_backward(x, x, A, none, none, dy[None], D=torch.ones(C, device="cuda"))
+    want = column_sums(dy)
+    off = (d["dD"].double() - want).abs().max().item() / want.max().item() / ref.U
+    print(f"    {off:.0f} roundings", flush=True)
+    assert off <= 256 + 4 + 8 + 1
