@@ -687,8 +687,6 @@ hipError_t launch_gated_norm(const GatedNormParams &P, hipStream_t st) {
 }
 
 hipError_t launch_gated_norm_backward(const GatedNormParams &P, hipStream_t st) {
-    if ((long)P.H * P.d == 0)
-        return hipSuccess;
     if (P.parts > 0) {
         const hipError_t e = P.bf16 ? gated_norm_t<bf16>(P, st, true) : gated_norm_t<float>(P, st, true);
         if (e != hipSuccess)

@@ -160,7 +160,7 @@ kdn_status kdn_gated_norm_backward(kdn_dtype dtype, int tokens, int H, int d,
     if (!gated_launchable(tokens, H, d, per_head))
         return KDN_ERR_SHAPE;
     const long long es = P.bf16 ? 2 : 4, row = (long long)H * d, n_w = per_head ? row : d;
-    if ((tokens * row > 0 && (!x || !weight || !d_y || !dx || (z && !dz))) || (H > 0 && !dweight) ||
+    if ((tokens * row > 0 && (!x || !weight || !d_y || !dx || (z && !dz))) || (n_w > 0 && !dweight) ||
         (!z && dz))
         return KDN_ERR_NULL;
     for (const void *p : {x, z, d_y, (const void *)dx, (const void *)dz})

@@ -100,3 +100,9 @@ def test_scan_sums_in_more_parts_of_many_tokens(lib):
         tiles = T // tile + -(-T // 256) + 1
         want = 2 * up(4 * tiles * C * S) + up(4 * tiles * C) + up(4 * sets * T * 2 * S) + up(4 * parts * C * (S + 2))
         assert lib.kdn_selective_scan_backward_workspace_size(BF16, 1, T, C, S, 1, None, None) == want, T
+
+
+def test_gated_gradients_of_no_heads_need_a_place(lib):
+    back = lambda dw, per_head: lib.kdn_gated_norm_backward(BF16, 5, 0, 16, 0, 1, per_head, 1e-5, 0, 0, None, None, None, None, None,  # noqa: E731
+                                                            None, dw, None, 0, None)
+    assert back(None, 0) == ENULL and back(None, 1) == OK

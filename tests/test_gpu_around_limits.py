@@ -252,3 +252,15 @@ def test_scan_sums_over_many_tokens():
     off = (d["dD"].double() - want).abs().max().item() / want.max().item() / ref.U
     print(f"    {off:.0f} roundings", flush=True)
     assert off <= 256 + 4 + 8 + 1
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+def test_gated_gradients_of_no_heads(dtype):
+    """A weight for all heads, and none of them: its gradient is zero, not left as it was."""
+    e = torch.empty(5, 0, 16, dtype=dtype, device="cuda")
+    for z in (None, e):
+        out = dict(dx=e, dgate=z, dweight=torch.full((16,), 7.0, device="cuda"))
+        kdn.gated_norm_backward(e.clone(), torch.ones(16, device="cuda"), e.clone(), z, out=out)
+        assert not out["dweight"].any()
+    d = kdn.gated_norm_backward(e, torch.ones(0, 16, device="cuda"), e)
+    assert d["dweight"].shape == (0, 16)
