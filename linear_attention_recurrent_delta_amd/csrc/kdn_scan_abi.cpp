@@ -314,8 +314,8 @@ kdn_status kdn_selective_scan_backward(kdn_dtype dtype, int N, int T, int C, int
     const long long es = P.bf16 ? 2 : 4, tok = P.tokens, gs = (long long)G * S;
     if (!launchable(((long long)C * (S + 2) + 63) / 64 + (tok * gs * 2 + 255) / 256 + 64, 256))
         return KDN_ERR_SHAPE;
-    if ((tok * C > 0 && (!x || !delta || !B || !Cm || !d_y || !dx || !ddelta || !dB || !dC || (z && !dz))) ||
-        (C > 0 && (!A || !dA)) || (!z && dz))
+    if ((tok * C > 0 && (!x || !delta || !B || !Cm || !d_y || !dx || !ddelta || (z && !dz))) ||
+        (tok * gs > 0 && (!dB || !dC)) || (C > 0 && (!A || !dA)) || (!z && dz))
         return KDN_ERR_NULL;
     if (kdn_status st = kdn::batch_tables(P, packed))
         return st;
@@ -374,7 +374,8 @@ kdn_status kdn_selective_scan_backward(kdn_dtype dtype, int N, int T, int C, int
     P.softplus = softplus != 0;
     P.x = x; P.delta = delta; P.z = z; P.B = B; P.Cm = Cm; P.A = A; P.D = D; P.bias = delta_bias;
     P.S0 = S0; P.d_y = d_y; P.dS_out = dS_out;
-    P.dx = dx; P.ddelta = ddelta; P.dA = dA; P.dB = dB; P.dC = dC; P.dD = dD; P.dz = dz;
+    P.dx = dx; P.ddelta = ddelta; P.dA = dA;
+    P.dB = gs > 0 ? dB : nullptr; P.dC = dC; P.dD = dD; P.dz = dz;
     P.dbias = ddelta_bias; P.dS0 = dS0;
     return done(kdn::launch_scan_backward(P, static_cast<hipStream_t>(stream)));
 }

@@ -434,7 +434,9 @@ template <typename T, int SPL> hipError_t launch_grad_t(const ScanParams &P, hip
             return e;
     }
     const long wide = ((long)P.C * (P.S + 2) + WAVE - 1) / WAVE;
-    const long bc = (P.tokens * P.G * 2 * P.S + NT - 1) / NT;
+    const long bc = P.dB ? (P.tokens * P.G * 2 * P.S + NT - 1) / NT : 0;
+    if (wide + bc == 0)
+        return hipSuccess;
     hipLaunchKernelGGL((scan_sum_kernel<T>), dim3((unsigned)(wide + bc + (P.block_offsets ? TAIL_WGS : 0))),
                        dim3(NT), 0, st, P, sets, wide, bc);
     return hipGetLastError();
@@ -443,9 +445,8 @@ template <typename T, int SPL> hipError_t launch_grad_t(const ScanParams &P, hip
 }  // namespace scan
 
 hipError_t launch_scan_backward(const ScanParams &P, hipStream_t st) {
-    if (P.C == 0)
-        return hipSuccess;
-    const hipError_t e = launch_scan_states(P, true, st);
+    // (without channels what is left are zeros in dB and dC)
+    const hipError_t e = P.C > 0 ? launch_scan_states(P, true, st) : hipSuccess;
     if (e != hipSuccess)
         return e;
     switch (P.S) {

@@ -6,7 +6,7 @@ import ctypes
 import pytest
 
 from linear_attention_recurrent_delta_amd import kdn
-from test_around_host import conv, decode, lib  # noqa: F401
+from test_around_host import conv, decode, lib, scan, scan_back  # noqa: F401
 from test_linear_host import BF16, ENULL, ESHAPE, F32, OK, packed
 
 # sequences, tokens, channels of packed batches
@@ -106,3 +106,10 @@ def test_gated_gradients_of_no_heads_need_a_place(lib):
     back = lambda dw, per_head: lib.kdn_gated_norm_backward(BF16, 5, 0, 16, 0, 1, per_head, 1e-5, 0, 0, None, None, None, None, None,  # noqa: E731
                                                             None, dw, None, 0, None)
     assert back(None, 0) == ENULL and back(None, 1) == OK
+
+
+def test_scan_gradients_of_no_channels_need_places(lib):
+    none = dict(C=0, z=None, dy=None, dl=None, dx=None, dd=None, da=None, dD=None, dz=None, dbias=None, ds=None, ws=None, wsb=0)
+    assert scan_back(lib, db=None, **none) == scan_back(lib, dc=None, **none) == ENULL
+    assert scan_back(lib, G=0, db=None, dc=None, **none) == OK
+    assert scan_back(lib, N=0, db=None, dc=None, **none) == OK

@@ -264,3 +264,20 @@ def test_gated_gradients_of_no_heads(dtype):
         assert not out["dweight"].any()
     d = kdn.gated_norm_backward(e, torch.ones(0, 16, device="cuda"), e)
     assert d["dweight"].shape == (0, 16)
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("packed", [False, True])
+def test_scan_gradients_of_no_channels(dtype, packed):
+    """Tokens with B and C and no channel: their gradients are zero, not left as they were."""
+    lead, S = (20,) if packed else (2, 10), 16
+    t = kdn.sequence_tables(i32([12, 0, 5]), 20, 64) if packed else None
+    e = torch.empty(lead + (0,), dtype=dtype, device="cuda")
+    for G in (0, 1, 3):
+        B = torch.full(lead + (G, S), math.nan, dtype=dtype, device="cuda")
+        seven = lambda: torch.full(lead + (G, S), 7.0, dtype=dtype, device="cuda")  # noqa: E731
+        none = torch.empty(0, device="cuda")
+        out = dict(dx=e, ddelta=e.clone(), dz=None, dB=seven(), dC=seven(), dA=torch.empty(0, S, device="cuda"), dD=None,
+                   ddelta_bias=None, dS0=None)
+        kdn.selective_scan_backward(e, e, torch.empty(0, S, device="cuda"), B, B, e, D=none, tables=t, out=out)
+        assert not out["dB"].any() and not out["dC"].any()
