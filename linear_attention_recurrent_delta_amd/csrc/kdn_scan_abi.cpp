@@ -69,19 +69,30 @@ kdn_status scan_shape(kdn::ScanParams &P, int dtype, int N, int T, int C, int S,
     return KDN_OK;
 }
 
-// Blocks of a dense call, and what follows from the blocks' number.
-kdn_status scan_blocks(kdn::ScanParams &P, bool packed, int block) {
+// Sequences of several blocks, or of what a packed batch may have.
+bool several(const kdn::ScanParams &P, bool packed) {
+    return packed ? P.block < P.tokens : P.nblocks > 1;
+}
+
+// Blocks of a dense call, and what follows from the blocks' number: the launches of the
+// outputs, of the tiles' own states (sequences of several blocks, and the gradients) and of
+// the joins.
+kdn_status scan_blocks(kdn::ScanParams &P, bool packed, int block, bool back) {
     if (!packed) {
         P.block = block;
         P.nblocks = P.T == 0 ? 0 : (P.T - 1) / block + 1;
     }
     const long long blocks = packed ? P.nblocks : (long long)P.N * P.nblocks;
-    // (grids have fours of runs)
-    const long long runs = P.C > 0 ? ((long long)kdn::scan_groups(P.C, P.G) * P.G + 3) / 4 * 4 : 0;
     P.tile_slots = kdn::tile_slots(P.tokens, blocks, P.S);
-    const long long pieces = ((long long)P.C * P.S + 255) / 256;
-    if (blocks >= (1LL << 32) || !launchable(blocks * runs + 32, 512) ||
-        !launchable(2LL * P.N * pieces, 256) || P.tile_slots * P.C >= (1LL << 40))
+    if (blocks >= (1LL << 32) || P.tile_slots * P.C >= (1LL << 40))
+        return KDN_ERR_SHAPE;
+    // grids have fours of runs: a wave each of the outputs, a workgroup each of the own
+    // states, with a few thousand workgroups more where there are less
+    const long long runs = P.C > 0 ? (long long)kdn::scan_groups(P.C, P.G) * P.G : 0;
+    const long long fours = blocks * ((runs + 3) / 4);
+    const long long pieces = ((long long)P.C * P.S / 2 + 255) / 256;
+    if (!launchable(fours + 1024, 256) || !launchable((back ? 2LL : 1LL) * P.N * pieces, 256) ||
+        ((back || several(P, packed)) && !launchable(4 * fours + (1 << 15), 256)))
         return KDN_ERR_SHAPE;
     return KDN_OK;
 }
@@ -89,11 +100,6 @@ kdn_status scan_blocks(kdn::ScanParams &P, bool packed, int block) {
 // Workspace of the tiles' states and sums of time steps.
 long long state_bytes(const kdn::ScanParams &P) { return up256(P.tile_slots * P.C * P.S * 4); }
 long long dt_bytes(const kdn::ScanParams &P) { return up256(P.tile_slots * P.C * 4); }
-
-// Sequences of several blocks, or of what a packed batch may have.
-bool several(const kdn::ScanParams &P, bool packed) {
-    return packed ? P.block < P.tokens : P.nblocks > 1;
-}
 
 // Blocks of the gradients: a wave a tile in the pass over the tiles' own states.  Of 128,
 // 256 and 512 tokens: B2 T4096 C2048 bf16 408, 397 and 397 us, 11 packed sequences of 518
@@ -168,7 +174,7 @@ unsigned long long kdn_selective_scan_workspace_size(kdn_dtype dtype, int N, int
     kdn::ScanParams P;
     kdn_status st = scan_shape(P, dtype, N, T, C, S, G, Strides{}, packed);
     if (st == KDN_OK)
-        st = scan_blocks(P, packed != nullptr, scan_block(P.tokens, N, C));
+        st = scan_blocks(P, packed != nullptr, scan_block(P.tokens, N, C), false);
     if (status)
         *status = st;
     return st == KDN_OK && C > 0 && several(P, packed != nullptr)
@@ -186,7 +192,7 @@ kdn_status kdn_selective_scan(kdn_dtype dtype, int N, int T, int C, int S, int G
     if (kdn_status st = scan_shape(P, dtype, N, T, C, S, G,
                                    Strides{x_stride, delta_stride, z_stride, B_stride, C_stride}, packed))
         return st;
-    if (kdn_status st = scan_blocks(P, packed != nullptr, scan_block(P.tokens, N, C)))
+    if (kdn_status st = scan_blocks(P, packed != nullptr, scan_block(P.tokens, N, C), false))
         return st;
     const long long es = P.bf16 ? 2 : 4, tok = P.tokens, gs = (long long)G * S;
     if (tok * C > 0 && (!x || !delta || !A || !B || !Cm || !y))
@@ -285,7 +291,7 @@ unsigned long long kdn_selective_scan_backward_workspace_size(kdn_dtype dtype, i
     kdn::ScanParams P;
     kdn_status st = scan_shape(P, dtype, N, T, C, S, G, Strides{}, packed);
     if (st == KDN_OK)
-        st = scan_blocks(P, packed != nullptr, GRAD_BLOCK);
+        st = scan_blocks(P, packed != nullptr, GRAD_BLOCK, true);
     if (status)
         *status = st;
     if (st != KDN_OK)
@@ -309,7 +315,7 @@ kdn_status kdn_selective_scan_backward(kdn_dtype dtype, int N, int T, int C, int
     if (kdn_status st = scan_shape(P, dtype, N, T, C, S, G,
                                    Strides{x_stride, delta_stride, z_stride, B_stride, C_stride}, packed))
         return st;
-    if (kdn_status st = scan_blocks(P, packed != nullptr, GRAD_BLOCK))
+    if (kdn_status st = scan_blocks(P, packed != nullptr, GRAD_BLOCK, true))
         return st;
     const long long es = P.bf16 ? 2 : 4, tok = P.tokens, gs = (long long)G * S;
     if (!launchable(((long long)C * (S + 2) + 63) / 64 + (tok * gs * 2 + 255) / 256 + 64, 256))

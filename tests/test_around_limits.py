@@ -113,3 +113,22 @@ def test_scan_gradients_of_no_channels_need_places(lib):
     assert scan_back(lib, db=None, **none) == scan_back(lib, dc=None, **none) == ENULL
     assert scan_back(lib, G=0, db=None, dc=None, **none) == OK
     assert scan_back(lib, N=0, db=None, dc=None, **none) == OK
+
+
+def test_scan_counts_what_it_launches(lib):
+    """2^24 workgroups: four runs of 16 channels of a block for the outputs, one for the tiles' own
+    states, 512 states of a sequence for the joins, both ways for the gradients."""
+    st = ctypes.c_int(0)
+    call = lambda want, **kw: scan(lib, x=None, **kw) == want  # noqa: E731
+    # a hundred thousand short prompts
+    assert call(ENULL, N=1 << 15, T=4, C=4096, G=1) and call(ENULL, N=100000, T=4, C=2048, G=1)
+    assert lib.kdn_selective_scan_workspace_size(BF16, 1 << 15, 4, 4096, 16, 1, None, ctypes.byref(st)) == 0 and st.value == OK
+    assert scan_back(lib, N=1 << 15, T=4, C=4096, dy=None) == ENULL
+    assert lib.kdn_selective_scan_backward_workspace_size(BF16, 1 << 15, 4, 4096, 16, 1, None, ctypes.byref(st)) > 0 and st.value == OK
+    # outputs: blocks of 16 runs; joins: 4096 states of a sequence in 8 workgroups
+    assert call(ENULL, N=(1 << 21) - 1, T=1, C=256, G=1) and call(ESHAPE, N=1 << 21, T=1, C=256, G=1)
+    assert call(ENULL, N=(1 << 22) - 1024, T=1, C=16, S=8, G=1) and call(ESHAPE, N=(1 << 24) - 1, T=1, C=16, S=8, G=1)
+    # sequences of several blocks: own states
+    pk = packed(1 << 27, 64, pool=8, N=4)
+    assert scan(lib, N=4, T=0, C=64, G=1, pk=pk, x=None) == ENULL and scan(lib, N=4, T=0, C=512, G=1, pk=pk, x=None) == ESHAPE
+    assert scan_back(lib, N=1 << 20, T=1, C=256, dy=None) == ESHAPE

@@ -281,3 +281,29 @@ def test_scan_gradients_of_no_channels(dtype, packed):
                    ddelta_bias=None, dS0=None)
         kdn.selective_scan_backward(e, e, torch.empty(0, S, device="cuda"), B, B, e, D=none, tables=t, out=out)
         assert not out["dB"].any() and not out["dC"].any()
+
+
+def test_scan_of_very_many_short_sequences():
+    """2^23 runs of channels: each sequence's outputs and gradients are those that it has alone."""
+    N, T, C, S = 1 << 15, 4, 4096, 16
+    args, kw = ts.case((N, T), C, S, 1, BF, seed=1)
+    dy = randn((N, T, C), BF, 11)
+    y, last = kdn.selective_scan(*args, **kw)
+    for n in (0, 1, 9999, N - 1):
+        one = [v if i == 2 else v[n:n + 1] for i, v in enumerate(args)]
+        wy, ws = kdn.selective_scan(*one, **dict(kw, z=kw["z"][n:n + 1]))
+        # (few runs go to another kernel, whose sums are in another order)
+        rows = tuple(v if i == 2 else v[0] for i, v in enumerate(one))
+        ts.check(rows, dict(kw, z=kw["z"][n]), None, y[n], last[n:n + 1], [slice(0, T)], [0])
+        ts.check(rows, dict(kw, z=kw["z"][n]), None, wy[0], ws, [slice(0, T)], [0])
+    del last
+    like = torch.empty_like
+    out = dict(dx=like(dy), ddelta=like(dy), dz=like(dy), dB=like(args[3]), dC=like(args[4]), dA=like(args[2]), dD=like(kw["D"]),
+               ddelta_bias=like(kw["D"]), dS0=None)
+    d = kdn.selective_scan_backward(*args, dy, out=out, **kw)
+    for n in (0, 1, 9999, N - 1):
+        one = [v if i == 2 else v[n:n + 1] for i, v in enumerate(args)]
+        g = kdn.selective_scan_backward(*one, dy[n:n + 1], **dict(kw, z=kw["z"][n:n + 1]))
+        for k in ("dx", "ddelta", "dz"):
+            assert torch.equal(d[k][n:n + 1], g[k]), k
+    assert all(torch.isfinite(d[k]).all() for k in ("dB", "dC", "dA", "dD", "ddelta_bias"))
