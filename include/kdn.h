@@ -616,7 +616,7 @@ unsigned long long kdn_causal_conv_backward_workspace_size(kdn_dtype dtype, int 
  *     dt_t = softplus(delta_t + delta_bias)   (softplus = 0: delta_t + delta_bias)
  *     h_t = exp(dt_t A) h_{t-1} + dt_t x_t B_t
  *     y_t = (sum_n C_t h_t + D x_t) silu(z_t)
- * (A < 0, not checked).  G groups of C / G consecutive channels share B and C.
+ * (A < 0, not checked; -inf, a state that forgets at once, where no dt is zero).  G groups of C / G consecutive channels share B and C.
  *
  *   x, delta    [tokens, C] dtype;  z [tokens, C] dtype or NULL (no gate)
  *   B, C        [tokens, G, S] dtype, rows by stride as all of these

@@ -202,13 +202,19 @@ __device__ __forceinline__ void store_states(float *p, const float (&v)[SPL]) {
     }
 }
 
+// A with -inf (states that forget at once) as the lowest number, so that a token that is
+// not there, of time step 0, leaves the state as it is: 0 (-inf) would be NaN.
+__device__ __forceinline__ float finite_A(float a) {
+    constexpr float LOWEST = -3.40282347e38f;
+    return a < LOWEST ? LOWEST : a;      // NaN stays NaN
+}
 // A's row of the lane's channel times log2(e): a = 2^(dt A2).
 template <int SPL>
 __device__ __forceinline__ void load_A(const ScanParams &P, int c, int j, float (&A2)[SPL]) {
     load_states<SPL>(P.A + (long)c * (4 * SPL) + j * SPL, A2);
 #pragma unroll
     for (int s = 0; s < SPL; ++s)
-        A2[s] *= LOG2E;
+        A2[s] = finite_A(A2[s] * LOG2E);
 }
 
 }  // namespace scan

@@ -307,3 +307,23 @@ def test_scan_of_very_many_short_sequences():
         for k in ("dx", "ddelta", "dz"):
             assert torch.equal(d[k][n:n + 1], g[k]), k
     assert all(torch.isfinite(d[k]).all() for k in ("dB", "dC", "dA", "dD", "ddelta_bias"))
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("B,T,C,S", [(2, 5, 20, 16), (1, 70, 33, 8), (2, 2333, 33, 32), (2, 2333, 33, 16), (300, 37, 80, 16)])
+def test_states_that_forget_at_once(dtype, B, T, C, S):
+    """A = -inf in some states: exp(dt A) is zero at every token and one at none, whatever the
+    length leaves of a tile."""
+    args, kw = ts.case((B, T), C, S, 1, dtype, seed=T)
+    S0 = randn((B, C, S), F32, 9)
+    A, far = args[2].clone(), args[2].clone()
+    A[:, ::3], far[:, ::3] = -math.inf, -1e30
+    A[3] = -math.inf
+    far[3] = -1e30
+    y, last = kdn.selective_scan(*args[:2], A, *args[3:], S0=S0, **kw)
+    want, state = kdn.selective_scan(*args[:2], far, *args[3:], S0=S0, **kw)
+    assert torch.isfinite(y).all() and torch.equal(y, want) and torch.equal(last, state)
+    tok = lambda a: [v if i == 2 else v[:, 0] for i, v in enumerate(args[:2] + (a,) + args[3:])]  # noqa: E731
+    kw["z"] = kw["z"][:, 0]
+    a, b = S0.clone(), S0.clone()
+    assert torch.equal(kdn.selective_decode(*tok(A), a, **kw), kdn.selective_decode(*tok(far), b, **kw)) and torch.equal(a, b)
