@@ -242,7 +242,10 @@ __global__ __launch_bounds__(grad_waves<SPL>() * WAVE, 2) void scan_grad_kernel(
                             const int step = rev ? -WAVE * SPL : WAVE * SPL;
                             const float *pa = &ends[0][rev ? NW - 1 : 0][e];
                             float *pe = &ends[rev ? 2 : 1][rev ? NW - 1 : 0][e];
-                            float va[NW], ve[NW], v = state[n];
+                            // behind the last channel nothing, so that its last state, which was
+                            // read without a branch, does not get into other states' sums
+                            const int behind = (per - (run0 + k) * SCAN_CHANNELS) * S - 1;
+                            float va[NW], ve[NW], v = e > behind ? 0.f : state[n];
 #pragma unroll
                             for (int q = 0; q < NW; ++q) {
                                 va[q] = pa[q * step];

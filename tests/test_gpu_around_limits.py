@@ -327,3 +327,27 @@ def test_states_that_forget_at_once(dtype, B, T, C, S):
     kw["z"] = kw["z"][:, 0]
     a, b = S0.clone(), S0.clone()
     assert torch.equal(kdn.selective_decode(*tok(A), a, **kw), kdn.selective_decode(*tok(far), b, **kw)) and torch.equal(a, b)
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("S", [8, 16, 32])
+@pytest.mark.parametrize("C,G", [(24, 1), (7, 1), (40, 2)])
+@pytest.mark.parametrize("bad", [math.inf, math.nan])
+def test_a_non_finite_state_stays_in_its_channel_and_state(dtype, S, C, G, bad):
+    """The last state of a group's last channel, whose run has lanes behind its channels."""
+    T, per = 100, C // G
+    args, kw = ts.case((1, T), C, S, G, dtype, seed=S)
+    S0, dS, dy = randn((1, C, S), F32, 9), randn((1, C, S), F32, 10), randn((1, T, C), dtype, 11)
+    want = kdn.selective_scan_backward(*args, dy, S0=S0, dS_out=dS, **kw)
+    S0[0, per - 1, S - 1] = dS[0, per - 1, S - 1] = bad
+    got = kdn.selective_scan_backward(*args, dy, S0=S0, dS_out=dS, **kw)
+    for k in ("dB", "dC"):
+        assert torch.equal(got[k][:, :, 1:], want[k][:, :, 1:]) and torch.equal(got[k][..., :-1], want[k][..., :-1]), k
+    rest = torch.arange(C, device="cuda") != per - 1
+    for k in ("dx", "ddelta", "dz"):
+        assert torch.equal(got[k][..., rest], want[k][..., rest]), k
+    for k in ("dA", "dD", "ddelta_bias"):
+        assert torch.equal(got[k][rest], want[k][rest]), k
+    assert torch.equal(got["dA"][per - 1, :-1], want["dA"][per - 1, :-1])
+    assert torch.equal(got["dS0"][0, rest], want["dS0"][0, rest])
+    assert torch.equal(got["dS0"][0, per - 1, :-1], want["dS0"][0, per - 1, :-1])
