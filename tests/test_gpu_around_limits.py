@@ -7,6 +7,7 @@ import torch
 
 import around_ref as ref
 import test_gpu_conv as tc
+import test_gpu_norm as tn
 import test_gpu_scan as ts
 from linear_attention_recurrent_delta_amd import kdn
 from test_gpu_conv import BF, F32, gen, i32, randn
@@ -351,3 +352,31 @@ def test_a_non_finite_state_stays_in_its_channel_and_state(dtype, S, C, G, bad):
     assert torch.equal(got["dA"][per - 1, :-1], want["dA"][per - 1, :-1])
     assert torch.equal(got["dS0"][0, rest], want["dS0"][0, rest])
     assert torch.equal(got["dS0"][0, per - 1, :-1], want["dS0"][0, per - 1, :-1])
+
+
+@pytest.mark.parametrize("dtype,stream", [(BF, BF), (BF, F32), (F32, F32)])
+@pytest.mark.parametrize("scale", ["none", "one", "channel"])
+@pytest.mark.parametrize("rows,D", [(2500, 1543), (1100, 4096), (3001, 513), (40000, 100)])
+def test_rounds_of_residual_gradients(dtype, stream, scale, rows, D):
+    """Several rounds of a workgroup over rows wider than a wave (and one case of rows within
+    one): the row ahead, the turns of the sums' memory, the last round that is not full."""
+    x, res = randn((rows, D), dtype, 1), randn((rows, D), stream, 2, size=3.0)
+    w = 1 + randn((D,), F32, 3, size=0.3)
+    s = None if scale == "none" else 0.5 + randn((1 if scale == "one" else D,), F32, 4, size=0.3)
+    dy = randn((rows, D), dtype, 5)
+    tn.check_residual(x, res, w, s, dy, randn((rows, D), stream, 6))
+    tn.check_residual(x, res, w, s, dy, None)
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("order,act", tn.KINDS)
+@pytest.mark.parametrize("per_head", [False, True])
+@pytest.mark.parametrize("tokens,H,d", [(1700, 3, 1000), (1100, 3, 2048), (2100, 2, 515)])
+def test_rounds_of_gated_gradients(dtype, order, act, per_head, tokens, H, d):
+    gate = act != "no gate"
+    act = act if gate else "silu"
+    x, z, w, dy = tn.case((tokens,), H, d, dtype, per_head, seed=d, gate=gate)
+    g = kdn.gated_norm_backward(x, w, dy, z, eps=tn.EPS, order=order, activation=act)
+    tn.check_gated(x, z, w, dy, order, act, dtype, None, g)
+    again = kdn.gated_norm_backward(x, w, dy, z, eps=tn.EPS, order=order, activation=act)
+    assert all(g[k] is None or torch.equal(g[k], again[k]) for k in g)
