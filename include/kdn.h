@@ -629,8 +629,9 @@ unsigned long long kdn_causal_conv_backward_workspace_size(kdn_dtype dtype, int 
  *               overlapping no other argument; NULL if that is 0
  * A, S0 and S_out on 16-byte boundaries.  S in {8, 16, 32}; C below 2^24; sizes whose
  * launches would have 2^32 work-items are refused (KDN_ERR_SHAPE).  States are
- * float32.  A packed batch's sequences are cut where its blocks cut them: tables with
- * blocks of kdn_selective_block tokens are quickest, any do.
+ * float32.  A packed batch's sequences are cut where its blocks cut them: any blocks
+ * do, those of kdn_selective_block tokens are quickest for sequences of much the same length
+ * (with one that is many times the others' they can be too long).
  */
 kdn_status kdn_selective_scan(kdn_dtype dtype, int N, int T, int C, int S, int G, int softplus,
                               long long x_stride, long long delta_stride, long long z_stride,

@@ -262,10 +262,10 @@ __global__ __launch_bounds__(WAVE) void conv_decode_kernel(ConvDecodeParams P, i
 // the state behind it added to its last rows.  Bound by memory: x and dy read, dx
 // written.  A lane walks RT tokens and the W - 1 behind them, whose ds it makes
 // again, with 8 bytes of each row: 16 would not leave registers for two workgroups a
-// CU.  B4 T4096 of 2048 channels, bf16: 52 us, 3.9 TB/s and 69 % of the vector units'
+// CU.  B4 T4096 of 2048 channels, bf16: 52 us, 3.9 TB/s and 66 % of the vector units'
 // time (each activation and its slope take an exponential and a division, (RT + W - 1)
-// / RT times), and the sums 4.7.  A workgroup keeps the sums of its channels over all its tiles (every
-// `parts`-th) in registers and writes them once; a second kernel adds the parts
+// / RT times), and the sums 4.8.  A workgroup keeps the sums of its channels over all its tiles (every
+// `parts`-th, 32 at most) in registers and writes them once; a second kernel adds the parts
 // in order, in 64 bits.
 // ---------------------------------------------------------------------------
 template <typename T, int VEC, int W, bool WHOLE>
@@ -453,7 +453,7 @@ __global__ __launch_bounds__(NT) void conv_sum_kernel(ConvParams P, long wide) {
 }
 
 // Rows of whole pieces of `bytes` bytes on such boundaries, near enough for 32 bits: they
-// are read through descriptors (37 packed prompts 112 us, by elements' addresses and
+// are read through descriptors (37 packed prompts 111 us, by elements' addresses and
 // branches 130; gradients B4 T4096 of 2048 channels 56 and 64).
 bool whole(int C, long stride, int es, int bytes, std::initializer_list<const void *> p) {
     bool ok = C * (long)es % bytes == 0 && stride * es % bytes == 0 && stride < (1l << 24);
@@ -479,7 +479,7 @@ struct Tiles {
 
 template <typename T, int VEC, int W>
 hipError_t launch_conv_fwd_t(const ConvParams &P, hipStream_t st) {
-    // tokens of a lane (8, 16 and 32: 37 packed prompts 122, 121 and 125 us)
+    // tokens of a lane (8, 16 and 32: 37 prompts of 590 tokens, C 6144 bf16, 116, 108 and 116 us)
     constexpr int RT = CONV_TILE / NW;
     const int chunks = conv_chunks(P.C, VEC);
     const Tiles q(P);

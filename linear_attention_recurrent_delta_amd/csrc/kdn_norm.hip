@@ -12,8 +12,9 @@
 // memory hides, and no row of finite values is lost to an overflow.
 //
 // Measured: residual stream and norm of 16384 x 4096 (bf16, stream float32) 146 us,
-// 5.5 TB/s; gradients of the gated norm of 262144 x 128 bf16 68 us, 4.9 TB/s (with the
-// gate's kind and whole rows known to the compiler; 91 without), and the parts' sums 5;
+// 5.5 TB/s; gradients of the gated norm of 262144 x 128 bf16 69 us, 4.9 TB/s, and the
+// parts' sums 5 (calls: with the gate's kind and whole rows known to the compiler 69 us,
+// whole rows alone 79, the kind alone 72, neither 85);
 // of the residual norm of 2500 x 1543 bf16 20 us and 4, where rows start on no boundary
 // and a row takes 256 threads of which 193 work; one token of 16 heads of 128 2 us of
 // the call's 9, which binding and launch take.
@@ -173,7 +174,8 @@ template <int VEC, bool FULL> struct Piece {
 };
 
 // What a gated norm's kernel knows of its gate: silu in either order, or nothing
-// (gradients of 262144 x 128: 68 us where it knows, 91 where it asks).
+// (gradients of 262144 x 128: 69 us where it knows, 79 where it asks; with a sigmoid, for
+// which it asks, 75, without a gate 43).
 enum Kind { NORM_SILU, SILU_NORM, ANY };
 template <Kind KIND> struct Gate {
     bool there, first;

@@ -79,9 +79,12 @@ __device__ __forceinline__ int by_length(const ScanParams &P, int p) {
 // tokens again, with their decays and inputs from registers (one more product and sum
 // for a state than a walk by one wave, which NW = 1 is).  The chain along a sequence
 // is then an eighth as long.  37 packed prompts (22 thousand tokens) of 4096 channels,
-// 16 states, bf16: 350 us with the vector units busy all the time (six instructions'
-// time for a state are 245; B and C from LDS, softplus, gate and sums over states the
-// rest), 2.1 TB/s; a prompt of 190 tokens and 2048 channels: 11 us.
+// 16 states, bf16: 361 to 370 us with the tables' 6 (420 where each kernel is traced by
+// itself), bound by the vector units: six instructions' time for a state are 245, B and C
+// from LDS, softplus, gate and sums over states the rest.  The instructions take 1.10 of
+// the vector units' time as counted, with two for an exponential; others are issued in its
+// second half, and a loop of one exponential and five others reaches 1.06.  2.0 TB/s.  A
+// prompt of 190 tokens and 2048 channels: 11 us.
 // ---------------------------------------------------------------------------
 template <typename T, int SPL, int NW>
 __global__ __launch_bounds__(NW == 1 ? 256 : NW *WAVE, 2) void scan_kernel(ScanParams P,
