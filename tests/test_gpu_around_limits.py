@@ -181,7 +181,7 @@ def test_conv_sums_over_many_tokens():
 
 @pytest.mark.parametrize("per_head,tokens,H", [(True, 24576, 512), (False, 64 * 24576, 8)])
 def test_gated_norm_sums_over_many_rows(per_head, tokens, H):
-    """dweight over 768 rows for each place of a workgroup of old.  A thread adds at most 256
+    """dweight over 768 rows for each place of the workgroups that run at once.  A thread adds at most 256
     rows in float32, then 16 rows' places; n is off by 8 roundings (its root, two products) and
     the result by one."""
     d = 64
@@ -199,7 +199,7 @@ def test_gated_norm_sums_over_many_rows(per_head, tokens, H):
 
 @pytest.mark.parametrize("scale", ["one", "channel"])
 def test_residual_norm_sums_over_many_rows(scale):
-    """dweight and dscale over 768 rows a workgroup of old: a thread adds at most 256 in float32.
+    """dweight and dscale over 768 rows for each of the workgroups that run at once: a thread adds at most 256 in float32.
     n is off by 8 roundings, the result by one; one scale adds four columns of a thread and
     nine steps of a workgroup, too."""
     tokens, D = 512 * 768, 2048
@@ -242,7 +242,7 @@ def test_norm_gradients_beyond_one_run_of_sums(dtype):
 
 
 def test_scan_sums_over_many_tokens():
-    """dD over 768 tiles of one workgroup of old: a wave adds 8 tokens of each of at most 256
+    """dD over 768 tiles, which one workgroup of so many channels could take: a wave adds 8 tokens of each of at most 256
     tiles in float32 (two in a lane, four lanes), then eight waves' sums are added, and the
     result is rounded."""
     T, C, S = 64 * 768, 32768, 8
