@@ -38,8 +38,8 @@ kdn_status conv_shape(kdn::ConvParams &P, int dtype, int N, int T, int C, int W,
 
 // Parts that the sums over tokens are made in: as many workgroups as run at once
 // (two a CU, by their registers), each over all the tiles it takes.  With 256, 512 and
-// 1024 of them: B4 T4096 C2048 bf16 74, 56 and 59 us, 11 packed sequences of 1030
-// channels in float32 52, 52 and 51.  A lane adds 16 tokens of a tile in float32: from
+// 1024 of them: B4 T4096 C2048 bf16 73, 56 and 59 us, 11 packed sequences of 1030
+// channels in float32 48, 49 and 48.  A lane adds 16 tokens of a tile in float32: from
 // PART_TILES tiles a part on there are twice, three times .. as many parts, so that no sum
 // is a chain of more than 512 of them, however long the sequences are.
 constexpr int GRAD_WGS = 512, PART_TILES = 32;

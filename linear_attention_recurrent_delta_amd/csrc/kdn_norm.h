@@ -53,8 +53,8 @@ struct ResidualNormParams {
 
 // Parts that the sums over tokens are made in: about as many workgroups as run at once
 // (of 256 and of 512 threads).  Half as many, these and twice as many: gated 262144 x 128
-// bf16 72, 71 and 73 us, 98304 x 192 float32 by head 91, 82 and 84; residual 2500 x 1543
-// bf16 30, 23 and 34, 16384 x 2048 64, 67 and 71.
+// bf16 72, 70 and 71 us, 98304 x 192 float32 by head 93, 80 and 85; residual 2500 x 1543
+// bf16 24, 23 and 32, 16384 x 2048 67, 69 and 72.
 constexpr int NORM_PARTS = 1024, RESIDUAL_PARTS = 512;
 // Rows of a column that a thread adds in float32: behind them a workgroup of the gated norm
 // writes its sums and begins anew, and of the residual norm another launch begins (as in the

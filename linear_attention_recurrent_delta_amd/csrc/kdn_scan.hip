@@ -22,8 +22,8 @@ namespace scan {
 //      4000    221  426   463  430   894  610   1786 1157
 constexpr long SCAN_MANY = 1024;
 // Workgroups that the pass over tiles' own states is shared out to.  With 1024, 4096
-// and 16384: one sequence of 16000 tokens and 1024 channels 214, 209 and 209 us,
-// gradients of 11 packed sequences of 518 channels, float32, 209, 204 and 215.
+// and 16384: one sequence of 16000 tokens and 1024 channels 213, 207 and 207 us,
+// gradients of 11 packed sequences of 518 channels, float32, 211, 205 and 216.
 constexpr long SCAN_OWN_WGS = 4096;
 
 // Tokens that a wave takes at a time: their decays and inputs stay in registers
@@ -336,8 +336,8 @@ __global__ __launch_bounds__(OWN_WAVES *WAVE) void scan_own_kernel(ScanParams P,
 // state at its start, h <- 2^(A2 sum dt) h + U; reverse (tiles last to first): Q
 // becomes the reverse state behind its end, and behind the first tile is dS0.  A
 // thread holds two states of a channel; the next JOIN tiles are on their way while as
-// many are joined (4, 8 and 16: one sequence of 16000 tokens and 1024 channels 212, 208
-// and 205 us, gradients of B2 T4096 398, 393 and 396).  Bound by a chain of as many
+// many are joined (4, 8 and 16: one sequence of 16000 tokens and 1024 channels 211, 207
+// and 204 us, gradients of B2 T4096 356, 355 and 355).  Bound by a chain of as many
 // loads as there are tiles: 16 us for two of 64 both ways, 2048 channels (27 with one
 // state a thread and no tiles on their way).
 // ---------------------------------------------------------------------------

@@ -102,11 +102,11 @@ long long state_bytes(const kdn::ScanParams &P) { return up256(P.tile_slots * P.
 long long dt_bytes(const kdn::ScanParams &P) { return up256(P.tile_slots * P.C * 4); }
 
 // Blocks of the gradients: a wave a tile in the pass over the tiles' own states.  Of 128,
-// 256 and 512 tokens: B2 T4096 C2048 bf16 408, 397 and 397 us, 11 packed sequences of 518
-// channels in float32 208, 204 and 207.
+// 256 and 512 tokens: B2 T4096 C2048 bf16 366, 354 and 351 us, 11 packed sequences of 518
+// channels in float32 207, 205 and 207.
 constexpr int GRAD_BLOCK = 256;
 // Workgroups of the gradients' kernel that run at once: one a CU (with two of them shared
-// out B2 T4096 C2048 is 405 us where it is 397, B1 T1000 C1024 76 where it is 59).
+// out B2 T4096 C2048 is 360 us where it is 354, B1 T1000 C1024 68 where it is 52).
 constexpr int GRAD_WGS = 256;
 // Tiles whose sums over tokens a wave of a workgroup adds in float32 (on average, where a
 // packed batch is uneven).
